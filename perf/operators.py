@@ -168,7 +168,8 @@ def prepare(case, seed):
         # logits as a model gives them: a wide floor, and a few dozen tokens that stand out by up to some e-folds
         x = 2.0 * torch.randn(N, V, generator=g, device=dev)
         at = torch.randint(0, V, (N, 48), generator=g, device=dev)
-        x.scatter_(1, at, 8.0 + 3.0 * torch.randn(N, 48, generator=g, device=dev))
+        # (the larger of two at one place: a plain scatter would leave open which stays)
+        x.scatter_reduce_(1, at, 8.0 + 3.0 * torch.randn(N, 48, generator=g, device=dev), "amax")
         if case["masked"]:
             x.masked_fill_(torch.rand(N, V, generator=g, device=dev) < 0.1, -math.inf)
         s["x"] = x.to(DTYPES[case["dtype"]])
