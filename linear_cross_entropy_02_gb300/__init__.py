@@ -35,6 +35,8 @@ __all__ = [
     "flce_profile_read", "linear_cross_entropy", "FusedLinearCrossEntropyLoss", "FlceError",
     "flce_vp_forward", "flce_vp_backward", "flce_vp_workspace", "vocab_parallel_linear_cross_entropy", "vp_shard_table",
     "vp_gather_partials", "vp_reduce_grad_h",
+    "flce_layer_norm", "flce_layer_norm_backward", "layer_norm", "MicroscaleTensor", "flce_microscale_quantize",
+    "flce_microscale_dequantize", "flce_microscale_linear", "flce_sample", "LanguageModelHead",
 ]
 
 _REDUCTIONS = {"mean": FLCE_REDUCTION_MEAN, "sum": FLCE_REDUCTION_SUM, "none": _lib.FLCE_REDUCTION_NONE}
@@ -750,7 +752,7 @@ def flce_profile_begin(enable: bool = True) -> None:
 
 def flce_profile_read() -> dict:
     """{kernel name: (launches, total ms)} of the launches recorded since flce_profile_begin(True)."""
-    n = _lib.FLCE_NUM_KERNELS
+    n = _lib.FLCE_HEAD_KERNEL_FIRST + _lib.FLCE_HEAD_KERNEL_COUNT  # the operators around the head follow the head's own
     launches = (ctypes.c_int64 * n)()
     ms = (ctypes.c_double * n)()
     rc = _lib.lib().flce_profile_read(launches, ms, n)
@@ -758,3 +760,8 @@ def flce_profile_read() -> dict:
         raise FlceError(-rc, "flce_profile_read")
     L = _lib.lib()
     return {L.flce_kernel_name(i).decode(): (int(launches[i]), float(ms[i])) for i in range(n) if launches[i]}
+
+
+from ._head import (LanguageModelHead, MicroscaleTensor, flce_layer_norm, flce_layer_norm_backward,  # noqa: E402
+                    flce_microscale_dequantize, flce_microscale_linear, flce_microscale_quantize, flce_sample,
+                    layer_norm)

@@ -16,7 +16,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libflce.so")
 
-SOURCES = ["engine.cpp", "gemm_tc.cu", "kernels_aux.cu", "kernels_ce.cu", "no_alloc.cu"]
+SOURCES = ["engine.cpp", "gemm_tc.cu", "kernels_aux.cu", "kernels_ce.cu", "no_alloc.cu",
+           "head_api.cpp", "norm.cu", "microscale.cu", "gemm_mx.cu", "sample.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -27,7 +28,7 @@ def _nvcc() -> str:
 
 def _deps():
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files.append(os.path.join(INCLUDE, "flce.h"))
+    files += [os.path.join(INCLUDE, f) for f in ("flce.h", "flce_head.h")]
     files.append(os.path.abspath(__file__))
     return files
 

@@ -1,0 +1,374 @@
+"""The operators around the fused head: the norm in front of it, its product on
+a microscaled 4-bit weight, and the choice of the next token (include/flce_head.h).
+
+As in the rest of the binding, nothing is computed here: arguments are checked,
+leading row dimensions are flattened, outputs and workspaces are torch's, and
+the library's kernels run on torch's current CUDA stream.
+"""
+from __future__ import annotations
+
+from typing import Optional, Union
+
+import torch
+
+from . import _lib
+from ._lib import FlceError
+
+_DTYPES = {torch.bfloat16: _lib.FLCE_DTYPE_BF16, torch.float32: _lib.FLCE_DTYPE_F32}
+
+
+def _call(device: torch.device, name: str, *args):
+    """Calls a C entry with `device` current and its current stream as the last argument."""
+    fn = getattr(_lib.lib(), name)
+    if torch.cuda.current_device() == device.index:
+        rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if rc != 0:
+        raise FlceError(rc, name)
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _cuda(name: str, t) -> None:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+
+
+def _floats(name: str, t) -> int:
+    _cuda(name, t)
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be bfloat16 or float32")
+    return code
+
+
+def _rows(t: torch.Tensor) -> torch.Tensor:
+    """t as [rows, last dimension] with unit stride in the last dimension (a copy only if it has none)."""
+    if t.dim() != 2:
+        t = t.reshape(-1, t.shape[-1])
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        t = t.contiguous()
+    return t
+
+
+def _ld(t: torch.Tensor) -> int:
+    """Row stride of a 2-D tensor; that of a single row is free, so torch may give any."""
+    return t.stride(0) if t.shape[0] > 1 and t.stride(0) >= t.shape[1] else t.shape[1]
+
+
+def _dense_rows(t: torch.Tensor) -> torch.Tensor:
+    """Rows that do not overlap (an expanded tensor is copied)."""
+    return t.contiguous() if t.shape[0] > 1 and t.stride(0) < t.shape[1] else t
+
+
+# ---------------------------------------------------------------- norm
+def _norm_weights(x: torch.Tensor, weight, bias):
+    code = _lib.FLCE_DTYPE_F32
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is None:
+            continue
+        code = _floats(name, t)
+        if t.shape != (x.shape[-1],) or t.device != x.device or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous [H] tensor on x's device")
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise ValueError("weight and bias must have one dtype")
+    return code
+
+
+def flce_layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None, *,
+                    eps: float = 1e-5, rms: bool = False, return_stats: bool = False):
+    """Layer norm (or RMS norm with rms=True) over the last dimension of x
+    (bf16 or fp32, any leading shape): (x - mean) rstd weight + bias in x's
+    dtype. weight and bias: [H] in one of the two dtypes, or None. With
+    return_stats also the fp32 mean (None for RMS norm) and rstd of each row,
+    which flce_layer_norm_backward takes."""
+    dtype = _floats("x", x)
+    if x.dim() == 0 or x.shape[-1] == 0:
+        raise ValueError("x must have a last dimension to normalise")
+    wcode = _norm_weights(x, weight, bias)
+    x2 = _dense_rows(_rows(x))
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    mean = rstd = None
+    if return_stats:
+        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        mean = None if rms else torch.empty_like(rstd)
+    _call(x.device, "flce_layer_norm", x2.data_ptr(), dtype, x2.shape[0], x2.shape[1], _ld(x2), _ptr(weight),
+          _ptr(bias), wcode, eps, int(rms), y.data_ptr(), _ptr(mean), _ptr(rstd))
+    return (y, mean, rstd) if return_stats else y
+
+
+def flce_layer_norm_backward(grad_y: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Tensor],
+                             mean: Optional[torch.Tensor], rstd: torch.Tensor, *, rms: bool = False,
+                             need_grad_x: bool = True, need_grad_weight: bool = True, need_grad_bias: bool = True,
+                             grad_weight: Optional[torch.Tensor] = None, grad_bias: Optional[torch.Tensor] = None) -> dict:
+    """Backward of flce_layer_norm from x and the saved statistics. Returns
+    dict(grad_x, grad_weight, grad_bias): grad_x in x's dtype, the other two
+    fp32 [H]. A grad_weight or grad_bias that is given (fp32, contiguous) is
+    ACCUMULATED in place, as the fused head does with grad_W."""
+    dtype = _floats("x", x)
+    _cuda("grad_y", grad_y)
+    if grad_y.shape != x.shape or grad_y.dtype != x.dtype or grad_y.device != x.device:
+        raise ValueError("grad_y must have x's shape, dtype and device")
+    wcode = _norm_weights(x, weight, None)
+    H = x.shape[-1]
+    for name, t in (("rstd", rstd), ("mean", None if rms else mean)):
+        if name == "mean" and rms:
+            continue
+        _cuda(name, t)
+        if t.dtype != torch.float32 or t.shape != x.shape[:-1] or not t.is_contiguous() or t.device != x.device:
+            raise ValueError(f"{name} must be a contiguous fp32 tensor of x's leading shape on x's device")
+    for name, t in (("grad_weight", grad_weight), ("grad_bias", grad_bias)):
+        if t is not None and (t.dtype != torch.float32 or t.shape != (H,) or not t.is_contiguous() or t.device != x.device):
+            raise ValueError(f"{name} must be a contiguous fp32 [H] tensor on x's device")
+    if (grad_weight is None) != (grad_bias is None) and need_grad_weight and need_grad_bias:
+        raise ValueError("give both grad_weight and grad_bias to accumulate into, or neither")
+    x2, g2 = _dense_rows(_rows(x)), _dense_rows(_rows(grad_y))
+    accumulate = grad_weight is not None or grad_bias is not None
+    gx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_grad_x else None
+    if need_grad_weight and grad_weight is None:
+        grad_weight = torch.empty(H, dtype=torch.float32, device=x.device)
+    if need_grad_bias and grad_bias is None:
+        grad_bias = torch.empty(H, dtype=torch.float32, device=x.device)
+    gw, gb = grad_weight if need_grad_weight else None, grad_bias if need_grad_bias else None
+    from . import _workspace
+    nbytes = _lib.lib().flce_layer_norm_workspace_size(x2.shape[0], H) if gw is not None or gb is not None else 0
+    ws = _workspace(x.device, nbytes) if nbytes else None
+    _call(x.device, "flce_layer_norm_backward", g2.data_ptr(), _ld(g2), x2.data_ptr(), _ld(x2), dtype, x2.shape[0], H,
+          _ptr(weight), wcode, None if rms else mean.data_ptr(), rstd.data_ptr(), int(rms), _ptr(gx), _ptr(gw),
+          _ptr(gb), int(accumulate), _ptr(ws), nbytes)
+    return {"grad_x": gx, "grad_weight": gw, "grad_bias": gb}
+
+
+class _LayerNorm(torch.autograd.Function):
+    """Autograd node of the norm: keeps x and the rows' statistics, not y."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps, rms):
+        y, mean, rstd = flce_layer_norm(x, weight, bias, eps=eps, rms=rms, return_stats=True)
+        ctx.rms = rms
+        ctx.bias_dtype = None if bias is None else bias.dtype
+        ctx.save_for_backward(x, weight, mean, rstd)
+        return y
+
+    @staticmethod
+    def backward(ctx, grad_y):
+        x, weight, mean, rstd = ctx.saved_tensors
+        need_x, need_w, need_b = ctx.needs_input_grad[:3]
+        out = flce_layer_norm_backward(grad_y, x, weight, mean, rstd, rms=ctx.rms, need_grad_x=need_x,
+                                       need_grad_weight=need_w, need_grad_bias=need_b)
+        gw, gb = out["grad_weight"], out["grad_bias"]
+        if gw is not None and weight.dtype != torch.float32:
+            gw = gw.to(weight.dtype)
+        if gb is not None and ctx.bias_dtype != torch.float32:
+            gb = gb.to(ctx.bias_dtype)
+        return out["grad_x"], gw, gb, None, None
+
+
+def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, rms: bool = False):
+    """Differentiable flce_layer_norm: gradients flow to x, weight and bias where they require grad."""
+    return _LayerNorm.apply(x, weight, bias, float(eps), bool(rms))
+
+
+# ---------------------------------------------------------------- microscaled 4-bit
+class MicroscaleTensor:
+    """A matrix [rows, cols] in microscaled 4-bit floating point (OCP MXFP4):
+    codes uint8 [rows, cols / 2], the even element in the low four bits, and
+    E8M0 scales uint8 [ceil(rows / 128), ceil(cols / 128), 32, 4, 4], where row
+    r, block c of 32 elements is at [r // 128, c // 4, r % 32, r % 128 // 32, c % 4]
+    and places without a block hold 127."""
+
+    __slots__ = ("codes", "scales", "shape")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor):
+        _cuda("codes", codes)
+        _cuda("scales", scales)
+        if codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or codes.device != scales.device:
+            raise ValueError("codes and scales must be uint8 tensors on one device")
+        if codes.dim() != 2 or codes.shape[1] == 0 or codes.shape[1] % 16 or not codes.is_contiguous():
+            raise ValueError("codes must be a contiguous [rows, cols / 2] tensor, cols a multiple of 32")
+        rows, cols = codes.shape[0], codes.shape[1] * 2
+        if scales.shape != ((rows + 127) // 128, (cols + 127) // 128, 32, 4, 4) or not scales.is_contiguous():
+            raise ValueError("scales must be a contiguous [ceil(rows / 128), ceil(cols / 128), 32, 4, 4] tensor")
+        self.codes, self.scales, self.shape = codes, scales, (rows, cols)
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    @property
+    def nbytes(self) -> int:
+        return self.codes.numel() + self.scales.numel()
+
+
+def flce_microscale_quantize(x: torch.Tensor) -> MicroscaleTensor:
+    """x [..., K] (bf16 or fp32, K a multiple of 32) in microscaled 4-bit
+    floating point, leading dimensions flattened: each block of 32 gets the
+    power of two that brings its largest magnitude into [4, 8), elements are
+    rounded to nearest (ties to even) and saturate at 6. A block with an
+    infinity or NaN reads back as NaN."""
+    dtype = _floats("x", x)
+    if x.dim() < 2 or x.shape[-1] == 0 or x.shape[-1] % 32:
+        raise ValueError("x must be [..., K] with K a multiple of 32")
+    x2 = _dense_rows(_rows(x))
+    rows, cols = x2.shape
+    codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=x.device)
+    scales = torch.empty(((rows + 127) // 128, (cols + 127) // 128, 32, 4, 4), dtype=torch.uint8, device=x.device)
+    _call(x.device, "flce_microscale_quantize", x2.data_ptr(), dtype, rows, cols, _ld(x2), codes.data_ptr(),
+          scales.data_ptr())
+    return MicroscaleTensor(codes, scales)
+
+
+def flce_microscale_dequantize(q: MicroscaleTensor, *, dtype: torch.dtype = torch.float32) -> torch.Tensor:
+    """What a microscaled matrix stands for, [rows, cols] in bf16 or fp32 (exact
+    in both but for bf16 values below its normal range)."""
+    if dtype not in _DTYPES:
+        raise ValueError("dtype must be bfloat16 or float32")
+    out = torch.empty(q.shape, dtype=dtype, device=q.device)
+    _call(q.device, "flce_microscale_dequantize", q.codes.data_ptr(), q.scales.data_ptr(), q.shape[0], q.shape[1],
+          out.data_ptr(), _DTYPES[dtype])
+    return out
+
+
+def flce_microscale_linear(h: Union[torch.Tensor, MicroscaleTensor], W: MicroscaleTensor, *, out_mult: float = 1.0,
+                           softcap: float = 0.0, out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """Logits [..., V] = cap(out_mult h W^T) on a microscaled weight W [V, K],
+    cap(z) = softcap tanh(z / softcap) where softcap > 0. h: [..., K] in bf16 or
+    fp32, microscaled by the call as flce_microscale_quantize does, or a
+    MicroscaleTensor [N, K]. out_dtype: bf16 or fp32 (h's dtype by default, bf16
+    for a MicroscaleTensor)."""
+    if not isinstance(W, MicroscaleTensor):
+        raise ValueError("W must be a MicroscaleTensor")
+    V, K = W.shape
+    from . import _workspace
+    if isinstance(h, MicroscaleTensor):
+        if h.shape[1] != K or h.device != W.device:
+            raise ValueError("h and W must have one K and one device")
+        out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
+        rows, lead = h.shape[0], (h.shape[0],)
+    else:
+        dtype = _floats("h", h)
+        if h.dim() == 0 or h.shape[-1] != K or h.device != W.device:
+            raise ValueError("h must be [..., K] with W's K, on W's device")
+        out_dtype = h.dtype if out_dtype is None else out_dtype
+        lead = h.shape[:-1]
+        h2 = _dense_rows(_rows(h))
+        rows = h2.shape[0]
+    code = _DTYPES.get(out_dtype)
+    if code is None:
+        raise ValueError("out_dtype must be bfloat16 or float32")
+    out = torch.empty((*lead, V), dtype=out_dtype, device=W.device)
+    if isinstance(h, MicroscaleTensor):
+        ws = _workspace(W.device, 256)
+        _call(W.device, "flce_microscale_matmul", h.codes.data_ptr(), h.scales.data_ptr(), rows, W.codes.data_ptr(),
+              W.scales.data_ptr(), V, K, out_mult, softcap, out.data_ptr(), code, V, ws.data_ptr(), 256)
+    else:
+        nbytes = 256 + (rows * (K // 2) + 255) // 256 * 256 + (rows + 127) // 128 * ((K + 127) // 128) * 512
+        ws = _workspace(W.device, nbytes)
+        _call(W.device, "flce_microscale_linear", h2.data_ptr(), dtype, _ld(h2), rows, W.codes.data_ptr(),
+              W.scales.data_ptr(), V, K, out_mult, softcap, out.data_ptr(), code, V, ws.data_ptr(), nbytes)
+    return out
+
+
+# ---------------------------------------------------------------- sampling
+def _setting(name: str, v, dtype: torch.dtype, lead, device):
+    """(pointer or None, scalar) of a setting given as a number or as one value per row."""
+    if not isinstance(v, torch.Tensor):
+        return None, (int(v) if dtype is torch.int32 else float(v))
+    if v.dtype != dtype or v.shape != lead or v.device != device or not v.is_contiguous():
+        raise ValueError(f"{name} must be a number, or a contiguous {dtype} tensor with one value per row")
+    return v.data_ptr(), 0
+
+
+def flce_sample(logits: torch.Tensor, u: torch.Tensor, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0,
+                return_logprobs: bool = True):
+    """One token per row of logits [..., V] (bf16 or fp32) from given random
+    numbers u [...] (fp32, uniform in [0, 1)). temperature, top_p and min_p are
+    numbers or fp32 tensors of one value per row, top_k a number or an int32
+    tensor. Filters apply in the order top_k, top_p, min_p, each to what the one
+    before it kept; <= 0 (top_k, min_p) and >= 1 (top_p) keep all, temperature
+    <= 0 takes the largest logit (the lowest index of several). Returns (tokens
+    int64, logprobs fp32), the second the log of the token's probability among
+    the kept ones (None without return_logprobs). A row with NaN or +infinity, or
+    without a finite logit, gives token -1. The result does not depend on how
+    the rows are batched."""
+    code = _floats("logits", logits)
+    if logits.dim() == 0 or logits.shape[-1] == 0:
+        raise ValueError("logits must be [..., V]")
+    lead = logits.shape[:-1]
+    _cuda("u", u)
+    if u.dtype != torch.float32 or u.shape != lead or u.device != logits.device or not u.is_contiguous():
+        raise ValueError("u must be a contiguous fp32 tensor of the logits' leading shape, on their device")
+    x = _dense_rows(_rows(logits))
+    tp, t = _setting("temperature", temperature, torch.float32, lead, x.device)
+    kp, k = _setting("top_k", top_k, torch.int32, lead, x.device)
+    pp, p = _setting("top_p", top_p, torch.float32, lead, x.device)
+    mp, m = _setting("min_p", min_p, torch.float32, lead, x.device)
+    tokens = torch.empty(lead, dtype=torch.int64, device=x.device)
+    logprobs = torch.empty(lead, dtype=torch.float32, device=x.device) if return_logprobs else None
+    _call(x.device, "flce_sample", x.data_ptr(), code, x.shape[0], x.shape[1], _ld(x), u.data_ptr(), tp, t, kp, k, pp, p,
+          mp, m, tokens.data_ptr(), _ptr(logprobs))
+    return tokens, logprobs
+
+
+# ---------------------------------------------------------------- the head as a model has it
+class LanguageModelHead(torch.nn.Module):
+    """A model's last layers: the final norm and the vocabulary projection W [V, H]
+    (bf16 or fp32), for training and for answering.
+
+    loss(hidden, labels) normalises and runs the fused linear cross-entropy;
+    gradients flow to hidden, the norm's weights and W where they require grad.
+    next_token(hidden, u, ...) normalises, multiplies with W in microscaled
+    4-bit (prepare_answers() lays it out once; call it again after W changed)
+    and samples. softcap and out_mult mean the same in both."""
+
+    def __init__(self, weight: torch.Tensor, norm_weight: Optional[torch.Tensor] = None,
+                 norm_bias: Optional[torch.Tensor] = None, *, eps: float = 1e-5, rms: bool = True, softcap: float = 0.0,
+                 out_mult: float = 1.0, ignore_index: int = -100, reduction: str = "mean"):
+        super().__init__()
+        if weight.dim() != 2:
+            raise ValueError("weight must be [V, H]")
+        self.weight = weight if isinstance(weight, torch.nn.Parameter) else torch.nn.Parameter(weight, requires_grad=False)
+        for name, t in (("norm_weight", norm_weight), ("norm_bias", norm_bias)):
+            if t is not None and t.shape != weight.shape[1:]:
+                raise ValueError(f"{name} must be [H]")
+            if t is not None and not isinstance(t, torch.nn.Parameter):
+                t = torch.nn.Parameter(t, requires_grad=False)
+            self.register_parameter(name, t)
+        self.eps, self.rms = float(eps), bool(rms)
+        self.softcap, self.out_mult = float(softcap), float(out_mult)
+        self.ignore_index, self.reduction = int(ignore_index), reduction
+        self.answers: Optional[MicroscaleTensor] = None
+
+    def normalise(self, hidden: torch.Tensor) -> torch.Tensor:
+        if torch.is_grad_enabled():
+            return layer_norm(hidden, self.norm_weight, self.norm_bias, eps=self.eps, rms=self.rms)
+        return flce_layer_norm(hidden, self.norm_weight, self.norm_bias, eps=self.eps, rms=self.rms)
+
+    def loss(self, hidden: torch.Tensor, labels: torch.Tensor):
+        """(loss, token_accuracy) of hidden [..., H] and int64 labels [...]."""
+        from . import linear_cross_entropy
+        return linear_cross_entropy(self.normalise(hidden), self.weight, labels, softcap=self.softcap,
+                                    out_mult=self.out_mult, ignore_index=self.ignore_index, reduction=self.reduction)
+
+    forward = loss
+
+    def prepare_answers(self) -> MicroscaleTensor:
+        """Microscales W for logits() and next_token(), and keeps it."""
+        self.answers = flce_microscale_quantize(self.weight.detach())
+        return self.answers
+
+    @torch.no_grad()
+    def logits(self, hidden: torch.Tensor, out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+        """Logits [..., V] on the microscaled W (made at the first call)."""
+        W = self.answers if self.answers is not None else self.prepare_answers()
+        return flce_microscale_linear(self.normalise(hidden), W, out_mult=self.out_mult, softcap=self.softcap,
+                                      out_dtype=out_dtype)
+
+    @torch.no_grad()
+    def next_token(self, hidden: torch.Tensor, u: torch.Tensor, **settings):
+        """(tokens, logprobs) for hidden [..., H] and random numbers u [...]; settings as in flce_sample."""
+        return flce_sample(self.logits(hidden), u, **settings)

@@ -51,6 +51,17 @@ EXPORTED = [
     "flce_profile_read", "flce_kernel_name", "flce_vp_workspace_size", "flce_vp_forward", "flce_vp_backward",
 ]
 
+# include/flce_head.h
+FLCE_SAMPLE_MAX_ROW_BYTES = 1474560
+FLCE_HEAD_KERNEL_FIRST = 32
+FLCE_HEAD_KERNEL_COUNT = 7
+
+HEAD_EXPORTED = [
+    "flce_layer_norm", "flce_layer_norm_workspace_size", "flce_layer_norm_backward", "flce_microscale_codes_size",
+    "flce_microscale_scales_size", "flce_microscale_quantize", "flce_microscale_dequantize",
+    "flce_microscale_workspace_size", "flce_microscale_matmul", "flce_microscale_linear", "flce_sample",
+]
+
 
 class FlceParams(ctypes.Structure):
     _fields_ = [
@@ -145,8 +156,29 @@ def lib() -> ctypes.CDLL:
                                        ctypes.POINTER(ctypes.c_int64), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                        _vp, _vp, _vp, _sz, _vp]
         L.flce_vp_backward.restype = ctypes.c_int
+        _bind_head(L)
         _lib = L
         return L
+
+
+def _bind_head(L: ctypes.CDLL) -> None:
+    """Argument types of the entries of include/flce_head.h."""
+    i, l, f = ctypes.c_int, ctypes.c_int64, ctypes.c_float
+    for name, res, args in (
+            ("flce_layer_norm", i, [_vp, i, l, l, l, _vp, _vp, i, f, i, _vp, _vp, _vp, _vp]),
+            ("flce_layer_norm_workspace_size", _sz, [l, l]),
+            ("flce_layer_norm_backward", i, [_vp, l, _vp, l, i, l, l, _vp, i, _vp, _vp, i, _vp, _vp, _vp, i, _vp, _sz,
+                                             _vp]),
+            ("flce_microscale_codes_size", _sz, [l, l]),
+            ("flce_microscale_scales_size", _sz, [l, l]),
+            ("flce_microscale_quantize", i, [_vp, i, l, l, l, _vp, _vp, _vp]),
+            ("flce_microscale_dequantize", i, [_vp, _vp, l, l, _vp, i, _vp]),
+            ("flce_microscale_workspace_size", _sz, [l, l]),
+            ("flce_microscale_matmul", i, [_vp, _vp, l, _vp, _vp, l, l, f, f, _vp, i, l, _vp, _sz, _vp]),
+            ("flce_microscale_linear", i, [_vp, i, l, l, _vp, _vp, l, l, f, f, _vp, i, l, _vp, _sz, _vp]),
+            ("flce_sample", i, [_vp, i, l, l, l, _vp, _vp, f, _vp, ctypes.c_int32, _vp, f, _vp, f, _vp, _vp, _vp])):
+        fn = getattr(L, name)
+        fn.restype, fn.argtypes = res, args
 
 
 def status_string(code: int) -> str:

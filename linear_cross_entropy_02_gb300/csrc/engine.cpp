@@ -29,6 +29,7 @@
 #include <mutex>
 #include <vector>
 
+#include "flce_host.h"
 #include "flce_internal.h"
 
 using namespace flce;
@@ -36,8 +37,6 @@ using namespace flce;
 namespace {
 
 constexpr int64_t kDefaultChunkRows = 8192;
-constexpr uint64_t kDefaultTimeoutNs = 2000000000ull;
-constexpr int kMaxDevices = 64;
 
 std::atomic<int64_t> g_launches{0};
 
@@ -50,31 +49,35 @@ std::mutex g_prof_mu;
 bool g_prof_on = false;
 std::vector<ProfRecord> g_prof;
 
-struct LaunchScope {
-  int kernel;
-  cudaStream_t stream;
-  cudaEvent_t start = nullptr, stop = nullptr;
-  LaunchScope(int k, cudaStream_t s) : kernel(k), stream(s) {
+}  // namespace
+
+namespace flce {
+
+LaunchScope::LaunchScope(int k, cudaStream_t s) : kernel(k), stream(s) {
+  std::lock_guard<std::mutex> lk(g_prof_mu);
+  if (!g_prof_on) return;
+  if (cudaEventCreate(&start) != cudaSuccess) {
+    start = nullptr;
+  } else if (cudaEventCreate(&stop) != cudaSuccess) {
+    cudaEventDestroy(start);
+    start = stop = nullptr;
+  } else {
+    cudaEventRecord(start, stream);
+  }
+}
+
+LaunchScope::~LaunchScope() {
+  g_launches.fetch_add(1);
+  if (start) {
+    cudaEventRecord(stop, stream);
     std::lock_guard<std::mutex> lk(g_prof_mu);
-    if (!g_prof_on) return;
-    if (cudaEventCreate(&start) != cudaSuccess) {
-      start = nullptr;
-    } else if (cudaEventCreate(&stop) != cudaSuccess) {
-      cudaEventDestroy(start);
-      start = stop = nullptr;
-    } else {
-      cudaEventRecord(start, stream);
-    }
+    g_prof.push_back({kernel, start, stop});
   }
-  ~LaunchScope() {
-    g_launches.fetch_add(1);
-    if (start) {
-      cudaEventRecord(stop, stream);
-      std::lock_guard<std::mutex> lk(g_prof_mu);
-      g_prof.push_back({kernel, start, stop});
-    }
-  }
-};
+}
+
+}  // namespace flce
+
+namespace {
 
 const char* const kKernelNames[FLCE_NUM_KERNELS] = {
     "prologue", "fwd_gemm_stats", "merge", "dlogits", "grad_h_gemm",
@@ -82,11 +85,20 @@ const char* const kKernelNames[FLCE_NUM_KERNELS] = {
     "ce_stats", "ce_grad", "recompute_dz_gemm", "convert_grad_h", "scale_gradient", "vp_merge",
     "split_tf32"};
 
+// Kernels of the operators around the head, from FLCE_HEAD_KERNEL_FIRST on.
+const char* const kHeadKernelNames[FLCE_HEAD_KERNEL_COUNT] = {
+    "layer_norm", "layer_norm_backward", "layer_norm_weight_grad", "microscale_quantize", "microscale_dequantize",
+    "microscale_gemm", "sample"};
+
+}  // namespace
+
+namespace flce {
+
 // ------------------------------------------------------------ device info
 // Per-device cache of the SM count and compute capability, packed into one
 // atomic word (cc << 16 | sms; 0 = not yet queried) so that host threads
 // making their first calls at once neither race nor see half an entry.
-std::atomic<uint32_t> g_dev_info[kMaxDevices] = {};
+static std::atomic<uint32_t> g_dev_info[kMaxDevices] = {};
 
 int device_info(int* sms, int* cc) {
   int dev = 0;
@@ -107,7 +119,7 @@ int device_info(int* sms, int* cc) {
 
 // ------------------------------------------------------------ tensor maps
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
-std::once_flag g_encode_once;
+static std::once_flag g_encode_once;
 
 bool load_encoder() {
   std::call_once(g_encode_once, [] {
@@ -121,6 +133,10 @@ bool load_encoder() {
   });
   return g_encode != nullptr;
 }
+
+}  // namespace flce
+
+namespace {
 
 // bf16 [outer][inner] with row stride `ld` elements; box = 64 x box_rows, 128-byte swizzle.
 bool encode_bf16(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t ld, uint32_t box_rows) {
@@ -392,12 +408,6 @@ bool pick_wide(int flags, const GemmParams& g, int sms) {
   const int64_t wide_waves = (units + sms - 1) / sms;
   return 182 * wide_waves < 100 * narrow;
 }
-
-#define FLCE_LAUNCH(kid, expr)                         \
-  do {                                                 \
-    LaunchScope _scope((kid), stream);                 \
-    if ((expr) != cudaSuccess) return FLCE_ERR_CUDA;   \
-  } while (0)
 
 struct Call {
   int mode;  // FLCE_MODE_*; host inputs come as FORWARD_BACKWARD or CE_ONLY with host_in set
@@ -1736,6 +1746,8 @@ int flce_profile_read(int64_t* launches, double* total_ms, int n) {
 }
 
 const char* flce_kernel_name(int id) {
+  if (id >= FLCE_HEAD_KERNEL_FIRST && id < FLCE_HEAD_KERNEL_FIRST + FLCE_HEAD_KERNEL_COUNT)
+    return kHeadKernelNames[id - FLCE_HEAD_KERNEL_FIRST];
   if (id < 0 || id >= FLCE_NUM_KERNELS) return "unknown";
   return kKernelNames[id];
 }

@@ -1,0 +1,366 @@
+// out = cap(m A W^T) of microscaled 4-bit operands on the tensor cores:
+// tcgen05.mma kind::mxf4 with a power-of-two scale per 32 elements, products
+// summed in fp32 in tensor memory.
+//
+// W's rows are the M dimension (128 vocabulary entries per tile) and the tokens
+// the N dimension, so that one token and a whole prompt run through the same
+// kernel: for a few tokens the tile is 128 x 16 and the kernel streams W once
+// through a deep ring of TMA copies, bound by HBM; for a prompt it is 128 x 192
+// and bound by the tensor cores and the L2. A lane of tensor memory is then a
+// vocabulary entry, and a warp's store for one token is one contiguous run of
+// logits whatever the row stride's alignment.
+//
+// K advances 256 elements (one 128-byte swizzle row of codes) per stage. Scales
+// come from HBM already in the order of tensor memory, 512 bytes per 128 rows x
+// 128 elements: one bulk copy per stage and operand, then tcgen05.cp spreads
+// each tile over four columns. An instruction covers K = 64 and picks its two
+// scale bytes of each column by the scale ids in its descriptor.
+//
+// Warp 0 loads, warp 1 issues the MMAs, warps 2-5 store: two accumulators, so
+// that the stores of one tile run under the MMAs of the next. Every wait is
+// bounded (flce_device.cuh) and ends the call with FLCE_ERR_TIMEOUT.
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include <atomic>
+
+#include "flce_device.cuh"
+#include "flce_host.h"
+#include "head_device.cuh"
+#include "head_internal.h"
+
+namespace flce {
+
+namespace {
+
+constexpr int kTileV = 128;                // vocabulary rows per tile
+constexpr int kStageK = 256;               // elements of K per stage
+constexpr int kRowBytes = 128;             // bytes of a row per stage
+constexpr int kWBytes = kTileV * kRowBytes;
+constexpr int kSfTiles = kStageK / kMxTileCols;  // scale tiles per 128 rows and stage
+constexpr int kThreads = 192;
+constexpr int kSmemBudget = 226 * 1024;
+
+// Shared and tensor memory of a tile of NT tokens.
+template <int NT>
+struct Plan {
+  static constexpr int row_tiles = (NT + 127) / 128;  // 128-row scale tiles that the tokens can touch
+  static constexpr int x_bytes = NT * kRowBytes;
+  static constexpr int w_sf = kSfTiles * kMxTileBytes;
+  static constexpr int x_sf = row_tiles * kSfTiles * kMxTileBytes;
+  static constexpr int stage = kWBytes + x_bytes + w_sf + x_sf;
+  static constexpr int d_cols = NT < 32 ? 32 : NT;      // one accumulator
+  static constexpr int sf_cols = 4 * kSfTiles * (1 + row_tiles);
+  static constexpr int by_smem = (kSmemBudget - 2048) / stage;
+  static constexpr int by_tmem = (512 - 2 * d_cols) / sf_cols;
+  static constexpr int stages = by_smem < by_tmem ? (by_smem < 10 ? by_smem : 10) : (by_tmem < 10 ? by_tmem : 10);
+  static constexpr int used_cols = 2 * d_cols + stages * sf_cols;
+  static constexpr int tmem_cols = used_cols <= 128 ? 128 : used_cols <= 256 ? 256 : 512;
+  static constexpr int smem = stages * stage + 1024 + 256;
+  static_assert(x_bytes % 1024 == 0, "operand tiles start on a swizzle atom");
+};
+
+struct MxArgs {
+  const uint8_t* w_scales;
+  const uint8_t* x_scales;
+  int rows, vocab, k_iters, k_tiles, k_mmas;  // k_mmas: instructions over all of K
+  int x_row_tiles;
+  int v_tiles, n_tiles;
+  float out_mult, softcap, inv_softcap;
+  void* out;
+  int64_t ld_out;
+  int32_t* status;
+  uint64_t timeout_ns;
+};
+
+// Instruction descriptor of kind::mxf4: E2M1 operands (1 in bits 7-9 and 10-12),
+// N >> 3 in bits 17-22, E8M0 scales (bit 23), M >> 4 in bits 24-28, and the
+// scale ids of B (bits 4-5) and A (bits 29-30): the byte of each 32-bit column
+// at which the instruction's two scales begin.
+__host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N, int sf) {
+  return (static_cast<uint32_t>(sf) << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (1u << 23) | (static_cast<uint32_t>(M >> 4) << 24) | (static_cast<uint32_t>(sf) << 29);
+}
+
+__device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                         uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+
+// One scale tile (32 rows of 16 bytes) into four columns, in all four lane quarters.
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+
+// Descriptor of a scale tile: no swizzle, eight-row groups 128 bytes apart.
+__device__ __forceinline__ uint64_t sdesc_scales(uint32_t smem_addr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(128u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  return d;
+}
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+template <int NT, typename T>
+__global__ void __launch_bounds__(kThreads, 1)
+    mx_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                   const MxArgs p) {
+  using P = Plan<NT>;
+  constexpr int S = P::stages;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* s_w = smem;
+  uint8_t* s_x = s_w + S * kWBytes;
+  uint8_t* s_wsf = s_x + S * P::x_bytes;
+  uint8_t* s_xsf = s_wsf + S * P::w_sf;
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_xsf + S * P::x_sf);
+  uint64_t* empty = full + S;
+  uint64_t* tfull = empty + S;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* mma_done = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+  int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], 128);
+    }
+    mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&map_w);
+    tma_prefetch_desc(&map_x);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, P::tmem_cols);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  const WaitCtx wc{abort_flag, p.status, p.timeout_ns};
+  const int total = p.v_tiles * p.n_tiles;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0, issued = 0;
+      uint32_t phase = 0;
+      bool aborted = false;
+      for (int t = blockIdx.x; t < total && !aborted; t += gridDim.x) {
+        const int vb = t / p.n_tiles, nb = t - vb * p.n_tiles;  // a tile of W meets all tokens while it is in the L2
+        const int xt0 = nb * NT / 128;
+        const int xts = min(P::row_tiles, p.x_row_tiles - xt0);
+        for (int k = 0; k < p.k_iters; ++k) {
+          if (!wait_bounded(&empty[stage], phase ^ 1u, wc)) {
+            aborted = true;
+            break;
+          }
+          const int kt = k * kSfTiles;
+          const uint32_t sf = static_cast<uint32_t>(min(kSfTiles, p.k_tiles - kt)) * kMxTileBytes;
+          mbar_arrive_expect_tx(&full[stage], kWBytes + P::x_bytes + sf * (1 + xts));
+          tma_load_2d(s_w + stage * kWBytes, &map_w, &full[stage], k * kRowBytes, vb * kTileV);
+          tma_load_2d(s_x + stage * P::x_bytes, &map_x, &full[stage], k * kRowBytes, nb * NT);
+          bulk_load(s_wsf + stage * P::w_sf, p.w_scales + (static_cast<int64_t>(vb) * p.k_tiles + kt) * kMxTileBytes,
+                    sf, &full[stage]);
+          for (int i = 0; i < xts; ++i)
+            bulk_load(s_xsf + stage * P::x_sf + i * kSfTiles * kMxTileBytes,
+                      p.x_scales + (static_cast<int64_t>(xt0 + i) * p.k_tiles + kt) * kMxTileBytes, sf, &full[stage]);
+          ++issued;
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (aborted) {
+        // loads that may still be in flight land before the shared memory goes away
+        const int n = issued < S ? issued : S;
+        int s = stage;
+        uint32_t ph = phase;
+        for (int i = 0; i < n; ++i) {
+          if (s == 0) {
+            s = S - 1;
+            ph ^= 1u;
+          } else {
+            --s;
+          }
+          wait_drain(&full[s], ph, p.timeout_ns, p.status);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool aborted = false;
+      const uint32_t w0 = smem_u32(s_w), x0 = smem_u32(s_x), wsf0 = smem_u32(s_wsf), xsf0 = smem_u32(s_xsf);
+      for (int t = blockIdx.x; t < total && !aborted; t += gridDim.x) {
+        const int nb = t % p.n_tiles;
+        const uint32_t x_shift = static_cast<uint32_t>(nb * NT % 128 / 32);  // first 32-row group of the tokens
+        if (!wait_bounded(&tempty[acc], acc_phase ^ 1u, wc)) break;
+        tc_fence_after_sync();
+        const uint32_t d = tmem + static_cast<uint32_t>(acc * P::d_cols);
+        for (int k = 0; k < p.k_iters; ++k) {
+          if (!wait_bounded(&full[stage], phase, wc)) {
+            aborted = true;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint32_t sf = tmem + static_cast<uint32_t>(2 * P::d_cols + stage * P::sf_cols);
+          const uint32_t sfx = sf + 4 * kSfTiles;
+          const int mmas = min(kStageK / 64, p.k_mmas - k * (kStageK / 64));
+          for (int j = 0; j * 2 < mmas; ++j) {
+            copy_scales(sf + 4 * j, sdesc_scales(wsf0 + stage * P::w_sf + j * kMxTileBytes));
+#pragma unroll
+            for (int i = 0; i < P::row_tiles; ++i)
+              copy_scales(sfx + 4 * (j * P::row_tiles + i),
+                          sdesc_scales(xsf0 + stage * P::x_sf + (i * kSfTiles + j) * kMxTileBytes));
+          }
+          for (int j = 0; j < mmas; ++j) {
+            const uint64_t a = sdesc_kmajor_sw128(w0 + stage * kWBytes + j * 32);
+            const uint64_t b = sdesc_kmajor_sw128(x0 + stage * P::x_bytes + j * 32);
+            mma_mxf4(d, a, b, (j & 1) ? idesc_mxf4(kTileV, NT, 2) : idesc_mxf4(kTileV, NT, 0), sf + 4 * (j >> 1),
+                     sfx + 4 * (j >> 1) * P::row_tiles + x_shift, (k | j) != 0 ? 1u : 0u);
+          }
+          tc_commit(&empty[stage]);
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (aborted) break;
+        tc_commit(&tfull[acc]);
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+      tc_commit(mma_done);
+      wait_drain(mma_done, 0, p.timeout_ns, p.status);
+    }
+  } else {
+    const int quarter = warp & 3;
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int t = blockIdx.x; t < total; t += gridDim.x) {
+      const int vb = t / p.n_tiles, nb = t - vb * p.n_tiles;
+      const bool ok = wait_bounded(&tfull[acc], acc_phase, wc);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after_sync();
+      const int v = vb * kTileV + quarter * 32 + lane;
+      const int n0 = nb * NT;
+      const int n_here = min(NT, p.rows - n0);
+      for (int c = 0; c < n_here; c += 32) {
+        uint32_t r[32];
+        tmem_load_32cols(t_lane + acc * P::d_cols + c, r);
+        tmem_load_wait_regs(r);
+        T* o = static_cast<T*>(p.out) + static_cast<int64_t>(n0 + c) * p.ld_out + v;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          if (c + j < n_here && v < p.vocab) {
+            float z = __uint_as_float(r[j]) * p.out_mult;
+            if (p.softcap > 0.f) z = p.softcap * tanhf(z * p.inv_softcap);
+            o[j * p.ld_out] = from_float<T>(z);
+          }
+        }
+      }
+      tc_fence_before_sync();
+      mbar_arrive(&tempty[acc]);
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, P::tmem_cols);
+  }
+}
+
+// Codes as bytes [rows][cols / 2], boxes of 128 bytes x box_rows, 128-byte swizzle.
+bool encode_codes(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int box_rows) {
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols / 2), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols / 2)};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(kRowBytes), static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t es[2] = {1, 1};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int NT, typename T>
+int run_tile(const MxGemmParams& p, int sms, cudaStream_t stream) {
+  using P = Plan<NT>;
+  auto kernel = mx_gemm_kernel<NT, T>;
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return FLCE_ERR_CUDA;
+  if (!(done.load() >> dev & 1)) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, P::smem) != cudaSuccess)
+      return FLCE_ERR_CUDA;
+    done.fetch_or(1ull << dev);
+  }
+  CUtensorMap map_w, map_x;
+  if (!encode_codes(&map_w, p.w_codes, p.vocab, p.cols, kTileV) || !encode_codes(&map_x, p.a_codes, p.rows, p.cols, NT))
+    return FLCE_ERR_UNSUPPORTED;
+  MxArgs a;
+  a.w_scales = p.w_scales;
+  a.x_scales = p.a_scales;
+  a.rows = static_cast<int>(p.rows);
+  a.vocab = static_cast<int>(p.vocab);
+  a.k_iters = static_cast<int>((p.cols + kStageK - 1) / kStageK);
+  a.k_tiles = static_cast<int>((p.cols + kMxTileCols - 1) / kMxTileCols);
+  a.k_mmas = static_cast<int>((p.cols + 63) / 64);
+  a.x_row_tiles = static_cast<int>((p.rows + 127) / 128);
+  a.v_tiles = static_cast<int>((p.vocab + kTileV - 1) / kTileV);
+  a.n_tiles = static_cast<int>((p.rows + NT - 1) / NT);
+  a.out_mult = p.out_mult;
+  a.softcap = p.softcap;
+  a.inv_softcap = p.inv_softcap;
+  a.out = p.out;
+  a.ld_out = p.ld_out;
+  a.status = p.status;
+  a.timeout_ns = p.timeout_ns;
+  const int64_t total = static_cast<int64_t>(a.v_tiles) * a.n_tiles;
+  if (total >= (1LL << 31)) return FLCE_ERR_ARG;
+  const int grid = static_cast<int>(total < sms ? total : sms);
+  FLCE_LAUNCH(K_MX_GEMM, (kernel<<<grid, kThreads, P::smem, stream>>>(map_w, map_x, a), cudaGetLastError()));
+  return FLCE_OK;
+}
+
+template <typename T>
+int run_typed(const MxGemmParams& p, int sms, cudaStream_t s) {
+  if (p.rows <= 16) return run_tile<16, T>(p, sms, s);
+  if (p.rows <= 32) return run_tile<32, T>(p, sms, s);
+  if (p.rows <= 64) return run_tile<64, T>(p, sms, s);
+  if (p.rows <= 128) return run_tile<128, T>(p, sms, s);
+  return run_tile<192, T>(p, sms, s);
+}
+
+}  // namespace
+
+int launch_mx_gemm(const MxGemmParams& p, int sms, cudaStream_t s) {
+  if (!load_encoder()) return FLCE_ERR_UNSUPPORTED;
+  return p.out_dtype == FLCE_DTYPE_F32 ? run_typed<float>(p, sms, s) : run_typed<uint16_t>(p, sms, s);
+}
+
+}  // namespace flce

@@ -1,0 +1,153 @@
+"""The head as a model has it: norm, loss and next token through one object, and
+the host-side agreement of include/flce_head.h with its binding."""
+import os
+import re
+
+import pytest
+import torch
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def header():
+    with open(os.path.join(ROOT, "include", "flce_head.h")) as f:
+        return re.sub(r"/\*.*?\*/", "", f.read(), flags=re.S)
+
+
+def test_header_matches_binding():
+    from linear_cross_entropy_02_gb300 import _lib
+    names = sorted(set(re.findall(r"\b(flce_[a-z_]+)\s*\(", header())))
+    assert sorted(_lib.HEAD_EXPORTED) == names
+    for n in names:
+        assert hasattr(_lib.lib(), n), n
+    for name, val in re.findall(r"#define (FLCE_[A-Z0-9_]+) (\d+)", header()):
+        assert getattr(_lib, name) == int(val), name
+
+
+def test_argument_counts_match_the_header():
+    from linear_cross_entropy_02_gb300 import _lib
+    for name, args in re.findall(r"\b(flce_[a-z_]+)\s*\(([^)]*)\)\s*;", header()):
+        assert len(getattr(_lib.lib(), name).argtypes) == args.count(",") + 1, name
+
+
+def test_kernel_names_of_the_head():
+    from linear_cross_entropy_02_gb300 import _lib as B
+    first, n = B.FLCE_HEAD_KERNEL_FIRST, B.FLCE_HEAD_KERNEL_COUNT
+    names = [B.lib().flce_kernel_name(i).decode() for i in range(first, first + n)]
+    assert names == ["layer_norm", "layer_norm_backward", "layer_norm_weight_grad", "microscale_quantize",
+                     "microscale_dequantize", "microscale_gemm", "sample"]
+    assert B.lib().flce_kernel_name(first - 1) == B.lib().flce_kernel_name(first + n) == b"unknown"
+
+
+def test_header_is_plain_c(tmp_path):
+    import subprocess
+    src = tmp_path / "t.c"
+    src.write_text('#include "flce_head.h"\nint main(void) { return flce_sample == 0; }\n')
+    r = subprocess.run(["gcc", "-std=c99", "-Wall", "-Werror", "-fsyntax-only", "-Wno-address", "-I",
+                        os.path.join(ROOT, "include"), str(src)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+
+
+def make(seed=0, V=1000, H=256, dtype=torch.bfloat16):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    W = (torch.randn(V, H, generator=g, device="cuda") * 0.1).to(dtype)
+    n = (1 + 0.1 * torch.randn(H, generator=g, device="cuda")).to(dtype)
+    h = torch.randn(3, 20, H, generator=g, device="cuda").to(dtype)
+    y = torch.randint(0, V, (3, 20), generator=g, device="cuda")
+    return W, n, h, y
+
+
+@pytest.mark.gpu
+def test_loss_and_gradients_through_the_norm():
+    import linear_cross_entropy_02_gb300 as flce
+    W, n, h, y = make()
+    W, n, h = torch.nn.Parameter(W), torch.nn.Parameter(n), h.requires_grad_()
+    y[0, :4] = -100
+    head = flce.LanguageModelHead(W, n, softcap=15.0, out_mult=0.5)
+    loss, _ = head(h, y)
+    loss.backward()
+    h64, n64, W64 = (t.detach().double().requires_grad_() for t in (h, n, W))
+    x = h64 * (h64.square().mean(-1, keepdim=True) + 1e-5).rsqrt() * n64
+    z = 15.0 * torch.tanh(0.5 * (x @ W64.t()) / 15.0)
+    ref = torch.nn.functional.cross_entropy(z.view(-1, 1000), y.view(-1))
+    ref.backward()
+    # x is rounded to bf16 between the two operators, dlogits inside the second: at most 2^-8 of an element each, and the outputs once more
+    assert abs(float(loss.detach()) - float(ref)) <= 2e-3 * float(ref)
+    for a, b in ((h, h64), (n, n64), (W, W64)):
+        assert float((a.grad.double() - b.grad).norm()) <= 1e-2 * float(b.grad.norm())
+
+
+@pytest.mark.gpu
+def test_answers_are_the_operators_one_after_another():
+    import linear_cross_entropy_02_gb300 as flce
+    W, n, h, _ = make(1)
+    head = flce.LanguageModelHead(W, n, softcap=30.0)
+    u = torch.rand(3, 20, device="cuda")
+    x = flce.flce_layer_norm(h, n, rms=True)
+    z = flce.flce_microscale_linear(x, flce.flce_microscale_quantize(W), softcap=30.0)
+    assert torch.equal(head.logits(h), z)
+    t, lp = head.next_token(h, u, temperature=0.8, top_k=20, top_p=0.9)
+    t2, lp2 = flce.flce_sample(z, u, temperature=0.8, top_k=20, top_p=0.9)
+    assert torch.equal(t, t2) and torch.equal(lp, lp2)
+    # the answer of one token alone is that of the batch
+    one, _ = head.next_token(h[1, 7], u[1, 7], temperature=0.8, top_k=20, top_p=0.9)
+    assert int(one) == int(t[1, 7])
+    # greedy answers follow the full-precision logits where the gap is wide: a planted row
+    h[0, 0] = (W[123].float() * 40).to(h.dtype)
+    assert int(head.next_token(h, u, temperature=0.0)[0][0, 0]) == 123
+    # W changed: laid out again on request
+    head.weight.data[5] = head.weight.data[123]
+    head.weight.data[123] = 0
+    head.prepare_answers()
+    assert int(head.next_token(h, u, temperature=0.0)[0][0, 0]) == 5
+
+
+@pytest.mark.gpu
+def test_answers_replay_in_a_graph():
+    """One token through norm, product and sampling, captured and replayed on new inputs."""
+    import linear_cross_entropy_02_gb300 as flce
+    W, n, h, _ = make(2)
+    head = flce.LanguageModelHead(W, n)
+    x, u = h[0, :1].clone(), torch.rand(1, device="cuda")
+    kw = dict(temperature=0.9, top_k=50, top_p=0.95)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        head.next_token(x, u, **kw)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        tokens, lp = head.next_token(x, u, **kw)
+    for i in range(5):
+        x.copy_(h[1, i:i + 1])
+        u.fill_(0.1 + 0.2 * i)
+        graph.replay()
+        want, want_lp = head.next_token(x, u, **kw)
+        assert torch.equal(tokens, want) and torch.equal(lp, want_lp)
+
+
+@pytest.mark.gpu
+def test_launches_are_counted_and_timed():
+    import linear_cross_entropy_02_gb300 as flce
+    W, n, h, _ = make(3)
+    head = flce.LanguageModelHead(W, n)
+    u = torch.rand(3, 20, device="cuda")
+    head.next_token(h, u)
+    flce.flce_profile_begin(True)
+    before = flce.flce_launch_count()
+    head.next_token(h, u)
+    got = flce.flce_profile_read()
+    flce.flce_profile_begin(False)
+    assert flce.flce_launch_count() - before == sum(c for c, _ in got.values())
+    assert {"layer_norm", "microscale_gemm", "sample"} <= set(got) and all(ms > 0 for _, ms in got.values())
+
+
+def test_refusals_without_a_gpu():
+    import linear_cross_entropy_02_gb300 as flce
+    W = torch.zeros(10, 32)
+    with pytest.raises(ValueError):
+        flce.LanguageModelHead(W[0])
+    with pytest.raises(ValueError):
+        flce.LanguageModelHead(W, torch.zeros(31))
+    with pytest.raises(ValueError, match="CUDA"):
+        flce.LanguageModelHead(W).next_token(torch.zeros(2, 32), torch.zeros(2))
