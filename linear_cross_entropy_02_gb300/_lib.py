@@ -52,7 +52,6 @@ EXPORTED = [
 ]
 
 # include/flce_head.h
-FLCE_SAMPLE_MAX_ROW_BYTES = 1474560
 FLCE_HEAD_KERNEL_FIRST = 32
 FLCE_HEAD_KERNEL_COUNT = 7
 

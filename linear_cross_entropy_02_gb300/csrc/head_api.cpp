@@ -269,7 +269,6 @@ int flce_sample(const void* logits, int logits_dtype, int64_t rows, int64_t voca
     return FLCE_ERR_ARG;
   if ((!temperatures && std::isnan(temperature)) || (!top_ps && std::isnan(top_p)) || (!min_ps && std::isnan(min_p)))
     return FLCE_ERR_ARG;
-  if (static_cast<size_t>(vocab) * element_size(logits_dtype) > FLCE_SAMPLE_MAX_ROW_BYTES) return FLCE_ERR_UNSUPPORTED;
   if (rows == 0) return FLCE_OK;
   if (!logits || !u || !tokens) return FLCE_ERR_ARG;
   if (!aligned(logits, element_size(logits_dtype)) || !aligned(u, 4) || !aligned(temperatures, 4) ||

@@ -1,29 +1,35 @@
 // One token per row of logits: temperature, top-k, top-p, min-p, and the inverse
 // of the kept tokens' distribution function at a given random number.
 //
-// Nothing is sorted. In rank order (falling logit, ties by index) every filter
-// keeps a prefix, so the kept set is described by one logit t and a number c:
-// all logits above t, and the first c of those equal to t. top-k needs t at a
-// count, top-p at a weight; both come from a histogram of 1024 bins followed by
-// an exact look at the bin that holds the answer. Weights are whole multiples
-// of 2^-40 of the largest one and are added as 64-bit integers, so that no sum
-// depends on the order or on how many CTAs share a row: the token is a function
-// of the logits, the settings and u alone.
+// The row is never sorted. In rank order (falling logit, ties by index) every
+// filter keeps a prefix, so only its end has to be found. Weights are whole
+// multiples of 2^-40 of the largest one and are added as 64-bit integers, so
+// that no sum depends on the order or on how many CTAs share a row: the token is
+// a function of the logits, the settings and u alone.
 //
-// Bound by memory: a row is read from HBM once, into the shared memory of a
-// cluster of up to eight CTAs, which exchange maxima, histograms and sums
-// through distributed shared memory. The steps, with a cluster barrier after
-// each: load and maximum; histogram; look into the bin; running sums and the
-// answer. top_k of up to kListKeys / 2 takes a shorter way: the k-th largest of
-// the threads' own maxima bounds the k-th logit from below, the few logits
-// above the bound are collected in one CTA and sorted there, and the rest of
-// the cluster is done.
+// A row takes two passes. The first reads it from HBM, keeps the maximum and
+// counts logits in 2048 bins of (x - anchor) / T, the anchor being the maximum
+// of the row's first part. Then:
+//   top_k that some bins cover with at most kListKeys logits: the second pass
+//     collects those logits in shared memory; they are sorted there, cut by all
+//     three filters, and the token is drawn from them.
+//   top_p: the counts times the weights of the bins' middles (exact float sums
+//     for the few largest) say in which bins the end of the prefix should lie;
+//     the second pass adds up all weights exactly, those above these bins by
+//     segments of the vocabulary, and collects the logits in the bins. The exact
+//     sums then confirm that the end lies among the collected logits.
+//   neither: the second pass adds up the weights by segments.
+// The segment that holds the answer is walked once more by a warp. Rows for
+// which this does not work out (more than kListKeys logits in the way, as when
+// most are equal, or an estimate that the exact sums refute) go through the
+// general selection: a histogram of exact weights, then splitting the bin that
+// holds the answer by the logits' bits until it is small enough or all equal.
 //
-// The histogram's bins are equal steps of the scaled distance from the maximum,
-// t = (x - m) / T in (-28, 0]; beyond that a weight rounds to zero. If the bin
-// that holds the answer has too many logits to list (bf16 logits repeat), it is
-// split by the bits of their order-preserving integers until it has few
-// enough or all are equal.
+// One CTA per row where there are rows for every SM: all exchange is within
+// the CTA, and the second pass finds the row in shared memory or, if it is too
+// long, in the L2 (152 rows of 0.5 MB fit). Few rows are spread over a cluster
+// of up to eight CTAs each, with maxima, counts and sums exchanged through
+// distributed shared memory.
 #include <math.h>
 
 #include <atomic>
@@ -36,39 +42,73 @@ namespace flce {
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kBins = 1024;
-constexpr int kListKeys = 2048;
+constexpr int kListKeys = 8192;
 constexpr float kRange = 28.f;  // exp(-28) 2^40 < 1
-constexpr float kBinsPerUnit = (kBins - 1) / kRange;
 constexpr float kFixed = 1099511627776.f;  // 2^40
-constexpr int kMaxSlice = FLCE_SAMPLE_MAX_ROW_BYTES / kMaxCluster;
+
+// General selection.
+constexpr int kBins = 1024;
+constexpr float kBinsPerUnit = (kBins - 1) / kRange;
+// Counts of the first pass: 2048 bins from 28 above the anchor to 28 below it.
+constexpr int kCountBins = 2048;
+constexpr int kAnchorBin = kCountBins / 2;
+constexpr float kCountsPerUnit = kAnchorBin / kRange;
+// Logits above 3 below the anchor are weighed one by one for the estimate: a
+// bin's middle is up to 1.4% off for one logit, which only matters where a few
+// logits carry the row. (All of a normal row's logits would slow the pass:
+// 3 below the maximum there are some per cent of them.)
+constexpr int kWeighedBins = kAnchorBin + 110;
+// How far around the estimated end logits are collected, of the whole weight:
+// the first margin if the list holds what lies in it, else the second.
+constexpr float kMargin = 0.0015f, kSmallMargin = 0.0002f;
+// Segments of a slice whose weights are kept apart: eight per warp.
+constexpr int kSubs = 8;
+constexpr int kSegments = kWarps * kSubs;
+constexpr int kFirstVectors = 4;  // per thread: the part of the row that sets the anchor
+constexpr int kAnswerBins = 2048;   // segments of the vocabulary for a list of kept tokens
+constexpr int kMostShared = 227 * 1024;
 
 struct Hist {
   uint32_t count[kBins];
   uint32_t lo[kBins];  // 64-bit weights in halves: shared memory adds 32 bits at a time
   uint32_t hi[kBins];
 };
+struct Counts {
+  uint32_t count[kCountBins];
+  float weight[kWeighedBins];
+};
+struct Answer {
+  uint32_t lo[kAnswerBins], hi[kAnswerBins];
+};
 
 // Shared memory of a CTA in front of its slice of the row; the same place in
 // every CTA of the cluster.
 struct Shared {
-  Hist hist[2];
   uint64_t list[kListKeys];
-  uint64_t seg_weight[kWarps];
+  union {
+    Hist hist[2];
+    Counts counts;
+    Answer answer;
+  };
+  uint64_t seg_weight[kSegments];
   uint32_t seg_ties[kWarps];
   uint64_t scan[kWarps + 1];
-  uint64_t found_above;
+  uint64_t sum_total, sum_above;  // of this slice, in the second pass
+  uint64_t found_above, found_value;
   uint32_t found_bin, found_count;
   float top;
   uint32_t bad;
   uint32_t first;      // lowest index of the largest logit in this slice
   uint32_t key_lo, key_hi;
-  uint32_t listed[3];  // lengths of the lists of a row, one counter per use
+  uint32_t listed[4];  // lengths of the lists of a row, one counter per use
   uint32_t result_key, result_count;
+  unsigned long long cut_lo[2], cut_hi[2];  // first and last bin to collect; low words: logits before and up to them
+  uint32_t general;         // CTA 0: the row needs the general selection
   uint32_t red[kWarps], red2[kWarps];
+  float fscan[kWarps];
 };
 
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -78,42 +118,63 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
 }
+// Rank order of a list: falling logit, then rising index.
+__device__ __forceinline__ uint64_t list_entry(float x, uint32_t index) {
+  return static_cast<uint64_t>(~order_key(x)) << 32 | index;
+}
+__device__ __forceinline__ float entry_value(uint64_t e) { return key_value(~static_cast<uint32_t>(e >> 32)); }
 
-// Barrier of the cluster's threads. Not the aligned form: threads come here
-// from code that only some of them run.
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+// ---------------------------------------------------------------- the row's CTAs
+// MULTI: the row is shared by a cluster; else by one CTA, and these are plain
+// barriers and accesses.
+// The cluster's barrier is not the aligned form: threads come here from code
+// that only some of them run.
+template <bool MULTI>
+__device__ __forceinline__ void row_barrier() {
+  if constexpr (MULTI)
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+  else
+    __syncthreads();
 }
 
-// Addresses and accesses in the shared memory of CTA `rank` of the cluster.
-template <typename V>
-__device__ __forceinline__ V remote(const V* mine, uint32_t rank) {
-  const uint32_t a = mapa_shared(smem_u32(mine), rank);
-  if constexpr (sizeof(V) == 8) {
-    uint64_t v;
-    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
-    return static_cast<V>(v);
+template <bool MULTI>
+__device__ __forceinline__ uint32_t remote(const uint32_t* mine, uint32_t rank) {
+  if constexpr (!MULTI) return *mine;
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(smem_u32(mine), rank)) : "memory");
+  return v;
+}
+template <bool MULTI>
+__device__ __forceinline__ float remote(const float* mine, uint32_t rank) {
+  return __uint_as_float(remote<MULTI>(reinterpret_cast<const uint32_t*>(mine), rank));
+}
+template <bool MULTI>
+__device__ __forceinline__ uint64_t remote(const uint64_t* mine, uint32_t rank) {
+  if constexpr (!MULTI) return *mine;
+  uint64_t v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(mapa_shared(smem_u32(mine), rank)) : "memory");
+  return v;
+}
+
+// Appends to CTA 0's list; what does not fit is only counted.
+template <bool MULTI>
+__device__ __forceinline__ void append(Shared& s, uint32_t* listed, uint64_t entry) {
+  if constexpr (!MULTI) {
+    const uint32_t at = atomicAdd(listed, 1u);
+    if (at < static_cast<uint32_t>(kListKeys)) s.list[at] = entry;
   } else {
-    uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-    if constexpr (sizeof(V) == 4 && static_cast<V>(0.5f) != static_cast<V>(0))
-      return __uint_as_float(v);
-    else
-      return static_cast<V>(v);
+    uint32_t at;
+    asm volatile("atom.shared::cluster.add.u32 %0, [%1], 1;"
+                 : "=r"(at)
+                 : "r"(mapa_shared(smem_u32(listed), 0))
+                 : "memory");
+    if (at < static_cast<uint32_t>(kListKeys))
+      asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(mapa_shared(smem_u32(&s.list[at]), 0)), "l"(entry)
+                   : "memory");
   }
 }
-__device__ __forceinline__ uint32_t remote_add(uint32_t* mine, uint32_t rank, uint32_t v) {
-  uint32_t old;
-  asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;"
-               : "=r"(old)
-               : "r"(mapa_shared(smem_u32(mine), rank)), "r"(v)
-               : "memory");
-  return old;
-}
-__device__ __forceinline__ void remote_store(uint64_t* mine, uint32_t rank, uint64_t v) {
-  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(mapa_shared(smem_u32(mine), rank)), "l"(v) : "memory");
-}
 
+// ---------------------------------------------------------------- sums and sorts in a CTA
 __device__ __forceinline__ uint64_t warp_inclusive(uint64_t v) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -123,9 +184,14 @@ __device__ __forceinline__ uint64_t warp_inclusive(uint64_t v) {
   }
   return v;
 }
+__device__ __forceinline__ uint64_t warp_total(uint64_t v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
 
-// Exclusive prefix sum over the CTA's threads; *total gets the whole. Begins and
-// ends with a barrier, so `scan` may be used again at once.
+// Exclusive prefix sum over the CTA's threads; *total gets the whole. Begins
+// with a barrier, so `scan` may be used again at once.
 __device__ uint64_t block_exclusive(uint64_t v, uint64_t* scan, uint64_t* total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t inc = warp_inclusive(v);
@@ -133,24 +199,44 @@ __device__ uint64_t block_exclusive(uint64_t v, uint64_t* scan, uint64_t* total)
   if (lane == 31) scan[warp] = inc;
   __syncthreads();
   if (warp == 0) {
-    const uint64_t w = lane < kWarps ? scan[lane] : 0;
+    const uint64_t w = scan[lane];
     const uint64_t wi = warp_inclusive(w);
     __syncwarp();
-    if (lane < kWarps) scan[lane] = wi - w;
-    if (lane == kWarps - 1) scan[kWarps] = wi;
+    scan[lane] = wi - w;
+    if (lane == 31) scan[kWarps] = wi;
   }
   __syncthreads();
   *total = scan[kWarps];
   return scan[warp] + inc - v;
 }
 
+__device__ float block_exclusive(float v, float* scan, float* total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const float n = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += n;
+  }
+  __syncthreads();
+  if (lane == 31) scan[warp] = inc;
+  __syncthreads();
+  float before = 0.f, all = 0.f;
+  for (int w = 0; w < kWarps; ++w) {  // one order for every thread
+    if (w == warp) before = all;
+    all += scan[w];
+  }
+  *total = all;
+  return before + inc - v;
+}
+
 // Adds a 64-bit weight to a bin, in halves with the carry.
-__device__ __forceinline__ void add_weight(Hist& h, int b, uint64_t w) {
-  const uint32_t lo = static_cast<uint32_t>(w);
-  uint32_t hi = static_cast<uint32_t>(w >> 32);
-  const uint32_t old = atomicAdd(&h.lo[b], lo);
-  if (old > ~lo) ++hi;
-  if (hi) atomicAdd(&h.hi[b], hi);
+__device__ __forceinline__ void add_weight(uint32_t* lo, uint32_t* hi, uint64_t w) {
+  const uint32_t low = static_cast<uint32_t>(w);
+  uint32_t high = static_cast<uint32_t>(w >> 32);
+  const uint32_t old = atomicAdd(lo, low);
+  if (old > ~low) ++high;
+  if (high) atomicAdd(hi, high);
 }
 
 // The smallest whole number b with (double)b >= bound: what lies before a kept
@@ -161,9 +247,27 @@ __device__ __forceinline__ uint64_t reach(double bound) {
   while (b > 1 && __ll2double_rn(b - 1) >= bound) --b;
   return static_cast<uint64_t>(b);
 }
+__device__ __forceinline__ uint64_t top_p_goal(float top_p, uint64_t whole) {
+  return reach(__dmul_rn(static_cast<double>(top_p), __ll2double_rn(static_cast<int64_t>(whole))));
+}
+// u times the kept weight, below it.
+__device__ __forceinline__ uint64_t answer_goal(float u, uint64_t whole) {
+  const int64_t n = static_cast<int64_t>(whole);
+  const int64_t g = static_cast<int64_t>(__dmul_rn(static_cast<double>(u), __ll2double_rn(n)));
+  return static_cast<uint64_t>(g < 0 ? 0 : g < n ? g : n - 1);
+}
 
-// Sorts `n` keys (padded to a power of two by the caller's size m) in place, rising.
-__device__ void sort_list(uint64_t* a, int m) {
+__device__ __forceinline__ int pow2_at_least(int n) {
+  int m = 2;
+  while (m < n) m <<= 1;
+  return m;
+}
+
+// Sorts the first n entries of the list, rising; returns n rounded up to a
+// power of two, the rest filled with the largest entry.
+__device__ int sort_list(uint64_t* a, int n) {
+  const int m = pow2_at_least(n);
+  for (int i = n + threadIdx.x; i < m; i += kThreads) a[i] = ~0ull;
   for (int size = 2; size <= m; size <<= 1) {
     for (int gap = size >> 1; gap > 0; gap >>= 1) {
       __syncthreads();
@@ -178,37 +282,53 @@ __device__ void sort_list(uint64_t* a, int m) {
     }
   }
   __syncthreads();
-}
-
-__device__ __forceinline__ int pow2_at_least(int n) {
-  int m = 2;
-  while (m < n) m <<= 1;
   return m;
 }
 
-// The row as one CTA sees it.
+// ---------------------------------------------------------------- a row
+// The part of a row that a CTA works on, and the row's settings.
 template <typename T>
 struct Row {
   static constexpr int E = 16 / sizeof(T);
-  const T* data;  // slice in shared memory, padded with -infinity to whole vectors
-  int vecs;
-  int c0;         // vocabulary index of the slice's first logit
+  const T* data;  // in shared memory (padded with -infinity to whole vectors) or in global memory
+  bool padded;    // shared memory
+  bool aligned;   // data is on a vector boundary
+  int n, vecs;
+  int c0;         // vocabulary index of the first logit
   float top, inv; // largest logit of the row, 1 / temperature
+  float anchor, per_bin;  // counting bins: (anchor - x) per_bin + kAnchorBin
   float min_p;
   uint32_t rank, ctas;
 
+  __device__ __forceinline__ Raw<T, E> get(int v) const {
+    if (aligned && (padded || (v + 1) * E <= n)) return load_raw<T, E>(data + v * E);
+    float x[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = v * E + e < n ? to_float<T>(data[v * E + e]) : -INFINITY;
+    return pack<T, E>(x);
+  }
   __device__ __forceinline__ float scaled(float x) const { return __fmul_rn(x - top, inv); }
+  __device__ __forceinline__ float exponential(float x) const { return expf(scaled(x)); }
+  __device__ __forceinline__ static uint64_t fixed(float e) { return __float2ull_rz(e * kFixed); }
+  __device__ __forceinline__ uint64_t weight(float x) const { return fixed(exponential(x)); }
+  // Bin of the general selection, and place among the counting bins.
   __device__ __forceinline__ int bin(float x) const {
     return min(kBins - 1, __float2int_rz(scaled(x) * -kBinsPerUnit));
   }
-  __device__ __forceinline__ uint64_t weight(float x) const { return __float2ull_rz(expf(scaled(x)) * kFixed); }
+  __device__ __forceinline__ float place(float x) const {
+    return __fmaf_rn(__fsub_rn(anchor, x), per_bin, static_cast<float>(kAnchorBin));
+  }
+  __device__ __forceinline__ static int count_bin(float place) {
+    return min(kCountBins - 1, max(0, __float2int_rz(place)));
+  }
+  __device__ __forceinline__ int sub_vecs() const { return (vecs + kSegments - 1) / kSegments; }
 
   // f(x, index) for this thread's logits.
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
     for (int v = threadIdx.x; v < vecs; v += kThreads) {
       float x[E];
-      unpack<T, E>(load_raw<T, E>(data + v * E), x);
+      unpack<T, E>(get(v), x);
 #pragma unroll
       for (int e = 0; e < E; ++e) f(x[e], static_cast<uint32_t>(c0 + v * E + e));
     }
@@ -220,36 +340,29 @@ __device__ void clear(Hist& h) {
   __syncthreads();
 }
 
-// Sums the cluster's histograms, bins 2 t and 2 t + 1 in thread t. want(total)
-// gives the goal; the bin whose running sum first reaches it goes to found_*
-// (found_bin = kBins if none does). WEIGHT: sums of weights, else counts.
-template <bool WEIGHT, typename F>
+// ---------------------------------------------------------------- general selection
+// Sums the row's histograms, a bin per thread. want(total) gives the goal; the
+// bin whose running sum first reaches it goes to found_* (found_bin = kBins if
+// none does). WEIGHT: sums of weights, else counts.
+template <bool MULTI, bool WEIGHT, typename F>
 __device__ void find_bin(Shared& s, const Hist& h, uint32_t ctas, F want) {
-  uint64_t v[2];
-  uint32_t n[2];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int b = 2 * threadIdx.x + j;
-    v[j] = 0;
-    n[j] = 0;
-    for (uint32_t r = 0; r < ctas; ++r) {
-      n[j] += remote(&h.count[b], r);
-      if (WEIGHT) v[j] += remote(&h.lo[b], r) + (static_cast<uint64_t>(remote(&h.hi[b], r)) << 32);
-    }
-    if (!WEIGHT) v[j] = n[j];
+  static_assert(kBins == kThreads, "a bin per thread");
+  const int b = threadIdx.x;
+  uint64_t v = 0;
+  uint32_t n = 0;
+  for (uint32_t r = 0; r < ctas; ++r) {
+    n += remote<MULTI>(&h.count[b], r);
+    if (WEIGHT) v += remote<MULTI>(&h.lo[b], r) + (static_cast<uint64_t>(remote<MULTI>(&h.hi[b], r)) << 32);
   }
-  if (threadIdx.x == 0) s.found_bin = kBins;
+  if (!WEIGHT) v = n;
+  if (b == 0) s.found_bin = kBins;
   uint64_t total;
-  uint64_t before = block_exclusive(v[0] + v[1], s.scan, &total);
+  const uint64_t before = block_exclusive(v, s.scan, &total);
   const uint64_t goal = want(total);
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    if (before < goal && goal <= before + v[j]) {
-      s.found_bin = 2 * threadIdx.x + j;
-      s.found_above = before;
-      s.found_count = n[j];
-    }
-    before += v[j];
+  if (before < goal && goal <= before + v) {
+    s.found_bin = b;
+    s.found_above = before;
+    s.found_count = n;
   }
   __syncthreads();
 }
@@ -257,7 +370,7 @@ __device__ void find_bin(Shared& s, const Hist& h, uint32_t ctas, F want) {
 // Finds the logit (as a key) and the number of logits equal to it at which the
 // running sum over the ranked logits above `limit` (a key) first reaches the
 // goal. Returns false if the sum never does: nothing is cut off.
-template <typename T, bool WEIGHT, typename F>
+template <typename T, bool MULTI, bool WEIGHT, typename F>
 __device__ bool select(const Row<T>& row, Shared& s, int& buf, uint32_t* listed, uint32_t limit, F want,
                        uint32_t* key_out, uint32_t* count_out) {
   Hist* h = &s.hist[buf];
@@ -265,14 +378,14 @@ __device__ bool select(const Row<T>& row, Shared& s, int& buf, uint32_t* listed,
   clear(*h);
   row.each([&](float x, uint32_t) {
     const int b = row.bin(x);
-    if (b < kBins - 1 && order_key(x) > limit) {
+    if (b < kBins - 1 && order_key(x) > limit) {  // the last bin's weights are zero
       atomicAdd(&h->count[b], 1u);
-      if (WEIGHT) add_weight(*h, b, row.weight(x));
+      if (WEIGHT) add_weight(&h->lo[b], &h->hi[b], row.weight(x));
     }
   });
-  cluster_barrier();
+  row_barrier<MULTI>();
   uint64_t goal = 0;
-  find_bin<WEIGHT>(s, *h, row.ctas, [&](uint64_t total) { return goal = want(total); });
+  find_bin<MULTI, WEIGHT>(s, *h, row.ctas, [&](uint64_t total) { return goal = want(total); });
   if (s.found_bin == kBins) return false;
   const int bin = static_cast<int>(s.found_bin);
   uint64_t above = s.found_above;
@@ -306,12 +419,12 @@ __device__ bool select(const Row<T>& row, Shared& s, int& buf, uint32_t* listed,
       s.key_lo = lo;
       s.key_hi = hi;
     }
-    cluster_barrier();
+    row_barrier<MULTI>();
     key_lo = 0xFFFFFFFFu;
     key_hi = 0;
     for (uint32_t r = 0; r < row.ctas; ++r) {
-      key_lo = min(key_lo, remote(&s.key_lo, r));
-      key_hi = max(key_hi, remote(&s.key_hi, r));
+      key_lo = min(key_lo, remote<MULTI>(&s.key_lo, r));
+      key_hi = max(key_hi, remote<MULTI>(&s.key_hi, r));
     }
     by_key = true;
     if (key_lo == key_hi) {
@@ -331,11 +444,11 @@ __device__ bool select(const Row<T>& row, Shared& s, int& buf, uint32_t* listed,
       if (k >= key_lo && k <= key_hi) {
         const int b = static_cast<int>((key_hi - k) >> shift);
         atomicAdd(&h->count[b], 1u);
-        if (WEIGHT) add_weight(*h, b, row.weight(x));
+        if (WEIGHT) add_weight(&h->lo[b], &h->hi[b], row.weight(x));
       }
     });
-    cluster_barrier();
-    find_bin<WEIGHT>(s, *h, row.ctas, [&](uint64_t) { return goal - above; });
+    row_barrier<MULTI>();
+    find_bin<MULTI, WEIGHT>(s, *h, row.ctas, [&](uint64_t) { return goal - above; });
     const uint32_t b = s.found_bin;
     above += s.found_above;
     count = s.found_count;
@@ -346,278 +459,60 @@ __device__ bool select(const Row<T>& row, Shared& s, int& buf, uint32_t* listed,
   }
   // few enough: CTA 0 sorts them
   row.each([&](float x, uint32_t i) {
-    if (inside(x)) {
-      const uint32_t at = remote_add(listed, 0, 1u);
-      if (at < static_cast<uint32_t>(kListKeys))
-        remote_store(&s.list[at], 0, static_cast<uint64_t>(~order_key(x)) << 32 | i);
-    }
+    if (inside(x)) append<MULTI>(s, listed, list_entry(x, i));
   });
-  cluster_barrier();
+  row_barrier<MULTI>();
   if (row.rank == 0) {
-    const int n = static_cast<int>(count), m = pow2_at_least(n);
-    for (int i = n + threadIdx.x; i < m; i += kThreads) s.list[i] = ~0ull;
-    sort_list(s.list, m);
-    constexpr int per = kListKeys / kThreads;
-    uint64_t w[per], sum = 0, total;
-#pragma unroll
+    const int n = static_cast<int>(count);
+    const int per = (sort_list(s.list, n) + kThreads - 1) / kThreads;
+    uint64_t sum = 0, total;
     for (int j = 0; j < per; ++j) {
       const int i = threadIdx.x * per + j;
-      w[j] = i < n ? (WEIGHT ? row.weight(key_value(~static_cast<uint32_t>(s.list[i] >> 32))) : 1) : 0;
-      sum += w[j];
+      sum += i < n ? (WEIGHT ? row.weight(entry_value(s.list[i])) : 1) : 0;
     }
     uint64_t before = above + block_exclusive(sum, s.scan, &total);
-#pragma unroll
     for (int j = 0; j < per; ++j) {
       const int i = threadIdx.x * per + j;
-      if (i < n && before < goal && goal <= before + w[j]) {
+      if (i >= n) break;
+      const uint64_t w = WEIGHT ? row.weight(entry_value(s.list[i])) : 1;
+      if (before < goal && goal <= before + w) {
         const uint32_t nk = static_cast<uint32_t>(s.list[i] >> 32);
         int f = i;
         while (f > 0 && static_cast<uint32_t>(s.list[f - 1] >> 32) == nk) --f;
         s.result_key = ~nk;
         s.result_count = static_cast<uint32_t>(i - f + 1);
       }
-      before += w[j];
+      before += w;
     }
   }
-  cluster_barrier();
-  *key_out = remote(&s.result_key, 0);
-  *count_out = remote(&s.result_count, 0);
+  row_barrier<MULTI>();
+  *key_out = remote<MULTI>(&s.result_key, 0);
+  *count_out = remote<MULTI>(&s.result_count, 0);
   return true;
 }
 
-// Everything after the selection of few candidates, by one CTA: `n` of them in
-// s.list as (inverted key, index), at least the first top_k by rank.
-template <typename T>
-__device__ void finish_list(const Row<T>& row, Shared& s, int n, int64_t top_k, float top_p, float u, int64_t* token,
-                            float* logprob) {
-  constexpr int per = kListKeys / kThreads;
-  const int m = pow2_at_least(n);
-  for (int i = n + threadIdx.x; i < m; i += kThreads) s.list[i] = ~0ull;
-  sort_list(s.list, m);
-  if (top_k > 0 && n > top_k) n = static_cast<int>(top_k);
-  uint64_t* weights = reinterpret_cast<uint64_t*>(&s.hist[0]);  // of kListKeys tokens
-  static_assert(sizeof(s.hist) >= sizeof(uint64_t) * kListKeys, "weights of a list in the histograms' place");
-  uint64_t w[per], sum = 0, whole;
-  bool pass[per];
-#pragma unroll
-  for (int j = 0; j < per; ++j) {
-    const int i = threadIdx.x * per + j;
-    w[j] = 0;
-    pass[j] = false;
-    if (i < n) {
-      const float e = expf(row.scaled(key_value(~static_cast<uint32_t>(s.list[i] >> 32))));
-      w[j] = __float2ull_rz(e * kFixed);
-      pass[j] = i == 0 || e >= row.min_p;
-    }
-    sum += w[j];
-  }
-  uint64_t before = block_exclusive(sum, s.scan, &whole);
-  const uint64_t far = top_p < 1.f ? reach(__dmul_rn(static_cast<double>(top_p), __ll2double_rn(static_cast<int64_t>(whole))))
-                                   : ~0ull;
-  if (threadIdx.x == 0) s.first = 0;
-  __syncthreads();
-#pragma unroll
-  for (int j = 0; j < per; ++j) {
-    const int i = threadIdx.x * per + j;
-    const bool keep = i < n && pass[j] && (i == 0 || before < far);
-    if (i < n) weights[i] = keep ? w[j] : 0;
-    if (keep) atomicMax(&s.first, static_cast<uint32_t>(i + 1));
-    before += w[j];
-  }
-  __syncthreads();
-  const int k = static_cast<int>(s.first), mk = pow2_at_least(k);  // nothing is kept from rank k on
-  // by index: (index, rank)
-  uint64_t entry[per];
-#pragma unroll
-  for (int j = 0; j < per; ++j) {
-    const int i = threadIdx.x + j * kThreads;
-    entry[j] = i < k ? (s.list[i] << 32) | static_cast<uint32_t>(i) : ~0ull;
-  }
-  uint32_t* keys = reinterpret_cast<uint32_t*>(weights + kListKeys);  // inverted keys by rank
-  static_assert(sizeof(s.hist) >= (sizeof(uint64_t) + sizeof(uint32_t)) * kListKeys, "weights and keys of a list");
-#pragma unroll
-  for (int j = 0; j < per; ++j) {
-    const int i = threadIdx.x + j * kThreads;
-    if (i < k) keys[i] = static_cast<uint32_t>(s.list[i] >> 32);
-  }
-  __syncthreads();
-#pragma unroll
-  for (int j = 0; j < per; ++j) {
-    const int i = threadIdx.x + j * kThreads;
-    if (i < mk) s.list[i] = entry[j];
-  }
-  sort_list(s.list, mk);
-  sum = 0;
-#pragma unroll
-  for (int j = 0; j < per; ++j) {
-    const int i = threadIdx.x * per + j;
-    w[j] = i < k ? weights[static_cast<uint32_t>(s.list[i])] : 0;
-    sum += w[j];
-  }
-  before = block_exclusive(sum, s.scan, &whole);
-  const int64_t total = static_cast<int64_t>(whole);
-  int64_t goal = static_cast<int64_t>(__dmul_rn(static_cast<double>(u), __ll2double_rn(total)));
-  goal = goal < 0 ? 0 : goal < total ? goal : total - 1;
-#pragma unroll
-  for (int j = 0; j < per; ++j) {
-    const int i = threadIdx.x * per + j;
-    const uint64_t g = static_cast<uint64_t>(goal);
-    if (i < k && before <= g && g < before + w[j]) {
-      *token = static_cast<int64_t>(s.list[i] >> 32);
-      if (logprob) {
-        const float x = key_value(~keys[static_cast<uint32_t>(s.list[i])]);
-        *logprob = row.scaled(x) - logf(__ll2float_rn(total) * (1.f / kFixed));
-      }
-    }
-    before += w[j];
-  }
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, const int slice) {
-  extern __shared__ __align__(16) uint8_t dyn[];
-  Shared& s = *reinterpret_cast<Shared*>(dyn);
-  T* data = reinterpret_cast<T*>(dyn + (sizeof(Shared) + 15) / 16 * 16);
+// The token by the general selection.
+template <typename T, bool MULTI>
+__device__ void general_answer(const Row<T>& row, Shared& s, const SampleParams& p, int64_t r, int64_t top_k,
+                               float top_p, float u) {
   constexpr int E = Row<T>::E;
-  Row<T> row;
-  row.rank = cluster_ctarank();
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(row.ctas));
-  const int64_t r = blockIdx.x / row.ctas;
-  row.data = data;
-  row.c0 = static_cast<int>(row.rank) * slice;
-  const int vocab = static_cast<int>(p.vocab);
-  const int n = max(0, min(slice, vocab - row.c0));
-  row.vecs = (n + E - 1) / E;
-  const T* x = static_cast<const T*>(p.x) + r * p.ld + row.c0;
-  const bool vec_ok = reinterpret_cast<uintptr_t>(x) % 16 == 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-  const float temperature = p.temperatures ? p.temperatures[r] : p.temperature;
-  const int64_t top_k = p.top_ks ? p.top_ks[r] : p.top_k;
-  const float top_p = p.top_ps ? p.top_ps[r] : p.top_p;
-  const float u = p.u[r];
-  row.min_p = p.min_ps ? p.min_ps[r] : p.min_p;
-
-  // ---- load, largest logit
-  float top = -INFINITY;
-  bool bad = false;
-#pragma unroll 4
-  for (int v = threadIdx.x; v < row.vecs; v += kThreads) {
-    float f[E];
-    Raw<T, E> raw;
-    if (vec_ok && (v + 1) * E <= n) {
-      raw = load_raw<T, E>(x + v * E);
-      unpack<T, E>(raw, f);
-    } else {
-#pragma unroll
-      for (int e = 0; e < E; ++e) f[e] = v * E + e < n ? to_float<T>(x[v * E + e]) : -INFINITY;
-      raw = pack<T, E>(f);
-    }
-    store_raw<T, E>(data + v * E, raw);
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      top = fmaxf(top, f[e]);
-      bad |= f[e] != f[e];
-    }
-  }
-  const float my_top = top;
-  {
-    const uint32_t k = __reduce_max_sync(0xffffffffu, order_key(top));
-    const bool any = __any_sync(0xffffffffu, bad);
-    if (lane == 0) {
-      s.red[warp] = k;
-      s.red2[warp] = any;
-    }
-    if (threadIdx.x < 3) s.listed[threadIdx.x] = 0;
-    __syncthreads();
-    if (warp == 0) {
-      const uint32_t k2 = __reduce_max_sync(0xffffffffu, lane < kWarps ? s.red[lane] : 0u);
-      const bool any2 = __any_sync(0xffffffffu, lane < kWarps && s.red2[lane]);
-      if (lane == 0) {
-        s.top = key_value(k2);
-        s.bad = any2;
-      }
-    }
-  }
-  cluster_barrier();
-  row.top = -INFINITY;
-  bad = false;
-  for (uint32_t c = 0; c < row.ctas; ++c) {
-    row.top = fmaxf(row.top, remote(&s.top, c));
-    bad |= remote(&s.bad, c) != 0;
-  }
-  bad |= !(fabsf(row.top) < INFINITY);  // no finite logit, or +infinity
-  bad |= temperature != temperature || top_p != top_p || row.min_p != row.min_p || u != u;
-  row.inv = 1.f / temperature;
-  const bool greedy = !(temperature > 0.f) || row.inv == INFINITY || top_k == 1 || top_p <= 0.f || row.min_p > 1.f;
-
-  if (bad || greedy) {
-    uint32_t first = 0xFFFFFFFFu;
-    if (!bad) row.each([&](float v, uint32_t i) {
-      if (v == row.top) first = min(first, i);
-    });
-    first = __reduce_min_sync(0xffffffffu, first);
-    if (lane == 0) s.red[warp] = first;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      for (int w = 1; w < kWarps; ++w) first = min(first, s.red[w]);
-      s.first = first;
-    }
-    cluster_barrier();
-    if (row.rank == 0 && threadIdx.x == 0) {
-      for (uint32_t c = 1; c < row.ctas; ++c) first = min(first, remote(&s.first, c));
-      p.tokens[r] = bad ? -1 : static_cast<int64_t>(first);
-      if (p.logprobs) p.logprobs[r] = bad ? __uint_as_float(0x7FC00000u) : 0.f;
-    }
-    cluster_barrier();  // CTA 0 has read the others' shared memory
-    return;
-  }
-
-  const bool need_k = top_k > 0 && top_k < p.vocab;
   int buf = 0;
-  if (need_k && top_k <= kListKeys / 2) {
-    Hist& h = s.hist[buf];
-    buf ^= 1;
-    clear(h);
-    if (threadIdx.x < row.vecs) atomicAdd(&h.count[row.bin(my_top)], 1u);
-    cluster_barrier();
-    find_bin<false>(s, h, row.ctas, [&](uint64_t) { return static_cast<uint64_t>(top_k); });
-    const int cut = min(static_cast<int>(s.found_bin), kBins - 2);  // the last bin's weights are zero
-    row.each([&](float v, uint32_t i) {
-      if (row.bin(v) <= cut) {
-        const uint32_t at = remote_add(&s.listed[0], 0, 1u);
-        if (at < static_cast<uint32_t>(kListKeys))
-          remote_store(&s.list[at], 0, static_cast<uint64_t>(~order_key(v)) << 32 | i);
-      }
-    });
-    cluster_barrier();
-    const uint32_t listed = remote(&s.listed[0], 0);
-    if (listed <= static_cast<uint32_t>(kListKeys)) {
-      if (row.rank == 0)
-        finish_list(row, s, static_cast<int>(listed), top_k, top_p, u, p.tokens + r,
-                    p.logprobs ? p.logprobs + r : nullptr);
-      cluster_barrier();  // CTA 0's counter has been read by all
-      return;
-    }
-  }
-
-  // ---- the kept set: logits above `key`, and the first `ties` of those equal to it
+  // the kept set: logits above `key`, and the first `ties` of those equal to it
   uint32_t key = 0, ties = 0;
-  if (need_k)
-    if (!select<T, false>(row, s, buf, &s.listed[1], 0u, [&](uint64_t) { return static_cast<uint64_t>(top_k); }, &key,
-                          &ties))
+  if (top_k > 0 && top_k < p.vocab)
+    if (!select<T, MULTI, false>(row, s, buf, &s.listed[1], 0u, [&](uint64_t) { return static_cast<uint64_t>(top_k); },
+                                 &key, &ties))
       key = ties = 0;
   if (top_p < 1.f) {
     const uint64_t w = ties ? row.weight(key_value(key)) : 0;
     uint64_t goal = 0, over = 0;
     uint32_t k2, t2;
-    const bool cut = select<T, true>(
+    const bool cut = select<T, MULTI, true>(
         row, s, buf, &s.listed[2], key,
         [&](uint64_t total) {
           over = total;
-          const int64_t whole = static_cast<int64_t>(total + ties * w);
-          goal = reach(__dmul_rn(static_cast<double>(top_p), __ll2double_rn(whole)));
-          return goal;
+          return goal = top_p_goal(top_p, total + ties * w);
         },
         &k2, &t2);
     if (cut) {
@@ -629,34 +524,35 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, 
     }
   }
 
-  // ---- running sums in index order: a warp per segment of the slice
-  const float e_tie = ties ? expf(row.scaled(key_value(key))) : 0.f;
-  const uint64_t w_tie = e_tie >= row.min_p ? __float2ull_rz(e_tie * kFixed) : 0;
+  // running sums in index order: a warp per segment of the slice
+  const float e_tie = ties ? row.exponential(key_value(key)) : 0.f;
+  const uint64_t w_tie = e_tie >= row.min_p ? Row<T>::fixed(e_tie) : 0;
   const int seg = (row.vecs + kWarps - 1) / kWarps;
   const int v0 = warp * seg, v1 = min(v0 + seg, row.vecs);
   auto kept_weight = [&](float f) -> uint64_t {
     if (order_key(f) <= key) return 0;
-    const float e = expf(row.scaled(f));
-    return e >= row.min_p ? __float2ull_rz(e * kFixed) : 0;
+    const float e = row.exponential(f);
+    return e >= row.min_p ? Row<T>::fixed(e) : 0;
   };
   uint64_t sum = 0;
   uint32_t equal = 0;
   for (int v = v0 + lane; v < v1; v += 32) {
     float f[E];
-    unpack<T, E>(load_raw<T, E>(data + v * E), f);
+    unpack<T, E>(row.get(v), f);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       sum += kept_weight(f[e]);
       if (ties) equal += order_key(f[e]) == key;
     }
   }
-  sum = warp_inclusive(sum);
+  sum = warp_total(sum);
   equal = __reduce_add_sync(0xffffffffu, equal);
-  if (lane == 31) {
+  __syncthreads();
+  if (lane == 0) {
     s.seg_weight[warp] = sum;
     s.seg_ties[warp] = equal;
   }
-  cluster_barrier();
+  row_barrier<MULTI>();
   // every warp finds the segment of the answer; it goes on if that is its own
   const int segs = static_cast<int>(row.ctas) * kWarps;
   uint64_t total = 0, my_before = 0, my_weight = 0;
@@ -664,12 +560,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, 
   const int mine = static_cast<int>(row.rank) * kWarps + warp;
   for (int base = 0; base < segs; base += 32) {
     const int i = base + lane;
-    uint64_t w = 0;
-    uint32_t t = 0;
-    if (i < segs) {
-      w = remote(&s.seg_weight[i % kWarps], i / kWarps);
-      t = remote(&s.seg_ties[i % kWarps], i / kWarps);
-    }
+    uint64_t w = remote<MULTI>(&s.seg_weight[i % kWarps], i / kWarps);
+    const uint32_t t = remote<MULTI>(&s.seg_ties[i % kWarps], i / kWarps);
     const uint32_t t_inc = static_cast<uint32_t>(warp_inclusive(t));
     const uint32_t t_before = tie_total + t_inc - t;
     const uint32_t t_kept = t_before < ties ? min(t, ties - t_before) : 0;
@@ -684,10 +576,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, 
     total += __shfl_sync(0xffffffffu, w_inc, 31);
     tie_total += __shfl_sync(0xffffffffu, t_inc, 31);
   }
-  const int64_t whole = static_cast<int64_t>(total);
-  int64_t g = static_cast<int64_t>(__dmul_rn(static_cast<double>(u), __ll2double_rn(whole)));
-  g = g < 0 ? 0 : g < whole ? g : whole - 1;
-  const uint64_t goal = static_cast<uint64_t>(g);
+  const uint64_t goal = answer_goal(u, total);
   if (my_before <= goal && goal < my_before + my_weight) {
     uint64_t before = my_before;
     uint32_t tie_before = my_tie_before;
@@ -697,7 +586,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, 
       uint32_t eq = 0;
       uint64_t w = 0;
       if (v < v1) {
-        unpack<T, E>(load_raw<T, E>(data + v * E), f);
+        unpack<T, E>(row.get(v), f);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           w += kept_weight(f[e]);
@@ -716,7 +605,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, 
           if (ties && order_key(f[e]) == key) we = tb++ < ties ? w_tie : 0;
           if (mb <= goal && goal < mb + we) {
             p.tokens[r] = row.c0 + v * E + e;
-            if (p.logprobs) p.logprobs[r] = row.scaled(f[e]) - logf(__ll2float_rn(whole) * (1.f / kFixed));
+            if (p.logprobs)
+              p.logprobs[r] = row.scaled(f[e]) - logf(__ll2float_rn(static_cast<int64_t>(total)) * (1.f / kFixed));
           }
           mb += we;
         }
@@ -725,36 +615,568 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, 
       tie_before += __shfl_sync(0xffffffffu, eq_inc, 31);
     }
   }
-  cluster_barrier();  // the segments' sums have been read by all
+  row_barrier<MULTI>();  // the segments' sums have been read by all
 }
 
-}  // namespace
+// ---------------------------------------------------------------- answers from a list
+// The token from a list of n candidates, at least the first top_k by rank.
+template <typename T>
+__device__ void list_answer(const Row<T>& row, Shared& s, int n, int64_t top_k, float top_p, float u, int vocab,
+                            int64_t* token, float* logprob) {
+  constexpr int kPer = kListKeys / kThreads;
+  const int per = (sort_list(s.list, n) + kThreads - 1) / kThreads;
+  if (top_k > 0 && n > top_k) n = static_cast<int>(top_k);
+  uint64_t w[kPer], sum = 0, whole;
+  uint32_t pass = 0;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int i = threadIdx.x * per + j;
+    w[j] = 0;
+    if (j < per && i < n) {
+      const float e = row.exponential(entry_value(s.list[i]));
+      w[j] = Row<T>::fixed(e);
+      if (i == 0 || e >= row.min_p) pass |= 1u << j;
+    }
+    sum += w[j];
+  }
+  uint64_t before = block_exclusive(sum, s.scan, &whole);
+  const uint64_t far = top_p < 1.f ? top_p_goal(top_p, whole) : ~0ull;
+  // kept weights by segments of the vocabulary, two per thread
+  Answer& a = s.answer;
+  static_assert(kAnswerBins == 2 * kThreads && kThreads * sizeof(uint32_t) * 2 + sizeof(Answer) <= sizeof(s.hist),
+                "segments, and the places of the tokens in one");
+  const uint32_t width = static_cast<uint32_t>((vocab + kAnswerBins - 1) / kAnswerBins);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) a.lo[2 * threadIdx.x + j] = a.hi[2 * threadIdx.x + j] = 0;
+  if (threadIdx.x == 0) s.listed[3] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int i = threadIdx.x * per + j;
+    if (pass >> j & 1) {
+      if (i == 0 || before < far) {
+        const uint32_t b = static_cast<uint32_t>(s.list[i]) / width;
+        add_weight(&a.lo[b], &a.hi[b], w[j]);
+      } else {
+        pass &= ~(1u << j);
+      }
+    }
+    before += w[j];
+  }
+  __syncthreads();
+  uint64_t b2[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int b = 2 * threadIdx.x + j;
+    b2[j] = a.lo[b] + (static_cast<uint64_t>(a.hi[b]) << 32);
+  }
+  before = block_exclusive(b2[0] + b2[1], s.scan, &whole);
+  const uint64_t goal = answer_goal(u, whole);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    if (before <= goal && goal < before + b2[j]) {
+      s.found_bin = 2 * threadIdx.x + j;
+      s.found_above = before;
+    }
+    before += b2[j];
+  }
+  __syncthreads();
+  // the tokens of that segment (at most `width`): each one's running sum is that of those before it
+  uint32_t* place = reinterpret_cast<uint32_t*>(&a + 1);
+  const uint32_t bin = s.found_bin;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int i = threadIdx.x * per + j;
+    if ((pass >> j & 1) && static_cast<uint32_t>(s.list[i]) / width == bin) place[atomicAdd(&s.listed[3], 1u)] = i;
+  }
+  __syncthreads();
+  const int here = static_cast<int>(s.listed[3]);
+  for (int i = threadIdx.x; i < here; i += kThreads) {
+    const uint64_t mine = s.list[place[i]];
+    const uint32_t index = static_cast<uint32_t>(mine);
+    uint64_t b = s.found_above;
+    for (int k = 0; k < here; ++k) {
+      const uint64_t other = s.list[place[k]];
+      if (static_cast<uint32_t>(other) < index) b += row.weight(entry_value(other));
+    }
+    if (b <= goal && goal < b + row.weight(entry_value(mine))) {
+      *token = index;
+      if (logprob)
+        *logprob = row.scaled(entry_value(mine)) - logf(__ll2float_rn(static_cast<int64_t>(whole)) * (1.f / kFixed));
+    }
+  }
+}
 
-cudaError_t launch_sample(const SampleParams& p, int sms, cudaStream_t s) {
-  const bool f32 = p.dtype == FLCE_DTYPE_F32;
-  const int64_t es = f32 ? 4 : 2;
-  // Slices of at most 64 KB let three CTAs share an SM, which hides one's
-  // barriers behind another's work; few rows are spread over more CTAs, down
-  // to 4096 logits each.
-  int ctas = 1;
-  while (ctas < kMaxCluster && (p.vocab * es + ctas - 1) / ctas > 64 * 1024) ctas *= 2;
-  while (ctas < kMaxCluster && p.rows * ctas * 2 <= sms && p.vocab / ctas > 4096) ctas *= 2;
+// ---------------------------------------------------------------- second pass
+// Adds up this slice's weights: *total all of them, *above those placed above
+// cut_lo, seg_weight[] the latter (at least min_p) by segments; logits placed
+// in [cut_lo, cut_hi) are appended to CTA 0's list. Without CUT every logit
+// counts as above and only the segments are summed. A warp has kSubs
+// consecutive segments, four vectors per lane in flight.
+template <typename T, bool MULTI, bool CUT>
+__device__ void sum_segments(const Row<T>& row, Shared& s, float cut_lo, float cut_hi) {
+  constexpr int E = Row<T>::E;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per = row.sub_vecs();
+  uint64_t total = 0, above = 0;
+#pragma unroll 1
+  for (int sub = 0; sub < kSubs; ++sub) {
+    const int seg = warp * kSubs + sub;
+    const int v1 = min((seg + 1) * per, row.vecs);
+    uint64_t acc = 0;
+    for (int v = seg * per + lane; v < v1; v += 32 * 4) {
+      Raw<T, E> raw[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (v + 32 * j < v1) raw[j] = row.get(v + 32 * j);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (v + 32 * j >= v1) break;
+        float x[E];
+        unpack<T, E>(raw[j], x);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float ex = row.exponential(x[e]);
+          const uint64_t w = Row<T>::fixed(ex);
+          if (CUT) {
+            const float place = row.place(x[e]);
+            total += w;
+            if (place < cut_lo) {
+              above += w;
+              if (ex >= row.min_p) acc += w;
+            } else if (place < cut_hi) {
+              append<MULTI>(s, &s.listed[0], list_entry(x[e], static_cast<uint32_t>(row.c0 + (v + 32 * j) * E + e)));
+            }
+          } else if (ex >= row.min_p) {
+            acc += w;
+          }
+        }
+      }
+    }
+    acc = warp_total(acc);
+    if (lane == 0) s.seg_weight[seg] = acc;
+  }
+  if (CUT) {
+    total = warp_total(total);
+    above = warp_total(above);
+    if (lane == 0) {
+      atomicAdd(reinterpret_cast<unsigned long long*>(&s.sum_total), static_cast<unsigned long long>(total));
+      atomicAdd(reinterpret_cast<unsigned long long*>(&s.sum_above), static_cast<unsigned long long>(above));
+    }
+  }
+}
+
+// The answer from the second pass's sums, by CTA 0: joins the kept part of the
+// list (n entries) with the segments and walks the segment of the answer.
+// Returns false if the exact sums do not confirm that the prefix ends in the list.
+template <typename T, bool MULTI>
+__device__ bool segment_answer(const Row<T>& row, Shared& s, const SampleParams& p, int64_t r, int slice, float top_p,
+                               float u, bool cut, float cut_lo, float cut_hi) {
+  constexpr int E = Row<T>::E;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int vocab = static_cast<int>(p.vocab);
+  uint64_t cut_entry = ~0ull;  // last kept entry of the list
+  int n = 0, per = 0;
+  if (cut) {
+    uint64_t total = 0, above = 0;
+    for (uint32_t c = 0; c < row.ctas; ++c) {
+      total += remote<MULTI>(&s.sum_total, c);
+      above += remote<MULTI>(&s.sum_above, c);
+    }
+    n = static_cast<int>(min(s.listed[0], static_cast<uint32_t>(kListKeys)));
+    const uint64_t goal = top_p_goal(top_p, total);
+    if (s.listed[0] > static_cast<uint32_t>(kListKeys) || above >= goal) return false;
+    per = (sort_list(s.list, n) + kThreads - 1) / kThreads;
+    uint64_t sum = 0, listed;
+    for (int j = 0; j < per; ++j) {
+      const int i = threadIdx.x * per + j;
+      if (i < n) sum += row.weight(entry_value(s.list[i]));
+    }
+    uint64_t before = above + block_exclusive(sum, s.scan, &listed);
+    if (above + listed < goal) return false;
+    for (int j = 0; j < per; ++j) {
+      const int i = threadIdx.x * per + j;
+      if (i < n) {
+        const uint64_t w = row.weight(entry_value(s.list[i]));
+        if (before < goal && goal <= before + w) s.found_value = s.list[i];
+        before += w;
+      }
+    }
+  }
+  // the segments of all slices, two per thread
+  Answer& a = s.answer;
+  static_assert(kAnswerBins == kMaxCluster * kSegments, "a bin per segment of the largest cluster");
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int b = 2 * threadIdx.x + j;
+    const uint64_t w = b < static_cast<int>(row.ctas) * kSegments ? remote<MULTI>(&s.seg_weight[b % kSegments], b / kSegments) : 0;
+    a.lo[b] = static_cast<uint32_t>(w);
+    a.hi[b] = static_cast<uint32_t>(w >> 32);
+  }
+  __syncthreads();
+  if (cut) {
+    cut_entry = s.found_value;
+    for (int j = 0; j < per; ++j) {
+      const int i = threadIdx.x * per + j;
+      if (i >= n || s.list[i] > cut_entry) break;
+      const float e = row.exponential(entry_value(s.list[i]));
+      if (e >= row.min_p) {
+        const int index = static_cast<int>(static_cast<uint32_t>(s.list[i]));
+        const int c = index / slice;
+        const int vecs = (min(slice, vocab - c * slice) + E - 1) / E;
+        const int b = c * kSegments + (index - c * slice) / E / ((vecs + kSegments - 1) / kSegments);
+        add_weight(&a.lo[b], &a.hi[b], Row<T>::fixed(e));
+      }
+    }
+    __syncthreads();
+  }
+  uint64_t b2[2], whole;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int b = 2 * threadIdx.x + j;
+    b2[j] = a.lo[b] + (static_cast<uint64_t>(a.hi[b]) << 32);
+  }
+  uint64_t before = block_exclusive(b2[0] + b2[1], s.scan, &whole);
+  const uint64_t goal = answer_goal(u, whole);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    if (before <= goal && goal < before + b2[j]) {
+      s.found_bin = 2 * threadIdx.x + j;
+      s.found_above = before;
+    }
+    before += b2[j];
+  }
+  __syncthreads();
+  if (warp != 0) return true;
+  // one warp walks the segment, from global memory if it is another CTA's
+  const int c = static_cast<int>(s.found_bin) / kSegments, seg = static_cast<int>(s.found_bin) % kSegments;
+  Row<T> part = row;
+  if (c != static_cast<int>(row.rank)) {
+    part.data = static_cast<const T*>(p.x) + r * p.ld + static_cast<int64_t>(c) * slice;
+    part.padded = false;
+    part.aligned = reinterpret_cast<uintptr_t>(part.data) % 16 == 0;
+    part.c0 = c * slice;
+    part.n = min(slice, vocab - part.c0);
+    part.vecs = (part.n + E - 1) / E;
+  }
+  const int sub = part.sub_vecs();
+  const int v1 = min((seg + 1) * sub, part.vecs);
+  uint64_t run = s.found_above;
+  for (int base = seg * sub; base < v1; base += 32) {
+    const int v = base + lane;
+    float x[E];
+    uint64_t w[E], sum = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) w[e] = 0;
+    if (v < v1) {
+      unpack<T, E>(part.get(v), x);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float ex = part.exponential(x[e]);
+        bool keep = ex >= part.min_p;
+        if (cut) {
+          const float place = part.place(x[e]);
+          keep = keep && place < cut_hi &&
+                 (place < cut_lo || list_entry(x[e], static_cast<uint32_t>(part.c0 + v * E + e)) <= cut_entry);
+        }
+        w[e] = keep ? Row<T>::fixed(ex) : 0;
+        sum += w[e];
+      }
+    }
+    const uint64_t inc = warp_inclusive(sum);
+    uint64_t b = run + inc - sum;
+    if (b <= goal && goal < b + sum) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        if (b <= goal && goal < b + w[e]) {
+          p.tokens[r] = part.c0 + v * E + e;
+          if (p.logprobs)
+            p.logprobs[r] = part.scaled(x[e]) - logf(__ll2float_rn(static_cast<int64_t>(whole)) * (1.f / kFixed));
+        }
+        b += w[e];
+      }
+    }
+    run += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  return true;
+}
+
+// ---------------------------------------------------------------- the kernel
+template <typename T, bool MULTI>
+__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, const int slice, const int in_smem) {
+  extern __shared__ __align__(16) uint8_t dyn[];
+  Shared& s = *reinterpret_cast<Shared*>(dyn);
+  T* kept = reinterpret_cast<T*>(dyn + (sizeof(Shared) + 15) / 16 * 16);
+  constexpr int E = Row<T>::E;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Row<T> row;
+  row.rank = 0;
+  row.ctas = 1;
+  if constexpr (MULTI) {
+    row.rank = cluster_ctarank();
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(row.ctas));
+  }
+  const int64_t r = blockIdx.x / row.ctas;
+  const int vocab = static_cast<int>(p.vocab);
+  row.c0 = static_cast<int>(row.rank) * slice;
+  row.n = max(0, min(slice, vocab - row.c0));
+  row.vecs = (row.n + E - 1) / E;
+  row.data = static_cast<const T*>(p.x) + r * p.ld + row.c0;
+  row.padded = false;
+  row.aligned = reinterpret_cast<uintptr_t>(row.data) % 16 == 0;
+
+  const float temperature = p.temperatures ? p.temperatures[r] : p.temperature;
+  const int64_t top_k = p.top_ks ? p.top_ks[r] : p.top_k;
+  const float top_p = p.top_ps ? p.top_ps[r] : p.top_p;
+  const float u = p.u[r];
+  row.min_p = p.min_ps ? p.min_ps[r] : p.min_p;
+  row.inv = 1.f / temperature;
+  row.per_bin = fminf(row.inv * kCountsPerUnit, 3e38f);
+  bool bad = temperature != temperature || top_p != top_p || row.min_p != row.min_p || u != u;
+  const bool greedy = !(temperature > 0.f) || row.inv == INFINITY || top_k == 1 || top_p <= 0.f || row.min_p > 1.f;
+  const bool need_k = top_k > 0 && top_k < p.vocab;
+  const bool need_counts = !greedy && !bad && (need_k || top_p < 1.f);
+
+  if (need_counts) {
+    for (int i = threadIdx.x; i < kCountBins; i += kThreads) s.counts.count[i] = 0;
+    for (int i = threadIdx.x; i < kWeighedBins; i += kThreads) s.counts.weight[i] = 0.f;
+  }
+  if (threadIdx.x < 4) s.listed[threadIdx.x] = 0;
+  if (threadIdx.x == 0) {
+    s.sum_total = s.sum_above = 0;
+    s.general = 0;
+  }
+  if (threadIdx.x < 2) {
+    s.cut_lo[threadIdx.x] = s.cut_hi[threadIdx.x] = ~0ull;
+  }
+
+  // ---- first pass: largest logit, counts
+  float top = -INFINITY;
+  int top_vec = -1;
+  auto count = [&](const Raw<T, E>& raw) {
+    float x[E];
+    unpack<T, E>(raw, x);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int b = Row<T>::count_bin(row.place(x[e]));
+      atomicAdd(&s.counts.count[b], 1u);
+      if (b < kWeighedBins) atomicAdd(&s.counts.weight[b], expf(fminf((x[e] - row.anchor) * row.inv, 60.f)));
+    }
+  };
+  // vectors [from, to), four per thread in flight
+  auto sweep = [&](int from, int to, bool counting) {
+    for (int v = from + threadIdx.x; v < to; v += 4 * kThreads) {
+      Raw<T, E> raw[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (v + j * kThreads < to) raw[j] = row.get(v + j * kThreads);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int w = v + j * kThreads;
+        if (w >= to) break;
+        if (in_smem) store_raw<T, E>(kept + w * E, raw[j]);
+        float x[E];
+        unpack<T, E>(raw[j], x);
+        float m = x[0];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          m = fmaxf(m, x[e]);
+          bad |= x[e] != x[e];
+        }
+        if (m > top) {
+          top = m;
+          top_vec = w;
+        }
+        if (counting) count(raw[j]);
+      }
+    }
+  };
+  // the largest of the CTA's `top`s so far
+  auto block_top = [&]() {
+    const uint32_t k = __reduce_max_sync(0xffffffffu, order_key(top));
+    __syncthreads();
+    if (lane == 0) s.red[warp] = k;
+    __syncthreads();
+    return key_value(__reduce_max_sync(0xffffffffu, s.red[lane]));
+  };
+  // without a cluster the first part of the row sets the anchor, and the counts
+  // of all but that part come with the only read from HBM; a cluster's slices
+  // are short and are looked through again with the row's maximum as the anchor
+  const int first = MULTI ? row.vecs : min(row.vecs, kFirstVectors * kThreads);
+  sweep(0, first, false);
+  if (!MULTI && need_counts) {
+    const float a = block_top();
+    row.anchor = fabsf(a) < INFINITY ? a : 0.f;
+    for (int v = threadIdx.x; v < first; v += kThreads) count(row.get(v));
+  } else {
+    row.anchor = 0.f;
+  }
+  sweep(first, row.vecs, need_counts);
+  if (in_smem) {
+    row.data = kept;
+    row.padded = row.aligned = true;
+  }
+  const float slice_top = block_top();
+  bad = __syncthreads_or(bad);
+  row.top = slice_top;
+  if constexpr (MULTI) {
+    if (threadIdx.x == 0) {
+      s.top = slice_top;
+      s.bad = bad;
+    }
+    row_barrier<MULTI>();
+    for (uint32_t c = 0; c < row.ctas; ++c) {
+      row.top = fmaxf(row.top, remote<MULTI>(&s.top, c));
+      bad |= remote<MULTI>(&s.bad, c) != 0;
+    }
+  }
+  bad |= !(fabsf(row.top) < INFINITY);  // no finite logit, or +infinity
+
+  if (bad || greedy) {
+    uint32_t at = 0xFFFFFFFFu;
+    if (!bad && top == row.top) {  // the thread's first vector with it
+      float x[E];
+      unpack<T, E>(row.get(top_vec), x);
+#pragma unroll
+      for (int e = E - 1; e >= 0; --e)
+        if (x[e] == top) at = static_cast<uint32_t>(row.c0 + top_vec * E + e);
+    }
+    at = __reduce_min_sync(0xffffffffu, at);
+    if (lane == 0) s.red2[warp] = at;
+    __syncthreads();
+    at = __reduce_min_sync(0xffffffffu, s.red2[lane]);
+    if constexpr (MULTI) {
+      if (threadIdx.x == 0) s.first = at;
+      row_barrier<MULTI>();
+      for (uint32_t c = 0; c < row.ctas; ++c) at = min(at, remote<MULTI>(&s.first, c));
+      row_barrier<MULTI>();  // all have read it
+    }
+    if (row.rank == 0 && threadIdx.x == 0) {
+      p.tokens[r] = bad ? -1 : static_cast<int64_t>(at);
+      if (p.logprobs) p.logprobs[r] = bad ? __uint_as_float(0x7FC00000u) : 0.f;
+    }
+    return;
+  }
+
+  // ---- where the prefix ends, by the counts
+  bool general = false, listing = false;
+  float cut_lo = INFINITY, cut_hi = INFINITY;
+  if (need_counts) {
+    if constexpr (MULTI) {
+      row.anchor = row.top;
+      row.each([&](float x, uint32_t) {
+        const int b = Row<T>::count_bin(row.place(x));
+        atomicAdd(&s.counts.count[b], 1u);
+        if (b < kWeighedBins) atomicAdd(&s.counts.weight[b], expf((x - row.anchor) * row.inv));
+      });
+      row_barrier<MULTI>();
+    }
+    uint32_t n[2];
+    float w[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int b = 2 * threadIdx.x + j;
+      n[j] = 0;
+      w[j] = 0.f;
+      for (uint32_t c = 0; c < row.ctas; ++c) {
+        n[j] += remote<MULTI>(&s.counts.count[b], c);
+        if (b < kWeighedBins) w[j] += remote<MULTI>(&s.counts.weight[b], c);
+      }
+      if (b >= kWeighedBins && b < kCountBins - 1)
+        w[j] = n[j] * expf((kAnchorBin - b - 0.5f) * (1.f / kCountsPerUnit));
+    }
+    uint64_t all;
+    uint64_t count_before = block_exclusive(static_cast<uint64_t>(n[0] + n[1]), s.scan, &all);
+    float whole;
+    float weight_before = block_exclusive(w[0] + w[1], s.fscan, &whole);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t b = 2 * threadIdx.x + j;
+      const uint64_t upto = count_before + n[j];
+      const unsigned long long bin = static_cast<unsigned long long>(b) << 32;
+      if (b == kCountBins - 1) {
+        s.found_count = static_cast<uint32_t>(count_before);  // logits in all bins but the last
+      } else if (need_k) {
+        const uint64_t k = static_cast<uint64_t>(top_k);
+        if (count_before < k && k <= upto) s.cut_hi[0] = bin | upto;
+      } else if (n[j]) {
+        // rounding may let two neighbouring bins seem to hold a bound, or none; the
+        // exact sums decide, but every CTA has to take the same one
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float margin = i == 0 ? kMargin : kSmallMargin;
+          const float lo = (top_p - margin) * whole, hi = (top_p + margin) * whole;
+          if (weight_before <= lo && lo < weight_before + w[j]) atomicMin(&s.cut_lo[i], bin | count_before);
+          if (weight_before <= hi && hi < weight_before + w[j]) atomicMin(&s.cut_hi[i], bin | upto);
+        }
+      }
+      count_before += n[j];
+      weight_before += w[j];
+    }
+    __syncthreads();
+    // from the first bin if none holds the lower bound; to the last but one, as the
+    // last bin's weights are zero, if none holds the upper
+    uint64_t from = 0, to = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      from = need_k || s.cut_lo[i] == ~0ull ? 0 : s.cut_lo[i];
+      to = s.cut_hi[i] != ~0ull ? s.cut_hi[i] : static_cast<uint64_t>(kCountBins - 2) << 32 | s.found_count;
+      general = static_cast<uint32_t>(to) - static_cast<uint32_t>(from) > static_cast<uint32_t>(kListKeys);
+      if (need_k || !general) break;
+    }
+    general |= !(whole < INFINITY);
+    listing = need_k && !general;
+    cut_lo = from >> 32 == 0 ? -INFINITY : static_cast<float>(from >> 32);
+    cut_hi = static_cast<float>((to >> 32) + 1);
+  }
+
+  // ---- second pass
+  if (listing) {
+    row.each([&](float x, uint32_t i) {
+      if (row.place(x) < cut_hi) append<MULTI>(s, &s.listed[0], list_entry(x, i));
+    });
+    row_barrier<MULTI>();
+    if (row.rank == 0)
+      list_answer(row, s, static_cast<int>(s.listed[0]), top_k, top_p, u, vocab, p.tokens + r,
+                  p.logprobs ? p.logprobs + r : nullptr);
+    return;  // nothing of the other CTAs is read any more
+  }
+  if (!general) {
+    const bool cut = need_counts;
+    if (cut)
+      sum_segments<T, MULTI, true>(row, s, cut_lo, cut_hi);
+    else
+      sum_segments<T, MULTI, false>(row, s, cut_lo, cut_hi);
+    row_barrier<MULTI>();
+    if (row.rank == 0 && !segment_answer<T, MULTI>(row, s, p, r, slice, top_p, u, cut, cut_lo, cut_hi) &&
+        threadIdx.x == 0)
+      s.general = 1;
+    row_barrier<MULTI>();
+    general = remote<MULTI>(&s.general, 0) != 0;
+    if constexpr (MULTI) row_barrier<MULTI>();  // CTA 0 stays until all have read it
+  }
+  if (general) general_answer<T, MULTI>(row, s, p, r, top_k, top_p, u);
+}
+
+template <typename T>
+cudaError_t run(const SampleParams& p, int ctas, cudaStream_t s) {
+  const size_t shared = (sizeof(Shared) + 15) / 16 * 16;
   const int slice = static_cast<int>(((p.vocab + ctas - 1) / ctas + 63) / 64 * 64);
-  const size_t smem = (sizeof(Shared) + 15) / 16 * 16 + static_cast<size_t>(slice) * es;
-  auto kernel = f32 ? sample_kernel<float> : sample_kernel<uint16_t>;
-  static_assert((sizeof(Shared) + 15) / 16 * 16 + kMaxSlice + 256 <= 227 * 1024, "a slice fits beside the rest");
+  const size_t kept = static_cast<size_t>(slice) * sizeof(T);
+  const bool in_smem = shared + kept <= kMostShared;
+  auto kernel = ctas > 1 ? sample_kernel<T, true> : sample_kernel<T, false>;
   static std::atomic<uint64_t> done[2];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
-  if (!(done[f32].load() >> (dev & 63) & 1)) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+  if (!(done[ctas > 1].load() >> (dev & 63) & 1)) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
     if (e != cudaSuccess) return e;
-    done[f32].fetch_or(1ull << (dev & 63));
+    done[ctas > 1].fetch_or(1ull << (dev & 63));
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.rows * ctas));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = shared + (in_smem ? kept : 0);
   cfg.stream = s;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -762,7 +1184,17 @@ cudaError_t launch_sample(const SampleParams& p, int sms, cudaStream_t s) {
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p, slice);
+  return cudaLaunchKernelEx(&cfg, kernel, p, slice, in_smem ? 1 : 0);
+}
+
+}  // namespace
+
+cudaError_t launch_sample(const SampleParams& p, int sms, cudaStream_t s) {
+  // One CTA per row where that occupies half of the SMs or more; fewer rows
+  // are spread over clusters, down to 4096 logits per CTA.
+  int ctas = 1;
+  while (ctas < kMaxCluster && p.rows * ctas * 2 <= sms && p.vocab / ctas > 4096) ctas *= 2;
+  return p.dtype == FLCE_DTYPE_F32 ? run<float>(p, ctas, s) : run<uint16_t>(p, ctas, s);
 }
 
 }  // namespace flce
