@@ -64,9 +64,8 @@ constexpr int kWeighedBins = kAnchorBin + 110;
 // How far around the estimated end logits are collected, of the whole weight:
 // the first margin if the list holds what lies in it, else the second.
 constexpr float kMargin = 0.0015f, kSmallMargin = 0.0002f;
-// Segments of a slice whose weights are kept apart: eight per warp.
-constexpr int kSubs = 8;
-constexpr int kSegments = kWarps * kSubs;
+// Segments of a slice whose weights are kept apart, at most.
+constexpr int kSegments = 256;
 constexpr int kFirstVectors = 4;  // per thread: the part of the row that sets the anchor
 constexpr int kAnswerBins = 2048;   // segments of the vocabulary for a list of kept tokens
 constexpr int kMostShared = 227 * 1024;
@@ -97,7 +96,7 @@ struct Shared {
   uint32_t seg_ties[kWarps];
   uint64_t scan[kWarps + 1];
   uint64_t sum_total, sum_above;  // of this slice, in the second pass
-  uint64_t found_above, found_value;
+  uint64_t found_above, found_value, goal;
   uint32_t found_bin, found_count;
   float top;
   uint32_t bad;
@@ -109,6 +108,7 @@ struct Shared {
   uint32_t general;         // CTA 0: the row needs the general selection
   uint32_t red[kWarps], red2[kWarps];
   float fscan[kWarps];
+  float told[3];  // CTA 0: where the prefix ends, for the others
 };
 
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -154,6 +154,14 @@ __device__ __forceinline__ uint64_t remote(const uint64_t* mine, uint32_t rank) 
   uint64_t v;
   asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(mapa_shared(smem_u32(mine), rank)) : "memory");
   return v;
+}
+
+// Adds to a word of CTA `rank`.
+__device__ __forceinline__ void remote_add(uint32_t* mine, uint32_t rank, uint32_t v) {
+  asm volatile("red.shared::cluster.add.u32 [%0], %1;" ::"r"(mapa_shared(smem_u32(mine), rank)), "r"(v) : "memory");
+}
+__device__ __forceinline__ void remote_add(float* mine, uint32_t rank, float v) {
+  asm volatile("red.shared::cluster.add.f32 [%0], %1;" ::"r"(mapa_shared(smem_u32(mine), rank)), "f"(v) : "memory");
 }
 
 // Appends to CTA 0's list; what does not fit is only counted.
@@ -256,6 +264,14 @@ __device__ __forceinline__ uint64_t answer_goal(float u, uint64_t whole) {
   const int64_t g = static_cast<int64_t>(__dmul_rn(static_cast<double>(u), __ll2double_rn(n)));
   return static_cast<uint64_t>(g < 0 ? 0 : g < n ? g : n - 1);
 }
+// f() of one thread for all of the CTA: goals take double precision, which 1024
+// threads would queue for.
+template <typename F>
+__device__ __forceinline__ uint64_t by_one(Shared& s, F f) {
+  if (threadIdx.x == 0) s.goal = f();
+  __syncthreads();
+  return s.goal;
+}
 
 __device__ __forceinline__ int pow2_at_least(int n) {
   int m = 2;
@@ -263,27 +279,118 @@ __device__ __forceinline__ int pow2_at_least(int n) {
   return m;
 }
 
-// Sorts the first n entries of the list, rising; returns n rounded up to a
-// power of two, the rest filled with the largest entry.
-__device__ int sort_list(uint64_t* a, int n) {
-  const int m = pow2_at_least(n);
-  for (int i = n + threadIdx.x; i < m; i += kThreads) a[i] = ~0ull;
+// Exchanges with the entry `gap` places on: the smaller stays below where the
+// run is to rise.
+__device__ __forceinline__ uint64_t in_order(uint64_t a, uint64_t b, bool low_place, bool rising) {
+  return (a > b) == (low_place == rising) ? b : a;
+}
+
+// Sorts the first n <= kListKeys entries of the list, rising; returns n rounded
+// up to a power of two, the rest filled with the largest entry. A bitonic network
+// with entry j kThreads + t in thread t's registers: gaps below 32 are shuffles,
+// gaps of kThreads and more are between a thread's own, and only those between
+// go through shared memory.
+template <int PER>
+__device__ void sort_entries(uint64_t* a, int n, int m) {
+  const int t = threadIdx.x;
+  uint64_t v[PER];
+#pragma unroll
+  for (int j = 0; j < PER; ++j) v[j] = j * kThreads + t < n ? a[j * kThreads + t] : ~0ull;
   for (int size = 2; size <= m; size <<= 1) {
     for (int gap = size >> 1; gap > 0; gap >>= 1) {
-      __syncthreads();
-      for (int i = threadIdx.x; i < m / 2; i += kThreads) {
-        const int l = 2 * i - (i & (gap - 1));
-        const uint64_t u = a[l], v = a[l + gap];
-        if ((u > v) == ((l & size) == 0)) {
-          a[l] = v;
-          a[l + gap] = u;
+      if (gap >= kThreads) {
+        const int g = gap / kThreads;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+#pragma unroll
+          for (int k = 1; k < PER; k <<= 1) {
+            if (k == g && (j & k) == 0) {
+              const bool rising = ((j * kThreads + t) & size) == 0;
+              const uint64_t lo = in_order(v[j], v[j | k], true, rising);
+              v[j | k] = in_order(v[j | k], v[j], false, rising);
+              v[j] = lo;
+            }
+          }
         }
+      } else if (gap >= 32) {
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < PER; ++j) a[j * kThreads + t] = v[j];
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+          v[j] = in_order(v[j], a[j * kThreads + (t ^ gap)], (t & gap) == 0, ((j * kThreads + t) & size) == 0);
+      } else {
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+          v[j] = in_order(v[j], __shfl_xor_sync(0xffffffffu, v[j], gap), (t & gap) == 0,
+                          ((j * kThreads + t) & size) == 0);
       }
     }
   }
   __syncthreads();
+#pragma unroll
+  for (int j = 0; j < PER; ++j) a[j * kThreads + t] = v[j];
+  __syncthreads();
+}
+
+__device__ int sort_list(uint64_t* a, int n) {
+  const int m = pow2_at_least(n);
+  __syncthreads();
+  if (m <= 256) {
+    // few: an entry's place is the number of smaller ones (entries differ by their index)
+    uint64_t mine = ~0ull;
+    int place = threadIdx.x;
+    if (threadIdx.x < n) {
+      mine = a[threadIdx.x];
+      place = 0;
+      for (int i = 0; i < n; ++i) place += a[i] < mine;
+    }
+    __syncthreads();
+    if (threadIdx.x < m) a[place] = mine;
+    __syncthreads();
+  } else if (m <= kThreads) {
+    sort_entries<1>(a, n, m);
+  } else if (m == 2 * kThreads) {
+    sort_entries<2>(a, n, m);
+  } else if (m == 4 * kThreads) {
+    sort_entries<4>(a, n, m);
+  } else {
+    sort_entries<8>(a, n, m);
+  }
   return m;
 }
+
+// floor(e 2^40) for e in [0, 1] as hi 2^20 + lo. Adding to 2^23 with rounding
+// towards zero leaves the whole part in the mantissa; what it left is exact.
+// (The 64-bit conversion instruction runs at the rate of double precision,
+// which this chip has little of: with it the second pass took three times as long.)
+struct Halves {
+  uint32_t hi, lo;
+};
+__device__ __forceinline__ Halves halves(float e) {
+  const float a = __fmaf_rz(e, 1048576.f, 8388608.f);
+  const float rest = __fmaf_rn(e, 1048576.f, 8388608.f - a);
+  const float b = __fmaf_rz(rest, 1048576.f, 8388608.f);
+  return {__float_as_uint(a) - 0x4B000000u, __float_as_uint(b) - 0x4B000000u};
+}
+
+// Sums of weights of up to 4096 logits, in halves that do not overflow.
+struct Sum {
+  uint32_t hi = 0, lo = 0;
+  __device__ __forceinline__ void add(Halves h) {
+    hi += h.hi;
+    lo += h.lo;
+  }
+  // over the warp's lanes
+  __device__ __forceinline__ uint64_t total() const {
+    const uint64_t h = __reduce_add_sync(0xffffffffu, hi & 0xFFFFu) +
+                       (static_cast<uint64_t>(__reduce_add_sync(0xffffffffu, hi >> 16)) << 16);
+    const uint64_t l = __reduce_add_sync(0xffffffffu, lo & 0xFFFFu) +
+                       (static_cast<uint64_t>(__reduce_add_sync(0xffffffffu, lo >> 16)) << 16);
+    return (h << 20) + l;
+  }
+};
 
 // ---------------------------------------------------------------- a row
 // The part of a row that a CTA works on, and the row's settings.
@@ -309,7 +416,10 @@ struct Row {
   }
   __device__ __forceinline__ float scaled(float x) const { return __fmul_rn(x - top, inv); }
   __device__ __forceinline__ float exponential(float x) const { return expf(scaled(x)); }
-  __device__ __forceinline__ static uint64_t fixed(float e) { return __float2ull_rz(e * kFixed); }
+  __device__ __forceinline__ static uint64_t fixed(float e) {
+    const Halves h = halves(e);
+    return (static_cast<uint64_t>(h.hi) << 20) + h.lo;
+  }
   __device__ __forceinline__ uint64_t weight(float x) const { return fixed(exponential(x)); }
   // Bin of the general selection, and place among the counting bins.
   __device__ __forceinline__ int bin(float x) const {
@@ -321,7 +431,10 @@ struct Row {
   __device__ __forceinline__ static int count_bin(float place) {
     return min(kCountBins - 1, max(0, __float2int_rz(place)));
   }
-  __device__ __forceinline__ int sub_vecs() const { return (vecs + kSegments - 1) / kSegments; }
+  // Vectors per segment: whole rounds of a warp.
+  __device__ __forceinline__ static int segment_vecs(int vecs) {
+    return max(32, (vecs + 32 * kSegments - 1) / (32 * kSegments) * 32);
+  }
 
   // f(x, index) for this thread's logits.
   template <typename F>
@@ -345,7 +458,7 @@ __device__ void clear(Hist& h) {
 // bin whose running sum first reaches it goes to found_* (found_bin = kBins if
 // none does). WEIGHT: sums of weights, else counts.
 template <bool MULTI, bool WEIGHT, typename F>
-__device__ void find_bin(Shared& s, const Hist& h, uint32_t ctas, F want) {
+__device__ uint64_t find_bin(Shared& s, const Hist& h, uint32_t ctas, F want, uint64_t* total) {
   static_assert(kBins == kThreads, "a bin per thread");
   const int b = threadIdx.x;
   uint64_t v = 0;
@@ -356,23 +469,24 @@ __device__ void find_bin(Shared& s, const Hist& h, uint32_t ctas, F want) {
   }
   if (!WEIGHT) v = n;
   if (b == 0) s.found_bin = kBins;
-  uint64_t total;
-  const uint64_t before = block_exclusive(v, s.scan, &total);
-  const uint64_t goal = want(total);
+  const uint64_t before = block_exclusive(v, s.scan, total);
+  const uint64_t goal = by_one(s, [&] { return want(*total); });
   if (before < goal && goal <= before + v) {
     s.found_bin = b;
     s.found_above = before;
     s.found_count = n;
   }
   __syncthreads();
+  return goal;
 }
 
 // Finds the logit (as a key) and the number of logits equal to it at which the
 // running sum over the ranked logits above `limit` (a key) first reaches the
-// goal. Returns false if the sum never does: nothing is cut off.
+// goal, which want(total) gives. Returns false if the sum never does: nothing is
+// cut off. *total_out and *goal_out: the whole sum and the goal.
 template <typename T, bool MULTI, bool WEIGHT, typename F>
 __device__ bool select(const Row<T>& row, Shared& s, int& buf, uint32_t* listed, uint32_t limit, F want,
-                       uint32_t* key_out, uint32_t* count_out) {
+                       uint32_t* key_out, uint32_t* count_out, uint64_t* total_out, uint64_t* goal_out) {
   Hist* h = &s.hist[buf];
   buf ^= 1;
   clear(*h);
@@ -385,7 +499,10 @@ __device__ bool select(const Row<T>& row, Shared& s, int& buf, uint32_t* listed,
   });
   row_barrier<MULTI>();
   uint64_t goal = 0;
-  find_bin<MULTI, WEIGHT>(s, *h, row.ctas, [&](uint64_t total) { return goal = want(total); });
+  uint64_t total = 0;
+  goal = find_bin<MULTI, WEIGHT>(s, *h, row.ctas, want, &total);
+  *total_out = total;
+  *goal_out = goal;
   if (s.found_bin == kBins) return false;
   const int bin = static_cast<int>(s.found_bin);
   uint64_t above = s.found_above;
@@ -448,7 +565,8 @@ __device__ bool select(const Row<T>& row, Shared& s, int& buf, uint32_t* listed,
       }
     });
     row_barrier<MULTI>();
-    find_bin<MULTI, WEIGHT>(s, *h, row.ctas, [&](uint64_t) { return goal - above; });
+    uint64_t inside_total;
+    find_bin<MULTI, WEIGHT>(s, *h, row.ctas, [&](uint64_t) { return goal - above; }, &inside_total);
     const uint32_t b = s.found_bin;
     above += s.found_above;
     count = s.found_count;
@@ -500,26 +618,22 @@ __device__ void general_answer(const Row<T>& row, Shared& s, const SampleParams&
   int buf = 0;
   // the kept set: logits above `key`, and the first `ties` of those equal to it
   uint32_t key = 0, ties = 0;
+  uint64_t over, goal_p;
   if (top_k > 0 && top_k < p.vocab)
     if (!select<T, MULTI, false>(row, s, buf, &s.listed[1], 0u, [&](uint64_t) { return static_cast<uint64_t>(top_k); },
-                                 &key, &ties))
+                                 &key, &ties, &over, &goal_p))
       key = ties = 0;
   if (top_p < 1.f) {
     const uint64_t w = ties ? row.weight(key_value(key)) : 0;
-    uint64_t goal = 0, over = 0;
     uint32_t k2, t2;
     const bool cut = select<T, MULTI, true>(
-        row, s, buf, &s.listed[2], key,
-        [&](uint64_t total) {
-          over = total;
-          return goal = top_p_goal(top_p, total + ties * w);
-        },
-        &k2, &t2);
+        row, s, buf, &s.listed[2], key, [&](uint64_t total) { return top_p_goal(top_p, total + ties * w); }, &k2, &t2,
+        &over, &goal_p);
     if (cut) {
       key = k2;
       ties = t2;
     } else if (ties) {
-      const uint64_t need = (goal - over + w - 1) / (w ? w : 1);
+      const uint64_t need = (goal_p - over + w - 1) / (w ? w : 1);
       ties = need < ties ? static_cast<uint32_t>(need) : ties;
     }
   }
@@ -576,7 +690,7 @@ __device__ void general_answer(const Row<T>& row, Shared& s, const SampleParams&
     total += __shfl_sync(0xffffffffu, w_inc, 31);
     tie_total += __shfl_sync(0xffffffffu, t_inc, 31);
   }
-  const uint64_t goal = answer_goal(u, total);
+  const uint64_t goal = by_one(s, [&] { return answer_goal(u, total); });
   if (my_before <= goal && goal < my_before + my_weight) {
     uint64_t before = my_before;
     uint32_t tie_before = my_tie_before;
@@ -640,7 +754,7 @@ __device__ void list_answer(const Row<T>& row, Shared& s, int n, int64_t top_k, 
     sum += w[j];
   }
   uint64_t before = block_exclusive(sum, s.scan, &whole);
-  const uint64_t far = top_p < 1.f ? top_p_goal(top_p, whole) : ~0ull;
+  const uint64_t far = by_one(s, [&] { return top_p < 1.f ? top_p_goal(top_p, whole) : ~0ull; });
   // kept weights by segments of the vocabulary, two per thread
   Answer& a = s.answer;
   static_assert(kAnswerBins == 2 * kThreads && kThreads * sizeof(uint32_t) * 2 + sizeof(Answer) <= sizeof(s.hist),
@@ -671,7 +785,7 @@ __device__ void list_answer(const Row<T>& row, Shared& s, int n, int64_t top_k, 
     b2[j] = a.lo[b] + (static_cast<uint64_t>(a.hi[b]) << 32);
   }
   before = block_exclusive(b2[0] + b2[1], s.scan, &whole);
-  const uint64_t goal = answer_goal(u, whole);
+  const uint64_t goal = by_one(s, [&] { return answer_goal(u, whole); });
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     if (before <= goal && goal < before + b2[j]) {
@@ -708,61 +822,81 @@ __device__ void list_answer(const Row<T>& row, Shared& s, int n, int64_t top_k, 
 }
 
 // ---------------------------------------------------------------- second pass
-// Adds up this slice's weights: *total all of them, *above those placed above
-// cut_lo, seg_weight[] the latter (at least min_p) by segments; logits placed
-// in [cut_lo, cut_hi) are appended to CTA 0's list. Without CUT every logit
-// counts as above and only the segments are summed. A warp has kSubs
-// consecutive segments, four vectors per lane in flight.
+// Adds up this slice's weights: sum_total all of them, sum_above those placed
+// above cut_lo, seg_weight[] the latter (at least min_p) by segments; logits
+// placed in [cut_lo, cut_hi) are appended to CTA 0's list. Without CUT every
+// logit counts as above and only the segments are summed. Warp w has segments
+// w, w + 32, ... and goes through them in rounds of 32 vectors, four rounds'
+// loads in flight.
 template <typename T, bool MULTI, bool CUT>
 __device__ void sum_segments(const Row<T>& row, Shared& s, float cut_lo, float cut_hi) {
   constexpr int E = Row<T>::E;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int per = row.sub_vecs();
-  uint64_t total = 0, above = 0;
-#pragma unroll 1
-  for (int sub = 0; sub < kSubs; ++sub) {
-    const int seg = warp * kSubs + sub;
-    const int v1 = min((seg + 1) * per, row.vecs);
-    uint64_t acc = 0;
-    for (int v = seg * per + lane; v < v1; v += 32 * 4) {
-      Raw<T, E> raw[4];
+  const int rounds = Row<T>::segment_vecs(row.vecs) / 32;  // per segment
+  const int segs = (row.vecs + rounds * 32 - 1) / (rounds * 32);
+  const int mine = segs > warp ? (segs - warp + kWarps - 1) / kWarps : 0;
+  for (int i = threadIdx.x; i < kSegments; i += kThreads)
+    if (i >= segs) s.seg_weight[i] = 0;
+  Sum acc, all, above;
+  uint64_t total = 0, over = 0;
+  int seg = warp, round = 0;  // of the next vector to load
+  int done = warp, done_round = 0;
+  for (int t = mine * rounds; t > 0; t -= 4) {
+    Raw<T, E> raw[4];
+    int at[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (v + 32 * j < v1) raw[j] = row.get(v + 32 * j);
+    for (int j = 0; j < 4; ++j) {
+      at[j] = (seg * rounds + round) * 32 + lane;
+      if (j < t && at[j] < row.vecs)
+        raw[j] = row.get(at[j]);
+      else
+        at[j] = -1;
+      if (++round == rounds) {
+        round = 0;
+        seg += kWarps;
+      }
+    }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (v + 32 * j >= v1) break;
+    for (int j = 0; j < 4; ++j) {
+      if (j >= t) break;
+      if (at[j] >= 0) {
         float x[E];
         unpack<T, E>(raw[j], x);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           const float ex = row.exponential(x[e]);
-          const uint64_t w = Row<T>::fixed(ex);
+          const Halves w = halves(ex);
           if (CUT) {
             const float place = row.place(x[e]);
-            total += w;
+            all.add(w);
             if (place < cut_lo) {
-              above += w;
-              if (ex >= row.min_p) acc += w;
+              above.add(w);
+              if (ex >= row.min_p) acc.add(w);
             } else if (place < cut_hi) {
-              append<MULTI>(s, &s.listed[0], list_entry(x[e], static_cast<uint32_t>(row.c0 + (v + 32 * j) * E + e)));
+              append<MULTI>(s, &s.listed[0], list_entry(x[e], static_cast<uint32_t>(row.c0 + at[j] * E + e)));
             }
           } else if (ex >= row.min_p) {
-            acc += w;
+            acc.add(w);
           }
         }
       }
+      if (++done_round == rounds) {
+        const uint64_t w = acc.total();
+        if (lane == 0) s.seg_weight[done] = w;
+        acc = Sum();
+        if (CUT) {
+          total += all.total();
+          over += above.total();
+          all = above = Sum();
+        }
+        done_round = 0;
+        done += kWarps;
+      }
     }
-    acc = warp_total(acc);
-    if (lane == 0) s.seg_weight[seg] = acc;
   }
-  if (CUT) {
-    total = warp_total(total);
-    above = warp_total(above);
-    if (lane == 0) {
-      atomicAdd(reinterpret_cast<unsigned long long*>(&s.sum_total), static_cast<unsigned long long>(total));
-      atomicAdd(reinterpret_cast<unsigned long long*>(&s.sum_above), static_cast<unsigned long long>(above));
-    }
+  if (CUT && lane == 0) {
+    atomicAdd(reinterpret_cast<unsigned long long*>(&s.sum_total), static_cast<unsigned long long>(total));
+    atomicAdd(reinterpret_cast<unsigned long long*>(&s.sum_above), static_cast<unsigned long long>(over));
   }
 }
 
@@ -784,7 +918,7 @@ __device__ bool segment_answer(const Row<T>& row, Shared& s, const SampleParams&
       above += remote<MULTI>(&s.sum_above, c);
     }
     n = static_cast<int>(min(s.listed[0], static_cast<uint32_t>(kListKeys)));
-    const uint64_t goal = top_p_goal(top_p, total);
+    const uint64_t goal = by_one(s, [&] { return top_p_goal(top_p, total); });
     if (s.listed[0] > static_cast<uint32_t>(kListKeys) || above >= goal) return false;
     per = (sort_list(s.list, n) + kThreads - 1) / kThreads;
     uint64_t sum = 0, listed;
@@ -805,6 +939,7 @@ __device__ bool segment_answer(const Row<T>& row, Shared& s, const SampleParams&
   }
   // the segments of all slices, two per thread
   Answer& a = s.answer;
+  static_assert(kListKeys == 8 * kThreads, "the largest sort");
   static_assert(kAnswerBins == kMaxCluster * kSegments, "a bin per segment of the largest cluster");
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
@@ -824,7 +959,7 @@ __device__ bool segment_answer(const Row<T>& row, Shared& s, const SampleParams&
         const int index = static_cast<int>(static_cast<uint32_t>(s.list[i]));
         const int c = index / slice;
         const int vecs = (min(slice, vocab - c * slice) + E - 1) / E;
-        const int b = c * kSegments + (index - c * slice) / E / ((vecs + kSegments - 1) / kSegments);
+        const int b = c * kSegments + (index - c * slice) / E / Row<T>::segment_vecs(vecs);
         add_weight(&a.lo[b], &a.hi[b], Row<T>::fixed(e));
       }
     }
@@ -837,7 +972,7 @@ __device__ bool segment_answer(const Row<T>& row, Shared& s, const SampleParams&
     b2[j] = a.lo[b] + (static_cast<uint64_t>(a.hi[b]) << 32);
   }
   uint64_t before = block_exclusive(b2[0] + b2[1], s.scan, &whole);
-  const uint64_t goal = answer_goal(u, whole);
+  const uint64_t goal = by_one(s, [&] { return answer_goal(u, whole); });
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     if (before <= goal && goal < before + b2[j]) {
@@ -859,7 +994,7 @@ __device__ bool segment_answer(const Row<T>& row, Shared& s, const SampleParams&
     part.n = min(slice, vocab - part.c0);
     part.vecs = (part.n + E - 1) / E;
   }
-  const int sub = part.sub_vecs();
+  const int sub = Row<T>::segment_vecs(part.vecs);
   const int v1 = min((seg + 1) * sub, part.vecs);
   uint64_t run = s.found_above;
   for (int base = seg * sub; base < v1; base += 32) {
@@ -1069,65 +1204,82 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, 
         atomicAdd(&s.counts.count[b], 1u);
         if (b < kWeighedBins) atomicAdd(&s.counts.weight[b], expf((x - row.anchor) * row.inv));
       });
-      row_barrier<MULTI>();
-    }
-    uint32_t n[2];
-    float w[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int b = 2 * threadIdx.x + j;
-      n[j] = 0;
-      w[j] = 0.f;
-      for (uint32_t c = 0; c < row.ctas; ++c) {
-        n[j] += remote<MULTI>(&s.counts.count[b], c);
-        if (b < kWeighedBins) w[j] += remote<MULTI>(&s.counts.weight[b], c);
-      }
-      if (b >= kWeighedBins && b < kCountBins - 1)
-        w[j] = n[j] * expf((kAnchorBin - b - 0.5f) * (1.f / kCountsPerUnit));
-    }
-    uint64_t all;
-    uint64_t count_before = block_exclusive(static_cast<uint64_t>(n[0] + n[1]), s.scan, &all);
-    float whole;
-    float weight_before = block_exclusive(w[0] + w[1], s.fscan, &whole);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint32_t b = 2 * threadIdx.x + j;
-      const uint64_t upto = count_before + n[j];
-      const unsigned long long bin = static_cast<unsigned long long>(b) << 32;
-      if (b == kCountBins - 1) {
-        s.found_count = static_cast<uint32_t>(count_before);  // logits in all bins but the last
-      } else if (need_k) {
-        const uint64_t k = static_cast<uint64_t>(top_k);
-        if (count_before < k && k <= upto) s.cut_hi[0] = bin | upto;
-      } else if (n[j]) {
-        // rounding may let two neighbouring bins seem to hold a bound, or none; the
-        // exact sums decide, but every CTA has to take the same one
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float margin = i == 0 ? kMargin : kSmallMargin;
-          const float lo = (top_p - margin) * whole, hi = (top_p + margin) * whole;
-          if (weight_before <= lo && lo < weight_before + w[j]) atomicMin(&s.cut_lo[i], bin | count_before);
-          if (weight_before <= hi && hi < weight_before + w[j]) atomicMin(&s.cut_hi[i], bin | upto);
+      __syncthreads();
+      // to CTA 0, which looks for the end and tells the others
+      if (row.rank != 0) {
+        for (int b = threadIdx.x; b < kCountBins; b += kThreads) {
+          const uint32_t c = s.counts.count[b];
+          if (c) remote_add(&s.counts.count[b], 0, c);
+          if (b < kWeighedBins && c) remote_add(&s.counts.weight[b], 0, s.counts.weight[b]);
         }
       }
-      count_before += n[j];
-      weight_before += w[j];
+      row_barrier<MULTI>();
     }
-    __syncthreads();
-    // from the first bin if none holds the lower bound; to the last but one, as the
-    // last bin's weights are zero, if none holds the upper
-    uint64_t from = 0, to = 0;
+    if (row.rank == 0) {
+      uint32_t n[2];
+      float w[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      from = need_k || s.cut_lo[i] == ~0ull ? 0 : s.cut_lo[i];
-      to = s.cut_hi[i] != ~0ull ? s.cut_hi[i] : static_cast<uint64_t>(kCountBins - 2) << 32 | s.found_count;
-      general = static_cast<uint32_t>(to) - static_cast<uint32_t>(from) > static_cast<uint32_t>(kListKeys);
-      if (need_k || !general) break;
+      for (int j = 0; j < 2; ++j) {
+        const int b = 2 * threadIdx.x + j;
+        n[j] = s.counts.count[b];
+        w[j] = b < kWeighedBins ? s.counts.weight[b]
+                                : b < kCountBins - 1 ? n[j] * expf((kAnchorBin - b - 0.5f) * (1.f / kCountsPerUnit)) : 0.f;
+      }
+      uint64_t all;
+      uint64_t count_before = block_exclusive(static_cast<uint64_t>(n[0] + n[1]), s.scan, &all);
+      float whole;
+      float weight_before = block_exclusive(w[0] + w[1], s.fscan, &whole);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t b = 2 * threadIdx.x + j;
+        const uint64_t upto = count_before + n[j];
+        const unsigned long long bin = static_cast<unsigned long long>(b) << 32;
+        if (b == kCountBins - 1) {
+          s.found_count = static_cast<uint32_t>(count_before);  // logits in all bins but the last
+        } else if (need_k) {
+          const uint64_t k = static_cast<uint64_t>(top_k);
+          if (count_before < k && k <= upto) s.cut_hi[0] = bin | upto;
+        } else if (n[j]) {
+          // (rounding may let two neighbouring bins seem to hold a bound, or none: the
+          // exact sums decide)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float margin = i == 0 ? kMargin : kSmallMargin;
+            const float lo = (top_p - margin) * whole, hi = (top_p + margin) * whole;
+            if (weight_before <= lo && lo < weight_before + w[j]) atomicMin(&s.cut_lo[i], bin | count_before);
+            if (weight_before <= hi && hi < weight_before + w[j]) atomicMin(&s.cut_hi[i], bin | upto);
+          }
+        }
+        count_before += n[j];
+        weight_before += w[j];
+      }
+      __syncthreads();
+      // from the first bin if none holds the lower bound; to the last but one, as the
+      // last bin's weights are zero, if none holds the upper
+      uint64_t from = 0, to = 0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        from = need_k || s.cut_lo[i] == ~0ull ? 0 : s.cut_lo[i];
+        to = s.cut_hi[i] != ~0ull ? s.cut_hi[i] : static_cast<uint64_t>(kCountBins - 2) << 32 | s.found_count;
+        general = static_cast<uint32_t>(to) - static_cast<uint32_t>(from) > static_cast<uint32_t>(kListKeys);
+        if (need_k || !general) break;
+      }
+      general |= !(whole < INFINITY);
+      cut_lo = from >> 32 == 0 ? -INFINITY : static_cast<float>(from >> 32);
+      cut_hi = static_cast<float>((to >> 32) + 1);
+      if (MULTI && threadIdx.x == 0) {
+        s.told[0] = cut_lo;
+        s.told[1] = cut_hi;
+        s.told[2] = general ? 1.f : 0.f;
+      }
     }
-    general |= !(whole < INFINITY);
+    if constexpr (MULTI) {
+      row_barrier<MULTI>();
+      cut_lo = remote<MULTI>(&s.told[0], 0);
+      cut_hi = remote<MULTI>(&s.told[1], 0);
+      general = remote<MULTI>(&s.told[2], 0) != 0.f;
+    }
     listing = need_k && !general;
-    cut_lo = from >> 32 == 0 ? -INFINITY : static_cast<float>(from >> 32);
-    cut_hi = static_cast<float>((to >> 32) + 1);
   }
 
   // ---- second pass
