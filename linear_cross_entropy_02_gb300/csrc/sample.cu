@@ -11,8 +11,8 @@
 // counts logits in 2048 bins of (x - anchor) / T, the anchor being the maximum
 // of the row's first part. Then:
 //   top_k that some bins cover with at most kListKeys logits: the second pass
-//     collects those logits in shared memory; they are sorted there, cut by all
-//     three filters, and the token is drawn from them.
+//     collects those logits in shared memory, where all three filters cut them
+//     and the token is drawn.
 //   top_p: the counts times the weights of the bins' middles (exact float sums
 //     for the few largest) say in which bins the end of the prefix should lie;
 //     the second pass adds up all weights exactly, those above these bins by
@@ -46,6 +46,8 @@ constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kListKeys = 8192;
+constexpr int kFew = 64;       // entries that are compared each with each
+constexpr int kShort = 256;    // the same for a list of candidates
 constexpr float kRange = 28.f;  // exp(-28) 2^40 < 1
 constexpr float kFixed = 1099511627776.f;  // 2^40
 
@@ -56,14 +58,14 @@ constexpr float kBinsPerUnit = (kBins - 1) / kRange;
 constexpr int kCountBins = 2048;
 constexpr int kAnchorBin = kCountBins / 2;
 constexpr float kCountsPerUnit = kAnchorBin / kRange;
-// Logits above 3 below the anchor are weighed one by one for the estimate: a
+// Logits above 4 below the anchor are weighed one by one for the estimate: a
 // bin's middle is up to 1.4% off for one logit, which only matters where a few
 // logits carry the row. (All of a normal row's logits would slow the pass:
-// 3 below the maximum there are some per cent of them.)
-constexpr int kWeighedBins = kAnchorBin + 110;
+// 4 below the maximum there are some per cent of them.)
+constexpr int kWeighedBins = kAnchorBin + 146;
 // How far around the estimated end logits are collected, of the whole weight:
 // the first margin if the list holds what lies in it, else the second.
-constexpr float kMargin = 0.0015f, kSmallMargin = 0.0002f;
+constexpr float kMargin = 0.0008f, kSmallMargin = 0.0002f;
 // Segments of a slice whose weights are kept apart, at most.
 constexpr int kSegments = 256;
 constexpr int kFirstVectors = 4;  // per thread: the part of the row that sets the anchor
@@ -103,6 +105,8 @@ struct Shared {
   uint32_t first;      // lowest index of the largest logit in this slice
   uint32_t key_lo, key_hi;
   uint32_t listed[4];  // lengths of the lists of a row, one counter per use
+  uint64_t few[kFew];
+  uint32_t few_count;
   uint32_t result_key, result_count;
   unsigned long long cut_lo[2], cut_hi[2];  // first and last bin to collect; low words: logits before and up to them
   uint32_t general;         // CTA 0: the row needs the general selection
@@ -273,94 +277,6 @@ __device__ __forceinline__ uint64_t by_one(Shared& s, F f) {
   return s.goal;
 }
 
-__device__ __forceinline__ int pow2_at_least(int n) {
-  int m = 2;
-  while (m < n) m <<= 1;
-  return m;
-}
-
-// Exchanges with the entry `gap` places on: the smaller stays below where the
-// run is to rise.
-__device__ __forceinline__ uint64_t in_order(uint64_t a, uint64_t b, bool low_place, bool rising) {
-  return (a > b) == (low_place == rising) ? b : a;
-}
-
-// Sorts the first n <= kListKeys entries of the list, rising; returns n rounded
-// up to a power of two, the rest filled with the largest entry. A bitonic network
-// with entry j kThreads + t in thread t's registers: gaps below 32 are shuffles,
-// gaps of kThreads and more are between a thread's own, and only those between
-// go through shared memory.
-template <int PER>
-__device__ void sort_entries(uint64_t* a, int n, int m) {
-  const int t = threadIdx.x;
-  uint64_t v[PER];
-#pragma unroll
-  for (int j = 0; j < PER; ++j) v[j] = j * kThreads + t < n ? a[j * kThreads + t] : ~0ull;
-  for (int size = 2; size <= m; size <<= 1) {
-    for (int gap = size >> 1; gap > 0; gap >>= 1) {
-      if (gap >= kThreads) {
-        const int g = gap / kThreads;
-#pragma unroll
-        for (int j = 0; j < PER; ++j) {
-#pragma unroll
-          for (int k = 1; k < PER; k <<= 1) {
-            if (k == g && (j & k) == 0) {
-              const bool rising = ((j * kThreads + t) & size) == 0;
-              const uint64_t lo = in_order(v[j], v[j | k], true, rising);
-              v[j | k] = in_order(v[j | k], v[j], false, rising);
-              v[j] = lo;
-            }
-          }
-        }
-      } else if (gap >= 32) {
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < PER; ++j) a[j * kThreads + t] = v[j];
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < PER; ++j)
-          v[j] = in_order(v[j], a[j * kThreads + (t ^ gap)], (t & gap) == 0, ((j * kThreads + t) & size) == 0);
-      } else {
-#pragma unroll
-        for (int j = 0; j < PER; ++j)
-          v[j] = in_order(v[j], __shfl_xor_sync(0xffffffffu, v[j], gap), (t & gap) == 0,
-                          ((j * kThreads + t) & size) == 0);
-      }
-    }
-  }
-  __syncthreads();
-#pragma unroll
-  for (int j = 0; j < PER; ++j) a[j * kThreads + t] = v[j];
-  __syncthreads();
-}
-
-__device__ int sort_list(uint64_t* a, int n) {
-  const int m = pow2_at_least(n);
-  __syncthreads();
-  if (m <= 256) {
-    // few: an entry's place is the number of smaller ones (entries differ by their index)
-    uint64_t mine = ~0ull;
-    int place = threadIdx.x;
-    if (threadIdx.x < n) {
-      mine = a[threadIdx.x];
-      place = 0;
-      for (int i = 0; i < n; ++i) place += a[i] < mine;
-    }
-    __syncthreads();
-    if (threadIdx.x < m) a[place] = mine;
-    __syncthreads();
-  } else if (m <= kThreads) {
-    sort_entries<1>(a, n, m);
-  } else if (m == 2 * kThreads) {
-    sort_entries<2>(a, n, m);
-  } else if (m == 4 * kThreads) {
-    sort_entries<4>(a, n, m);
-  } else {
-    sort_entries<8>(a, n, m);
-  }
-  return m;
-}
-
 // floor(e 2^40) for e in [0, 1] as hi 2^20 + lo. Adding to 2^23 with rounding
 // towards zero leaves the whole part in the mantissa; what it left is exact.
 // (The 64-bit conversion instruction runs at the rate of double precision,
@@ -431,6 +347,23 @@ struct Row {
   __device__ __forceinline__ static int count_bin(float place) {
     return min(kCountBins - 1, max(0, __float2int_rz(place)));
   }
+  // The smallest logit with a place before `cut` (places fall as logits rise),
+  // infinity if there is none. For a whole warp: each step tries 32 points of the
+  // range of keys that is left.
+  __device__ __forceinline__ float first_before(float cut) const {
+    const uint32_t lane = threadIdx.x & 31;
+    uint32_t lo = order_key(-INFINITY), hi = order_key(INFINITY);  // hi: known to be before, or infinity
+    while (lo < hi) {
+      const uint32_t step = (hi - lo + 31) / 32;
+      const uint32_t k = lo + lane * step;
+      const uint32_t yes = __ballot_sync(0xffffffffu, k >= hi || place(key_value(k)) < cut);
+      const uint32_t at = yes ? __ffs(yes) - 1 : 32;  // the first point that is before
+      const uint32_t l = lo;
+      if (at < 32) hi = min(hi, l + at * step);
+      if (at > 0) lo = l + (at - 1) * step + 1;
+    }
+    return key_value(hi);
+  }
   // Vectors per segment: whole rounds of a warp.
   __device__ __forceinline__ static int segment_vecs(int vecs) {
     return max(32, (vecs + 32 * kSegments - 1) / (32 * kSegments) * 32);
@@ -451,6 +384,102 @@ struct Row {
 __device__ void clear(Hist& h) {
   for (int i = threadIdx.x; i < kBins; i += kThreads) h.count[i] = h.lo[i] = h.hi[i] = 0;
   __syncthreads();
+}
+
+template <typename T>
+__device__ __forceinline__ void write_answer(const Row<T>& row, const SampleParams& p, int64_t r, uint32_t index, float x,
+                                             uint64_t whole) {
+  p.tokens[r] = index;
+  if (p.logprobs) p.logprobs[r] = row.scaled(x) - logf(__ll2float_rn(static_cast<int64_t>(whole)) * (1.f / kFixed));
+}
+
+// Over the CTA, in every thread.
+__device__ __forceinline__ uint64_t block_total(Shared& s, uint64_t v) {
+  v = warp_total(v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) s.scan[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return warp_total(s.scan[threadIdx.x & 31]);
+}
+
+// The entry of the CTA's list of n at which the running sum in rank order,
+// `start` before the first, reaches the goal (start < goal <= start + sum). WEIGHT:
+// sums of weights, else counts. A histogram over the range of entries (they are
+// whole numbers in rank order, all different), again over the bin that holds the
+// goal, until that has at most kFew. Uses the first histogram.
+template <typename T, bool WEIGHT>
+__device__ uint64_t list_reach(const Row<T>& row, Shared& s, int n, uint64_t start, uint64_t goal) {
+  Hist& h = s.hist[0];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint64_t lo = ~0ull, hi = 0;
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    lo = min(lo, s.list[i]);
+    hi = max(hi, s.list[i]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+  }
+  __syncthreads();
+  if (lane == 0) {
+    s.scan[warp] = lo;
+    s.few[warp] = hi;
+  }
+  __syncthreads();
+  lo = s.scan[lane];
+  hi = s.few[lane];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+  }
+  while (true) {
+    const int bits = 64 - __clzll(static_cast<long long>(hi - lo));
+    const int shift = bits > 10 ? bits - 10 : 0;
+    static_assert(kBins == 1 << 10, "a range of 10 + shift bits");
+    clear(h);
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+      const uint64_t e = s.list[i];
+      if (e >= lo && e <= hi) {
+        const int b = static_cast<int>((e - lo) >> shift);
+        atomicAdd(&h.count[b], 1u);
+        if (WEIGHT) add_weight(&h.lo[b], &h.hi[b], row.weight(entry_value(e)));
+      }
+    }
+    __syncthreads();
+    const int b = threadIdx.x;
+    const uint64_t v = WEIGHT ? h.lo[b] + (static_cast<uint64_t>(h.hi[b]) << 32) : h.count[b];
+    uint64_t total;
+    const uint64_t before = start + block_exclusive(v, s.scan, &total);
+    if (before < goal && goal <= before + v) {
+      s.found_bin = b;
+      s.found_above = before;
+      s.found_count = h.count[b];
+      s.few_count = 0;
+    }
+    __syncthreads();
+    start = s.found_above;
+    lo += static_cast<uint64_t>(s.found_bin) << shift;
+    hi = min(hi, lo + ((uint64_t{1} << shift) - 1));
+    if (s.found_count <= static_cast<uint32_t>(kFew)) break;
+    __syncthreads();
+  }
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const uint64_t e = s.list[i];
+    if (e >= lo && e <= hi) s.few[atomicAdd(&s.few_count, 1u)] = e;
+  }
+  __syncthreads();
+  const int few = static_cast<int>(s.found_count);
+  if (threadIdx.x < few) {
+    const uint64_t e = s.few[threadIdx.x];
+    uint64_t before = start;
+    for (int i = 0; i < few; ++i)
+      if (s.few[i] < e) before += WEIGHT ? row.weight(entry_value(s.few[i])) : 1;
+    if (before < goal && goal <= before + (WEIGHT ? row.weight(entry_value(e)) : 1)) s.found_value = e;
+  }
+  __syncthreads();
+  return s.found_value;
 }
 
 // ---------------------------------------------------------------- general selection
@@ -575,32 +604,23 @@ __device__ bool select(const Row<T>& row, Shared& s, int& buf, uint32_t* listed,
     key_lo = top - key_lo > width ? top - width : key_lo;
     key_hi = top;
   }
-  // few enough: CTA 0 sorts them
+  // few enough: CTA 0 looks through them
   row.each([&](float x, uint32_t i) {
     if (inside(x)) append<MULTI>(s, listed, list_entry(x, i));
   });
   row_barrier<MULTI>();
   if (row.rank == 0) {
-    const int n = static_cast<int>(count);
-    const int per = (sort_list(s.list, n) + kThreads - 1) / kThreads;
-    uint64_t sum = 0, total;
-    for (int j = 0; j < per; ++j) {
-      const int i = threadIdx.x * per + j;
-      sum += i < n ? (WEIGHT ? row.weight(entry_value(s.list[i])) : 1) : 0;
-    }
-    uint64_t before = above + block_exclusive(sum, s.scan, &total);
-    for (int j = 0; j < per; ++j) {
-      const int i = threadIdx.x * per + j;
-      if (i >= n) break;
-      const uint64_t w = WEIGHT ? row.weight(entry_value(s.list[i])) : 1;
-      if (before < goal && goal <= before + w) {
-        const uint32_t nk = static_cast<uint32_t>(s.list[i] >> 32);
-        int f = i;
-        while (f > 0 && static_cast<uint32_t>(s.list[f - 1] >> 32) == nk) --f;
-        s.result_key = ~nk;
-        s.result_count = static_cast<uint32_t>(i - f + 1);
-      }
-      before += w;
+    const uint64_t e = list_reach<T, WEIGHT>(row, s, static_cast<int>(count), above, goal);
+    uint32_t ties = 0;  // of the same logit, up to that entry
+    for (int i = threadIdx.x; i < static_cast<int>(count); i += kThreads)
+      ties += s.list[i] >> 32 == e >> 32 && s.list[i] <= e;
+    ties = __reduce_add_sync(0xffffffffu, ties);
+    if ((threadIdx.x & 31) == 0) s.red[threadIdx.x >> 5] = ties;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int w = 1; w < kWarps; ++w) ties += s.red[w];
+      s.result_key = ~static_cast<uint32_t>(e >> 32);
+      s.result_count = ties;
     }
   }
   row_barrier<MULTI>();
@@ -718,9 +738,7 @@ __device__ void general_answer(const Row<T>& row, Shared& s, const SampleParams&
           uint64_t we = kept_weight(f[e]);
           if (ties && order_key(f[e]) == key) we = tb++ < ties ? w_tie : 0;
           if (mb <= goal && goal < mb + we) {
-            p.tokens[r] = row.c0 + v * E + e;
-            if (p.logprobs)
-              p.logprobs[r] = row.scaled(f[e]) - logf(__ll2float_rn(static_cast<int64_t>(total)) * (1.f / kFixed));
+            write_answer(row, p, r, static_cast<uint32_t>(row.c0 + v * E + e), f[e], total);
           }
           mb += we;
         }
@@ -733,58 +751,89 @@ __device__ void general_answer(const Row<T>& row, Shared& s, const SampleParams&
 }
 
 // ---------------------------------------------------------------- answers from a list
-// The token from a list of n candidates, at least the first top_k by rank.
+// The token from a list of n <= kShort candidates, at least the first top_k by
+// rank. An entry's rank and what lies before it come from comparing it with all
+// the others, in rank order and again in index order: few barriers, no sort.
 template <typename T>
-__device__ void list_answer(const Row<T>& row, Shared& s, int n, int64_t top_k, float top_p, float u, int vocab,
-                            int64_t* token, float* logprob) {
-  constexpr int kPer = kListKeys / kThreads;
-  const int per = (sort_list(s.list, n) + kThreads - 1) / kThreads;
-  if (top_k > 0 && n > top_k) n = static_cast<int>(top_k);
-  uint64_t w[kPer], sum = 0, whole;
-  uint32_t pass = 0;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int i = threadIdx.x * per + j;
-    w[j] = 0;
-    if (j < per && i < n) {
-      const float e = row.exponential(entry_value(s.list[i]));
-      w[j] = Row<T>::fixed(e);
-      if (i == 0 || e >= row.min_p) pass |= 1u << j;
-    }
-    sum += w[j];
+__device__ void short_list_answer(const Row<T>& row, Shared& s, const SampleParams& p, int64_t r, int n, int64_t top_k,
+                                  float top_p, float u) {
+  uint64_t* weights = reinterpret_cast<uint64_t*>(&s.hist[0]);
+  static_assert(sizeof(s.hist) >= kShort * sizeof(uint64_t) && kShort <= kThreads, "weights in the histograms' place");
+  const int i = threadIdx.x;
+  uint64_t mine = ~0ull, w = 0, before = 0;
+  float e = 0.f;
+  int rank = 0;
+  __syncthreads();
+  if (i < n) {
+    mine = s.list[i];
+    e = row.exponential(entry_value(mine));
+    weights[i] = w = Row<T>::fixed(e);
   }
-  uint64_t before = block_exclusive(sum, s.scan, &whole);
-  const uint64_t far = by_one(s, [&] { return top_p < 1.f ? top_p_goal(top_p, whole) : ~0ull; });
+  __syncthreads();
+  if (i < n) {
+    for (int k = 0; k < n; ++k) {
+      const bool first = s.list[k] < mine;
+      rank += first;
+      before += first ? weights[k] : 0;
+    }
+  }
+  bool keep = i < n && (top_k <= 0 || rank < top_k);
+  if (top_p < 1.f) {
+    const uint64_t whole = block_total(s, keep ? w : 0);
+    const uint64_t far = by_one(s, [&] { return top_p_goal(top_p, whole); });
+    keep = keep && (rank == 0 || before < far);
+  }
+  keep = keep && (rank == 0 || e >= row.min_p);
+  const uint64_t whole = block_total(s, keep ? w : 0);
+  if (i < n) weights[i] = keep ? w : 0;
+  const uint64_t goal = by_one(s, [&] { return answer_goal(u, whole); });
+  if (keep) {
+    const uint32_t index = static_cast<uint32_t>(mine);
+    before = 0;
+    for (int k = 0; k < n; ++k) before += static_cast<uint32_t>(s.list[k]) < index ? weights[k] : 0;
+    if (before <= goal && goal < before + w) write_answer(row, p, r, index, entry_value(mine), whole);
+  }
+}
+
+// The same for a long list.
+template <typename T>
+__device__ void list_answer(const Row<T>& row, Shared& s, const SampleParams& p, int64_t r, int n, int64_t top_k,
+                            float top_p, float u) {
+  uint64_t last = ~0ull;  // last entry that the filters by rank keep
+  if (top_k > 0 && n > top_k) last = list_reach<T, false>(row, s, n, 0, static_cast<uint64_t>(top_k));
+  if (top_p < 1.f) {
+    uint64_t sum = 0;
+    for (int i = threadIdx.x; i < n; i += kThreads)
+      if (s.list[i] <= last) sum += row.weight(entry_value(s.list[i]));
+    const uint64_t whole = block_total(s, sum);
+    const uint64_t goal = by_one(s, [&] { return top_p_goal(top_p, whole); });
+    last = min(last, list_reach<T, true>(row, s, n, 0, goal));
+  }
   // kept weights by segments of the vocabulary, two per thread
   Answer& a = s.answer;
   static_assert(kAnswerBins == 2 * kThreads && kThreads * sizeof(uint32_t) * 2 + sizeof(Answer) <= sizeof(s.hist),
                 "segments, and the places of the tokens in one");
-  const uint32_t width = static_cast<uint32_t>((vocab + kAnswerBins - 1) / kAnswerBins);
+  const uint32_t width = static_cast<uint32_t>((p.vocab + kAnswerBins - 1) / kAnswerBins);
+  __syncthreads();
 #pragma unroll
   for (int j = 0; j < 2; ++j) a.lo[2 * threadIdx.x + j] = a.hi[2 * threadIdx.x + j] = 0;
-  if (threadIdx.x == 0) s.listed[3] = 0;
   __syncthreads();
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int i = threadIdx.x * per + j;
-    if (pass >> j & 1) {
-      if (i == 0 || before < far) {
-        const uint32_t b = static_cast<uint32_t>(s.list[i]) / width;
-        add_weight(&a.lo[b], &a.hi[b], w[j]);
-      } else {
-        pass &= ~(1u << j);
-      }
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const uint64_t entry = s.list[i];
+    const float e = row.exponential(entry_value(entry));
+    if (entry <= last && e >= row.min_p) {
+      const uint32_t b = static_cast<uint32_t>(entry) / width;
+      add_weight(&a.lo[b], &a.hi[b], Row<T>::fixed(e));
     }
-    before += w[j];
   }
   __syncthreads();
-  uint64_t b2[2];
+  uint64_t b2[2], whole;
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const int b = 2 * threadIdx.x + j;
     b2[j] = a.lo[b] + (static_cast<uint64_t>(a.hi[b]) << 32);
   }
-  before = block_exclusive(b2[0] + b2[1], s.scan, &whole);
+  uint64_t before = block_exclusive(b2[0] + b2[1], s.scan, &whole);
   const uint64_t goal = by_one(s, [&] { return answer_goal(u, whole); });
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
@@ -798,10 +847,10 @@ __device__ void list_answer(const Row<T>& row, Shared& s, int n, int64_t top_k, 
   // the tokens of that segment (at most `width`): each one's running sum is that of those before it
   uint32_t* place = reinterpret_cast<uint32_t*>(&a + 1);
   const uint32_t bin = s.found_bin;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int i = threadIdx.x * per + j;
-    if ((pass >> j & 1) && static_cast<uint32_t>(s.list[i]) / width == bin) place[atomicAdd(&s.listed[3], 1u)] = i;
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const uint64_t entry = s.list[i];
+    if (entry <= last && static_cast<uint32_t>(entry) / width == bin && row.exponential(entry_value(entry)) >= row.min_p)
+      place[atomicAdd(&s.listed[3], 1u)] = i;
   }
   __syncthreads();
   const int here = static_cast<int>(s.listed[3]);
@@ -813,11 +862,8 @@ __device__ void list_answer(const Row<T>& row, Shared& s, int n, int64_t top_k, 
       const uint64_t other = s.list[place[k]];
       if (static_cast<uint32_t>(other) < index) b += row.weight(entry_value(other));
     }
-    if (b <= goal && goal < b + row.weight(entry_value(mine))) {
-      *token = index;
-      if (logprob)
-        *logprob = row.scaled(entry_value(mine)) - logf(__ll2float_rn(static_cast<int64_t>(whole)) * (1.f / kFixed));
-    }
+    if (b <= goal && goal < b + row.weight(entry_value(mine)))
+      write_answer(row, p, r, index, entry_value(mine), whole);
   }
 }
 
@@ -828,7 +874,8 @@ __device__ void list_answer(const Row<T>& row, Shared& s, int n, int64_t top_k, 
 // logit counts as above and only the segments are summed. Warp w has segments
 // w, w + 32, ... and goes through them in rounds of 32 vectors, four rounds'
 // loads in flight.
-template <typename T, bool MULTI, bool CUT>
+// MIN_P: the row has that filter; without it the segments' sum is sum_above.
+template <typename T, bool MULTI, bool CUT, bool MIN_P>
 __device__ void sum_segments(const Row<T>& row, Shared& s, float cut_lo, float cut_hi) {
   constexpr int E = Row<T>::E;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -839,6 +886,8 @@ __device__ void sum_segments(const Row<T>& row, Shared& s, float cut_lo, float c
     if (i >= segs) s.seg_weight[i] = 0;
   Sum acc, all, above;
   uint64_t total = 0, over = 0;
+  // the same cuts as logits: above from x_lo on, listed from x_hi on
+  const float x_lo = CUT ? row.first_before(cut_lo) : 0.f, x_hi = CUT ? row.first_before(cut_hi) : 0.f;
   int seg = warp, round = 0;  // of the next vector to load
   int done = warp, done_round = 0;
   for (int t = mine * rounds; t > 0; t -= 4) {
@@ -867,15 +916,14 @@ __device__ void sum_segments(const Row<T>& row, Shared& s, float cut_lo, float c
           const float ex = row.exponential(x[e]);
           const Halves w = halves(ex);
           if (CUT) {
-            const float place = row.place(x[e]);
             all.add(w);
-            if (place < cut_lo) {
-              above.add(w);
-              if (ex >= row.min_p) acc.add(w);
-            } else if (place < cut_hi) {
+            if (x[e] >= x_lo) {
+              if (MIN_P) above.add(w);
+              if (!MIN_P || ex >= row.min_p) acc.add(w);
+            } else if (x[e] >= x_hi) {
               append<MULTI>(s, &s.listed[0], list_entry(x[e], static_cast<uint32_t>(row.c0 + at[j] * E + e)));
             }
-          } else if (ex >= row.min_p) {
+          } else if (!MIN_P || ex >= row.min_p) {
             acc.add(w);
           }
         }
@@ -886,7 +934,7 @@ __device__ void sum_segments(const Row<T>& row, Shared& s, float cut_lo, float c
         acc = Sum();
         if (CUT) {
           total += all.total();
-          over += above.total();
+          over += MIN_P ? above.total() : w;
           all = above = Sum();
         }
         done_round = 0;
@@ -910,7 +958,7 @@ __device__ bool segment_answer(const Row<T>& row, Shared& s, const SampleParams&
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int vocab = static_cast<int>(p.vocab);
   uint64_t cut_entry = ~0ull;  // last kept entry of the list
-  int n = 0, per = 0;
+  int n = 0;
   if (cut) {
     uint64_t total = 0, above = 0;
     for (uint32_t c = 0; c < row.ctas; ++c) {
@@ -920,26 +968,14 @@ __device__ bool segment_answer(const Row<T>& row, Shared& s, const SampleParams&
     n = static_cast<int>(min(s.listed[0], static_cast<uint32_t>(kListKeys)));
     const uint64_t goal = by_one(s, [&] { return top_p_goal(top_p, total); });
     if (s.listed[0] > static_cast<uint32_t>(kListKeys) || above >= goal) return false;
-    per = (sort_list(s.list, n) + kThreads - 1) / kThreads;
-    uint64_t sum = 0, listed;
-    for (int j = 0; j < per; ++j) {
-      const int i = threadIdx.x * per + j;
-      if (i < n) sum += row.weight(entry_value(s.list[i]));
-    }
-    uint64_t before = above + block_exclusive(sum, s.scan, &listed);
-    if (above + listed < goal) return false;
-    for (int j = 0; j < per; ++j) {
-      const int i = threadIdx.x * per + j;
-      if (i < n) {
-        const uint64_t w = row.weight(entry_value(s.list[i]));
-        if (before < goal && goal <= before + w) s.found_value = s.list[i];
-        before += w;
-      }
-    }
+    uint64_t sum = 0;
+    for (int i = threadIdx.x; i < n; i += kThreads) sum += row.weight(entry_value(s.list[i]));
+    if (above + block_total(s, sum) < goal) return false;
+    cut_entry = list_reach<T, true>(row, s, n, above, goal);
+    __syncthreads();  // the histogram's place is used again
   }
   // the segments of all slices, two per thread
   Answer& a = s.answer;
-  static_assert(kListKeys == 8 * kThreads, "the largest sort");
   static_assert(kAnswerBins == kMaxCluster * kSegments, "a bin per segment of the largest cluster");
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
@@ -950,10 +986,8 @@ __device__ bool segment_answer(const Row<T>& row, Shared& s, const SampleParams&
   }
   __syncthreads();
   if (cut) {
-    cut_entry = s.found_value;
-    for (int j = 0; j < per; ++j) {
-      const int i = threadIdx.x * per + j;
-      if (i >= n || s.list[i] > cut_entry) break;
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+      if (s.list[i] > cut_entry) continue;
       const float e = row.exponential(entry_value(s.list[i]));
       if (e >= row.min_p) {
         const int index = static_cast<int>(static_cast<uint32_t>(s.list[i]));
@@ -1024,9 +1058,7 @@ __device__ bool segment_answer(const Row<T>& row, Shared& s, const SampleParams&
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         if (b <= goal && goal < b + w[e]) {
-          p.tokens[r] = part.c0 + v * E + e;
-          if (p.logprobs)
-            p.logprobs[r] = part.scaled(x[e]) - logf(__ll2float_rn(static_cast<int64_t>(whole)) * (1.f / kFixed));
+          write_answer(part, p, r, static_cast<uint32_t>(part.c0 + v * E + e), x[e], whole);
         }
         b += w[e];
       }
@@ -1288,17 +1320,25 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, 
       if (row.place(x) < cut_hi) append<MULTI>(s, &s.listed[0], list_entry(x, i));
     });
     row_barrier<MULTI>();
-    if (row.rank == 0)
-      list_answer(row, s, static_cast<int>(s.listed[0]), top_k, top_p, u, vocab, p.tokens + r,
-                  p.logprobs ? p.logprobs + r : nullptr);
+    if (row.rank == 0) {
+      const int n = static_cast<int>(s.listed[0]);
+      if (n <= kShort)
+        short_list_answer(row, s, p, r, n, top_k, top_p, u);
+      else
+        list_answer(row, s, p, r, n, top_k, top_p, u);
+    }
     return;  // nothing of the other CTAs is read any more
   }
   if (!general) {
-    const bool cut = need_counts;
-    if (cut)
-      sum_segments<T, MULTI, true>(row, s, cut_lo, cut_hi);
+    const bool cut = need_counts, min_p = row.min_p > 0.f;
+    if (cut && min_p)
+      sum_segments<T, MULTI, true, true>(row, s, cut_lo, cut_hi);
+    else if (cut)
+      sum_segments<T, MULTI, true, false>(row, s, cut_lo, cut_hi);
+    else if (min_p)
+      sum_segments<T, MULTI, false, true>(row, s, cut_lo, cut_hi);
     else
-      sum_segments<T, MULTI, false>(row, s, cut_lo, cut_hi);
+      sum_segments<T, MULTI, false, false>(row, s, cut_lo, cut_hi);
     row_barrier<MULTI>();
     if (row.rank == 0 && !segment_answer<T, MULTI>(row, s, p, r, slice, top_p, u, cut, cut_lo, cut_hi) &&
         threadIdx.x == 0)
