@@ -11,22 +11,38 @@ from typing import Optional, Union
 
 import torch
 
-from . import _lib
+from . import _lib, _workspaces
 from ._lib import FlceError
 
 _DTYPES = {torch.bfloat16: _lib.FLCE_DTYPE_BF16, torch.float32: _lib.FLCE_DTYPE_F32}
+# The current stream's handle, without making a torch.cuda.Stream of it (2 of a
+# small call's 8 us) where torch offers that.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      None) or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_entries: dict = {}
 
 
-def _call(device: torch.device, name: str, *args):
-    """Calls a C entry with `device` current and its current stream as the last argument."""
-    fn = getattr(_lib.lib(), name)
-    if torch.cuda.current_device() == device.index:
-        rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+def _call(index: int, name: str, *args):
+    """Calls a C entry with CUDA device `index` current and its current stream as the last argument."""
+    fn = _entries.get(name)
+    if fn is None:
+        fn = _entries[name] = getattr(_lib.lib(), name)
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(device):
-            rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+        with torch.cuda.device(index):
+            rc = fn(*args, _raw_stream(index))
     if rc != 0:
         raise FlceError(rc, name)
+
+
+def _space(index: int, nbytes: int) -> torch.Tensor:
+    """The package's cached workspace of this device and its current stream, of at least nbytes."""
+    ws = _workspaces.get((index, _raw_stream(index)))
+    if ws is None or ws.numel() < nbytes:
+        from . import _workspace
+        return _workspace(torch.device("cuda", index), nbytes)
+    return ws
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -39,43 +55,44 @@ def _cuda(name: str, t) -> None:
 
 
 def _floats(name: str, t) -> int:
-    _cuda(name, t)
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
     code = _DTYPES.get(t.dtype)
     if code is None:
         raise ValueError(f"{name} must be bfloat16 or float32")
     return code
 
 
-def _rows(t: torch.Tensor) -> torch.Tensor:
-    """t as [rows, last dimension] with unit stride in the last dimension (a copy only if it has none)."""
-    if t.dim() != 2:
-        t = t.reshape(-1, t.shape[-1])
-    if t.shape[1] > 1 and t.stride(1) != 1:
+def _rows(t: torch.Tensor):
+    """(t as [rows, last dimension], rows, row stride): unit stride in the last
+    dimension, rows that do not overlap; a copy only if t is not laid out so."""
+    H = t.shape[-1]
+    if t.is_contiguous():
+        return t, t.numel() // H, H
+    t = t.reshape(-1, H)
+    rows, ld = t.shape[0], t.stride(0)
+    if (H > 1 and t.stride(1) != 1) or (rows > 1 and ld < H):
         t = t.contiguous()
-    return t
+        ld = H
+    return t, rows, ld if rows > 1 else H
 
 
-def _ld(t: torch.Tensor) -> int:
-    """Row stride of a 2-D tensor; that of a single row is free, so torch may give any."""
-    return t.stride(0) if t.shape[0] > 1 and t.stride(0) >= t.shape[1] else t.shape[1]
-
-
-def _dense_rows(t: torch.Tensor) -> torch.Tensor:
-    """Rows that do not overlap (an expanded tensor is copied)."""
-    return t.contiguous() if t.shape[0] > 1 and t.stride(0) < t.shape[1] else t
+def _vector(name: str, t, n: int, index: int) -> None:
+    if t.dim() != 1 or t.numel() != n or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [H] tensor on x's device")
 
 
 # ---------------------------------------------------------------- norm
-def _norm_weights(x: torch.Tensor, weight, bias):
+def _norm_weights(H: int, index: int, weight, bias) -> int:
     code = _lib.FLCE_DTYPE_F32
-    for name, t in (("weight", weight), ("bias", bias)):
-        if t is None:
-            continue
-        code = _floats(name, t)
-        if t.shape != (x.shape[-1],) or t.device != x.device or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous [H] tensor on x's device")
-    if weight is not None and bias is not None and weight.dtype != bias.dtype:
-        raise ValueError("weight and bias must have one dtype")
+    if weight is not None:
+        code = _floats("weight", weight)
+        _vector("weight", weight, H, index)
+    if bias is not None:
+        code = _floats("bias", bias)
+        _vector("bias", bias, H, index)
+        if weight is not None and weight.dtype != bias.dtype:
+            raise ValueError("weight and bias must have one dtype")
     return code
 
 
@@ -89,15 +106,16 @@ def flce_layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias
     dtype = _floats("x", x)
     if x.dim() == 0 or x.shape[-1] == 0:
         raise ValueError("x must have a last dimension to normalise")
-    wcode = _norm_weights(x, weight, bias)
-    x2 = _dense_rows(_rows(x))
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    H, index = x.shape[-1], x.get_device()
+    wcode = _norm_weights(H, index, weight, bias)
+    x2, rows, ld = _rows(x)
+    y = torch.empty_like(x, memory_format=torch.contiguous_format)
     mean = rstd = None
     if return_stats:
         rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
         mean = None if rms else torch.empty_like(rstd)
-    _call(x.device, "flce_layer_norm", x2.data_ptr(), dtype, x2.shape[0], x2.shape[1], _ld(x2), _ptr(weight),
-          _ptr(bias), wcode, eps, int(rms), y.data_ptr(), _ptr(mean), _ptr(rstd))
+    _call(index, "flce_layer_norm", x2.data_ptr(), dtype, rows, H, ld, _ptr(weight), _ptr(bias), wcode, eps, int(rms),
+          y.data_ptr(), _ptr(mean), _ptr(rstd))
     return (y, mean, rstd) if return_stats else y
 
 
@@ -111,35 +129,37 @@ def flce_layer_norm_backward(grad_y: torch.Tensor, x: torch.Tensor, weight: Opti
     ACCUMULATED in place, as the fused head does with grad_W."""
     dtype = _floats("x", x)
     _cuda("grad_y", grad_y)
-    if grad_y.shape != x.shape or grad_y.dtype != x.dtype or grad_y.device != x.device:
+    index = x.get_device()
+    if grad_y.shape != x.shape or grad_y.dtype != x.dtype or grad_y.get_device() != index:
         raise ValueError("grad_y must have x's shape, dtype and device")
-    wcode = _norm_weights(x, weight, None)
     H = x.shape[-1]
-    for name, t in (("rstd", rstd), ("mean", None if rms else mean)):
-        if name == "mean" and rms:
-            continue
+    wcode = _norm_weights(H, index, weight, None)
+    for name, t in (("rstd", rstd), ("mean", rstd if rms else mean)):
         _cuda(name, t)
-        if t.dtype != torch.float32 or t.shape != x.shape[:-1] or not t.is_contiguous() or t.device != x.device:
+        if t.dtype != torch.float32 or t.shape != x.shape[:-1] or not t.is_contiguous() or t.get_device() != index:
             raise ValueError(f"{name} must be a contiguous fp32 tensor of x's leading shape on x's device")
     for name, t in (("grad_weight", grad_weight), ("grad_bias", grad_bias)):
         if t is not None and (t.dtype != torch.float32 or t.shape != (H,) or not t.is_contiguous() or t.device != x.device):
             raise ValueError(f"{name} must be a contiguous fp32 [H] tensor on x's device")
-    if (grad_weight is None) != (grad_bias is None) and need_grad_weight and need_grad_bias:
-        raise ValueError("give both grad_weight and grad_bias to accumulate into, or neither")
-    x2, g2 = _dense_rows(_rows(x)), _dense_rows(_rows(grad_y))
     accumulate = grad_weight is not None or grad_bias is not None
-    gx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_grad_x else None
+    if accumulate and need_grad_weight and need_grad_bias and (grad_weight is None or grad_bias is None):
+        raise ValueError("give both grad_weight and grad_bias to accumulate into, or neither")
+    x2, rows, ld = _rows(x)
+    g2, _, ld_g = _rows(grad_y)
+    gx = torch.empty_like(x, memory_format=torch.contiguous_format) if need_grad_x else None
     if need_grad_weight and grad_weight is None:
         grad_weight = torch.empty(H, dtype=torch.float32, device=x.device)
     if need_grad_bias and grad_bias is None:
         grad_bias = torch.empty(H, dtype=torch.float32, device=x.device)
     gw, gb = grad_weight if need_grad_weight else None, grad_bias if need_grad_bias else None
-    from . import _workspace
-    nbytes = _lib.lib().flce_layer_norm_workspace_size(x2.shape[0], H) if gw is not None or gb is not None else 0
-    ws = _workspace(x.device, nbytes) if nbytes else None
-    _call(x.device, "flce_layer_norm_backward", g2.data_ptr(), _ld(g2), x2.data_ptr(), _ld(x2), dtype, x2.shape[0], H,
-          _ptr(weight), wcode, None if rms else mean.data_ptr(), rstd.data_ptr(), int(rms), _ptr(gx), _ptr(gw),
-          _ptr(gb), int(accumulate), _ptr(ws), nbytes)
+    ws, nbytes = None, 0
+    if gw is not None or gb is not None:
+        with torch.cuda.device(index):
+            nbytes = _lib.lib().flce_layer_norm_workspace_size(rows, H)
+        ws = _space(index, nbytes)
+    _call(index, "flce_layer_norm_backward", g2.data_ptr(), ld_g, x2.data_ptr(), ld, dtype, rows, H, _ptr(weight), wcode,
+          None if rms else mean.data_ptr(), rstd.data_ptr(), int(rms), _ptr(gx), _ptr(gw), _ptr(gb), int(accumulate),
+          _ptr(ws), nbytes)
     return {"grad_x": gx, "grad_weight": gw, "grad_bias": gb}
 
 
@@ -195,6 +215,14 @@ class MicroscaleTensor:
             raise ValueError("scales must be a contiguous [ceil(rows / 128), ceil(cols / 128), 32, 4, 4] tensor")
         self.codes, self.scales, self.shape = codes, scales, (rows, cols)
 
+    @classmethod
+    def _empty(cls, rows: int, cols: int, device) -> "MicroscaleTensor":
+        q = cls.__new__(cls)
+        q.codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=device)
+        q.scales = torch.empty(((rows + 127) // 128, (cols + 127) // 128, 32, 4, 4), dtype=torch.uint8, device=device)
+        q.shape = (rows, cols)
+        return q
+
     @property
     def device(self):
         return self.codes.device
@@ -213,23 +241,24 @@ def flce_microscale_quantize(x: torch.Tensor) -> MicroscaleTensor:
     dtype = _floats("x", x)
     if x.dim() < 2 or x.shape[-1] == 0 or x.shape[-1] % 32:
         raise ValueError("x must be [..., K] with K a multiple of 32")
-    x2 = _dense_rows(_rows(x))
-    rows, cols = x2.shape
-    codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=x.device)
-    scales = torch.empty(((rows + 127) // 128, (cols + 127) // 128, 32, 4, 4), dtype=torch.uint8, device=x.device)
-    _call(x.device, "flce_microscale_quantize", x2.data_ptr(), dtype, rows, cols, _ld(x2), codes.data_ptr(),
-          scales.data_ptr())
-    return MicroscaleTensor(codes, scales)
+    x2, rows, ld = _rows(x)
+    cols = x.shape[-1]
+    q = MicroscaleTensor._empty(rows, cols, x.device)
+    _call(x.get_device(), "flce_microscale_quantize", x2.data_ptr(), dtype, rows, cols, ld, q.codes.data_ptr(),
+          q.scales.data_ptr())
+    return q
 
 
 def flce_microscale_dequantize(q: MicroscaleTensor, *, dtype: torch.dtype = torch.float32) -> torch.Tensor:
     """What a microscaled matrix stands for, [rows, cols] in bf16 or fp32 (exact
     in both but for bf16 values below its normal range)."""
-    if dtype not in _DTYPES:
+    code = _DTYPES.get(dtype)
+    if code is None:
         raise ValueError("dtype must be bfloat16 or float32")
-    out = torch.empty(q.shape, dtype=dtype, device=q.device)
-    _call(q.device, "flce_microscale_dequantize", q.codes.data_ptr(), q.scales.data_ptr(), q.shape[0], q.shape[1],
-          out.data_ptr(), _DTYPES[dtype])
+    rows, cols = q.shape
+    out = torch.empty((rows, cols), dtype=dtype, device=q.codes.device)
+    _call(out.get_device(), "flce_microscale_dequantize", q.codes.data_ptr(), q.scales.data_ptr(), rows, cols, out.data_ptr(),
+          code)
     return out
 
 
@@ -243,42 +272,40 @@ def flce_microscale_linear(h: Union[torch.Tensor, MicroscaleTensor], W: Microsca
     if not isinstance(W, MicroscaleTensor):
         raise ValueError("W must be a MicroscaleTensor")
     V, K = W.shape
-    from . import _workspace
+    index = W.codes.get_device()
     if isinstance(h, MicroscaleTensor):
-        if h.shape[1] != K or h.device != W.device:
+        if h.shape[1] != K or h.codes.get_device() != index:
             raise ValueError("h and W must have one K and one device")
         out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
         rows, lead = h.shape[0], (h.shape[0],)
     else:
         dtype = _floats("h", h)
-        if h.dim() == 0 or h.shape[-1] != K or h.device != W.device:
+        if h.dim() == 0 or h.shape[-1] != K or h.get_device() != index:
             raise ValueError("h must be [..., K] with W's K, on W's device")
         out_dtype = h.dtype if out_dtype is None else out_dtype
         lead = h.shape[:-1]
-        h2 = _dense_rows(_rows(h))
-        rows = h2.shape[0]
+        h2, rows, ld = _rows(h)
     code = _DTYPES.get(out_dtype)
     if code is None:
         raise ValueError("out_dtype must be bfloat16 or float32")
-    out = torch.empty((*lead, V), dtype=out_dtype, device=W.device)
+    out = torch.empty((*lead, V), dtype=out_dtype, device=W.codes.device)
     if isinstance(h, MicroscaleTensor):
-        ws = _workspace(W.device, 256)
-        _call(W.device, "flce_microscale_matmul", h.codes.data_ptr(), h.scales.data_ptr(), rows, W.codes.data_ptr(),
-              W.scales.data_ptr(), V, K, out_mult, softcap, out.data_ptr(), code, V, ws.data_ptr(), 256)
+        _call(index, "flce_microscale_matmul", h.codes.data_ptr(), h.scales.data_ptr(), rows, W.codes.data_ptr(),
+              W.scales.data_ptr(), V, K, out_mult, softcap, out.data_ptr(), code, V, _space(index, 256).data_ptr(), 256)
     else:
+        # (flce_microscale_workspace_size's sum)
         nbytes = 256 + (rows * (K // 2) + 255) // 256 * 256 + (rows + 127) // 128 * ((K + 127) // 128) * 512
-        ws = _workspace(W.device, nbytes)
-        _call(W.device, "flce_microscale_linear", h2.data_ptr(), dtype, _ld(h2), rows, W.codes.data_ptr(),
-              W.scales.data_ptr(), V, K, out_mult, softcap, out.data_ptr(), code, V, ws.data_ptr(), nbytes)
+        _call(index, "flce_microscale_linear", h2.data_ptr(), dtype, ld, rows, W.codes.data_ptr(), W.scales.data_ptr(), V, K,
+              out_mult, softcap, out.data_ptr(), code, V, _space(index, nbytes).data_ptr(), nbytes)
     return out
 
 
 # ---------------------------------------------------------------- sampling
-def _setting(name: str, v, dtype: torch.dtype, lead, device):
+def _setting(name: str, v, dtype: torch.dtype, lead, index: int):
     """(pointer or None, scalar) of a setting given as a number or as one value per row."""
     if not isinstance(v, torch.Tensor):
-        return None, (int(v) if dtype is torch.int32 else float(v))
-    if v.dtype != dtype or v.shape != lead or v.device != device or not v.is_contiguous():
+        return None, v
+    if v.dtype != dtype or v.shape != lead or v.get_device() != index or not v.is_contiguous():
         raise ValueError(f"{name} must be a number, or a contiguous {dtype} tensor with one value per row")
     return v.data_ptr(), 0
 
@@ -298,19 +325,19 @@ def flce_sample(logits: torch.Tensor, u: torch.Tensor, *, temperature=1.0, top_k
     code = _floats("logits", logits)
     if logits.dim() == 0 or logits.shape[-1] == 0:
         raise ValueError("logits must be [..., V]")
-    lead = logits.shape[:-1]
+    lead, V, index = logits.shape[:-1], logits.shape[-1], logits.get_device()
     _cuda("u", u)
-    if u.dtype != torch.float32 or u.shape != lead or u.device != logits.device or not u.is_contiguous():
+    if u.dtype != torch.float32 or u.shape != lead or u.get_device() != index or not u.is_contiguous():
         raise ValueError("u must be a contiguous fp32 tensor of the logits' leading shape, on their device")
-    x = _dense_rows(_rows(logits))
-    tp, t = _setting("temperature", temperature, torch.float32, lead, x.device)
-    kp, k = _setting("top_k", top_k, torch.int32, lead, x.device)
-    pp, p = _setting("top_p", top_p, torch.float32, lead, x.device)
-    mp, m = _setting("min_p", min_p, torch.float32, lead, x.device)
-    tokens = torch.empty(lead, dtype=torch.int64, device=x.device)
-    logprobs = torch.empty(lead, dtype=torch.float32, device=x.device) if return_logprobs else None
-    _call(x.device, "flce_sample", x.data_ptr(), code, x.shape[0], x.shape[1], _ld(x), u.data_ptr(), tp, t, kp, k, pp, p,
-          mp, m, tokens.data_ptr(), _ptr(logprobs))
+    x, rows, ld = _rows(logits)
+    tp, t = _setting("temperature", temperature, torch.float32, lead, index)
+    kp, k = _setting("top_k", top_k, torch.int32, lead, index)
+    pp, p = _setting("top_p", top_p, torch.float32, lead, index)
+    mp, m = _setting("min_p", min_p, torch.float32, lead, index)
+    tokens = torch.empty(lead, dtype=torch.int64, device=u.device)
+    logprobs = torch.empty_like(u) if return_logprobs else None
+    _call(index, "flce_sample", x.data_ptr(), code, rows, V, ld, u.data_ptr(), tp, t, kp, int(k), pp, p, mp, m,
+          tokens.data_ptr(), _ptr(logprobs))
     return tokens, logprobs
 
 

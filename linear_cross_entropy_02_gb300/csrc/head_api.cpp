@@ -86,7 +86,7 @@ extern "C" {
 int flce_layer_norm(const void* x, int dtype, int64_t rows, int64_t hidden, int64_t ld_x, const void* weight,
                     const void* bias, int weight_dtype, float eps, int rms, void* y, float* mean, float* rstd,
                     void* stream_handle) {
-  if (!dtype_ok(dtype) || !dtype_ok(weight_dtype) || rows < 0 || hidden <= 0 || hidden > kMaxHidden ||
+  if (!dtype_ok(dtype) || !dtype_ok(weight_dtype) || rows < 0 || rows > kMaxRows || hidden <= 0 || hidden > kMaxHidden ||
       ld_x < hidden || !(eps >= 0.f) || !std::isfinite(eps))
     return FLCE_ERR_ARG;
   if (rows == 0) return FLCE_OK;
@@ -123,7 +123,7 @@ int flce_layer_norm(const void* x, int dtype, int64_t rows, int64_t hidden, int6
 size_t flce_layer_norm_workspace_size(int64_t rows, int64_t hidden) {
   int sms = 0;
   if (rows < 0 || hidden <= 0 || hidden > kMaxHidden || device_check(&sms) != FLCE_OK) return 0;
-  const int64_t parts = norm_partial_rows(rows, sms);
+  const int64_t parts = norm_partial_rows(rows, hidden, sms);
   return kHeaderBytes + 2 * round256(sizeof(float) * static_cast<size_t>(parts > 0 ? parts : 1) * hidden);
 }
 
@@ -131,7 +131,7 @@ int flce_layer_norm_backward(const void* grad_y, int64_t ld_grad_y, const void* 
                              int64_t rows, int64_t hidden, const void* weight, int weight_dtype, const float* mean,
                              const float* rstd, int rms, void* grad_x, float* grad_weight, float* grad_bias,
                              int accumulate, void* workspace, size_t workspace_bytes, void* stream_handle) {
-  if (!dtype_ok(dtype) || !dtype_ok(weight_dtype) || rows < 0 || hidden <= 0 || hidden > kMaxHidden ||
+  if (!dtype_ok(dtype) || !dtype_ok(weight_dtype) || rows < 0 || rows > kMaxRows || hidden <= 0 || hidden > kMaxHidden ||
       ld_x < hidden || ld_grad_y < hidden)
     return FLCE_ERR_ARG;
   if (!grad_x && !grad_weight && !grad_bias) return FLCE_OK;
@@ -147,7 +147,7 @@ int flce_layer_norm_backward(const void* grad_y, int64_t ld_grad_y, const void* 
   const int rc = device_check(&sms);
   if (rc != FLCE_OK) return rc;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_handle);
-  const size_t half = round256(sizeof(float) * static_cast<size_t>(rows > 0 ? norm_partial_rows(rows, sms) : 1) * hidden);
+  const size_t half = round256(sizeof(float) * static_cast<size_t>(rows > 0 ? norm_partial_rows(rows, hidden, sms) : 1) * hidden);
   if (sums && workspace_bytes < kHeaderBytes + 2 * half) return FLCE_ERR_WORKSPACE;
   NormParams p = {};
   p.x = x;

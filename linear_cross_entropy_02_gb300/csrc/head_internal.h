@@ -38,7 +38,7 @@ struct NormParams {
   float* part_b;
 };
 // Most partial rows that launch_norm_bwd writes for a call on this device.
-int norm_partial_rows(int64_t rows, int sms);
+int norm_partial_rows(int64_t rows, int64_t hidden, int sms);
 cudaError_t launch_norm(const NormParams& p, int sms, cudaStream_t s);
 // Writes grad_x and the partial sums; *partials = rows of part_w / part_b written.
 cudaError_t launch_norm_bwd(const NormParams& p, int sms, int* partials, cudaStream_t s);

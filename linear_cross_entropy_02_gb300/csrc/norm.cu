@@ -1,18 +1,27 @@
 // Layer norm and RMS norm in front of the head, forward and backward.
 //
 // Both directions are bound by memory: the forward reads and writes N H
-// elements, the backward reads 2 N H and writes N H, with about ten operations
-// for each. A row stays on chip between the pass that takes its statistics and
-// the pass that uses them, so that HBM sees each element once:
-//   rows of up to 128 16-byte vectors   one warp per row, no block barrier
-//   longer rows                         one CTA per row, C vectors per thread
-//   rows beyond that (or 8192 unaligned elements)   three passes through the L2
-// A CTA keeps taking rows (grid = what the SMs hold at once): the next row's
-// vectors are on their way while the current row's sums go through the
-// barrier, and the backward adds up its columns of the weight's gradient in
-// registers over all its rows. Those per-CTA sums go to the workspace once and
-// a second kernel adds them in a fixed order; no atomics, so the gradient is
-// the same in every run.
+// elements, the backward reads 2 N H and writes N H. A row stays in registers
+// between the pass that takes its sums and the pass that uses them, so that HBM
+// sees each element once.
+//
+// Forward: a small CTA per row (128 threads where a row has at most eight
+// vectors for each), many of them on an SM and none of them staying for a second
+// row. On 32768 x 7168 bf16 that is 137 us (6.8 TB/s, a plain copy's rate);
+// persistent CTAs of 448 threads that load the next row ahead of time took 172
+// to 215, however many barriers were saved. Rows of up to 128 vectors take a
+// warp each, or a part of one, without any barrier.
+//
+// Backward: the weight's gradient is a sum over rows, so here a CTA stays: a
+// thread keeps its columns for all of its CTA's rows and adds their terms in
+// registers. The rows after the current one are copied ahead of time into a ring
+// of shared memory that each thread fills and reads for itself. What bounds it is
+// instructions as much as bytes: everything that an element needs is done in one
+// visit before the row's sums are known, and two operations are left for after
+// them. (Packed pairs, f32x2, were tried: the moves into register pairs cost
+// what the arithmetic saved, 27 to 33 instructions an element against 12 here.)
+// Per-CTA sums go to the workspace once and a second kernel adds them in a fixed
+// order; no atomics, so the gradient is the same in every run.
 //
 // The variance is the mean of the squared distances from the mean, from
 // registers, not mean(x^2) - mean^2, which cancels for rows with an offset. The
@@ -30,87 +39,94 @@ namespace flce {
 
 namespace {
 
-// Vectors per thread and threads per CTA of the three kinds of rows.
-// E = 8: bf16 vectors, E = 4: fp32 vectors, E = 1: elements.
-constexpr int cta_vecs(int E) { return E == 8 ? 2 : E == 4 ? 4 : 8; }
-constexpr int warp_vecs(int E) { return E == 8 ? 4 : 8; }
-constexpr int kWarpRowThreads = 256;  // eight rows per CTA
+constexpr int kMaxVecs = 8;           // vectors per thread of a forward row
+constexpr int kWarpRowThreads = 256;  // eight warps per CTA
 constexpr int kMaxThreads = 1024;
 
-// Sums of a and b over the CTA, in every thread. `slot` alternates between 0
-// and 1 from call to call: the barrier of the call between keeps a slot's
-// readers ahead of its next writers.
-__device__ __forceinline__ void block_sum2(float& a, float& b, float2* smem, int& slot) {
-  a = warp_sum(a);
-  b = warp_sum(b);
-  float2* s = smem + slot * 32;
+// Backward: vectors per thread of a CTA's row, and per lane of a warp's row.
+// E = 8: bf16 vectors, E = 4: fp32 vectors, E = 1: elements (rows off the vector boundary).
+constexpr int cta_vecs(int E) { return E == 8 ? 2 : E == 4 ? 4 : 8; }
+constexpr int warp_vecs(int E) { return E == 8 ? 4 : 8; }
+
+// Sums of two values (or only of the first) over the CTA, in every thread.
+// `slot` alternates between 0 and 1 from call to call: the barrier of the call
+// between keeps a slot's readers ahead of its next writers. After the barrier
+// every thread adds up the warps' sums itself: for up to 16 warps a few wide
+// reads are quicker than five more shuffles in a chain.
+struct BlockSums {
+  float4 v[2][2][8];  // [slot][which value][32 warps]
+};
+template <bool BOTH>
+__device__ __forceinline__ void block_sum(float& a, float& b, BlockSums& smem, int& slot) {
+  float4(&s)[2][8] = smem.v[slot];
   slot ^= 1;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (lane == 0) s[warp] = make_float2(a, b);
-  __syncthreads();
-  const int warps = blockDim.x >> 5;
-  const float2 v = lane < warps ? s[lane] : make_float2(0.f, 0.f);
-  a = warp_sum(v.x);
-  b = warp_sum(v.y);
-}
-
-template <bool WARP>
-__device__ __forceinline__ void row_sum2(float& a, float& b, float2* smem, int& slot) {
-  if (WARP) {
-    a = warp_sum(a);
-    b = warp_sum(b);
-  } else {
-    block_sum2(a, b, smem, slot);
-  }
-}
-
-template <typename T, int E, int C, bool WARP>
-__global__ void __launch_bounds__(WARP ? kWarpRowThreads : kMaxThreads) norm_kernel(const NormParams p) {
-  __shared__ float2 sums[64];
-  int slot = 0;
-  const int H = static_cast<int>(p.hidden);
-  const int vecs = H / E;
-  const int tpr = WARP ? 32 : blockDim.x;
-  const int t = WARP ? (threadIdx.x & 31) : threadIdx.x;
-  const int per = WARP ? kWarpRowThreads / 32 : 1;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * per;
-  const T* x = static_cast<const T*>(p.x);
-  T* y = static_cast<T*>(p.out);
-  const float inv_h = 1.f / static_cast<float>(H);
-  Raw<T, E> next[C];
-  int64_t row = static_cast<int64_t>(blockIdx.x) * per + (WARP ? threadIdx.x >> 5 : 0);
-  if (row < p.rows) {
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-      if (t + c * tpr < vecs) next[c] = load_raw<T, E>(x + row * p.ld_x + (t + c * tpr) * E);
-  }
-  for (; row < p.rows; row += step) {
-    Raw<T, E> cur[C];
-#pragma unroll
-    for (int c = 0; c < C; ++c) cur[c] = next[c];
-    if (row + step < p.rows) {
-#pragma unroll
-      for (int c = 0; c < C; ++c)
-        if (t + c * tpr < vecs) next[c] = load_raw<T, E>(x + (row + step) * p.ld_x + (t + c * tpr) * E);
-    }
-    float mean = 0.f, none = 0.f;
-    if (!p.rms) {
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        if (t + c * tpr < vecs) {
-          float v[E];
-          unpack<T, E>(cur[c], v);
-#pragma unroll
-          for (int e = 0; e < E; ++e) mean += v[e];
-        }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  a = warp_sum(a);
+  if (BOTH) b = warp_sum(b);
+  if (lane == 0) {
+    reinterpret_cast<float*>(s[0])[warp] = a;
+    if (BOTH) reinterpret_cast<float*>(s[1])[warp] = b;
+    // the rest of the last group of four
+    if (warp == warps - 1) {
+      for (int i = warps; i & 3; ++i) {
+        reinterpret_cast<float*>(s[0])[i] = 0.f;
+        if (BOTH) reinterpret_cast<float*>(s[1])[i] = 0.f;
       }
-      row_sum2<WARP>(mean, none, sums, slot);
-      mean *= inv_h;
     }
-    float sq = 0.f, rest = 0.f;
+  }
+  __syncthreads();
+  a = b = 0.f;
+  for (int i = 0; i * 4 < warps; ++i) {
+    const float4 v = s[0][i];
+    a += (v.x + v.y) + (v.z + v.w);
+    if (BOTH) {
+      const float4 w = s[1][i];
+      b += (w.x + w.y) + (w.z + w.w);
+    }
+  }
+}
+
+// Sum over groups of `lanes` (a power of two) lanes.
+__device__ __forceinline__ float group_sum(float v, int lanes) {
+  for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// ------------------------------------------------------------------ forward
+// A row held as C vectors per thread, `stride` apart: its statistics and y.
+// sum(a, b, Both() or One()) sums a (and b) over the row's threads; vecs is 0 in
+// threads without a row.
+struct Both {
+  static constexpr bool value = true;
+};
+struct One {
+  static constexpr bool value = false;
+};
+template <typename T, int E, int C, typename S>
+__device__ __forceinline__ void norm_row(const NormParams& p, const T* x, T* y, int64_t row, int t, int stride, int vecs,
+                                         S sum) {
+  Raw<T, E> cur[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+    if (t + c * stride < vecs) cur[c] = load_raw<T, E>(x + (t + c * stride) * E);
+  const float inv_h = 1.f / static_cast<float>(static_cast<int>(p.hidden));
+  float mean = 0.f, rest = 0.f, sq = 0.f;
+  if (!p.rms) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      if (t + c * tpr < vecs) {
+      if (t + c * stride < vecs) {
+        float v[E];
+        unpack<T, E>(cur[c], v);
+#pragma unroll
+        for (int e = 0; e < E; ++e) mean += v[e];
+      }
+    }
+    sum(mean, rest, One());
+    mean *= inv_h;
+    rest = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      if (t + c * stride < vecs) {
         float v[E];
         unpack<T, E>(cur[c], v);
 #pragma unroll
@@ -121,62 +137,98 @@ __global__ void __launch_bounds__(WARP ? kWarpRowThreads : kMaxThreads) norm_ker
         }
       }
     }
-    row_sum2<WARP>(sq, rest, sums, slot);
-    rest = p.rms ? 0.f : rest * inv_h;
-    const float rstd = 1.f / sqrtf(fmaxf(sq * inv_h - rest * rest, 0.f) + p.eps);
-    if (t == 0) {
-      if (p.mean && !p.rms) p.mean[row] = mean + rest;
-      if (p.rstd) p.rstd[row] = rstd;
-    }
+    sum(sq, rest, Both());
+    rest *= inv_h;
+  } else {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int i = (t + c * tpr) * E;
-      if (t + c * tpr < vecs) {
-        float v[E], w[E];
+      if (t + c * stride < vecs) {
+        float v[E];
         unpack<T, E>(cur[c], v);
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = (v[e] - mean - rest) * rstd;
-        if (p.weight) {
-          load_weight<E>(p.weight, p.w_f32 != 0, i, w);
-#pragma unroll
-          for (int e = 0; e < E; ++e) v[e] *= w[e];
-        }
-        if (p.bias) {
-          load_weight<E>(p.bias, p.w_f32 != 0, i, w);
-#pragma unroll
-          for (int e = 0; e < E; ++e) v[e] += w[e];
-        }
-        store_raw<T, E>(y + row * p.hidden + i, pack<T, E>(v));
+        for (int e = 0; e < E; ++e) sq += v[e] * v[e];
       }
     }
+    sum(sq, rest, One());
+    rest = 0.f;
   }
+  const float rstd = 1.f / sqrtf(fmaxf(sq * inv_h - rest * rest, 0.f) + p.eps);
+  if (t == 0 && vecs > 0) {
+    if (p.mean && !p.rms) p.mean[row] = mean + rest;
+    if (p.rstd) p.rstd[row] = rstd;
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int i = (t + c * stride) * E;
+    if (t + c * stride < vecs) {
+      float v[E], w[E];
+      unpack<T, E>(cur[c], v);
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = (v[e] - mean - rest) * rstd;
+      if (p.weight) {
+        load_weight<E>(p.weight, p.w_f32 != 0, i, w);
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] *= w[e];
+      }
+      if (p.bias) {
+        load_weight<E>(p.bias, p.w_f32 != 0, i, w);
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] += w[e];
+      }
+      store_raw<T, E>(y + i, pack<T, E>(v));
+    }
+  }
+}
+
+// A row per CTA.
+template <typename T, int E, int C>
+__global__ void __launch_bounds__(kMaxThreads) norm_cta_kernel(const NormParams p) {
+  __shared__ BlockSums sums;
+  int slot = 0;
+  const int64_t row = blockIdx.x;
+  norm_row<T, E, C>(p, static_cast<const T*>(p.x) + row * p.ld_x, static_cast<T*>(p.out) + row * p.hidden, row, threadIdx.x,
+                    blockDim.x, static_cast<int>(p.hidden) / E,
+                    [&](float& a, float& b, auto both) { block_sum<both.value>(a, b, sums, slot); });
+}
+
+// A row per group of `lanes` lanes (32, or fewer if the row has fewer vectors).
+template <typename T, int E, int C>
+__global__ void __launch_bounds__(kWarpRowThreads) norm_warp_kernel(const NormParams p, const int lanes) {
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kWarpRowThreads / lanes) + threadIdx.x / lanes;
+  const int vecs = row < p.rows ? static_cast<int>(p.hidden) / E : 0;
+  norm_row<T, E, C>(p, static_cast<const T*>(p.x) + row * p.ld_x, static_cast<T*>(p.out) + row * p.hidden, row,
+                    threadIdx.x & (lanes - 1), 32, vecs, [&](float& a, float& b, auto both) {
+                      a = group_sum(a, lanes);
+                      if (both.value) b = group_sum(b, lanes);
+                    });
 }
 
 // Rows that no register file holds: a CTA per row, which is read three times.
 template <typename T>
 __global__ void __launch_bounds__(kMaxThreads) norm_long_kernel(const NormParams p) {
-  __shared__ float2 sums[64];
+  __shared__ BlockSums sums;
   int slot = 0;
   const int H = static_cast<int>(p.hidden);
   const float inv_h = 1.f / static_cast<float>(H);
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
     const T* x = static_cast<const T*>(p.x) + row * p.ld_x;
     T* y = static_cast<T*>(p.out) + row * p.hidden;
-    float mean = 0.f, none = 0.f;
+    float mean = 0.f, rest = 0.f;
+    float s[2] = {0.f, 0.f};
     if (!p.rms) {
-      for (int i = threadIdx.x; i < H; i += blockDim.x) mean += to_float<T>(x[i]);
-      block_sum2(mean, none, sums, slot);
-      mean *= inv_h;
+      for (int i = threadIdx.x; i < H; i += blockDim.x) s[0] += to_float<T>(x[i]);
+      block_sum<true>(s[0], s[1], sums, slot);
+      mean = s[0] * inv_h;
     }
-    float sq = 0.f, rest = 0.f;
+    s[0] = s[1] = 0.f;
     for (int i = threadIdx.x; i < H; i += blockDim.x) {
       const float d = to_float<T>(x[i]) - mean;
-      rest += d;
-      sq += d * d;
+      s[0] += d * d;
+      s[1] += d;
     }
-    block_sum2(sq, rest, sums, slot);
-    rest = p.rms ? 0.f : rest * inv_h;
-    const float rstd = 1.f / sqrtf(fmaxf(sq * inv_h - rest * rest, 0.f) + p.eps);
+    block_sum<true>(s[0], s[1], sums, slot);
+    rest = p.rms ? 0.f : s[1] * inv_h;
+    const float rstd = 1.f / sqrtf(fmaxf(s[0] * inv_h - rest * rest, 0.f) + p.eps);
     if (threadIdx.x == 0) {
       if (p.mean && !p.rms) p.mean[row] = mean + rest;
       if (p.rstd) p.rstd[row] = rstd;
@@ -197,27 +249,56 @@ __global__ void __launch_bounds__(kMaxThreads) norm_long_kernel(const NormParams
 }
 
 // ------------------------------------------------------------------ backward
-// A ring of `stages` rows of x and grad_y in shared memory, filled by copies
-// that each thread issues for its own vectors and reads back itself: they keep
-// two rows beyond the current one in flight without holding registers and
-// without a barrier. Single bf16 elements are too small for such a copy and are
-// loaded directly (stages is not used).
-template <typename T, int E, int C, bool WARP, int NB>
-__global__ void __launch_bounds__(WARP ? kWarpRowThreads : kMaxThreads)
-    norm_bwd_kernel(const NormParams p, const int stages) {
-  constexpr bool RING = sizeof(T) * E >= 4;
+// One vector before its row's sums are known: with d = x - mean and
+// g = rstd grad_y w, adds grad_y xhat and grad_y to the columns' sums and g and
+// g d to the row's, and leaves d and g for after them.
+template <typename T, int E, int NB, bool RMS>
+__device__ __forceinline__ void bwd_visit(const Raw<T, E>& rx, const Raw<T, E>& rg, const NormParams& p, int i, float mean,
+                                          float rstd, float (&d)[E], float (&g)[E], float (&acc_w)[E], float (&acc_b)[E],
+                                          float& sg, float& sgd) {
+  unpack<T, E>(rx, d);
+  unpack<T, E>(rg, g);
+  float w[E];
+  if (p.weight) load_weight<E>(p.weight, p.w_f32 != 0, i, w);
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    if (!RMS) d[e] -= mean;
+    if (NB == 2) acc_b[e] += g[e];
+    g[e] *= rstd;
+    acc_w[e] += g[e] * d[e];
+    if (p.weight) g[e] *= w[e];
+    if (!RMS) sg += g[e];
+    sgd += g[e] * d[e];
+  }
+}
+
+// grad_x = g + c0 + c2 d, c0 = -mean(g), c2 = -rstd^2 mean(g d).
+template <typename T, int E, bool RMS>
+__device__ __forceinline__ Raw<T, E> bwd_out(const float (&d)[E], const float (&g)[E], float c0, float c2) {
+  float v[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) v[e] = d[e] * c2 + (RMS ? g[e] : g[e] + c0);
+  return pack<T, E>(v);
+}
+
+template <typename T, int E>
+constexpr bool kRing = sizeof(T) * E >= 4;  // the smallest asynchronous copy is of 4 bytes
+
+// A row per CTA at a time. The ring's vectors are private to the thread that
+// copies them, so it needs no barrier of its own. Single bf16 elements are
+// loaded a row ahead into registers instead. REGS: with 72 registers two CTAs
+// of up to 448 threads share an SM (a row of 7168 bf16 elements).
+template <typename T, int E, int C, int NB, int REGS, bool RMS>
+__global__ void __maxnreg__(REGS) norm_bwd_cta_kernel(const NormParams p, const int stages) {
+  constexpr bool RING = kRing<T, E>;
   extern __shared__ __align__(16) uint8_t dyn[];
-  __shared__ float2 sums[64];
+  __shared__ BlockSums sums;
   int slot = 0;
   Raw<T, E>* ring = reinterpret_cast<Raw<T, E>*>(dyn);
-  const int H = static_cast<int>(p.hidden);
-  const int vecs = H / E;
-  const int tpr = WARP ? 32 : blockDim.x;
-  const int t = WARP ? (threadIdx.x & 31) : threadIdx.x;
-  const int per = WARP ? kWarpRowThreads / 32 : 1;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * per;
-  const T* x = static_cast<const T*>(p.x);
-  const T* gy = static_cast<const T*>(p.gy);
+  const int H = static_cast<int>(p.hidden), vecs = H / E;
+  const int t = threadIdx.x, T_ = blockDim.x;
+  const T* x = static_cast<const T*>(p.x) + t * E;
+  const T* gy = static_cast<const T*>(p.gy) + t * E;
   T* gx = static_cast<T*>(p.out);
   const float inv_h = 1.f / static_cast<float>(H);
   float acc_w[C][E], acc_b[C][E];
@@ -226,127 +307,207 @@ __global__ void __launch_bounds__(WARP ? kWarpRowThreads : kMaxThreads)
 #pragma unroll
     for (int e = 0; e < E; ++e) acc_w[c][e] = acc_b[c][e] = 0.f;
 
-  auto at = [&](int stage, int which, int c) { return ((stage * 2 + which) * C + c) * blockDim.x + threadIdx.x; };
-  auto fetch = [&](int64_t r, int stage) {
-    if (RING && r < p.rows) {
+  Raw<T, E> next_x[C], next_g[C];
+  auto fetch = [&](int64_t row, int stage) {
+    if (row < p.rows) {
+      const T* xr = x + row * p.ld_x;
+      const T* gr = gy + row * p.ld_gy;
+      Raw<T, E>* to = ring + stage * 2 * C * T_ + t;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        if (t + c * tpr < vecs) {
-          copy_async<RING ? static_cast<int>(sizeof(T) * E) : 4>(&ring[at(stage, 0, c)],
-                                                                 x + r * p.ld_x + (t + c * tpr) * E);
-          copy_async<RING ? static_cast<int>(sizeof(T) * E) : 4>(&ring[at(stage, 1, c)],
-                                                                 gy + r * p.ld_gy + (t + c * tpr) * E);
+        if (t + c * T_ < vecs) {
+          if constexpr (RING) {
+            copy_async<sizeof(T) * E>(to + c * T_, xr + c * T_ * E);
+            copy_async<sizeof(T) * E>(to + (C + c) * T_, gr + c * T_ * E);
+          } else {
+            next_x[c] = load_raw<T, E>(xr + c * T_ * E);
+            next_g[c] = load_raw<T, E>(gr + c * T_ * E);
+          }
         }
       }
     }
-    if (RING) copies_commit();
+    if constexpr (RING) copies_commit();
   };
 
-  int64_t row = static_cast<int64_t>(blockIdx.x) * per + (WARP ? threadIdx.x >> 5 : 0);
-  for (int i = 0; i < stages - 1; ++i) fetch(row + i * step, i);
+  int64_t row = blockIdx.x;
+  for (int i = 0; i < stages - 1; ++i) fetch(row + static_cast<int64_t>(i) * gridDim.x, i);
+  float mean = !RMS && row < p.rows ? __ldg(p.mean + row) : 0.f, rstd = row < p.rows ? __ldg(p.rstd + row) : 0.f;
   int stage = 0, fill = stages - 1;
-  for (; row < p.rows; row += step) {
+  for (; row < p.rows; row += gridDim.x) {
     Raw<T, E> rx[C], rg[C];
-    const float mean = p.rms ? 0.f : __ldg(p.mean + row);
-    const float rstd = __ldg(p.rstd + row);
-    if (RING) {
-      fetch(row + (stages - 1) * step, fill);
-      if (stages == 3)
+    if constexpr (!RING) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        rx[c] = next_x[c];
+        rg[c] = next_g[c];
+      }
+    }
+    fetch(row + static_cast<int64_t>(stages - 1) * gridDim.x, fill);
+    // the next row's statistics are on their way too
+    const int64_t after = row + gridDim.x;
+    const float next_mean = !RMS && after < p.rows ? __ldg(p.mean + after) : 0.f;
+    const float next_rstd = after < p.rows ? __ldg(p.rstd + after) : 0.f;
+    if constexpr (RING) {
+      if (stages == 4)
+        copies_wait<3>();
+      else if (stages == 3)
         copies_wait<2>();
       else if (stages == 2)
         copies_wait<1>();
       else
         copies_wait<0>();
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        if (t + c * tpr < vecs) {
-          rx[c] = ring[at(stage, 0, c)];
-          rg[c] = ring[at(stage, 1, c)];
-        }
-      }
-      if (++stage == stages) stage = 0;
-      if (++fill == stages) fill = 0;
-    } else {
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        if (t + c * tpr < vecs) {
-          rx[c] = load_raw<T, E>(x + row * p.ld_x + (t + c * tpr) * E);
-          rg[c] = load_raw<T, E>(gy + row * p.ld_gy + (t + c * tpr) * E);
-        }
-      }
     }
-    float sg = 0.f, sgx = 0.f;
+    float d[C][E], g[C][E], sg = 0.f, sgd = 0.f;
+    const Raw<T, E>* from = ring + stage * 2 * C * T_ + t;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      if (t + c * tpr < vecs) {
-        float xv[E], gv[E], w[E];
-        unpack<T, E>(rx[c], xv);
-        unpack<T, E>(rg[c], gv);
-        if (p.weight) load_weight<E>(p.weight, p.w_f32 != 0, (t + c * tpr) * E, w);
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float xhat = (xv[e] - mean) * rstd;
-          const float g = p.weight ? gv[e] * w[e] : gv[e];
-          sg += g;
-          sgx += g * xhat;
-          acc_w[c][e] += gv[e] * xhat;
-          if (NB == 2) acc_b[c][e] += gv[e];
-        }
+      if (t + c * T_ < vecs) {
+        if constexpr (RING)
+          bwd_visit<T, E, NB, RMS>(from[c * T_], from[(C + c) * T_], p, (t + c * T_) * E, mean, rstd, d[c], g[c], acc_w[c], acc_b[c],
+                              sg, sgd);
+        else
+          bwd_visit<T, E, NB, RMS>(rx[c], rg[c], p, (t + c * T_) * E, mean, rstd, d[c], g[c], acc_w[c], acc_b[c], sg, sgd);
       }
     }
-    if (gx == nullptr) continue;  // uniform over the grid
-    row_sum2<WARP>(sg, sgx, sums, slot);
-    sg = p.rms ? 0.f : sg * inv_h;
-    sgx *= inv_h;
+    if (gx) {
+      block_sum<!RMS>(sgd, sg, sums, slot);
+      const float c0 = RMS ? 0.f : -sg * inv_h, c2 = -rstd * rstd * (sgd * inv_h);
+      T* o = gx + row * p.hidden + t * E;
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      if (t + c * tpr < vecs) {
-        float xv[E], gv[E], w[E];
-        unpack<T, E>(rx[c], xv);
-        unpack<T, E>(rg[c], gv);
-        if (p.weight) load_weight<E>(p.weight, p.w_f32 != 0, (t + c * tpr) * E, w);
+      for (int c = 0; c < C; ++c)
+        if (t + c * T_ < vecs) store_raw<T, E>(o + c * T_ * E, bwd_out<T, E, RMS>(d[c], g[c], c0, c2));
+    }
+    mean = next_mean;
+    rstd = next_rstd;
+    if (++stage == stages) stage = 0;
+    if (++fill == stages) fill = 0;
+  }
+  if constexpr (RING) copies_wait<0>();
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float xhat = (xv[e] - mean) * rstd;
-          const float g = p.weight ? gv[e] * w[e] : gv[e];
-          xv[e] = rstd * (g - sg - xhat * sgx);
-        }
-        store_raw<T, E>(gx + row * p.hidden + (t + c * tpr) * E, pack<T, E>(xv));
+  for (int c = 0; c < C; ++c) {
+    if (t + c * T_ < vecs) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int64_t at = blockIdx.x * p.hidden + (t + c * T_) * E + e;
+        if (p.part_w) p.part_w[at] = acc_w[c][e];
+        if (NB == 2 && p.part_b) p.part_b[at] = acc_b[c][e];
       }
     }
   }
-  if (RING) copies_wait<0>();
+}
 
-  // This CTA's sums of its columns. Eight warps with rows of their own add up
-  // through shared memory first, in the order of the warps.
+// Rows on groups of `lanes` lanes (32, or fewer if the row has fewer vectors),
+// each with a ring of its own; no barrier until the CTA's groups add up their
+// sums, in order.
+template <typename T, int E, int C, int NB, bool RMS>
+__global__ void __launch_bounds__(kWarpRowThreads)
+    norm_bwd_warp_kernel(const NormParams p, const int lanes, const int stages) {
+  constexpr bool RING = kRing<T, E>;
+  extern __shared__ __align__(16) uint8_t dyn[];
+  Raw<T, E>* ring = reinterpret_cast<Raw<T, E>*>(dyn) + threadIdx.x;
+  const int H = static_cast<int>(p.hidden), vecs = H / E;
+  const int t = threadIdx.x & (lanes - 1), group = threadIdx.x / lanes, groups = kWarpRowThreads / lanes;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+  const T* x = static_cast<const T*>(p.x) + t * E;
+  const T* gy = static_cast<const T*>(p.gy) + t * E;
+  T* gx = static_cast<T*>(p.out);
+  const float inv_h = 1.f / static_cast<float>(H);
+  float acc_w[C][E], acc_b[C][E];
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc_w[c][e] = acc_b[c][e] = 0.f;
+  Raw<T, E> next_x[C], next_g[C];
+  auto fetch = [&](int64_t row, int stage) {
+    if (row < p.rows) {
+      const T* xr = x + row * p.ld_x;
+      const T* gr = gy + row * p.ld_gy;
+      Raw<T, E>* to = ring + stage * 2 * C * kWarpRowThreads;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        if (t + c * 32 < vecs) {
+          if constexpr (RING) {
+            copy_async<sizeof(T) * E>(to + c * kWarpRowThreads, xr + c * 32 * E);
+            copy_async<sizeof(T) * E>(to + (C + c) * kWarpRowThreads, gr + c * 32 * E);
+          } else {
+            next_x[c] = load_raw<T, E>(xr + c * 32 * E);
+            next_g[c] = load_raw<T, E>(gr + c * 32 * E);
+          }
+        }
+      }
+    }
+    if constexpr (RING) copies_commit();
+  };
+  // whole warps go through the loop together: the groups' sums are shuffles of the warp
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * groups + (threadIdx.x >> 5) * (32 / lanes);
+  int64_t row = first + (threadIdx.x & 31) / lanes;
+  for (int i = 0; i < stages - 1; ++i) fetch(row + i * step, i);
+  float mean = !RMS && row < p.rows ? __ldg(p.mean + row) : 0.f, rstd = row < p.rows ? __ldg(p.rstd + row) : 0.f;
+  int stage = 0, fill = stages - 1;
+  for (int64_t base = first; base < p.rows; base += step, row += step) {
+    Raw<T, E> rx[C], rg[C];
+    if constexpr (!RING) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        rx[c] = next_x[c];
+        rg[c] = next_g[c];
+      }
+    }
+    fetch(row + (stages - 1) * step, fill);
+    const int64_t n = row + step;
+    const float next_mean = !RMS && n < p.rows ? __ldg(p.mean + n) : 0.f, next_rstd = n < p.rows ? __ldg(p.rstd + n) : 0.f;
+    if constexpr (RING) {
+      if (stages == 4)
+        copies_wait<3>();
+      else
+        copies_wait<2>();
+    }
+    const int here = row < p.rows ? vecs : 0;
+    float d[C][E], g[C][E], sg = 0.f, sgd = 0.f;
+    const Raw<T, E>* from = ring + stage * 2 * C * kWarpRowThreads;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      if (t + c * 32 < here) {
+        if constexpr (RING)
+          bwd_visit<T, E, NB, RMS>(from[c * kWarpRowThreads], from[(C + c) * kWarpRowThreads], p, (t + c * 32) * E, mean, rstd, d[c],
+                              g[c], acc_w[c], acc_b[c], sg, sgd);
+        else
+          bwd_visit<T, E, NB, RMS>(rx[c], rg[c], p, (t + c * 32) * E, mean, rstd, d[c], g[c], acc_w[c], acc_b[c], sg, sgd);
+      }
+    }
+    if (gx) {
+      if (!RMS) sg = group_sum(sg, lanes);
+      sgd = group_sum(sgd, lanes);
+      const float c0 = RMS ? 0.f : -sg * inv_h, c2 = -rstd * rstd * (sgd * inv_h);
+      T* o = gx + row * p.hidden + t * E;
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        if (t + c * 32 < here) store_raw<T, E>(o + c * 32 * E, bwd_out<T, E, RMS>(d[c], g[c], c0, c2));
+    }
+    mean = next_mean;
+    rstd = next_rstd;
+    if (++stage == stages) stage = 0;
+    if (++fill == stages) fill = 0;
+  }
+  if constexpr (RING) copies_wait<0>();
+  float* comb = reinterpret_cast<float*>(dyn);
 #pragma unroll
   for (int which = 0; which < NB; ++which) {
     float* part = which == 0 ? p.part_w : p.part_b;
     if (part == nullptr) continue;
-    part += static_cast<int64_t>(blockIdx.x) * p.hidden;
-    float* comb = reinterpret_cast<float*>(dyn);
-    if (WARP) __syncthreads();
+    __syncthreads();
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      if (t + c * tpr < vecs) {
+      if (t + c * 32 < vecs) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float v = which == 0 ? acc_w[c][e] : acc_b[c][e];
-          const int i = (t + c * tpr) * E + e;
-          if (WARP)
-            comb[(threadIdx.x >> 5) * H + i] = v;
-          else
-            part[i] = v;
-        }
+        for (int e = 0; e < E; ++e) comb[group * H + (t + c * 32) * E + e] = which == 0 ? acc_w[c][e] : acc_b[c][e];
       }
     }
-    if (WARP) {
-      __syncthreads();
-      for (int i = threadIdx.x; i < H; i += blockDim.x) {
-        float v = 0.f;
-        for (int w = 0; w < per; ++w) v += comb[w * H + i];
-        part[i] = v;
-      }
+    __syncthreads();
+    for (int i = threadIdx.x; i < H; i += kWarpRowThreads) {
+      float v = 0.f;
+      for (int g = 0; g < groups; ++g) v += comb[g * H + i];
+      part[blockIdx.x * p.hidden + i] = v;
     }
   }
 }
@@ -354,7 +515,7 @@ __global__ void __launch_bounds__(WARP ? kWarpRowThreads : kMaxThreads)
 // Long rows: grad_x by a CTA per row in two passes through the L2.
 template <typename T>
 __global__ void __launch_bounds__(kMaxThreads) norm_bwd_long_kernel(const NormParams p) {
-  __shared__ float2 sums[64];
+  __shared__ BlockSums sums;
   int slot = 0;
   const int H = static_cast<int>(p.hidden);
   const float inv_h = 1.f / static_cast<float>(H);
@@ -363,16 +524,15 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_long_kernel(const NormPa
     const T* gy = static_cast<const T*>(p.gy) + row * p.ld_gy;
     T* gx = static_cast<T*>(p.out) + row * p.hidden;
     const float mean = p.rms ? 0.f : p.mean[row], rstd = p.rstd[row];
-    float sg = 0.f, sgx = 0.f, w[1] = {1.f};
+    float s[2] = {0.f, 0.f}, w[1] = {1.f};
     for (int i = threadIdx.x; i < H; i += blockDim.x) {
       if (p.weight) load_weight<1>(p.weight, p.w_f32 != 0, i, w);
       const float g = to_float<T>(gy[i]) * w[0];
-      sg += g;
-      sgx += g * ((to_float<T>(x[i]) - mean) * rstd);
+      s[0] += g;
+      s[1] += g * ((to_float<T>(x[i]) - mean) * rstd);
     }
-    block_sum2(sg, sgx, sums, slot);
-    sg = p.rms ? 0.f : sg * inv_h;
-    sgx *= inv_h;
+    block_sum<true>(s[0], s[1], sums, slot);
+    const float sg = p.rms ? 0.f : s[0] * inv_h, sgx = s[1] * inv_h;
     for (int i = threadIdx.x; i < H; i += blockDim.x) {
       if (p.weight) load_weight<1>(p.weight, p.w_f32 != 0, i, w);
       const float g = to_float<T>(gy[i]) * w[0];
@@ -429,126 +589,149 @@ inline bool aligned(const void* p, int64_t ld, size_t es) {
   return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld * static_cast<int64_t>(es)) % 16 == 0);
 }
 
-enum RowKind { ROW_WARP, ROW_CTA, ROW_LONG };
-
-struct Shape {
-  bool vec;
-  int E;
-  RowKind kind;
-  int threads;  // of a ROW_CTA
-};
-
-Shape shape_of(const NormParams& p) {
+// Whether rows can be taken as 16-byte vectors.
+bool vectors(const NormParams& p) {
   const size_t es = p.dtype == FLCE_DTYPE_F32 ? 4 : 2;
-  Shape s;
-  s.vec = aligned(p.x, p.ld_x, es) && aligned(p.gy, p.ld_gy, es) && aligned(p.out, p.hidden, es) &&
-          p.hidden % (16 / es) == 0 && aligned(p.weight, 0, 1) && aligned(p.bias, 0, 1);
-  s.E = s.vec ? static_cast<int>(16 / es) : 1;
-  const int64_t vecs = p.hidden / s.E;
-  const int C = cta_vecs(s.E);
-  s.kind = vecs <= 32 * warp_vecs(s.E) ? ROW_WARP : vecs <= static_cast<int64_t>(kMaxThreads) * C ? ROW_CTA : ROW_LONG;
-  s.threads = static_cast<int>(((vecs + C - 1) / C + 31) / 32 * 32);
-  return s;
+  return aligned(p.x, p.ld_x, es) && aligned(p.gy, p.ld_gy, es) && aligned(p.out, p.hidden, es) &&
+         p.hidden % (16 / es) == 0 && aligned(p.weight, 0, 1) && aligned(p.bias, 0, 1);
 }
-
-constexpr size_t kRingBudget = 96 * 1024;  // two CTAs of an SM keep a ring each
 
 inline unsigned grid_of(int64_t want, int64_t most) { return static_cast<unsigned>(want < most ? want : most); }
 
-template <typename T, int E>
-cudaError_t run_fwd(const NormParams& p, const Shape& h, int sms, cudaStream_t s) {
-  if (h.kind == ROW_WARP) {
-    norm_kernel<T, E, warp_vecs(E), true><<<grid_of((p.rows + 7) / 8, 4LL * sms), kWarpRowThreads, 0, s>>>(p);
-  } else {
-    norm_kernel<T, E, cta_vecs(E), false>
-        <<<grid_of(p.rows, static_cast<int64_t>(sms) * (h.threads > 512 ? 1 : 1024 / h.threads)), h.threads, 0, s>>>(p);
+// Lanes for a row of `vecs` vectors: a power of two.
+inline int lanes_for(int64_t vecs) {
+  int l = 1;
+  while (l < vecs && l < 32) l *= 2;
+  return l;
+}
+
+// CTAs per SM of the backward: shorter rows take more of them, and each writes
+// one partial row, so that the partial sums stay within about a sixth of a
+// large batch's bytes.
+inline int bwd_ctas(int64_t hidden) {
+  const int64_t n = 16384 / hidden;
+  return n < 1 ? 1 : n > 8 ? 8 : static_cast<int>(n);
+}
+
+template <typename T, int E, int C>
+cudaError_t run_fwd_cta(const NormParams& p, int c, int threads, cudaStream_t s) {
+  if constexpr (C <= kMaxVecs) {
+    if (c > C) return run_fwd_cta<T, E, C + 1>(p, c, threads, s);
+    norm_cta_kernel<T, E, C><<<static_cast<unsigned>(p.rows), threads, 0, s>>>(p);
   }
   return cudaGetLastError();
 }
 
-template <typename T, int E, bool WARP, int NB>
-cudaError_t run_bwd_typed(const NormParams& p, int threads, int stages, size_t smem, int grid, cudaStream_t s) {
-  auto k = norm_bwd_kernel<T, E, WARP ? warp_vecs(E) : cta_vecs(E), WARP, NB>;
-  static std::atomic<uint64_t> done{0};
+template <typename T, int E>
+cudaError_t run_fwd(const NormParams& p, int sms, cudaStream_t s) {
+  const int64_t vecs = p.hidden / E;
+  if (vecs <= 32 * 4) {
+    const int lanes = lanes_for(vecs);
+    const int64_t per = kWarpRowThreads / lanes;
+    const unsigned grid = static_cast<unsigned>((p.rows + per - 1) / per);
+    if (vecs <= 32)
+      norm_warp_kernel<T, E, 1><<<grid, kWarpRowThreads, 0, s>>>(p, lanes);
+    else
+      norm_warp_kernel<T, E, 4><<<grid, kWarpRowThreads, 0, s>>>(p, lanes);
+    return cudaGetLastError();
+  }
+  if (vecs <= static_cast<int64_t>(kMaxThreads) * kMaxVecs) {
+    int most = 128;
+    while (most * kMaxVecs < vecs) most *= 2;
+    const int c = static_cast<int>((vecs + most - 1) / most);
+    const int threads = static_cast<int>(((vecs + c - 1) / c + 31) / 32 * 32);
+    return run_fwd_cta<T, E, 1>(p, c, threads, s);
+  }
+  norm_long_kernel<T><<<grid_of(p.rows, 2LL * sms), kMaxThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+constexpr size_t kMostShared = 220 * 1024;
+
+// Launches k with dynamic shared memory above the default limit.
+template <typename K, typename... A>
+cudaError_t launch_large(K k, std::atomic<uint64_t>& done, unsigned grid, int threads, size_t smem, cudaStream_t s, A... args) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
-  if (smem > 48 * 1024 && !(done.load() >> (dev & 63) & 1)) {
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+  if (smem > 40 * 1024 && !(done.load() >> (dev & 63) & 1)) {
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
     if (e != cudaSuccess) return e;
     done.fetch_or(1ull << (dev & 63));
   }
-  k<<<grid, threads, smem, s>>>(p, stages);
+  k<<<grid, threads, smem, s>>>(args...);
   return cudaGetLastError();
 }
 
+template <typename T, int E, int NB, bool RMS>
+cudaError_t run_bwd_row(const NormParams& p, int sms, int* partials, cudaStream_t s) {
+  const int64_t vecs = p.hidden / E;
+  if (vecs <= 32 * warp_vecs(E)) {
+    constexpr int C = warp_vecs(E);
+    const int lanes = lanes_for(vecs);
+    const int64_t groups = kWarpRowThreads / lanes;
+    // one vector per lane: three rows ahead are few registers and little shared memory
+    const int c = vecs <= 32 ? 1 : C, stages = !kRing<T, E> ? 2 : vecs <= 32 ? 4 : 3;
+    const size_t ring = kRing<T, E> ? static_cast<size_t>(kWarpRowThreads) * c * 2 * sizeof(Raw<T, E>) * stages : 0;
+    const size_t comb = static_cast<size_t>(groups) * p.hidden * sizeof(float);
+    const size_t smem = ring > comb ? ring : comb;
+    const unsigned grid = grid_of((p.rows + groups - 1) / groups, static_cast<int64_t>(sms) * (vecs <= 32 ? 4 : 2));
+    *partials = static_cast<int>(grid);
+    static std::atomic<uint64_t> done[2];
+    if (vecs <= 32)
+      return launch_large(norm_bwd_warp_kernel<T, E, 1, NB, RMS>, done[0], grid, kWarpRowThreads, smem, s, p, lanes, stages);
+    return launch_large(norm_bwd_warp_kernel<T, E, C, NB, RMS>, done[1], grid, kWarpRowThreads, smem, s, p, lanes, stages);
+  }
+  constexpr int C = cta_vecs(E);
+  const int threads = static_cast<int>(((vecs + C - 1) / C + 31) / 32 * 32);
+  const int regs = threads <= 448 ? 72 : 64;
+  int ctas = 65536 / (regs * threads);
+  if (ctas > bwd_ctas(p.hidden)) ctas = bwd_ctas(p.hidden);
+  const size_t row = kRing<T, E> ? static_cast<size_t>(threads) * C * 2 * sizeof(Raw<T, E>) : 0;
+  int stages = kRing<T, E> ? 3 : 2;
+  while (stages > 1 && row * stages * ctas > kMostShared) --stages;
+  const unsigned grid = grid_of(p.rows, static_cast<int64_t>(sms) * ctas);
+  *partials = static_cast<int>(grid);
+  static std::atomic<uint64_t> done[2];
+  if (regs == 72)
+    return launch_large(norm_bwd_cta_kernel<T, E, C, NB, 72, RMS>, done[0], grid, threads, row * stages, s, p, stages);
+  return launch_large(norm_bwd_cta_kernel<T, E, C, NB, 64, RMS>, done[1], grid, threads, row * stages, s, p, stages);
+}
+
 template <typename T, int E>
-cudaError_t run_bwd(const NormParams& p, const Shape& h, int sms, int* partials, cudaStream_t s) {
-  const bool warp = h.kind == ROW_WARP;
-  const int threads = warp ? kWarpRowThreads : h.threads;
-  const int C = warp ? warp_vecs(E) : cta_vecs(E);
-  const size_t stage = static_cast<size_t>(threads) * C * 2 * sizeof(Raw<T, E>);
-  int stages = static_cast<int>(kRingBudget / stage);
-  stages = stages > 3 ? 3 : stages < 1 ? 1 : stages;
-  size_t smem = stage * stages;
-  const size_t comb = warp ? static_cast<size_t>(p.hidden) * (kWarpRowThreads / 32) * sizeof(float) : 0;
-  if (comb > smem) smem = comb;
-  int grid;
-  if (warp)
-    grid = static_cast<int>(grid_of((p.rows + 7) / 8, 2LL * sms));
-  else
-    grid = static_cast<int>(grid_of(p.rows, static_cast<int64_t>(sms) * (h.threads > 512 ? 1 : 2)));
-  *partials = grid;
-  if (warp)
-    return p.part_b ? run_bwd_typed<T, E, true, 2>(p, threads, stages, smem, grid, s)
-                    : run_bwd_typed<T, E, true, 1>(p, threads, stages, smem, grid, s);
-  return p.part_b ? run_bwd_typed<T, E, false, 2>(p, threads, stages, smem, grid, s)
-                  : run_bwd_typed<T, E, false, 1>(p, threads, stages, smem, grid, s);
+cudaError_t run_bwd(const NormParams& p, int sms, int* partials, cudaStream_t s) {
+  if (p.hidden / E <= static_cast<int64_t>(kMaxThreads) * cta_vecs(E))
+    return p.part_b ? (p.rms ? run_bwd_row<T, E, 2, true>(p, sms, partials, s) : run_bwd_row<T, E, 2, false>(p, sms, partials, s))
+                    : (p.rms ? run_bwd_row<T, E, 1, true>(p, sms, partials, s) : run_bwd_row<T, E, 1, false>(p, sms, partials, s));
+  if (p.out) {
+    norm_bwd_long_kernel<T><<<grid_of(p.rows, 2LL * sms), kMaxThreads, 0, s>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  const int groups = norm_partial_rows(p.rows, p.hidden, sms);
+  const int64_t group = (p.rows + groups - 1) / groups;
+  *partials = static_cast<int>((p.rows + group - 1) / group);
+  if (!p.part_w && !p.part_b) return cudaSuccess;
+  const dim3 grid(static_cast<unsigned>((p.hidden + 255) / 256), static_cast<unsigned>(*partials));
+  norm_bwd_long_cols_kernel<T><<<grid, 256, 0, s>>>(p, group);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-int norm_partial_rows(int64_t rows, int sms) { return static_cast<int>(rows < 2LL * sms ? rows : 2LL * sms); }
+int norm_partial_rows(int64_t rows, int64_t hidden, int sms) {
+  const int64_t most = static_cast<int64_t>(sms) * bwd_ctas(hidden);
+  return static_cast<int>(rows < most ? rows : most);
+}
 
 cudaError_t launch_norm(const NormParams& p, int sms, cudaStream_t s) {
-  const Shape h = shape_of(p);
-  const bool f32 = p.dtype == FLCE_DTYPE_F32;
-  if (h.kind == ROW_LONG) {
-    const unsigned grid = grid_of(p.rows, 2LL * sms);
-    if (f32)
-      norm_long_kernel<float><<<grid, kMaxThreads, 0, s>>>(p);
-    else
-      norm_long_kernel<uint16_t><<<grid, kMaxThreads, 0, s>>>(p);
-    return cudaGetLastError();
-  }
-  if (f32) return h.vec ? run_fwd<float, 4>(p, h, sms, s) : run_fwd<float, 1>(p, h, sms, s);
-  return h.vec ? run_fwd<uint16_t, 8>(p, h, sms, s) : run_fwd<uint16_t, 1>(p, h, sms, s);
+  if (p.dtype == FLCE_DTYPE_F32) return vectors(p) ? run_fwd<float, 4>(p, sms, s) : run_fwd<float, 1>(p, sms, s);
+  return vectors(p) ? run_fwd<uint16_t, 8>(p, sms, s) : run_fwd<uint16_t, 1>(p, sms, s);
 }
 
 cudaError_t launch_norm_bwd(const NormParams& p, int sms, int* partials, cudaStream_t s) {
-  const Shape h = shape_of(p);
-  const bool f32 = p.dtype == FLCE_DTYPE_F32;
-  if (h.kind == ROW_LONG) {
-    if (p.out) {
-      const unsigned grid = grid_of(p.rows, 2LL * sms);
-      if (f32)
-        norm_bwd_long_kernel<float><<<grid, kMaxThreads, 0, s>>>(p);
-      else
-        norm_bwd_long_kernel<uint16_t><<<grid, kMaxThreads, 0, s>>>(p);
-      if (cudaGetLastError() != cudaSuccess) return cudaErrorLaunchFailure;
-    }
-    const int groups = norm_partial_rows(p.rows, sms);
-    const int64_t group = (p.rows + groups - 1) / groups;
-    *partials = static_cast<int>((p.rows + group - 1) / group);
-    if (!p.part_w && !p.part_b) return cudaSuccess;
-    const dim3 grid(static_cast<unsigned>((p.hidden + 255) / 256), static_cast<unsigned>(*partials));
-    if (f32)
-      norm_bwd_long_cols_kernel<float><<<grid, 256, 0, s>>>(p, group);
-    else
-      norm_bwd_long_cols_kernel<uint16_t><<<grid, 256, 0, s>>>(p, group);
-    return cudaGetLastError();
-  }
-  if (f32) return h.vec ? run_bwd<float, 4>(p, h, sms, partials, s) : run_bwd<float, 1>(p, h, sms, partials, s);
-  return h.vec ? run_bwd<uint16_t, 8>(p, h, sms, partials, s) : run_bwd<uint16_t, 1>(p, h, sms, partials, s);
+  if (p.dtype == FLCE_DTYPE_F32)
+    return vectors(p) ? run_bwd<float, 4>(p, sms, partials, s) : run_bwd<float, 1>(p, sms, partials, s);
+  return vectors(p) ? run_bwd<uint16_t, 8>(p, sms, partials, s) : run_bwd<uint16_t, 1>(p, sms, partials, s);
 }
 
 cudaError_t launch_norm_wgrad(const float* part_w, const float* part_b, int partials, int64_t hidden, float* grad_w,
