@@ -12,13 +12,21 @@
 //
 // K advances 256 elements (one 128-byte swizzle row of codes) per stage. Scales
 // come from HBM already in the order of tensor memory, 512 bytes per 128 rows x
-// 128 elements: one bulk copy per stage and operand, then tcgen05.cp spreads
-// each tile over four columns. An instruction covers K = 64 and picks its two
-// scale bytes of each column by the scale ids in its descriptor.
+// 128 elements, by one bulk copy per stage and operand. Four warps of their own
+// carry them on to tensor memory (every lane quarter needs a copy: each warp
+// writes its own). tcgen05.cp would do that in one instruction, but it waits for
+// the MMAs before it and they for it: with it a stage took 1080 cycles for one
+// token as for 192, and one token on 129280 x 7168 took 111 us instead of 83.
+// An instruction covers K = 64 and picks its two scale bytes of each column by
+// the scale ids in its descriptor.
 //
-// Warp 0 loads, warp 1 issues the MMAs, warps 2-5 store: two accumulators, so
-// that the stores of one tile run under the MMAs of the next. Every wait is
-// bounded (flce_device.cuh) and ends the call with FLCE_ERR_TIMEOUT.
+// For a few tokens A stays in shared memory, all of its K with its scales, if it
+// leaves room for the ring: re-reading it for every tile of W cost 10 us of 82.
+//
+// Warp 0 loads, warp 1 issues the MMAs, warps 2-5 store, warps 6-9 carry scales:
+// two accumulators, so that the stores of one tile run under the MMAs of the
+// next. Every wait is bounded (flce_device.cuh) and ends the call with
+// FLCE_ERR_TIMEOUT.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -38,25 +46,34 @@ constexpr int kStageK = 256;               // elements of K per stage
 constexpr int kRowBytes = 128;             // bytes of a row per stage
 constexpr int kWBytes = kTileV * kRowBytes;
 constexpr int kSfTiles = kStageK / kMxTileCols;  // scale tiles per 128 rows and stage
-constexpr int kThreads = 192;
+constexpr int kThreads = 320;
 constexpr int kSmemBudget = 226 * 1024;
 
-// Shared and tensor memory of a tile of NT tokens.
-template <int NT>
+// Shared and tensor memory of a tile of NT tokens. RESIDENT: A's codes and scales
+// stay in shared memory in front of the ring, which then holds W alone.
+template <int NT, bool RESIDENT>
 struct Plan {
   static constexpr int row_tiles = (NT + 127) / 128;  // 128-row scale tiles that the tokens can touch
   static constexpr int x_bytes = NT * kRowBytes;
   static constexpr int w_sf = kSfTiles * kMxTileBytes;
   static constexpr int x_sf = row_tiles * kSfTiles * kMxTileBytes;
-  static constexpr int stage = kWBytes + x_bytes + w_sf + x_sf;
+  static constexpr int x_all = x_bytes + x_sf;  // of one stage's K
+  static constexpr int stage = kWBytes + w_sf + (RESIDENT ? 0 : x_all);
   static constexpr int d_cols = NT < 32 ? 32 : NT;      // one accumulator
   static constexpr int sf_cols = 4 * kSfTiles * (1 + row_tiles);
-  static constexpr int by_smem = (kSmemBudget - 2048) / stage;
   static constexpr int by_tmem = (512 - 2 * d_cols) / sf_cols;
-  static constexpr int stages = by_smem < by_tmem ? (by_smem < 10 ? by_smem : 10) : (by_tmem < 10 ? by_tmem : 10);
-  static constexpr int used_cols = 2 * d_cols + stages * sf_cols;
+  static constexpr int most = by_tmem < 10 ? by_tmem : 10;
+  // Stages of the ring when k_iters stages' worth of A is resident (0: they do not fit).
+  static constexpr int stages(int k_iters) {
+    const int room = kSmemBudget - 2048 - (RESIDENT ? k_iters * x_all : 0);
+    const int n = room / stage;
+    return n > most ? most : n < 4 ? 0 : n;
+  }
+  static constexpr int smem(int k_iters) {
+    return stages(k_iters) * stage + (RESIDENT ? k_iters * x_all : 0) + 1024 + 512;
+  }
+  static constexpr int used_cols = 2 * d_cols + most * sf_cols;
   static constexpr int tmem_cols = used_cols <= 128 ? 128 : used_cols <= 256 ? 256 : 512;
-  static constexpr int smem = stages * stage + 1024 + 256;
   static_assert(x_bytes % 1024 == 0, "operand tiles start on a swizzle atom");
 };
 
@@ -65,7 +82,7 @@ struct MxArgs {
   const uint8_t* x_scales;
   int rows, vocab, k_iters, k_tiles, k_mmas;  // k_mmas: instructions over all of K
   int x_row_tiles;
-  int v_tiles, n_tiles;
+  int v_tiles, n_tiles, stages;
   float out_mult, softcap, inv_softcap;
   void* out;
   int64_t ld_out;
@@ -92,19 +109,15 @@ __device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uin
       : "memory");
 }
 
-// One scale tile (32 rows of 16 bytes) into four columns, in all four lane quarters.
-__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+// This lane's rows of two scale tiles (16 bytes each, in shared memory) into
+// eight columns of this warp's lane quarter.
+__device__ __forceinline__ void store_scales2(uint32_t tmem, const uint8_t* a, const uint8_t* b) {
+  const uint4 u = *reinterpret_cast<const uint4*>(a), v = *reinterpret_cast<const uint4*>(b);
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(tmem), "r"(u.x),
+               "r"(u.y), "r"(u.z), "r"(u.w), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
 }
-
-// Descriptor of a scale tile: no swizzle, eight-row groups 128 bytes apart.
-__device__ __forceinline__ uint64_t sdesc_scales(uint32_t smem_addr) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(128u >> 4) << 32;
-  d |= static_cast<uint64_t>(1u) << 46;
-  return d;
-}
+__device__ __forceinline__ void store_scales_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
@@ -113,24 +126,27 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
-template <int NT, typename T>
+template <int NT, bool RESIDENT, typename T>
 __global__ void __launch_bounds__(kThreads, 1)
     mx_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                    const MxArgs p) {
-  using P = Plan<NT>;
-  constexpr int S = P::stages;
+  using P = Plan<NT, RESIDENT>;
+  const int S = p.stages;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int x_slots = RESIDENT ? p.k_iters : S;  // A's slices: all of them, or one per stage
   uint8_t* s_w = smem;
   uint8_t* s_x = s_w + S * kWBytes;
-  uint8_t* s_wsf = s_x + S * P::x_bytes;
+  uint8_t* s_wsf = s_x + x_slots * P::x_bytes;
   uint8_t* s_xsf = s_wsf + S * P::w_sf;
-  uint64_t* full = reinterpret_cast<uint64_t*>(s_xsf + S * P::x_sf);
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_xsf + x_slots * P::x_sf);
   uint64_t* empty = full + S;
-  uint64_t* tfull = empty + S;
+  uint64_t* scaled = empty + S;  // the stage's scales are in tensor memory
+  uint64_t* tfull = scaled + S;
   uint64_t* tempty = tfull + 2;
   uint64_t* mma_done = tempty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+  uint64_t* x_full = mma_done + 1;  // RESIDENT: all of A has arrived
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(x_full + 1);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -138,12 +154,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < S; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
+      mbar_init(&scaled[s], 4);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
       mbar_init(&tempty[b], 128);
     }
     mbar_init(mma_done, 1);
+    mbar_init(x_full, 1);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&map_w);
@@ -165,6 +183,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       int stage = 0, issued = 0;
       uint32_t phase = 0;
       bool aborted = false;
+      if (RESIDENT) {  // one tile of tokens, whose scales are one row of tiles
+        mbar_arrive_expect_tx(x_full, p.k_iters * P::x_bytes + p.k_tiles * kMxTileBytes);
+        for (int k = 0; k < p.k_iters; ++k)
+          tma_load_2d(s_x + k * P::x_bytes, &map_x, x_full, k * kRowBytes, 0);
+        bulk_load(s_xsf, p.x_scales, static_cast<uint32_t>(p.k_tiles) * kMxTileBytes, x_full);
+      }
       for (int t = blockIdx.x; t < total && !aborted; t += gridDim.x) {
         const int vb = t / p.n_tiles, nb = t - vb * p.n_tiles;  // a tile of W meets all tokens while it is in the L2
         const int xt0 = nb * NT / 128;
@@ -176,14 +200,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const int kt = k * kSfTiles;
           const uint32_t sf = static_cast<uint32_t>(min(kSfTiles, p.k_tiles - kt)) * kMxTileBytes;
-          mbar_arrive_expect_tx(&full[stage], kWBytes + P::x_bytes + sf * (1 + xts));
+          mbar_arrive_expect_tx(&full[stage], kWBytes + sf + (RESIDENT ? 0 : P::x_bytes + sf * xts));
           tma_load_2d(s_w + stage * kWBytes, &map_w, &full[stage], k * kRowBytes, vb * kTileV);
-          tma_load_2d(s_x + stage * P::x_bytes, &map_x, &full[stage], k * kRowBytes, nb * NT);
           bulk_load(s_wsf + stage * P::w_sf, p.w_scales + (static_cast<int64_t>(vb) * p.k_tiles + kt) * kMxTileBytes,
                     sf, &full[stage]);
-          for (int i = 0; i < xts; ++i)
-            bulk_load(s_xsf + stage * P::x_sf + i * kSfTiles * kMxTileBytes,
-                      p.x_scales + (static_cast<int64_t>(xt0 + i) * p.k_tiles + kt) * kMxTileBytes, sf, &full[stage]);
+          if (!RESIDENT) {
+            tma_load_2d(s_x + stage * P::x_bytes, &map_x, &full[stage], k * kRowBytes, nb * NT);
+            for (int i = 0; i < xts; ++i)
+              bulk_load(s_xsf + stage * P::x_sf + i * kSfTiles * kMxTileBytes,
+                        p.x_scales + (static_cast<int64_t>(xt0 + i) * p.k_tiles + kt) * kMxTileBytes, sf, &full[stage]);
+          }
           ++issued;
           if (++stage == S) {
             stage = 0;
@@ -191,6 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
+      if (RESIDENT && aborted) wait_drain(x_full, 0, p.timeout_ns, p.status);
       if (aborted) {
         // loads that may still be in flight land before the shared memory goes away
         const int n = issued < S ? issued : S;
@@ -212,7 +239,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool aborted = false;
-      const uint32_t w0 = smem_u32(s_w), x0 = smem_u32(s_x), wsf0 = smem_u32(s_wsf), xsf0 = smem_u32(s_xsf);
+      const uint32_t w0 = smem_u32(s_w), x0 = smem_u32(s_x);
+      if (RESIDENT) aborted = !wait_bounded(x_full, 0, wc);
       for (int t = blockIdx.x; t < total && !aborted; t += gridDim.x) {
         const int nb = t % p.n_tiles;
         const uint32_t x_shift = static_cast<uint32_t>(nb * NT % 128 / 32);  // first 32-row group of the tokens
@@ -220,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after_sync();
         const uint32_t d = tmem + static_cast<uint32_t>(acc * P::d_cols);
         for (int k = 0; k < p.k_iters; ++k) {
-          if (!wait_bounded(&full[stage], phase, wc)) {
+          if (!wait_bounded(&full[stage], phase, wc) || !wait_bounded(&scaled[stage], phase, wc)) {
             aborted = true;
             break;
           }
@@ -228,16 +256,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t sf = tmem + static_cast<uint32_t>(2 * P::d_cols + stage * P::sf_cols);
           const uint32_t sfx = sf + 4 * kSfTiles;
           const int mmas = min(kStageK / 64, p.k_mmas - k * (kStageK / 64));
-          for (int j = 0; j * 2 < mmas; ++j) {
-            copy_scales(sf + 4 * j, sdesc_scales(wsf0 + stage * P::w_sf + j * kMxTileBytes));
-#pragma unroll
-            for (int i = 0; i < P::row_tiles; ++i)
-              copy_scales(sfx + 4 * (j * P::row_tiles + i),
-                          sdesc_scales(xsf0 + stage * P::x_sf + (i * kSfTiles + j) * kMxTileBytes));
-          }
           for (int j = 0; j < mmas; ++j) {
             const uint64_t a = sdesc_kmajor_sw128(w0 + stage * kWBytes + j * 32);
-            const uint64_t b = sdesc_kmajor_sw128(x0 + stage * P::x_bytes + j * 32);
+            const uint64_t b = sdesc_kmajor_sw128(x0 + (RESIDENT ? k : stage) * P::x_bytes + j * 32);
             mma_mxf4(d, a, b, (j & 1) ? idesc_mxf4(kTileV, NT, 2) : idesc_mxf4(kTileV, NT, 0), sf + 4 * (j >> 1),
                      sfx + 4 * (j >> 1) * P::row_tiles + x_shift, (k | j) != 0 ? 1u : 0u);
           }
@@ -254,6 +275,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_commit(mma_done);
       wait_drain(mma_done, 0, p.timeout_ns, p.status);
+    }
+  } else if (warp >= 6) {
+    // Scales of a stage whose copies have landed: its last MMAs are done, since the
+    // loader waited for them, so its columns are free.
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = !RESIDENT || wait_bounded(x_full, 0, wc);
+    for (int t = blockIdx.x; t < total && __all_sync(0xffffffffu, ok); t += gridDim.x) {
+      for (int k = 0; k < p.k_iters; ++k) {
+        ok = wait_bounded(&full[stage], phase, wc);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after_sync();
+        const uint32_t sf = t_lane + static_cast<uint32_t>(2 * P::d_cols + stage * P::sf_cols);
+        const uint8_t* w = s_wsf + stage * P::w_sf + lane * 16;
+        // (a last stage of one tile carries the stage before's bytes in the other's place: not used)
+        store_scales2(sf, w, w + kMxTileBytes);
+        const uint8_t* x = s_xsf + (RESIDENT ? k : stage) * P::x_sf + lane * 16;
+        if (P::row_tiles == 1) {
+          store_scales2(sf + 8, x, x + kMxTileBytes);
+        } else {
+          // columns by K-tile, rows in order within one
+          store_scales2(sf + 8, x, x + 2 * kMxTileBytes);
+          store_scales2(sf + 16, x + kMxTileBytes, x + 3 * kMxTileBytes);
+        }
+        store_scales_wait();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&scaled[stage]);
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
     }
   } else {
     const int quarter = warp & 3;
@@ -307,15 +362,15 @@ bool encode_codes(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, 
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int NT, typename T>
+template <int NT, bool RESIDENT, typename T>
 int run_tile(const MxGemmParams& p, int sms, cudaStream_t stream) {
-  using P = Plan<NT>;
-  auto kernel = mx_gemm_kernel<NT, T>;
+  using P = Plan<NT, RESIDENT>;
+  auto kernel = mx_gemm_kernel<NT, RESIDENT, T>;
   static std::atomic<uint64_t> done{0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return FLCE_ERR_CUDA;
   if (!(done.load() >> dev & 1)) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, P::smem) != cudaSuccess)
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget) != cudaSuccess)
       return FLCE_ERR_CUDA;
     done.fetch_or(1ull << dev);
   }
@@ -328,6 +383,7 @@ int run_tile(const MxGemmParams& p, int sms, cudaStream_t stream) {
   a.rows = static_cast<int>(p.rows);
   a.vocab = static_cast<int>(p.vocab);
   a.k_iters = static_cast<int>((p.cols + kStageK - 1) / kStageK);
+  a.stages = P::stages(a.k_iters);
   a.k_tiles = static_cast<int>((p.cols + kMxTileCols - 1) / kMxTileCols);
   a.k_mmas = static_cast<int>((p.cols + 63) / 64);
   a.x_row_tiles = static_cast<int>((p.rows + 127) / 128);
@@ -343,17 +399,25 @@ int run_tile(const MxGemmParams& p, int sms, cudaStream_t stream) {
   const int64_t total = static_cast<int64_t>(a.v_tiles) * a.n_tiles;
   if (total >= (1LL << 31)) return FLCE_ERR_ARG;
   const int grid = static_cast<int>(total < sms ? total : sms);
-  FLCE_LAUNCH(K_MX_GEMM, (kernel<<<grid, kThreads, P::smem, stream>>>(map_w, map_x, a), cudaGetLastError()));
+  FLCE_LAUNCH(K_MX_GEMM, (kernel<<<grid, kThreads, P::smem(a.k_iters), stream>>>(map_w, map_x, a), cudaGetLastError()));
   return FLCE_OK;
+}
+
+// One tile of tokens, with A resident if it fits beside a ring of four stages.
+template <int NT, typename T>
+int run_few(const MxGemmParams& p, int sms, cudaStream_t s) {
+  const int k_iters = static_cast<int>((p.cols + kStageK - 1) / kStageK);
+  if (Plan<NT, true>::stages(k_iters) > 0) return run_tile<NT, true, T>(p, sms, s);
+  return run_tile<NT, false, T>(p, sms, s);
 }
 
 template <typename T>
 int run_typed(const MxGemmParams& p, int sms, cudaStream_t s) {
-  if (p.rows <= 16) return run_tile<16, T>(p, sms, s);
-  if (p.rows <= 32) return run_tile<32, T>(p, sms, s);
-  if (p.rows <= 64) return run_tile<64, T>(p, sms, s);
-  if (p.rows <= 128) return run_tile<128, T>(p, sms, s);
-  return run_tile<192, T>(p, sms, s);
+  if (p.rows <= 16) return run_few<16, T>(p, sms, s);
+  if (p.rows <= 32) return run_few<32, T>(p, sms, s);
+  if (p.rows <= 64) return run_few<64, T>(p, sms, s);
+  if (p.rows <= 128) return run_few<128, T>(p, sms, s);
+  return run_tile<192, false, T>(p, sms, s);
 }
 
 }  // namespace
