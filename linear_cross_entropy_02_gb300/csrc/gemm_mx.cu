@@ -119,6 +119,20 @@ __device__ __forceinline__ void store_scales2(uint32_t tmem, const uint8_t* a, c
 }
 __device__ __forceinline__ void store_scales_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// True in one lane of a converged warp. Loader and MMA warps run their loops as
+// whole warps and issue from the elected lane: in code that a single lane runs,
+// the compiler has to move every operand of an MMA or copy to uniform registers
+// anew, and a stage of four MMAs took 1000 cycles instead of 400.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
+}
+// wait_bounded by a whole warp, which then agrees on the outcome.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtx& w) {
+  return __all_sync(0xffffffffu, wait_bounded(bar, parity, w));
+}
+
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                    smem_u32(dst)),
@@ -179,25 +193,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int total = p.v_tiles * p.n_tiles;
 
   if (warp == 0) {
-    if (lane == 0) {
-      int stage = 0, issued = 0;
-      uint32_t phase = 0;
-      bool aborted = false;
-      if (RESIDENT) {  // one tile of tokens, whose scales are one row of tiles
-        mbar_arrive_expect_tx(x_full, p.k_iters * P::x_bytes + p.k_tiles * kMxTileBytes);
-        for (int k = 0; k < p.k_iters; ++k)
-          tma_load_2d(s_x + k * P::x_bytes, &map_x, x_full, k * kRowBytes, 0);
-        bulk_load(s_xsf, p.x_scales, static_cast<uint32_t>(p.k_tiles) * kMxTileBytes, x_full);
-      }
-      for (int t = blockIdx.x; t < total && !aborted; t += gridDim.x) {
-        const int vb = t / p.n_tiles, nb = t - vb * p.n_tiles;  // a tile of W meets all tokens while it is in the L2
-        const int xt0 = nb * NT / 128;
-        const int xts = min(P::row_tiles, p.x_row_tiles - xt0);
-        for (int k = 0; k < p.k_iters; ++k) {
-          if (!wait_bounded(&empty[stage], phase ^ 1u, wc)) {
-            aborted = true;
-            break;
-          }
+    int stage = 0, issued = 0;
+    uint32_t phase = 0;
+    bool aborted = false;
+    if (RESIDENT && elect_one()) {  // one tile of tokens, whose scales are one row of tiles
+      mbar_arrive_expect_tx(x_full, p.k_iters * P::x_bytes + p.k_tiles * kMxTileBytes);
+      for (int k = 0; k < p.k_iters; ++k) tma_load_2d(s_x + k * P::x_bytes, &map_x, x_full, k * kRowBytes, 0);
+      bulk_load(s_xsf, p.x_scales, static_cast<uint32_t>(p.k_tiles) * kMxTileBytes, x_full);
+    }
+    __syncwarp();
+    for (int t = blockIdx.x; t < total && !aborted; t += gridDim.x) {
+      const int vb = t / p.n_tiles, nb = t - vb * p.n_tiles;  // a tile of W meets all tokens while it is in the L2
+      const int xt0 = nb * NT / 128;
+      const int xts = min(P::row_tiles, p.x_row_tiles - xt0);
+      for (int k = 0; k < p.k_iters; ++k) {
+        if (!warp_wait(&empty[stage], phase ^ 1u, wc)) {
+          aborted = true;
+          break;
+        }
+        if (elect_one()) {
           const int kt = k * kSfTiles;
           const uint32_t sf = static_cast<uint32_t>(min(kSfTiles, p.k_tiles - kt)) * kMxTileBytes;
           mbar_arrive_expect_tx(&full[stage], kWBytes + sf + (RESIDENT ? 0 : P::x_bytes + sf * xts));
@@ -210,72 +224,76 @@ __global__ void __launch_bounds__(kThreads, 1)
               bulk_load(s_xsf + stage * P::x_sf + i * kSfTiles * kMxTileBytes,
                         p.x_scales + (static_cast<int64_t>(xt0 + i) * p.k_tiles + kt) * kMxTileBytes, sf, &full[stage]);
           }
-          ++issued;
-          if (++stage == S) {
-            stage = 0;
-            phase ^= 1u;
-          }
+        }
+        __syncwarp();
+        ++issued;
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      if (RESIDENT && aborted) wait_drain(x_full, 0, p.timeout_ns, p.status);
-      if (aborted) {
-        // loads that may still be in flight land before the shared memory goes away
-        const int n = issued < S ? issued : S;
-        int s = stage;
-        uint32_t ph = phase;
-        for (int i = 0; i < n; ++i) {
-          if (s == 0) {
-            s = S - 1;
-            ph ^= 1u;
-          } else {
-            --s;
-          }
-          wait_drain(&full[s], ph, p.timeout_ns, p.status);
+    }
+    if (aborted && lane == 0) {
+      // loads that may still be in flight land before the shared memory goes away
+      if (RESIDENT) wait_drain(x_full, 0, p.timeout_ns, p.status);
+      const int n = issued < S ? issued : S;
+      int s = stage;
+      uint32_t ph = phase;
+      for (int i = 0; i < n; ++i) {
+        if (s == 0) {
+          s = S - 1;
+          ph ^= 1u;
+        } else {
+          --s;
         }
+        wait_drain(&full[s], ph, p.timeout_ns, p.status);
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      int stage = 0, acc = 0;
-      uint32_t phase = 0, acc_phase = 0;
-      bool aborted = false;
-      const uint32_t w0 = smem_u32(s_w), x0 = smem_u32(s_x);
-      if (RESIDENT) aborted = !wait_bounded(x_full, 0, wc);
-      for (int t = blockIdx.x; t < total && !aborted; t += gridDim.x) {
-        const int nb = t % p.n_tiles;
-        const uint32_t x_shift = static_cast<uint32_t>(nb * NT % 128 / 32);  // first 32-row group of the tokens
-        if (!wait_bounded(&tempty[acc], acc_phase ^ 1u, wc)) break;
-        tc_fence_after_sync();
-        const uint32_t d = tmem + static_cast<uint32_t>(acc * P::d_cols);
-        for (int k = 0; k < p.k_iters; ++k) {
-          if (!wait_bounded(&full[stage], phase, wc) || !wait_bounded(&scaled[stage], phase, wc)) {
-            aborted = true;
-            break;
-          }
-          tc_fence_after_sync();
-          const uint32_t sf = tmem + static_cast<uint32_t>(2 * P::d_cols + stage * P::sf_cols);
-          const uint32_t sfx = sf + 4 * kSfTiles;
-          const int mmas = min(kStageK / 64, p.k_mmas - k * (kStageK / 64));
-          for (int j = 0; j < mmas; ++j) {
-            const uint64_t a = sdesc_kmajor_sw128(w0 + stage * kWBytes + j * 32);
-            const uint64_t b = sdesc_kmajor_sw128(x0 + (RESIDENT ? k : stage) * P::x_bytes + j * 32);
-            mma_mxf4(d, a, b, (j & 1) ? idesc_mxf4(kTileV, NT, 2) : idesc_mxf4(kTileV, NT, 0), sf + 4 * (j >> 1),
-                     sfx + 4 * (j >> 1) * P::row_tiles + x_shift, (k | j) != 0 ? 1u : 0u);
-          }
-          tc_commit(&empty[stage]);
-          if (++stage == S) {
-            stage = 0;
-            phase ^= 1u;
-          }
+    int stage = 0, acc = 0;
+    uint32_t phase = 0, acc_phase = 0;
+    const uint32_t w0 = smem_u32(s_w), x0 = smem_u32(s_x);
+    bool aborted = RESIDENT && !warp_wait(x_full, 0, wc);
+    for (int t = blockIdx.x; t < total && !aborted; t += gridDim.x) {
+      const int nb = t % p.n_tiles;
+      const uint32_t x_shift = static_cast<uint32_t>(nb * NT % 128 / 32);  // first 32-row group of the tokens
+      if (!warp_wait(&tempty[acc], acc_phase ^ 1u, wc)) break;
+      tc_fence_after_sync();
+      const uint32_t d = tmem + static_cast<uint32_t>(acc * P::d_cols);
+      for (int k = 0; k < p.k_iters; ++k) {
+        if (!warp_wait(&full[stage], phase, wc) || !warp_wait(&scaled[stage], phase, wc)) {
+          aborted = true;
+          break;
         }
-        if (aborted) break;
-        tc_commit(&tfull[acc]);
-        acc ^= 1;
-        if (acc == 0) acc_phase ^= 1u;
+        tc_fence_after_sync();
+        if (elect_one()) {
+          const uint32_t sf = tmem + static_cast<uint32_t>(2 * P::d_cols + stage * P::sf_cols);
+          const uint32_t sfx = sf + 4 * kSfTiles + x_shift;
+          const uint32_t a0 = w0 + stage * kWBytes, b0 = x0 + (RESIDENT ? k : stage) * P::x_bytes;
+          const int mmas = p.k_mmas - k * (kStageK / 64);
+#pragma unroll
+          for (int j = 0; j < kStageK / 64; ++j)
+            if (j < mmas)
+              mma_mxf4(d, sdesc_kmajor_sw128(a0 + j * 32), sdesc_kmajor_sw128(b0 + j * 32),
+                       idesc_mxf4(kTileV, NT, (j & 1) * 2), sf + 4 * (j >> 1), sfx + 4 * (j >> 1) * P::row_tiles,
+                       (k | j) != 0 ? 1u : 0u);
+          tc_commit(&empty[stage]);
+          if (k == p.k_iters - 1) tc_commit(&tfull[acc]);
+        }
+        __syncwarp();
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
+    }
+    if (elect_one()) {
       tc_commit(mma_done);
       wait_drain(mma_done, 0, p.timeout_ns, p.status);
     }
+    __syncwarp();
   } else if (warp >= 6) {
     // Scales of a stage whose copies have landed: its last MMAs are done, since the
     // loader waited for them, so its columns are free.
@@ -396,6 +414,10 @@ int run_tile(const MxGemmParams& p, int sms, cudaStream_t stream) {
   a.ld_out = p.ld_out;
   a.status = p.status;
   a.timeout_ns = p.timeout_ns;
+  // An MMA's scales start on an even column of tensor memory: token tiles other
+  // than the first need 64 rows or a multiple of it.
+  static_assert(NT % 64 == 0 || NT < 64, "even scale columns");
+  if (a.n_tiles > 1 && NT % 64 != 0) return FLCE_ERR_ARG;
   const int64_t total = static_cast<int64_t>(a.v_tiles) * a.n_tiles;
   if (total >= (1LL << 31)) return FLCE_ERR_ARG;
   const int grid = static_cast<int>(total < sms ? total : sms);
