@@ -70,7 +70,7 @@ size_t flce_microscale_codes_size(int64_t rows, int64_t cols);
 size_t flce_microscale_scales_size(int64_t rows, int64_t cols);
 int flce_microscale_quantize(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ld_x, void* codes,
                              void* scales, void* stream);
-/* out [rows, cols] contiguous = what the codes stand for, in out_dtype. */
+/* out [rows, cols] contiguous, 32-byte aligned = what the codes stand for, in out_dtype. */
 int flce_microscale_dequantize(const void* codes, const void* scales, int64_t rows, int64_t cols, void* out,
                                int out_dtype, void* stream);
 

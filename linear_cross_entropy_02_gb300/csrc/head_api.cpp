@@ -203,14 +203,14 @@ int flce_microscale_dequantize(const void* codes, const void* scales, int64_t ro
   if (!dtype_ok(out_dtype) || !mx_shape_ok(rows, cols)) return FLCE_ERR_ARG;
   if (rows == 0) return FLCE_OK;
   if (!out) return FLCE_ERR_ARG;
-  if (!aligned(out, 16)) return FLCE_ERR_ALIGN;
+  if (!aligned(out, 32)) return FLCE_ERR_ALIGN;
   int rc = mx_buffers(rows, codes, scales);
   if (rc != FLCE_OK) return rc;
   int sms = 0;
   if ((rc = device_check(&sms)) != FLCE_OK) return rc;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_handle);
   FLCE_LAUNCH(K_MX_DEQUANT, launch_mx_dequantize(static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales),
-                                                 rows, cols, out, out_dtype, sms, stream));
+                                                 rows, cols, out, out_dtype, stream));
   return FLCE_OK;
 }
 

@@ -62,7 +62,7 @@ struct MxQuantParams {
 };
 cudaError_t launch_mx_quantize(const MxQuantParams& p, int sms, cudaStream_t s);
 cudaError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, void* out,
-                                 int out_dtype, int sms, cudaStream_t s);
+                                 int out_dtype, cudaStream_t s);
 
 struct MxGemmParams {
   const uint8_t* a_codes;

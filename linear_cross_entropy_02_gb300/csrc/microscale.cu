@@ -8,10 +8,12 @@
 // x 2^-e is then exact, and the conversion instruction rounds it to the nearest
 // code, ties to the even one, at most 6.
 //
-// Both kernels move memory and little else: a warp takes 256 consecutive
-// elements of a row, eight per lane, so that reads and writes are whole lines;
-// the four lanes of a block share its magnitude by two shuffles, and the four
-// scale bytes that lie together in a scale tile leave as one word.
+// Both kernels move memory and little else. A lane takes 16 consecutive elements,
+// one 32-byte load of bf16, and the two lanes of a block share its magnitude by
+// one shuffle. The matrix is taken as one sequence of such units, whatever its
+// width, by CTAs that do a fixed number of them and leave. Four scale bytes that
+// lie together in a scale tile leave as one word where all of a row's tiles are
+// whole.
 #include "head_device.cuh"
 #include "head_internal.h"
 
@@ -19,7 +21,9 @@ namespace flce {
 
 namespace {
 
-constexpr int kChunk = 256;  // elements of a row per warp step
+constexpr int kUnit = 16;      // elements per lane and step
+constexpr int kThreads = 256;
+constexpr int kSteps = 2;      // units per thread, their loads in flight together
 
 // Eight floats to eight codes: v[0] in the lowest four bits.
 __device__ __forceinline__ uint32_t encode8(const float (&v)[8]) {
@@ -65,153 +69,219 @@ __device__ __forceinline__ int64_t scale_word(int64_t r, int64_t kt, int64_t k_t
   return ((r / kMxTileRows) * k_tiles + kt) * kMxTileBytes + (r % 32) * 16 + (r % kMxTileRows / 32) * 4;
 }
 
-// Work of a warp: `seg` chunks of a row, part `part` of `parts`. Warp w of the
-// grid takes tasks w, w + warps, ... in the order of (row, part).
-struct Split {
-  int64_t rows;  // rows to visit
-  int parts, seg, chunks;
+// 16 elements from 16- or 32-byte aligned memory (wide), or one by one.
+template <typename T>
+__device__ __forceinline__ void load16(const T* p, bool wide, uint32_t (&r)[4 * sizeof(T)]) {
+  if (wide) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
+      asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(r[8 * i]), "=r"(r[8 * i + 1]), "=r"(r[8 * i + 2]), "=r"(r[8 * i + 3]), "=r"(r[8 * i + 4]),
+                     "=r"(r[8 * i + 5]), "=r"(r[8 * i + 6]), "=r"(r[8 * i + 7])
+                   : "l"(p + i * 32 / sizeof(T)));
+  } else if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = p[2 * i] | static_cast<uint32_t>(p[2 * i + 1]) << 16;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(p[i]);
+  }
+}
+template <int N>
+__device__ __forceinline__ void store32(void* p, const uint32_t (&r)[N], int i) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]),
+               "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
+               : "memory");
+}
+
+// The largest magnitude's biased exponent. Magnitudes are compared as bit
+// patterns: NaN is above infinity, both above every number.
+__device__ __forceinline__ uint32_t exponent16(const uint32_t (&r)[8]) {  // bf16 pairs
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = __vmaxu2(m, r[i] & 0x7FFF7FFFu);
+  return max(m >> 16, m & 0xFFFFu) >> 7;
+}
+__device__ __forceinline__ uint32_t exponent16(const uint32_t (&r)[16]) {  // fp32
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) m = max(m, r[i] & 0x7FFFFFFFu);
+  return m >> 23;
+}
+
+struct Shape {
+  uint32_t units_per_row;
+  int64_t units;      // of the whole matrix
+  int64_t work_ctas;  // CTAs for them; the rest fill the scale tiles' other places
+  int64_t k_tiles;
 };
 
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) mx_quantize_kernel(const MxQuantParams p, const Split sp) {
-  const int lane = threadIdx.x & 31;
+Shape shape_of(int64_t rows, int64_t cols) {
+  Shape s;
+  s.units_per_row = static_cast<uint32_t>(cols / kUnit);
+  s.units = rows * s.units_per_row;
+  s.work_ctas = (s.units + kThreads * kSteps - 1) / (kThreads * kSteps);
+  s.k_tiles = (cols + kMxTileCols - 1) / kMxTileCols;
+  return s;
+}
+
+// Row and unit within the row of a unit.
+__device__ __forceinline__ void place_of(int64_t unit, uint32_t per_row, int64_t& row, uint32_t& u) {
+  if (unit >> 32 == 0) {
+    const uint32_t r = static_cast<uint32_t>(unit) / per_row;
+    row = r;
+    u = static_cast<uint32_t>(unit) - r * per_row;
+  } else {
+    row = unit / per_row;
+    u = static_cast<uint32_t>(unit - row * per_row);
+  }
+}
+
+// WORDS: cols is a multiple of 128, so that eight lanes hold a whole scale word.
+template <typename T, bool WORDS>
+__global__ void __launch_bounds__(kThreads) mx_quantize_kernel(const MxQuantParams p, const Shape sh, const bool wide) {
   if (p.status && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
-  const int64_t tasks = sp.rows * sp.parts;
-  const int64_t k_tiles = (p.cols + kMxTileCols - 1) / kMxTileCols;
+  if (blockIdx.x >= sh.work_ctas) {
+    // places without a block hold 127: rows beyond the last, blocks beyond the width
+    const int64_t all = (p.rows + kMxTileRows - 1) / kMxTileRows * kMxTileRows;
+    const int blocks = static_cast<int>(p.cols / kMxBlock);
+    const int64_t step = static_cast<int64_t>(gridDim.x - sh.work_ctas) * kThreads;
+    const int64_t first = (blockIdx.x - sh.work_ctas) * kThreads + threadIdx.x;
+    for (int64_t i = first; i < (all - p.rows) * sh.k_tiles; i += step)
+      *reinterpret_cast<uint32_t*>(p.scales + scale_word(p.rows + i / sh.k_tiles, i % sh.k_tiles, sh.k_tiles)) = 0x7F7F7F7Fu;
+    if (!WORDS)
+      for (int64_t row = first; row < p.rows; row += step)
+        for (int b = blocks; b < sh.k_tiles * 4; ++b) p.scales[scale_word(row, b / 4, sh.k_tiles) + b % 4] = 127;
+    return;
+  }
   const T* x = static_cast<const T*>(p.x);
-  for (int64_t task = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); task < tasks; task += warps) {
-    const int64_t row = task / sp.parts;
-    const int part = static_cast<int>(task - row * sp.parts);
-    const int c0 = part * sp.seg, c1 = min(c0 + sp.seg, sp.chunks);
-    const bool real = row < p.rows;  // rows that only fill the last scale tile are not read
-#pragma unroll 2
-    for (int ch = c0; ch < c1; ++ch) {
-      const int64_t col = static_cast<int64_t>(ch) * kChunk + lane * 8;
-      const bool in = real && col < p.cols;
+  uint32_t raw[kSteps][4 * sizeof(T)];
+  int64_t row[kSteps];
+  uint32_t u[kSteps];
+  bool in[kSteps];
+#pragma unroll
+  for (int k = 0; k < kSteps; ++k) {
+    const int64_t unit = (blockIdx.x * static_cast<int64_t>(kSteps) + k) * kThreads + threadIdx.x;
+    in[k] = unit < sh.units;
+    if (in[k]) {
+      place_of(unit, sh.units_per_row, row[k], u[k]);
+      load16<T>(x + row[k] * p.ld_x + static_cast<int64_t>(u[k]) * kUnit, wide, raw[k]);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kSteps; ++k) {
+    uint32_t E = in[k] ? exponent16(raw[k]) : 0;
+    E = max(E, __shfl_xor_sync(0xffffffffu, E, 1));
+    const uint32_t byte = E == 255u ? 255u : E > 2u ? E - 2u : 0u;
+    uint32_t word = byte;
+    if (WORDS) {
+      word |= __shfl_down_sync(0xffffffffu, word, 2) << 8;
+      word = (word & 0xFFFFu) | __shfl_down_sync(0xffffffffu, word, 4) << 16;
+    }
+    if (!in[k]) continue;
+    if (WORDS) {
+      if ((threadIdx.x & 7) == 0)
+        *reinterpret_cast<uint32_t*>(p.scales + scale_word(row[k], u[k] / 8, sh.k_tiles)) = word;
+    } else if ((threadIdx.x & 1) == 0) {
+      p.scales[scale_word(row[k], u[k] / 8, sh.k_tiles) + (u[k] / 2 & 3)] = static_cast<uint8_t>(byte);
+    }
+    const float inv = E == 255u ? 0.f : __uint_as_float((254u - byte) << 23);
+    uint2 c;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
       float v[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = 0.f;
-      if (in) {
-        const T* q = x + row * p.ld_x + col;
-        if constexpr (!VEC) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = to_float<T>(q[j]);
-        } else if constexpr (sizeof(T) == 2) {
-          const Raw<T, 8> r = load_raw<T, 8>(q);
-          unpack<T, 8>(r, v);
+      for (int j = 0; j < 8; ++j) {
+        if constexpr (sizeof(T) == 2) {
+          const uint32_t w = raw[k][h * 4 + j / 2];
+          v[j] = __uint_as_float(j & 1 ? w & 0xFFFF0000u : w << 16) * inv;
         } else {
-          const float4 a = *reinterpret_cast<const float4*>(q), b = *reinterpret_cast<const float4*>(q + 4);
-          v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-          v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+          v[j] = __uint_as_float(raw[k][h * 8 + j]) * inv;
         }
       }
-      uint32_t top = 0;  // magnitudes as bit patterns: NaN is above infinity, both above every number
-#pragma unroll
-      for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const uint32_t E = top >> 23;
-      const uint32_t byte = E == 255u ? 255u : E > 2u ? E - 2u : 0u;
-      if (in) {
-        const float inv = E == 255u ? 0.f : __uint_as_float((254u - byte) << 23);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= inv;
-        const uint32_t c = E == 255u ? 0u : encode8(v);
-        *reinterpret_cast<uint32_t*>(p.codes + row * (p.cols / 2) + col / 2) = c;
-      }
-      // the four blocks of a K-tile: lanes 0, 4, 8, 12 (and 16, ...)
-      uint32_t word = in ? byte : 127u;
-      word = word | (__shfl_down_sync(0xffffffffu, word, 4) << 8);
-      word = (word & 0xFFFFu) | (__shfl_down_sync(0xffffffffu, word, 8) << 16);
-      const int64_t kt = col / kMxTileCols;
-      if ((lane & 15) == 0 && kt < k_tiles)
-        *reinterpret_cast<uint32_t*>(p.scales + scale_word(row, kt, k_tiles)) = word;
+      (h ? c.y : c.x) = E == 255u ? 0u : encode8(v);
     }
+    *reinterpret_cast<uint2*>(p.codes + row[k] * (p.cols / 2) + u[k] * 8) = c;
   }
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256) mx_dequantize_kernel(const uint8_t* codes, const uint8_t* scales, int64_t cols,
-                                                            T* out, const Split sp) {
-  const int lane = threadIdx.x & 31;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
-  const int64_t tasks = sp.rows * sp.parts;
-  const int64_t k_tiles = (cols + kMxTileCols - 1) / kMxTileCols;
-  for (int64_t task = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); task < tasks; task += warps) {
-    const int64_t row = task / sp.parts;
-    const int part = static_cast<int>(task - row * sp.parts);
-    const int c0 = part * sp.seg, c1 = min(c0 + sp.seg, sp.chunks);
-#pragma unroll 2
-    for (int ch = c0; ch < c1; ++ch) {
-      const int64_t col = static_cast<int64_t>(ch) * kChunk + lane * 8;
-      if (col >= cols) continue;
-      const uint32_t c = __ldg(reinterpret_cast<const uint32_t*>(codes + row * (cols / 2) + col / 2));
-      const float s = scale_value(__ldg(scales + scale_word(row, col / kMxTileCols, k_tiles) + (lane >> 2 & 3)));
-      float v[8];
-      decode8(c, v);
+__global__ void __launch_bounds__(kThreads)
+    mx_dequantize_kernel(const uint8_t* codes, const uint8_t* scales, T* out, const Shape sh) {
+  uint2 c[kSteps];
+  uint32_t byte[kSteps];
+  int64_t unit[kSteps];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= s;
-      T* o = out + row * cols + col;
-      if constexpr (sizeof(T) == 2) {
-        store_raw<T, 8>(o, pack<T, 8>(v));
-      } else {
-        *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
-        *reinterpret_cast<float4*>(o + 4) = make_float4(v[4], v[5], v[6], v[7]);
-      }
+  for (int k = 0; k < kSteps; ++k) {
+    unit[k] = (blockIdx.x * static_cast<int64_t>(kSteps) + k) * kThreads + threadIdx.x;
+    if (unit[k] < sh.units) {
+      int64_t row;
+      uint32_t u;
+      place_of(unit[k], sh.units_per_row, row, u);
+      c[k] = __ldg(reinterpret_cast<const uint2*>(codes) + unit[k]);
+      byte[k] = __ldg(scales + scale_word(row, u / 8, sh.k_tiles) + (u / 2 & 3));
     }
   }
-}
-
-// Rows are cut into parts until every SM has its 64 warps, and no further: a
-// part of several chunks keeps two loads per lane in flight.
-Split split_rows(int64_t rows, int64_t cols, int sms) {
-  Split s;
-  s.rows = rows;
-  s.chunks = static_cast<int>((cols + kChunk - 1) / kChunk);
-  const int64_t want = 64LL * sms;
-  int64_t parts = (want + rows - 1) / rows;
-  if (parts > s.chunks) parts = s.chunks;
-  s.seg = static_cast<int>((s.chunks + parts - 1) / parts);
-  s.parts = (s.chunks + s.seg - 1) / s.seg;
-  return s;
-}
-
-inline unsigned grid_of(const Split& s, int sms) {
-  const int64_t want = (s.rows * s.parts + 7) / 8, most = 16LL * sms;
-  return static_cast<unsigned>(want < most ? want : most);
+#pragma unroll
+  for (int k = 0; k < kSteps; ++k) {
+    if (unit[k] >= sh.units) continue;
+    const float s = scale_value(byte[k]);
+    uint32_t r[4 * sizeof(T)];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float v[8];
+      decode8(h ? c[k].y : c[k].x, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[j] *= s;
+        if constexpr (sizeof(T) == 4) r[h * 8 + j] = __float_as_uint(v[j]);
+      }
+      if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r[h * 4 + j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+      }
+    }
+    T* o = out + unit[k] * kUnit;
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) store32(o + i * 32 / sizeof(T), r, 8 * i);
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_mx_quantize(const MxQuantParams& p, int sms, cudaStream_t s) {
-  const int64_t rows = (p.rows + kMxTileRows - 1) / kMxTileRows * kMxTileRows;
-  const Split sp = split_rows(rows, p.cols, sms);
-  const unsigned grid = grid_of(sp, sms);
+  const Shape sh = shape_of(p.rows, p.cols);
   const int64_t es = p.dtype == FLCE_DTYPE_F32 ? 4 : 2;
-  const bool vec = reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && p.ld_x * es % 16 == 0;
+  const bool wide = reinterpret_cast<uintptr_t>(p.x) % 32 == 0 && p.ld_x * es % 32 == 0;
+  const bool words = p.cols % kMxTileCols == 0;
+  const int64_t pad = (words ? 0 : p.rows) + (kMxTileRows - p.rows % kMxTileRows) % kMxTileRows * sh.k_tiles;
+  const int64_t pad_ctas = (pad + kThreads - 1) / kThreads;
+  const int64_t grid = sh.work_ctas + (pad_ctas < sms ? pad_ctas : sms);
+  if (grid >= (int64_t{1} << 31)) return cudaErrorInvalidValue;
+  const unsigned g = static_cast<unsigned>(grid);
   if (p.dtype == FLCE_DTYPE_F32) {
-    if (vec)
-      mx_quantize_kernel<float, true><<<grid, 256, 0, s>>>(p, sp);
+    if (words)
+      mx_quantize_kernel<float, true><<<g, kThreads, 0, s>>>(p, sh, wide);
     else
-      mx_quantize_kernel<float, false><<<grid, 256, 0, s>>>(p, sp);
+      mx_quantize_kernel<float, false><<<g, kThreads, 0, s>>>(p, sh, wide);
   } else {
-    if (vec)
-      mx_quantize_kernel<uint16_t, true><<<grid, 256, 0, s>>>(p, sp);
+    if (words)
+      mx_quantize_kernel<uint16_t, true><<<g, kThreads, 0, s>>>(p, sh, wide);
     else
-      mx_quantize_kernel<uint16_t, false><<<grid, 256, 0, s>>>(p, sp);
+      mx_quantize_kernel<uint16_t, false><<<g, kThreads, 0, s>>>(p, sh, wide);
   }
   return cudaGetLastError();
 }
 
 cudaError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, void* out,
-                                 int out_dtype, int sms, cudaStream_t s) {
-  const Split sp = split_rows(rows, cols, sms);
-  const unsigned grid = grid_of(sp, sms);
+                                 int out_dtype, cudaStream_t s) {
+  const Shape sh = shape_of(rows, cols);
+  if (sh.work_ctas >= (int64_t{1} << 31)) return cudaErrorInvalidValue;
+  const unsigned g = static_cast<unsigned>(sh.work_ctas);
   if (out_dtype == FLCE_DTYPE_F32)
-    mx_dequantize_kernel<float><<<grid, 256, 0, s>>>(codes, scales, cols, static_cast<float*>(out), sp);
+    mx_dequantize_kernel<float><<<g, kThreads, 0, s>>>(codes, scales, static_cast<float*>(out), sh);
   else
-    mx_dequantize_kernel<uint16_t><<<grid, 256, 0, s>>>(codes, scales, cols, static_cast<uint16_t*>(out), sp);
+    mx_dequantize_kernel<uint16_t><<<g, kThreads, 0, s>>>(codes, scales, static_cast<uint16_t*>(out), sh);
   return cudaGetLastError();
 }
 
