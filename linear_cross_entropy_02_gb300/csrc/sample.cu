@@ -8,7 +8,7 @@
 // a function of the logits, the settings and u alone.
 //
 // A row takes two passes. The first reads it from HBM, keeps the maximum and
-// counts logits in 2048 bins of (x - anchor) / T, the anchor being the maximum
+// counts logits in 4096 bins of (x - anchor) / T, the anchor being the maximum
 // of the row's first part. Then:
 //   top_k that some bins cover with at most kListKeys logits: the second pass
 //     collects those logits in shared memory, where all three filters cut them
@@ -54,18 +54,21 @@ constexpr float kFixed = 1099511627776.f;  // 2^40
 // General selection.
 constexpr int kBins = 1024;
 constexpr float kBinsPerUnit = (kBins - 1) / kRange;
-// Counts of the first pass: 2048 bins from 28 above the anchor to 28 below it.
-constexpr int kCountBins = 2048;
-constexpr int kAnchorBin = kCountBins / 2;
-constexpr float kCountsPerUnit = kAnchorBin / kRange;
+// Counts of the first pass: 4096 bins from 8 above the anchor to 28 below it;
+// the last one holds what is further below, whose weights are zero.
+constexpr int kCountBins = 4096;
+constexpr int kBinsPerThread = kCountBins / kThreads;
+constexpr float kAbove = 8.f;
+constexpr float kPlaces = kAbove + kRange;  // a place of 0 to 1 is this many units of t
+constexpr float kUnitsPerBin = kPlaces / (kCountBins - 1);
 // Logits above 4 below the anchor are weighed one by one for the estimate: a
-// bin's middle is up to 1.4% off for one logit, which only matters where a few
+// bin's middle is up to 0.4% off for one logit, which only matters where a few
 // logits carry the row. (All of a normal row's logits would slow the pass:
 // 4 below the maximum there are some per cent of them.)
-constexpr int kWeighedBins = kAnchorBin + 146;
+constexpr int kWeighedBins = static_cast<int>((kAbove + 4.f) / kUnitsPerBin);
 // How far around the estimated end logits are collected, of the whole weight:
 // the first margin if the list holds what lies in it, else the second.
-constexpr float kMargin = 0.0008f, kSmallMargin = 0.0002f;
+constexpr float kMargin = 0.0005f, kSmallMargin = 0.0001f;
 // Segments of a slice whose weights are kept apart, at most.
 constexpr int kSegments = 256;
 constexpr int kFirstVectors = 4;  // per thread: the part of the row that sets the anchor
@@ -112,7 +115,8 @@ struct Shared {
   uint32_t general;         // CTA 0: the row needs the general selection
   uint32_t red[kWarps], red2[kWarps];
   float fscan[kWarps];
-  float told[3];  // CTA 0: where the prefix ends, for the others
+  float cut_x[2];
+  uint32_t told[3];  // CTA 0: where the prefix ends, for the others
 };
 
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -168,7 +172,8 @@ __device__ __forceinline__ void remote_add(float* mine, uint32_t rank, float v) 
   asm volatile("red.shared::cluster.add.f32 [%0], %1;" ::"r"(mapa_shared(smem_u32(mine), rank)), "f"(v) : "memory");
 }
 
-// Appends to CTA 0's list; what does not fit is only counted.
+// Appends to CTA 0's list; what does not fit is only counted. (One addition to
+// the length for a warp's entries together, by votes or a scan, measured slower.)
 template <bool MULTI>
 __device__ __forceinline__ void append(Shared& s, uint32_t* listed, uint64_t entry) {
   if constexpr (!MULTI) {
@@ -186,7 +191,7 @@ __device__ __forceinline__ void append(Shared& s, uint32_t* listed, uint64_t ent
   }
 }
 
-// ---------------------------------------------------------------- sums and sorts in a CTA
+// ---------------------------------------------------------------- sums in a CTA
 __device__ __forceinline__ uint64_t warp_inclusive(uint64_t v) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -222,24 +227,44 @@ __device__ uint64_t block_exclusive(uint64_t v, uint64_t* scan, uint64_t* total)
   return scan[warp] + inc - v;
 }
 
-__device__ float block_exclusive(float v, float* scan, float* total) {
+// The same of a count and an estimated weight at once.
+__device__ __forceinline__ void block_exclusive(Shared& s, uint32_t n, float w, uint32_t* n_before, float* w_before,
+                                                float* w_total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float inc = v;
+  uint32_t ni = n;
+  float wi = w;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const float n = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += n;
+    const uint32_t a = __shfl_up_sync(0xffffffffu, ni, o);
+    const float b = __shfl_up_sync(0xffffffffu, wi, o);
+    if (lane >= o) {
+      ni += a;
+      wi += b;
+    }
   }
   __syncthreads();
-  if (lane == 31) scan[warp] = inc;
-  __syncthreads();
-  float before = 0.f, all = 0.f;
-  for (int w = 0; w < kWarps; ++w) {  // one order for every thread
-    if (w == warp) before = all;
-    all += scan[w];
+  if (lane == 31) {
+    s.red[warp] = ni;
+    s.fscan[warp] = wi;
   }
-  *total = all;
-  return before + inc - v;
+  __syncthreads();
+  // every warp adds up the warps before it, in one order
+  uint32_t a = s.red[lane];
+  float b = s.fscan[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t c = __shfl_up_sync(0xffffffffu, a, o);
+    const float d = __shfl_up_sync(0xffffffffu, b, o);
+    if (lane >= o) {
+      a += c;
+      b += d;
+    }
+  }
+  *w_total = __shfl_sync(0xffffffffu, b, 31);
+  const uint32_t pn = __shfl_sync(0xffffffffu, a, warp == 0 ? 0 : warp - 1);
+  const float pw = __shfl_sync(0xffffffffu, b, warp == 0 ? 0 : warp - 1);
+  *n_before = (warp == 0 ? 0u : pn) + ni - n;
+  *w_before = (warp == 0 ? 0.f : pw) + wi - w;
 }
 
 // Adds a 64-bit weight to a bin, in halves with the carry.
@@ -319,7 +344,7 @@ struct Row {
   int n, vecs;
   int c0;         // vocabulary index of the first logit
   float top, inv; // largest logit of the row, 1 / temperature
-  float anchor, per_bin;  // counting bins: (anchor - x) per_bin + kAnchorBin
+  float anchor, per_place;  // places: (anchor - x) per_place + kAbove / kPlaces, kept in [0, 1]
   float min_p;
   uint32_t rank, ctas;
 
@@ -341,22 +366,27 @@ struct Row {
   __device__ __forceinline__ int bin(float x) const {
     return min(kBins - 1, __float2int_rz(scaled(x) * -kBinsPerUnit));
   }
-  __device__ __forceinline__ float place(float x) const {
-    return __fmaf_rn(__fsub_rn(anchor, x), per_bin, static_cast<float>(kAnchorBin));
+  // Counting bin: two multiply-adds, the second rounding towards zero into the
+  // mantissa of 2^23. Falls as x rises.
+  __device__ __forceinline__ int count_bin(float x) const {
+    const float u = __saturatef(__fmaf_rn(__fsub_rn(anchor, x), per_place, kAbove / kPlaces));
+    return static_cast<int>(__float_as_uint(__fmaf_rz(u, static_cast<float>(kCountBins - 1), 8388608.f)) - 0x4B000000u);
   }
-  __device__ __forceinline__ static int count_bin(float place) {
-    return min(kCountBins - 1, max(0, __float2int_rz(place)));
-  }
-  // The smallest logit with a place before `cut` (places fall as logits rise),
-  // infinity if there is none. For a whole warp: each step tries 32 points of the
-  // range of keys that is left.
-  __device__ __forceinline__ float first_before(float cut) const {
+  // The smallest logit in a counting bin before `cut`, infinity if there is none.
+  // For a whole warp: each step tries 32 points of the range of keys that is left,
+  // at first the neighbourhood of the inverse of count_bin, if it holds the answer.
+  __device__ __forceinline__ float first_before(int cut) const {
     const uint32_t lane = threadIdx.x & 31;
+    const float guess = anchor - (static_cast<float>(cut) * (1.f / (kCountBins - 1)) - kAbove / kPlaces) / per_place;
+    const float off = 1e-6f * (fabsf(anchor) + fabsf(guess));
     uint32_t lo = order_key(-INFINITY), hi = order_key(INFINITY);  // hi: known to be before, or infinity
+    const float below = guess - off, above = guess + off;
+    if (fabsf(below) < INFINITY && count_bin(below) >= cut) lo = order_key(below);
+    if (fabsf(above) < INFINITY && count_bin(above) < cut) hi = order_key(above);
     while (lo < hi) {
       const uint32_t step = (hi - lo + 31) / 32;
       const uint32_t k = lo + lane * step;
-      const uint32_t yes = __ballot_sync(0xffffffffu, k >= hi || place(key_value(k)) < cut);
+      const uint32_t yes = __ballot_sync(0xffffffffu, k >= hi || count_bin(key_value(k)) < cut);
       const uint32_t at = yes ? __ffs(yes) - 1 : 32;  // the first point that is before
       const uint32_t l = lo;
       if (at < 32) hi = min(hi, l + at * step);
@@ -369,14 +399,22 @@ struct Row {
     return max(32, (vecs + 32 * kSegments - 1) / (32 * kSegments) * 32);
   }
 
-  // f(x, index) for this thread's logits.
+  // f(x, index) for this thread's logits, four vectors' loads in flight.
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
-    for (int v = threadIdx.x; v < vecs; v += kThreads) {
-      float x[E];
-      unpack<T, E>(get(v), x);
+    for (int v = threadIdx.x; v < vecs; v += 4 * kThreads) {
+      Raw<T, E> raw[4];
 #pragma unroll
-      for (int e = 0; e < E; ++e) f(x[e], static_cast<uint32_t>(c0 + v * E + e));
+      for (int j = 0; j < 4; ++j)
+        if (v + j * kThreads < vecs) raw[j] = get(v + j * kThreads);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (v + j * kThreads >= vecs) break;
+        float x[E];
+        unpack<T, E>(raw[j], x);
+#pragma unroll
+        for (int e = 0; e < E; ++e) f(x[e], static_cast<uint32_t>(c0 + (v + j * kThreads) * E + e));
+      }
     }
   }
 };
@@ -403,37 +441,16 @@ __device__ __forceinline__ uint64_t block_total(Shared& s, uint64_t v) {
 }
 
 // The entry of the CTA's list of n at which the running sum in rank order,
-// `start` before the first, reaches the goal (start < goal <= start + sum). WEIGHT:
-// sums of weights, else counts. A histogram over the range of entries (they are
-// whole numbers in rank order, all different), again over the bin that holds the
-// goal, until that has at most kFew. Uses the first histogram.
+// `start` before the first, reaches the goal (start < goal); ~0 if it does not.
+// All entries lie in [lo, hi]. WEIGHT: sums of weights, else counts. A histogram
+// over the range of entries (they are whole numbers in rank order, all
+// different), again over the bin that holds the goal, until that has at most
+// kFew. Uses the first histogram.
 template <typename T, bool WEIGHT>
-__device__ uint64_t list_reach(const Row<T>& row, Shared& s, int n, uint64_t start, uint64_t goal) {
+__device__ uint64_t list_reach(const Row<T>& row, Shared& s, int n, uint64_t lo, uint64_t hi, uint64_t start,
+                               uint64_t goal) {
   Hist& h = s.hist[0];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint64_t lo = ~0ull, hi = 0;
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    lo = min(lo, s.list[i]);
-    hi = max(hi, s.list[i]);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-  }
-  __syncthreads();
-  if (lane == 0) {
-    s.scan[warp] = lo;
-    s.few[warp] = hi;
-  }
-  __syncthreads();
-  lo = s.scan[lane];
-  hi = s.few[lane];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-  }
+  __syncthreads();  // the list is complete, the histogram's place free
   while (true) {
     const int bits = 64 - __clzll(static_cast<long long>(hi - lo));
     const int shift = bits > 10 ? bits - 10 : 0;
@@ -452,6 +469,7 @@ __device__ uint64_t list_reach(const Row<T>& row, Shared& s, int n, uint64_t sta
     const uint64_t v = WEIGHT ? h.lo[b] + (static_cast<uint64_t>(h.hi[b]) << 32) : h.count[b];
     uint64_t total;
     const uint64_t before = start + block_exclusive(v, s.scan, &total);
+    if (start + total < goal) return ~0ull;
     if (before < goal && goal <= before + v) {
       s.found_bin = b;
       s.found_above = before;
@@ -610,7 +628,8 @@ __device__ bool select(const Row<T>& row, Shared& s, int& buf, uint32_t* listed,
   });
   row_barrier<MULTI>();
   if (row.rank == 0) {
-    const uint64_t e = list_reach<T, WEIGHT>(row, s, static_cast<int>(count), above, goal);
+    const uint64_t e = list_reach<T, WEIGHT>(row, s, static_cast<int>(count), list_entry(row.top, 0), list_entry(-INFINITY, ~0u),
+                                             above, goal);
     uint32_t ties = 0;  // of the same logit, up to that entry
     for (int i = threadIdx.x; i < static_cast<int>(count); i += kThreads)
       ties += s.list[i] >> 32 == e >> 32 && s.list[i] <= e;
@@ -798,16 +817,17 @@ __device__ void short_list_answer(const Row<T>& row, Shared& s, const SamplePara
 // The same for a long list.
 template <typename T>
 __device__ void list_answer(const Row<T>& row, Shared& s, const SampleParams& p, int64_t r, int n, int64_t top_k,
-                            float top_p, float u) {
+                            float top_p, float u, float x_hi) {
+  const uint64_t lo = list_entry(row.top, 0), hi = list_entry(x_hi, ~0u);
   uint64_t last = ~0ull;  // last entry that the filters by rank keep
-  if (top_k > 0 && n > top_k) last = list_reach<T, false>(row, s, n, 0, static_cast<uint64_t>(top_k));
+  if (top_k > 0 && n > top_k) last = list_reach<T, false>(row, s, n, lo, hi, 0, static_cast<uint64_t>(top_k));
   if (top_p < 1.f) {
     uint64_t sum = 0;
     for (int i = threadIdx.x; i < n; i += kThreads)
       if (s.list[i] <= last) sum += row.weight(entry_value(s.list[i]));
     const uint64_t whole = block_total(s, sum);
     const uint64_t goal = by_one(s, [&] { return top_p_goal(top_p, whole); });
-    last = min(last, list_reach<T, true>(row, s, n, 0, goal));
+    last = min(last, list_reach<T, true>(row, s, n, lo, hi, 0, goal));
   }
   // kept weights by segments of the vocabulary, two per thread
   Answer& a = s.answer;
@@ -868,83 +888,80 @@ __device__ void list_answer(const Row<T>& row, Shared& s, const SampleParams& p,
 }
 
 // ---------------------------------------------------------------- second pass
-// Adds up this slice's weights: sum_total all of them, sum_above those placed
-// above cut_lo, seg_weight[] the latter (at least min_p) by segments; logits
-// placed in [cut_lo, cut_hi) are appended to CTA 0's list. Without CUT every
-// logit counts as above and only the segments are summed. Warp w has segments
-// w, w + 32, ... and goes through them in rounds of 32 vectors, four rounds'
-// loads in flight.
-// MIN_P: the row has that filter; without it the segments' sum is sum_above.
+// One vector's logits: their weights to `all` and, from x_lo on (and at least
+// min_p), to `acc`; logits from x_hi to x_lo to CTA 0's list. Without CUT every
+// logit counts as above. MIN_P: the row has that filter, and `above` gets what
+// is above without it.
 template <typename T, bool MULTI, bool CUT, bool MIN_P>
-__device__ void sum_segments(const Row<T>& row, Shared& s, float cut_lo, float cut_hi) {
+__device__ __forceinline__ void sum_vector(const Row<T>& row, Shared& s, const Raw<T, Row<T>::E>& raw, int v, float x_lo,
+                                           float x_hi, Sum& acc, Sum& all, Sum& above) {
   constexpr int E = Row<T>::E;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rounds = Row<T>::segment_vecs(row.vecs) / 32;  // per segment
-  const int segs = (row.vecs + rounds * 32 - 1) / (rounds * 32);
-  const int mine = segs > warp ? (segs - warp + kWarps - 1) / kWarps : 0;
-  for (int i = threadIdx.x; i < kSegments; i += kThreads)
-    if (i >= segs) s.seg_weight[i] = 0;
-  Sum acc, all, above;
-  uint64_t total = 0, over = 0;
-  // the same cuts as logits: above from x_lo on, listed from x_hi on
-  const float x_lo = CUT ? row.first_before(cut_lo) : 0.f, x_hi = CUT ? row.first_before(cut_hi) : 0.f;
-  int seg = warp, round = 0;  // of the next vector to load
-  int done = warp, done_round = 0;
-  for (int t = mine * rounds; t > 0; t -= 4) {
-    Raw<T, E> raw[4];
-    int at[4];
+  float x[E];
+  unpack<T, E>(raw, x);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      at[j] = (seg * rounds + round) * 32 + lane;
-      if (j < t && at[j] < row.vecs)
-        raw[j] = row.get(at[j]);
-      else
-        at[j] = -1;
-      if (++round == rounds) {
-        round = 0;
-        seg += kWarps;
+  for (int e = 0; e < E; ++e) {
+    const float ex = row.exponential(x[e]);
+    const Halves w = halves(ex);
+    if (CUT) {
+      all.add(w);
+      if (x[e] >= x_lo) {
+        if (MIN_P) above.add(w);
+        if (!MIN_P || ex >= row.min_p) acc.add(w);
+      } else if (x[e] >= x_hi) {
+        append<MULTI>(s, &s.listed[0], list_entry(x[e], static_cast<uint32_t>(row.c0 + v * E + e)));
       }
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (j >= t) break;
-      if (at[j] >= 0) {
-        float x[E];
-        unpack<T, E>(raw[j], x);
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float ex = row.exponential(x[e]);
-          const Halves w = halves(ex);
-          if (CUT) {
-            all.add(w);
-            if (x[e] >= x_lo) {
-              if (MIN_P) above.add(w);
-              if (!MIN_P || ex >= row.min_p) acc.add(w);
-            } else if (x[e] >= x_hi) {
-              append<MULTI>(s, &s.listed[0], list_entry(x[e], static_cast<uint32_t>(row.c0 + at[j] * E + e)));
-            }
-          } else if (!MIN_P || ex >= row.min_p) {
-            acc.add(w);
-          }
-        }
-      }
-      if (++done_round == rounds) {
-        const uint64_t w = acc.total();
-        if (lane == 0) s.seg_weight[done] = w;
-        acc = Sum();
-        if (CUT) {
-          total += all.total();
-          over += MIN_P ? above.total() : w;
-          all = above = Sum();
-        }
-        done_round = 0;
-        done += kWarps;
-      }
+    } else if (!MIN_P || ex >= row.min_p) {
+      acc.add(w);
     }
   }
-  if (CUT && lane == 0) {
-    atomicAdd(reinterpret_cast<unsigned long long*>(&s.sum_total), static_cast<unsigned long long>(total));
-    atomicAdd(reinterpret_cast<unsigned long long*>(&s.sum_above), static_cast<unsigned long long>(over));
+}
+
+// Adds up this slice's weights: sum_total all of them, sum_above those from x_lo
+// on, seg_weight[] the latter (at least min_p) by segments. Warp w has segments
+// w, w + 32, ..., each a few rounds of 32 vectors; four vectors' loads per lane
+// are in flight.
+template <typename T, bool MULTI, bool CUT, bool MIN_P>
+__device__ void sum_segments(const Row<T>& row, Shared& s, float x_lo, float x_hi) {
+  constexpr int E = Row<T>::E;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per = Row<T>::segment_vecs(row.vecs);  // vectors per segment
+  const int segs = (row.vecs + per - 1) / per;
+  for (int i = threadIdx.x; i < kSegments; i += kThreads)
+    if (i >= segs) s.seg_weight[i] = 0;
+  Sum all, above;
+  uint64_t total = 0, over = 0;
+  for (int seg = warp; seg < segs; seg += kWarps) {
+    Sum acc;
+    const int v0 = seg * per, v1 = min(v0 + per, row.vecs);
+    int base = v0;
+    if (row.aligned) {
+      const T* q = row.data + (v0 + lane) * E;
+      for (; base + 128 <= v1 && (row.padded || (base + 128) * E <= row.n); base += 128, q += 128 * E) {
+        Raw<T, E> raw[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) raw[j] = load_raw<T, E>(q + j * 32 * E);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          sum_vector<T, MULTI, CUT, MIN_P>(row, s, raw[j], base + j * 32 + lane, x_lo, x_hi, acc, all, above);
+      }
+    }
+#pragma unroll 2
+    for (int v = base + lane; v < v1; v += 32)
+      sum_vector<T, MULTI, CUT, MIN_P>(row, s, row.get(v), v, x_lo, x_hi, acc, all, above);
+    const uint64_t w = acc.total();
+    if (lane == 0) s.seg_weight[seg] = w;
+    if (!MIN_P) over += w;
+    if (CUT && (per >= 1024 || seg + kWarps >= segs)) {  // a long row's sums would overflow their halves
+      total += all.total();
+      if (MIN_P) over += above.total();
+      all = above = Sum();
+    }
+  }
+  if (CUT) {
+    if (lane == 0) {
+      atomicAdd(reinterpret_cast<unsigned long long*>(&s.sum_total), static_cast<unsigned long long>(total));
+      atomicAdd(reinterpret_cast<unsigned long long*>(&s.sum_above), static_cast<unsigned long long>(over));
+    }
   }
 }
 
@@ -953,7 +970,7 @@ __device__ void sum_segments(const Row<T>& row, Shared& s, float cut_lo, float c
 // Returns false if the exact sums do not confirm that the prefix ends in the list.
 template <typename T, bool MULTI>
 __device__ bool segment_answer(const Row<T>& row, Shared& s, const SampleParams& p, int64_t r, int slice, float top_p,
-                               float u, bool cut, float cut_lo, float cut_hi) {
+                               float u, bool cut, float x_lo, float x_hi) {
   constexpr int E = Row<T>::E;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int vocab = static_cast<int>(p.vocab);
@@ -968,10 +985,10 @@ __device__ bool segment_answer(const Row<T>& row, Shared& s, const SampleParams&
     n = static_cast<int>(min(s.listed[0], static_cast<uint32_t>(kListKeys)));
     const uint64_t goal = by_one(s, [&] { return top_p_goal(top_p, total); });
     if (s.listed[0] > static_cast<uint32_t>(kListKeys) || above >= goal) return false;
-    uint64_t sum = 0;
-    for (int i = threadIdx.x; i < n; i += kThreads) sum += row.weight(entry_value(s.list[i]));
-    if (above + block_total(s, sum) < goal) return false;
-    cut_entry = list_reach<T, true>(row, s, n, above, goal);
+    // entries of the list lie from x_hi to below x_lo
+    cut_entry = list_reach<T, true>(row, s, n, static_cast<uint64_t>(~(order_key(x_lo) - 1u)) << 32,
+                                    static_cast<uint64_t>(~order_key(x_hi)) << 32 | 0xFFFFFFFFu, above, goal);
+    if (cut_entry == ~0ull) return false;
     __syncthreads();  // the histogram's place is used again
   }
   // the segments of all slices, two per thread
@@ -1031,23 +1048,27 @@ __device__ bool segment_answer(const Row<T>& row, Shared& s, const SampleParams&
   const int sub = Row<T>::segment_vecs(part.vecs);
   const int v1 = min((seg + 1) * sub, part.vecs);
   uint64_t run = s.found_above;
-  for (int base = seg * sub; base < v1; base += 32) {
+  Raw<T, E> ahead[4];
+  for (int base = seg * sub, k = 0; base < v1; base += 32, ++k) {
     const int v = base + lane;
+    if ((k & 3) == 0) {  // four rounds' loads at once
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (v + 32 * j < v1) ahead[j] = part.get(v + 32 * j);
+    }
     float x[E];
     uint64_t w[E], sum = 0;
 #pragma unroll
     for (int e = 0; e < E; ++e) w[e] = 0;
     if (v < v1) {
-      unpack<T, E>(part.get(v), x);
+      unpack<T, E>((k & 3) == 0 ? ahead[0] : (k & 3) == 1 ? ahead[1] : (k & 3) == 2 ? ahead[2] : ahead[3], x);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const float ex = part.exponential(x[e]);
         bool keep = ex >= part.min_p;
-        if (cut) {
-          const float place = part.place(x[e]);
-          keep = keep && place < cut_hi &&
-                 (place < cut_lo || list_entry(x[e], static_cast<uint32_t>(part.c0 + v * E + e)) <= cut_entry);
-        }
+        if (cut)
+          keep = keep && x[e] >= x_hi &&
+                 (x[e] >= x_lo || list_entry(x[e], static_cast<uint32_t>(part.c0 + v * E + e)) <= cut_entry);
         w[e] = keep ? Row<T>::fixed(ex) : 0;
         sum += w[e];
       }
@@ -1098,7 +1119,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, 
   const float u = p.u[r];
   row.min_p = p.min_ps ? p.min_ps[r] : p.min_p;
   row.inv = 1.f / temperature;
-  row.per_bin = fminf(row.inv * kCountsPerUnit, 3e38f);
+  row.per_place = fminf(row.inv * (1.f / kPlaces), 3e38f);
   bool bad = temperature != temperature || top_p != top_p || row.min_p != row.min_p || u != u;
   const bool greedy = !(temperature > 0.f) || row.inv == INFINITY || top_k == 1 || top_p <= 0.f || row.min_p > 1.f;
   const bool need_k = top_k > 0 && top_k < p.vocab;
@@ -1125,8 +1146,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, 
     unpack<T, E>(raw, x);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const int b = Row<T>::count_bin(row.place(x[e]));
-      atomicAdd(&s.counts.count[b], 1u);
+      const int b = row.count_bin(x[e]);
+      if (b < kCountBins - 1) atomicAdd(&s.counts.count[b], 1u);  // the last bin's are not needed
       if (b < kWeighedBins) atomicAdd(&s.counts.weight[b], expf(fminf((x[e] - row.anchor) * row.inv, 60.f)));
     }
   };
@@ -1227,13 +1248,13 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, 
 
   // ---- where the prefix ends, by the counts
   bool general = false, listing = false;
-  float cut_lo = INFINITY, cut_hi = INFINITY;
+  int cut_lo = 0, cut_hi = 0;  // bins to collect: from cut_lo on, before cut_hi
   if (need_counts) {
     if constexpr (MULTI) {
       row.anchor = row.top;
       row.each([&](float x, uint32_t) {
-        const int b = Row<T>::count_bin(row.place(x));
-        atomicAdd(&s.counts.count[b], 1u);
+        const int b = row.count_bin(x);
+        if (b < kCountBins - 1) atomicAdd(&s.counts.count[b], 1u);
         if (b < kWeighedBins) atomicAdd(&s.counts.weight[b], expf((x - row.anchor) * row.inv));
       });
       __syncthreads();
@@ -1248,26 +1269,26 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, 
       row_barrier<MULTI>();
     }
     if (row.rank == 0) {
-      uint32_t n[2];
-      float w[2];
+      uint32_t n[kBinsPerThread], n_sum = 0;
+      float w[kBinsPerThread], w_sum = 0.f;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int b = 2 * threadIdx.x + j;
+      for (int j = 0; j < kBinsPerThread; ++j) {
+        const int b = kBinsPerThread * threadIdx.x + j;
         n[j] = s.counts.count[b];
-        w[j] = b < kWeighedBins ? s.counts.weight[b]
-                                : b < kCountBins - 1 ? n[j] * expf((kAnchorBin - b - 0.5f) * (1.f / kCountsPerUnit)) : 0.f;
+        w[j] = b < kWeighedBins ? s.counts.weight[b] : n[j] ? n[j] * expf(kAbove - (b + 0.5f) * kUnitsPerBin) : 0.f;
+        n_sum += n[j];
+        w_sum += w[j];
       }
-      uint64_t all;
-      uint64_t count_before = block_exclusive(static_cast<uint64_t>(n[0] + n[1]), s.scan, &all);
-      float whole;
-      float weight_before = block_exclusive(w[0] + w[1], s.fscan, &whole);
+      uint32_t count_before;
+      float weight_before, whole;
+      block_exclusive(s, n_sum, w_sum, &count_before, &weight_before, &whole);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint32_t b = 2 * threadIdx.x + j;
-        const uint64_t upto = count_before + n[j];
+      for (int j = 0; j < kBinsPerThread; ++j) {
+        const uint32_t b = kBinsPerThread * threadIdx.x + j;
+        const uint32_t upto = count_before + n[j];
         const unsigned long long bin = static_cast<unsigned long long>(b) << 32;
         if (b == kCountBins - 1) {
-          s.found_count = static_cast<uint32_t>(count_before);  // logits in all bins but the last
+          s.found_count = count_before;  // logits in all bins but the last, which is not counted
         } else if (need_k) {
           const uint64_t k = static_cast<uint64_t>(top_k);
           if (count_before < k && k <= upto) s.cut_hi[0] = bin | upto;
@@ -1297,27 +1318,38 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, 
         if (need_k || !general) break;
       }
       general |= !(whole < INFINITY);
-      cut_lo = from >> 32 == 0 ? -INFINITY : static_cast<float>(from >> 32);
-      cut_hi = static_cast<float>((to >> 32) + 1);
+      cut_lo = static_cast<int>(from >> 32);
+      cut_hi = static_cast<int>(to >> 32) + 1;
       if (MULTI && threadIdx.x == 0) {
         s.told[0] = cut_lo;
         s.told[1] = cut_hi;
-        s.told[2] = general ? 1.f : 0.f;
+        s.told[2] = general;
       }
     }
     if constexpr (MULTI) {
       row_barrier<MULTI>();
       cut_lo = remote<MULTI>(&s.told[0], 0);
       cut_hi = remote<MULTI>(&s.told[1], 0);
-      general = remote<MULTI>(&s.told[2], 0) != 0.f;
+      general = remote<MULTI>(&s.told[2], 0) != 0;
     }
     listing = need_k && !general;
+  }
+  // the same as logits: above the collected bins from x_lo on, in them from x_hi on
+  float x_lo = INFINITY, x_hi = INFINITY;
+  if (need_counts && !general) {
+    if (warp < 2) {
+      const float x = (warp == 0 ? cut_lo : cut_hi) > 0 ? row.first_before(warp == 0 ? cut_lo : cut_hi) : INFINITY;
+      if (lane == 0) s.cut_x[warp] = x;
+    }
+    __syncthreads();
+    x_lo = s.cut_x[0];
+    x_hi = s.cut_x[1];
   }
 
   // ---- second pass
   if (listing) {
     row.each([&](float x, uint32_t i) {
-      if (row.place(x) < cut_hi) append<MULTI>(s, &s.listed[0], list_entry(x, i));
+      if (x >= x_hi) append<MULTI>(s, &s.listed[0], list_entry(x, i));
     });
     row_barrier<MULTI>();
     if (row.rank == 0) {
@@ -1325,22 +1357,22 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, 
       if (n <= kShort)
         short_list_answer(row, s, p, r, n, top_k, top_p, u);
       else
-        list_answer(row, s, p, r, n, top_k, top_p, u);
+        list_answer(row, s, p, r, n, top_k, top_p, u, x_hi);
     }
     return;  // nothing of the other CTAs is read any more
   }
   if (!general) {
     const bool cut = need_counts, min_p = row.min_p > 0.f;
     if (cut && min_p)
-      sum_segments<T, MULTI, true, true>(row, s, cut_lo, cut_hi);
+      sum_segments<T, MULTI, true, true>(row, s, x_lo, x_hi);
     else if (cut)
-      sum_segments<T, MULTI, true, false>(row, s, cut_lo, cut_hi);
+      sum_segments<T, MULTI, true, false>(row, s, x_lo, x_hi);
     else if (min_p)
-      sum_segments<T, MULTI, false, true>(row, s, cut_lo, cut_hi);
+      sum_segments<T, MULTI, false, true>(row, s, x_lo, x_hi);
     else
-      sum_segments<T, MULTI, false, false>(row, s, cut_lo, cut_hi);
+      sum_segments<T, MULTI, false, false>(row, s, x_lo, x_hi);
     row_barrier<MULTI>();
-    if (row.rank == 0 && !segment_answer<T, MULTI>(row, s, p, r, slice, top_p, u, cut, cut_lo, cut_hi) &&
+    if (row.rank == 0 && !segment_answer<T, MULTI>(row, s, p, r, slice, top_p, u, cut, x_lo, x_hi) &&
         threadIdx.x == 0)
       s.general = 1;
     row_barrier<MULTI>();
