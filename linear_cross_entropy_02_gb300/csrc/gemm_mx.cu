@@ -22,6 +22,8 @@
 //
 // For a few tokens A stays in shared memory, all of its K with its scales, if it
 // leaves room for the ring: re-reading it for every tile of W cost 10 us of 82.
+// Up to kMostFused elements are encoded by every CTA for itself, straight into
+// the swizzled tiles, while the first copies of W are on their way: a launch less.
 //
 // Warp 0 loads, warp 1 issues the MMAs, warps 2-5 store, warps 6-9 carry scales:
 // two accumulators, so that the stores of one tile run under the MMAs of the
@@ -36,6 +38,7 @@
 #include "flce_host.h"
 #include "head_device.cuh"
 #include "head_internal.h"
+#include "microscale_device.cuh"
 
 namespace flce {
 
@@ -48,6 +51,7 @@ constexpr int kWBytes = kTileV * kRowBytes;
 constexpr int kSfTiles = kStageK / kMxTileCols;  // scale tiles per 128 rows and stage
 constexpr int kThreads = 320;
 constexpr int kSmemBudget = 226 * 1024;
+constexpr int64_t kMostFused = 40960;  // 4 tokens of 7168: 83.0 us so, 83.8 with a launch before; 8: 86.9 and 85
 
 // Shared and tensor memory of a tile of NT tokens. RESIDENT: A's codes and scales
 // stay in shared memory in front of the ring, which then holds W alone.
@@ -82,6 +86,9 @@ struct MxArgs {
   const uint8_t* x_scales;
   int rows, vocab, k_iters, k_tiles, k_mmas;  // k_mmas: instructions over all of K
   int x_row_tiles;
+  const void* x;  // FUSED: the tokens as they are
+  int x_f32, cols;
+  int64_t ld_x;
   int v_tiles, n_tiles, stages;
   float out_mult, softcap, inv_softcap;
   void* out;
@@ -140,10 +147,49 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
-template <int NT, bool RESIDENT, typename T>
+// The tokens' codes and scales by warps 2 to 9, at the places that TMA with
+// 128-byte swizzle would give them (16-byte piece c of a row is at c ^ (row & 7))
+// and in the order of a scale tile. The last instruction's K is filled up with
+// zeros; rows beyond the tokens are left as they are: their results are not stored.
+template <int NT, typename T>
+__device__ __forceinline__ void encode_tokens(const MxArgs& p, uint8_t* s_x, uint8_t* s_xsf) {
+  using P = Plan<NT, true>;
+  constexpr int kLanes = kThreads - 64;
+  const int per_row = p.k_mmas * (64 / kUnit), real = p.cols / kUnit, total = p.rows * per_row;
+  const bool wide = reinterpret_cast<uintptr_t>(p.x) % 32 == 0 && p.ld_x * sizeof(T) % 32 == 0;
+  constexpr int kAhead = 4;  // units per lane whose loads are in flight together
+  for (int base = 0; base < total; base += kAhead * kLanes) {
+    uint32_t raw[kAhead][4 * sizeof(T)];
+    int row[kAhead], u[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = base + k * kLanes + threadIdx.x - 64;
+      row[k] = i / per_row;
+      u[k] = i < total ? i - row[k] * per_row : -1;
+      if (u[k] >= 0 && u[k] < real) load16<T>(static_cast<const T*>(p.x) + row[k] * p.ld_x + u[k] * kUnit, wide, raw[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const bool in = u[k] >= 0 && u[k] < real;
+      uint32_t E = in ? exponent16(raw[k]) : 0;
+      E = max(E, __shfl_xor_sync(0xffffffffu, E, 1));  // the other half of the block
+      if (u[k] >= 0) {
+        const int slice = u[k] / 16, piece = u[k] % 16 / 2;
+        uint8_t* to = s_x + slice * P::x_bytes + row[k] * kRowBytes + ((piece ^ (row[k] & 7)) << 4) + (u[k] & 1) * 8;
+        *reinterpret_cast<uint2*>(to) = in ? encode16(raw[k], E) : make_uint2(0u, 0u);
+        if ((u[k] & 1) == 0)
+          s_xsf[u[k] / 8 * kMxTileBytes + row[k] % 32 * 16 + row[k] / 32 * 4 + (u[k] / 2 & 3)] =
+              static_cast<uint8_t>(in ? scale_byte(E) : 127u);
+      }
+    }
+  }
+}
+
+template <int NT, bool RESIDENT, bool FUSED, typename T>
 __global__ void __launch_bounds__(kThreads, 1)
     mx_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                    const MxArgs p) {
+  static_assert(RESIDENT || !FUSED, "encoded tokens stay in shared memory");
   using P = Plan<NT, RESIDENT>;
   const int S = p.stages;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -164,6 +210,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  // (the first wait can run out seconds after this, and all CTAs run at once)
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&full[s], 1);
@@ -175,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&tempty[b], 128);
     }
     mbar_init(mma_done, 1);
-    mbar_init(x_full, 1);
+    mbar_init(x_full, FUSED ? 8 : 1);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&map_w);
@@ -192,11 +240,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   const WaitCtx wc{abort_flag, p.status, p.timeout_ns};
   const int total = p.v_tiles * p.n_tiles;
 
+  if (FUSED && warp >= 2) {
+    if (p.x_f32)
+      encode_tokens<NT, float>(p, s_x, s_xsf);
+    else
+      encode_tokens<NT, uint16_t>(p, s_x, s_xsf);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(x_full);
+  }
+
   if (warp == 0) {
     int stage = 0, issued = 0;
     uint32_t phase = 0;
     bool aborted = false;
-    if (RESIDENT && elect_one()) {  // one tile of tokens, whose scales are one row of tiles
+    if (RESIDENT && !FUSED && elect_one()) {  // one tile of tokens, whose scales are one row of tiles
       mbar_arrive_expect_tx(x_full, p.k_iters * P::x_bytes + p.k_tiles * kMxTileBytes);
       for (int k = 0; k < p.k_iters; ++k) tma_load_2d(s_x + k * P::x_bytes, &map_x, x_full, k * kRowBytes, 0);
       bulk_load(s_xsf, p.x_scales, static_cast<uint32_t>(p.k_tiles) * kMxTileBytes, x_full);
@@ -235,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (aborted && lane == 0) {
       // loads that may still be in flight land before the shared memory goes away
-      if (RESIDENT) wait_drain(x_full, 0, p.timeout_ns, p.status);
+      if (RESIDENT && !FUSED) wait_drain(x_full, 0, p.timeout_ns, p.status);
       const int n = issued < S ? issued : S;
       int s = stage;
       uint32_t ph = phase;
@@ -380,10 +438,10 @@ bool encode_codes(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, 
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int NT, bool RESIDENT, typename T>
+template <int NT, bool RESIDENT, bool FUSED, typename T>
 int run_tile(const MxGemmParams& p, int sms, cudaStream_t stream) {
   using P = Plan<NT, RESIDENT>;
-  auto kernel = mx_gemm_kernel<NT, RESIDENT, T>;
+  auto kernel = mx_gemm_kernel<NT, RESIDENT, FUSED, T>;
   static std::atomic<uint64_t> done{0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return FLCE_ERR_CUDA;
@@ -393,11 +451,18 @@ int run_tile(const MxGemmParams& p, int sms, cudaStream_t stream) {
     done.fetch_or(1ull << dev);
   }
   CUtensorMap map_w, map_x;
-  if (!encode_codes(&map_w, p.w_codes, p.vocab, p.cols, kTileV) || !encode_codes(&map_x, p.a_codes, p.rows, p.cols, NT))
+  if (!encode_codes(&map_w, p.w_codes, p.vocab, p.cols, kTileV)) return FLCE_ERR_UNSUPPORTED;
+  if (FUSED)
+    map_x = map_w;  // not used
+  else if (!encode_codes(&map_x, p.a_codes, p.rows, p.cols, NT))
     return FLCE_ERR_UNSUPPORTED;
   MxArgs a;
   a.w_scales = p.w_scales;
   a.x_scales = p.a_scales;
+  a.x = p.x;
+  a.x_f32 = p.x_dtype == FLCE_DTYPE_F32;
+  a.cols = static_cast<int>(p.cols);
+  a.ld_x = p.ld_x;
   a.rows = static_cast<int>(p.rows);
   a.vocab = static_cast<int>(p.vocab);
   a.k_iters = static_cast<int>((p.cols + kStageK - 1) / kStageK);
@@ -426,11 +491,16 @@ int run_tile(const MxGemmParams& p, int sms, cudaStream_t stream) {
 }
 
 // One tile of tokens, with A resident if it fits beside a ring of four stages.
+template <int NT>
+bool resident(int64_t cols) {
+  return Plan<NT, true>::stages(static_cast<int>((cols + kStageK - 1) / kStageK)) > 0;
+}
 template <int NT, typename T>
 int run_few(const MxGemmParams& p, int sms, cudaStream_t s) {
-  const int k_iters = static_cast<int>((p.cols + kStageK - 1) / kStageK);
-  if (Plan<NT, true>::stages(k_iters) > 0) return run_tile<NT, true, T>(p, sms, s);
-  return run_tile<NT, false, T>(p, sms, s);
+  if constexpr (NT <= 64)
+    if (p.x) return run_tile<NT, true, true, T>(p, sms, s);
+  if (resident<NT>(p.cols)) return run_tile<NT, true, false, T>(p, sms, s);
+  return run_tile<NT, false, false, T>(p, sms, s);
 }
 
 template <typename T>
@@ -439,10 +509,15 @@ int run_typed(const MxGemmParams& p, int sms, cudaStream_t s) {
   if (p.rows <= 32) return run_few<32, T>(p, sms, s);
   if (p.rows <= 64) return run_few<64, T>(p, sms, s);
   if (p.rows <= 128) return run_few<128, T>(p, sms, s);
-  return run_tile<192, false, T>(p, sms, s);
+  return run_tile<192, false, false, T>(p, sms, s);
 }
 
 }  // namespace
+
+bool mx_gemm_encodes(int64_t rows, int64_t cols) {
+  if (rows > 64 || rows * cols > kMostFused) return false;
+  return rows <= 16 ? resident<16>(cols) : rows <= 32 ? resident<32>(cols) : resident<64>(cols);
+}
 
 int launch_mx_gemm(const MxGemmParams& p, int sms, cudaStream_t s) {
   if (!load_encoder()) return FLCE_ERR_UNSUPPORTED;

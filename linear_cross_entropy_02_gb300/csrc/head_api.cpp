@@ -60,7 +60,7 @@ int check_product(int64_t rows, int64_t vocab, int64_t cols, const void* w_codes
 MxGemmParams product(int64_t rows, int64_t vocab, int64_t cols, const void* a_codes, const void* a_scales,
                      const void* w_codes, const void* w_scales, float out_mult, float softcap, void* out,
                      int out_dtype, int64_t ld_out, void* workspace) {
-  MxGemmParams g;
+  MxGemmParams g = {};
   g.a_codes = static_cast<const uint8_t*>(a_codes);
   g.a_scales = static_cast<const uint8_t*>(a_scales);
   g.w_codes = static_cast<const uint8_t*>(w_codes);
@@ -193,7 +193,7 @@ int flce_microscale_quantize(const void* x, int dtype, int64_t rows, int64_t col
   int sms = 0;
   if ((rc = device_check(&sms)) != FLCE_OK) return rc;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_handle);
-  MxQuantParams q = {x, dtype, rows, cols, ld_x, static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales), nullptr};
+  MxQuantParams q = {x, dtype, rows, cols, ld_x, static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales)};
   FLCE_LAUNCH(K_MX_QUANT, launch_mx_quantize(q, sms, stream));
   return FLCE_OK;
 }
@@ -231,7 +231,6 @@ int flce_microscale_matmul(const void* a_codes, const void* a_scales, int64_t ro
   int sms = 0;
   if ((rc = device_check(&sms)) != FLCE_OK) return rc;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_handle);
-  if (cudaMemsetAsync(workspace, 0, sizeof(int32_t), stream) != cudaSuccess) return FLCE_ERR_CUDA;
   return launch_mx_gemm(product(rows, vocab, cols, a_codes, a_scales, w_codes, w_scales, out_mult, softcap, out,
                                 out_dtype, ld_out, workspace),
                         sms, stream);
@@ -253,11 +252,17 @@ int flce_microscale_linear(const void* x, int dtype, int64_t ld_x, int64_t rows,
   cudaStream_t stream = static_cast<cudaStream_t>(stream_handle);
   uint8_t* codes = static_cast<uint8_t*>(workspace) + kHeaderBytes;
   uint8_t* scales = codes + round256(mx_codes(rows, cols));
-  MxQuantParams q = {x, dtype, rows, cols, ld_x, codes, scales, &static_cast<Header*>(workspace)->status};
-  FLCE_LAUNCH(K_MX_QUANT, launch_mx_quantize(q, sms, stream));
-  return launch_mx_gemm(product(rows, vocab, cols, codes, scales, w_codes, w_scales, out_mult, softcap, out, out_dtype,
-                                ld_out, workspace),
-                        sms, stream);
+  MxGemmParams g = product(rows, vocab, cols, codes, scales, w_codes, w_scales, out_mult, softcap, out, out_dtype, ld_out,
+                           workspace);
+  if (mx_gemm_encodes(rows, cols)) {
+    g.x = x;
+    g.x_dtype = dtype;
+    g.ld_x = ld_x;
+  } else {
+    MxQuantParams q = {x, dtype, rows, cols, ld_x, codes, scales};
+    FLCE_LAUNCH(K_MX_QUANT, launch_mx_quantize(q, sms, stream));
+  }
+  return launch_mx_gemm(g, sms, stream);
 }
 
 int flce_sample(const void* logits, int logits_dtype, int64_t rows, int64_t vocab, int64_t ld_logits, const float* u,

@@ -58,13 +58,15 @@ struct MxQuantParams {
   int64_t rows, cols, ld_x;
   uint8_t* codes;
   uint8_t* scales;
-  int32_t* status;  // zeroed by the kernel when not null (a following product's status word)
 };
 cudaError_t launch_mx_quantize(const MxQuantParams& p, int sms, cudaStream_t s);
 cudaError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, void* out,
                                  int out_dtype, cudaStream_t s);
 
 struct MxGemmParams {
+  const void* x;  // tokens that the kernel encodes itself (then a_codes, a_scales are not used), or null
+  int x_dtype;
+  int64_t ld_x;
   const uint8_t* a_codes;
   const uint8_t* a_scales;
   const uint8_t* w_codes;
@@ -77,7 +79,9 @@ struct MxGemmParams {
   int32_t* status;
   uint64_t timeout_ns;
 };
-// FLCE_* code: the tensor maps are encoded here.
+// Whether launch_mx_gemm takes tokens of this shape as x.
+bool mx_gemm_encodes(int64_t rows, int64_t cols);
+// FLCE_* code: the tensor maps are encoded here. Sets *status to 0 first.
 int launch_mx_gemm(const MxGemmParams& p, int sms, cudaStream_t s);
 
 // ------------------------------------------------------------ sampling

@@ -109,6 +109,12 @@ __device__ __forceinline__ void norm_row(const NormParams& p, const T* x, T* y, 
 #pragma unroll
   for (int c = 0; c < C; ++c)
     if (t + c * stride < vecs) cur[c] = load_raw<T, E>(x + (t + c * stride) * E);
+  // one vector per thread: its weight is on its way before the row's sums
+  float w0[E], b0[E];
+  if (C == 1 && t < vecs) {
+    if (p.weight) load_weight<E>(p.weight, p.w_f32 != 0, t * E, w0);
+    if (p.bias) load_weight<E>(p.bias, p.w_f32 != 0, t * E, b0);
+  }
   const float inv_h = 1.f / static_cast<float>(static_cast<int>(p.hidden));
   float mean = 0.f, rest = 0.f, sq = 0.f;
   if (!p.rms) {
@@ -166,14 +172,14 @@ __device__ __forceinline__ void norm_row(const NormParams& p, const T* x, T* y, 
 #pragma unroll
       for (int e = 0; e < E; ++e) v[e] = (v[e] - mean - rest) * rstd;
       if (p.weight) {
-        load_weight<E>(p.weight, p.w_f32 != 0, i, w);
+        if (C > 1) load_weight<E>(p.weight, p.w_f32 != 0, i, w);
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[e] *= w[e];
+        for (int e = 0; e < E; ++e) v[e] *= C > 1 ? w[e] : w0[e];
       }
       if (p.bias) {
-        load_weight<E>(p.bias, p.w_f32 != 0, i, w);
+        if (C > 1) load_weight<E>(p.bias, p.w_f32 != 0, i, w);
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[e] += w[e];
+        for (int e = 0; e < E; ++e) v[e] += C > 1 ? w[e] : b0[e];
       }
       store_raw<T, E>(y + i, pack<T, E>(v));
     }
@@ -636,7 +642,8 @@ cudaError_t run_fwd(const NormParams& p, int sms, cudaStream_t s) {
     return cudaGetLastError();
   }
   if (vecs <= static_cast<int64_t>(kMaxThreads) * kMaxVecs) {
-    int most = 128;
+    // few rows: a thread per vector, for the shortest chain of loads
+    int most = p.rows < 2LL * sms ? kMaxThreads : 128;
     while (most * kMaxVecs < vecs) most *= 2;
     const int c = static_cast<int>((vecs + most - 1) / most);
     const int threads = static_cast<int>(((vecs + c - 1) / c + 31) / 32 * 32);
