@@ -57,14 +57,13 @@ constexpr int64_t kMostFused = 40960;  // 4 tokens of 7168: 83.0 us so, 83.8 wit
 // stay in shared memory in front of the ring, which then holds W alone.
 template <int NT, bool RESIDENT>
 struct Plan {
-  static constexpr int row_tiles = (NT + 127) / 128;  // 128-row scale tiles that the tokens can touch
   static constexpr int x_bytes = NT * kRowBytes;
   static constexpr int w_sf = kSfTiles * kMxTileBytes;
-  static constexpr int x_sf = row_tiles * kSfTiles * kMxTileBytes;
+  static constexpr int x_sf = kSfTiles * kMxTileBytes;
   static constexpr int x_all = x_bytes + x_sf;  // of one stage's K
   static constexpr int stage = kWBytes + w_sf + (RESIDENT ? 0 : x_all);
   static constexpr int d_cols = NT < 32 ? 32 : NT;      // one accumulator
-  static constexpr int sf_cols = 4 * kSfTiles * (1 + row_tiles);
+  static constexpr int sf_cols = 2 * 4 * kSfTiles;
   static constexpr int by_tmem = (512 - 2 * d_cols) / sf_cols;
   static constexpr int most = by_tmem < 10 ? by_tmem : 10;
   // Stages of the ring when k_iters stages' worth of A is resident (0: they do not fit).
@@ -85,11 +84,10 @@ struct MxArgs {
   const uint8_t* w_scales;
   const uint8_t* x_scales;
   int rows, vocab, k_iters, k_tiles, k_mmas;  // k_mmas: instructions over all of K
-  int x_row_tiles;
   const void* x;  // FUSED: the tokens as they are
   int x_f32, cols;
   int64_t ld_x;
-  int v_tiles, n_tiles, stages;
+  int v_tiles, stages;
   float out_mult, softcap, inv_softcap;
   void* out;
   int64_t ld_out;
@@ -138,6 +136,12 @@ __device__ __forceinline__ bool elect_one() {
 // wait_bounded by a whole warp, which then agrees on the outcome.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtx& w) {
   return __all_sync(0xffffffffu, wait_bounded(bar, parity, w));
+}
+
+// A sum of the accumulator as the logit that leaves the kernel.
+__device__ __forceinline__ float finish(const MxArgs& p, uint32_t sum) {
+  const float z = __uint_as_float(sum) * p.out_mult;
+  return p.softcap > 0.f ? p.softcap * tanhf(z * p.inv_softcap) : z;
 }
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -238,8 +242,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   const WaitCtx wc{abort_flag, p.status, p.timeout_ns};
-  const int total = p.v_tiles * p.n_tiles;
-
   if (FUSED && warp >= 2) {
     if (p.x_f32)
       encode_tokens<NT, float>(p, s_x, s_xsf);
@@ -260,10 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bulk_load(s_xsf, p.x_scales, static_cast<uint32_t>(p.k_tiles) * kMxTileBytes, x_full);
     }
     __syncwarp();
-    for (int t = blockIdx.x; t < total && !aborted; t += gridDim.x) {
-      const int vb = t / p.n_tiles, nb = t - vb * p.n_tiles;  // a tile of W meets all tokens while it is in the L2
-      const int xt0 = nb * NT / 128;
-      const int xts = min(P::row_tiles, p.x_row_tiles - xt0);
+    for (int vb = blockIdx.x; vb < p.v_tiles && !aborted; vb += gridDim.x) {
       for (int k = 0; k < p.k_iters; ++k) {
         if (!warp_wait(&empty[stage], phase ^ 1u, wc)) {
           aborted = true;
@@ -272,15 +271,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) {
           const int kt = k * kSfTiles;
           const uint32_t sf = static_cast<uint32_t>(min(kSfTiles, p.k_tiles - kt)) * kMxTileBytes;
-          mbar_arrive_expect_tx(&full[stage], kWBytes + sf + (RESIDENT ? 0 : P::x_bytes + sf * xts));
+          mbar_arrive_expect_tx(&full[stage], kWBytes + sf + (RESIDENT ? 0 : P::x_bytes + sf));
           tma_load_2d(s_w + stage * kWBytes, &map_w, &full[stage], k * kRowBytes, vb * kTileV);
           bulk_load(s_wsf + stage * P::w_sf, p.w_scales + (static_cast<int64_t>(vb) * p.k_tiles + kt) * kMxTileBytes,
                     sf, &full[stage]);
           if (!RESIDENT) {
-            tma_load_2d(s_x + stage * P::x_bytes, &map_x, &full[stage], k * kRowBytes, nb * NT);
-            for (int i = 0; i < xts; ++i)
-              bulk_load(s_xsf + stage * P::x_sf + i * kSfTiles * kMxTileBytes,
-                        p.x_scales + (static_cast<int64_t>(xt0 + i) * p.k_tiles + kt) * kMxTileBytes, sf, &full[stage]);
+            tma_load_2d(s_x + stage * P::x_bytes, &map_x, &full[stage], k * kRowBytes, 0);
+            bulk_load(s_xsf + stage * P::x_sf, p.x_scales + kt * kMxTileBytes, sf, &full[stage]);
           }
         }
         __syncwarp();
@@ -312,9 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t phase = 0, acc_phase = 0;
     const uint32_t w0 = smem_u32(s_w), x0 = smem_u32(s_x);
     bool aborted = RESIDENT && !warp_wait(x_full, 0, wc);
-    for (int t = blockIdx.x; t < total && !aborted; t += gridDim.x) {
-      const int nb = t % p.n_tiles;
-      const uint32_t x_shift = static_cast<uint32_t>(nb * NT % 128 / 32);  // first 32-row group of the tokens
+    for (int vb = blockIdx.x; vb < p.v_tiles && !aborted; vb += gridDim.x) {
       if (!warp_wait(&tempty[acc], acc_phase ^ 1u, wc)) break;
       tc_fence_after_sync();
       const uint32_t d = tmem + static_cast<uint32_t>(acc * P::d_cols);
@@ -326,14 +321,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after_sync();
         if (elect_one()) {
           const uint32_t sf = tmem + static_cast<uint32_t>(2 * P::d_cols + stage * P::sf_cols);
-          const uint32_t sfx = sf + 4 * kSfTiles + x_shift;
+          const uint32_t sfx = sf + 4 * kSfTiles;
           const uint32_t a0 = w0 + stage * kWBytes, b0 = x0 + (RESIDENT ? k : stage) * P::x_bytes;
           const int mmas = p.k_mmas - k * (kStageK / 64);
 #pragma unroll
           for (int j = 0; j < kStageK / 64; ++j)
             if (j < mmas)
               mma_mxf4(d, sdesc_kmajor_sw128(a0 + j * 32), sdesc_kmajor_sw128(b0 + j * 32),
-                       idesc_mxf4(kTileV, NT, (j & 1) * 2), sf + 4 * (j >> 1), sfx + 4 * (j >> 1) * P::row_tiles,
+                       idesc_mxf4(kTileV, NT, (j & 1) * 2), sf + 4 * (j >> 1), sfx + 4 * (j >> 1),
                        (k | j) != 0 ? 1u : 0u);
           tc_commit(&empty[stage]);
           if (k == p.k_iters - 1) tc_commit(&tfull[acc]);
@@ -359,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int stage = 0;
     uint32_t phase = 0;
     bool ok = !RESIDENT || wait_bounded(x_full, 0, wc);
-    for (int t = blockIdx.x; t < total && __all_sync(0xffffffffu, ok); t += gridDim.x) {
+    for (int vb = blockIdx.x; vb < p.v_tiles && __all_sync(0xffffffffu, ok); vb += gridDim.x) {
       for (int k = 0; k < p.k_iters; ++k) {
         ok = wait_bounded(&full[stage], phase, wc);
         if (!__all_sync(0xffffffffu, ok)) break;
@@ -369,13 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (a last stage of one tile carries the stage before's bytes in the other's place: not used)
         store_scales2(sf, w, w + kMxTileBytes);
         const uint8_t* x = s_xsf + (RESIDENT ? k : stage) * P::x_sf + lane * 16;
-        if (P::row_tiles == 1) {
-          store_scales2(sf + 8, x, x + kMxTileBytes);
-        } else {
-          // columns by K-tile, rows in order within one
-          store_scales2(sf + 8, x, x + 2 * kMxTileBytes);
-          store_scales2(sf + 16, x + kMxTileBytes, x + 3 * kMxTileBytes);
-        }
+        store_scales2(sf + 8, x, x + kMxTileBytes);
         store_scales_wait();
         tc_fence_before_sync();
         __syncwarp();
@@ -391,26 +380,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int t = blockIdx.x; t < total; t += gridDim.x) {
-      const int vb = t / p.n_tiles, nb = t - vb * p.n_tiles;
+    for (int vb = blockIdx.x; vb < p.v_tiles; vb += gridDim.x) {
       const bool ok = wait_bounded(&tfull[acc], acc_phase, wc);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after_sync();
       const int v = vb * kTileV + quarter * 32 + lane;
-      const int n0 = nb * NT;
-      const int n_here = min(NT, p.rows - n0);
-      for (int c = 0; c < n_here; c += 32) {
+      for (int c = 0; c < p.rows; c += 32) {
         uint32_t r[32];
         tmem_load_32cols(t_lane + acc * P::d_cols + c, r);
         tmem_load_wait_regs(r);
-        T* o = static_cast<T*>(p.out) + static_cast<int64_t>(n0 + c) * p.ld_out + v;
+        T* o = static_cast<T*>(p.out) + static_cast<int64_t>(c) * p.ld_out + v;
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
-          if (c + j < n_here && v < p.vocab) {
-            float z = __uint_as_float(r[j]) * p.out_mult;
-            if (p.softcap > 0.f) z = p.softcap * tanhf(z * p.inv_softcap);
-            o[j * p.ld_out] = from_float<T>(z);
-          }
+          if (c + j < p.rows && v < p.vocab) o[j * p.ld_out] = from_float<T>(finish(p, r[j]));
         }
       }
       tc_fence_before_sync();
@@ -427,6 +409,360 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// More than 128 tokens: 256 x 256 tiles over a cluster of two CTAs on two SMs.
+// A single CTA's 128 x 192 tile draws 43 KB per K = 256 for 384 cycles of MMAs,
+// and an SM takes about 64 bytes a cycle from the L2: 4096 tokens on 128256 x 4096
+// took 1106 us, 786 of them with the MMAs left out. Here each CTA holds 128 rows
+// of M and 128 of N, 35 KB with the scales for 512 cycles. M = 256, N = 256 fill
+// half of tensor memory, so that the other half holds scales and the accumulator
+// is one: sixteen warps take it into registers at once and store from there, under
+// the next tile's MMAs.
+//
+// TOKENS_M: the tokens are M, a thread has 128 neighbouring logits of one token
+// and stores whole 32-byte sectors, for which rows of logits start on 32 bytes.
+// Else the vocabulary is M, and a warp's store is 32 neighbouring logits of one
+// token, at any alignment.
+//
+// Both CTAs' codes are counted by the leader's barriers, each CTA's scales by its
+// own; its scale warps then arrive at the leader's `scaled`. The leader's commits
+// go to both CTAs.
+constexpr int kPairThreads = 768;
+constexpr int kPairStages = 6;
+constexpr int kPairStageBytes = 2 * kWBytes + 3 * kSfTiles * kMxTileBytes;
+constexpr int kPairSfCols = 3 * 4 * kSfTiles;  // M's 128 rows and N's 256
+constexpr int kPairD = 256;
+constexpr int kPairSmem = kPairStages * kPairStageBytes + 1024 + 512;
+static_assert(kPairD + kPairStages * kPairSfCols <= 512, "tensor memory");
+static_assert(kPairSmem <= kSmemBudget, "shared memory");
+
+struct PairArgs {
+  MxArgs c;
+  const uint8_t* m_scales;  // of the operand whose rows are M, and N
+  const uint8_t* n_scales;
+  int m_row_tiles, n_row_tiles;  // 128-row tiles of either
+  int units, token_units;        // tiles in all, and along the tokens
+};
+
+__device__ __forceinline__ void mma_mxf4_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                              uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void store_sector(float* o, const float (&z)[8]) {
+  uint32_t r[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(z[j]);
+  store32(o, r, 0);
+}
+__device__ __forceinline__ void store_sector(uint16_t* o, const float (&z)[16]) {
+  uint32_t r[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    r[j] = from_float<uint16_t>(z[2 * j]) | static_cast<uint32_t>(from_float<uint16_t>(z[2 * j + 1])) << 16;
+  store32(o, r, 0);
+}
+
+// Arrives at a barrier of the pair's other CTA or its own. What this orders between
+// the CTAs is tensor memory, for which tcgen05.fence::before_thread_sync stands in
+// front; a release at cluster scope would wait for all the SM's memory traffic as
+// well: 1300 cycles a stage, and 1430 us where this takes @@ us.
+__device__ __forceinline__ void arrive_pair(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+constexpr uint64_t kDrainNs = 10 * 1000 * 1000;  // copies in flight land in microseconds
+
+template <bool TOKENS_M, typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUtensorMap map_n,
+                        const __grid_constant__ PairArgs q) {
+  constexpr int S = kPairStages;
+  const MxArgs& p = q.c;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* s_m = smem;
+  uint8_t* s_n = s_m + S * kWBytes;
+  uint8_t* s_sf = s_n + S * kWBytes;  // per pair of stages: M's scale tiles, those of N's first 128 rows, of its other
+  constexpr int kSfRun = 2 * kSfTiles * kMxTileBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_sf + S / 2 * 3 * kSfRun);
+  uint64_t* sf_full = full + S / 2;
+  uint64_t* scaled = sf_full + S / 2;  // the leader's: codes have landed and scales are in tensor memory, in both CTAs
+  uint64_t* empty = scaled + S / 2;
+  uint64_t* tfull = empty + S;
+  uint64_t* tempty = tfull + 1;
+  uint64_t* mma_done = tempty + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+  int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+
+  // (the first wait can run out seconds after this, and all CTAs run at once)
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) mbar_init(&empty[s], 1);
+    for (int s = 0; s < S / 2; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&sf_full[s], 1);
+      mbar_init(&scaled[s], 2 * 4);
+    }
+    mbar_init(tfull, 1);
+    mbar_init(tempty, 2 * 16);
+    mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&map_m);
+    tma_prefetch_desc(&map_n);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before_sync();
+  cluster_sync_all();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  const int k_pairs = (p.k_iters + 1) / 2;
+  const WaitCtx wc{abort_flag, p.status, p.timeout_ns};
+  const int first = static_cast<int>(blockIdx.x >> 1), step = static_cast<int>(gridDim.x >> 1);
+
+  if (warp == 0 || warp == 22) {
+    // Codes of M, of N: one warp for all copies of a stage took 670 cycles to issue them.
+    const bool is_m = warp == 0;
+    const CUtensorMap* map = is_m ? &map_m : &map_n;
+    uint8_t* to = is_m ? s_m : s_n;
+    const uint32_t full0 = mapa_shared(smem_u32(full), 0);
+    int stage = 0, issued = 0;
+    uint32_t phase = 0;
+    bool aborted = false;
+    for (int t = first; t < q.units && !aborted; t += step) {
+      const int vu = t / q.token_units, tu = t - vu * q.token_units;  // a tile of W meets all tokens while in the L2
+      const int row = ((is_m == TOKENS_M ? tu : vu) * 2 + rank) * 128;
+      for (int k = 0; k < 2 * k_pairs; ++k) {
+        if (!warp_wait(&empty[stage], phase ^ 1u, wc)) {
+          aborted = true;
+          break;
+        }
+        if (k < p.k_iters && elect_one()) {
+          if (is_m && rank == 0 && (k & 1) == 0)
+            mbar_arrive_expect_tx(&full[stage / 2], min(2, p.k_iters - k) * 4 * kWBytes);
+          tma_load_2d_pair(to + stage * kWBytes, map, full0 + static_cast<uint32_t>(stage / 2) * 8u, k * kRowBytes, row);
+        }
+        __syncwarp();
+        ++issued;
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (aborted && lane == 0) {
+      // Loads that may still be in flight land before the shared memory goes away. Of a
+      // pair of stages not all of which was issued the barrier does not complete, and
+      // the other CTA's copies are counted by the leader: it waits for what nobody signals.
+      const int n = min((issued + 1) / 2, S / 2);
+      int s = (stage + 1) / 2 % (S / 2);
+      uint32_t ph = (stage + 1) / 2 == S / 2 ? phase ^ 1u : phase;
+      for (int i = 0; i < n && rank == 0; ++i) {
+        if (s == 0) {
+          s = S / 2 - 1;
+          ph ^= 1u;
+        } else {
+          --s;
+        }
+        wait_drain(&full[s], ph, kDrainNs, p.status);
+      }
+      if (rank != 0) wait_drain(mma_done, 0, kDrainNs, p.status);
+    }
+    __syncwarp();
+  } else if (warp == 23) {
+    // Scales, for a pair of stages at once.
+    int two = 0, issued = 0;
+    uint32_t phase = 0;
+    bool aborted = false;
+    for (int t = first; t < q.units && !aborted; t += step) {
+      const int vu = t / q.token_units, tu = t - vu * q.token_units;
+      const int m_tile = 2 * (TOKENS_M ? tu : vu) + rank, n_tile = 2 * (TOKENS_M ? vu : tu);
+      const int m_here = m_tile < q.m_row_tiles ? 1 : 0, n_here = min(2, q.n_row_tiles - n_tile);
+      const uint8_t* m_from = q.m_scales + static_cast<int64_t>(m_tile) * p.k_tiles * kMxTileBytes;
+      const uint8_t* n_from = q.n_scales + static_cast<int64_t>(n_tile) * p.k_tiles * kMxTileBytes;
+      for (int k = 0; k < k_pairs; ++k) {
+        if (!warp_wait(&empty[2 * two], phase ^ 1u, wc) || !warp_wait(&empty[2 * two + 1], phase ^ 1u, wc)) {
+          aborted = true;
+          break;
+        }
+        if (elect_one()) {
+          uint8_t* s = s_sf + two * 3 * kSfRun;
+          const uint32_t bytes = min(2 * kSfTiles, p.k_tiles - k * 2 * kSfTiles) * kMxTileBytes;
+          mbar_arrive_expect_tx(&sf_full[two], bytes * (m_here + n_here));
+          if (m_here) bulk_load(s, m_from + k * kSfRun, bytes, &sf_full[two]);
+          bulk_load(s + kSfRun, n_from + k * kSfRun, bytes, &sf_full[two]);
+          if (n_here > 1)
+            bulk_load(s + 2 * kSfRun, n_from + p.k_tiles * kMxTileBytes + k * kSfRun, bytes, &sf_full[two]);
+        }
+        __syncwarp();
+        ++issued;
+        if (++two == S / 2) {
+          two = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (aborted && lane == 0) {
+      const int n = min(issued, S / 2);
+      for (int i = 0; i < n; ++i) {
+        if (two == 0) {
+          two = S / 2 - 1;
+          phase ^= 1u;
+        } else {
+          --two;
+        }
+        wait_drain(&sf_full[two], phase, kDrainNs, p.status);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (rank == 0) {
+      int two = 0;  // the pair of stages
+      uint32_t phase = 0, acc_phase = 0;
+      const uint32_t m0 = smem_u32(s_m), n0 = smem_u32(s_n);
+      bool aborted = false;
+      for (int t = first; t < q.units && !aborted; t += step) {
+        if (!warp_wait(tempty, acc_phase ^ 1u, wc)) break;
+        acc_phase ^= 1u;
+        tc_fence_after_sync();
+        for (int k = 0; k < k_pairs; ++k) {
+          if (!warp_wait(&scaled[two], phase, wc)) {
+            aborted = true;
+            break;
+          }
+          tc_fence_after_sync();
+          if (elect_one()) {
+            const int mmas = p.k_mmas - 2 * k * (kStageK / 64);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int stage = 2 * two + h;
+              const uint32_t sf = tmem + static_cast<uint32_t>(kPairD + stage * kPairSfCols);
+              const uint32_t a0 = m0 + stage * kWBytes, b0 = n0 + stage * kWBytes;
+#pragma unroll
+              for (int j = 0; j < kStageK / 64; ++j)
+                if (h * (kStageK / 64) + j < mmas)
+                  mma_mxf4_pair(tmem, sdesc_kmajor_sw128(a0 + j * 32), sdesc_kmajor_sw128(b0 + j * 32),
+                                idesc_mxf4(256, 256, (j & 1) * 2), sf + 4 * (j >> 1), sf + 8 + 8 * (j >> 1),
+                                (k | h | j) != 0 ? 1u : 0u);
+              tc_commit_pair(&empty[stage], 0x3);
+            }
+            if (k == k_pairs - 1) tc_commit_pair(tfull, 0x3);
+          }
+          __syncwarp();
+          if (++two == S / 2) {
+            two = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (elect_one()) {
+        tc_commit_pair(mma_done, 0x1);
+        wait_drain(mma_done, 0, p.timeout_ns, p.status);
+      }
+      __syncwarp();
+    }
+  } else if (warp < 6) {
+    // Scales of a pair of stages whose copies have landed: its last MMAs are done,
+    // since the loader waited for them, so its columns are free. The MMA warp has one
+    // thing to wait for: each wait of its own showed in the time between its MMAs.
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t scaled0 = mapa_shared(smem_u32(scaled), 0);
+    int two = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int t = first; t < q.units && ok; t += step) {
+      for (int k = 0; k < k_pairs; ++k) {
+        ok = warp_wait(&sf_full[two], phase, wc);
+        if (!ok) break;
+        tc_fence_after_sync();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (2 * k + h >= p.k_iters) break;
+          const int stage = 2 * two + h;
+          const uint32_t sf = t_lane + static_cast<uint32_t>(kPairD + stage * kPairSfCols);
+          const uint8_t* m = s_sf + two * 3 * kSfRun + h * kSfTiles * kMxTileBytes + lane * 16;
+          const uint8_t *n = m + kSfRun, *n2 = n + kSfRun;
+          // (what was not loaded, of K or of rows, is an earlier use's bytes: not used, or not stored)
+          store_scales2(sf, m, m + kMxTileBytes);
+          // columns by K-tile, rows in order within one
+          store_scales2(sf + 8, n, n2);
+          store_scales2(sf + 16, n + kMxTileBytes, n2 + kMxTileBytes);
+        }
+        store_scales_wait();
+        if (rank == 0) ok = warp_wait(&full[two], phase, wc);
+        if (!ok) break;
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) arrive_pair(scaled0 + static_cast<uint32_t>(two) * 8u);
+        if (++two == S / 2) {
+          two = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+  } else {
+    const int quarter = warp & 3, part = (warp - 6) >> 2;
+    const uint32_t t_here = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + part * 64;
+    const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0);
+    uint32_t acc_phase = 0;
+    for (int t = first; t < q.units; t += step) {
+      const int vu = t / q.token_units, tu = t - vu * q.token_units;
+      if (!warp_wait(tfull, acc_phase, wc)) break;
+      acc_phase ^= 1u;
+      tc_fence_after_sync();
+      const int m = ((TOKENS_M ? tu : vu) * 2 + rank) * 128 + quarter * 32 + lane;
+      uint32_t r[2][32];
+      tmem_load_32cols(t_here, r[0]);
+      tmem_load_32cols(t_here + 32, r[1]);
+      tmem_load_wait_regs(r[0]);
+      tmem_load_wait_regs(r[1]);
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) arrive_pair(tempty0);
+      const int n = (TOKENS_M ? vu : tu) * 256 + part * 64;
+      if (TOKENS_M && m < p.rows) {
+        T* o = static_cast<T*>(p.out) + static_cast<int64_t>(m) * p.ld_out + n;
+        constexpr int V = 32 / sizeof(T);
+#pragma unroll
+        for (int c = 0; c < 64; c += V) {
+          float z[V];
+#pragma unroll
+          for (int j = 0; j < V; ++j) z[j] = finish(p, r[(c + j) / 32][(c + j) % 32]);
+          if (n + c + V <= p.vocab) {
+            store_sector(o + c, z);
+          } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+              if (n + c + j < p.vocab) o[c + j] = from_float<T>(z[j]);
+          }
+        }
+      } else if (!TOKENS_M && m < p.vocab) {
+        T* o = static_cast<T*>(p.out) + static_cast<int64_t>(n) * p.ld_out + m;
+#pragma unroll
+        for (int c = 0; c < 64; ++c)
+          if (n + c < p.rows) o[c * p.ld_out] = from_float<T>(finish(p, r[c / 32][c % 32]));
+      }
+      __syncwarp();
+    }
+  }
+  tc_fence_before_sync();
+  cluster_sync_all();  // neither CTA leaves while the other may still signal it
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
 // Codes as bytes [rows][cols / 2], boxes of 128 bytes x box_rows, 128-byte swizzle.
 bool encode_codes(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int box_rows) {
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols / 2), static_cast<cuuint64_t>(rows)};
@@ -438,11 +774,9 @@ bool encode_codes(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, 
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int NT, bool RESIDENT, bool FUSED, typename T>
-int run_tile(const MxGemmParams& p, int sms, cudaStream_t stream) {
-  using P = Plan<NT, RESIDENT>;
-  auto kernel = mx_gemm_kernel<NT, RESIDENT, FUSED, T>;
-  static std::atomic<uint64_t> done{0};
+// Opts a kernel in to kSmemBudget on this device, once.
+template <typename K>
+int opt_in(K kernel, std::atomic<uint64_t>& done) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return FLCE_ERR_CUDA;
   if (!(done.load() >> dev & 1)) {
@@ -450,13 +784,11 @@ int run_tile(const MxGemmParams& p, int sms, cudaStream_t stream) {
       return FLCE_ERR_CUDA;
     done.fetch_or(1ull << dev);
   }
-  CUtensorMap map_w, map_x;
-  if (!encode_codes(&map_w, p.w_codes, p.vocab, p.cols, kTileV)) return FLCE_ERR_UNSUPPORTED;
-  if (FUSED)
-    map_x = map_w;  // not used
-  else if (!encode_codes(&map_x, p.a_codes, p.rows, p.cols, NT))
-    return FLCE_ERR_UNSUPPORTED;
-  MxArgs a;
+  return FLCE_OK;
+}
+
+MxArgs arguments(const MxGemmParams& p) {
+  MxArgs a = {};
   a.w_scales = p.w_scales;
   a.x_scales = p.a_scales;
   a.x = p.x;
@@ -466,12 +798,9 @@ int run_tile(const MxGemmParams& p, int sms, cudaStream_t stream) {
   a.rows = static_cast<int>(p.rows);
   a.vocab = static_cast<int>(p.vocab);
   a.k_iters = static_cast<int>((p.cols + kStageK - 1) / kStageK);
-  a.stages = P::stages(a.k_iters);
   a.k_tiles = static_cast<int>((p.cols + kMxTileCols - 1) / kMxTileCols);
   a.k_mmas = static_cast<int>((p.cols + 63) / 64);
-  a.x_row_tiles = static_cast<int>((p.rows + 127) / 128);
   a.v_tiles = static_cast<int>((p.vocab + kTileV - 1) / kTileV);
-  a.n_tiles = static_cast<int>((p.rows + NT - 1) / NT);
   a.out_mult = p.out_mult;
   a.softcap = p.softcap;
   a.inv_softcap = p.inv_softcap;
@@ -479,14 +808,50 @@ int run_tile(const MxGemmParams& p, int sms, cudaStream_t stream) {
   a.ld_out = p.ld_out;
   a.status = p.status;
   a.timeout_ns = p.timeout_ns;
-  // An MMA's scales start on an even column of tensor memory: token tiles other
-  // than the first need 64 rows or a multiple of it.
-  static_assert(NT % 64 == 0 || NT < 64, "even scale columns");
-  if (a.n_tiles > 1 && NT % 64 != 0) return FLCE_ERR_ARG;
-  const int64_t total = static_cast<int64_t>(a.v_tiles) * a.n_tiles;
-  if (total >= (1LL << 31)) return FLCE_ERR_ARG;
-  const int grid = static_cast<int>(total < sms ? total : sms);
+  return a;
+}
+
+template <int NT, bool RESIDENT, bool FUSED, typename T>
+int run_tile(const MxGemmParams& p, int sms, cudaStream_t stream) {
+  using P = Plan<NT, RESIDENT>;
+  auto kernel = mx_gemm_kernel<NT, RESIDENT, FUSED, T>;
+  static std::atomic<uint64_t> done{0};
+  if (const int e = opt_in(kernel, done)) return e;
+  CUtensorMap map_w, map_x;
+  if (!encode_codes(&map_w, p.w_codes, p.vocab, p.cols, kTileV)) return FLCE_ERR_UNSUPPORTED;
+  if (FUSED)
+    map_x = map_w;  // not used
+  else if (!encode_codes(&map_x, p.a_codes, p.rows, p.cols, NT))
+    return FLCE_ERR_UNSUPPORTED;
+  MxArgs a = arguments(p);
+  a.stages = P::stages(a.k_iters);
+  const int grid = a.v_tiles < sms ? a.v_tiles : sms;
   FLCE_LAUNCH(K_MX_GEMM, (kernel<<<grid, kThreads, P::smem(a.k_iters), stream>>>(map_w, map_x, a), cudaGetLastError()));
+  return FLCE_OK;
+}
+
+template <bool TOKENS_M, typename T>
+int run_pair(const MxGemmParams& p, int sms, cudaStream_t stream) {
+  auto kernel = mx_gemm_pair_kernel<TOKENS_M, T>;
+  static std::atomic<uint64_t> done{0};
+  if (const int e = opt_in(kernel, done)) return e;
+  CUtensorMap map_w, map_x;
+  if (!encode_codes(&map_w, p.w_codes, p.vocab, p.cols, 128) || !encode_codes(&map_x, p.a_codes, p.rows, p.cols, 128))
+    return FLCE_ERR_UNSUPPORTED;
+  PairArgs q = {};
+  q.c = arguments(p);
+  const int x_tiles = static_cast<int>((p.rows + 127) / 128);
+  q.m_scales = TOKENS_M ? p.a_scales : p.w_scales;
+  q.n_scales = TOKENS_M ? p.w_scales : p.a_scales;
+  q.m_row_tiles = TOKENS_M ? x_tiles : q.c.v_tiles;
+  q.n_row_tiles = TOKENS_M ? q.c.v_tiles : x_tiles;
+  q.token_units = (x_tiles + 1) / 2;
+  const int64_t units = static_cast<int64_t>((q.c.v_tiles + 1) / 2) * q.token_units;
+  if (units >= (1LL << 30)) return FLCE_ERR_ARG;
+  q.units = static_cast<int>(units);
+  const int clusters = q.units < sms / 2 ? q.units : sms / 2;
+  FLCE_LAUNCH(K_MX_GEMM, (kernel<<<2 * clusters, kPairThreads, kPairSmem, stream>>>(
+                              TOKENS_M ? map_x : map_w, TOKENS_M ? map_w : map_x, q), cudaGetLastError()));
   return FLCE_OK;
 }
 
@@ -509,7 +874,8 @@ int run_typed(const MxGemmParams& p, int sms, cudaStream_t s) {
   if (p.rows <= 32) return run_few<32, T>(p, sms, s);
   if (p.rows <= 64) return run_few<64, T>(p, sms, s);
   if (p.rows <= 128) return run_few<128, T>(p, sms, s);
-  return run_tile<192, false, false, T>(p, sms, s);
+  if (reinterpret_cast<uintptr_t>(p.out) % 32 == 0 && p.ld_out * sizeof(T) % 32 == 0) return run_pair<true, T>(p, sms, s);
+  return run_pair<false, T>(p, sms, s);
 }
 
 }  // namespace
