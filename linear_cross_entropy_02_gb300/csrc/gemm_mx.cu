@@ -2,13 +2,13 @@
 // tcgen05.mma kind::mxf4 with a power-of-two scale per 32 elements, products
 // summed in fp32 in tensor memory.
 //
-// W's rows are the M dimension (128 vocabulary entries per tile) and the tokens
-// the N dimension, so that one token and a whole prompt run through the same
-// kernel: for a few tokens the tile is 128 x 16 and the kernel streams W once
-// through a deep ring of TMA copies, bound by HBM; for a prompt it is 128 x 192
-// and bound by the tensor cores and the L2. A lane of tensor memory is then a
-// vocabulary entry, and a warp's store for one token is one contiguous run of
-// logits whatever the row stride's alignment.
+// Two kernels: up to 128 tokens, where W is streamed once and HBM bounds the time,
+// and for more of them pairs of CTAs on 256 x 256 tiles (further down), bound by the
+// tensor cores. In the first, W's rows are the M dimension (128 vocabulary entries
+// per tile) and the tokens the N dimension (16 to 128): a lane of tensor memory is a
+// vocabulary entry, and a warp's store for one token is one contiguous run of logits
+// whatever the row stride's alignment. One token on 129280 x 7168 takes 79 us, 93% of
+// the copy bandwidth; 128 on 128256 x 4096 take 57.
 //
 // K advances 256 elements (one 128-byte swizzle row of codes) per stage. Scales
 // come from HBM already in the order of tensor memory, 512 bytes per 128 rows x
@@ -25,8 +25,8 @@
 // Up to kMostFused elements are encoded by every CTA for itself, straight into
 // the swizzled tiles, while the first copies of W are on their way: a launch less.
 //
-// Warp 0 loads, warp 1 issues the MMAs, warps 2-5 store, warps 6-9 carry scales:
-// two accumulators, so that the stores of one tile run under the MMAs of the
+// Warp 0 loads, warp 1 issues the MMAs, warps 2-5 store, warps 6-9 carry scales;
+// there are two accumulators, so that the stores of one tile run under the MMAs of the
 // next. Every wait is bounded (flce_device.cuh) and ends the call with
 // FLCE_ERR_TIMEOUT.
 #include <cuda_bf16.h>
@@ -410,18 +410,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // More than 128 tokens: 256 x 256 tiles over a cluster of two CTAs on two SMs.
-// A single CTA's 128 x 192 tile draws 43 KB per K = 256 for 384 cycles of MMAs,
-// and an SM takes about 64 bytes a cycle from the L2: 4096 tokens on 128256 x 4096
-// took 1106 us, 786 of them with the MMAs left out. Here each CTA holds 128 rows
-// of M and 128 of N, 35 KB with the scales for 512 cycles. M = 256, N = 256 fill
-// half of tensor memory, so that the other half holds scales and the accumulator
-// is one: sixteen warps take it into registers at once and store from there, under
-// the next tile's MMAs.
+// A single CTA's 128 x 192 tile drew 43 KB per K = 256 for 384 cycles of MMAs, more
+// than an SM gets from the L2: 4096 tokens on 128256 x 4096 took 1106 us, 786 of
+// them with the MMAs left out. Here each CTA holds 128 rows of M and 128 of N, 35 KB
+// with the scales for 512 cycles, and the same product takes 628 us (6.9 PFLOP/s);
+// the MMAs alone 505, the copies alone 376. M = 256, N = 256 fill half of tensor
+// memory, so that the other half holds scales and the accumulator is one: sixteen
+// warps take it into registers at once and store from there, under the next tile's
+// MMAs. Between two tiles the MMAs rest for about 960 of 8200 cycles.
 //
 // TOKENS_M: the tokens are M, a thread has 128 neighbouring logits of one token
 // and stores whole 32-byte sectors, for which rows of logits start on 32 bytes.
 // Else the vocabulary is M, and a warp's store is 32 neighbouring logits of one
-// token, at any alignment.
+// token, at any alignment (663 us for 128250 entries).
 //
 // Both CTAs' codes are counted by the leader's barriers, each CTA's scales by its
 // own; its scale warps then arrive at the leader's `scaled`. The leader's commits
@@ -453,24 +454,30 @@ __device__ __forceinline__ void mma_mxf4_pair(uint32_t d, uint64_t a, uint64_t b
       : "memory");
 }
 
-__device__ __forceinline__ void store_sector(float* o, const float (&z)[8]) {
+// 32 bytes of logits. They go out of the L2 before the operands, which are read
+// again: 636 us instead of 662 for 4096 tokens on 128256 x 4096.
+__device__ __forceinline__ void store_sector(void* o, const uint32_t (&r)[8], uint64_t policy) {
+  asm volatile("st.global.L1::no_allocate.L2::cache_hint.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8}, %9;" ::"l"(o),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "l"(policy)
+               : "memory");
+}
+__device__ __forceinline__ void store_sector(float* o, const float (&z)[8], uint64_t policy) {
   uint32_t r[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(z[j]);
-  store32(o, r, 0);
+  store_sector(static_cast<void*>(o), r, policy);
 }
-__device__ __forceinline__ void store_sector(uint16_t* o, const float (&z)[16]) {
+__device__ __forceinline__ void store_sector(uint16_t* o, const float (&z)[16], uint64_t policy) {
   uint32_t r[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    r[j] = from_float<uint16_t>(z[2 * j]) | static_cast<uint32_t>(from_float<uint16_t>(z[2 * j + 1])) << 16;
-  store32(o, r, 0);
+  for (int j = 0; j < 8; ++j) r[j] = pack_bf16(z[2 * j], z[2 * j + 1]);
+  store_sector(static_cast<void*>(o), r, policy);
 }
 
 // Arrives at a barrier of the pair's other CTA or its own. What this orders between
 // the CTAs is tensor memory, for which tcgen05.fence::before_thread_sync stands in
-// front; a release at cluster scope would wait for all the SM's memory traffic as
-// well: 1300 cycles a stage, and 1430 us where this takes @@ us.
+// front; a release at cluster scope waits for the SM's memory traffic as well, 1300
+// cycles a stage: 4096 tokens on 128256 x 4096 took 1430 us with it and 773 without.
 __device__ __forceinline__ void arrive_pair(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
@@ -714,6 +721,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const int quarter = warp & 3, part = (warp - 6) >> 2;
     const uint32_t t_here = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + part * 64;
     const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0);
+    const uint64_t policy = l2_policy_evict_first();
     uint32_t acc_phase = 0;
     for (int t = first; t < q.units; t += step) {
       const int vu = t / q.token_units, tu = t - vu * q.token_units;
@@ -739,7 +747,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
           for (int j = 0; j < V; ++j) z[j] = finish(p, r[(c + j) / 32][(c + j) % 32]);
           if (n + c + V <= p.vocab) {
-            store_sector(o + c, z);
+            store_sector(o + c, z, policy);
           } else {
 #pragma unroll
             for (int j = 0; j < V; ++j)
