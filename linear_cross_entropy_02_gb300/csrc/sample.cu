@@ -42,8 +42,7 @@ namespace flce {
 
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kWarps = kThreads / 32;
+constexpr int kMostWarps = 32;
 constexpr int kMaxCluster = 8;
 constexpr int kListKeys = 8192;
 constexpr int kFew = 64;       // entries that are compared each with each
@@ -57,7 +56,6 @@ constexpr float kBinsPerUnit = (kBins - 1) / kRange;
 // Counts of the first pass: 4096 bins from 8 above the anchor to 28 below it;
 // the last one holds what is further below, whose weights are zero.
 constexpr int kCountBins = 4096;
-constexpr int kBinsPerThread = kCountBins / kThreads;
 constexpr float kAbove = 8.f;
 constexpr float kPlaces = kAbove + kRange;  // a place of 0 to 1 is this many units of t
 constexpr float kUnitsPerBin = kPlaces / (kCountBins - 1);
@@ -74,6 +72,7 @@ constexpr int kSegments = 256;
 constexpr int kFirstVectors = 4;  // per thread: the part of the row that sets the anchor
 constexpr int kAnswerBins = 2048;   // segments of the vocabulary for a list of kept tokens
 constexpr int kMostShared = 227 * 1024;
+constexpr int kMostVocab = 1 << 22;
 
 struct Hist {
   uint32_t count[kBins];
@@ -98,8 +97,8 @@ struct Shared {
     Answer answer;
   };
   uint64_t seg_weight[kSegments];
-  uint32_t seg_ties[kWarps];
-  uint64_t scan[kWarps + 1];
+  uint32_t seg_ties[kMostWarps];
+  uint64_t scan[kMostWarps + 1];
   uint64_t sum_total, sum_above;  // of this slice, in the second pass
   uint64_t found_above, found_value, goal;
   uint32_t found_bin, found_count;
@@ -113,8 +112,8 @@ struct Shared {
   uint32_t result_key, result_count;
   unsigned long long cut_lo[2], cut_hi[2];  // first and last bin to collect; low words: logits before and up to them
   uint32_t general;         // CTA 0: the row needs the general selection
-  uint32_t red[kWarps], red2[kWarps];
-  float fscan[kWarps];
+  uint32_t red[kMostWarps], red2[kMostWarps];
+  float fscan[kMostWarps];
   float cut_x[2];
   uint32_t told[3];  // CTA 0: where the prefix ends, for the others
 };
@@ -209,6 +208,7 @@ __device__ __forceinline__ uint64_t warp_total(uint64_t v) {
 
 // Exclusive prefix sum over the CTA's threads; *total gets the whole. Begins
 // with a barrier, so `scan` may be used again at once.
+template <int kThreads>
 __device__ uint64_t block_exclusive(uint64_t v, uint64_t* scan, uint64_t* total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t inc = warp_inclusive(v);
@@ -216,18 +216,19 @@ __device__ uint64_t block_exclusive(uint64_t v, uint64_t* scan, uint64_t* total)
   if (lane == 31) scan[warp] = inc;
   __syncthreads();
   if (warp == 0) {
-    const uint64_t w = scan[lane];
+    const uint64_t w = lane < kThreads / 32 ? scan[lane] : 0;
     const uint64_t wi = warp_inclusive(w);
     __syncwarp();
     scan[lane] = wi - w;
-    if (lane == 31) scan[kWarps] = wi;
+    if (lane == 31) scan[kMostWarps] = wi;
   }
   __syncthreads();
-  *total = scan[kWarps];
+  *total = scan[kMostWarps];
   return scan[warp] + inc - v;
 }
 
 // The same of a count and an estimated weight at once.
+template <int kThreads>
 __device__ __forceinline__ void block_exclusive(Shared& s, uint32_t n, float w, uint32_t* n_before, float* w_before,
                                                 float* w_total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -249,8 +250,8 @@ __device__ __forceinline__ void block_exclusive(Shared& s, uint32_t n, float w, 
   }
   __syncthreads();
   // every warp adds up the warps before it, in one order
-  uint32_t a = s.red[lane];
-  float b = s.fscan[lane];
+  uint32_t a = lane < kThreads / 32 ? s.red[lane] : 0;
+  float b = lane < kThreads / 32 ? s.fscan[lane] : 0.f;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const uint32_t c = __shfl_up_sync(0xffffffffu, a, o);
@@ -335,7 +336,7 @@ struct Sum {
 
 // ---------------------------------------------------------------- a row
 // The part of a row that a CTA works on, and the row's settings.
-template <typename T>
+template <typename T, int kThreads>
 struct Row {
   static constexpr int E = 16 / sizeof(T);
   const T* data;  // in shared memory (padded with -infinity to whole vectors) or in global memory
@@ -419,25 +420,27 @@ struct Row {
   }
 };
 
+template <int kThreads>
 __device__ void clear(Hist& h) {
   for (int i = threadIdx.x; i < kBins; i += kThreads) h.count[i] = h.lo[i] = h.hi[i] = 0;
   __syncthreads();
 }
 
-template <typename T>
-__device__ __forceinline__ void write_answer(const Row<T>& row, const SampleParams& p, int64_t r, uint32_t index, float x,
+template <typename T, int kThreads>
+__device__ __forceinline__ void write_answer(const Row<T, kThreads>& row, const SampleParams& p, int64_t r, uint32_t index, float x,
                                              uint64_t whole) {
   p.tokens[r] = index;
   if (p.logprobs) p.logprobs[r] = row.scaled(x) - logf(__ll2float_rn(static_cast<int64_t>(whole)) * (1.f / kFixed));
 }
 
 // Over the CTA, in every thread.
+template <int kThreads>
 __device__ __forceinline__ uint64_t block_total(Shared& s, uint64_t v) {
   v = warp_total(v);
   __syncthreads();
   if ((threadIdx.x & 31) == 0) s.scan[threadIdx.x >> 5] = v;
   __syncthreads();
-  return warp_total(s.scan[threadIdx.x & 31]);
+  return warp_total((threadIdx.x & 31) < kThreads / 32 ? s.scan[threadIdx.x & 31] : 0);
 }
 
 // The entry of the CTA's list of n at which the running sum in rank order,
@@ -446,8 +449,8 @@ __device__ __forceinline__ uint64_t block_total(Shared& s, uint64_t v) {
 // over the range of entries (they are whole numbers in rank order, all
 // different), again over the bin that holds the goal, until that has at most
 // kFew. Uses the first histogram.
-template <typename T, bool WEIGHT>
-__device__ uint64_t list_reach(const Row<T>& row, Shared& s, int n, uint64_t lo, uint64_t hi, uint64_t start,
+template <typename T, int kThreads, bool WEIGHT>
+__device__ uint64_t list_reach(const Row<T, kThreads>& row, Shared& s, int n, uint64_t lo, uint64_t hi, uint64_t start,
                                uint64_t goal) {
   Hist& h = s.hist[0];
   __syncthreads();  // the list is complete, the histogram's place free
@@ -455,7 +458,7 @@ __device__ uint64_t list_reach(const Row<T>& row, Shared& s, int n, uint64_t lo,
     const int bits = 64 - __clzll(static_cast<long long>(hi - lo));
     const int shift = bits > 10 ? bits - 10 : 0;
     static_assert(kBins == 1 << 10, "a range of 10 + shift bits");
-    clear(h);
+    clear<kThreads>(h);
     for (int i = threadIdx.x; i < n; i += kThreads) {
       const uint64_t e = s.list[i];
       if (e >= lo && e <= hi) {
@@ -465,16 +468,25 @@ __device__ uint64_t list_reach(const Row<T>& row, Shared& s, int n, uint64_t lo,
       }
     }
     __syncthreads();
-    const int b = threadIdx.x;
-    const uint64_t v = WEIGHT ? h.lo[b] + (static_cast<uint64_t>(h.hi[b]) << 32) : h.count[b];
-    uint64_t total;
-    const uint64_t before = start + block_exclusive(v, s.scan, &total);
+    constexpr int B = kBins / kThreads;  // bins of a thread
+    uint64_t v[B], sum = 0, total;
+#pragma unroll
+    for (int j = 0; j < B; ++j) {
+      const int b = B * threadIdx.x + j;
+      v[j] = WEIGHT ? h.lo[b] + (static_cast<uint64_t>(h.hi[b]) << 32) : h.count[b];
+      sum += v[j];
+    }
+    uint64_t before = start + block_exclusive<kThreads>(sum, s.scan, &total);
     if (start + total < goal) return ~0ull;
-    if (before < goal && goal <= before + v) {
-      s.found_bin = b;
-      s.found_above = before;
-      s.found_count = h.count[b];
-      s.few_count = 0;
+#pragma unroll
+    for (int j = 0; j < B; ++j) {
+      if (before < goal && goal <= before + v[j]) {
+        s.found_bin = B * threadIdx.x + j;
+        s.found_above = before;
+        s.found_count = h.count[B * threadIdx.x + j];
+        s.few_count = 0;
+      }
+      before += v[j];
     }
     __syncthreads();
     start = s.found_above;
@@ -501,27 +513,36 @@ __device__ uint64_t list_reach(const Row<T>& row, Shared& s, int n, uint64_t lo,
 }
 
 // ---------------------------------------------------------------- general selection
-// Sums the row's histograms, a bin per thread. want(total) gives the goal; the
+// Sums the row's histograms. want(total) gives the goal; the
 // bin whose running sum first reaches it goes to found_* (found_bin = kBins if
 // none does). WEIGHT: sums of weights, else counts.
-template <bool MULTI, bool WEIGHT, typename F>
+template <int kThreads, bool MULTI, bool WEIGHT, typename F>
 __device__ uint64_t find_bin(Shared& s, const Hist& h, uint32_t ctas, F want, uint64_t* total) {
-  static_assert(kBins == kThreads, "a bin per thread");
-  const int b = threadIdx.x;
-  uint64_t v = 0;
-  uint32_t n = 0;
-  for (uint32_t r = 0; r < ctas; ++r) {
-    n += remote<MULTI>(&h.count[b], r);
-    if (WEIGHT) v += remote<MULTI>(&h.lo[b], r) + (static_cast<uint64_t>(remote<MULTI>(&h.hi[b], r)) << 32);
+  constexpr int B = kBins / kThreads;  // bins of a thread
+  uint64_t v[B], sum = 0;
+  uint32_t n[B];
+#pragma unroll
+  for (int j = 0; j < B; ++j) {
+    const int b = B * threadIdx.x + j;
+    v[j] = n[j] = 0;
+    for (uint32_t r = 0; r < ctas; ++r) {
+      n[j] += remote<MULTI>(&h.count[b], r);
+      if (WEIGHT) v[j] += remote<MULTI>(&h.lo[b], r) + (static_cast<uint64_t>(remote<MULTI>(&h.hi[b], r)) << 32);
+    }
+    if (!WEIGHT) v[j] = n[j];
+    sum += v[j];
   }
-  if (!WEIGHT) v = n;
-  if (b == 0) s.found_bin = kBins;
-  const uint64_t before = block_exclusive(v, s.scan, total);
+  if (threadIdx.x == 0) s.found_bin = kBins;
+  uint64_t before = block_exclusive<kThreads>(sum, s.scan, total);
   const uint64_t goal = by_one(s, [&] { return want(*total); });
-  if (before < goal && goal <= before + v) {
-    s.found_bin = b;
-    s.found_above = before;
-    s.found_count = n;
+#pragma unroll
+  for (int j = 0; j < B; ++j) {
+    if (before < goal && goal <= before + v[j]) {
+      s.found_bin = B * threadIdx.x + j;
+      s.found_above = before;
+      s.found_count = n[j];
+    }
+    before += v[j];
   }
   __syncthreads();
   return goal;
@@ -531,12 +552,12 @@ __device__ uint64_t find_bin(Shared& s, const Hist& h, uint32_t ctas, F want, ui
 // running sum over the ranked logits above `limit` (a key) first reaches the
 // goal, which want(total) gives. Returns false if the sum never does: nothing is
 // cut off. *total_out and *goal_out: the whole sum and the goal.
-template <typename T, bool MULTI, bool WEIGHT, typename F>
-__device__ bool select(const Row<T>& row, Shared& s, int& buf, uint32_t* listed, uint32_t limit, F want,
+template <typename T, int kThreads, bool MULTI, bool WEIGHT, typename F>
+__device__ bool select(const Row<T, kThreads>& row, Shared& s, int& buf, uint32_t* listed, uint32_t limit, F want,
                        uint32_t* key_out, uint32_t* count_out, uint64_t* total_out, uint64_t* goal_out) {
   Hist* h = &s.hist[buf];
   buf ^= 1;
-  clear(*h);
+  clear<kThreads>(*h);
   row.each([&](float x, uint32_t) {
     const int b = row.bin(x);
     if (b < kBins - 1 && order_key(x) > limit) {  // the last bin's weights are zero
@@ -547,7 +568,7 @@ __device__ bool select(const Row<T>& row, Shared& s, int& buf, uint32_t* listed,
   row_barrier<MULTI>();
   uint64_t goal = 0;
   uint64_t total = 0;
-  goal = find_bin<MULTI, WEIGHT>(s, *h, row.ctas, want, &total);
+  goal = find_bin<kThreads, MULTI, WEIGHT>(s, *h, row.ctas, want, &total);
   *total_out = total;
   *goal_out = goal;
   if (s.found_bin == kBins) return false;
@@ -576,7 +597,7 @@ __device__ bool select(const Row<T>& row, Shared& s, int& buf, uint32_t* listed,
     }
     __syncthreads();
     if (threadIdx.x == 0) {
-      for (int w = 1; w < kWarps; ++w) {
+      for (int w = 1; w < kThreads / 32; ++w) {
         lo = min(lo, s.red[w]);
         hi = max(hi, s.red2[w]);
       }
@@ -602,7 +623,7 @@ __device__ bool select(const Row<T>& row, Shared& s, int& buf, uint32_t* listed,
     while (((key_hi - key_lo) >> shift) >= static_cast<uint32_t>(kBins)) ++shift;
     h = &s.hist[buf];
     buf ^= 1;
-    clear(*h);
+    clear<kThreads>(*h);
     row.each([&](float x, uint32_t) {
       const uint32_t k = order_key(x);
       if (k >= key_lo && k <= key_hi) {
@@ -613,7 +634,7 @@ __device__ bool select(const Row<T>& row, Shared& s, int& buf, uint32_t* listed,
     });
     row_barrier<MULTI>();
     uint64_t inside_total;
-    find_bin<MULTI, WEIGHT>(s, *h, row.ctas, [&](uint64_t) { return goal - above; }, &inside_total);
+    find_bin<kThreads, MULTI, WEIGHT>(s, *h, row.ctas, [&](uint64_t) { return goal - above; }, &inside_total);
     const uint32_t b = s.found_bin;
     above += s.found_above;
     count = s.found_count;
@@ -628,7 +649,7 @@ __device__ bool select(const Row<T>& row, Shared& s, int& buf, uint32_t* listed,
   });
   row_barrier<MULTI>();
   if (row.rank == 0) {
-    const uint64_t e = list_reach<T, WEIGHT>(row, s, static_cast<int>(count), list_entry(row.top, 0), list_entry(-INFINITY, ~0u),
+    const uint64_t e = list_reach<T, kThreads, WEIGHT>(row, s, static_cast<int>(count), list_entry(row.top, 0), list_entry(-INFINITY, ~0u),
                                              above, goal);
     uint32_t ties = 0;  // of the same logit, up to that entry
     for (int i = threadIdx.x; i < static_cast<int>(count); i += kThreads)
@@ -637,7 +658,7 @@ __device__ bool select(const Row<T>& row, Shared& s, int& buf, uint32_t* listed,
     if ((threadIdx.x & 31) == 0) s.red[threadIdx.x >> 5] = ties;
     __syncthreads();
     if (threadIdx.x == 0) {
-      for (int w = 1; w < kWarps; ++w) ties += s.red[w];
+      for (int w = 1; w < kThreads / 32; ++w) ties += s.red[w];
       s.result_key = ~static_cast<uint32_t>(e >> 32);
       s.result_count = ties;
     }
@@ -649,23 +670,23 @@ __device__ bool select(const Row<T>& row, Shared& s, int& buf, uint32_t* listed,
 }
 
 // The token by the general selection.
-template <typename T, bool MULTI>
-__device__ void general_answer(const Row<T>& row, Shared& s, const SampleParams& p, int64_t r, int64_t top_k,
+template <typename T, int kThreads, bool MULTI>
+__device__ void general_answer(const Row<T, kThreads>& row, Shared& s, const SampleParams& p, int64_t r, int64_t top_k,
                                float top_p, float u) {
-  constexpr int E = Row<T>::E;
+  constexpr int E = Row<T, kThreads>::E, kWarps = kThreads / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int buf = 0;
   // the kept set: logits above `key`, and the first `ties` of those equal to it
   uint32_t key = 0, ties = 0;
   uint64_t over, goal_p;
   if (top_k > 0 && top_k < p.vocab)
-    if (!select<T, MULTI, false>(row, s, buf, &s.listed[1], 0u, [&](uint64_t) { return static_cast<uint64_t>(top_k); },
+    if (!select<T, kThreads, MULTI, false>(row, s, buf, &s.listed[1], 0u, [&](uint64_t) { return static_cast<uint64_t>(top_k); },
                                  &key, &ties, &over, &goal_p))
       key = ties = 0;
   if (top_p < 1.f) {
     const uint64_t w = ties ? row.weight(key_value(key)) : 0;
     uint32_t k2, t2;
-    const bool cut = select<T, MULTI, true>(
+    const bool cut = select<T, kThreads, MULTI, true>(
         row, s, buf, &s.listed[2], key, [&](uint64_t total) { return top_p_goal(top_p, total + ties * w); }, &k2, &t2,
         &over, &goal_p);
     if (cut) {
@@ -679,13 +700,13 @@ __device__ void general_answer(const Row<T>& row, Shared& s, const SampleParams&
 
   // running sums in index order: a warp per segment of the slice
   const float e_tie = ties ? row.exponential(key_value(key)) : 0.f;
-  const uint64_t w_tie = e_tie >= row.min_p ? Row<T>::fixed(e_tie) : 0;
+  const uint64_t w_tie = e_tie >= row.min_p ? Row<T, kThreads>::fixed(e_tie) : 0;
   const int seg = (row.vecs + kWarps - 1) / kWarps;
   const int v0 = warp * seg, v1 = min(v0 + seg, row.vecs);
   auto kept_weight = [&](float f) -> uint64_t {
     if (order_key(f) <= key) return 0;
     const float e = row.exponential(f);
-    return e >= row.min_p ? Row<T>::fixed(e) : 0;
+    return e >= row.min_p ? Row<T, kThreads>::fixed(e) : 0;
   };
   uint64_t sum = 0;
   uint32_t equal = 0;
@@ -713,8 +734,8 @@ __device__ void general_answer(const Row<T>& row, Shared& s, const SampleParams&
   const int mine = static_cast<int>(row.rank) * kWarps + warp;
   for (int base = 0; base < segs; base += 32) {
     const int i = base + lane;
-    uint64_t w = remote<MULTI>(&s.seg_weight[i % kWarps], i / kWarps);
-    const uint32_t t = remote<MULTI>(&s.seg_ties[i % kWarps], i / kWarps);
+    uint64_t w = i < segs ? remote<MULTI>(&s.seg_weight[i % kWarps], i / kWarps) : 0;
+    const uint32_t t = i < segs ? remote<MULTI>(&s.seg_ties[i % kWarps], i / kWarps) : 0;
     const uint32_t t_inc = static_cast<uint32_t>(warp_inclusive(t));
     const uint32_t t_before = tie_total + t_inc - t;
     const uint32_t t_kept = t_before < ties ? min(t, ties - t_before) : 0;
@@ -773,8 +794,8 @@ __device__ void general_answer(const Row<T>& row, Shared& s, const SampleParams&
 // The token from a list of n <= kShort candidates, at least the first top_k by
 // rank. An entry's rank and what lies before it come from comparing it with all
 // the others, in rank order and again in index order: few barriers, no sort.
-template <typename T>
-__device__ void short_list_answer(const Row<T>& row, Shared& s, const SampleParams& p, int64_t r, int n, int64_t top_k,
+template <typename T, int kThreads>
+__device__ void short_list_answer(const Row<T, kThreads>& row, Shared& s, const SampleParams& p, int64_t r, int n, int64_t top_k,
                                   float top_p, float u) {
   uint64_t* weights = reinterpret_cast<uint64_t*>(&s.hist[0]);
   static_assert(sizeof(s.hist) >= kShort * sizeof(uint64_t) && kShort <= kThreads, "weights in the histograms' place");
@@ -786,7 +807,7 @@ __device__ void short_list_answer(const Row<T>& row, Shared& s, const SamplePara
   if (i < n) {
     mine = s.list[i];
     e = row.exponential(entry_value(mine));
-    weights[i] = w = Row<T>::fixed(e);
+    weights[i] = w = Row<T, kThreads>::fixed(e);
   }
   __syncthreads();
   if (i < n) {
@@ -798,12 +819,12 @@ __device__ void short_list_answer(const Row<T>& row, Shared& s, const SamplePara
   }
   bool keep = i < n && (top_k <= 0 || rank < top_k);
   if (top_p < 1.f) {
-    const uint64_t whole = block_total(s, keep ? w : 0);
+    const uint64_t whole = block_total<kThreads>(s, keep ? w : 0);
     const uint64_t far = by_one(s, [&] { return top_p_goal(top_p, whole); });
     keep = keep && (rank == 0 || before < far);
   }
   keep = keep && (rank == 0 || e >= row.min_p);
-  const uint64_t whole = block_total(s, keep ? w : 0);
+  const uint64_t whole = block_total<kThreads>(s, keep ? w : 0);
   if (i < n) weights[i] = keep ? w : 0;
   const uint64_t goal = by_one(s, [&] { return answer_goal(u, whole); });
   if (keep) {
@@ -814,56 +835,69 @@ __device__ void short_list_answer(const Row<T>& row, Shared& s, const SamplePara
   }
 }
 
+// The segment that holds the answer, of those in s.answer: to found_bin, and what
+// lies before it to found_above. Returns the goal.
+template <int kThreads>
+__device__ uint64_t answer_bin(Shared& s, float u, uint64_t* whole) {
+  constexpr int A = kAnswerBins / kThreads;
+  const Answer& a = s.answer;
+  uint64_t w[A], sum = 0;
+#pragma unroll
+  for (int j = 0; j < A; ++j) {
+    const int b = A * threadIdx.x + j;
+    w[j] = a.lo[b] + (static_cast<uint64_t>(a.hi[b]) << 32);
+    sum += w[j];
+  }
+  uint64_t before = block_exclusive<kThreads>(sum, s.scan, whole);
+  const uint64_t total = *whole, goal = by_one(s, [&] { return answer_goal(u, total); });
+#pragma unroll
+  for (int j = 0; j < A; ++j) {
+    if (before <= goal && goal < before + w[j]) {
+      s.found_bin = A * threadIdx.x + j;
+      s.found_above = before;
+    }
+    before += w[j];
+  }
+  __syncthreads();
+  return goal;
+}
+
 // The same for a long list.
-template <typename T>
-__device__ void list_answer(const Row<T>& row, Shared& s, const SampleParams& p, int64_t r, int n, int64_t top_k,
+template <typename T, int kThreads>
+__device__ void list_answer(const Row<T, kThreads>& row, Shared& s, const SampleParams& p, int64_t r, int n, int64_t top_k,
                             float top_p, float u, float x_hi) {
   const uint64_t lo = list_entry(row.top, 0), hi = list_entry(x_hi, ~0u);
   uint64_t last = ~0ull;  // last entry that the filters by rank keep
-  if (top_k > 0 && n > top_k) last = list_reach<T, false>(row, s, n, lo, hi, 0, static_cast<uint64_t>(top_k));
+  if (top_k > 0 && n > top_k) last = list_reach<T, kThreads, false>(row, s, n, lo, hi, 0, static_cast<uint64_t>(top_k));
   if (top_p < 1.f) {
     uint64_t sum = 0;
     for (int i = threadIdx.x; i < n; i += kThreads)
       if (s.list[i] <= last) sum += row.weight(entry_value(s.list[i]));
-    const uint64_t whole = block_total(s, sum);
+    const uint64_t whole = block_total<kThreads>(s, sum);
     const uint64_t goal = by_one(s, [&] { return top_p_goal(top_p, whole); });
-    last = min(last, list_reach<T, true>(row, s, n, lo, hi, 0, goal));
+    last = min(last, list_reach<T, kThreads, true>(row, s, n, lo, hi, 0, goal));
   }
-  // kept weights by segments of the vocabulary, two per thread
+  // kept weights by segments of the vocabulary, A of them per thread
   Answer& a = s.answer;
-  static_assert(kAnswerBins == 2 * kThreads && kThreads * sizeof(uint32_t) * 2 + sizeof(Answer) <= sizeof(s.hist),
+  constexpr int A = kAnswerBins / kThreads;
+  static_assert(kMostVocab / kAnswerBins * sizeof(uint32_t) + sizeof(Answer) <= sizeof(s.hist),
                 "segments, and the places of the tokens in one");
   const uint32_t width = static_cast<uint32_t>((p.vocab + kAnswerBins - 1) / kAnswerBins);
   __syncthreads();
 #pragma unroll
-  for (int j = 0; j < 2; ++j) a.lo[2 * threadIdx.x + j] = a.hi[2 * threadIdx.x + j] = 0;
+  for (int j = 0; j < A; ++j) a.lo[A * threadIdx.x + j] = a.hi[A * threadIdx.x + j] = 0;
   __syncthreads();
   for (int i = threadIdx.x; i < n; i += kThreads) {
     const uint64_t entry = s.list[i];
     const float e = row.exponential(entry_value(entry));
     if (entry <= last && e >= row.min_p) {
       const uint32_t b = static_cast<uint32_t>(entry) / width;
-      add_weight(&a.lo[b], &a.hi[b], Row<T>::fixed(e));
+      add_weight(&a.lo[b], &a.hi[b], Row<T, kThreads>::fixed(e));
     }
   }
   __syncthreads();
-  uint64_t b2[2], whole;
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int b = 2 * threadIdx.x + j;
-    b2[j] = a.lo[b] + (static_cast<uint64_t>(a.hi[b]) << 32);
-  }
-  uint64_t before = block_exclusive(b2[0] + b2[1], s.scan, &whole);
-  const uint64_t goal = by_one(s, [&] { return answer_goal(u, whole); });
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    if (before <= goal && goal < before + b2[j]) {
-      s.found_bin = 2 * threadIdx.x + j;
-      s.found_above = before;
-    }
-    before += b2[j];
-  }
-  __syncthreads();
+  uint64_t whole;
+  const uint64_t goal = answer_bin<kThreads>(s, u, &whole);
   // the tokens of that segment (at most `width`): each one's running sum is that of those before it
   uint32_t* place = reinterpret_cast<uint32_t*>(&a + 1);
   const uint32_t bin = s.found_bin;
@@ -892,39 +926,46 @@ __device__ void list_answer(const Row<T>& row, Shared& s, const SampleParams& p,
 // min_p), to `acc`; logits from x_hi to x_lo to CTA 0's list. Without CUT every
 // logit counts as above. MIN_P: the row has that filter, and `above` gets what
 // is above without it.
-template <typename T, bool MULTI, bool CUT, bool MIN_P>
-__device__ __forceinline__ void sum_vector(const Row<T>& row, Shared& s, const Raw<T, Row<T>::E>& raw, int v, float x_lo,
+template <typename T, int kThreads, bool MULTI, bool CUT, bool MIN_P>
+__device__ __forceinline__ void sum_vector(const Row<T, kThreads>& row, Shared& s, const Raw<T, Row<T, kThreads>::E>& raw, int v, float x_lo,
                                            float x_hi, Sum& acc, Sum& all, Sum& above) {
-  constexpr int E = Row<T>::E;
+  constexpr int E = Row<T, kThreads>::E;
   float x[E];
   unpack<T, E>(raw, x);
+  bool some = false;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     const float ex = row.exponential(x[e]);
-    const Halves w = halves(ex);
+    const Halves w = halves(ex), none = {0u, 0u};
+    const bool enough = !MIN_P || ex >= row.min_p;
     if (CUT) {
+      const bool over = x[e] >= x_lo;
       all.add(w);
-      if (x[e] >= x_lo) {
-        if (MIN_P) above.add(w);
-        if (!MIN_P || ex >= row.min_p) acc.add(w);
-      } else if (x[e] >= x_hi) {
-        append<MULTI>(s, &s.listed[0], list_entry(x[e], static_cast<uint32_t>(row.c0 + v * E + e)));
-      }
-    } else if (!MIN_P || ex >= row.min_p) {
-      acc.add(w);
+      if (MIN_P) above.add(over ? w : none);
+      acc.add(over && enough ? w : none);
+      some |= !over && x[e] >= x_hi;
+    } else {
+      acc.add(enough ? w : none);
     }
+  }
+  // (asked once for a vector: a branch at each logit cost a third of the pass)
+  if (CUT && some) {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (x[e] >= x_hi && !(x[e] >= x_lo))
+        append<MULTI>(s, &s.listed[0], list_entry(x[e], static_cast<uint32_t>(row.c0 + v * E + e)));
   }
 }
 
 // Adds up this slice's weights: sum_total all of them, sum_above those from x_lo
-// on, seg_weight[] the latter (at least min_p) by segments. Warp w has segments
-// w, w + 32, ..., each a few rounds of 32 vectors; four vectors' loads per lane
+// on, seg_weight[] the latter (at least min_p) by segments. The warps take the
+// segments in turn, each a few rounds of 32 vectors; four vectors' loads per lane
 // are in flight.
-template <typename T, bool MULTI, bool CUT, bool MIN_P>
-__device__ void sum_segments(const Row<T>& row, Shared& s, float x_lo, float x_hi) {
-  constexpr int E = Row<T>::E;
+template <typename T, int kThreads, bool MULTI, bool CUT, bool MIN_P>
+__device__ void sum_segments(const Row<T, kThreads>& row, Shared& s, float x_lo, float x_hi) {
+  constexpr int E = Row<T, kThreads>::E, kWarps = kThreads / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int per = Row<T>::segment_vecs(row.vecs);  // vectors per segment
+  const int per = Row<T, kThreads>::segment_vecs(row.vecs);  // vectors per segment
   const int segs = (row.vecs + per - 1) / per;
   for (int i = threadIdx.x; i < kSegments; i += kThreads)
     if (i >= segs) s.seg_weight[i] = 0;
@@ -942,12 +983,12 @@ __device__ void sum_segments(const Row<T>& row, Shared& s, float x_lo, float x_h
         for (int j = 0; j < 4; ++j) raw[j] = load_raw<T, E>(q + j * 32 * E);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          sum_vector<T, MULTI, CUT, MIN_P>(row, s, raw[j], base + j * 32 + lane, x_lo, x_hi, acc, all, above);
+          sum_vector<T, kThreads, MULTI, CUT, MIN_P>(row, s, raw[j], base + j * 32 + lane, x_lo, x_hi, acc, all, above);
       }
     }
 #pragma unroll 2
     for (int v = base + lane; v < v1; v += 32)
-      sum_vector<T, MULTI, CUT, MIN_P>(row, s, row.get(v), v, x_lo, x_hi, acc, all, above);
+      sum_vector<T, kThreads, MULTI, CUT, MIN_P>(row, s, row.get(v), v, x_lo, x_hi, acc, all, above);
     const uint64_t w = acc.total();
     if (lane == 0) s.seg_weight[seg] = w;
     if (!MIN_P) over += w;
@@ -968,10 +1009,10 @@ __device__ void sum_segments(const Row<T>& row, Shared& s, float x_lo, float x_h
 // The answer from the second pass's sums, by CTA 0: joins the kept part of the
 // list (n entries) with the segments and walks the segment of the answer.
 // Returns false if the exact sums do not confirm that the prefix ends in the list.
-template <typename T, bool MULTI>
-__device__ bool segment_answer(const Row<T>& row, Shared& s, const SampleParams& p, int64_t r, int slice, float top_p,
+template <typename T, int kThreads, bool MULTI>
+__device__ bool segment_answer(const Row<T, kThreads>& row, Shared& s, const SampleParams& p, int64_t r, int slice, float top_p,
                                float u, bool cut, float x_lo, float x_hi) {
-  constexpr int E = Row<T>::E;
+  constexpr int E = Row<T, kThreads>::E;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int vocab = static_cast<int>(p.vocab);
   uint64_t cut_entry = ~0ull;  // last kept entry of the list
@@ -986,17 +1027,18 @@ __device__ bool segment_answer(const Row<T>& row, Shared& s, const SampleParams&
     const uint64_t goal = by_one(s, [&] { return top_p_goal(top_p, total); });
     if (s.listed[0] > static_cast<uint32_t>(kListKeys) || above >= goal) return false;
     // entries of the list lie from x_hi to below x_lo
-    cut_entry = list_reach<T, true>(row, s, n, static_cast<uint64_t>(~(order_key(x_lo) - 1u)) << 32,
+    cut_entry = list_reach<T, kThreads, true>(row, s, n, static_cast<uint64_t>(~(order_key(x_lo) - 1u)) << 32,
                                     static_cast<uint64_t>(~order_key(x_hi)) << 32 | 0xFFFFFFFFu, above, goal);
     if (cut_entry == ~0ull) return false;
     __syncthreads();  // the histogram's place is used again
   }
-  // the segments of all slices, two per thread
+  // the segments of all slices
   Answer& a = s.answer;
+  constexpr int A = kAnswerBins / kThreads;
   static_assert(kAnswerBins == kMaxCluster * kSegments, "a bin per segment of the largest cluster");
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int b = 2 * threadIdx.x + j;
+  for (int j = 0; j < A; ++j) {
+    const int b = A * threadIdx.x + j;
     const uint64_t w = b < static_cast<int>(row.ctas) * kSegments ? remote<MULTI>(&s.seg_weight[b % kSegments], b / kSegments) : 0;
     a.lo[b] = static_cast<uint32_t>(w);
     a.hi[b] = static_cast<uint32_t>(w >> 32);
@@ -1010,33 +1052,18 @@ __device__ bool segment_answer(const Row<T>& row, Shared& s, const SampleParams&
         const int index = static_cast<int>(static_cast<uint32_t>(s.list[i]));
         const int c = index / slice;
         const int vecs = (min(slice, vocab - c * slice) + E - 1) / E;
-        const int b = c * kSegments + (index - c * slice) / E / Row<T>::segment_vecs(vecs);
-        add_weight(&a.lo[b], &a.hi[b], Row<T>::fixed(e));
+        const int b = c * kSegments + (index - c * slice) / E / Row<T, kThreads>::segment_vecs(vecs);
+        add_weight(&a.lo[b], &a.hi[b], Row<T, kThreads>::fixed(e));
       }
     }
     __syncthreads();
   }
-  uint64_t b2[2], whole;
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int b = 2 * threadIdx.x + j;
-    b2[j] = a.lo[b] + (static_cast<uint64_t>(a.hi[b]) << 32);
-  }
-  uint64_t before = block_exclusive(b2[0] + b2[1], s.scan, &whole);
-  const uint64_t goal = by_one(s, [&] { return answer_goal(u, whole); });
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    if (before <= goal && goal < before + b2[j]) {
-      s.found_bin = 2 * threadIdx.x + j;
-      s.found_above = before;
-    }
-    before += b2[j];
-  }
-  __syncthreads();
+  uint64_t whole;
+  const uint64_t goal = answer_bin<kThreads>(s, u, &whole);
   if (warp != 0) return true;
   // one warp walks the segment, from global memory if it is another CTA's
   const int c = static_cast<int>(s.found_bin) / kSegments, seg = static_cast<int>(s.found_bin) % kSegments;
-  Row<T> part = row;
+  Row<T, kThreads> part = row;
   if (c != static_cast<int>(row.rank)) {
     part.data = static_cast<const T*>(p.x) + r * p.ld + static_cast<int64_t>(c) * slice;
     part.padded = false;
@@ -1045,7 +1072,7 @@ __device__ bool segment_answer(const Row<T>& row, Shared& s, const SampleParams&
     part.n = min(slice, vocab - part.c0);
     part.vecs = (part.n + E - 1) / E;
   }
-  const int sub = Row<T>::segment_vecs(part.vecs);
+  const int sub = Row<T, kThreads>::segment_vecs(part.vecs);
   const int v1 = min((seg + 1) * sub, part.vecs);
   uint64_t run = s.found_above;
   Raw<T, E> ahead[4];
@@ -1069,7 +1096,7 @@ __device__ bool segment_answer(const Row<T>& row, Shared& s, const SampleParams&
         if (cut)
           keep = keep && x[e] >= x_hi &&
                  (x[e] >= x_lo || list_entry(x[e], static_cast<uint32_t>(part.c0 + v * E + e)) <= cut_entry);
-        w[e] = keep ? Row<T>::fixed(ex) : 0;
+        w[e] = keep ? Row<T, kThreads>::fixed(ex) : 0;
         sum += w[e];
       }
     }
@@ -1090,14 +1117,14 @@ __device__ bool segment_answer(const Row<T>& row, Shared& s, const SampleParams&
 }
 
 // ---------------------------------------------------------------- the kernel
-template <typename T, bool MULTI>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, const int slice, const int in_smem) {
+template <typename T, int kThreads, bool MULTI>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const SampleParams p, const int slice, const int in_smem) {
   extern __shared__ __align__(16) uint8_t dyn[];
   Shared& s = *reinterpret_cast<Shared*>(dyn);
   T* kept = reinterpret_cast<T*>(dyn + (sizeof(Shared) + 15) / 16 * 16);
-  constexpr int E = Row<T>::E;
+  constexpr int E = Row<T, kThreads>::E, kWarps = kThreads / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  Row<T> row;
+  Row<T, kThreads> row;
   row.rank = 0;
   row.ctas = 1;
   if constexpr (MULTI) {
@@ -1185,7 +1212,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, 
     __syncthreads();
     if (lane == 0) s.red[warp] = k;
     __syncthreads();
-    return key_value(__reduce_max_sync(0xffffffffu, s.red[lane]));
+    return key_value(__reduce_max_sync(0xffffffffu, lane < kWarps ? s.red[lane] : 0u));
   };
   // without a cluster the first part of the row sets the anchor, and the counts
   // of all but that part come with the only read from HBM; a cluster's slices
@@ -1232,7 +1259,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, 
     at = __reduce_min_sync(0xffffffffu, at);
     if (lane == 0) s.red2[warp] = at;
     __syncthreads();
-    at = __reduce_min_sync(0xffffffffu, s.red2[lane]);
+    at = __reduce_min_sync(0xffffffffu, lane < kWarps ? s.red2[lane] : 0xFFFFFFFFu);
     if constexpr (MULTI) {
       if (threadIdx.x == 0) s.first = at;
       row_barrier<MULTI>();
@@ -1269,6 +1296,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, 
       row_barrier<MULTI>();
     }
     if (row.rank == 0) {
+      constexpr int kBinsPerThread = kCountBins / kThreads;
       uint32_t n[kBinsPerThread], n_sum = 0;
       float w[kBinsPerThread], w_sum = 0.f;
 #pragma unroll
@@ -1281,7 +1309,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, 
       }
       uint32_t count_before;
       float weight_before, whole;
-      block_exclusive(s, n_sum, w_sum, &count_before, &weight_before, &whole);
+      block_exclusive<kThreads>(s, n_sum, w_sum, &count_before, &weight_before, &whole);
 #pragma unroll
       for (int j = 0; j < kBinsPerThread; ++j) {
         const uint32_t b = kBinsPerThread * threadIdx.x + j;
@@ -1364,38 +1392,39 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, 
   if (!general) {
     const bool cut = need_counts, min_p = row.min_p > 0.f;
     if (cut && min_p)
-      sum_segments<T, MULTI, true, true>(row, s, x_lo, x_hi);
+      sum_segments<T, kThreads, MULTI, true, true>(row, s, x_lo, x_hi);
     else if (cut)
-      sum_segments<T, MULTI, true, false>(row, s, x_lo, x_hi);
+      sum_segments<T, kThreads, MULTI, true, false>(row, s, x_lo, x_hi);
     else if (min_p)
-      sum_segments<T, MULTI, false, true>(row, s, x_lo, x_hi);
+      sum_segments<T, kThreads, MULTI, false, true>(row, s, x_lo, x_hi);
     else
-      sum_segments<T, MULTI, false, false>(row, s, x_lo, x_hi);
+      sum_segments<T, kThreads, MULTI, false, false>(row, s, x_lo, x_hi);
     row_barrier<MULTI>();
-    if (row.rank == 0 && !segment_answer<T, MULTI>(row, s, p, r, slice, top_p, u, cut, x_lo, x_hi) &&
+    if (row.rank == 0 && !segment_answer<T, kThreads, MULTI>(row, s, p, r, slice, top_p, u, cut, x_lo, x_hi) &&
         threadIdx.x == 0)
       s.general = 1;
     row_barrier<MULTI>();
     general = remote<MULTI>(&s.general, 0) != 0;
     if constexpr (MULTI) row_barrier<MULTI>();  // CTA 0 stays until all have read it
   }
-  if (general) general_answer<T, MULTI>(row, s, p, r, top_k, top_p, u);
+  if (general) general_answer<T, kThreads, MULTI>(row, s, p, r, top_k, top_p, u);
 }
 
-template <typename T>
+template <typename T, int kThreads, bool MULTI>
 cudaError_t run(const SampleParams& p, int ctas, cudaStream_t s) {
-  const size_t shared = (sizeof(Shared) + 15) / 16 * 16;
+  constexpr size_t shared = (sizeof(Shared) + 15) / 16 * 16, most = kMostShared / (1024 / kThreads) / 1024 * 1024;
+  static_assert(shared <= most, "two CTAs of half the threads share an SM");
   const int slice = static_cast<int>(((p.vocab + ctas - 1) / ctas + 63) / 64 * 64);
   const size_t kept = static_cast<size_t>(slice) * sizeof(T);
-  const bool in_smem = shared + kept <= kMostShared;
-  auto kernel = ctas > 1 ? sample_kernel<T, true> : sample_kernel<T, false>;
-  static std::atomic<uint64_t> done[2];
+  const bool in_smem = shared + kept <= most;
+  auto kernel = sample_kernel<T, kThreads, MULTI>;
+  static std::atomic<uint64_t> done{0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
-  if (!(done[ctas > 1].load() >> (dev & 63) & 1)) {
+  if (!(done.load() >> (dev & 63) & 1)) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
     if (e != cudaSuccess) return e;
-    done[ctas > 1].fetch_or(1ull << (dev & 63));
+    done.fetch_or(1ull << (dev & 63));
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.rows * ctas));
@@ -1411,14 +1440,22 @@ cudaError_t run(const SampleParams& p, int ctas, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, kernel, p, slice, in_smem ? 1 : 0);
 }
 
+template <typename T>
+cudaError_t run_typed(const SampleParams& p, int sms, cudaStream_t s) {
+  // One CTA per row where that occupies half of the SMs or more; fewer rows
+  // are spread over clusters, down to 4096 logits per CTA. More rows than SMs
+  // run two to an SM, so that one row's short phases, which wait on barriers, run
+  // under the other's passes: 512 x 129280 fp32 @@ us so, @@ one to an SM.
+  if (p.rows > sms) return run<T, 512, false>(p, 1, s);
+  int ctas = 1;
+  while (ctas < kMaxCluster && p.rows * ctas * 2 <= sms && p.vocab / ctas > 4096) ctas *= 2;
+  return ctas > 1 ? run<T, 1024, true>(p, ctas, s) : run<T, 1024, false>(p, 1, s);
+}
+
 }  // namespace
 
 cudaError_t launch_sample(const SampleParams& p, int sms, cudaStream_t s) {
-  // One CTA per row where that occupies half of the SMs or more; fewer rows
-  // are spread over clusters, down to 4096 logits per CTA.
-  int ctas = 1;
-  while (ctas < kMaxCluster && p.rows * ctas * 2 <= sms && p.vocab / ctas > 4096) ctas *= 2;
-  return p.dtype == FLCE_DTYPE_F32 ? run<float>(p, ctas, s) : run<uint16_t>(p, ctas, s);
+  return p.dtype == FLCE_DTYPE_F32 ? run_typed<float>(p, sms, s) : run_typed<uint16_t>(p, sms, s);
 }
 
 }  // namespace flce
