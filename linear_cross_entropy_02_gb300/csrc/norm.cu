@@ -255,24 +255,107 @@ __global__ void __launch_bounds__(kMaxThreads) norm_long_kernel(const NormParams
 }
 
 // ------------------------------------------------------------------ backward
+// Where a row's vectors lie. With SHIFT rows need not start on a vector boundary:
+// vectors are counted from the boundary before the row, `off` elements earlier, and
+// the first and last of them may hold elements that are not the row's. (10007 x 1337
+// bf16: 52 us so, 75 by single elements. Aligned rows have kernels without all this,
+// which cost them a tenth.)
+struct Place {
+  int hidden, off, vecs;
+  template <int E>
+  __device__ __forceinline__ bool inside(int v) const {
+    return v * E >= off && (v + 1) * E - off <= hidden;
+  }
+};
+// What x, grad_y and grad_x have in common: the distance of `row` from a boundary.
+template <typename T, int E, bool SHIFT>
+__device__ __forceinline__ Place place_of(const NormParams& p, int64_t row) {
+  const int64_t at = static_cast<int64_t>(reinterpret_cast<uintptr_t>(p.x) / sizeof(T)) + row * p.ld_x;
+  const int off = SHIFT ? static_cast<int>(at % E) : 0, hidden = static_cast<int>(p.hidden);
+  return {hidden, off, (hidden + off + E - 1) / E};
+}
+// Whether vector v of the row lies between the first row's first element and the
+// last row's last, as its neighbours' elements may be read but nothing else.
+template <int E>
+__device__ __forceinline__ bool in_matrix(const Place& pl, int64_t row, int64_t ld, int64_t rows, int v) {
+  const int64_t start = row * ld + v * E - pl.off;
+  return start >= 0 && start + E <= (rows - 1) * ld + pl.hidden;
+}
+// Vector v of the row (`base`: its element of index 0 of that vector), elements of the row only.
+template <typename T, int E>
+__device__ __forceinline__ Raw<T, E> load_edge(const T* base, const Place& pl, int v) {
+  float f[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int i = v * E - pl.off + e;
+    f[e] = i >= 0 && i < pl.hidden ? to_float<T>(base[e]) : 0.f;
+  }
+  return pack<T, E>(f);
+}
+template <typename T, int E>
+__device__ __forceinline__ void mask_edge(Raw<T, E>& r, const Place& pl, int v) {
+  float f[E];
+  unpack<T, E>(r, f);
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int i = v * E - pl.off + e;
+    if (i < 0 || i >= pl.hidden) f[e] = 0.f;
+  }
+  r = pack<T, E>(f);
+}
+
+// A thread's weights where they are not on vector boundaries themselves: as fp32 in
+// shared memory, in vectors of four `stride` apart; ones if the norm has none,
+// zeros beside the row.
+template <int E>
+struct Weights {
+  static constexpr int per = E / 4;
+  float4* v;
+  int stride;
+  __device__ __forceinline__ void fill(const NormParams& p, const Place& pl, int c, int vec) const {
+    float w[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int i = vec * E - pl.off + e;
+      float one[1] = {0.f};
+      if (i >= 0 && i < pl.hidden) {
+        one[0] = 1.f;
+        if (p.weight) load_weight<1>(p.weight, p.w_f32 != 0, i, one);
+      }
+      w[e] = one[0];
+    }
+#pragma unroll
+    for (int k = 0; k < per; ++k)
+      v[(c * per + k) * stride] = make_float4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+  }
+  __device__ __forceinline__ void get(int c, float (&w)[E]) const {
+#pragma unroll
+    for (int k = 0; k < per; ++k) {
+      const float4 q = v[(c * per + k) * stride];
+      w[4 * k] = q.x;
+      w[4 * k + 1] = q.y;
+      w[4 * k + 2] = q.z;
+      w[4 * k + 3] = q.w;
+    }
+  }
+};
+
 // One vector before its row's sums are known: with d = x - mean and
 // g = rstd grad_y w, adds grad_y xhat and grad_y to the columns' sums and g and
-// g d to the row's, and leaves d and g for after them.
+// g d to the row's, and leaves g for after them.
 template <typename T, int E, int NB, bool RMS>
-__device__ __forceinline__ void bwd_visit(const Raw<T, E>& rx, const Raw<T, E>& rg, const NormParams& p, int i, float mean,
-                                          float rstd, float (&d)[E], float (&g)[E], float (&acc_w)[E], float (&acc_b)[E],
+__device__ __forceinline__ void bwd_visit(const Raw<T, E>& rx, const Raw<T, E>& rg, bool weighted, const float (&w)[E],
+                                          float mean, float rstd, float (&d)[E], float (&g)[E], float (&acc_w)[E], float (&acc_b)[E],
                                           float& sg, float& sgd) {
   unpack<T, E>(rx, d);
   unpack<T, E>(rg, g);
-  float w[E];
-  if (p.weight) load_weight<E>(p.weight, p.w_f32 != 0, i, w);
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     if (!RMS) d[e] -= mean;
     if (NB == 2) acc_b[e] += g[e];
     g[e] *= rstd;
     acc_w[e] += g[e] * d[e];
-    if (p.weight) g[e] *= w[e];
+    if (weighted) g[e] *= w[e];
     if (!RMS) sg += g[e];
     sgd += g[e] * d[e];
   }
@@ -280,79 +363,110 @@ __device__ __forceinline__ void bwd_visit(const Raw<T, E>& rx, const Raw<T, E>& 
 
 // grad_x = g + c0 + c2 d, c0 = -mean(g), c2 = -rstd^2 mean(g d).
 template <typename T, int E, bool RMS>
-__device__ __forceinline__ Raw<T, E> bwd_out(const float (&d)[E], const float (&g)[E], float c0, float c2) {
+__device__ __forceinline__ void bwd_out(T* o, const float (&d)[E], const float (&g)[E], float c0, float c2, bool inside,
+                                        const Place& pl, int vec) {
   float v[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) v[e] = d[e] * c2 + (RMS ? g[e] : g[e] + c0);
-  return pack<T, E>(v);
+  if (inside) {
+    store_raw<T, E>(o, pack<T, E>(v));
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int i = vec * E - pl.off + e;
+      if (i >= 0 && i < pl.hidden) o[e] = from_float<T>(v[e]);
+    }
+  }
 }
 
 template <typename T, int E>
 constexpr bool kRing = sizeof(T) * E >= 4;  // the smallest asynchronous copy is of 4 bytes
 
-// A row per CTA at a time. The ring's vectors are private to the thread that
-// copies them, so it needs no barrier of its own. Single bf16 elements are
-// loaded a row ahead into registers instead. REGS: with 72 registers two CTAs
-// of up to 448 threads share an SM (a row of 7168 bf16 elements).
-template <typename T, int E, int C, int NB, int REGS, bool RMS>
-__global__ void __maxnreg__(REGS) norm_bwd_cta_kernel(const NormParams p, const int stages) {
-  constexpr bool RING = kRing<T, E>;
-  extern __shared__ __align__(16) uint8_t dyn[];
-  __shared__ BlockSums sums;
-  int slot = 0;
-  Raw<T, E>* ring = reinterpret_cast<Raw<T, E>*>(dyn);
-  const int H = static_cast<int>(p.hidden), vecs = H / E;
-  const int t = threadIdx.x, T_ = blockDim.x;
-  const T* x = static_cast<const T*>(p.x) + t * E;
-  const T* gy = static_cast<const T*>(p.gy) + t * E;
-  T* gx = static_cast<T*>(p.out);
-  const float inv_h = 1.f / static_cast<float>(H);
+// C vectors per thread of a row, `stride` apart, and the ring of rows ahead: what
+// both kernels below share. KEEP: x - mean stays in registers until the row's sums
+// are known; else it is made again from the ring, and the registers serve for more
+// threads. (32768 x 7168 bf16 RMS: 278 us with, 267 without, 252 with a ring of two
+// stages instead of three; but a warp's rows of 576 with a bias 57 with, 62 without.)
+template <typename T, int E, int C, int NB, bool RMS, bool SHIFT, bool KEEP>
+struct BwdRow {
+  static_assert(E > 1 || !SHIFT, "single elements are always in place");
+  static constexpr bool RING = kRing<T, E>;
+  const NormParams& p;
+  Place pl;
+  int t, stride, threads;  // first vector, distance between vectors, distance in the ring
+  Raw<T, E>* ring;
+  Weights<E> weights;  // SHIFT
+  uint32_t inside = 0;
+  Raw<T, E> next_x[RING ? 1 : C], next_g[RING ? 1 : C];
   float acc_w[C][E], acc_b[C][E];
-#pragma unroll
-  for (int c = 0; c < C; ++c)
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc_w[c][e] = acc_b[c][e] = 0.f;
 
-  Raw<T, E> next_x[C], next_g[C];
-  auto fetch = [&](int64_t row, int stage) {
+  __device__ __forceinline__ BwdRow(const NormParams& params, const Place& place, int first, int apart, int ring_apart,
+                                    Raw<T, E>* r, const Weights<E>& w)
+      : p(params), pl(place), t(first), stride(apart), threads(ring_apart), ring(r), weights(w) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      if constexpr (SHIFT) {
+        if (pl.template inside<E>(t + c * stride)) inside |= 1u << c;
+        if (t + c * stride < pl.vecs) weights.fill(p, pl, c, t + c * stride);
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc_w[c][e] = acc_b[c][e] = 0.f;
+    }
+  }
+  __device__ __forceinline__ bool is_inside(int c) const { return !SHIFT || (inside >> c & 1u); }
+
+  __device__ __forceinline__ void fetch(int64_t row, int stage) {
     if (row < p.rows) {
-      const T* xr = x + row * p.ld_x;
-      const T* gr = gy + row * p.ld_gy;
-      Raw<T, E>* to = ring + stage * 2 * C * T_ + t;
+      const T* xr = static_cast<const T*>(p.x) + row * p.ld_x + (t * E - pl.off);
+      const T* gr = static_cast<const T*>(p.gy) + row * p.ld_gy + (t * E - pl.off);
+      Raw<T, E>* to = ring + stage * 2 * C * threads;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        if (t + c * T_ < vecs) {
+        const int v = t + c * stride;
+        if (v < pl.vecs) {
           if constexpr (RING) {
-            copy_async<sizeof(T) * E>(to + c * T_, xr + c * T_ * E);
-            copy_async<sizeof(T) * E>(to + (C + c) * T_, gr + c * T_ * E);
+            if (is_inside(c) || (in_matrix<E>(pl, row, p.ld_x, p.rows, v) && in_matrix<E>(pl, row, p.ld_gy, p.rows, v))) {
+              copy_async<sizeof(T) * E>(to + c * threads, xr + c * stride * E);
+              copy_async<sizeof(T) * E>(to + (C + c) * threads, gr + c * stride * E);
+            } else {
+              to[c * threads] = load_edge<T, E>(xr + c * stride * E, pl, v);
+              to[(C + c) * threads] = load_edge<T, E>(gr + c * stride * E, pl, v);
+            }
           } else {
-            next_x[c] = load_raw<T, E>(xr + c * T_ * E);
-            next_g[c] = load_raw<T, E>(gr + c * T_ * E);
+            next_x[c] = load_raw<T, E>(xr + c * stride * E);
+            next_g[c] = load_raw<T, E>(gr + c * stride * E);
           }
         }
       }
     }
     if constexpr (RING) copies_commit();
-  };
+  }
 
-  int64_t row = blockIdx.x;
-  for (int i = 0; i < stages - 1; ++i) fetch(row + static_cast<int64_t>(i) * gridDim.x, i);
-  float mean = !RMS && row < p.rows ? __ldg(p.mean + row) : 0.f, rstd = row < p.rows ? __ldg(p.rstd + row) : 0.f;
-  int stage = 0, fill = stages - 1;
-  for (; row < p.rows; row += gridDim.x) {
-    Raw<T, E> rx[C], rg[C];
+  // Vector c of the row in `stage`; `rx` where there is no ring.
+  __device__ __forceinline__ Raw<T, E> take(int stage, int which, int c, const Raw<T, E>& held) const {
+    if constexpr (RING) {
+      Raw<T, E> r = ring[stage * 2 * C * threads + (which * C + c) * threads];
+      if (SHIFT && !is_inside(c)) mask_edge<T, E>(r, pl, t + c * stride);
+      return r;
+    } else {
+      return held;
+    }
+  }
+
+  // The row in `stage` (vecs: 0 in threads without a row), the row that is `ahead`
+  // fetched meanwhile; sum(sgd, sg) adds up over the row's threads.
+  template <typename S>
+  __device__ __forceinline__ void visit(int64_t row, int vecs, int stage, int64_t ahead, int fill, float mean, float rstd,
+                                        int stages, S sum) {
+    Raw<T, E> hx[RING ? 1 : C], hg[RING ? 1 : C];
     if constexpr (!RING) {
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        rx[c] = next_x[c];
-        rg[c] = next_g[c];
+        hx[c] = next_x[c];
+        hg[c] = next_g[c];
       }
     }
-    fetch(row + static_cast<int64_t>(stages - 1) * gridDim.x, fill);
-    // the next row's statistics are on their way too
-    const int64_t after = row + gridDim.x;
-    const float next_mean = !RMS && after < p.rows ? __ldg(p.mean + after) : 0.f;
-    const float next_rstd = after < p.rows ? __ldg(p.rstd + after) : 0.f;
+    fetch(ahead, fill);
     if constexpr (RING) {
       if (stages == 4)
         copies_wait<3>();
@@ -363,133 +477,123 @@ __global__ void __maxnreg__(REGS) norm_bwd_cta_kernel(const NormParams p, const 
       else
         copies_wait<0>();
     }
-    float d[C][E], g[C][E], sg = 0.f, sgd = 0.f;
-    const Raw<T, E>* from = ring + stage * 2 * C * T_ + t;
+    float d[KEEP ? C : 1][E], g[C][E], sg = 0.f, sgd = 0.f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      if (t + c * T_ < vecs) {
-        if constexpr (RING)
-          bwd_visit<T, E, NB, RMS>(from[c * T_], from[(C + c) * T_], p, (t + c * T_) * E, mean, rstd, d[c], g[c], acc_w[c], acc_b[c],
-                              sg, sgd);
-        else
-          bwd_visit<T, E, NB, RMS>(rx[c], rg[c], p, (t + c * T_) * E, mean, rstd, d[c], g[c], acc_w[c], acc_b[c], sg, sgd);
+      if (t + c * stride < vecs) {
+        float w[E];
+        if constexpr (SHIFT)
+          weights.get(c, w);
+        else if (p.weight)
+          load_weight<E>(p.weight, p.w_f32 != 0, (t + c * stride) * E, w);
+        bwd_visit<T, E, NB, RMS>(take(stage, 0, c, hx[RING ? 0 : c]), take(stage, 1, c, hg[RING ? 0 : c]),
+                                 SHIFT || p.weight != nullptr, w, mean, rstd,
+                                 d[KEEP ? c : 0], g[c], acc_w[c], acc_b[c], sg, sgd);
       }
     }
-    if (gx) {
-      block_sum<!RMS>(sgd, sg, sums, slot);
+    if (p.out) {
+      sum(sgd, sg);
+      const float inv_h = 1.f / static_cast<float>(pl.hidden);
       const float c0 = RMS ? 0.f : -sg * inv_h, c2 = -rstd * rstd * (sgd * inv_h);
-      T* o = gx + row * p.hidden + t * E;
+      T* o = static_cast<T*>(p.out) + row * p.hidden + (t * E - pl.off);
 #pragma unroll
-      for (int c = 0; c < C; ++c)
-        if (t + c * T_ < vecs) store_raw<T, E>(o + c * T_ * E, bwd_out<T, E, RMS>(d[c], g[c], c0, c2));
+      for (int c = 0; c < C; ++c) {
+        if (t + c * stride < vecs) {
+          if (!KEEP) {
+            unpack<T, E>(take(stage, 0, c, hx[RING ? 0 : c]), d[0]);
+            if (!RMS) {
+#pragma unroll
+              for (int e = 0; e < E; ++e) d[0][e] -= mean;
+            }
+          }
+          bwd_out<T, E, RMS>(o + c * stride * E, d[KEEP ? c : 0], g[c], c0, c2, is_inside(c), pl, t + c * stride);
+        }
+      }
     }
+  }
+
+  // f(column, c, e) for this thread's columns.
+  template <typename F>
+  __device__ __forceinline__ void columns(F f) const {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int i = (t + c * stride) * E - pl.off + e;
+        if (SHIFT ? i >= 0 && i < pl.hidden : t + c * stride < pl.vecs) f(i, c, e);
+      }
+    }
+  }
+};
+
+// A row per CTA at a time. The ring's vectors are private to the thread that
+// copies them, so it needs no barrier of its own. Single bf16 elements are
+// loaded a row ahead into registers instead. A CTA's rows are a multiple of eight
+// apart, so that they all start at the same distance from a vector boundary and
+// its threads keep their columns. REGS: with 72 registers two CTAs of up to 448
+// threads share an SM (a row of 7168 bf16 elements).
+template <typename T, int E, int C, int NB, int REGS, bool RMS, bool SHIFT>
+__global__ void __maxnreg__(REGS) norm_bwd_cta_kernel(const NormParams p, const int stages) {
+  constexpr bool RING = kRing<T, E>;
+  extern __shared__ __align__(16) uint8_t dyn[];
+  __shared__ BlockSums sums;
+  int slot = 0;
+  const int T_ = blockDim.x;
+  float4* w = reinterpret_cast<float4*>(dyn);
+  Raw<T, E>* ring = reinterpret_cast<Raw<T, E>*>(w + (SHIFT ? C * Weights<E>::per * T_ : 0)) + threadIdx.x;
+  int64_t row = blockIdx.x;
+  BwdRow<T, E, C, NB, RMS, SHIFT, false> r(p, place_of<T, E, SHIFT>(p, row), threadIdx.x, T_, T_, ring, {w + threadIdx.x, T_});
+  for (int i = 0; i < stages - 1; ++i) r.fetch(row + static_cast<int64_t>(i) * gridDim.x, i);
+  float mean = !RMS && row < p.rows ? __ldg(p.mean + row) : 0.f, rstd = row < p.rows ? __ldg(p.rstd + row) : 0.f;
+  int stage = 0, fill = stages - 1;
+  for (; row < p.rows; row += gridDim.x) {
+    // the next row's statistics are on their way too
+    const int64_t after = row + gridDim.x;
+    const float next_mean = !RMS && after < p.rows ? __ldg(p.mean + after) : 0.f;
+    const float next_rstd = after < p.rows ? __ldg(p.rstd + after) : 0.f;
+    r.visit(row, r.pl.vecs, stage, row + static_cast<int64_t>(stages - 1) * gridDim.x, fill, mean, rstd, stages,
+            [&](float& sgd, float& sg) { block_sum<!RMS>(sgd, sg, sums, slot); });
     mean = next_mean;
     rstd = next_rstd;
     if (++stage == stages) stage = 0;
     if (++fill == stages) fill = 0;
   }
   if constexpr (RING) copies_wait<0>();
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    if (t + c * T_ < vecs) {
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int64_t at = blockIdx.x * p.hidden + (t + c * T_) * E + e;
-        if (p.part_w) p.part_w[at] = acc_w[c][e];
-        if (NB == 2 && p.part_b) p.part_b[at] = acc_b[c][e];
-      }
-    }
-  }
+  r.columns([&](int i, int c, int e) {
+    if (p.part_w) p.part_w[blockIdx.x * p.hidden + i] = r.acc_w[c][e];
+    if (NB == 2 && p.part_b) p.part_b[blockIdx.x * p.hidden + i] = r.acc_b[c][e];
+  });
 }
 
 // Rows on groups of `lanes` lanes (32, or fewer if the row has fewer vectors),
 // each with a ring of its own; no barrier until the CTA's groups add up their
-// sums, in order.
-template <typename T, int E, int C, int NB, bool RMS>
+// sums, in order. A group's rows are a multiple of eight apart, too.
+template <typename T, int E, int C, int NB, bool RMS, bool SHIFT>
 __global__ void __launch_bounds__(kWarpRowThreads)
     norm_bwd_warp_kernel(const NormParams p, const int lanes, const int stages) {
   constexpr bool RING = kRing<T, E>;
   extern __shared__ __align__(16) uint8_t dyn[];
-  Raw<T, E>* ring = reinterpret_cast<Raw<T, E>*>(dyn) + threadIdx.x;
-  const int H = static_cast<int>(p.hidden), vecs = H / E;
+  float4* w = reinterpret_cast<float4*>(dyn);
+  Raw<T, E>* ring = reinterpret_cast<Raw<T, E>*>(w + (SHIFT ? C * Weights<E>::per * kWarpRowThreads : 0)) + threadIdx.x;
+  const int H = static_cast<int>(p.hidden);
   const int t = threadIdx.x & (lanes - 1), group = threadIdx.x / lanes, groups = kWarpRowThreads / lanes;
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
-  const T* x = static_cast<const T*>(p.x) + t * E;
-  const T* gy = static_cast<const T*>(p.gy) + t * E;
-  T* gx = static_cast<T*>(p.out);
-  const float inv_h = 1.f / static_cast<float>(H);
-  float acc_w[C][E], acc_b[C][E];
-#pragma unroll
-  for (int c = 0; c < C; ++c)
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc_w[c][e] = acc_b[c][e] = 0.f;
-  Raw<T, E> next_x[C], next_g[C];
-  auto fetch = [&](int64_t row, int stage) {
-    if (row < p.rows) {
-      const T* xr = x + row * p.ld_x;
-      const T* gr = gy + row * p.ld_gy;
-      Raw<T, E>* to = ring + stage * 2 * C * kWarpRowThreads;
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        if (t + c * 32 < vecs) {
-          if constexpr (RING) {
-            copy_async<sizeof(T) * E>(to + c * kWarpRowThreads, xr + c * 32 * E);
-            copy_async<sizeof(T) * E>(to + (C + c) * kWarpRowThreads, gr + c * 32 * E);
-          } else {
-            next_x[c] = load_raw<T, E>(xr + c * 32 * E);
-            next_g[c] = load_raw<T, E>(gr + c * 32 * E);
-          }
-        }
-      }
-    }
-    if constexpr (RING) copies_commit();
-  };
   // whole warps go through the loop together: the groups' sums are shuffles of the warp
   const int64_t first = static_cast<int64_t>(blockIdx.x) * groups + (threadIdx.x >> 5) * (32 / lanes);
   int64_t row = first + (threadIdx.x & 31) / lanes;
-  for (int i = 0; i < stages - 1; ++i) fetch(row + i * step, i);
+  BwdRow<T, E, C, NB, RMS, SHIFT, NB == 2> r(p, place_of<T, E, SHIFT>(p, row), t, 32, kWarpRowThreads, ring,
+                                    {w + threadIdx.x, kWarpRowThreads});
+  for (int i = 0; i < stages - 1; ++i) r.fetch(row + i * step, i);
   float mean = !RMS && row < p.rows ? __ldg(p.mean + row) : 0.f, rstd = row < p.rows ? __ldg(p.rstd + row) : 0.f;
   int stage = 0, fill = stages - 1;
   for (int64_t base = first; base < p.rows; base += step, row += step) {
-    Raw<T, E> rx[C], rg[C];
-    if constexpr (!RING) {
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        rx[c] = next_x[c];
-        rg[c] = next_g[c];
-      }
-    }
-    fetch(row + (stages - 1) * step, fill);
     const int64_t n = row + step;
     const float next_mean = !RMS && n < p.rows ? __ldg(p.mean + n) : 0.f, next_rstd = n < p.rows ? __ldg(p.rstd + n) : 0.f;
-    if constexpr (RING) {
-      if (stages == 4)
-        copies_wait<3>();
-      else
-        copies_wait<2>();
-    }
-    const int here = row < p.rows ? vecs : 0;
-    float d[C][E], g[C][E], sg = 0.f, sgd = 0.f;
-    const Raw<T, E>* from = ring + stage * 2 * C * kWarpRowThreads;
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      if (t + c * 32 < here) {
-        if constexpr (RING)
-          bwd_visit<T, E, NB, RMS>(from[c * kWarpRowThreads], from[(C + c) * kWarpRowThreads], p, (t + c * 32) * E, mean, rstd, d[c],
-                              g[c], acc_w[c], acc_b[c], sg, sgd);
-        else
-          bwd_visit<T, E, NB, RMS>(rx[c], rg[c], p, (t + c * 32) * E, mean, rstd, d[c], g[c], acc_w[c], acc_b[c], sg, sgd);
-      }
-    }
-    if (gx) {
-      if (!RMS) sg = group_sum(sg, lanes);
-      sgd = group_sum(sgd, lanes);
-      const float c0 = RMS ? 0.f : -sg * inv_h, c2 = -rstd * rstd * (sgd * inv_h);
-      T* o = gx + row * p.hidden + t * E;
-#pragma unroll
-      for (int c = 0; c < C; ++c)
-        if (t + c * 32 < here) store_raw<T, E>(o + c * 32 * E, bwd_out<T, E, RMS>(d[c], g[c], c0, c2));
-    }
+    r.visit(row, row < p.rows ? r.pl.vecs : 0, stage, row + (stages - 1) * step, fill, mean, rstd, stages,
+            [&](float& sgd, float& sg) {
+              if (!RMS) sg = group_sum(sg, lanes);
+              sgd = group_sum(sgd, lanes);
+            });
     mean = next_mean;
     rstd = next_rstd;
     if (++stage == stages) stage = 0;
@@ -502,13 +606,7 @@ __global__ void __launch_bounds__(kWarpRowThreads)
     float* part = which == 0 ? p.part_w : p.part_b;
     if (part == nullptr) continue;
     __syncthreads();
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      if (t + c * 32 < vecs) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) comb[group * H + (t + c * 32) * E + e] = which == 0 ? acc_w[c][e] : acc_b[c][e];
-      }
-    }
+    r.columns([&](int i, int c, int e) { comb[group * H + i] = which == 0 ? r.acc_w[c][e] : r.acc_b[c][e]; });
     __syncthreads();
     for (int i = threadIdx.x; i < H; i += kWarpRowThreads) {
       float v = 0.f;
@@ -578,7 +676,7 @@ __global__ void __launch_bounds__(1024) norm_wgrad_kernel(const float* part_w, c
   const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x;
   float v = 0.f;
   if (col < hidden) {
-#pragma unroll 4
+#pragma unroll 8
     for (int i = threadIdx.y; i < partials; i += 32) v += part[i * hidden + col];
   }
   s[threadIdx.y][threadIdx.x] = v;
@@ -600,6 +698,15 @@ bool vectors(const NormParams& p) {
   const size_t es = p.dtype == FLCE_DTYPE_F32 ? 4 : 2;
   return aligned(p.x, p.ld_x, es) && aligned(p.gy, p.ld_gy, es) && aligned(p.out, p.hidden, es) &&
          p.hidden % (16 / es) == 0 && aligned(p.weight, 0, 1) && aligned(p.bias, 0, 1);
+}
+
+// Whether a row starts at the same distance from a 16-byte boundary in x, grad_y
+// and grad_x, so that the same vectors serve for all of them.
+bool in_step(const NormParams& p) {
+  const int64_t es = p.dtype == FLCE_DTYPE_F32 ? 4 : 2, E = 16 / es;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(p.x) % 16;
+  return p.hidden >= 2 * E && (p.ld_x - p.hidden) % E == 0 && (p.ld_gy - p.hidden) % E == 0 &&
+         reinterpret_cast<uintptr_t>(p.gy) % 16 == x && (!p.out || reinterpret_cast<uintptr_t>(p.out) % 16 == x);
 }
 
 inline unsigned grid_of(int64_t want, int64_t most) { return static_cast<unsigned>(want < most ? want : most); }
@@ -654,6 +761,7 @@ cudaError_t run_fwd(const NormParams& p, int sms, cudaStream_t s) {
 }
 
 constexpr size_t kMostShared = 220 * 1024;
+constexpr int kCtaStages = 2;  // see BwdRow
 
 // Launches k with dynamic shared memory above the default limit.
 template <typename K, typename... A>
@@ -669,46 +777,57 @@ cudaError_t launch_large(K k, std::atomic<uint64_t>& done, unsigned grid, int th
   return cudaGetLastError();
 }
 
-template <typename T, int E, int NB, bool RMS>
+// Most vectors of a row.
+inline int64_t most_vecs(int64_t hidden, int E, bool shift) { return shift ? (hidden + 2 * E - 2) / E : hidden / E; }
+
+template <typename T, int E, int NB, bool RMS, bool SHIFT>
 cudaError_t run_bwd_row(const NormParams& p, int sms, int* partials, cudaStream_t s) {
-  const int64_t vecs = p.hidden / E;
+  const int64_t vecs = most_vecs(p.hidden, E, SHIFT);
+  static std::atomic<uint64_t> done[2];
   if (vecs <= 32 * warp_vecs(E)) {
     constexpr int C = warp_vecs(E);
     const int lanes = lanes_for(vecs);
     const int64_t groups = kWarpRowThreads / lanes;
     // one vector per lane: three rows ahead are few registers and little shared memory
-    const int c = vecs <= 32 ? 1 : C, stages = !kRing<T, E> ? 2 : vecs <= 32 ? 4 : 3;
-    const size_t ring = kRing<T, E> ? static_cast<size_t>(kWarpRowThreads) * c * 2 * sizeof(Raw<T, E>) * stages : 0;
+    const int c = vecs <= 32 ? 1 : C, stages = !kRing<T, E> ? 2 : vecs <= 32 ? 4 : SHIFT ? 2 : 3;
+    const size_t ring = static_cast<size_t>(kWarpRowThreads) * c *
+                        ((kRing<T, E> ? 2 * sizeof(Raw<T, E>) * stages : 0) + (SHIFT ? E * sizeof(float) : 0));
     const size_t comb = static_cast<size_t>(groups) * p.hidden * sizeof(float);
     const size_t smem = ring > comb ? ring : comb;
     const unsigned grid = grid_of((p.rows + groups - 1) / groups, static_cast<int64_t>(sms) * (vecs <= 32 ? 4 : 2));
     *partials = static_cast<int>(grid);
-    static std::atomic<uint64_t> done[2];
     if (vecs <= 32)
-      return launch_large(norm_bwd_warp_kernel<T, E, 1, NB, RMS>, done[0], grid, kWarpRowThreads, smem, s, p, lanes, stages);
-    return launch_large(norm_bwd_warp_kernel<T, E, C, NB, RMS>, done[1], grid, kWarpRowThreads, smem, s, p, lanes, stages);
+      return launch_large(norm_bwd_warp_kernel<T, E, 1, NB, RMS, SHIFT>, done[0], grid, kWarpRowThreads, smem, s, p, lanes, stages);
+    return launch_large(norm_bwd_warp_kernel<T, E, C, NB, RMS, SHIFT>, done[1], grid, kWarpRowThreads, smem, s, p, lanes, stages);
   }
   constexpr int C = cta_vecs(E);
   const int threads = static_cast<int>(((vecs + C - 1) / C + 31) / 32 * 32);
   const int regs = threads <= 448 ? 72 : 64;
   int ctas = 65536 / (regs * threads);
   if (ctas > bwd_ctas(p.hidden)) ctas = bwd_ctas(p.hidden);
+  const size_t weights = SHIFT ? static_cast<size_t>(threads) * C * E * sizeof(float) : 0;
   const size_t row = kRing<T, E> ? static_cast<size_t>(threads) * C * 2 * sizeof(Raw<T, E>) : 0;
-  int stages = kRing<T, E> ? 3 : 2;
-  while (stages > 1 && row * stages * ctas > kMostShared) --stages;
-  const unsigned grid = grid_of(p.rows, static_cast<int64_t>(sms) * ctas);
+  int stages = !kRing<T, E> ? 2 : kCtaStages;
+  while (stages > 1 && (row * stages + weights) * ctas > kMostShared) --stages;
+  // rows that a CTA visits are a multiple of eight apart
+  int64_t grid = static_cast<int64_t>(sms) * ctas;
+  grid = p.rows <= grid ? p.rows : grid / 8 * 8;
   *partials = static_cast<int>(grid);
-  static std::atomic<uint64_t> done[2];
+  const unsigned n = static_cast<unsigned>(grid);
+  const size_t smem = row * stages + weights;
+  static std::atomic<uint64_t> opted[2];
   if (regs == 72)
-    return launch_large(norm_bwd_cta_kernel<T, E, C, NB, 72, RMS>, done[0], grid, threads, row * stages, s, p, stages);
-  return launch_large(norm_bwd_cta_kernel<T, E, C, NB, 64, RMS>, done[1], grid, threads, row * stages, s, p, stages);
+    return launch_large(norm_bwd_cta_kernel<T, E, C, NB, 72, RMS, SHIFT>, opted[0], n, threads, smem, s, p, stages);
+  return launch_large(norm_bwd_cta_kernel<T, E, C, NB, 64, RMS, SHIFT>, opted[1], n, threads, smem, s, p, stages);
 }
 
-template <typename T, int E>
+template <typename T, int E, bool SHIFT>
 cudaError_t run_bwd(const NormParams& p, int sms, int* partials, cudaStream_t s) {
-  if (p.hidden / E <= static_cast<int64_t>(kMaxThreads) * cta_vecs(E))
-    return p.part_b ? (p.rms ? run_bwd_row<T, E, 2, true>(p, sms, partials, s) : run_bwd_row<T, E, 2, false>(p, sms, partials, s))
-                    : (p.rms ? run_bwd_row<T, E, 1, true>(p, sms, partials, s) : run_bwd_row<T, E, 1, false>(p, sms, partials, s));
+  if (most_vecs(p.hidden, E, SHIFT) <= static_cast<int64_t>(kMaxThreads) * cta_vecs(E)) {
+    if (p.part_b)
+      return p.rms ? run_bwd_row<T, E, 2, true, SHIFT>(p, sms, partials, s) : run_bwd_row<T, E, 2, false, SHIFT>(p, sms, partials, s);
+    return p.rms ? run_bwd_row<T, E, 1, true, SHIFT>(p, sms, partials, s) : run_bwd_row<T, E, 1, false, SHIFT>(p, sms, partials, s);
+  }
   if (p.out) {
     norm_bwd_long_kernel<T><<<grid_of(p.rows, 2LL * sms), kMaxThreads, 0, s>>>(p);
     const cudaError_t e = cudaGetLastError();
@@ -735,10 +854,14 @@ cudaError_t launch_norm(const NormParams& p, int sms, cudaStream_t s) {
   return vectors(p) ? run_fwd<uint16_t, 8>(p, sms, s) : run_fwd<uint16_t, 1>(p, sms, s);
 }
 
+template <typename T, int E>
+static cudaError_t launch_bwd(const NormParams& p, int sms, int* partials, cudaStream_t s) {
+  if (vectors(p)) return run_bwd<T, E, false>(p, sms, partials, s);
+  return in_step(p) ? run_bwd<T, E, true>(p, sms, partials, s) : run_bwd<T, 1, false>(p, sms, partials, s);
+}
+
 cudaError_t launch_norm_bwd(const NormParams& p, int sms, int* partials, cudaStream_t s) {
-  if (p.dtype == FLCE_DTYPE_F32)
-    return vectors(p) ? run_bwd<float, 4>(p, sms, partials, s) : run_bwd<float, 1>(p, sms, partials, s);
-  return vectors(p) ? run_bwd<uint16_t, 8>(p, sms, partials, s) : run_bwd<uint16_t, 1>(p, sms, partials, s);
+  return p.dtype == FLCE_DTYPE_F32 ? launch_bwd<float, 4>(p, sms, partials, s) : launch_bwd<uint16_t, 8>(p, sms, partials, s);
 }
 
 cudaError_t launch_norm_wgrad(const float* part_w, const float* part_b, int partials, int64_t hidden, float* grad_w,
