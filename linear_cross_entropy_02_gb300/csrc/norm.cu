@@ -31,6 +31,7 @@
 #include <math.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "head_device.cuh"
 #include "head_internal.h"
@@ -163,37 +164,45 @@ __device__ __forceinline__ void norm_row(const NormParams& p, const T* x, T* y, 
     if (p.mean && !p.rms) p.mean[row] = mean + rest;
     if (p.rstd) p.rstd[row] = rstd;
   }
+  const float shift = -rest * rstd;
+  // (the weights' type is asked once, not for each vector)
+  auto finish = [&](auto f32) {
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int i = (t + c * stride) * E;
-    if (t + c * stride < vecs) {
-      float v[E], w[E];
-      unpack<T, E>(cur[c], v);
+    for (int c = 0; c < C; ++c) {
+      const int i = (t + c * stride) * E;
+      if (t + c * stride < vecs) {
+        float v[E], w[E], b[E];
+        unpack<T, E>(cur[c], v);
 #pragma unroll
-      for (int e = 0; e < E; ++e) v[e] = (v[e] - mean - rest) * rstd;
-      if (p.weight) {
-        if (C > 1) load_weight<E>(p.weight, p.w_f32 != 0, i, w);
+        for (int e = 0; e < E; ++e) v[e] = fmaf(v[e] - mean, rstd, shift);
+        if (p.weight) {
+          if (C > 1) load_weight<E>(p.weight, f32.value, i, w);
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[e] *= C > 1 ? w[e] : w0[e];
+          for (int e = 0; e < E; ++e) v[e] *= C > 1 ? w[e] : w0[e];
+        }
+        if (p.bias) {
+          if (C > 1) load_weight<E>(p.bias, f32.value, i, b);
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[e] += C > 1 ? b[e] : b0[e];
+        }
+        store_raw<T, E>(y + i, pack<T, E>(v));
       }
-      if (p.bias) {
-        if (C > 1) load_weight<E>(p.bias, p.w_f32 != 0, i, w);
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[e] += C > 1 ? w[e] : b0[e];
-      }
-      store_raw<T, E>(y + i, pack<T, E>(v));
     }
-  }
+  };
+  if (p.w_f32)
+    finish(std::true_type());
+  else
+    finish(std::false_type());
 }
 
-// A row per CTA.
-template <typename T, int E, int C>
-__global__ void __launch_bounds__(kMaxThreads) norm_cta_kernel(const NormParams p) {
+// A row per CTA, of THREADS threads if that is not 0.
+template <typename T, int E, int C, int THREADS>
+__global__ void __launch_bounds__(THREADS ? THREADS : kMaxThreads) norm_cta_kernel(const NormParams p) {
   __shared__ BlockSums sums;
   int slot = 0;
   const int64_t row = blockIdx.x;
   norm_row<T, E, C>(p, static_cast<const T*>(p.x) + row * p.ld_x, static_cast<T*>(p.out) + row * p.hidden, row, threadIdx.x,
-                    blockDim.x, static_cast<int>(p.hidden) / E,
+                    THREADS ? THREADS : blockDim.x, static_cast<int>(p.hidden) / E,
                     [&](float& a, float& b, auto both) { block_sum<both.value>(a, b, sums, slot); });
 }
 
@@ -726,35 +735,46 @@ inline int bwd_ctas(int64_t hidden) {
   return n < 1 ? 1 : n > 8 ? 8 : static_cast<int>(n);
 }
 
-template <typename T, int E, int C>
-cudaError_t run_fwd_cta(const NormParams& p, int c, int threads, cudaStream_t s) {
-  if constexpr (C <= kMaxVecs) {
-    if (c > C) return run_fwd_cta<T, E, C + 1>(p, c, threads, s);
-    norm_cta_kernel<T, E, C><<<static_cast<unsigned>(p.rows), threads, 0, s>>>(p);
-  }
+// C vectors for each of THREADS threads (0: `threads`), in steps of STEP.
+template <typename T, int E, int THREADS, int STEP, int MOST, int C = STEP>
+cudaError_t run_fwd_cta(const NormParams& p, int64_t c, int threads, cudaStream_t s) {
+  if constexpr (C < MOST)
+    if (c > C) return run_fwd_cta<T, E, THREADS, STEP, MOST, C + STEP>(p, c, threads, s);
+  norm_cta_kernel<T, E, C, THREADS><<<static_cast<unsigned>(p.rows), threads, 0, s>>>(p);
   return cudaGetLastError();
 }
 
 template <typename T, int E>
 cudaError_t run_fwd(const NormParams& p, int sms, cudaStream_t s) {
   const int64_t vecs = p.hidden / E;
-  if (vecs <= 32 * 4) {
+  if (vecs <= 32 * (E == 1 ? 16 : 4)) {
     const int lanes = lanes_for(vecs);
     const int64_t per = kWarpRowThreads / lanes;
     const unsigned grid = static_cast<unsigned>((p.rows + per - 1) / per);
     if (vecs <= 32)
       norm_warp_kernel<T, E, 1><<<grid, kWarpRowThreads, 0, s>>>(p, lanes);
-    else
+    else if (vecs <= 32 * 4)
       norm_warp_kernel<T, E, 4><<<grid, kWarpRowThreads, 0, s>>>(p, lanes);
+    else if constexpr (E == 1)
+      norm_warp_kernel<T, E, 16><<<grid, kWarpRowThreads, 0, s>>>(p, lanes);
     return cudaGetLastError();
   }
-  if (vecs <= static_cast<int64_t>(kMaxThreads) * kMaxVecs) {
-    // few rows: a thread per vector, for the shortest chain of loads
-    int most = p.rows < 2LL * sms ? kMaxThreads : 128;
+  // few rows: a thread per vector, for the shortest chain of loads
+  const bool few = p.rows < 2LL * sms;
+  if constexpr (E == 1) {
+    // Single elements: what a thread does once for a row is worth several elements, so
+    // that fewer threads take more of them. (10007 x 1337 fp32: 25 us with 128 threads,
+    // 31 with 64, 44 with 224; 8000 x 5003 bf16: 66 with 512, 87 with 256.)
+    if (!few && vecs <= 128 * 16) return run_fwd_cta<T, E, 128, 4, 16>(p, (vecs + 127) / 128, 128, s);
+    if (!few && vecs <= 256 * 16) return run_fwd_cta<T, E, 256, 4, 16>(p, (vecs + 255) / 256, 256, s);
+    if (!few && vecs <= 512 * 32) return run_fwd_cta<T, E, 512, 4, 32>(p, (vecs + 511) / 512, 512, s);
+    if (vecs <= kMaxThreads * 16) return run_fwd_cta<T, E, kMaxThreads, 4, 16>(p, (vecs + kMaxThreads - 1) / kMaxThreads, kMaxThreads, s);
+  } else if (vecs <= static_cast<int64_t>(kMaxThreads) * kMaxVecs) {
+    if (!few && vecs <= 128 * kMaxVecs) return run_fwd_cta<T, E, 128, 1, kMaxVecs>(p, (vecs + 127) / 128, 128, s);
+    int most = few ? kMaxThreads : 128;
     while (most * kMaxVecs < vecs) most *= 2;
-    const int c = static_cast<int>((vecs + most - 1) / most);
-    const int threads = static_cast<int>(((vecs + c - 1) / c + 31) / 32 * 32);
-    return run_fwd_cta<T, E, 1>(p, c, threads, s);
+    const int64_t c = (vecs + most - 1) / most;
+    return run_fwd_cta<T, E, 0, 1, kMaxVecs>(p, c, static_cast<int>(((vecs + c - 1) / c + 31) / 32 * 32), s);
   }
   norm_long_kernel<T><<<grid_of(p.rows, 2LL * sms), kMaxThreads, 0, s>>>(p);
   return cudaGetLastError();
