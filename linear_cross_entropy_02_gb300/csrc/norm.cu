@@ -44,10 +44,9 @@ constexpr int kMaxVecs = 8;           // vectors per thread of a forward row
 constexpr int kWarpRowThreads = 256;  // eight warps per CTA
 constexpr int kMaxThreads = 1024;
 
-// Backward: vectors per thread of a CTA's row, and per lane of a warp's row.
-// E = 8: bf16 vectors, E = 4: fp32 vectors, E = 1: elements (rows off the vector boundary).
+// Backward: most vectors per thread of a CTA's row. E = 8: bf16 vectors, E = 4: fp32
+// vectors, E = 1: elements (tensors whose rows lie differently to vector boundaries).
 constexpr int cta_vecs(int E) { return E == 8 ? 2 : E == 4 ? 4 : 8; }
-constexpr int warp_vecs(int E) { return E == 8 ? 4 : 8; }
 
 // Sums of two values (or only of the first) over the CTA, in every thread.
 // `slot` alternates between 0 and 1 from call to call: the barrier of the call
@@ -392,14 +391,14 @@ template <typename T, int E>
 constexpr bool kRing = sizeof(T) * E >= 4;  // the smallest asynchronous copy is of 4 bytes
 
 // C vectors per thread of a row, `stride` apart, and the ring of rows ahead: what
-// both kernels below share. KEEP: x - mean stays in registers until the row's sums
-// are known; else it is made again from the ring, and the registers serve for more
-// threads. (32768 x 7168 bf16 RMS: 278 us with, 267 without, 252 with a ring of two
-// stages instead of three; but a warp's rows of 576 with a bias 57 with, 62 without.)
-template <typename T, int E, int C, int NB, bool RMS, bool SHIFT, bool KEEP>
+// both kernels below share. x - mean stays in registers until the row's sums are
+// known (KEEP) only for one vector; else it is made again from the ring, and the
+// registers serve for more threads. (32768 x 7168 bf16 RMS: 278 us with, 267
+// without, 252 with a ring of two stages instead of three.)
+template <typename T, int E, int C, int NB, bool RMS, bool SHIFT>
 struct BwdRow {
   static_assert(E > 1 || !SHIFT, "single elements are always in place");
-  static constexpr bool RING = kRing<T, E>;
+  static constexpr bool RING = kRing<T, E>, KEEP = C == 1;
   const NormParams& p;
   Place pl;
   int t, stride, threads;  // first vector, distance between vectors, distance in the ring
@@ -551,7 +550,7 @@ __global__ void __maxnreg__(REGS) norm_bwd_cta_kernel(const NormParams p, const 
   float4* w = reinterpret_cast<float4*>(dyn);
   Raw<T, E>* ring = reinterpret_cast<Raw<T, E>*>(w + (SHIFT ? C * Weights<E>::per * T_ : 0)) + threadIdx.x;
   int64_t row = blockIdx.x;
-  BwdRow<T, E, C, NB, RMS, SHIFT, false> r(p, place_of<T, E, SHIFT>(p, row), threadIdx.x, T_, T_, ring, {w + threadIdx.x, T_});
+  BwdRow<T, E, C, NB, RMS, SHIFT> r(p, place_of<T, E, SHIFT>(p, row), threadIdx.x, T_, T_, ring, {w + threadIdx.x, T_});
   for (int i = 0; i < stages - 1; ++i) r.fetch(row + static_cast<int64_t>(i) * gridDim.x, i);
   float mean = !RMS && row < p.rows ? __ldg(p.mean + row) : 0.f, rstd = row < p.rows ? __ldg(p.rstd + row) : 0.f;
   int stage = 0, fill = stages - 1;
@@ -577,10 +576,11 @@ __global__ void __maxnreg__(REGS) norm_bwd_cta_kernel(const NormParams p, const 
 // Rows on groups of `lanes` lanes (32, or fewer if the row has fewer vectors),
 // each with a ring of its own; no barrier until the CTA's groups add up their
 // sums, in order. A group's rows are a multiple of eight apart, too.
-template <typename T, int E, int C, int NB, bool RMS, bool SHIFT>
+template <typename T, int E, int NB, bool RMS, bool SHIFT>
 __global__ void __launch_bounds__(kWarpRowThreads)
     norm_bwd_warp_kernel(const NormParams p, const int lanes, const int stages) {
   constexpr bool RING = kRing<T, E>;
+  constexpr int C = 1;  // vectors per lane
   extern __shared__ __align__(16) uint8_t dyn[];
   float4* w = reinterpret_cast<float4*>(dyn);
   Raw<T, E>* ring = reinterpret_cast<Raw<T, E>*>(w + (SHIFT ? C * Weights<E>::per * kWarpRowThreads : 0)) + threadIdx.x;
@@ -590,7 +590,7 @@ __global__ void __launch_bounds__(kWarpRowThreads)
   // whole warps go through the loop together: the groups' sums are shuffles of the warp
   const int64_t first = static_cast<int64_t>(blockIdx.x) * groups + (threadIdx.x >> 5) * (32 / lanes);
   int64_t row = first + (threadIdx.x & 31) / lanes;
-  BwdRow<T, E, C, NB, RMS, SHIFT, NB == 2> r(p, place_of<T, E, SHIFT>(p, row), t, 32, kWarpRowThreads, ring,
+  BwdRow<T, E, C, NB, RMS, SHIFT> r(p, place_of<T, E, SHIFT>(p, row), t, 32, kWarpRowThreads, ring,
                                     {w + threadIdx.x, kWarpRowThreads});
   for (int i = 0; i < stages - 1; ++i) r.fetch(row + i * step, i);
   float mean = !RMS && row < p.rows ? __ldg(p.mean + row) : 0.f, rstd = row < p.rows ? __ldg(p.rstd + row) : 0.f;
@@ -727,14 +727,6 @@ inline int lanes_for(int64_t vecs) {
   return l;
 }
 
-// CTAs per SM of the backward: shorter rows take more of them, and each writes
-// one partial row, so that the partial sums stay within about a sixth of a
-// large batch's bytes.
-inline int bwd_ctas(int64_t hidden) {
-  const int64_t n = 16384 / hidden;
-  return n < 1 ? 1 : n > 8 ? 8 : static_cast<int>(n);
-}
-
 // C vectors for each of THREADS threads (0: `threads`), in steps of STEP.
 template <typename T, int E, int THREADS, int STEP, int MOST, int C = STEP>
 cudaError_t run_fwd_cta(const NormParams& p, int64_t c, int threads, cudaStream_t s) {
@@ -783,6 +775,15 @@ cudaError_t run_fwd(const NormParams& p, int sms, cudaStream_t s) {
 constexpr size_t kMostShared = 220 * 1024;
 constexpr int kCtaStages = 2;  // see BwdRow
 
+
+// CTAs per SM of the backward: shorter rows take more of them, and each writes
+// one partial row, so that the partial sums stay within about a sixth of a
+// large batch's bytes.
+inline int bwd_ctas(int64_t hidden) {
+  const int64_t n = 16384 / hidden;
+  return n < 1 ? 1 : n > 8 ? 8 : static_cast<int>(n);
+}
+
 // Launches k with dynamic shared memory above the default limit.
 template <typename K, typename... A>
 cudaError_t launch_large(K k, std::atomic<uint64_t>& done, unsigned grid, int threads, size_t smem, cudaStream_t s, A... args) {
@@ -801,29 +802,24 @@ cudaError_t launch_large(K k, std::atomic<uint64_t>& done, unsigned grid, int th
 inline int64_t most_vecs(int64_t hidden, int E, bool shift) { return shift ? (hidden + 2 * E - 2) / E : hidden / E; }
 
 template <typename T, int E, int NB, bool RMS, bool SHIFT>
-cudaError_t run_bwd_row(const NormParams& p, int sms, int* partials, cudaStream_t s) {
-  const int64_t vecs = most_vecs(p.hidden, E, SHIFT);
-  static std::atomic<uint64_t> done[2];
-  if (vecs <= 32 * warp_vecs(E)) {
-    constexpr int C = warp_vecs(E);
-    const int lanes = lanes_for(vecs);
-    const int64_t groups = kWarpRowThreads / lanes;
-    // one vector per lane: three rows ahead are few registers and little shared memory
-    const int c = vecs <= 32 ? 1 : C, stages = !kRing<T, E> ? 2 : vecs <= 32 ? 4 : SHIFT ? 2 : 3;
-    const size_t ring = static_cast<size_t>(kWarpRowThreads) * c *
-                        ((kRing<T, E> ? 2 * sizeof(Raw<T, E>) * stages : 0) + (SHIFT ? E * sizeof(float) : 0));
-    const size_t comb = static_cast<size_t>(groups) * p.hidden * sizeof(float);
-    const size_t smem = ring > comb ? ring : comb;
-    const unsigned grid = grid_of((p.rows + groups - 1) / groups, static_cast<int64_t>(sms) * (vecs <= 32 ? 4 : 2));
-    *partials = static_cast<int>(grid);
-    if (vecs <= 32)
-      return launch_large(norm_bwd_warp_kernel<T, E, 1, NB, RMS, SHIFT>, done[0], grid, kWarpRowThreads, smem, s, p, lanes, stages);
-    return launch_large(norm_bwd_warp_kernel<T, E, C, NB, RMS, SHIFT>, done[1], grid, kWarpRowThreads, smem, s, p, lanes, stages);
-  }
-  constexpr int C = cta_vecs(E);
+cudaError_t run_bwd_warp(const NormParams& p, int64_t vecs, int sms, int* partials, cudaStream_t s) {
+  const int lanes = lanes_for(vecs);
+  const int64_t groups = kWarpRowThreads / lanes;
+  // one vector per lane: three rows ahead are few registers and little shared memory
+  const int stages = !kRing<T, E> ? 2 : 4;
+  const size_t ring = static_cast<size_t>(kWarpRowThreads) * ((kRing<T, E> ? 2 * sizeof(Raw<T, E>) * stages : 0) + (SHIFT ? E * sizeof(float) : 0));
+  const size_t comb = static_cast<size_t>(groups) * p.hidden * sizeof(float);
+  const size_t smem = ring > comb ? ring : comb;
+  const unsigned grid = grid_of((p.rows + groups - 1) / groups, static_cast<int64_t>(sms) * 4);
+  *partials = static_cast<int>(grid);
+  static std::atomic<uint64_t> done{0};
+  return launch_large(norm_bwd_warp_kernel<T, E, NB, RMS, SHIFT>, done, grid, kWarpRowThreads, smem, s, p, lanes, stages);
+}
+
+template <typename T, int E, int C, int REGS, int NB, bool RMS, bool SHIFT>
+cudaError_t run_bwd_cta(const NormParams& p, int64_t vecs, int sms, int* partials, cudaStream_t s) {
   const int threads = static_cast<int>(((vecs + C - 1) / C + 31) / 32 * 32);
-  const int regs = threads <= 448 ? 72 : 64;
-  int ctas = 65536 / (regs * threads);
+  int ctas = 65536 / (REGS * threads);
   if (ctas > bwd_ctas(p.hidden)) ctas = bwd_ctas(p.hidden);
   const size_t weights = SHIFT ? static_cast<size_t>(threads) * C * E * sizeof(float) : 0;
   const size_t row = kRing<T, E> ? static_cast<size_t>(threads) * C * 2 * sizeof(Raw<T, E>) : 0;
@@ -833,12 +829,29 @@ cudaError_t run_bwd_row(const NormParams& p, int sms, int* partials, cudaStream_
   int64_t grid = static_cast<int64_t>(sms) * ctas;
   grid = p.rows <= grid ? p.rows : grid / 8 * 8;
   *partials = static_cast<int>(grid);
-  const unsigned n = static_cast<unsigned>(grid);
-  const size_t smem = row * stages + weights;
-  static std::atomic<uint64_t> opted[2];
-  if (regs == 72)
-    return launch_large(norm_bwd_cta_kernel<T, E, C, NB, 72, RMS, SHIFT>, opted[0], n, threads, smem, s, p, stages);
-  return launch_large(norm_bwd_cta_kernel<T, E, C, NB, 64, RMS, SHIFT>, opted[1], n, threads, smem, s, p, stages);
+  static std::atomic<uint64_t> done{0};
+  return launch_large(norm_bwd_cta_kernel<T, E, C, NB, REGS, RMS, SHIFT>, done, static_cast<unsigned>(grid), threads,
+                      row * stages + weights, s, p, stages);
+}
+
+template <typename T, int E, int NB, bool RMS, bool SHIFT>
+cudaError_t run_bwd_row(const NormParams& p, int sms, int* partials, cudaStream_t s) {
+  const int64_t vecs = most_vecs(p.hidden, E, SHIFT);
+  if (vecs <= 32) return run_bwd_warp<T, E, NB, RMS, SHIFT>(p, vecs, sms, partials, s);
+  // (Rows of up to four vectors per lane on a warp: 32768 x 1024 bf16 RMS 48 us so, 54
+  // by CTAs, but 30000 x 576 with a bias 57 and 48, 20000 x 201 fp32 38 and 27.)
+  // Short rows on more threads, for the latency of a row: 10007 x 1337 bf16 46 us with
+  // one vector each, 52 with two; fp32 40 with two, 56 with four. Not long ones:
+  // 32768 x 4096 bf16 194 us with one, 154 with two; 8192 x 8192 fp32 138 and 133.
+  if constexpr (E == 8)
+    if (vecs <= 256) return run_bwd_cta<T, E, 1, 64, NB, RMS, SHIFT>(p, vecs, sms, partials, s);
+  if constexpr (E == 4) {
+    if (vecs <= 128) return run_bwd_cta<T, E, 1, 64, NB, RMS, SHIFT>(p, vecs, sms, partials, s);
+    if (vecs <= 2 * 448) return run_bwd_cta<T, E, 2, 72, NB, RMS, SHIFT>(p, vecs, sms, partials, s);
+  }
+  constexpr int C = cta_vecs(E);
+  if (vecs <= 448 * C) return run_bwd_cta<T, E, C, 72, NB, RMS, SHIFT>(p, vecs, sms, partials, s);
+  return run_bwd_cta<T, E, C, 64, NB, RMS, SHIFT>(p, vecs, sms, partials, s);
 }
 
 template <typename T, int E, bool SHIFT>
