@@ -136,6 +136,59 @@ def test_strides_and_alignment_change_nothing(H, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("H,gap,off,same", [(1337, 8, 0, True), (1337, 40, 3, False), (203, 16, 0, True), (203, 5, 1, True),
+                                            (16, 8, 0, True), (17, 8, 0, True), (4099, 8, 0, True), (9001, 16, 8, True)])
+def test_backward_of_rows_with_gaps(H, gap, off, same, dtype):
+    """Rows inside wider tensors, on vector boundaries or off them, all alike
+    (`same`) or x and grad_y differently: NaN lies in the gaps, before the first
+    row and behind the last, and nothing of it may come in or be written over.
+    Tolerances as in test_forward_and_backward."""
+    import linear_cross_entropy_02_gb300 as flce
+    rows = 300
+    x, w, b, gy = make(rows, H, dtype, torch.float32, True, H + gap + off)
+
+    def inside(t, at):
+        wide = torch.full((rows, H + gap), float("nan"), dtype=dtype, device="cuda")
+        wide[:, at:at + H] = t
+        return wide[:, at:at + H]
+    _, mean, rstd = flce.flce_layer_norm(x, w, b, return_stats=True)
+    out = flce.flce_layer_norm_backward(inside(gy, off), inside(x, off if same else 0), w, mean, rstd)
+    xhat = (x.double() - mean.double().unsqueeze(-1)) * rstd.double().unsqueeze(-1)
+    gx, gw, gb = formula_grad(gy, xhat, rstd.double(), w, False)
+    size = (rstd.double().unsqueeze(-1) * (gy.double() * w.double()).abs().amax(-1, keepdim=True)).abs().max()
+    tol = 16 * EPS32 * size * (1 + xhat.abs().max())
+    assert bool(((out["grad_x"].double() - gx).abs() <= tol + (gx.abs() * 2.0 ** -8 if dtype == torch.bfloat16 else 0)).all())
+    assert bool(((out["grad_weight"].double() - gw).abs() <= N_CHAIN * EPS32 * (gy.double() * xhat).abs().sum(0).max()).all())
+    assert bool(((out["grad_bias"].double() - gb).abs() <= N_CHAIN * EPS32 * gy.double().abs().sum(0).max()).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H", [1337, 2048, 301])
+def test_backward_writes_only_its_rows(H):
+    """grad_x into the middle of a larger buffer, by the C entry."""
+    import linear_cross_entropy_02_gb300 as flce
+    from linear_cross_entropy_02_gb300._lib import lib
+    rows = 61
+    x, w, _, gy = make(rows, H, torch.bfloat16, torch.bfloat16, False, H)
+    _, mean, rstd = flce.flce_layer_norm(x, w, return_stats=True)
+    ref = flce.flce_layer_norm_backward(gy, x, w, mean, rstd, need_grad_bias=False)["grad_x"]
+    for at in (0, 8, 3):
+        buf = torch.full((rows * H + 24,), 7.0, dtype=torch.bfloat16, device="cuda")
+        n = lib().flce_layer_norm_workspace_size(rows, H)
+        ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+        rc = lib().flce_layer_norm_backward(gy.data_ptr(), H, x.data_ptr(), H, 0, rows, H, w.data_ptr(), 0, mean.data_ptr(),
+                                            rstd.data_ptr(), 0, buf[at:].data_ptr(), None, None, 0, ws.data_ptr(), n,
+                                            torch.cuda.current_stream().cuda_stream)
+        assert rc == 0
+        got = buf[at:at + rows * H].view(rows, H)
+        assert bool((buf[:at] == 7).all()) and bool((buf[at + rows * H:] == 7).all())
+        if at != 3:
+            assert torch.equal(got, ref)
+        close(got, ref.float(), extra=2.0 ** 17)  # another order of additions, then one rounding to bf16
+
+
+@pytest.mark.gpu
 def test_offset_rows_do_not_cancel():
     """Rows far from zero: the variance comes from centred values. With mean 1000
     and deviation 1 the inputs' own rounding is exact here, and mean(x^2) -

@@ -144,6 +144,31 @@ def test_product_matches_the_values(N, K, V, out):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("N,K,V", [(5, 13056, 300), (30, 10016, 200), (60, 8224, 150), (100, 5120, 260),
+                                   (257, 64, 1024), (600, 1312, 1504), (131, 1056, 272), (520, 512, 4112)])
+def test_product_of_long_rows_and_of_prompts(N, K, V):
+    """Few tokens whose codes do not fit beside the ring, and prompts on whole and
+    partial tiles, with rows of logits on 32-byte boundaries and off them."""
+    import linear_cross_entropy_02_gb300 as flce
+    g = torch.Generator(device="cuda").manual_seed(N + K + V)
+    h = torch.randn(N, K, generator=g, device="cuda").to(torch.bfloat16)
+    W = flce.flce_microscale_quantize(torch.randn(V, K, generator=g, device="cuda") * 0.02)
+    A = flce.flce_microscale_quantize(h)
+    ref, size = product(flce.flce_microscale_dequantize(A).double(), flce.flce_microscale_dequantize(W).double())
+    for out in (torch.bfloat16, torch.float32):
+        got = flce.flce_microscale_linear(h, W, out_dtype=out)
+        check_product(got, ref, size, K)
+        # rows of logits off the boundary, in a wider buffer
+        wide = torch.full((N + 1, V + 3), 7.0, dtype=out, device="cuda")
+        ws = torch.empty(flce._lib.lib().flce_microscale_workspace_size(N, K), dtype=torch.uint8, device="cuda")
+        rc = flce._lib.lib().flce_microscale_linear(h.data_ptr(), 0, K, N, W.codes.data_ptr(), W.scales.data_ptr(), V, K, 1.0, 0.0,
+                                                    wide.data_ptr(), 0 if out == torch.bfloat16 else 1, V + 3, ws.data_ptr(),
+                                                    ws.numel(), torch.cuda.current_stream().cuda_stream)
+        assert rc == 0
+        assert torch.equal(wide[:N, :V], got) and bool((wide[:, V:] == 7).all()) and bool((wide[N] == 7).all())
+
+
+@pytest.mark.gpu
 def test_product_scales_go_to_their_blocks():
     """Every block of W and A on a scale of its own, over the whole exponent range
     that the sum survives: a scale read from a wrong row or block shows at once."""

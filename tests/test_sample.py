@@ -157,6 +157,25 @@ def test_settings_per_row(dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [3, 700, 9001, 30011])
+def test_more_rows_than_multiprocessors(V, dtype):
+    """Such batches run two rows to a multiprocessor, with fewer threads each: every
+    kind of row, also those with equal logits, NaN and single candidates."""
+    N = 10 * len(SETTINGS)
+    x, u = logits(N, V, dtype, V + 5, masked=True)
+    x[:, 0] = 1.0  # something finite in each
+    x[7::20] = 0.25
+    x[11::20, V // 2] = math.nan
+    x[13::20] = -math.inf
+    x[13::20, V - 1] = -3.0
+    per_row = lambda name, default, dt: torch.tensor([float(SETTINGS[i % len(SETTINGS)].get(name, default)) for i in range(N)],  # noqa: E731
+                                                     device="cuda").to(dt)
+    check(x, u, per_row("T", 1.0, torch.float32), per_row("k", 0, torch.int32), per_row("p", 1.0, torch.float32),
+          per_row("q", 0.0, torch.float32))
+
+
+@pytest.mark.gpu
 def test_a_row_does_not_depend_on_its_batch():
     """One row alone is spread over more CTAs than in a batch: same token, same bits."""
     import linear_cross_entropy_02_gb300 as flce
