@@ -102,8 +102,8 @@ struct Shared {
   uint64_t sum_total, sum_above;  // of this slice, in the second pass
   uint64_t found_above, found_value, goal;
   uint32_t found_bin, found_count;
-  float top;
-  uint32_t bad;
+  float tops[kMaxCluster];  // of all CTAs
+  uint32_t bads[kMaxCluster];
   uint32_t first;      // lowest index of the largest logit in this slice
   uint32_t key_lo, key_hi;
   uint32_t listed[4];  // lengths of the lists of a row, one counter per use
@@ -115,7 +115,7 @@ struct Shared {
   uint32_t red[kMostWarps], red2[kMostWarps];
   float fscan[kMostWarps];
   float cut_x[2];
-  uint32_t told[3];  // CTA 0: where the prefix ends, for the others
+  uint32_t told[3];  // by CTA 0: where the prefix ends
 };
 
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -169,6 +169,10 @@ __device__ __forceinline__ void remote_add(uint32_t* mine, uint32_t rank, uint32
 }
 __device__ __forceinline__ void remote_add(float* mine, uint32_t rank, float v) {
   asm volatile("red.shared::cluster.add.f32 [%0], %1;" ::"r"(mapa_shared(smem_u32(mine), rank)), "f"(v) : "memory");
+}
+
+__device__ __forceinline__ void remote_store(uint32_t* mine, uint32_t rank, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(smem_u32(mine), rank)), "r"(v) : "memory");
 }
 
 // Appends to CTA 0's list; what does not fit is only counted. (One addition to
@@ -798,41 +802,54 @@ template <typename T, int kThreads>
 __device__ void short_list_answer(const Row<T, kThreads>& row, Shared& s, const SampleParams& p, int64_t r, int n, int64_t top_k,
                                   float top_p, float u) {
   uint64_t* weights = reinterpret_cast<uint64_t*>(&s.hist[0]);
-  static_assert(sizeof(s.hist) >= kShort * sizeof(uint64_t) && kShort <= kThreads, "weights in the histograms' place");
-  const int i = threadIdx.x;
+  static_assert(sizeof(s.hist) >= kShort * sizeof(uint64_t), "weights in the histograms' place");
+  constexpr int P = kThreads / kShort;  // lanes that share an entry's comparisons
+  const int i = threadIdx.x / P, part = threadIdx.x % P;
   uint64_t mine = ~0ull, w = 0, before = 0;
   float e = 0.f;
   int rank = 0;
+  // over an entry's lanes
+  auto joined = [](uint64_t v) {
+#pragma unroll
+    for (int o = 1; o < P; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  };
   __syncthreads();
   if (i < n) {
     mine = s.list[i];
     e = row.exponential(entry_value(mine));
-    weights[i] = w = Row<T, kThreads>::fixed(e);
+    w = Row<T, kThreads>::fixed(e);
+    if (part == 0) weights[i] = w;
   }
   __syncthreads();
   if (i < n) {
-    for (int k = 0; k < n; ++k) {
+#pragma unroll 4
+    for (int k = part; k < n; k += P) {
       const bool first = s.list[k] < mine;
       rank += first;
       before += first ? weights[k] : 0;
     }
   }
+  rank = static_cast<int>(joined(static_cast<uint64_t>(rank)));
+  before = joined(before);
   bool keep = i < n && (top_k <= 0 || rank < top_k);
   if (top_p < 1.f) {
-    const uint64_t whole = block_total<kThreads>(s, keep ? w : 0);
+    const uint64_t whole = block_total<kThreads>(s, keep && part == 0 ? w : 0);
     const uint64_t far = by_one(s, [&] { return top_p_goal(top_p, whole); });
     keep = keep && (rank == 0 || before < far);
   }
   keep = keep && (rank == 0 || e >= row.min_p);
-  const uint64_t whole = block_total<kThreads>(s, keep ? w : 0);
-  if (i < n) weights[i] = keep ? w : 0;
+  const uint64_t whole = block_total<kThreads>(s, keep && part == 0 ? w : 0);
+  if (i < n && part == 0) weights[i] = keep ? w : 0;
   const uint64_t goal = by_one(s, [&] { return answer_goal(u, whole); });
+  const uint32_t index = static_cast<uint32_t>(mine);
+  before = 0;
   if (keep) {
-    const uint32_t index = static_cast<uint32_t>(mine);
-    before = 0;
-    for (int k = 0; k < n; ++k) before += static_cast<uint32_t>(s.list[k]) < index ? weights[k] : 0;
-    if (before <= goal && goal < before + w) write_answer(row, p, r, index, entry_value(mine), whole);
+#pragma unroll 4
+    for (int k = part; k < n; k += P) before += static_cast<uint32_t>(s.list[k]) < index ? weights[k] : 0;
   }
+  before = joined(before);
+  if (keep && part == 0 && before <= goal && goal < before + w) write_answer(row, p, r, index, entry_value(mine), whole);
 }
 
 // The segment that holds the answer, of those in s.answer: to found_bin, and what
@@ -1130,6 +1147,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
   if constexpr (MULTI) {
     row.rank = cluster_ctarank();
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(row.ctas));
+    // waited for before the first write into another CTA: it has to be running
+    asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
   }
   const int64_t r = blockIdx.x / row.ctas;
   const int vocab = static_cast<int>(p.vocab);
@@ -1235,14 +1254,16 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
   bad = __syncthreads_or(bad);
   row.top = slice_top;
   if constexpr (MULTI) {
-    if (threadIdx.x == 0) {
-      s.top = slice_top;
-      s.bad = bad;
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+    // told to all before the barrier: reading the others' after it takes 1200 cycles more
+    if (threadIdx.x < row.ctas) {
+      remote_store(reinterpret_cast<uint32_t*>(&s.tops[row.rank]), threadIdx.x, __float_as_uint(slice_top));
+      remote_store(&s.bads[row.rank], threadIdx.x, bad);
     }
     row_barrier<MULTI>();
     for (uint32_t c = 0; c < row.ctas; ++c) {
-      row.top = fmaxf(row.top, remote<MULTI>(&s.top, c));
-      bad |= remote<MULTI>(&s.bad, c) != 0;
+      row.top = fmaxf(row.top, s.tops[c]);
+      bad |= s.bads[c] != 0;
     }
   }
   bad |= !(fabsf(row.top) < INFINITY);  // no finite logit, or +infinity
@@ -1348,17 +1369,17 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
       general |= !(whole < INFINITY);
       cut_lo = static_cast<int>(from >> 32);
       cut_hi = static_cast<int>(to >> 32) + 1;
-      if (MULTI && threadIdx.x == 0) {
-        s.told[0] = cut_lo;
-        s.told[1] = cut_hi;
-        s.told[2] = general;
+      if (MULTI && threadIdx.x < row.ctas) {
+        remote_store(&s.told[0], threadIdx.x, static_cast<uint32_t>(cut_lo));
+        remote_store(&s.told[1], threadIdx.x, static_cast<uint32_t>(cut_hi));
+        remote_store(&s.told[2], threadIdx.x, general);
       }
     }
     if constexpr (MULTI) {
       row_barrier<MULTI>();
-      cut_lo = remote<MULTI>(&s.told[0], 0);
-      cut_hi = remote<MULTI>(&s.told[1], 0);
-      general = remote<MULTI>(&s.told[2], 0) != 0;
+      cut_lo = static_cast<int>(s.told[0]);
+      cut_hi = static_cast<int>(s.told[1]);
+      general = s.told[2] != 0;
     }
     listing = need_k && !general;
   }
