@@ -25,11 +25,14 @@
 // general selection: a histogram of exact weights, then splitting the bin that
 // holds the answer by the logits' bits until it is small enough or all equal.
 //
-// One CTA per row where there are rows for every SM: all exchange is within
-// the CTA, and the second pass finds the row in shared memory or, if it is too
-// long, in the L2 (152 rows of 0.5 MB fit). Few rows are spread over a cluster
-// of up to eight CTAs each, with maxima, counts and sums exchanged through
-// distributed shared memory.
+// One CTA per row, or two rows to an SM, where there are rows for every SM: all
+// exchange is within the CTA, and the second pass finds the row in shared memory or,
+// if it is too long, in the L2. Few rows are spread over a cluster of up to eight
+// CTAs each, with maxima, counts and sums exchanged through distributed shared memory.
+//
+// One row of 129280 bf16 with top-k 50 takes 16.6 us, nearly all of it a chain of
+// barriers; 77 rows of 50257 with top-k 100 23 us; 512 rows of 129280 fp32 with top-p
+// 180 us (1.5 TB/s), bound by instructions: about 20 a logit for the exact sums.
 #include <math.h>
 
 #include <atomic>
