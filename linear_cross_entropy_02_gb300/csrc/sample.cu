@@ -9,7 +9,7 @@
 //
 // A row takes two passes. The first reads it from HBM, keeps the maximum and
 // counts logits in 4096 bins of (x - anchor) / T, the anchor being the maximum
-// of the row's first part. Then:
+// of the row's first part (of the row, if that part holds nothing finite). Then:
 //   top_k that some bins cover with at most kListKeys logits: the second pass
 //     collects those logits in shared memory, where all three filters cut them
 //     and the token is drawn.
@@ -1238,17 +1238,19 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
   };
   // without a cluster the first part of the row sets the anchor, and the counts
   // of all but that part come with the only read from HBM; a cluster's slices
-  // are short and are looked through again with the row's maximum as the anchor
+  // are short and are looked through again with the row's maximum as the anchor,
+  // and so is a row whose first part holds nothing finite. (The anchor must not lie
+  // above the maximum: logits in the last bin are left out as weighing nothing.)
   const int first = MULTI ? row.vecs : min(row.vecs, kFirstVectors * kThreads);
   sweep(0, first, false);
+  bool anchored = false;
   if (!MULTI && need_counts) {
-    const float a = block_top();
-    row.anchor = fabsf(a) < INFINITY ? a : 0.f;
-    for (int v = threadIdx.x; v < first; v += kThreads) count(row.get(v));
-  } else {
-    row.anchor = 0.f;
+    row.anchor = block_top();
+    anchored = fabsf(row.anchor) < INFINITY;
+    if (anchored)
+      for (int v = threadIdx.x; v < first; v += kThreads) count(row.get(v));
   }
-  sweep(first, row.vecs, need_counts);
+  sweep(first, row.vecs, anchored);
   if (in_smem) {
     row.data = kept;
     row.padded = row.aligned = true;
@@ -1301,7 +1303,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
   bool general = false, listing = false;
   int cut_lo = 0, cut_hi = 0;  // bins to collect: from cut_lo on, before cut_hi
   if (need_counts) {
-    if constexpr (MULTI) {
+    if (!anchored) {
       row.anchor = row.top;
       row.each([&](float x, uint32_t) {
         const int b = row.count_bin(x);
@@ -1309,6 +1311,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
         if (b < kWeighedBins) atomicAdd(&s.counts.weight[b], expf((x - row.anchor) * row.inv));
       });
       __syncthreads();
+    }
+    if constexpr (MULTI) {
       // to CTA 0, which looks for the end and tells the others
       if (row.rank != 0) {
         for (int b = threadIdx.x; b < kCountBins; b += kThreads) {

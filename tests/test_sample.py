@@ -282,3 +282,33 @@ def test_refusals_without_a_gpu():
     odd = ctypes.c_void_p((1 << 20) + 2)
     assert call(x=odd) == call(u=odd) == call(tokens=ctypes.c_void_p((1 << 20) + 4)) == call(lp=odd) == B.FLCE_ERR_ALIGN
     assert call(rows=0, x=None) == B.FLCE_OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [40000, 50257])
+def test_rows_that_begin_masked(V, dtype):
+    """Nothing finite in the part of the row that is read first, and every logit
+    behind it far below 0: a batch's rows, each on one CTA, are counted by the row's
+    own maximum, and give what rows spread over several CTAs do."""
+    import linear_cross_entropy_02_gb300 as flce
+    g = torch.Generator(device="cuda").manual_seed(V)
+    x = torch.full((320, V), -math.inf, device="cuda")
+    x[3::4] = torch.finfo(dtype).min  # a mask of the type's lowest value instead
+    for r in range(320):
+        n = (1, 2, 40, 300, 3000)[r % 5]
+        at = 33000 + torch.randperm(V - 33000, generator=g, device="cuda")[:n]
+        x[r, at] = (-18.0, -60.0, -1e4)[r % 3] + 1.4 * torch.randn(n, generator=g, device="cuda")
+    x, u = x.to(dtype), torch.rand(320, generator=g, device="cuda")
+    for s in (dict(k=50), dict(k=50, T=0.5), dict(k=50, T=0.3, p=0.9), dict(k=2500, T=0.4), dict(k=50, q=0.05), dict(p=0.9),
+              dict(T=0.4, p=0.95, q=0.01)):
+        kw = dict(temperature=s.get("T", 1.0), top_k=s.get("k", 0), top_p=s.get("p", 1.0), min_p=s.get("q", 0.0))
+        check(x[:15], u[:15], **s)  # on clusters
+        few = [flce.flce_sample(x[i:i + 64], u[i:i + 64], **kw) for i in range(0, 320, 64)]
+        for N in (77, 160, 320):
+            # the outputs' memory is in use here: what a row does not write, a NaN or a -7, would show
+            a = torch.full((N,), -7, dtype=torch.int64, device="cuda"), torch.full((N,), math.nan, device="cuda")
+            del a
+            got = flce.flce_sample(x[:N], u[:N], **kw)
+            for j in range(2):
+                assert torch.equal(got[j], torch.cat([f[j] for f in few])[:N]), (N, s)
