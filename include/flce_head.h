@@ -110,7 +110,9 @@ int flce_microscale_linear(const void* x, int dtype, int64_t ld_x, int64_t rows,
  * temperature, top_k, top_p, min_p: the arrays hold one value per row (device);
  * NULL takes the scalar beside it for every row. tokens [rows] int64.
  * logprobs [rows] fp32, nullable: log of the answer's probability among the
- * kept tokens. A temperature so small that its reciprocal overflows counts as 0.
+ * kept tokens. A temperature so small that its reciprocal overflows counts as 0;
+ * for +infinity the reciprocal is taken as the smallest positive number, so that
+ * finite logits weigh alike and those of -infinity nothing.
  * vocab < 2^22. */
 int flce_sample(const void* logits, int logits_dtype, int64_t rows, int64_t vocab, int64_t ld_logits, const float* u,
                 const float* temperatures, float temperature, const int32_t* top_ks, int32_t top_k,

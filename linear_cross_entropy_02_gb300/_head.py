@@ -317,8 +317,8 @@ def flce_sample(logits: torch.Tensor, u: torch.Tensor, *, temperature=1.0, top_k
     numbers or fp32 tensors of one value per row, top_k a number or an int32
     tensor. Filters apply in the order top_k, top_p, min_p, each to what the one
     before it kept; <= 0 (top_k, min_p) and >= 1 (top_p) keep all, temperature
-    <= 0 takes the largest logit (the lowest index of several). Returns (tokens
-    int64, logprobs fp32), the second the log of the token's probability among
+    <= 0 takes the largest logit (the lowest index of several), +infinity weighs
+    all finite logits alike. Returns (tokens int64, logprobs fp32), the second the log of the token's probability among
     the kept ones (None without return_logprobs). A row with NaN or +infinity, or
     without a finite logit, gives token -1. The result does not depend on how
     the rows are batched."""

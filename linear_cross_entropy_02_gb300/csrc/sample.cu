@@ -52,6 +52,7 @@ constexpr int kFew = 64;       // entries that are compared each with each
 constexpr int kShort = 256;    // the same for a list of candidates
 constexpr float kRange = 28.f;  // exp(-28) 2^40 < 1
 constexpr float kFixed = 1099511627776.f;  // 2^40
+constexpr float kLeast = 1.4e-45f;  // the smallest positive number
 
 // General selection.
 constexpr int kBins = 1024;
@@ -1167,8 +1168,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
   const float top_p = p.top_ps ? p.top_ps[r] : p.top_p;
   const float u = p.u[r];
   row.min_p = p.min_ps ? p.min_ps[r] : p.min_p;
-  row.inv = 1.f / temperature;
-  row.per_place = fminf(row.inv * (1.f / kPlaces), 3e38f);
+  // (a reciprocal of zero would make NaN of a logit of -infinity)
+  row.inv = fmaxf(1.f / temperature, kLeast);
+  row.per_place = fmaxf(fminf(row.inv * (1.f / kPlaces), 3e38f), kLeast);
   bool bad = temperature != temperature || top_p != top_p || row.min_p != row.min_p || u != u;
   const bool greedy = !(temperature > 0.f) || row.inv == INFINITY || top_k == 1 || top_p <= 0.f || row.min_p > 1.f;
   const bool need_k = top_k > 0 && top_k < p.vocab;

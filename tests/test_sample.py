@@ -312,3 +312,24 @@ def test_rows_that_begin_masked(V, dtype):
             got = flce.flce_sample(x[:N], u[:N], **kw)
             for j in range(2):
                 assert torch.equal(got[j], torch.cat([f[j] for f in few])[:N]), (N, s)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V,masked", [(300, 20), (20000, 60), (20000, 15000), (100000, 60), (100000, 40000)])
+def test_infinite_temperature(V, masked, dtype):
+    """All finite logits weigh 1, those of -infinity nothing: what a temperature gives
+    that is large enough for every exponential to round to 1, which the definition covers."""
+    import linear_cross_entropy_02_gb300 as flce
+    x, u = logits(160, V, dtype, V + masked)
+    x[:, torch.randperm(V, device="cuda", generator=torch.Generator(device="cuda").manual_seed(V))[:masked]] = -math.inf
+    mixed = torch.full((160,), math.inf, device="cuda")
+    mixed[::2] = 3e38
+    for kw in (dict(), dict(k=50), dict(p=0.3), dict(k=V // 2, p=0.5), dict(q=0.5), dict(k=9000, q=0.1)):
+        check(x[:2], u[:2], T=3e38, **kw)
+        s = dict(top_k=kw.get("k", 0), top_p=kw.get("p", 1.0), min_p=kw.get("q", 0.0))
+        want = flce.flce_sample(x, u, temperature=3e38, **s)
+        assert bool(torch.isfinite(x.gather(1, want[0].unsqueeze(1))).all())
+        for T, n in ((math.inf, 160), (mixed, 160), (math.inf, 3)):
+            got = flce.flce_sample(x[:n], u[:n], temperature=T, **s)
+            assert torch.equal(got[0], want[0][:n]) and torch.equal(got[1], want[1][:n])
