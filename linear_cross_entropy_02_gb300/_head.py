@@ -126,7 +126,8 @@ def flce_layer_norm_backward(grad_y: torch.Tensor, x: torch.Tensor, weight: Opti
     """Backward of flce_layer_norm from x and the saved statistics. Returns
     dict(grad_x, grad_weight, grad_bias): grad_x in x's dtype, the other two
     fp32 [H]. A grad_weight or grad_bias that is given (fp32, contiguous) is
-    ACCUMULATED in place, as the fused head does with grad_W."""
+    ACCUMULATED in place, as the fused head does with grad_W; where both are
+    wanted, both or neither. One that is given but not wanted is left alone."""
     dtype = _floats("x", x)
     _cuda("grad_y", grad_y)
     index = x.get_device()
@@ -141,17 +142,18 @@ def flce_layer_norm_backward(grad_y: torch.Tensor, x: torch.Tensor, weight: Opti
     for name, t in (("grad_weight", grad_weight), ("grad_bias", grad_bias)):
         if t is not None and (t.dtype != torch.float32 or t.shape != (H,) or not t.is_contiguous() or t.device != x.device):
             raise ValueError(f"{name} must be a contiguous fp32 [H] tensor on x's device")
-    accumulate = grad_weight is not None or grad_bias is not None
-    if accumulate and need_grad_weight and need_grad_bias and (grad_weight is None or grad_bias is None):
+    # what is given for a gradient that is not wanted counts for nothing
+    gw, gb = grad_weight if need_grad_weight else None, grad_bias if need_grad_bias else None
+    accumulate = gw is not None or gb is not None
+    if accumulate and need_grad_weight and need_grad_bias and (gw is None or gb is None):
         raise ValueError("give both grad_weight and grad_bias to accumulate into, or neither")
     x2, rows, ld = _rows(x)
     g2, _, ld_g = _rows(grad_y)
     gx = torch.empty_like(x, memory_format=torch.contiguous_format) if need_grad_x else None
-    if need_grad_weight and grad_weight is None:
-        grad_weight = torch.empty(H, dtype=torch.float32, device=x.device)
-    if need_grad_bias and grad_bias is None:
-        grad_bias = torch.empty(H, dtype=torch.float32, device=x.device)
-    gw, gb = grad_weight if need_grad_weight else None, grad_bias if need_grad_bias else None
+    if need_grad_weight and gw is None:
+        gw = torch.empty(H, dtype=torch.float32, device=x.device)
+    if need_grad_bias and gb is None:
+        gb = torch.empty(H, dtype=torch.float32, device=x.device)
     ws, nbytes = None, 0
     if gw is not None or gb is not None:
         with torch.cuda.device(index):

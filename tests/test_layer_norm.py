@@ -312,3 +312,36 @@ def test_refusals_without_a_gpu():
     assert bwd(x=None) == bwd(gy=None) == bwd(rstd=None) == bwd(mean=None) == bwd(gw=q) == B.FLCE_ERR_ARG
     assert bwd(gx=None) == B.FLCE_OK                                             # nothing wanted
     assert bwd(gx=ctypes.c_void_p(2)) == bwd(gw=q, ws=ctypes.c_void_p(8), n=1 << 30) == B.FLCE_ERR_ALIGN
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("give_w", [False, True])
+@pytest.mark.parametrize("give_b", [False, True])
+def test_accumulators_of_gradients_that_are_not_wanted(give_w, give_b):
+    """Every combination of wanted gradients and given buffers: a given buffer is
+    added to if its gradient is wanted and stays as it was if not, and a buffer
+    that the call makes itself holds the sum alone."""
+    import linear_cross_entropy_02_gb300 as flce
+    x, w, b, gy = make(90, 264, torch.float32, torch.float32, True, 31)
+    _, mean, rstd = flce.flce_layer_norm(x, w, b, return_stats=True)
+    ref = flce.flce_layer_norm_backward(gy, x, w, mean, rstd)
+    for need_w, need_b in ((False, False), (False, True), (True, False), (True, True)):
+        gw = torch.randn(264, device="cuda") if give_w else None
+        gb = torch.randn(264, device="cuda") if give_b else None
+        was = [None if t is None else t.clone() for t in (gw, gb)]
+        args = dict(need_grad_weight=need_w, need_grad_bias=need_b, grad_weight=gw, grad_bias=gb)
+        if need_w and need_b and give_w != give_b:
+            with pytest.raises(ValueError):
+                flce.flce_layer_norm_backward(gy, x, w, mean, rstd, **args)
+            continue
+        # memory that holds something, for the buffers that the call makes
+        junk = [torch.full((264,), 1e6, device="cuda") for _ in range(8)]
+        del junk
+        out = flce.flce_layer_norm_backward(gy, x, w, mean, rstd, **args)
+        for name, need, given, old in (("grad_weight", need_w, gw, was[0]), ("grad_bias", need_b, gb, was[1])):
+            if not need:
+                assert out[name] is None and (given is None or torch.equal(given, old))
+            elif given is None:
+                assert torch.equal(out[name], ref[name])
+            else:
+                assert out[name] is given and torch.equal(given, old + ref[name])
