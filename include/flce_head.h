@@ -43,8 +43,9 @@ int flce_layer_norm(const void* x, int dtype, int64_t rows, int64_t hidden, int6
  * accumulate != 0 adds the two sums to what grad_weight and grad_bias hold,
  * as the fused head does with grad_W. The sums are taken in a fixed order:
  * results do not change from run to run. rows = 0 gives zero sums. The workspace
- * is needed for the two sums only; it begins with the status word of
- * flce_get_status, which this call leaves 0. */
+ * is needed for the two sums only. The call finds no errors on the device and
+ * leaves the workspace's first 256 bytes, with the status word of flce_get_status,
+ * as they are: a workspace that the fused head used keeps that call's status. */
 size_t flce_layer_norm_workspace_size(int64_t rows, int64_t hidden);
 int flce_layer_norm_backward(const void* grad_y, int64_t ld_grad_y, const void* x, int64_t ld_x, int dtype,
                              int64_t rows, int64_t hidden, const void* weight, int weight_dtype, const float* mean,

@@ -158,7 +158,8 @@ def flce_layer_norm_backward(grad_y: torch.Tensor, x: torch.Tensor, weight: Opti
     if gw is not None or gb is not None:
         with torch.cuda.device(index):
             nbytes = _lib.lib().flce_layer_norm_workspace_size(rows, H)
-        ws = _space(index, nbytes)
+        # (memory of this call's own: the cached one holds the fused head's status)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
     _call(index, "flce_layer_norm_backward", g2.data_ptr(), ld_g, x2.data_ptr(), ld, dtype, rows, H, _ptr(weight), wcode,
           None if rms else mean.data_ptr(), rstd.data_ptr(), int(rms), _ptr(gx), _ptr(gw), _ptr(gb), int(accumulate),
           _ptr(ws), nbytes)

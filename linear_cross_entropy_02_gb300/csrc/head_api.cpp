@@ -170,7 +170,7 @@ int flce_layer_norm_backward(const void* grad_y, int64_t ld_grad_y, const void* 
   if (rows > 0) FLCE_LAUNCH(K_NORM_BWD, launch_norm_bwd(p, sms, &partials, stream));
   if (sums)
     FLCE_LAUNCH(K_NORM_WGRAD, launch_norm_wgrad(p.part_w, p.part_b, partials, hidden, grad_weight, grad_bias,
-                                                accumulate, &static_cast<Header*>(workspace)->status, stream));
+                                                accumulate, stream));
   return FLCE_OK;
 }
 

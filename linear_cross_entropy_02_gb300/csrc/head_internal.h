@@ -42,9 +42,9 @@ int norm_partial_rows(int64_t rows, int64_t hidden, int sms);
 cudaError_t launch_norm(const NormParams& p, int sms, cudaStream_t s);
 // Writes grad_x and the partial sums; *partials = rows of part_w / part_b written.
 cudaError_t launch_norm_bwd(const NormParams& p, int sms, int* partials, cudaStream_t s);
-// grad_w[j] (+)= sum over i of part_w[i][j], in a fixed order (and the same for b); *status = 0.
+// grad_w[j] (+)= sum over i of part_w[i][j], in a fixed order (and the same for b).
 cudaError_t launch_norm_wgrad(const float* part_w, const float* part_b, int partials, int64_t hidden, float* grad_w,
-                              float* grad_b, int accumulate, int32_t* status, cudaStream_t s);
+                              float* grad_b, int accumulate, cudaStream_t s);
 
 // ------------------------------------------------------------ microscaled 4-bit
 constexpr int kMxBlock = 32;        // elements per scale

@@ -678,9 +678,8 @@ __global__ void __launch_bounds__(256) norm_bwd_long_cols_kernel(const NormParam
 // and the 32 sums are added in order.
 __global__ void __launch_bounds__(1024) norm_wgrad_kernel(const float* part_w, const float* part_b, int partials,
                                                           int64_t hidden, float* grad_w, float* grad_b,
-                                                          int accumulate, int32_t* status) {
+                                                          int accumulate) {
   __shared__ float s[32][33];
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && threadIdx.y == 0) *status = 0;
   const float* part = blockIdx.y == 0 ? part_w : part_b;
   float* grad = blockIdx.y == 0 ? grad_w : grad_b;
   if (grad == nullptr) return;
@@ -900,9 +899,9 @@ cudaError_t launch_norm_bwd(const NormParams& p, int sms, int* partials, cudaStr
 }
 
 cudaError_t launch_norm_wgrad(const float* part_w, const float* part_b, int partials, int64_t hidden, float* grad_w,
-                              float* grad_b, int accumulate, int32_t* status, cudaStream_t s) {
+                              float* grad_b, int accumulate, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>((hidden + 31) / 32), grad_b ? 2 : 1);
-  norm_wgrad_kernel<<<grid, dim3(32, 32), 0, s>>>(part_w, part_b, partials, hidden, grad_w, grad_b, accumulate, status);
+  norm_wgrad_kernel<<<grid, dim3(32, 32), 0, s>>>(part_w, part_b, partials, hidden, grad_w, grad_b, accumulate);
   return cudaGetLastError();
 }
 

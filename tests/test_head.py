@@ -151,3 +151,20 @@ def test_refusals_without_a_gpu():
         flce.LanguageModelHead(W, torch.zeros(31))
     with pytest.raises(ValueError, match="CUDA"):
         flce.LanguageModelHead(W).next_token(torch.zeros(2, 32), torch.zeros(2))
+
+
+@pytest.mark.gpu
+def test_a_bad_label_stays_in_the_status_after_the_norm_s_backward():
+    import linear_cross_entropy_02_gb300 as flce
+    from linear_cross_entropy_02_gb300 import _lib as B
+    W, n, h, y = make(4)
+    head = flce.LanguageModelHead(torch.nn.Parameter(W), torch.nn.Parameter(n))
+    y[1, 3] = 1000 + 5                     # outside the vocabulary
+    loss, _ = head(h.requires_grad_(), y)
+    loss.backward()
+    assert n.shape == head.norm_weight.grad.shape
+    assert flce.flce_get_status() & B.FLCE_ERR_LABEL
+    y[1, 3] = 5
+    loss, _ = head(h, y)
+    loss.backward()
+    assert flce.flce_get_status() == 0
