@@ -41,6 +41,8 @@ __all__ = [
 
 _REDUCTIONS = {"mean": FLCE_REDUCTION_MEAN, "sum": FLCE_REDUCTION_SUM, "none": _lib.FLCE_REDUCTION_NONE}
 _workspaces: dict = {}
+# The workspace of the last microscaled product on a device and stream, for its status word alone.
+_product_workspaces: dict = {}
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -136,6 +138,7 @@ def flce_release_workspaces() -> None:
     largest call so far); torch's allocator then holds the memory for reuse.
     Call it after the last use on a stream, not while a call may still run."""
     _workspaces.clear()
+    _product_workspaces.clear()
 
 
 def _native(device: torch.device, name: str, *args):
@@ -727,19 +730,22 @@ class FusedLinearCrossEntropyLoss(torch.nn.Module):
 
 def flce_get_status(device=None, workspace: Optional[torch.Tensor] = None) -> int:
     """Synchronises the current stream and returns the device status word of
-    the last call on the cached workspace of this device and stream, or on
-    `workspace` when given (0 = no device error)."""
+    the last call on the cached workspace of this device and stream, joined with
+    that of the last microscaled product there, or the one in `workspace` when
+    given (0 = no device error)."""
     if workspace is not None:
         dev = workspace.device
-        ws = workspace
+        spaces = [workspace]
     else:
         dev = torch.device("cuda", torch.cuda.current_device() if device is None else device)
-        ws = _workspaces.get((dev.index, torch.cuda.current_stream(dev).cuda_stream))
-    if ws is None:
-        return 0
-    st = ctypes.c_int32(0)
-    _raise(_native(dev, "flce_get_status", _ptr(ws), _stream_handle(dev), ctypes.byref(st)), "flce_get_status")
-    return int(st.value)
+        key = (dev.index, torch.cuda.current_stream(dev).cuda_stream)
+        spaces = [d[key] for d in (_workspaces, _product_workspaces) if key in d]
+    status = 0
+    for ws in spaces:
+        st = ctypes.c_int32(0)
+        _raise(_native(dev, "flce_get_status", _ptr(ws), _stream_handle(dev), ctypes.byref(st)), "flce_get_status")
+        status |= int(st.value)
+    return status
 
 
 def flce_launch_count() -> int:

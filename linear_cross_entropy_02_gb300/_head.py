@@ -11,7 +11,7 @@ from typing import Optional, Union
 
 import torch
 
-from . import _lib, _workspaces
+from . import _lib, _product_workspaces
 from ._lib import FlceError
 
 _DTYPES = {torch.bfloat16: _lib.FLCE_DTYPE_BF16, torch.float32: _lib.FLCE_DTYPE_F32}
@@ -34,15 +34,6 @@ def _call(index: int, name: str, *args):
             rc = fn(*args, _raw_stream(index))
     if rc != 0:
         raise FlceError(rc, name)
-
-
-def _space(index: int, nbytes: int) -> torch.Tensor:
-    """The package's cached workspace of this device and its current stream, of at least nbytes."""
-    ws = _workspaces.get((index, _raw_stream(index)))
-    if ws is None or ws.numel() < nbytes:
-        from . import _workspace
-        return _workspace(torch.device("cuda", index), nbytes)
-    return ws
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -266,12 +257,17 @@ def flce_microscale_dequantize(q: MicroscaleTensor, *, dtype: torch.dtype = torc
 
 
 def flce_microscale_linear(h: Union[torch.Tensor, MicroscaleTensor], W: MicroscaleTensor, *, out_mult: float = 1.0,
-                           softcap: float = 0.0, out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+                           softcap: float = 0.0, out_dtype: Optional[torch.dtype] = None,
+                           workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Logits [..., V] = cap(out_mult h W^T) on a microscaled weight W [V, K],
     cap(z) = softcap tanh(z / softcap) where softcap > 0. h: [..., K] in bf16 or
     fp32, microscaled by the call as flce_microscale_quantize does, or a
     MicroscaleTensor [N, K]. out_dtype: bf16 or fp32 (h's dtype by default, bf16
-    for a MicroscaleTensor)."""
+    for a MicroscaleTensor). Every call has a workspace of its own, so that host
+    threads may share a stream and graphs each replay in their own memory;
+    flce_get_status() reads that of the stream's last call outside of a capture. A
+    captured call's status is in the `workspace` given to it: uint8, 16-byte
+    aligned, flce_microscale_workspace_size bytes (256 for a MicroscaleTensor)."""
     if not isinstance(W, MicroscaleTensor):
         raise ValueError("W must be a MicroscaleTensor")
     V, K = W.shape
@@ -292,14 +288,23 @@ def flce_microscale_linear(h: Union[torch.Tensor, MicroscaleTensor], W: Microsca
     if code is None:
         raise ValueError("out_dtype must be bfloat16 or float32")
     out = torch.empty((*lead, V), dtype=out_dtype, device=W.codes.device)
+    nbytes = 256
+    if not isinstance(h, MicroscaleTensor):
+        # (flce_microscale_workspace_size's sum)
+        nbytes += (rows * (K // 2) + 255) // 256 * 256 + (rows + 127) // 128 * ((K + 127) // 128) * 512
+    ws = workspace
+    if ws is None:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=out.device)
+    elif ws.dtype != torch.uint8 or ws.device != out.device or not ws.is_contiguous() or ws.numel() < nbytes:
+        raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {nbytes} bytes on {out.device}")
     if isinstance(h, MicroscaleTensor):
         _call(index, "flce_microscale_matmul", h.codes.data_ptr(), h.scales.data_ptr(), rows, W.codes.data_ptr(),
-              W.scales.data_ptr(), V, K, out_mult, softcap, out.data_ptr(), code, V, _space(index, 256).data_ptr(), 256)
+              W.scales.data_ptr(), V, K, out_mult, softcap, out.data_ptr(), code, V, ws.data_ptr(), nbytes)
     else:
-        # (flce_microscale_workspace_size's sum)
-        nbytes = 256 + (rows * (K // 2) + 255) // 256 * 256 + (rows + 127) // 128 * ((K + 127) // 128) * 512
         _call(index, "flce_microscale_linear", h2.data_ptr(), dtype, ld, rows, W.codes.data_ptr(), W.scales.data_ptr(), V, K,
-              out_mult, softcap, out.data_ptr(), code, V, _space(index, nbytes).data_ptr(), nbytes)
+              out_mult, softcap, out.data_ptr(), code, V, ws.data_ptr(), nbytes)
+    if workspace is None and rows > 0 and not torch.cuda.is_current_stream_capturing():
+        _product_workspaces[index, _raw_stream(index)] = ws
     return out
 
 

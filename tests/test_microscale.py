@@ -280,3 +280,102 @@ def test_sizes_and_refusals_without_a_gpu():
     assert linear(w=odd) == linear(ws=odd) == linear(out=ctypes.c_void_p(2)) == B.FLCE_ERR_ALIGN
     assert linear(n=512) == B.FLCE_ERR_WORKSPACE
     assert linear(rows=0) == B.FLCE_OK
+
+
+@pytest.mark.gpu
+def test_a_graph_keeps_its_scratch():
+    """A product whose tokens are encoded into the workspace, captured on the stream
+    that it was warmed up on. A larger call on that stream and whatever takes the
+    memory afterwards change nothing in a replay, and a replay nothing in them."""
+    import linear_cross_entropy_02_gb300 as flce
+    N, K, V = 48, 2048, 3000
+    W = flce.flce_microscale_quantize(torch.randn(V, K, device="cuda"))
+    h = torch.randn(N, K, device="cuda", dtype=torch.bfloat16)
+    more = torch.randn(40 * N, K, device="cuda", dtype=torch.bfloat16)
+    want, other = flce.flce_microscale_linear(h, W), flce.flce_microscale_linear(h.flip(0), W)
+    flce.flce_release_workspaces()
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        flce.flce_microscale_linear(h, W)
+    graph, ws = torch.cuda.CUDAGraph(), torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=stream):
+        out = flce.flce_microscale_linear(h, W)
+        told = flce.flce_microscale_linear(h, W, workspace=ws)
+    with torch.cuda.stream(stream):
+        big = flce.flce_microscale_linear(more, W)
+        took = [torch.full((1 << 16,), 5, dtype=torch.uint8, device="cuda") for _ in range(64)]
+        for tokens, ref in ((h, want), (h.flip(0), other)):
+            h.copy_(tokens.clone())
+            graph.replay()
+            stream.synchronize()
+            assert torch.equal(out, ref) and torch.equal(told, ref)
+        assert all(bool((t == 5).all()) for t in took)
+        assert flce.flce_get_status() == 0 and flce.flce_get_status(workspace=ws) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(big, flce.flce_microscale_linear(more, W))
+
+
+@pytest.mark.gpu
+def test_graphs_replay_on_two_streams():
+    """Two graphs captured one after the other, replayed at once."""
+    import linear_cross_entropy_02_gb300 as flce
+    N, K, V = 64, 2048, 20000
+    W = flce.flce_microscale_quantize(torch.randn(V, K, device="cuda"))
+    hs = [torch.randn(N, K, device="cuda", dtype=torch.bfloat16) for _ in range(2)]
+    want = [flce.flce_microscale_linear(h, W) for h in hs]
+    graphs, outs = [torch.cuda.CUDAGraph() for _ in hs], []
+    for g, h in zip(graphs, hs):
+        with torch.cuda.graph(g):
+            outs.append([flce.flce_microscale_linear(h, W) for _ in range(4)])
+    streams = [torch.cuda.Stream() for _ in hs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for got, ref in zip(outs, want):
+        assert all(torch.equal(t, ref) for t in got)
+
+
+@pytest.mark.gpu
+def test_host_threads_share_a_stream():
+    """Calls of several host threads on one stream, each of two launches that meet in a workspace."""
+    import threading
+
+    import linear_cross_entropy_02_gb300 as flce
+    N, K, V = 48, 2048, 2000
+    W = flce.flce_microscale_quantize(torch.randn(V, K, device="cuda"))
+    hs = [torch.randn(N + 16 * i, K, device="cuda", dtype=torch.bfloat16) for i in range(4)]
+    rstd = [torch.ones(h.shape[0], device="cuda") for h in hs]
+
+    def both(i):
+        out = flce.flce_layer_norm_backward(hs[i], hs[i], None, None, rstd[i], rms=True, need_grad_bias=False)
+        return flce.flce_microscale_linear(hs[i], W), out["grad_weight"]
+    want = [both(i) for i in range(4)]
+    got = [[] for _ in hs]
+    threads = [threading.Thread(target=lambda i=i: got[i].extend(both(i) for _ in range(60))) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for i, w in enumerate(want):
+        assert len(got[i]) == 60 and all(torch.equal(a, b) for g in got[i] for a, b in zip(g, w))
+    assert flce.flce_get_status() == 0
+
+
+@pytest.mark.gpu
+def test_workspace_of_the_caller():
+    import linear_cross_entropy_02_gb300 as flce
+    h = torch.randn(50, 64, device="cuda")
+    W = flce.flce_microscale_quantize(torch.randn(70, 64, device="cuda"))
+    n = flce._lib.lib().flce_microscale_workspace_size(50, 64)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+    assert torch.equal(flce.flce_microscale_linear(h, W, workspace=ws), flce.flce_microscale_linear(h, W))
+    assert flce.flce_get_status(workspace=ws) == 0
+    for bad in (ws[:n - 1], ws.int(), ws.cpu(), torch.zeros(2 * n, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            flce.flce_microscale_linear(h, W, workspace=bad)
