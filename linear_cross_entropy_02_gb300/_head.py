@@ -357,8 +357,12 @@ class LanguageModelHead(torch.nn.Module):
     loss(hidden, labels) normalises and runs the fused linear cross-entropy;
     gradients flow to hidden, the norm's weights and W where they require grad.
     next_token(hidden, u, ...) normalises, multiplies with W in microscaled
-    4-bit (prepare_answers() lays it out once; call it again after W changed)
-    and samples. softcap and out_mult mean the same in both."""
+    4-bit (H a multiple of 32) and samples. The 4-bit W is laid out at the first
+    use and again when W has changed: another parameter, memory or device, or a
+    change that torch counts (an optimiser's step, load_state_dict, an edit in
+    place). After an edit through .data, which torch does not count, call
+    prepare_answers(). A graph replays the one that it was captured with. softcap
+    and out_mult mean the same in both."""
 
     def __init__(self, weight: torch.Tensor, norm_weight: Optional[torch.Tensor] = None,
                  norm_bias: Optional[torch.Tensor] = None, *, eps: float = 1e-5, rms: bool = True, softcap: float = 0.0,
@@ -377,6 +381,7 @@ class LanguageModelHead(torch.nn.Module):
         self.softcap, self.out_mult = float(softcap), float(out_mult)
         self.ignore_index, self.reduction = int(ignore_index), reduction
         self.answers: Optional[MicroscaleTensor] = None
+        self._made = (None, None)  # what prepare_answers() made, and from which W
 
     def normalise(self, hidden: torch.Tensor) -> torch.Tensor:
         if torch.is_grad_enabled():
@@ -394,13 +399,25 @@ class LanguageModelHead(torch.nn.Module):
     def prepare_answers(self) -> MicroscaleTensor:
         """Microscales W for logits() and next_token(), and keeps it."""
         self.answers = flce_microscale_quantize(self.weight.detach())
+        self._made = (self.answers, self._state_of_weight())
         return self.answers
+
+    def _state_of_weight(self):
+        w = self.weight
+        return w.data_ptr(), w.device, w.dtype, w.shape, None if w.is_inference() else w._version
+
+    def _current_answers(self) -> MicroscaleTensor:
+        made, state = self._made
+        if self.answers is not None and (self.answers is not made or state == self._state_of_weight()):
+            return self.answers  # (one that was put there stays)
+        if torch.cuda.is_current_stream_capturing():
+            return flce_microscale_quantize(self.weight.detach())  # its values come with the replay: not kept
+        return self.prepare_answers()
 
     @torch.no_grad()
     def logits(self, hidden: torch.Tensor, out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
-        """Logits [..., V] on the microscaled W (made at the first call)."""
-        W = self.answers if self.answers is not None else self.prepare_answers()
-        return flce_microscale_linear(self.normalise(hidden), W, out_mult=self.out_mult, softcap=self.softcap,
+        """Logits [..., V] on the microscaled W."""
+        return flce_microscale_linear(self.normalise(hidden), self._current_answers(), out_mult=self.out_mult, softcap=self.softcap,
                                       out_dtype=out_dtype)
 
     @torch.no_grad()

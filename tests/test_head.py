@@ -168,3 +168,56 @@ def test_a_bad_label_stays_in_the_status_after_the_norm_s_backward():
     loss, _ = head(h, y)
     loss.backward()
     assert flce.flce_get_status() == 0
+
+
+@pytest.mark.gpu
+def test_answers_follow_the_weight():
+    """After an optimiser's step, an edit in place, a loaded state or another W, the
+    answers are those of the W that the head has, without being told."""
+    import linear_cross_entropy_02_gb300 as flce
+    W, n, h, y = make(5)
+    h = h.detach()
+    head = flce.LanguageModelHead(torch.nn.Parameter(W.clone()), n)
+
+    def want():
+        return flce.flce_microscale_linear(flce.flce_layer_norm(h, n, rms=True), flce.flce_microscale_quantize(head.weight.detach()))
+    assert torch.equal(head.logits(h), want())
+    kept = head.answers
+    assert torch.equal(head.logits(h), want()) and head.answers is kept      # laid out once
+    opt = torch.optim.SGD([head.weight], lr=1.0)
+    head.loss(h, y)[0].backward()
+    opt.step()
+    assert torch.equal(head.logits(h), want()) and head.answers is not kept
+    with torch.no_grad():
+        head.weight[7].mul_(-3)
+    assert torch.equal(head.logits(h), want())
+    other = flce.LanguageModelHead(W.flip(0).contiguous(), n)
+    head.load_state_dict(other.state_dict())
+    assert torch.equal(head.logits(h), want())
+    head.weight = torch.nn.Parameter(W.roll(1, 0).contiguous())
+    assert torch.equal(head.logits(h), want())
+    head.prepare_answers()
+    head.weight.data = W.clone()          # another memory, the same counter of changes
+    assert torch.equal(head.logits(h), want())
+    mine = flce.flce_microscale_quantize(W * 2)
+    head.answers = mine                   # put there: stays
+    assert torch.equal(head.logits(h), 2 * want()) and head.answers is mine
+
+
+@pytest.mark.gpu
+def test_a_capture_before_the_first_answer():
+    """The 4-bit W is then made in the graph, with every replay, and is not taken for finished outside of it."""
+    import linear_cross_entropy_02_gb300 as flce
+    W, n, h, _ = make(6)
+    h = h.detach()
+    want = flce.LanguageModelHead(W, n).logits(h)
+    head = flce.LanguageModelHead(W.clone(), n)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        z = head.logits(h)
+    assert head.answers is None and torch.equal(head.logits(h), want)
+    graph.replay()
+    assert torch.equal(z, want)
+    head.weight.data.copy_(W.flip(0))
+    graph.replay()
+    assert torch.equal(z, want.flip(2))
