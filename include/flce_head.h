@@ -39,7 +39,8 @@ int flce_layer_norm(const void* x, int dtype, int64_t rows, int64_t hidden, int6
  *   grad_x      = rstd (g - mean(g) - xhat mean(g xhat))    (rms: no mean(g))
  *   grad_weight = sum over rows of grad_y xhat               (fp32 [H])
  *   grad_bias   = sum over rows of grad_y                    (fp32 [H])
- * grad_x [rows, H] contiguous in x's dtype; any of the three may be NULL.
+ * grad_x [rows, H] contiguous in x's dtype, not overlapping x or grad_y unless it
+ * is one of them itself with a row stride of H; any of the three may be NULL.
  * accumulate != 0 adds the two sums to what grad_weight and grad_bias hold,
  * as the fused head does with grad_W. The sums are taken in a fixed order:
  * results do not change from run to run. rows = 0 gives zero sums. The workspace

@@ -22,6 +22,14 @@ inline bool dtype_ok(int d) { return d == FLCE_DTYPE_BF16 || d == FLCE_DTYPE_F32
 inline size_t element_size(int d) { return d == FLCE_DTYPE_F32 ? 4 : 2; }
 inline bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
+// Whether a result [rows, hidden] at `out` may be written while `in` [rows, ld] is
+// read: apart from it, or the same memory row by row.
+bool apart_or_same(const void* in, int64_t ld, const void* out, int64_t rows, int64_t hidden, size_t es) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(in), b = reinterpret_cast<uintptr_t>(out);
+  const uintptr_t an = (static_cast<uintptr_t>(rows - 1) * ld + hidden) * es, bn = static_cast<uintptr_t>(rows) * hidden * es;
+  return a >= b + bn || b >= a + an || (a == b && (ld == hidden || rows == 1));
+}
+
 int device_check(int* sms) {
   int cc = 0;
   const int rc = device_info(sms, &cc);
@@ -95,9 +103,7 @@ int flce_layer_norm(const void* x, int dtype, int64_t rows, int64_t hidden, int6
   if (!aligned(x, es) || !aligned(y, es) || !aligned(weight, ws) || !aligned(bias, ws) || !aligned(mean, 4) ||
       !aligned(rstd, 4))
     return FLCE_ERR_ALIGN;
-  const uintptr_t x0 = reinterpret_cast<uintptr_t>(x), y0 = reinterpret_cast<uintptr_t>(y);
-  const uintptr_t xb = (static_cast<uintptr_t>(rows - 1) * ld_x + hidden) * es, yb = static_cast<uintptr_t>(rows) * hidden * es;
-  if (x0 < y0 + yb && y0 < x0 + xb && !(x0 == y0 && ld_x == hidden)) return FLCE_ERR_ARG;
+  if (!apart_or_same(x, ld_x, y, rows, hidden, es)) return FLCE_ERR_ARG;
   int sms = 0;
   const int rc = device_check(&sms);
   if (rc != FLCE_OK) return rc;
@@ -143,6 +149,9 @@ int flce_layer_norm_backward(const void* grad_y, int64_t ld_grad_y, const void* 
       !aligned(weight, element_size(weight_dtype)) || !aligned(mean, 4) || !aligned(rstd, 4) ||
       !aligned(grad_weight, 4) || !aligned(grad_bias, 4) || !aligned(workspace, 16))
     return FLCE_ERR_ALIGN;
+  if (rows > 0 && grad_x &&
+      (!apart_or_same(x, ld_x, grad_x, rows, hidden, es) || !apart_or_same(grad_y, ld_grad_y, grad_x, rows, hidden, es)))
+    return FLCE_ERR_ARG;
   int sms = 0;
   const int rc = device_check(&sms);
   if (rc != FLCE_OK) return rc;

@@ -862,17 +862,16 @@ cudaError_t run_bwd(const NormParams& p, int sms, int* partials, cudaStream_t s)
       return p.rms ? run_bwd_row<T, E, 2, true, SHIFT>(p, sms, partials, s) : run_bwd_row<T, E, 2, false, SHIFT>(p, sms, partials, s);
     return p.rms ? run_bwd_row<T, E, 1, true, SHIFT>(p, sms, partials, s) : run_bwd_row<T, E, 1, false, SHIFT>(p, sms, partials, s);
   }
-  if (p.out) {
-    norm_bwd_long_kernel<T><<<grid_of(p.rows, 2LL * sms), kMaxThreads, 0, s>>>(p);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-  }
   const int groups = norm_partial_rows(p.rows, p.hidden, sms);
   const int64_t group = (p.rows + groups - 1) / groups;
   *partials = static_cast<int>((p.rows + group - 1) / group);
-  if (!p.part_w && !p.part_b) return cudaSuccess;
-  const dim3 grid(static_cast<unsigned>((p.hidden + 255) / 256), static_cast<unsigned>(*partials));
-  norm_bwd_long_cols_kernel<T><<<grid, 256, 0, s>>>(p, group);
+  if (p.part_w || p.part_b) {  // first, as grad_x may take the place of x or grad_y
+    const dim3 grid(static_cast<unsigned>((p.hidden + 255) / 256), static_cast<unsigned>(*partials));
+    norm_bwd_long_cols_kernel<T><<<grid, 256, 0, s>>>(p, group);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  if (p.out) norm_bwd_long_kernel<T><<<grid_of(p.rows, 2LL * sms), kMaxThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 

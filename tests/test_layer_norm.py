@@ -345,3 +345,46 @@ def test_accumulators_of_gradients_that_are_not_wanted(give_w, give_b):
                 assert torch.equal(out[name], ref[name])
             else:
                 assert out[name] is given and torch.equal(given, old + ref[name])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("H", [24, 520, 1337, 2048, 20000])
+def test_backward_in_place(H, dtype):
+    """grad_x in x's or grad_y's own memory, by the C entry: the bits of a grad_x of its own."""
+    import linear_cross_entropy_02_gb300 as flce
+    from linear_cross_entropy_02_gb300 import _lib as B
+    rows = 333
+    x, w, b, gy = make(rows, H, dtype, torch.float32, True, H)
+    _, mean, rstd = flce.flce_layer_norm(x, w, b, return_stats=True)
+    ref = flce.flce_layer_norm_backward(gy, x, w, mean, rstd)
+    n = B.lib().flce_layer_norm_workspace_size(rows, H)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    for which in range(2):
+        a, c = x.clone(), gy.clone()
+        gw, gb = torch.zeros(H, device="cuda"), torch.zeros(H, device="cuda")
+        rc = B.lib().flce_layer_norm_backward(c.data_ptr(), H, a.data_ptr(), H, int(dtype == torch.float32), rows, H, w.data_ptr(),
+                                              1, mean.data_ptr(), rstd.data_ptr(), 0, (a, c)[which].data_ptr(), gw.data_ptr(),
+                                              gb.data_ptr(), 0, ws.data_ptr(), n, torch.cuda.current_stream().cuda_stream)
+        assert rc == B.FLCE_OK
+        assert torch.equal((a, c)[which], ref["grad_x"])
+        assert torch.equal(gw, ref["grad_weight"]) and torch.equal(gb, ref["grad_bias"])
+
+
+@pytest.mark.gpu
+def test_backward_refuses_overlaps():
+    """grad_x on x or grad_y is the same memory in whole, or none of it."""
+    import linear_cross_entropy_02_gb300 as flce  # noqa: F401
+    from linear_cross_entropy_02_gb300 import _lib as B
+    buf = torch.zeros(4096, device="cuda")
+    a, b, size = buf.data_ptr() + 4 * 512, buf.data_ptr() + 4 * 2048, 4 * 64 * 4
+    stat = torch.ones(4, device="cuda")
+
+    def bwd(gx, ld_x=64, ld_gy=64):
+        return B.lib().flce_layer_norm_backward(b, ld_gy, a, ld_x, 1, 4, 64, None, 1, stat.data_ptr(), stat.data_ptr(), 0, gx, None,
+                                                None, 0, None, 0, torch.cuda.current_stream().cuda_stream)
+    for gx in (a + 64, a + size - 4, a - size + 4, b + 64, b - 4):
+        assert bwd(gx) == B.FLCE_ERR_ARG
+    assert bwd(a, ld_x=80) == B.FLCE_ERR_ARG     # x's rows lie further apart than grad_x's
+    assert bwd(b, ld_gy=80) == B.FLCE_ERR_ARG
+    assert bwd(a + size) == bwd(a - size) == bwd(b) == bwd(a) == B.FLCE_OK
