@@ -10,6 +10,7 @@ from __future__ import annotations
 from typing import Optional, Union
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib, _product_workspaces
 from ._lib import FlceError
@@ -169,6 +170,7 @@ class _LayerNorm(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_y):
         x, weight, mean, rstd = ctx.saved_tensors
         need_x, need_w, need_b = ctx.needs_input_grad[:3]
@@ -183,7 +185,8 @@ class _LayerNorm(torch.autograd.Function):
 
 
 def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, rms: bool = False):
-    """Differentiable flce_layer_norm: gradients flow to x, weight and bias where they require grad."""
+    """Differentiable flce_layer_norm: gradients flow to x, weight and bias where
+    they require grad. Once: a derivative of the gradients raises an error."""
     return _LayerNorm.apply(x, weight, bias, float(eps), bool(rms))
 
 

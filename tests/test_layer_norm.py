@@ -388,3 +388,13 @@ def test_backward_refuses_overlaps():
     assert bwd(a, ld_x=80) == B.FLCE_ERR_ARG     # x's rows lie further apart than grad_x's
     assert bwd(b, ld_gy=80) == B.FLCE_ERR_ARG
     assert bwd(a + size) == bwd(a - size) == bwd(b) == bwd(a) == B.FLCE_OK
+
+
+@pytest.mark.gpu
+def test_a_second_derivative_is_refused():
+    import linear_cross_entropy_02_gb300 as flce
+    x = torch.randn(4, 32, device="cuda", requires_grad=True)
+    w = torch.randn(32, device="cuda", requires_grad=True)
+    (gx,) = torch.autograd.grad(flce.layer_norm(x, w).square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        (gx.sum() + x.square().sum()).backward()
