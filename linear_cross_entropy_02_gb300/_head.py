@@ -343,11 +343,12 @@ def flce_sample(logits: torch.Tensor, u: torch.Tensor, *, temperature=1.0, top_k
     x, rows, ld = _rows(logits)
     tp, t = _setting("temperature", temperature, torch.float32, lead, index)
     kp, k = _setting("top_k", top_k, torch.int32, lead, index)
+    k = max(0, min(int(k), V))  # (the entry's is 32 bits wide; both ends keep all)
     pp, p = _setting("top_p", top_p, torch.float32, lead, index)
     mp, m = _setting("min_p", min_p, torch.float32, lead, index)
     tokens = torch.empty(lead, dtype=torch.int64, device=u.device)
     logprobs = torch.empty_like(u) if return_logprobs else None
-    _call(index, "flce_sample", x.data_ptr(), code, rows, V, ld, u.data_ptr(), tp, t, kp, int(k), pp, p, mp, m,
+    _call(index, "flce_sample", x.data_ptr(), code, rows, V, ld, u.data_ptr(), tp, t, kp, k, pp, p, mp, m,
           tokens.data_ptr(), _ptr(logprobs))
     return tokens, logprobs
 

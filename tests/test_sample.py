@@ -333,3 +333,16 @@ def test_infinite_temperature(V, masked, dtype):
         for T, n in ((math.inf, 160), (mixed, 160), (math.inf, 3)):
             got = flce.flce_sample(x[:n], u[:n], temperature=T, **s)
             assert torch.equal(got[0], want[0][:n]) and torch.equal(got[1], want[1][:n])
+
+
+@pytest.mark.gpu
+def test_settings_beyond_the_entry_s_types():
+    """top_k is 32 bits wide at the C entry: a larger one keeps all, as any top_k from the vocabulary's size on does."""
+    import linear_cross_entropy_02_gb300 as flce
+    x, u = logits(3, 1000, torch.float32, 17)
+    want = flce.flce_sample(x, u)
+    for k in (2 ** 31, 2 ** 32 + 1, 2 ** 63 + 1, -2 ** 32 + 1):
+        got = flce.flce_sample(x, u, top_k=k)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    with pytest.raises(flce.FlceError):
+        flce.flce_sample(x, u, top_p=math.nan)
