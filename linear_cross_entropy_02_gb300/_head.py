@@ -125,6 +125,8 @@ def flce_layer_norm_backward(grad_y: torch.Tensor, x: torch.Tensor, weight: Opti
     index = x.get_device()
     if grad_y.shape != x.shape or grad_y.dtype != x.dtype or grad_y.get_device() != index:
         raise ValueError("grad_y must have x's shape, dtype and device")
+    if x.dim() == 0 or x.shape[-1] == 0:
+        raise ValueError("x must have a last dimension that was normalised")
     H = x.shape[-1]
     wcode = _norm_weights(H, index, weight, None)
     for name, t in (("rstd", rstd), ("mean", rstd if rms else mean)):

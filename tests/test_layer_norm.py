@@ -398,3 +398,12 @@ def test_a_second_derivative_is_refused():
     (gx,) = torch.autograd.grad(flce.layer_norm(x, w).square().sum(), x, create_graph=True)
     with pytest.raises(RuntimeError, match="once_differentiable"):
         (gx.sum() + x.square().sum()).backward()
+
+
+@pytest.mark.gpu
+def test_backward_refuses_rows_without_elements():
+    import linear_cross_entropy_02_gb300 as flce
+    one = torch.ones((), device="cuda")
+    for x, r in ((one, one), (torch.empty(3, 0, device="cuda"), torch.ones(3, device="cuda"))):
+        with pytest.raises(ValueError):
+            flce.flce_layer_norm_backward(x, x, None, r, r)
