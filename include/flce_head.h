@@ -91,6 +91,13 @@ int flce_microscale_matmul(const void* a_codes, const void* a_scales, int64_t ro
 int flce_microscale_linear(const void* x, int dtype, int64_t ld_x, int64_t rows, const void* w_codes,
                            const void* w_scales, int64_t vocab, int64_t cols, float out_mult, float softcap, void* out,
                            int out_dtype, int64_t ld_out, void* workspace, size_t workspace_bytes, void* stream);
+/* The same with the limit of each bounded device wait (0 => 2 s) and flags: 0, or
+ * FLCE_FLAG_TEST_STALL, a test hook: no product is taken, so that the waits run
+ * out and the call ends with FLCE_ERR_TIMEOUT in the status word. */
+int flce_microscale_linear_limited(const void* x, int dtype, int64_t ld_x, int64_t rows, const void* w_codes,
+                                   const void* w_scales, int64_t vocab, int64_t cols, float out_mult, float softcap,
+                                   void* out, int out_dtype, int64_t ld_out, void* workspace, size_t workspace_bytes,
+                                   int64_t timeout_ns, int flags, void* stream);
 
 /* ---------------------------------------------------------------- sampling
  * One token per row of logits [rows, vocab] (row stride ld_logits) from given

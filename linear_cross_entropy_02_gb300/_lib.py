@@ -58,7 +58,8 @@ FLCE_HEAD_KERNEL_COUNT = 7
 HEAD_EXPORTED = [
     "flce_layer_norm", "flce_layer_norm_workspace_size", "flce_layer_norm_backward", "flce_microscale_codes_size",
     "flce_microscale_scales_size", "flce_microscale_quantize", "flce_microscale_dequantize",
-    "flce_microscale_workspace_size", "flce_microscale_matmul", "flce_microscale_linear", "flce_sample",
+    "flce_microscale_workspace_size", "flce_microscale_matmul", "flce_microscale_linear", "flce_microscale_linear_limited",
+    "flce_sample",
 ]
 
 
@@ -175,6 +176,7 @@ def _bind_head(L: ctypes.CDLL) -> None:
             ("flce_microscale_workspace_size", _sz, [l, l]),
             ("flce_microscale_matmul", i, [_vp, _vp, l, _vp, _vp, l, l, f, f, _vp, i, l, _vp, _sz, _vp]),
             ("flce_microscale_linear", i, [_vp, i, l, l, _vp, _vp, l, l, f, f, _vp, i, l, _vp, _sz, _vp]),
+            ("flce_microscale_linear_limited", i, [_vp, i, l, l, _vp, _vp, l, l, f, f, _vp, i, l, _vp, _sz, l, i, _vp]),
             ("flce_sample", i, [_vp, i, l, l, l, _vp, _vp, f, _vp, ctypes.c_int32, _vp, f, _vp, f, _vp, _vp, _vp])):
         fn = getattr(L, name)
         fn.restype, fn.argtypes = res, args

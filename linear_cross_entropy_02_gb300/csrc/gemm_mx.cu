@@ -93,6 +93,7 @@ struct MxArgs {
   int64_t ld_out;
   int32_t* status;
   uint64_t timeout_ns;
+  int stall;  // test hook: the MMA warp issues nothing, so that every other wait runs out
 };
 
 // Instruction descriptor of kind::mxf4: E2M1 operands (1 in bits 7-9 and 10-12),
@@ -133,6 +134,15 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
   return p != 0;
 }
+// For a thread of a CTA in which a wait gave up, after all of the CTA's warps have
+// left their loops: copies may still be in flight, and the shared memory that they
+// write to stays as long as this thread does. They land in microseconds.
+constexpr uint64_t kDrainNs = 10 * 1000 * 1000;
+__device__ __forceinline__ void let_copies_land() {
+  const uint64_t t0 = global_timer_ns();
+  for (int i = 0; i < 100000 && global_timer_ns() - t0 < kDrainNs; ++i) __nanosleep(1000);
+}
+
 // wait_bounded by a whole warp, which then agrees on the outcome.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtx& w) {
   return __all_sync(0xffffffffu, wait_bounded(bar, parity, w));
@@ -253,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   if (warp == 0) {
-    int stage = 0, issued = 0;
+    int stage = 0;
     uint32_t phase = 0;
     bool aborted = false;
     if (RESIDENT && !FUSED && elect_one()) {  // one tile of tokens, whose scales are one row of tiles
@@ -281,27 +291,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         __syncwarp();
-        ++issued;
         if (++stage == S) {
           stage = 0;
           phase ^= 1u;
         }
-      }
-    }
-    if (aborted && lane == 0) {
-      // loads that may still be in flight land before the shared memory goes away
-      if (RESIDENT && !FUSED) wait_drain(x_full, 0, p.timeout_ns, p.status);
-      const int n = issued < S ? issued : S;
-      int s = stage;
-      uint32_t ph = phase;
-      for (int i = 0; i < n; ++i) {
-        if (s == 0) {
-          s = S - 1;
-          ph ^= 1u;
-        } else {
-          --s;
-        }
-        wait_drain(&full[s], ph, p.timeout_ns, p.status);
       }
     }
   } else if (warp == 1) {
@@ -309,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t phase = 0, acc_phase = 0;
     const uint32_t w0 = smem_u32(s_w), x0 = smem_u32(s_x);
     bool aborted = RESIDENT && !warp_wait(x_full, 0, wc);
-    for (int vb = blockIdx.x; vb < p.v_tiles && !aborted; vb += gridDim.x) {
+    for (int vb = p.stall ? p.v_tiles : blockIdx.x; vb < p.v_tiles && !aborted; vb += gridDim.x) {
       if (!warp_wait(&tempty[acc], acc_phase ^ 1u, wc)) break;
       tc_fence_after_sync();
       const uint32_t d = tmem + static_cast<uint32_t>(acc * P::d_cols);
@@ -407,6 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after_sync();
     tmem_dealloc(tmem, P::tmem_cols);
   }
+  if (threadIdx.x == 0 && *abort_flag) let_copies_land();
 }
 
 // More than 128 tokens: 256 x 256 tiles over a cluster of two CTAs on two SMs.
@@ -482,8 +476,6 @@ __device__ __forceinline__ void arrive_pair(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
-constexpr uint64_t kDrainNs = 10 * 1000 * 1000;  // copies in flight land in microseconds
-
 template <bool TOKENS_M, typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUtensorMap map_n,
@@ -543,7 +535,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const CUtensorMap* map = is_m ? &map_m : &map_n;
     uint8_t* to = is_m ? s_m : s_n;
     const uint32_t full0 = mapa_shared(smem_u32(full), 0);
-    int stage = 0, issued = 0;
+    int stage = 0;
     uint32_t phase = 0;
     bool aborted = false;
     for (int t = first; t < q.units && !aborted; t += step) {
@@ -560,35 +552,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           tma_load_2d_pair(to + stage * kWBytes, map, full0 + static_cast<uint32_t>(stage / 2) * 8u, k * kRowBytes, row);
         }
         __syncwarp();
-        ++issued;
         if (++stage == S) {
           stage = 0;
           phase ^= 1u;
         }
       }
     }
-    if (aborted && lane == 0) {
-      // Loads that may still be in flight land before the shared memory goes away. Of a
-      // pair of stages not all of which was issued the barrier does not complete, and
-      // the other CTA's copies are counted by the leader: it waits for what nobody signals.
-      const int n = min((issued + 1) / 2, S / 2);
-      int s = (stage + 1) / 2 % (S / 2);
-      uint32_t ph = (stage + 1) / 2 == S / 2 ? phase ^ 1u : phase;
-      for (int i = 0; i < n && rank == 0; ++i) {
-        if (s == 0) {
-          s = S / 2 - 1;
-          ph ^= 1u;
-        } else {
-          --s;
-        }
-        wait_drain(&full[s], ph, kDrainNs, p.status);
-      }
-      if (rank != 0) wait_drain(mma_done, 0, kDrainNs, p.status);
-    }
-    __syncwarp();
   } else if (warp == 23) {
     // Scales, for a pair of stages at once.
-    int two = 0, issued = 0;
+    int two = 0;
     uint32_t phase = 0;
     bool aborted = false;
     for (int t = first; t < q.units && !aborted; t += step) {
@@ -612,33 +584,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             bulk_load(s + 2 * kSfRun, n_from + p.k_tiles * kMxTileBytes + k * kSfRun, bytes, &sf_full[two]);
         }
         __syncwarp();
-        ++issued;
         if (++two == S / 2) {
           two = 0;
           phase ^= 1u;
         }
       }
     }
-    if (aborted && lane == 0) {
-      const int n = min(issued, S / 2);
-      for (int i = 0; i < n; ++i) {
-        if (two == 0) {
-          two = S / 2 - 1;
-          phase ^= 1u;
-        } else {
-          --two;
-        }
-        wait_drain(&sf_full[two], phase, kDrainNs, p.status);
-      }
-    }
-    __syncwarp();
   } else if (warp == 1) {
     if (rank == 0) {
       int two = 0;  // the pair of stages
       uint32_t phase = 0, acc_phase = 0;
       const uint32_t m0 = smem_u32(s_m), n0 = smem_u32(s_n);
       bool aborted = false;
-      for (int t = first; t < q.units && !aborted; t += step) {
+      for (int t = p.stall ? q.units : first; t < q.units && !aborted; t += step) {
         if (!warp_wait(tempty, acc_phase ^ 1u, wc)) break;
         acc_phase ^= 1u;
         tc_fence_after_sync();
@@ -764,7 +722,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
   }
   tc_fence_before_sync();
-  cluster_sync_all();  // neither CTA leaves while the other may still signal it
+  __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag) let_copies_land();
+  __syncwarp();
+  cluster_sync_all();  // neither CTA leaves while the other, or its copies, may still signal it
   if (warp == 1) {
     tc_fence_after_sync();
     tmem_dealloc_pair(tmem, 512);
@@ -816,6 +777,7 @@ MxArgs arguments(const MxGemmParams& p) {
   a.ld_out = p.ld_out;
   a.status = p.status;
   a.timeout_ns = p.timeout_ns;
+  a.stall = p.stall;
   return a;
 }
 

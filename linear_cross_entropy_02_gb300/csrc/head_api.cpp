@@ -249,6 +249,15 @@ int flce_microscale_linear(const void* x, int dtype, int64_t ld_x, int64_t rows,
                            const void* w_scales, int64_t vocab, int64_t cols, float out_mult, float softcap, void* out,
                            int out_dtype, int64_t ld_out, void* workspace, size_t workspace_bytes,
                            void* stream_handle) {
+  return flce_microscale_linear_limited(x, dtype, ld_x, rows, w_codes, w_scales, vocab, cols, out_mult, softcap, out,
+                                        out_dtype, ld_out, workspace, workspace_bytes, 0, 0, stream_handle);
+}
+
+int flce_microscale_linear_limited(const void* x, int dtype, int64_t ld_x, int64_t rows, const void* w_codes,
+                                   const void* w_scales, int64_t vocab, int64_t cols, float out_mult, float softcap,
+                                   void* out, int out_dtype, int64_t ld_out, void* workspace, size_t workspace_bytes,
+                                   int64_t timeout_ns, int flags, void* stream_handle) {
+  if (timeout_ns < 0 || (flags & ~FLCE_FLAG_TEST_STALL)) return FLCE_ERR_ARG;
   int rc = check_product(rows, vocab, cols, w_codes, w_scales, out_mult, softcap, out, out_dtype, &ld_out, workspace);
   if (rc != FLCE_OK) return rc;
   if (!dtype_ok(dtype) || ld_x < cols) return FLCE_ERR_ARG;
@@ -263,6 +272,8 @@ int flce_microscale_linear(const void* x, int dtype, int64_t ld_x, int64_t rows,
   uint8_t* scales = codes + round256(mx_codes(rows, cols));
   MxGemmParams g = product(rows, vocab, cols, codes, scales, w_codes, w_scales, out_mult, softcap, out, out_dtype, ld_out,
                            workspace);
+  if (timeout_ns > 0) g.timeout_ns = static_cast<uint64_t>(timeout_ns);
+  g.stall = (flags & FLCE_FLAG_TEST_STALL) != 0;
   if (mx_gemm_encodes(rows, cols)) {
     g.x = x;
     g.x_dtype = dtype;

@@ -78,6 +78,7 @@ struct MxGemmParams {
   int64_t ld_out;
   int32_t* status;
   uint64_t timeout_ns;
+  int stall;  // FLCE_FLAG_TEST_STALL
 };
 // Whether launch_mx_gemm takes tokens of this shape as x.
 bool mx_gemm_encodes(int64_t rows, int64_t cols);

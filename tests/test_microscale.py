@@ -379,3 +379,37 @@ def test_workspace_of_the_caller():
     for bad in (ws[:n - 1], ws.int(), ws.cpu(), torch.zeros(2 * n, dtype=torch.uint8, device="cuda")[::2]):
         with pytest.raises(ValueError, match="workspace"):
             flce.flce_microscale_linear(h, W, workspace=bad)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,K,V", [(3, 2048, 40000), (3, 64, 300), (40, 1056, 3000), (30, 10016, 2000), (100, 2048, 30000),
+                                   (128, 8224, 500), (300, 2048, 20000), (300, 96, 20001), (700, 4096, 4097)])
+def test_waits_that_run_out(N, K, V):
+    """The product's MMAs held back: the copies of as many stages as there are come in,
+    every other wait gives up, the call ends with its status soon after the limit, and
+    the next one is right. Short and long rows, tokens encoded in place, resident and
+    streamed, and prompts on pairs of CTAs with both forms of output."""
+    import time
+
+    import linear_cross_entropy_02_gb300 as flce
+    from linear_cross_entropy_02_gb300 import _lib as B
+    h = torch.randn(N, K, device="cuda", dtype=torch.bfloat16)
+    W = flce.flce_microscale_quantize(torch.randn(V, K, device="cuda"))
+    want = flce.flce_microscale_linear(h, W)
+    out = torch.empty_like(want)
+    ws = torch.empty(B.lib().flce_microscale_workspace_size(N, K), dtype=torch.uint8, device="cuda")
+
+    def call(timeout_ns, flags):
+        return B.lib().flce_microscale_linear_limited(h.data_ptr(), 0, K, N, W.codes.data_ptr(), W.scales.data_ptr(), V, K, 1.0,
+                                                      0.0, out.data_ptr(), 0, V, ws.data_ptr(), ws.numel(), timeout_ns, flags,
+                                                      torch.cuda.current_stream().cuda_stream)
+    assert call(-1, 0) == call(0, 1) == B.FLCE_ERR_ARG
+    torch.cuda.synchronize()
+    t0 = time.perf_counter()
+    assert call(50_000_000, flce.FLCE_FLAG_TEST_STALL) == B.FLCE_OK
+    torch.cuda.synchronize()
+    # the limit, 10 ms more, and a host that may be slow to notice
+    assert 0.05 <= time.perf_counter() - t0 < 1.0
+    assert flce.flce_get_status(workspace=ws) == B.FLCE_ERR_TIMEOUT
+    assert call(0, 0) == B.FLCE_OK
+    assert flce.flce_get_status(workspace=ws) == 0 and torch.equal(out, want)
