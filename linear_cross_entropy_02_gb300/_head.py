@@ -428,5 +428,7 @@ class LanguageModelHead(torch.nn.Module):
 
     @torch.no_grad()
     def next_token(self, hidden: torch.Tensor, u: torch.Tensor, **settings):
-        """(tokens, logprobs) for hidden [..., H] and random numbers u [...]; settings as in flce_sample."""
+        """(tokens, logprobs) for hidden [..., H] and random numbers u [...]; settings
+        as in flce_sample. The logits are rounded to hidden's dtype in between; for
+        32 bits of them take flce_sample(self.logits(hidden, torch.float32), u, ...)."""
         return flce_sample(self.logits(hidden), u, **settings)

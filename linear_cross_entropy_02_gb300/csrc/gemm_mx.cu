@@ -51,7 +51,12 @@ constexpr int kWBytes = kTileV * kRowBytes;
 constexpr int kSfTiles = kStageK / kMxTileCols;  // scale tiles per 128 rows and stage
 constexpr int kThreads = 320;
 constexpr int kSmemBudget = 226 * 1024;
-constexpr int64_t kMostFused = 40960;  // 4 tokens of 7168: 83.0 us so, 83.8 with a launch before; 8: 86.9 and 85
+// (Microseconds of a single cold call so, and with a launch before it: 5 tokens of 7168 on 129280
+// entries 100.4 and 102.4, 8 102.4 and 102.6, 12 105.3 and 103.3; 8 of 4096 on 128256
+// 66.7 and 69.9, 12 67.6 and 70.1, 16 70.0 and 70.2, 24 71.7 and 68; 37 of 1056 on 50257
+// 20.5 and 23.6, 64 24.6 and 23.6; 16 of 2048 on 32000 18.4 and 21.5, 32 22.5 and 21.5.
+// They meet between 50000 and 65000 elements on all four.)
+constexpr int64_t kMostFused = 40960;
 
 // Shared and tensor memory of a tile of NT tokens. RESIDENT: A's codes and scales
 // stay in shared memory in front of the ring, which then holds W alone.
@@ -407,8 +412,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // A single CTA's 128 x 192 tile drew 43 KB per K = 256 for 384 cycles of MMAs, more
 // than an SM gets from the L2: 4096 tokens on 128256 x 4096 took 1106 us, 786 of
 // them with the MMAs left out. Here each CTA holds 128 rows of M and 128 of N, 35 KB
-// with the scales for 512 cycles, and the same product takes 628 us (6.9 PFLOP/s);
-// the MMAs alone 505, the copies alone 376. M = 256, N = 256 fill half of tensor
+// with the scales for 512 cycles, and the same product takes 625 to 640 us (6.7 to
+// 6.9 PFLOP/s) of encoded tokens in calls now and then, 700 (6.2) after hundreds back
+// to back, when the clock falls; the MMAs alone 505, the copies alone 376. M = 256, N = 256 fill half of tensor
 // memory, so that the other half holds scales and the accumulator is one: sixteen
 // warps take it into registers at once and store from there, under the next tile's
 // MMAs. Between two tiles the MMAs rest for about 960 of 8200 cycles.
