@@ -1,0 +1,87 @@
+/*
+ * flce_model.h - C ABI of the operators at the two ends of a model whose head is
+ * the fused linear cross-entropy: embeddings in the head's weight, the residual's
+ * addition with the norm behind it, 8-bit checkpoints of what that norm keeps for
+ * its backward pass, and the verification of drafted tokens.
+ *
+ * The conventions of flce.h and flce_head.h hold: device pointers owned by the
+ * caller, no allocation, no host synchronisation, asynchronous on `stream`, FLCE_*
+ * return codes found on the host before any launch, nothing trapped or thrown, the
+ * current device owns the stream and every pointer. Element types are
+ * FLCE_DTYPE_BF16 and FLCE_DTYPE_F32; every sum and statistic is held in 32 bits
+ * or more, and bf16 results are rounded once (to nearest even). Outputs overlap
+ * neither each other nor an input. The calls find no errors on the device; their
+ * workspaces hold no status.
+ */
+#ifndef FLCE_MODEL_H
+#define FLCE_MODEL_H
+
+#include "flce_head.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* ---------------------------------------------------------------- 8-bit checkpoints
+ * A matrix [rows, H] of activations in 8 bits with a scale for each 32 consecutive
+ * elements of a row (the last block of a row may be shorter):
+ *   e    = the least whole number >= -127 with max |x| of the block <= 448 2^e
+ *   code = x 2^-e rounded to nearest (ties to even) in E4M3
+ * codes [rows, H] bytes and scales [rows, ceil(H / 32)] bytes (e + 127, E8M0), both
+ * contiguous. A block with an infinity or NaN gets the NaN scale (255) and reads
+ * back as NaN. H up to 2^24. flce_checkpoint_load writes what they stand for,
+ * out [rows, H] contiguous, in out_dtype (exact but below its normal range). */
+int flce_checkpoint_store(const void* x, int dtype, int64_t rows, int64_t hidden, int64_t ld_x, void* codes, void* scales,
+                          void* stream);
+int flce_checkpoint_load(const void* codes, const void* scales, int64_t rows, int64_t hidden, void* out, int out_dtype,
+                         void* stream);
+
+/* ---------------------------------------------------------------- residual and norm
+ *   s = x + residual, rounded to x's type;  y = norm(s), as flce_layer_norm of s
+ * residual [rows, ld_residual], NULL for s = x. sum [rows, H] gets s, codes and
+ * scales its 8-bit checkpoint; sum, and codes with scales, are nullable. The rest is
+ * as in flce_layer_norm; y, sum, codes are contiguous. */
+int flce_add_layer_norm(const void* x, int64_t ld_x, const void* residual, int64_t ld_residual, int dtype, int64_t rows,
+                        int64_t hidden, const void* weight, const void* bias, int weight_dtype, float eps, int rms, void* y,
+                        void* sum, void* codes, void* scales, float* mean, float* rstd, void* stream);
+
+/* Backward, from s (x [rows, ld_x]) or, where x is NULL, from its checkpoint, and the
+ * saved statistics:
+ *   grad_x = grad_sum + the norm's gradient (flce_layer_norm_backward of grad_y),
+ * rounded once to `dtype`, the type of grad_y, grad_sum, grad_x and x; it is the gradient
+ * of x and of the residual alike. grad_sum is the gradient of s from its other uses, NULL
+ * for none. The rest is as in flce_layer_norm_backward. */
+size_t flce_add_layer_norm_workspace_size(int64_t rows, int64_t hidden);
+int flce_add_layer_norm_backward(const void* grad_y, int64_t ld_grad_y, const void* grad_sum, int64_t ld_grad_sum, const void* x,
+                                 int64_t ld_x, const void* codes, const void* scales, int dtype, int64_t rows, int64_t hidden,
+                                 const void* weight, int weight_dtype, const float* mean, const float* rstd, int rms, void* grad_x,
+                                 float* grad_weight, float* grad_bias, int accumulate, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+/* ---------------------------------------------------------------- embeddings
+ *   out[i] = scale W[tokens[i]],  W [vocab, ld_w], out [rows, H] contiguous in out_dtype
+ * A negative token stands for none and gives a row of zeros; one at or behind the
+ * vocabulary gives a row of NaN. */
+int flce_embedding(const int64_t* tokens, int64_t rows, const void* W, int dtype, int64_t ld_w, int64_t vocab, int64_t hidden,
+                   float scale, void* out, int out_dtype, void* stream);
+
+/* Its gradient: grad_W[t] = scale (sum of grad_out[i] over i with tokens[i] = t), fp32
+ * [vocab, H] contiguous, summed in an order that depends on the tokens alone: results do
+ * not change from run to run. accumulate != 0 adds it to what grad_W holds (the fused
+ * head's accumulator, for a weight that is both), else absent tokens' rows are zeroed.
+ * Tokens outside of the vocabulary count for nothing. vocab < 2^31 - 1. */
+size_t flce_embedding_workspace_size(int64_t rows, int64_t hidden);
+int flce_embedding_backward(const void* grad_out, int dtype, int64_t ld_grad, const int64_t* tokens, int64_t rows, int64_t vocab,
+                            int64_t hidden, float scale, float* grad_W, int accumulate, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
+/* Kernel ids of these operators for flce_profile_read and flce_kernel_name: a
+ * read of n > FLCE_MODEL_KERNEL_FIRST entries reaches them. */
+#define FLCE_MODEL_KERNEL_FIRST 48
+#define FLCE_MODEL_KERNEL_COUNT 7
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* FLCE_MODEL_H */

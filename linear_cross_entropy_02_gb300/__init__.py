@@ -37,6 +37,8 @@ __all__ = [
     "vp_gather_partials", "vp_reduce_grad_h",
     "flce_layer_norm", "flce_layer_norm_backward", "layer_norm", "MicroscaleTensor", "flce_microscale_quantize",
     "flce_microscale_dequantize", "flce_microscale_linear", "flce_sample", "LanguageModelHead",
+    "flce_add_layer_norm", "flce_add_layer_norm_backward", "add_layer_norm", "CheckpointTensor", "flce_checkpoint_store",
+    "flce_checkpoint_load", "flce_embedding", "flce_embedding_backward", "embedding",
 ]
 
 _REDUCTIONS = {"mean": FLCE_REDUCTION_MEAN, "sum": FLCE_REDUCTION_SUM, "none": _lib.FLCE_REDUCTION_NONE}
@@ -758,7 +760,7 @@ def flce_profile_begin(enable: bool = True) -> None:
 
 def flce_profile_read() -> dict:
     """{kernel name: (launches, total ms)} of the launches recorded since flce_profile_begin(True)."""
-    n = _lib.FLCE_HEAD_KERNEL_FIRST + _lib.FLCE_HEAD_KERNEL_COUNT  # the operators around the head follow the head's own
+    n = _lib.FLCE_MODEL_KERNEL_FIRST + _lib.FLCE_MODEL_KERNEL_COUNT  # the operators around the head and at the model's ends follow the head's own
     launches = (ctypes.c_int64 * n)()
     ms = (ctypes.c_double * n)()
     rc = _lib.lib().flce_profile_read(launches, ms, n)
@@ -771,3 +773,5 @@ def flce_profile_read() -> dict:
 from ._head import (LanguageModelHead, MicroscaleTensor, flce_layer_norm, flce_layer_norm_backward,  # noqa: E402
                     flce_microscale_dequantize, flce_microscale_linear, flce_microscale_quantize, flce_sample,
                     layer_norm)
+from ._model import (CheckpointTensor, add_layer_norm, embedding, flce_add_layer_norm, flce_add_layer_norm_backward,  # noqa: E402
+                     flce_checkpoint_load, flce_checkpoint_store, flce_embedding, flce_embedding_backward)

@@ -17,7 +17,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libflce.so")
 
 SOURCES = ["engine.cpp", "gemm_tc.cu", "kernels_aux.cu", "kernels_ce.cu", "no_alloc.cu",
-           "head_api.cpp", "norm.cu", "microscale.cu", "gemm_mx.cu", "sample.cu"]
+           "head_api.cpp", "norm.cu", "microscale.cu", "gemm_mx.cu", "sample.cu",
+           "model_api.cpp", "add_norm.cu", "add_norm_8bit.cu", "checkpoint.cu", "embedding.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -28,7 +29,7 @@ def _nvcc() -> str:
 
 def _deps():
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files += [os.path.join(INCLUDE, f) for f in ("flce.h", "flce_head.h")]
+    files += [os.path.join(INCLUDE, f) for f in ("flce.h", "flce_head.h", "flce_model.h")]
     files.append(os.path.abspath(__file__))
     return files
 

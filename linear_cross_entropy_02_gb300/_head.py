@@ -368,11 +368,14 @@ class LanguageModelHead(torch.nn.Module):
     change that torch counts (an optimiser's step, load_state_dict, an edit in
     place). After an edit through .data, which torch does not count, call
     prepare_answers(). A graph replays the one that it was captured with. softcap
-    and out_mult mean the same in both."""
+    and out_mult mean the same in both. Where the last layer's residual is given, it
+    is added in front of the norm, in the same pass. With checkpoint_8bit the norm
+    keeps what it normalised in 8 bits for its backward pass. embed(tokens) looks
+    tokens up in W, for a model whose embedding and head are one weight."""
 
     def __init__(self, weight: torch.Tensor, norm_weight: Optional[torch.Tensor] = None,
                  norm_bias: Optional[torch.Tensor] = None, *, eps: float = 1e-5, rms: bool = True, softcap: float = 0.0,
-                 out_mult: float = 1.0, ignore_index: int = -100, reduction: str = "mean"):
+                 out_mult: float = 1.0, ignore_index: int = -100, reduction: str = "mean", checkpoint_8bit: bool = False):
         super().__init__()
         if weight.dim() != 2:
             raise ValueError("weight must be [V, H]")
@@ -386,18 +389,31 @@ class LanguageModelHead(torch.nn.Module):
         self.eps, self.rms = float(eps), bool(rms)
         self.softcap, self.out_mult = float(softcap), float(out_mult)
         self.ignore_index, self.reduction = int(ignore_index), reduction
+        self.checkpoint_8bit = bool(checkpoint_8bit)
         self.answers: Optional[MicroscaleTensor] = None
         self._made = (None, None)  # what prepare_answers() made, and from which W
 
-    def normalise(self, hidden: torch.Tensor) -> torch.Tensor:
+    def normalise(self, hidden: torch.Tensor, residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+        from . import _model
+        kw = dict(eps=self.eps, rms=self.rms)
         if torch.is_grad_enabled():
-            return layer_norm(hidden, self.norm_weight, self.norm_bias, eps=self.eps, rms=self.rms)
-        return flce_layer_norm(hidden, self.norm_weight, self.norm_bias, eps=self.eps, rms=self.rms)
+            if residual is None and not self.checkpoint_8bit:
+                return layer_norm(hidden, self.norm_weight, self.norm_bias, **kw)
+            return _model.add_layer_norm(hidden, residual, self.norm_weight, self.norm_bias, checkpoint_8bit=self.checkpoint_8bit,
+                                         need_sum=False, **kw)[0]
+        if residual is None:
+            return flce_layer_norm(hidden, self.norm_weight, self.norm_bias, **kw)
+        return _model.flce_add_layer_norm(hidden, residual, self.norm_weight, self.norm_bias, need_sum=False, **kw)["y"]
 
-    def loss(self, hidden: torch.Tensor, labels: torch.Tensor):
-        """(loss, token_accuracy) of hidden [..., H] and int64 labels [...]."""
+    def embed(self, tokens: torch.Tensor, scale: float = 1.0) -> torch.Tensor:
+        """scale W[tokens], [..., H]; negative tokens give zeros. The gradient flows to W."""
+        from . import _model
+        return _model.embedding(tokens, self.weight, scale=scale)
+
+    def loss(self, hidden: torch.Tensor, labels: torch.Tensor, residual: Optional[torch.Tensor] = None):
+        """(loss, token_accuracy) of hidden [..., H] (plus residual) and int64 labels [...]."""
         from . import linear_cross_entropy
-        return linear_cross_entropy(self.normalise(hidden), self.weight, labels, softcap=self.softcap,
+        return linear_cross_entropy(self.normalise(hidden, residual), self.weight, labels, softcap=self.softcap,
                                     out_mult=self.out_mult, ignore_index=self.ignore_index, reduction=self.reduction)
 
     forward = loss
@@ -421,14 +437,14 @@ class LanguageModelHead(torch.nn.Module):
         return self.prepare_answers()
 
     @torch.no_grad()
-    def logits(self, hidden: torch.Tensor, out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    def logits(self, hidden: torch.Tensor, out_dtype: Optional[torch.dtype] = None, residual: Optional[torch.Tensor] = None) -> torch.Tensor:
         """Logits [..., V] on the microscaled W."""
-        return flce_microscale_linear(self.normalise(hidden), self._current_answers(), out_mult=self.out_mult, softcap=self.softcap,
-                                      out_dtype=out_dtype)
+        return flce_microscale_linear(self.normalise(hidden, residual), self._current_answers(), out_mult=self.out_mult,
+                                      softcap=self.softcap, out_dtype=out_dtype)
 
     @torch.no_grad()
-    def next_token(self, hidden: torch.Tensor, u: torch.Tensor, **settings):
-        """(tokens, logprobs) for hidden [..., H] and random numbers u [...]; settings
+    def next_token(self, hidden: torch.Tensor, u: torch.Tensor, residual: Optional[torch.Tensor] = None, **settings):
+        """(tokens, logprobs) for hidden [..., H] (plus residual) and random numbers u [...]; settings
         as in flce_sample. The logits are rounded to hidden's dtype in between; for
         32 bits of them take flce_sample(self.logits(hidden, torch.float32), u, ...)."""
-        return flce_sample(self.logits(hidden), u, **settings)
+        return flce_sample(self.logits(hidden, residual=residual), u, **settings)

@@ -62,6 +62,15 @@ HEAD_EXPORTED = [
     "flce_sample",
 ]
 
+# include/flce_model.h
+FLCE_MODEL_KERNEL_FIRST = 48
+FLCE_MODEL_KERNEL_COUNT = 7
+
+MODEL_EXPORTED = [
+    "flce_checkpoint_store", "flce_checkpoint_load", "flce_add_layer_norm", "flce_add_layer_norm_workspace_size",
+    "flce_add_layer_norm_backward", "flce_embedding", "flce_embedding_workspace_size", "flce_embedding_backward",
+]
+
 
 class FlceParams(ctypes.Structure):
     _fields_ = [
@@ -157,6 +166,7 @@ def lib() -> ctypes.CDLL:
                                        _vp, _vp, _vp, _sz, _vp]
         L.flce_vp_backward.restype = ctypes.c_int
         _bind_head(L)
+        _bind_model(L)
         _lib = L
         return L
 
@@ -178,6 +188,23 @@ def _bind_head(L: ctypes.CDLL) -> None:
             ("flce_microscale_linear", i, [_vp, i, l, l, _vp, _vp, l, l, f, f, _vp, i, l, _vp, _sz, _vp]),
             ("flce_microscale_linear_limited", i, [_vp, i, l, l, _vp, _vp, l, l, f, f, _vp, i, l, _vp, _sz, l, i, _vp]),
             ("flce_sample", i, [_vp, i, l, l, l, _vp, _vp, f, _vp, ctypes.c_int32, _vp, f, _vp, f, _vp, _vp, _vp])):
+        fn = getattr(L, name)
+        fn.restype, fn.argtypes = res, args
+
+
+def _bind_model(L: ctypes.CDLL) -> None:
+    """Argument types of the entries of include/flce_model.h."""
+    i, l, f = ctypes.c_int, ctypes.c_int64, ctypes.c_float
+    for name, res, args in (
+            ("flce_checkpoint_store", i, [_vp, i, l, l, l, _vp, _vp, _vp]),
+            ("flce_checkpoint_load", i, [_vp, _vp, l, l, _vp, i, _vp]),
+            ("flce_add_layer_norm", i, [_vp, l, _vp, l, i, l, l, _vp, _vp, i, f, i, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+            ("flce_add_layer_norm_workspace_size", _sz, [l, l]),
+            ("flce_add_layer_norm_backward", i, [_vp, l, _vp, l, _vp, l, _vp, _vp, i, l, l, _vp, i, _vp, _vp, i, _vp, _vp, _vp, i,
+                                                 _vp, _sz, _vp]),
+            ("flce_embedding", i, [_vp, l, _vp, i, l, l, l, f, _vp, i, _vp]),
+            ("flce_embedding_workspace_size", _sz, [l, l]),
+            ("flce_embedding_backward", i, [_vp, i, l, _vp, l, l, l, f, _vp, i, _vp, _sz, _vp])):
         fn = getattr(L, name)
         fn.restype, fn.argtypes = res, args
 

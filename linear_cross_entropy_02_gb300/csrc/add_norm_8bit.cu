@@ -1,0 +1,12 @@
+// Backward pass of the norm from an 8-bit checkpoint of what it normalised
+// (norm_device.cuh, checkpoint_device.cuh).
+#include "model_internal.h"
+#include "norm_device.cuh"
+
+namespace flce {
+
+cudaError_t launch_add_norm_bwd_8bit(const NormParams& p, int sms, int* partials, cudaStream_t s) {
+  return p.dtype == FLCE_DTYPE_F32 ? launch_bwd<float, 4, kAdd8>(p, sms, partials, s) : launch_bwd<uint16_t, 8, kAdd8>(p, sms, partials, s);
+}
+
+}  // namespace flce

@@ -1,0 +1,386 @@
+// Embeddings: rows of W looked up by token and scaled, and the gradient, which adds
+// rows up by token.
+//
+// The lookup is a copy, bound by memory: a warp takes a piece of a row with kUnroll
+// vectors per lane in flight.
+//
+// The gradient sorts (token, position) pairs and then adds up runs of one token, so
+// that every row of grad_W is written once, by one thread per column, in the order of
+// the positions: no atomics decide an order, and the result is the same in every run.
+// Pieces of kChunk tokens are sorted in shared memory; a key's place among all of them
+// is its place in its piece plus what the others hold before it, found by binary search.
+// The sorted rows are then cut into tiles of kEmbeddingTile: a tile's CTA walks its rows
+// with the sum in registers and writes it where the token changes. Frequent tokens (in
+// text the first takes a tenth of all places) fill many tiles; what such a tile sums of a
+// run that does not end in it goes to the workspace, and a second kernel joins these sums
+// in order. Where the gradient is not added to what grad_W holds, the rows of absent
+// tokens are zeroed by CTAs of the same launch: nothing is written twice.
+#include "flce_host.h"
+#include "head_device.cuh"
+#include "model_internal.h"
+
+namespace flce {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kUnroll = 4;
+constexpr int kChunk = 1024;       // keys sorted by a CTA
+constexpr int kSortThreads = 512;
+constexpr int kGradThreads = 128;
+constexpr int kTile = kEmbeddingTile;
+constexpr int kBatch = 8;          // rows of a tile in flight
+constexpr int kZeroFloats = 65536; // of absent rows per CTA, about
+
+// ------------------------------------------------------------------ forward
+template <typename T, int E>
+__device__ __forceinline__ void store_floats(T* to, const float (&v)[E]) {
+  if constexpr (E == 1) {
+    to[0] = from_float<T>(v[0]);
+  } else if constexpr (sizeof(T) * E == 8) {
+    *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+  } else if constexpr (sizeof(T) == 2) {
+    store_raw<T, E>(to, pack<T, E>(v));
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; e += 4) *reinterpret_cast<float4*>(to + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+  }
+}
+
+template <typename TI, typename TO, int E>
+__global__ void __launch_bounds__(kThreads) embedding_kernel(const EmbeddingParams p, const int64_t chunks) {
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32;
+  if (unit >= p.rows * chunks) return;
+  const int64_t row = unit / chunks, vecs = p.hidden / E;
+  const int64_t first = (unit - row * chunks) * (32 * kUnroll) + (threadIdx.x & 31);
+  const int64_t token = __ldg(p.tokens + row);
+  const bool real = token >= 0 && token < p.vocab;
+  const TI* w = static_cast<const TI*>(p.in) + (real ? token : 0) * p.ld;
+  TO* out = static_cast<TO*>(p.out) + row * p.hidden;
+  Raw<TI, E> raw[kUnroll];
+#pragma unroll
+  for (int j = 0; j < kUnroll; ++j)
+    if (real && first + j * 32 < vecs) raw[j] = load_raw<TI, E>(w + (first + j * 32) * E);
+  // no token gives zeros, one behind the vocabulary NaN
+  const float other = token < 0 ? 0.f : __uint_as_float(0x7FC00000u);
+#pragma unroll
+  for (int j = 0; j < kUnroll; ++j) {
+    const int64_t v = first + j * 32;
+    if (v < vecs) {
+      float f[E];
+      if (real) {
+        unpack<TI, E>(raw[j], f);
+#pragma unroll
+        for (int e = 0; e < E; ++e) f[e] *= p.scale;
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) f[e] = other;
+      }
+      store_floats<TO, E>(out + v * E, f);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ sort
+// Sorts kChunk (token, position) keys of the CTA's piece; tokens outside of the
+// vocabulary count as `vocab` and come last.
+__global__ void __launch_bounds__(kSortThreads) embedding_chunk_kernel(const int64_t* tokens, const int64_t rows, const int64_t vocab,
+                                                                     uint32_t* sorted, uint32_t* places) {
+  __shared__ uint64_t key[kChunk];
+  const int64_t base = static_cast<int64_t>(blockIdx.x) * kChunk;
+  for (int i = threadIdx.x; i < kChunk; i += kSortThreads) {
+    uint64_t k = ~0ull;  // behind the last row
+    if (base + i < rows) {
+      const int64_t t = __ldg(tokens + base + i);
+      k = static_cast<uint64_t>(t >= 0 && t < vocab ? t : vocab) << 32 | static_cast<uint32_t>(base + i);
+    }
+    key[i] = k;
+  }
+  __syncthreads();
+  // bitonic: runs of `run` are merged into runs of twice that, up and down in turn
+  for (int run = 2; run <= kChunk; run *= 2) {
+    for (int step = run / 2; step > 0; step /= 2) {
+      const int i = 2 * threadIdx.x - (threadIdx.x & (step - 1));  // the pair's first
+      const uint64_t a = key[i], b = key[i + step];
+      if ((a > b) == ((i & run) == 0)) {
+        key[i] = b;
+        key[i + step] = a;
+      }
+      __syncthreads();
+    }
+  }
+  for (int i = threadIdx.x; i < kChunk && base + i < rows; i += kSortThreads) {
+    sorted[base + i] = static_cast<uint32_t>(key[i] >> 32);
+    places[base + i] = static_cast<uint32_t>(key[i]);
+  }
+}
+
+// Keys of a[0, n) that come before t: less than t, or (UPTO) equal to it.
+template <bool UPTO>
+__device__ __forceinline__ uint32_t keys_before(const uint32_t* a, uint32_t n, uint32_t t) {
+  uint32_t lo = 0, hi = n;
+  while (lo < hi) {
+    const uint32_t mid = (lo + hi) / 2;
+    const uint32_t k = __ldg(a + mid);
+    if (UPTO ? k <= t : k < t)
+      lo = mid + 1;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+// Joins `group` sorted runs of `run` keys each: a key moves to the number of keys before
+// it. Of equal tokens the earlier run's come first, as their positions do.
+__global__ void __launch_bounds__(kThreads) embedding_merge_kernel(const uint32_t* sorted, const uint32_t* places, uint32_t* to_sorted,
+                                                                 uint32_t* to_places, const int64_t rows, const int64_t run,
+                                                                 const int group) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  if (i >= rows) return;
+  const uint32_t t = __ldg(sorted + i), place = __ldg(places + i);
+  const int64_t mine = i / run, first = mine / group * group;
+  int64_t at = first * run + (i - mine * run);
+  for (int64_t r = first; r < first + group && r * run < rows; ++r) {
+    const uint32_t n = static_cast<uint32_t>(min(run, rows - r * run));
+    if (r < mine)
+      at += keys_before<true>(sorted + r * run, n, t);
+    else if (r > mine)
+      at += keys_before<false>(sorted + r * run, n, t);
+  }
+  to_sorted[at] = t;
+  to_places[at] = place;
+}
+
+// ------------------------------------------------------------------ gradient
+// A thread's columns: C vectors of E, kGradThreads apart.
+template <int E>
+__device__ __forceinline__ void put(float* to, const float (&v)[E], float scale, bool add) {
+  if constexpr (E == 1) {
+    if (add)
+      atomicAdd(to, v[0] * scale);  // (the only addition to this element in the launch)
+    else
+      *to = v[0] * scale;
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; e += 4) {
+      const float4 f = make_float4(v[e] * scale, v[e + 1] * scale, v[e + 2] * scale, v[e + 3] * scale);
+      if (add)
+        atomicAdd(reinterpret_cast<float4*>(to + e), f);
+      else
+        *reinterpret_cast<float4*>(to + e) = f;
+    }
+  }
+}
+
+// CTAs from `tiles` * `slices` on zero rows of absent tokens.
+template <typename T, int E, int C>
+__global__ void __launch_bounds__(kGradThreads) embedding_grad_kernel(const EmbeddingParams p, const int64_t tiles, const int slices,
+                                                                    const int zero_rows) {
+  constexpr int kColumns = kGradThreads * E * C;
+  const int64_t work = tiles * slices;
+  float* grad_W = static_cast<float*>(p.out);
+  if (blockIdx.x >= work) {
+    __shared__ bool present[kGradThreads];
+    const int64_t r0 = (blockIdx.x - work) * zero_rows;
+    const int n = static_cast<int>(min(static_cast<int64_t>(zero_rows), p.vocab - r0));
+    if (threadIdx.x < n) {
+      const uint32_t t = static_cast<uint32_t>(r0 + threadIdx.x);
+      const uint32_t at = keys_before<false>(p.sorted, static_cast<uint32_t>(p.rows), t);
+      present[threadIdx.x] = at < p.rows && p.sorted[at] == t;
+    }
+    __syncthreads();
+    for (int r = 0; r < n; ++r) {
+      if (present[r]) continue;
+      float* row = grad_W + (r0 + r) * p.hidden;
+      if constexpr (E > 1) {
+        for (int64_t i = threadIdx.x * 4; i < p.hidden; i += kGradThreads * 4) *reinterpret_cast<float4*>(row + i) = make_float4(0, 0, 0, 0);
+      } else {
+        for (int64_t i = threadIdx.x; i < p.hidden; i += kGradThreads) row[i] = 0.f;
+      }
+    }
+    return;
+  }
+  // tokens of the tile with one on either side; none is vocab + 1
+  __shared__ uint32_t token[kTile + 2], place[kTile];
+  const int64_t tile = blockIdx.x / slices, r0 = tile * kTile;
+  const int slice = static_cast<int>(blockIdx.x - tile * slices);
+  const uint32_t none = static_cast<uint32_t>(p.vocab) + 1, skipped = static_cast<uint32_t>(p.vocab);
+  if (threadIdx.x < kTile + 2) {
+    const int64_t i = r0 + static_cast<int>(threadIdx.x) - 1;
+    token[threadIdx.x] = i >= 0 && i < p.rows ? p.sorted[i] : none;
+    if (threadIdx.x >= 1 && threadIdx.x <= kTile) place[threadIdx.x - 1] = i < p.rows ? p.places[i] : 0;
+  }
+  __syncthreads();
+  const int64_t col = static_cast<int64_t>(slice) * kColumns + threadIdx.x * E;
+  float acc[C][E];
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[c][e] = 0.f;
+  bool leading = token[1] == token[0];  // the run began before this tile
+  for (int b = 0; b < kTile; b += kBatch) {
+    Raw<T, E> raw[kBatch][C];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const uint32_t t = token[b + j + 1];
+      if (t < skipped) {
+        const T* row = static_cast<const T*>(p.in) + place[b + j] * p.ld + col;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+          if (col + c * kGradThreads * E < p.hidden) raw[j][c] = load_raw<T, E>(row + c * kGradThreads * E);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const uint32_t t = token[b + j + 1];
+      if (t >= skipped) return;  // nothing of the vocabulary comes behind
+      const bool ends = token[b + j + 2] != t, last = b + j == kTile - 1;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        if (col + c * kGradThreads * E < p.hidden) {
+          float v[E];
+          unpack<T, E>(raw[j][c], v);
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[c][e] += v[e];
+          if (ends || last) {
+            const int64_t at = col + c * kGradThreads * E;
+            if (leading)
+              put<E>(p.head + tile * p.hidden + at, acc[c], 1.f, false);
+            else if (!ends)
+              put<E>(p.tail + tile * p.hidden + at, acc[c], 1.f, false);
+            else
+              put<E>(grad_W + t * p.hidden + at, acc[c], p.scale, p.accumulate != 0);
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[c][e] = 0.f;
+          }
+        }
+      }
+      if (ends) leading = false;
+    }
+  }
+}
+
+// Joins the sums of a run that begins in the CTA's tile and goes on behind it.
+template <int E>
+__global__ void __launch_bounds__(kGradThreads) embedding_join_kernel(const EmbeddingParams p, const int slices) {
+  const int64_t tile = blockIdx.x / slices, r0 = tile * kTile, next = r0 + kTile;
+  const int slice = static_cast<int>(blockIdx.x - tile * slices);
+  if (next >= p.rows) return;
+  const uint32_t t = p.sorted[next - 1];
+  if (t >= p.vocab || p.sorted[next] != t) return;
+  if (p.sorted[r0] == t && r0 > 0 && p.sorted[r0 - 1] == t) return;  // it began earlier
+  // the tiles that it reaches into
+  const int64_t end = next + keys_before<true>(p.sorted + next, static_cast<uint32_t>(p.rows - next), t);
+  const int64_t last = (end - 1) / kTile;
+  const int64_t col = (static_cast<int64_t>(slice) * kGradThreads + threadIdx.x) * E;
+  if (col >= p.hidden) return;
+  float acc[E];
+  auto read = [&](const float* from, float (&v)[E]) {
+    if constexpr (E == 1) {
+      v[0] = *from;
+    } else {
+      const float4 f = *reinterpret_cast<const float4*>(from);
+      v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+    }
+  };
+  read(p.tail + tile * p.hidden + col, acc);
+#pragma unroll 8
+  for (int64_t i = tile + 1; i <= last; ++i) {
+    float v[E];
+    read(p.head + i * p.hidden + col, v);
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] += v[e];
+  }
+  put<E>(static_cast<float*>(p.out) + t * p.hidden + col, acc, p.scale, p.accumulate != 0);
+}
+
+inline bool on_vectors(const void* p, int64_t ld, size_t es, int E) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % E == 0 && es * E == 16;
+}
+
+template <typename TI, typename TO>
+cudaError_t run_forward(const EmbeddingParams& p, cudaStream_t s) {
+  constexpr int E = 16 / sizeof(TI);
+  const bool vectors = p.hidden % E == 0 && on_vectors(p.in, p.ld, sizeof(TI), E) && reinterpret_cast<uintptr_t>(p.out) % 16 == 0;
+  const int64_t per = 32LL * kUnroll * (vectors ? E : 1);
+  const int64_t chunks = (p.hidden + per - 1) / per, ctas = (p.rows * chunks + kThreads / 32 - 1) / (kThreads / 32);
+  if (ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  if (vectors)
+    embedding_kernel<TI, TO, E><<<static_cast<unsigned>(ctas), kThreads, 0, s>>>(p, chunks);
+  else
+    embedding_kernel<TI, TO, 1><<<static_cast<unsigned>(ctas), kThreads, 0, s>>>(p, chunks);
+  return cudaGetLastError();
+}
+
+template <typename T, int E, int C>
+int run_grad(const EmbeddingParams& p, cudaStream_t stream) {
+  const int64_t tiles = (p.rows + kTile - 1) / kTile;
+  constexpr int64_t columns = static_cast<int64_t>(kGradThreads) * E * C;
+  const int64_t slices = (p.hidden + columns - 1) / columns;
+  int zero_rows = 0;
+  int64_t ctas = tiles * slices;
+  if (!p.accumulate) {
+    int64_t z = kZeroFloats / p.hidden;
+    zero_rows = static_cast<int>(z < 1 ? 1 : z > kGradThreads ? kGradThreads : z);
+    ctas += (p.vocab + zero_rows - 1) / zero_rows;
+  }
+  if (ctas == 0) return FLCE_OK;
+  if (ctas > 0x7FFFFFFF) return FLCE_ERR_ARG;
+  FLCE_LAUNCH(K_EMBEDDING_GRAD, (embedding_grad_kernel<T, E, C><<<static_cast<unsigned>(ctas), kGradThreads, 0, stream>>>(
+                                     p, tiles, static_cast<int>(slices), zero_rows),
+                                 cudaGetLastError()));
+  if (tiles > 1) {
+    constexpr int JE = E > 1 ? 4 : 1;
+    const int64_t join = (p.hidden + kGradThreads * JE - 1) / (kGradThreads * JE);
+    if (tiles * join > 0x7FFFFFFF) return FLCE_ERR_ARG;
+    FLCE_LAUNCH(K_EMBEDDING_GRAD, (embedding_join_kernel<JE><<<static_cast<unsigned>(tiles * join), kGradThreads, 0, stream>>>(
+                                       p, static_cast<int>(join)),
+                                   cudaGetLastError()));
+  }
+  return FLCE_OK;
+}
+
+template <typename T>
+int run_grad_typed(const EmbeddingParams& p, cudaStream_t s) {
+  constexpr int E = 16 / sizeof(T);
+  if (p.hidden % E == 0 && on_vectors(p.in, p.ld, sizeof(T), E) && reinterpret_cast<uintptr_t>(p.out) % 16 == 0)
+    return run_grad<T, E, 1>(p, s);
+  return run_grad<T, 1, 4>(p, s);
+}
+
+}  // namespace
+
+cudaError_t launch_embedding(const EmbeddingParams& p, cudaStream_t s) {
+  if (p.dtype == FLCE_DTYPE_F32)
+    return p.out_dtype == FLCE_DTYPE_F32 ? run_forward<float, float>(p, s) : run_forward<float, uint16_t>(p, s);
+  return p.out_dtype == FLCE_DTYPE_F32 ? run_forward<uint16_t, float>(p, s) : run_forward<uint16_t, uint16_t>(p, s);
+}
+
+int launch_embedding_sort(EmbeddingParams* p, cudaStream_t stream) {
+  const int64_t chunks = (p->rows + kChunk - 1) / kChunk;
+  FLCE_LAUNCH(K_EMBEDDING_SORT, (embedding_chunk_kernel<<<static_cast<unsigned>(chunks), kSortThreads, 0, stream>>>(
+                                     p->tokens, p->rows, p->vocab, p->sorted, p->places),
+                                 cudaGetLastError()));
+  for (int64_t run = kChunk; run < p->rows;) {
+    const int64_t runs = (p->rows + run - 1) / run;
+    const int group = static_cast<int>(run == kChunk && runs <= 32 ? runs : runs < 8 ? runs : 8);
+    FLCE_LAUNCH(K_EMBEDDING_SORT,
+                (embedding_merge_kernel<<<static_cast<unsigned>((p->rows + kThreads - 1) / kThreads), kThreads, 0, stream>>>(
+                     p->sorted, p->places, p->sorted2, p->places2, p->rows, run, group),
+                 cudaGetLastError()));
+    uint32_t* t = p->sorted;
+    p->sorted = p->sorted2;
+    p->sorted2 = t;
+    t = p->places;
+    p->places = p->places2;
+    p->places2 = t;
+    run *= group;
+  }
+  return FLCE_OK;
+}
+
+int launch_embedding_grad(const EmbeddingParams& p, cudaStream_t s) {
+  return p.dtype == FLCE_DTYPE_F32 ? run_grad_typed<float>(p, s) : run_grad_typed<uint16_t>(p, s);
+}
+
+}  // namespace flce

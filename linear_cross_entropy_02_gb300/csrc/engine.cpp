@@ -30,6 +30,7 @@
 #include <vector>
 
 #include "flce_host.h"
+#include "flce_model.h"
 #include "flce_internal.h"
 
 using namespace flce;
@@ -89,6 +90,11 @@ const char* const kKernelNames[FLCE_NUM_KERNELS] = {
 const char* const kHeadKernelNames[FLCE_HEAD_KERNEL_COUNT] = {
     "layer_norm", "layer_norm_backward", "layer_norm_weight_grad", "microscale_quantize", "microscale_dequantize",
     "microscale_gemm", "sample"};
+
+// Those of the operators at a model's two ends, from FLCE_MODEL_KERNEL_FIRST on.
+const char* const kModelKernelNames[FLCE_MODEL_KERNEL_COUNT] = {
+    "add_layer_norm", "add_layer_norm_backward", "checkpoint_store", "checkpoint_load", "embedding", "embedding_sort",
+    "embedding_grad"};
 
 }  // namespace
 
@@ -1748,6 +1754,8 @@ int flce_profile_read(int64_t* launches, double* total_ms, int n) {
 const char* flce_kernel_name(int id) {
   if (id >= FLCE_HEAD_KERNEL_FIRST && id < FLCE_HEAD_KERNEL_FIRST + FLCE_HEAD_KERNEL_COUNT)
     return kHeadKernelNames[id - FLCE_HEAD_KERNEL_FIRST];
+  if (id >= FLCE_MODEL_KERNEL_FIRST && id < FLCE_MODEL_KERNEL_FIRST + FLCE_MODEL_KERNEL_COUNT)
+    return kModelKernelNames[id - FLCE_MODEL_KERNEL_FIRST];
   if (id < 0 || id >= FLCE_NUM_KERNELS) return "unknown";
   return kKernelNames[id];
 }

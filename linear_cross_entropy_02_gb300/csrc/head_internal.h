@@ -36,6 +36,16 @@ struct NormParams {
   float* rstd;
   float* part_w;     // backward: per-CTA partial sums [grid][hidden], or null
   float* part_b;
+  // behind the residual's addition (model_internal.h): what is added, the sum and its
+  // 8-bit checkpoint, each nullable; backward: the checkpoint in the place of x, and a
+  // gradient of the sum
+  const void* residual;
+  int64_t ld_res;
+  void* sum;
+  uint8_t* codes;
+  uint8_t* scales;
+  const void* gs;
+  int64_t ld_gs;
 };
 // Most partial rows that launch_norm_bwd writes for a call on this device.
 int norm_partial_rows(int64_t rows, int64_t hidden, int sms);

@@ -1,0 +1,65 @@
+// Internal interface between the host entries of the operators at a model's two ends
+// (model_api.cpp) and their kernels.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "flce_model.h"
+#include "head_internal.h"
+
+namespace flce {
+
+enum ModelKernelId {
+  K_ADD_NORM = FLCE_MODEL_KERNEL_FIRST,
+  K_ADD_NORM_BWD,
+  K_CHECKPOINT_STORE,
+  K_CHECKPOINT_LOAD,
+  K_EMBEDDING,
+  K_EMBEDDING_SORT,
+  K_EMBEDDING_GRAD,
+};
+
+// ------------------------------------------------------------ residual and norm
+// (NormParams' last members; K_NORM_WGRAD joins the partial sums)
+cudaError_t launch_add_norm(const NormParams& p, int sms, cudaStream_t s);
+cudaError_t launch_add_norm_bwd(const NormParams& p, int sms, int* partials, cudaStream_t s);
+cudaError_t launch_add_norm_bwd_8bit(const NormParams& p, int sms, int* partials, cudaStream_t s);
+
+// ------------------------------------------------------------ 8-bit checkpoints
+struct CheckpointParams {
+  const void* x;  // store: input
+  void* out;      // load: output
+  int dtype;
+  int64_t rows, hidden, ld;
+  uint8_t* codes;
+  uint8_t* scales;
+};
+cudaError_t launch_checkpoint_store(const CheckpointParams& p, cudaStream_t s);
+cudaError_t launch_checkpoint_load(const CheckpointParams& p, cudaStream_t s);
+
+// ------------------------------------------------------------ embeddings
+struct EmbeddingParams {
+  const int64_t* tokens;
+  int64_t rows, vocab, hidden, ld;  // ld: row stride of W (forward) or of grad_out (backward)
+  float scale;
+  int dtype, out_dtype;
+  const void* in;  // W, or grad_out
+  void* out;       // embeddings, or grad_W (fp32)
+  int accumulate;  // backward
+  // backward: tokens in rising order, their positions rising within one, and the sums of
+  // segments that cross tiles of kEmbeddingTile of them
+  uint32_t* sorted;
+  uint32_t* places;
+  uint32_t* sorted2;  // the other side of a merge
+  uint32_t* places2;
+  float* head;
+  float* tail;
+};
+constexpr int kEmbeddingTile = 32;
+cudaError_t launch_embedding(const EmbeddingParams& p, cudaStream_t s);
+// Sorts the tokens into p->sorted and p->places, which it may swap with the other side.
+int launch_embedding_sort(EmbeddingParams* p, cudaStream_t stream);
+int launch_embedding_grad(const EmbeddingParams& p, cudaStream_t stream);
+
+}  // namespace flce
