@@ -75,10 +75,41 @@ int flce_embedding_backward(const void* grad_out, int dtype, int64_t ld_grad, co
                             int64_t hidden, float scale, float* grad_W, int accumulate, void* workspace, size_t workspace_bytes,
                             void* stream);
 
+/* ---------------------------------------------------------------- verification
+ * For each of `batch` requests: `drafts` drafted tokens d_i, drawn one after another
+ * from a draft model, and the target's logits at their places and at the one behind
+ * them. With p_i the distribution that flce_sample draws from for the target's row i
+ * (whole weights w of the tokens that the request's temperature, top_k, top_p and min_p
+ * keep, W their sum, p = w / W), and q_i that for the draft's row i, or, where `draft` is
+ * NULL, all weight on d_i:
+ *   accepted  the drafts before the first with not u_i q_i(d_i) < p_i(d_i)  (in fp64)
+ *   then one token more, at place n = accepted: where d_n was compared and not accepted,
+ *   drawn from the weights r = floor(max(p_n - q_n, 0) 2^40), p and q as w (1 / W) in fp32
+ *   (from those of p_n if all are 0); else, n = drafts or d_n no token, from p_n's weights:
+ *   the first index at which the running sum of the weights is above u_drafts times
+ *   their sum, as in flce_sample.
+ * That way the tokens are distributed as if drawn from the target alone. A draft outside
+ * of [0, vocab) stands for none: requests may have fewer drafts than others. tokens
+ * [batch, drafts + 1]: the accepted drafts, the token drawn, -1 behind it. accepted
+ * [batch]. logprobs [batch, drafts + 1], nullable: log p of each token, 0 behind the last.
+ * Where a request comes to a row without a distribution (as in flce_sample: NaN or
+ * +infinity, no finite logit, a NaN setting) or to a NaN u, its token there is -1, with a NaN
+ * log-probability, and its last.
+ * target [batch, drafts + 1, vocab] with strides of ld_target (rows) and batch_ld_target
+ * (requests), draft [batch, drafts, vocab] likewise, both of logits_dtype; u [batch, drafts + 1];
+ * draft_tokens [batch, drafts]. temperature and the rest: arrays of one value per request, or
+ * NULL for the scalar beside it. drafts up to 1024, vocab < 2^22. */
+size_t flce_verify_workspace_size(int64_t batch, int64_t drafts);
+int flce_verify(const void* target, int logits_dtype, int64_t batch, int64_t drafts, int64_t vocab, int64_t ld_target,
+                int64_t batch_ld_target, const int64_t* draft_tokens, const void* draft, int64_t ld_draft, int64_t batch_ld_draft,
+                const float* u, const float* temperatures, float temperature, const int32_t* top_ks, int32_t top_k,
+                const float* top_ps, float top_p, const float* min_ps, float min_p, int64_t* tokens, int64_t* accepted,
+                float* logprobs, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Kernel ids of these operators for flce_profile_read and flce_kernel_name: a
  * read of n > FLCE_MODEL_KERNEL_FIRST entries reaches them. */
 #define FLCE_MODEL_KERNEL_FIRST 48
-#define FLCE_MODEL_KERNEL_COUNT 7
+#define FLCE_MODEL_KERNEL_COUNT 9
 
 #ifdef __cplusplus
 }

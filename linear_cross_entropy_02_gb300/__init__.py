@@ -38,7 +38,7 @@ __all__ = [
     "flce_layer_norm", "flce_layer_norm_backward", "layer_norm", "MicroscaleTensor", "flce_microscale_quantize",
     "flce_microscale_dequantize", "flce_microscale_linear", "flce_sample", "LanguageModelHead",
     "flce_add_layer_norm", "flce_add_layer_norm_backward", "add_layer_norm", "CheckpointTensor", "flce_checkpoint_store",
-    "flce_checkpoint_load", "flce_embedding", "flce_embedding_backward", "embedding",
+    "flce_checkpoint_load", "flce_embedding", "flce_embedding_backward", "embedding", "flce_verify",
 ]
 
 _REDUCTIONS = {"mean": FLCE_REDUCTION_MEAN, "sum": FLCE_REDUCTION_SUM, "none": _lib.FLCE_REDUCTION_NONE}
@@ -774,4 +774,4 @@ from ._head import (LanguageModelHead, MicroscaleTensor, flce_layer_norm, flce_l
                     flce_microscale_dequantize, flce_microscale_linear, flce_microscale_quantize, flce_sample,
                     layer_norm)
 from ._model import (CheckpointTensor, add_layer_norm, embedding, flce_add_layer_norm, flce_add_layer_norm_backward,  # noqa: E402
-                     flce_checkpoint_load, flce_checkpoint_store, flce_embedding, flce_embedding_backward)
+                     flce_checkpoint_load, flce_checkpoint_store, flce_embedding, flce_embedding_backward, flce_verify)

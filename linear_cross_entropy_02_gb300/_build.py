@@ -18,7 +18,7 @@ LIB = os.path.join(PKG, "libflce.so")
 
 SOURCES = ["engine.cpp", "gemm_tc.cu", "kernels_aux.cu", "kernels_ce.cu", "no_alloc.cu",
            "head_api.cpp", "norm.cu", "microscale.cu", "gemm_mx.cu", "sample.cu",
-           "model_api.cpp", "add_norm.cu", "add_norm_8bit.cu", "checkpoint.cu", "embedding.cu"]
+           "model_api.cpp", "add_norm.cu", "add_norm_8bit.cu", "checkpoint.cu", "embedding.cu", "verify.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -371,7 +371,8 @@ class LanguageModelHead(torch.nn.Module):
     and out_mult mean the same in both. Where the last layer's residual is given, it
     is added in front of the norm, in the same pass. With checkpoint_8bit the norm
     keeps what it normalised in 8 bits for its backward pass. embed(tokens) looks
-    tokens up in W, for a model whose embedding and head are one weight."""
+    tokens up in W, for a model whose embedding and head are one weight. verify(...)
+    checks drafted tokens against the answers' distribution."""
 
     def __init__(self, weight: torch.Tensor, norm_weight: Optional[torch.Tensor] = None,
                  norm_bias: Optional[torch.Tensor] = None, *, eps: float = 1e-5, rms: bool = True, softcap: float = 0.0,
@@ -448,3 +449,12 @@ class LanguageModelHead(torch.nn.Module):
         as in flce_sample. The logits are rounded to hidden's dtype in between; for
         32 bits of them take flce_sample(self.logits(hidden, torch.float32), u, ...)."""
         return flce_sample(self.logits(hidden, residual=residual), u, **settings)
+
+    @torch.no_grad()
+    def verify(self, hidden: torch.Tensor, draft_tokens: torch.Tensor, u: torch.Tensor, draft_logits: Optional[torch.Tensor] = None,
+               residual: Optional[torch.Tensor] = None, **settings):
+        """(tokens, accepted, logprobs) for hidden [..., K + 1, H] (plus residual) at the places of K
+        drafted tokens [..., K] and the one behind them; draft_logits [..., K, V] in hidden's dtype, u
+        [..., K + 1] and settings as in flce_verify."""
+        from . import _model
+        return _model.flce_verify(self.logits(hidden, residual=residual), draft_tokens, u, draft_logits, **settings)

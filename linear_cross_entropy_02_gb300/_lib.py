@@ -64,11 +64,12 @@ HEAD_EXPORTED = [
 
 # include/flce_model.h
 FLCE_MODEL_KERNEL_FIRST = 48
-FLCE_MODEL_KERNEL_COUNT = 7
+FLCE_MODEL_KERNEL_COUNT = 9
 
 MODEL_EXPORTED = [
     "flce_checkpoint_store", "flce_checkpoint_load", "flce_add_layer_norm", "flce_add_layer_norm_workspace_size",
-    "flce_add_layer_norm_backward", "flce_embedding", "flce_embedding_workspace_size", "flce_embedding_backward",
+    "flce_add_layer_norm_backward", "flce_embedding", "flce_embedding_workspace_size", "flce_embedding_backward", "flce_verify",
+    "flce_verify_workspace_size",
 ]
 
 
@@ -204,7 +205,10 @@ def _bind_model(L: ctypes.CDLL) -> None:
                                                  _vp, _sz, _vp]),
             ("flce_embedding", i, [_vp, l, _vp, i, l, l, l, f, _vp, i, _vp]),
             ("flce_embedding_workspace_size", _sz, [l, l]),
-            ("flce_embedding_backward", i, [_vp, i, l, _vp, l, l, l, f, _vp, i, _vp, _sz, _vp])):
+            ("flce_embedding_backward", i, [_vp, i, l, _vp, l, l, l, f, _vp, i, _vp, _sz, _vp]),
+            ("flce_verify_workspace_size", _sz, [l, l]),
+            ("flce_verify", i, [_vp, i, l, l, l, l, l, _vp, _vp, l, l, _vp, _vp, f, _vp, ctypes.c_int32, _vp, f, _vp, f, _vp, _vp, _vp,
+                                _vp, _sz, _vp])):
         fn = getattr(L, name)
         fn.restype, fn.argtypes = res, args
 

@@ -1,6 +1,6 @@
 """The operators at a model's two ends: embeddings in the head's weight, the residual's
-addition with the norm behind it, and 8-bit checkpoints of what that norm keeps for its
-backward pass (include/flce_model.h).
+addition with the norm behind it, 8-bit checkpoints of what that norm keeps for its
+backward pass, and the verification of drafted tokens (include/flce_model.h).
 
 As in the rest of the binding, nothing is computed here: arguments are checked,
 leading row dimensions are flattened, outputs and workspaces are torch's (a call's own),
@@ -14,7 +14,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _lib
-from ._head import _DTYPES, _call, _cuda, _floats, _norm_weights, _ptr, _rows
+from ._head import _DTYPES, _call, _cuda, _floats, _norm_weights, _ptr, _rows, _setting
 
 
 def _same(name: str, t, x: torch.Tensor, of: str = "x") -> None:
@@ -308,3 +308,61 @@ class _Embedding(torch.autograd.Function):
 def embedding(tokens, W, *, scale: float = 1.0):
     """Differentiable flce_embedding in W's dtype; the gradient flows to W, once."""
     return _Embedding.apply(tokens, W, float(scale))
+
+
+# ---------------------------------------------------------------- verification
+def _logits3(name: str, t: torch.Tensor, rows: int):
+    """t as [requests, rows, V] with unit stride in the last dimension; a copy only if it does not lie so."""
+    V = t.shape[-1]
+    t = t.reshape(t.numel() // max(1, rows * V) if t.numel() else 0, rows, V) if t.dim() != 3 else t
+    return t if V == 1 or t.stride(2) == 1 else t.contiguous()
+
+
+def flce_verify(target_logits: torch.Tensor, draft_tokens: torch.Tensor, u: torch.Tensor, draft_logits: Optional[torch.Tensor] = None, *,
+                temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, return_logprobs: bool = True):
+    """Verifies K drafted tokens [..., K] (int64) of each request against the target's logits
+    [..., K + 1, V] (bf16 or fp32) at their places and the one behind them, from given random
+    numbers u [..., K + 1] (fp32, uniform in [0, 1)). The drafts were drawn by flce_sample from
+    draft_logits [..., K, V] (the target's dtype) under the same settings; None: they were not drawn
+    but found, and have no distribution. temperature, top_k, top_p and min_p are as in flce_sample, a
+    tensor with one value per request. Drafts are accepted while u_i q(d_i) < p(d_i); one token more is
+    drawn, from max(p - q, 0) at the first that is not, else from p, so that tokens are
+    distributed as the target's own. A draft outside of [0, V) stands for none, so requests may
+    have fewer than K. Returns (tokens int64 [..., K + 1], accepted int64 [...], logprobs fp32
+    [..., K + 1]): the accepted drafts and the token behind them, -1 after it, and log p of each
+    (None without return_logprobs). A request that comes to a row without a distribution ends with token -1
+    and a NaN log-probability there."""
+    code = _floats("target_logits", target_logits)
+    index = target_logits.get_device()
+    _cuda("draft_tokens", draft_tokens)
+    if draft_tokens.dtype != torch.int64 or draft_tokens.dim() == 0 or draft_tokens.get_device() != index:
+        raise ValueError("draft_tokens must be an int64 tensor [..., K] on the logits' device")
+    lead, K = draft_tokens.shape[:-1], draft_tokens.shape[-1]
+    if target_logits.dim() < 2 or target_logits.shape[:-1] != (*lead, K + 1) or target_logits.shape[-1] == 0:
+        raise ValueError("target_logits must be [..., K + 1, V] for draft_tokens [..., K]")
+    V = target_logits.shape[-1]
+    _cuda("u", u)
+    if u.dtype != torch.float32 or u.shape != (*lead, K + 1) or u.get_device() != index or not u.is_contiguous():
+        raise ValueError("u must be a contiguous fp32 tensor [..., K + 1] on the logits' device")
+    if draft_logits is not None:
+        _cuda("draft_logits", draft_logits)
+        if draft_logits.shape != (*lead, K, V) or draft_logits.dtype != target_logits.dtype or draft_logits.get_device() != index:
+            raise ValueError("draft_logits must be [..., K, V] in the target's dtype, on its device")
+    x = _logits3("target_logits", target_logits, K + 1)
+    q = None if draft_logits is None or K == 0 else _logits3("draft_logits", draft_logits, K)
+    d = draft_tokens.contiguous()
+    B = x.shape[0]
+    tp, t = _setting("temperature", temperature, torch.float32, lead, index)
+    kp, k = _setting("top_k", top_k, torch.int32, lead, index)
+    k = max(0, min(int(k), V))  # (the entry's is 32 bits wide; both ends keep all)
+    pp, p = _setting("top_p", top_p, torch.float32, lead, index)
+    mp, m = _setting("min_p", min_p, torch.float32, lead, index)
+    tokens = torch.empty((*lead, K + 1), dtype=torch.int64, device=u.device)
+    accepted = torch.empty(lead, dtype=torch.int64, device=u.device)
+    logprobs = torch.empty_like(u) if return_logprobs else None
+    nbytes = _lib.lib().flce_verify_workspace_size(B, K)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=u.device)
+    _call(index, "flce_verify", x.data_ptr(), code, B, K, V, x.stride(1), x.stride(0), d.data_ptr(), _ptr(q),
+          0 if q is None else q.stride(1), 0 if q is None else q.stride(0), u.data_ptr(), tp, t, kp, k, pp, p, mp, m, tokens.data_ptr(),
+          accepted.data_ptr(), _ptr(logprobs), ws.data_ptr(), nbytes)
+    return tokens, accepted, logprobs

@@ -94,7 +94,7 @@ const char* const kHeadKernelNames[FLCE_HEAD_KERNEL_COUNT] = {
 // Those of the operators at a model's two ends, from FLCE_MODEL_KERNEL_FIRST on.
 const char* const kModelKernelNames[FLCE_MODEL_KERNEL_COUNT] = {
     "add_layer_norm", "add_layer_norm_backward", "checkpoint_store", "checkpoint_load", "embedding", "embedding_sort",
-    "embedding_grad"};
+    "embedding_grad", "verify_cut", "verify"};
 
 }  // namespace
 

@@ -96,6 +96,15 @@ bool mx_gemm_encodes(int64_t rows, int64_t cols);
 int launch_mx_gemm(const MxGemmParams& p, int sms, cudaStream_t s);
 
 // ------------------------------------------------------------ sampling
+// What the filters keep of a row of logits: those up to `last` in rank order (list
+// entries: complemented order key, index) whose exponential is at least min_p.
+struct RowCut {
+  uint64_t last;
+  uint64_t whole;   // sum of the kept weights
+  float top, inv;   // largest logit, 1 / temperature
+  float min_p;
+  uint32_t bad;     // no distribution: the rest says nothing
+};
 struct SampleParams {
   const void* x;
   int dtype;
@@ -109,6 +118,13 @@ struct SampleParams {
   int32_t top_k;
   int64_t* tokens;
   float* logprobs;
+  // verification (model_internal.h): rows of the target [batch][drafts + 1], then of the
+  // draft [batch][drafts], and what is kept of each
+  const void* draft;
+  const int64_t* draft_tokens;
+  int64_t target_rows, drafts;
+  int64_t batch_ld, draft_ld, draft_batch_ld;
+  RowCut* cuts;
 };
 cudaError_t launch_sample(const SampleParams& p, int sms, cudaStream_t s);
 

@@ -15,6 +15,7 @@ namespace {
 
 constexpr int64_t kMaxHidden = int64_t{1} << 24;
 constexpr int64_t kMaxRows = (int64_t{1} << 31) - 1;
+constexpr int64_t kMostDrafts = 1024;
 constexpr int64_t kBlock = 32;  // elements of a checkpoint that share a scale
 
 inline size_t round256(size_t n) { return (n + 255) / 256 * 256; }
@@ -64,6 +65,12 @@ struct EmbeddingSpace {
 EmbeddingSpace embedding_space(int64_t rows, int64_t hidden) {
   const size_t tiles = static_cast<size_t>((rows + kEmbeddingTile - 1) / kEmbeddingTile);
   return {round256(sizeof(uint32_t) * static_cast<size_t>(rows)), round256(sizeof(float) * tiles * static_cast<size_t>(hidden))};
+}
+
+// Rows that a verification looks at, 0 if there are too many.
+int64_t verify_rows(int64_t batch, int64_t drafts, bool with_draft) {
+  if (batch < 0 || drafts < 0 || drafts > kMostDrafts || batch > kMaxRows / 8 / (2 * drafts + 1)) return -1;
+  return batch * (with_draft ? 2 * drafts + 1 : drafts + 1);
 }
 
 }  // namespace
@@ -308,6 +315,73 @@ int flce_embedding_backward(const void* grad_out, int dtype, int64_t ld_grad, co
     if (sorted != FLCE_OK) return sorted;
   }
   return launch_embedding_grad(p, stream);
+}
+
+size_t flce_verify_workspace_size(int64_t batch, int64_t drafts) {
+  const int64_t rows = verify_rows(batch, drafts, true);
+  return rows < 0 ? 0 : sizeof(RowCut) * static_cast<size_t>(rows);
+}
+
+int flce_verify(const void* target, int logits_dtype, int64_t batch, int64_t drafts, int64_t vocab, int64_t ld_target,
+                int64_t batch_ld_target, const int64_t* draft_tokens, const void* draft, int64_t ld_draft, int64_t batch_ld_draft,
+                const float* u, const float* temperatures, float temperature, const int32_t* top_ks, int32_t top_k,
+                const float* top_ps, float top_p, const float* min_ps, float min_p, int64_t* tokens, int64_t* accepted,
+                float* logprobs, void* workspace, size_t workspace_bytes, void* stream_handle) {
+  if (drafts == 0) draft = nullptr;
+  const int64_t rows = verify_rows(batch, drafts, draft != nullptr);
+  if (!dtype_ok(logits_dtype) || rows < 0 || vocab <= 0 || vocab >= (int64_t{1} << 22) || ld_target < 0 || batch_ld_target < 0 ||
+      (draft && (ld_draft < 0 || batch_ld_draft < 0)))
+    return FLCE_ERR_ARG;
+  if ((!temperatures && std::isnan(temperature)) || (!top_ps && std::isnan(top_p)) || (!min_ps && std::isnan(min_p)))
+    return FLCE_ERR_ARG;
+  if (batch == 0) return FLCE_OK;
+  if (!target || !u || !tokens || !accepted || !workspace || (drafts > 0 && !draft_tokens)) return FLCE_ERR_ARG;
+  const size_t es = element_size(logits_dtype);
+  if (!aligned(target, es) || !aligned(draft, es) || !aligned(u, 4) || !aligned(draft_tokens, 8) || !aligned(temperatures, 4) ||
+      !aligned(top_ks, 4) || !aligned(top_ps, 4) || !aligned(min_ps, 4) || !aligned(tokens, 8) || !aligned(accepted, 8) ||
+      !aligned(logprobs, 4) || !aligned(workspace, 16))
+    return FLCE_ERR_ALIGN;
+  const size_t space = sizeof(RowCut) * static_cast<size_t>(rows);
+  if (workspace_bytes < space) return FLCE_ERR_WORKSPACE;
+  const size_t b = static_cast<size_t>(batch), places = b * (static_cast<size_t>(drafts) + 1);
+  const Span in[] = {{target, ((b - 1) * batch_ld_target + drafts * ld_target + vocab) * es},
+                     {draft, draft ? ((b - 1) * batch_ld_draft + (drafts - 1) * ld_draft + vocab) * es : 0},
+                     {u, places * 4}, {draft_tokens, b * drafts * 8}, {temperatures, b * 4}, {top_ks, b * 4}, {top_ps, b * 4},
+                     {min_ps, b * 4}};
+  const Span out[] = {{tokens, places * 8}, {accepted, b * 8}, {logprobs, places * 4}, {workspace, space}};
+  if (!outputs_apart(out, in)) return FLCE_ERR_ARG;
+  int sms = 0;
+  const int rc = device_check(&sms);
+  if (rc != FLCE_OK) return rc;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_handle);
+  SampleParams p = {};
+  p.x = target;
+  p.dtype = logits_dtype;
+  p.rows = rows;
+  p.vocab = vocab;
+  p.ld = ld_target;
+  p.batch_ld = batch_ld_target;
+  p.u = u;
+  p.temperatures = temperatures;
+  p.temperature = temperature;
+  p.top_ks = top_ks;
+  p.top_k = top_k;
+  p.top_ps = top_ps;
+  p.top_p = top_p;
+  p.min_ps = min_ps;
+  p.min_p = min_p;
+  p.tokens = tokens;
+  p.logprobs = logprobs;
+  p.draft = draft;
+  p.draft_ld = ld_draft;
+  p.draft_batch_ld = batch_ld_draft;
+  p.draft_tokens = draft_tokens;
+  p.drafts = drafts;
+  p.target_rows = batch * (drafts + 1);
+  p.cuts = static_cast<RowCut*>(workspace);
+  FLCE_LAUNCH(K_VERIFY_CUT, launch_verify_cuts(p, sms, stream));
+  FLCE_LAUNCH(K_VERIFY, launch_verify(p, batch, accepted, sms, stream));
+  return FLCE_OK;
 }
 
 }  // extern "C"

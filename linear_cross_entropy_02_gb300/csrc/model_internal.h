@@ -18,6 +18,8 @@ enum ModelKernelId {
   K_EMBEDDING,
   K_EMBEDDING_SORT,
   K_EMBEDDING_GRAD,
+  K_VERIFY_CUT,
+  K_VERIFY,
 };
 
 // ------------------------------------------------------------ residual and norm
@@ -61,5 +63,12 @@ cudaError_t launch_embedding(const EmbeddingParams& p, cudaStream_t s);
 // Sorts the tokens into p->sorted and p->places, which it may swap with the other side.
 int launch_embedding_sort(EmbeddingParams* p, cudaStream_t stream);
 int launch_embedding_grad(const EmbeddingParams& p, cudaStream_t stream);
+
+// ------------------------------------------------------------ verification
+// SampleParams with its last members; u [batch][drafts + 1], tokens and logprobs
+// [batch][drafts + 1]; p.rows: all rows, of the target and of the draft (if it has any).
+// launch_verify_cuts fills p.cuts, launch_verify reads it.
+cudaError_t launch_verify_cuts(const SampleParams& p, int sms, cudaStream_t s);
+cudaError_t launch_verify(const SampleParams& p, int64_t batch, int64_t* accepted, int sms, cudaStream_t s);
 
 }  // namespace flce

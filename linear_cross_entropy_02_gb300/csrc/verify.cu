@@ -1,0 +1,298 @@
+// Verification of drafted tokens against the target's distribution, from given random
+// numbers: draft i is accepted while u_i q(d_i) < p(d_i), and one token more is drawn,
+// from what p has above q at the first draft that is not accepted, from p itself if all
+// were. That way the tokens are distributed as if the target had drawn them itself.
+//
+// Two kernels. The first finds what the filters keep of every row, and the kept weights'
+// sum, with the kernels of sampling (sample_device.cuh), so that p and q are exactly the
+// distributions that flce_sample draws from. The second takes a request: it compares the
+// drafts, and goes over one row of the target and one of the draft to draw the last token.
+// That row's weights are whole multiples of 2^-40, as in sampling: sums do not depend on
+// the order or on how many CTAs share a row. Few requests are spread over clusters.
+#include "model_internal.h"
+#include "sample_device.cuh"
+
+namespace flce {
+
+namespace {
+
+constexpr int kVerifyThreads = 1024;
+constexpr int kVerifyWarps = kVerifyThreads / 32;
+
+// What became of a request's drafts.
+enum Stop { kRejected, kNoDraft, kBad };
+
+struct VerifyShared {
+  uint64_t seg_weight[kSegments];
+  uint64_t totals[kMaxCluster];  // of the CTAs' slices
+  uint64_t goal;
+  int count;
+  int stop;
+};
+
+// A row's distribution: whole weights of its logits.
+struct Kept {
+  RowCut c;
+  uint32_t last_key;  // the last kept logit's order key, complemented; ties are cut by index
+  __device__ __forceinline__ Kept(const RowCut& cut) : c(cut), last_key(static_cast<uint32_t>(cut.last >> 32)) {}
+  __device__ __forceinline__ Halves weight(float x, uint32_t index) const {
+    const uint32_t k = ~order_key(x);
+    const bool keep = k < last_key || (k == last_key && index <= static_cast<uint32_t>(c.last));
+    const float e = expf(__fmul_rn(x - c.top, c.inv));
+    if (!keep || !(e >= c.min_p)) return {0u, 0u};
+    return halves(e);
+  }
+  // the weight as a number (it has at most 24 bits) over the sum
+  __device__ __forceinline__ float share(Halves w, float over) const {
+    return __fmul_rn(fmaf(__uint2float_rn(w.hi), 1048576.f, __uint2float_rn(w.lo)), over);
+  }
+  __device__ __forceinline__ float over() const { return __double2float_rn(__drcp_rn(__ll2double_rn(static_cast<int64_t>(c.whole)))); }
+  __device__ __forceinline__ double probability(Halves w) const {
+    return __ddiv_rn(__ll2double_rn((static_cast<int64_t>(w.hi) << 20) + w.lo), __ll2double_rn(static_cast<int64_t>(c.whole)));
+  }
+  __device__ __forceinline__ float logprob(float x) const {
+    return __fmul_rn(x - c.top, c.inv) - logf(__ll2float_rn(static_cast<int64_t>(c.whole)) * (1.f / kFixed));
+  }
+};
+
+template <typename T, bool MULTI>
+__global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const SampleParams p, int64_t* accepted, const int slice) {
+  __shared__ VerifyShared s;
+  constexpr int E = 16 / sizeof(T);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t rank = 0, ctas = 1;
+  if constexpr (MULTI) {
+    rank = cluster_ctarank();
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
+    asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");  // all are running before the first write into another
+  }
+  const int64_t b = blockIdx.x / ctas, K = p.drafts;
+  const T* target = static_cast<const T*>(p.x) + b * p.batch_ld;
+  const T* draft = p.draft ? static_cast<const T*>(p.draft) + b * p.draft_batch_ld : nullptr;
+  const int64_t* drafts = p.draft_tokens + b * K;
+  const float* u = p.u + b * (K + 1);
+  const RowCut* cuts = p.cuts + b * (K + 1);
+  const RowCut* draft_cuts = p.cuts + p.target_rows + b * K;
+  int64_t* tokens = p.tokens + b * (K + 1);
+  float* logprobs = p.logprobs ? p.logprobs + b * (K + 1) : nullptr;
+
+  // ---- the drafts, a lane each
+  if (warp == 0) {
+    int count = 0, stop = kNoDraft;
+    for (int64_t base = 0; base < K; base += 32) {
+      const int64_t i = base + lane;
+      int mine = -1;  // accepted
+      if (i < K) {
+        const int64_t d = drafts[i];
+        bool ended = false;  // an earlier lane has no draft: this row was not looked at
+        for (int64_t j = base; j < i; ++j) ended |= !(drafts[j] >= 0 && drafts[j] < p.vocab);
+        if (ended || d < 0 || d >= p.vocab) {
+          mine = kNoDraft;
+        } else {
+          const Kept t(cuts[i]);
+          const float v = u[i];
+          if (t.c.bad || v != v) {
+            mine = kBad;
+          } else {
+            const float x = to_float<T>(target[i * p.ld + d]);
+            double q = 1.0;
+            if (draft) {
+              const Kept g(draft_cuts[i]);
+              if (g.c.bad)
+                mine = kBad;
+              else
+                q = g.probability(g.weight(to_float<T>(draft[i * p.draft_ld + d]), static_cast<uint32_t>(d)));
+            }
+            if (mine < 0 && !(__dmul_rn(static_cast<double>(v), q) < t.probability(t.weight(x, static_cast<uint32_t>(d))))) mine = kRejected;
+            if (mine < 0 && rank == 0 && logprobs) logprobs[i] = t.logprob(x);
+          }
+        }
+      }
+      const uint32_t stopped = __ballot_sync(0xffffffffu, mine >= 0);
+      if (stopped) {
+        const int first = __ffs(stopped) - 1;
+        stop = __shfl_sync(0xffffffffu, mine, first);
+        count += first;
+        break;
+      }
+      count += static_cast<int>(K - base < 32 ? K - base : 32);
+    }
+    if (lane == 0) {
+      s.count = count;
+      s.stop = stop;
+    }
+  }
+  __syncthreads();
+  const int n = s.count;
+  int stop = s.stop;
+  const float v = u[K];
+  if (stop != kBad && (cuts[n].bad || v != v)) stop = kBad;
+  if (rank == 0) {
+    for (int64_t i = threadIdx.x; i <= K; i += kVerifyThreads) {
+      if (i == n && stop != kBad) continue;  // the drawn token's place
+      tokens[i] = i < n ? drafts[i] : -1;
+      if (logprobs && i >= n) logprobs[i] = i > n ? 0.f : __uint_as_float(0x7FC00000u);
+    }
+    if (threadIdx.x == 0) accepted[b] = n;
+  }
+  if (stop == kBad) {
+    if constexpr (MULTI) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+    return;
+  }
+
+  // ---- the token behind them
+  const Kept kept(cuts[n]);
+  const T* row = target + n * p.ld;
+  const T* other = stop == kRejected && draft ? draft + n * p.draft_ld : nullptr;
+  const Kept drafted(other ? draft_cuts[n] : cuts[n]);
+  const uint32_t rejected = stop == kRejected ? static_cast<uint32_t>(drafts[n]) : 0u;
+  const float over = kept.over(), other_over = drafted.over();
+  const int vocab = static_cast<int>(p.vocab), c0 = static_cast<int>(rank) * slice, size = max(0, min(slice, vocab - c0));
+  const int vecs = (size + E - 1) / E;
+  const bool aligned = reinterpret_cast<uintptr_t>(row) % 16 == 0 && (!other || reinterpret_cast<uintptr_t>(other) % 16 == 0);
+  bool rest = stop == kRejected;  // draw from max(p - q, 0)
+  auto read = [&](const T* from, int vec, float (&x)[E]) {
+    if (aligned && (vec + 1) * E <= size) {
+      unpack<T, E>(load_raw<T, E>(from + c0 + vec * E), x);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[e] = vec * E + e < size ? to_float<T>(from[c0 + vec * E + e]) : -INFINITY;
+    }
+  };
+  auto weights = [&](int vec, Halves (&w)[E]) {
+    float x[E], y[E];
+    read(row, vec, x);
+    if (rest && other) read(other, vec, y);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const uint32_t index = static_cast<uint32_t>(c0 + vec * E + e);
+      w[e] = kept.weight(x[e], index);
+      if (rest) {
+        const float q = other ? drafted.share(drafted.weight(y[e], index), other_over) : index == rejected ? 1.f : 0.f;
+        w[e] = halves(fminf(fmaxf(__fsub_rn(kept.share(w[e], over), q), 0.f), 1.f));
+      }
+    }
+  };
+  const int per = Row<T, kVerifyThreads>::segment_vecs(vecs), segs = (vecs + per - 1) / per;
+  if constexpr (MULTI) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+  uint64_t total, before;
+  while (true) {
+    for (int i = threadIdx.x; i < kSegments; i += kVerifyThreads)
+      if (i >= segs) s.seg_weight[i] = 0;
+    for (int seg = warp; seg < segs; seg += kVerifyWarps) {
+      Sum acc;
+      const int v1 = min((seg + 1) * per, vecs);
+      for (int vec = seg * per + lane; vec < v1; vec += 32) {
+        Halves w[E];
+        weights(vec, w);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc.add(w[e]);
+      }
+      const uint64_t sum = acc.total();
+      if (lane == 0) s.seg_weight[seg] = sum;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      uint64_t sum = 0;
+      for (int i = lane; i < kSegments; i += 32) sum += s.seg_weight[i];
+      sum = warp_total(sum);
+      if (lane < static_cast<int>(ctas)) {
+        if constexpr (MULTI)
+          asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(mapa_shared(smem_u32(&s.totals[rank]), lane)), "l"(sum) : "memory");
+        else
+          s.totals[0] = sum;
+      }
+    }
+    row_barrier<MULTI>();
+    total = before = 0;
+    for (uint32_t c = 0; c < ctas; ++c) {
+      if (c < rank) before += s.totals[c];
+      total += s.totals[c];
+    }
+    if (total > 0 || !rest) break;
+    // p nowhere above q, as far as whole multiples of 2^-40 show it: from p itself
+    rest = false;
+    row_barrier<MULTI>();  // the totals have been read by all
+  }
+  // ---- the first token whose running sum is above u times the whole
+  if (warp != 0) return;
+  if (lane == 0) s.goal = answer_goal(v, total);
+  __syncwarp();
+  const uint64_t goal = s.goal;
+  if (goal < before || goal >= before + s.totals[rank]) return;
+  int found = 0;
+  for (int base = 0; base < kSegments; base += 32) {
+    const uint64_t w = s.seg_weight[base + lane], inc = warp_inclusive(w);
+    const uint32_t hit = __ballot_sync(0xffffffffu, before + inc > goal);
+    if (hit) {
+      const int at = __ffs(hit) - 1;
+      found = base + at;
+      before += __shfl_sync(0xffffffffu, inc - w, at);
+      break;
+    }
+    before += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  const int v1 = min((found + 1) * per, vecs);
+  for (int base = found * per; base < v1; base += 32) {
+    const int vec = base + lane;
+    Halves w[E];
+    uint64_t sum = 0;
+    if (vec < v1) {
+      weights(vec, w);
+#pragma unroll
+      for (int e = 0; e < E; ++e) sum += (static_cast<uint64_t>(w[e].hi) << 20) + w[e].lo;
+    }
+    const uint64_t inc = warp_inclusive(sum);
+    uint64_t run = before + inc - sum;
+    if (run <= goal && goal < run + sum) {
+      float x[E];
+      read(row, vec, x);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const uint64_t we = (static_cast<uint64_t>(w[e].hi) << 20) + w[e].lo;
+        if (run <= goal && goal < run + we) {
+          tokens[n] = c0 + vec * E + e;
+          if (logprobs) logprobs[n] = kept.logprob(x[e]);
+        }
+        run += we;
+      }
+    }
+    if (__any_sync(0xffffffffu, goal < before + __shfl_sync(0xffffffffu, inc, 31))) break;
+    before += __shfl_sync(0xffffffffu, inc, 31);
+  }
+}
+
+template <typename T, bool MULTI>
+cudaError_t run_verify(const SampleParams& p, int64_t batch, int64_t* accepted, int ctas, cudaStream_t s) {
+  const int slice = static_cast<int>(((p.vocab + ctas - 1) / ctas + 63) / 64 * 64);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(batch * ctas));
+  cfg.blockDim = dim3(kVerifyThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(ctas);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, verify_kernel<T, MULTI>, p, accepted, slice);
+}
+
+template <typename T>
+cudaError_t run_verify_typed(const SampleParams& p, int64_t batch, int64_t* accepted, int sms, cudaStream_t s) {
+  int ctas = 1;
+  while (ctas < kMaxCluster && batch * ctas * 2 <= sms && p.vocab / ctas > 4096) ctas *= 2;
+  return ctas > 1 ? run_verify<T, true>(p, batch, accepted, ctas, s) : run_verify<T, false>(p, batch, accepted, 1, s);
+}
+
+}  // namespace
+
+cudaError_t launch_verify_cuts(const SampleParams& p, int sms, cudaStream_t s) {
+  return p.dtype == FLCE_DTYPE_F32 ? run_typed<float, true>(p, sms, s) : run_typed<uint16_t, true>(p, sms, s);
+}
+
+cudaError_t launch_verify(const SampleParams& p, int64_t batch, int64_t* accepted, int sms, cudaStream_t s) {
+  return p.dtype == FLCE_DTYPE_F32 ? run_verify_typed<float>(p, batch, accepted, sms, s) : run_verify_typed<uint16_t>(p, batch, accepted, sms, s);
+}
+
+}  // namespace flce
