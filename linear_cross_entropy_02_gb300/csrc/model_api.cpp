@@ -177,7 +177,7 @@ int flce_add_layer_norm(const void* x, int64_t ld_x, const void* residual, int64
 size_t flce_add_layer_norm_workspace_size(int64_t rows, int64_t hidden) {
   int sms = 0;
   if (!shape_ok(rows, hidden) || device_check(&sms) != FLCE_OK) return 0;
-  const int64_t parts = norm_partial_rows(rows, hidden, sms);
+  const int64_t parts = add_norm_partial_rows(rows, hidden, sms);
   return 2 * round256(sizeof(float) * static_cast<size_t>(parts > 0 ? parts : 1) * hidden);
 }
 
@@ -208,7 +208,7 @@ int flce_add_layer_norm_backward(const void* grad_y, int64_t ld_grad_y, const vo
   const int rc = device_check(&sms);
   if (rc != FLCE_OK) return rc;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_handle);
-  const size_t half = round256(sizeof(float) * static_cast<size_t>(rows > 0 ? norm_partial_rows(rows, hidden, sms) : 1) * hidden);
+  const size_t half = round256(sizeof(float) * static_cast<size_t>(rows > 0 ? add_norm_partial_rows(rows, hidden, sms) : 1) * hidden);
   if (sums && workspace_bytes < 2 * half) return FLCE_ERR_WORKSPACE;
   NormParams p = {};
   p.x = x;

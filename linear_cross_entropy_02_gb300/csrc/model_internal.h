@@ -24,6 +24,8 @@ enum ModelKernelId {
 
 // ------------------------------------------------------------ residual and norm
 // (NormParams' last members; K_NORM_WGRAD joins the partial sums)
+// Most partial rows that the backward passes write for a call on this device.
+int add_norm_partial_rows(int64_t rows, int64_t hidden, int sms);
 cudaError_t launch_add_norm(const NormParams& p, int sms, cudaStream_t s);
 cudaError_t launch_add_norm_bwd(const NormParams& p, int sms, int* partials, cudaStream_t s);
 cudaError_t launch_add_norm_bwd_8bit(const NormParams& p, int sms, int* partials, cudaStream_t s);

@@ -1199,6 +1199,24 @@ __device__ bool segment_answer(const Row<T, kThreads>& row, Shared& s, const Sam
   return true;
 }
 
+// Verification: row r's first logit and the request whose settings it has; rows of the
+// target come first, then those of the draft. False if it lies behind the request's last draft.
+template <typename T>
+__device__ __forceinline__ bool verify_row(const SampleParams& p, int64_t r, const T** start, int64_t* request) {
+  const bool target = r < p.target_rows;
+  const int64_t at = target ? r : r - p.target_rows;
+  const int per = static_cast<int>(p.drafts) + (target ? 1 : 0), place = static_cast<int>(at % per);
+  *request = at / per;
+  *start = target ? static_cast<const T*>(p.x) + *request * p.batch_ld + place * p.ld
+                  : static_cast<const T*>(p.draft) + *request * p.draft_batch_ld + place * p.draft_ld;
+  bool used = true;
+  for (int i = 0; i < place + (target ? 0 : 1); ++i) {
+    const int64_t token = __ldg(p.draft_tokens + *request * p.drafts + i);
+    used = used && token >= 0 && token < p.vocab;
+  }
+  return used;
+}
+
 // ---------------------------------------------------------------- the kernel
 // CUTS: no token is drawn; what the filters keep of each row goes to p.cuts.
 template <typename T, int kThreads, bool MULTI, bool CUTS>
@@ -1222,19 +1240,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
   int64_t setting = r;
   const T* start = static_cast<const T*>(p.x) + r * p.ld;
   if constexpr (CUTS) {
-    // rows of the target, then those of the draft; a request's rows share its settings
-    const bool target = r < p.target_rows;
-    const int64_t at = target ? r : r - p.target_rows;
-    const int per = static_cast<int>(p.drafts) + (target ? 1 : 0), place = static_cast<int>(at % per);
-    setting = at / per;
-    start = target ? static_cast<const T*>(p.x) + setting * p.batch_ld + place * p.ld
-                   : static_cast<const T*>(p.draft) + setting * p.draft_batch_ld + place * p.draft_ld;
+    const bool used = verify_row(p, r, &start, &setting);
     // rows behind a request's last draft are not looked at
-    bool used = true;
-    for (int i = 0; i < place + (target ? 0 : 1); ++i) {
-      const int64_t token = __ldg(p.draft_tokens + setting * p.drafts + i);
-      used = used && token >= 0 && token < p.vocab;
-    }
     if (!used) {
       if constexpr (MULTI) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
       return;

@@ -55,6 +55,151 @@ struct Kept {
   }
 };
 
+// ---------------------------------------------------------------- rows without filters
+// Their kept set is the row, so only its maximum and the sum of its weights are wanted:
+// one pass, with the slice of the row in registers between the two. A cluster per row, of
+// as many CTAs as its registers need, two of them on an SM so that one loads while the
+// other adds up. (64 requests of 5 drafts on 129280 bf16, 704 rows: 61 us, 130 with sampling's kernel.)
+constexpr int kPlainThreads = 512, kPlainVecs = 8, kPlainWarps = kPlainThreads / 32;
+
+__device__ __forceinline__ uint32_t max_nan(uint32_t a, uint32_t b, const uint16_t*) {  // bf16 pairs
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_nan(uint32_t a, uint32_t b, const float*) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)));
+  return __float_as_uint(r);
+}
+
+struct PlainShared {
+  uint32_t tops[kMaxCluster];
+  unsigned long long totals[kMaxCluster];
+  uint32_t keys[kPlainWarps];
+  unsigned long long sums[kPlainWarps];
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kPlainThreads, 2) verify_plain_kernel(const SampleParams p, const int slice) {
+  __shared__ PlainShared s;
+  constexpr int E = 16 / sizeof(T);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  uint32_t ctas;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
+  asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");  // all are running before the first write into another
+  const int64_t r = blockIdx.x / ctas;
+  const T* start;
+  int64_t request;
+  if (!verify_row(p, r, &start, &request)) {
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+    return;
+  }
+  const int vocab = static_cast<int>(p.vocab), c0 = static_cast<int>(rank) * slice, size = max(0, min(slice, vocab - c0));
+  start += c0;
+  const bool aligned = reinterpret_cast<uintptr_t>(start) % 16 == 0;
+  Raw<T, E> raw[kPlainVecs];
+#pragma unroll
+  for (int j = 0; j < kPlainVecs; ++j) {
+    const int v = static_cast<int>(threadIdx.x) + j * kPlainThreads;
+    if (aligned && (v + 1) * E <= size) {
+      raw[j] = load_raw<T, E>(start + v * E);
+    } else {
+      float x[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[e] = v * E + e < size ? to_float<T>(start[v * E + e]) : -INFINITY;
+      raw[j] = pack<T, E>(x);
+    }
+  }
+  // the largest logit, NaN if there is one
+  uint32_t most = raw[0].u.x;
+#pragma unroll
+  for (int j = 0; j < kPlainVecs; ++j) {
+    const uint32_t w[4] = {raw[j].u.x, raw[j].u.y, raw[j].u.z, raw[j].u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) most = max_nan(most, w[i], static_cast<const T*>(nullptr));
+  }
+  float top = __uint_as_float(most);
+  if constexpr (sizeof(T) == 2) top = __uint_as_float(max_nan(most << 16, most & 0xFFFF0000u, static_cast<const float*>(nullptr)));
+  // (a NaN, made positive, ranks above infinity)
+  uint32_t key = __reduce_max_sync(0xffffffffu, top != top ? 0xFFFFFFFFu : order_key(top));
+  if (lane == 0) s.keys[warp] = key;
+  __syncthreads();
+  key = __reduce_max_sync(0xffffffffu, s.keys[lane % kPlainWarps]);
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+  if (threadIdx.x < ctas) remote_store(&s.tops[rank], threadIdx.x, key);
+  row_barrier<true>();
+  for (uint32_t c = 0; c < ctas; ++c) key = max(key, s.tops[c]);
+  top = key_value(key);
+  const bool bad = !(fabsf(top) < INFINITY);
+  const float inv = fmaxf(1.f / p.temperature, kLeast);
+  // Weights in halves, as halves() takes them; what it subtracts from each comes off the sums at the end.
+  uint32_t hi = 0, lo = 0;
+#pragma unroll
+  for (int j = 0; j < kPlainVecs; ++j) {
+    float x[E];
+    unpack<T, E>(raw[j], x);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float w = expf(__fmul_rn(x[e] - top, inv));
+      const float a = __fmaf_rz(w, 1048576.f, 8388608.f);
+      const float b = __fmaf_rz(__fmaf_rn(w, 1048576.f, 8388608.f - a), 1048576.f, 8388608.f);
+      hi += __float_as_uint(a);
+      lo += __float_as_uint(b);
+    }
+  }
+  constexpr uint32_t kLess = static_cast<uint32_t>(uint64_t{0x4B000000} * (kPlainVecs * E));
+  Sum sum;
+  sum.hi = hi - kLess;
+  sum.lo = lo - kLess;
+  const uint64_t mine = sum.total();
+  if (lane == 0) s.sums[warp] = mine;
+  __syncthreads();
+  if (warp == 0) {
+    const uint64_t all = warp_total(lane < kPlainWarps ? s.sums[lane] : 0);
+    if (lane == 0)
+      asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(mapa_shared(smem_u32(&s.totals[rank]), 0)), "l"(all) : "memory");
+  }
+  row_barrier<true>();
+  if (rank == 0 && threadIdx.x == 0) {
+    uint64_t whole = 0;
+    for (uint32_t c = 0; c < ctas; ++c) whole += s.totals[c];
+    p.cuts[r] = {~0ull, whole, top, inv, 0.f, bad ? 1u : 0u};
+  }
+}
+
+template <typename T>
+constexpr int64_t kPlainSlice = int64_t{kPlainThreads} * kPlainVecs * (16 / static_cast<int>(sizeof(T)));
+
+// Whether no row has a filter, as far as the host knows, and a cluster's registers hold one.
+template <typename T>
+bool plain_rows(const SampleParams& p) {
+  if (p.temperatures || p.top_ks || p.top_ps || p.min_ps) return false;
+  if (!(p.temperature > 0.f) || 1.f / p.temperature > 3e38f || p.top_p < 1.f || p.min_p > 0.f) return false;
+  return (p.top_k <= 0 || p.top_k >= p.vocab) && p.vocab <= kMaxCluster * kPlainSlice<T>;
+}
+
+template <typename T>
+cudaError_t run_plain(const SampleParams& p, int sms, cudaStream_t s) {
+  // few rows are spread further, down to 4096 logits per CTA
+  int ctas = 1;
+  while (ctas * kPlainSlice<T> < p.vocab || (ctas < kMaxCluster && p.rows * ctas * 2 <= 2LL * sms && p.vocab / ctas > 4096)) ctas *= 2;
+  const int slice = static_cast<int>(((p.vocab + ctas - 1) / ctas + 63) / 64 * 64);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.rows * ctas));
+  cfg.blockDim = dim3(kPlainThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(ctas);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, verify_plain_kernel<T>, p, slice);
+}
+
+// ---------------------------------------------------------------- a request
 template <typename T, bool MULTI>
 __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const SampleParams p, int64_t* accepted, const int slice) {
   __shared__ VerifyShared s;
@@ -288,7 +433,8 @@ cudaError_t run_verify_typed(const SampleParams& p, int64_t batch, int64_t* acce
 }  // namespace
 
 cudaError_t launch_verify_cuts(const SampleParams& p, int sms, cudaStream_t s) {
-  return p.dtype == FLCE_DTYPE_F32 ? run_typed<float, true>(p, sms, s) : run_typed<uint16_t, true>(p, sms, s);
+  if (p.dtype == FLCE_DTYPE_F32) return plain_rows<float>(p) ? run_plain<float>(p, sms, s) : run_typed<float, true>(p, sms, s);
+  return plain_rows<uint16_t>(p) ? run_plain<uint16_t>(p, sms, s) : run_typed<uint16_t, true>(p, sms, s);
 }
 
 cudaError_t launch_verify(const SampleParams& p, int64_t batch, int64_t* accepted, int sms, cudaStream_t s) {
