@@ -311,7 +311,7 @@ int flce_embedding_backward(const void* grad_out, int dtype, int64_t ld_grad, co
     p.places2 = reinterpret_cast<uint32_t*>(ws + 3 * space.keys);
     p.head = reinterpret_cast<float*>(ws + 4 * space.keys);
     p.tail = reinterpret_cast<float*>(ws + 4 * space.keys + space.sums);
-    const int sorted = launch_embedding_sort(&p, stream);
+    const int sorted = launch_embedding_sort(&p, sms, stream);
     if (sorted != FLCE_OK) return sorted;
   }
   return launch_embedding_grad(p, stream);

@@ -63,7 +63,7 @@ struct EmbeddingParams {
 constexpr int kEmbeddingTile = 32;
 cudaError_t launch_embedding(const EmbeddingParams& p, cudaStream_t s);
 // Sorts the tokens into p->sorted and p->places, which it may swap with the other side.
-int launch_embedding_sort(EmbeddingParams* p, cudaStream_t stream);
+int launch_embedding_sort(EmbeddingParams* p, int sms, cudaStream_t stream);
 int launch_embedding_grad(const EmbeddingParams& p, cudaStream_t stream);
 
 // ------------------------------------------------------------ verification

@@ -16,7 +16,7 @@ namespace flce {
 
 namespace {
 
-constexpr int kVerifyThreads = 1024;
+constexpr int kVerifyThreads = 512;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 
 // What became of a request's drafts.
@@ -28,23 +28,65 @@ struct VerifyShared {
   uint64_t goal;
   int count;
   int stop;
+  float over[2];  // 1 / sum of the weights, of the target's row and the draft's
 };
+
+__device__ __forceinline__ uint64_t f2_fma_rz(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rz.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// Two logits at a time: packed arithmetic rounds each half as the single instruction does.
+struct Pairs {
+  uint64_t minus_top, inv;
+  __device__ __forceinline__ Pairs(float top, float inverse) : minus_top(f2_pack(-top, -top)), inv(f2_pack(inverse, inverse)) {}
+  __device__ __forceinline__ uint64_t exponentials(float x0, float x1) const {
+    float t0, t1;
+    f2_unpack(f2_mul(f2_add(f2_pack(x0, x1), minus_top), inv), t0, t1);
+    return f2_pack(expf(t0), expf(t1));
+  }
+  // halves() of two exponentials, 2^23 above each half: a for the upper ones, b for the lower.
+  __device__ __forceinline__ static void split(uint64_t e, uint64_t& a, uint64_t& b) {
+    const uint64_t scale = f2_pack(1048576.f, 1048576.f), large = f2_pack(8388608.f, 8388608.f), minus = f2_pack(-1.f, -1.f);
+    a = f2_fma_rz(e, scale, large);
+    b = f2_fma_rz(f2_fma(e, scale, f2_fma(a, minus, large)), scale, large);
+  }
+  // the whole weights as numbers over the sum
+  __device__ __forceinline__ static uint64_t shares(uint64_t e, uint64_t over) {
+    uint64_t a, b;
+    split(e, a, b);
+    const uint64_t less = f2_pack(-8388608.f, -8388608.f);
+    return f2_mul(f2_fma(f2_add(a, less), f2_pack(1048576.f, 1048576.f), f2_add(b, less)), over);
+  }
+};
+constexpr uint32_t kLarge = 0x4B000000u;  // bits of 2^23
 
 // A row's distribution: whole weights of its logits.
 struct Kept {
   RowCut c;
   uint32_t last_key;  // the last kept logit's order key, complemented; ties are cut by index
-  __device__ __forceinline__ Kept(const RowCut& cut) : c(cut), last_key(static_cast<uint32_t>(cut.last >> 32)) {}
-  __device__ __forceinline__ Halves weight(float x, uint32_t index) const {
+  float least;        // no logit below it is kept
+  bool all;           // all are
+  __device__ __forceinline__ Kept(const RowCut& cut) : c(cut), last_key(static_cast<uint32_t>(cut.last >> 32)) {
+    all = c.last == ~0ull && !(c.min_p > 0.f);
+    least = c.last == ~0ull ? -INFINITY : key_value(~last_key);
+  }
+  // The exponential, 0 for what is not kept.
+  __device__ __forceinline__ float exponential(float x, uint32_t index) const {
+    const float e = expf(__fmul_rn(x - c.top, c.inv));
+    if (all) return e;
     const uint32_t k = ~order_key(x);
     const bool keep = k < last_key || (k == last_key && index <= static_cast<uint32_t>(c.last));
-    const float e = expf(__fmul_rn(x - c.top, c.inv));
-    if (!keep || !(e >= c.min_p)) return {0u, 0u};
-    return halves(e);
+    return keep && e >= c.min_p ? e : 0.f;
   }
-  // the weight as a number (it has at most 24 bits) over the sum
-  __device__ __forceinline__ float share(Halves w, float over) const {
-    return __fmul_rn(fmaf(__uint2float_rn(w.hi), 1048576.f, __uint2float_rn(w.lo)), over);
+  __device__ __forceinline__ Halves weight(float x, uint32_t index) const { return halves(exponential(x, index)); }
+  // The whole weight, as a number (it has at most 24 bits), over the sum.
+  __device__ __forceinline__ float share(float x, uint32_t index, float over) const {
+    const float e = exponential(x, index);
+    const float a = __fmaf_rz(e, 1048576.f, 8388608.f);
+    const float b = __fmaf_rz(__fmaf_rn(e, 1048576.f, 8388608.f - a), 1048576.f, 8388608.f);
+    return __fmul_rn(fmaf(a - 8388608.f, 1048576.f, b - 8388608.f), over);
   }
   __device__ __forceinline__ float over() const { return __double2float_rn(__drcp_rn(__ll2double_rn(static_cast<int64_t>(c.whole)))); }
   __device__ __forceinline__ double probability(Halves w) const {
@@ -58,9 +100,10 @@ struct Kept {
 // ---------------------------------------------------------------- rows without filters
 // Their kept set is the row, so only its maximum and the sum of its weights are wanted:
 // one pass, with the slice of the row in registers between the two. A cluster per row, of
-// as many CTAs as its registers need, two of them on an SM so that one loads while the
-// other adds up. (64 requests of 5 drafts on 129280 bf16, 704 rows: 61 us, 130 with sampling's kernel.)
-constexpr int kPlainThreads = 512, kPlainVecs = 8, kPlainWarps = kPlainThreads / 32;
+// as many CTAs as its registers need, several of them on an SM so that one loads while the
+// others add up. 64 requests of 5 drafts on 129280 bf16, 704 rows, take 74 us (2.5 TB/s), some 115 with
+// sampling's kernel: 19 instructions a logit, half of them the exponential, fill 62% of the issue slots.
+constexpr int kPlainVecs = 8, kPlainWarps = 16;  // (of the larger CTAs)
 
 __device__ __forceinline__ uint32_t max_nan(uint32_t a, uint32_t b, const uint16_t*) {  // bf16 pairs
   uint32_t r;
@@ -80,8 +123,8 @@ struct PlainShared {
   unsigned long long sums[kPlainWarps];
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kPlainThreads, 2) verify_plain_kernel(const SampleParams p, const int slice) {
+template <typename T, int kPlainThreads>
+__global__ void __launch_bounds__(kPlainThreads, 1024 / kPlainThreads) verify_plain_kernel(const SampleParams p, const int slice) {
   __shared__ PlainShared s;
   constexpr int E = 16 / sizeof(T);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -126,7 +169,7 @@ __global__ void __launch_bounds__(kPlainThreads, 2) verify_plain_kernel(const Sa
   uint32_t key = __reduce_max_sync(0xffffffffu, top != top ? 0xFFFFFFFFu : order_key(top));
   if (lane == 0) s.keys[warp] = key;
   __syncthreads();
-  key = __reduce_max_sync(0xffffffffu, s.keys[lane % kPlainWarps]);
+  key = __reduce_max_sync(0xffffffffu, s.keys[lane % (kPlainThreads / 32)]);
   asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
   if (threadIdx.x < ctas) remote_store(&s.tops[rank], threadIdx.x, key);
   row_barrier<true>();
@@ -136,20 +179,20 @@ __global__ void __launch_bounds__(kPlainThreads, 2) verify_plain_kernel(const Sa
   const float inv = fmaxf(1.f / p.temperature, kLeast);
   // Weights in halves, as halves() takes them; what it subtracts from each comes off the sums at the end.
   uint32_t hi = 0, lo = 0;
+  const Pairs pairs(top, inv);
 #pragma unroll
   for (int j = 0; j < kPlainVecs; ++j) {
     float x[E];
     unpack<T, E>(raw[j], x);
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float w = expf(__fmul_rn(x[e] - top, inv));
-      const float a = __fmaf_rz(w, 1048576.f, 8388608.f);
-      const float b = __fmaf_rz(__fmaf_rn(w, 1048576.f, 8388608.f - a), 1048576.f, 8388608.f);
-      hi += __float_as_uint(a);
-      lo += __float_as_uint(b);
+    for (int e = 0; e < E; e += 2) {
+      uint64_t a, b;
+      Pairs::split(pairs.exponentials(x[e], x[e + 1]), a, b);
+      hi += static_cast<uint32_t>(a) + static_cast<uint32_t>(a >> 32);
+      lo += static_cast<uint32_t>(b) + static_cast<uint32_t>(b >> 32);
     }
   }
-  constexpr uint32_t kLess = static_cast<uint32_t>(uint64_t{0x4B000000} * (kPlainVecs * E));
+  constexpr uint32_t kLess = static_cast<uint32_t>(uint64_t{kLarge} * (kPlainVecs * E));
   Sum sum;
   sum.hi = hi - kLess;
   sum.lo = lo - kLess;
@@ -157,7 +200,7 @@ __global__ void __launch_bounds__(kPlainThreads, 2) verify_plain_kernel(const Sa
   if (lane == 0) s.sums[warp] = mine;
   __syncthreads();
   if (warp == 0) {
-    const uint64_t all = warp_total(lane < kPlainWarps ? s.sums[lane] : 0);
+    const uint64_t all = warp_total(lane < kPlainThreads / 32 ? s.sums[lane] : 0);
     if (lane == 0)
       asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(mapa_shared(smem_u32(&s.totals[rank]), 0)), "l"(all) : "memory");
   }
@@ -169,22 +212,27 @@ __global__ void __launch_bounds__(kPlainThreads, 2) verify_plain_kernel(const Sa
   }
 }
 
+// Logits that a CTA's registers hold.
 template <typename T>
-constexpr int64_t kPlainSlice = int64_t{kPlainThreads} * kPlainVecs * (16 / static_cast<int>(sizeof(T)));
+constexpr int64_t plain_slice(int threads) {
+  return int64_t{threads} * kPlainVecs * (16 / static_cast<int64_t>(sizeof(T)));
+}
 
 // Whether no row has a filter, as far as the host knows, and a cluster's registers hold one.
 template <typename T>
 bool plain_rows(const SampleParams& p) {
   if (p.temperatures || p.top_ks || p.top_ps || p.min_ps) return false;
   if (!(p.temperature > 0.f) || 1.f / p.temperature > 3e38f || p.top_p < 1.f || p.min_p > 0.f) return false;
-  return (p.top_k <= 0 || p.top_k >= p.vocab) && p.vocab <= kMaxCluster * kPlainSlice<T>;
+  return (p.top_k <= 0 || p.top_k >= p.vocab) && p.vocab <= kMaxCluster * plain_slice<T>(512);
 }
 
-template <typename T>
+template <typename T, int kPlainThreads>
 cudaError_t run_plain(const SampleParams& p, int sms, cudaStream_t s) {
   // few rows are spread further, down to 4096 logits per CTA
   int ctas = 1;
-  while (ctas * kPlainSlice<T> < p.vocab || (ctas < kMaxCluster && p.rows * ctas * 2 <= 2LL * sms && p.vocab / ctas > 4096)) ctas *= 2;
+  while (ctas * plain_slice<T>(kPlainThreads) < p.vocab ||
+         (ctas < kMaxCluster && p.rows * ctas * 2 <= 1024LL / kPlainThreads * sms && p.vocab / ctas > 4096))
+    ctas *= 2;
   const int slice = static_cast<int>(((p.vocab + ctas - 1) / ctas + 63) / 64 * 64);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.rows * ctas));
@@ -196,12 +244,18 @@ cudaError_t run_plain(const SampleParams& p, int sms, cudaStream_t s) {
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, verify_plain_kernel<T>, p, slice);
+  return cudaLaunchKernelEx(&cfg, verify_plain_kernel<T, kPlainThreads>, p, slice);
+}
+
+// Smaller CTAs, four on an SM, where eight of them hold a row: 704 rows of 129280 bf16 74 us, 78 with the larger ones.
+template <typename T>
+cudaError_t run_plain_typed(const SampleParams& p, int sms, cudaStream_t s) {
+  return p.vocab <= kMaxCluster * plain_slice<T>(256) ? run_plain<T, 256>(p, sms, s) : run_plain<T, 512>(p, sms, s);
 }
 
 // ---------------------------------------------------------------- a request
 template <typename T, bool MULTI>
-__global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const SampleParams p, int64_t* accepted, const int slice) {
+__global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const SampleParams p, int64_t* accepted, const int slice) {
   __shared__ VerifyShared s;
   constexpr int E = 16 / sizeof(T);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -227,11 +281,11 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const SamplePara
     for (int64_t base = 0; base < K; base += 32) {
       const int64_t i = base + lane;
       int mine = -1;  // accepted
+      const uint32_t none = __ballot_sync(0xffffffffu, i < K && !(drafts[i] >= 0 && drafts[i] < p.vocab));
       if (i < K) {
         const int64_t d = drafts[i];
-        bool ended = false;  // an earlier lane has no draft: this row was not looked at
-        for (int64_t j = base; j < i; ++j) ended |= !(drafts[j] >= 0 && drafts[j] < p.vocab);
-        if (ended || d < 0 || d >= p.vocab) {
+        // (an earlier lane without a draft: this row was not looked at)
+        if (none & ((2u << lane) - 1u)) {
           mine = kNoDraft;
         } else {
           const Kept t(cuts[i]);
@@ -262,6 +316,11 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const SamplePara
       }
       count += static_cast<int>(K - base < 32 ? K - base : 32);
     }
+    // (double precision in two lanes: 1024 threads would queue for it, 13 us)
+    if (lane < 2) {
+      const bool compared = stop == kRejected && draft;
+      s.over[lane] = Kept(lane == 0 || !compared ? cuts[count] : draft_cuts[count]).over();
+    }
     if (lane == 0) {
       s.count = count;
       s.stop = stop;
@@ -291,11 +350,13 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const SamplePara
   const T* other = stop == kRejected && draft ? draft + n * p.draft_ld : nullptr;
   const Kept drafted(other ? draft_cuts[n] : cuts[n]);
   const uint32_t rejected = stop == kRejected ? static_cast<uint32_t>(drafts[n]) : 0u;
-  const float over = kept.over(), other_over = drafted.over();
+  const float over = s.over[0], other_over = s.over[1];
   const int vocab = static_cast<int>(p.vocab), c0 = static_cast<int>(rank) * slice, size = max(0, min(slice, vocab - c0));
   const int vecs = (size + E - 1) / E;
   const bool aligned = reinterpret_cast<uintptr_t>(row) % 16 == 0 && (!other || reinterpret_cast<uintptr_t>(other) % 16 == 0);
   bool rest = stop == kRejected;  // draw from max(p - q, 0)
+  const bool whole_rows = kept.all && drafted.all;  // nothing is cut
+  const Pairs kept_pairs(kept.c.top, kept.c.inv), other_pairs(drafted.c.top, drafted.c.inv);
   auto read = [&](const T* from, int vec, float (&x)[E]) {
     if (aligned && (vec + 1) * E <= size) {
       unpack<T, E>(load_raw<T, E>(from + c0 + vec * E), x);
@@ -304,18 +365,48 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const SamplePara
       for (int e = 0; e < E; ++e) x[e] = vec * E + e < size ? to_float<T>(from[c0 + vec * E + e]) : -INFINITY;
     }
   };
+  // (most of a filtered row's vectors hold nothing that is kept)
   auto weights = [&](int vec, Halves (&w)[E]) {
     float x[E], y[E];
     read(row, vec, x);
-    if (rest && other) read(other, vec, y);
+    float most = x[0];
+#pragma unroll
+    for (int e = 1; e < E; ++e) most = fmaxf(most, x[e]);
+    if (most < kept.least) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) w[e] = {0u, 0u};
+      return;
+    }
+    const uint32_t first = static_cast<uint32_t>(c0 + vec * E);
+    if (whole_rows) {
+      if (other) read(other, vec, y);
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        uint64_t v = kept_pairs.exponentials(x[e], x[e + 1]), a, b;
+        if (rest) {
+          v = Pairs::shares(v, f2_pack(over, over));
+          const uint64_t q = other ? Pairs::shares(other_pairs.exponentials(y[e], y[e + 1]), f2_pack(other_over, other_over))
+                                   : f2_pack(first + e == rejected ? 1.f : 0.f, first + e + 1 == rejected ? 1.f : 0.f);
+          float r0, r1;
+          f2_unpack(f2_fma(q, f2_pack(-1.f, -1.f), v), r0, r1);  // (one rounding: of the difference)
+          v = f2_pack(__saturatef(r0), __saturatef(r1));
+        }
+        Pairs::split(v, a, b);
+        w[e] = {static_cast<uint32_t>(a) - kLarge, static_cast<uint32_t>(b) - kLarge};
+        w[e + 1] = {static_cast<uint32_t>(a >> 32) - kLarge, static_cast<uint32_t>(b >> 32) - kLarge};
+      }
+      return;
+    }
+    if (!rest) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) w[e] = kept.weight(x[e], first + e);
+      return;
+    }
+    if (other) read(other, vec, y);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const uint32_t index = static_cast<uint32_t>(c0 + vec * E + e);
-      w[e] = kept.weight(x[e], index);
-      if (rest) {
-        const float q = other ? drafted.share(drafted.weight(y[e], index), other_over) : index == rejected ? 1.f : 0.f;
-        w[e] = halves(fminf(fmaxf(__fsub_rn(kept.share(w[e], over), q), 0.f), 1.f));
-      }
+      const float q = other ? drafted.share(y[e], first + e, other_over) : first + e == rejected ? 1.f : 0.f;
+      w[e] = halves(__saturatef(__fsub_rn(kept.share(x[e], first + e, over), q)));
     }
   };
   const int per = Row<T, kVerifyThreads>::segment_vecs(vecs), segs = (vecs + per - 1) / per;
@@ -426,15 +517,15 @@ cudaError_t run_verify(const SampleParams& p, int64_t batch, int64_t* accepted, 
 template <typename T>
 cudaError_t run_verify_typed(const SampleParams& p, int64_t batch, int64_t* accepted, int sms, cudaStream_t s) {
   int ctas = 1;
-  while (ctas < kMaxCluster && batch * ctas * 2 <= sms && p.vocab / ctas > 4096) ctas *= 2;
+  while (ctas < kMaxCluster && batch * ctas * 2 <= 2LL * sms && p.vocab / ctas > 4096) ctas *= 2;
   return ctas > 1 ? run_verify<T, true>(p, batch, accepted, ctas, s) : run_verify<T, false>(p, batch, accepted, 1, s);
 }
 
 }  // namespace
 
 cudaError_t launch_verify_cuts(const SampleParams& p, int sms, cudaStream_t s) {
-  if (p.dtype == FLCE_DTYPE_F32) return plain_rows<float>(p) ? run_plain<float>(p, sms, s) : run_typed<float, true>(p, sms, s);
-  return plain_rows<uint16_t>(p) ? run_plain<uint16_t>(p, sms, s) : run_typed<uint16_t, true>(p, sms, s);
+  if (p.dtype == FLCE_DTYPE_F32) return plain_rows<float>(p) ? run_plain_typed<float>(p, sms, s) : run_typed<float, true>(p, sms, s);
+  return plain_rows<uint16_t>(p) ? run_plain_typed<uint16_t>(p, sms, s) : run_typed<uint16_t, true>(p, sms, s);
 }
 
 cudaError_t launch_verify(const SampleParams& p, int64_t batch, int64_t* accepted, int sms, cudaStream_t s) {
