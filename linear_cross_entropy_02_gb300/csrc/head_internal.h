@@ -100,10 +100,10 @@ int launch_mx_gemm(const MxGemmParams& p, int sms, cudaStream_t s);
 // entries: complemented order key, index) whose exponential is at least min_p.
 struct RowCut {
   uint64_t last;
-  uint64_t whole;   // sum of the kept weights
+  uint64_t whole;   // sum of the kept weights; 0: no distribution, the rest says nothing
   float top, inv;   // largest logit, 1 / temperature
   float min_p;
-  uint32_t bad;     // no distribution: the rest says nothing
+  float over;       // 1 / whole, rounded to 64 bits and then to 32
 };
 struct SampleParams {
   const void* x;

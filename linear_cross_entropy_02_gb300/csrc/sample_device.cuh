@@ -438,11 +438,15 @@ __device__ void clear(Hist& h) {
   __syncthreads();
 }
 
+__device__ __forceinline__ float reciprocal(uint64_t whole) {
+  return __double2float_rn(__drcp_rn(__ll2double_rn(static_cast<int64_t>(whole))));
+}
+
 // The row's kept set (CUTS), by one thread: all logits up to `last` in rank order, of at
 // least min_p.
 template <typename T, int kThreads>
 __device__ __forceinline__ void write_cut(const Row<T, kThreads>& row, const SampleParams& p, int64_t r, uint64_t last, uint64_t whole) {
-  p.cuts[r] = {last, whole, row.top, row.inv, row.min_p, 0u};
+  p.cuts[r] = {last, whole, row.top, row.inv, row.min_p, reciprocal(whole)};
 }
 
 template <typename T, int kThreads>
@@ -777,7 +781,7 @@ __device__ void general_answer(const Row<T, kThreads>& row, Shared& s, const Sam
       cut.top = row.top;
       cut.inv = row.inv;
       cut.min_p = row.min_p;
-      cut.bad = 0;
+      cut.over = reciprocal(total);
       if (ties == 0) cut.last = key == 0 ? ~0ull : (static_cast<uint64_t>(~key) << 32) - 1;
     }
     if (ties > 0 && my_tie_before < ties && ties <= my_tie_before + equal) {
@@ -1387,7 +1391,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
     }
     if constexpr (CUTS) {
       // the one token that is kept, with a weight of 1
-      if (row.rank == 0 && threadIdx.x == 0) p.cuts[r] = {bad ? 0 : list_entry(row.top, at), uint64_t{1} << 40, row.top, 1.f, 0.f, bad ? 1u : 0u};
+      if (row.rank == 0 && threadIdx.x == 0) p.cuts[r] = {bad ? 0 : list_entry(row.top, at), bad ? 0 : uint64_t{1} << 40, row.top, 1.f, 0.f, 1.f / kFixed};
       return;
     }
     if (row.rank == 0 && threadIdx.x == 0) {

@@ -28,7 +28,6 @@ struct VerifyShared {
   uint64_t goal;
   int count;
   int stop;
-  float over[2];  // 1 / sum of the weights, of the target's row and the draft's
 };
 
 __device__ __forceinline__ uint64_t f2_fma_rz(uint64_t a, uint64_t b, uint64_t c) {
@@ -82,14 +81,14 @@ struct Kept {
   }
   __device__ __forceinline__ Halves weight(float x, uint32_t index) const { return halves(exponential(x, index)); }
   // The whole weight, as a number (it has at most 24 bits), over the sum.
-  __device__ __forceinline__ float share(float x, uint32_t index, float over) const {
+  __device__ __forceinline__ float share(float x, uint32_t index) const {
     const float e = exponential(x, index);
     const float a = __fmaf_rz(e, 1048576.f, 8388608.f);
     const float b = __fmaf_rz(__fmaf_rn(e, 1048576.f, 8388608.f - a), 1048576.f, 8388608.f);
-    return __fmul_rn(fmaf(a - 8388608.f, 1048576.f, b - 8388608.f), over);
+    return __fmul_rn(fmaf(a - 8388608.f, 1048576.f, b - 8388608.f), c.over);
   }
-  __device__ __forceinline__ float over() const { return __double2float_rn(__drcp_rn(__ll2double_rn(static_cast<int64_t>(c.whole)))); }
-  __device__ __forceinline__ double probability(Halves w) const {
+  __device__ __forceinline__ double probability(float x, uint32_t index) const {
+    const Halves w = weight(x, index);
     return __ddiv_rn(__ll2double_rn((static_cast<int64_t>(w.hi) << 20) + w.lo), __ll2double_rn(static_cast<int64_t>(c.whole)));
   }
   __device__ __forceinline__ float logprob(float x) const {
@@ -208,7 +207,7 @@ __global__ void __launch_bounds__(kPlainThreads, 1024 / kPlainThreads) verify_pl
   if (rank == 0 && threadIdx.x == 0) {
     uint64_t whole = 0;
     for (uint32_t c = 0; c < ctas; ++c) whole += s.totals[c];
-    p.cuts[r] = {~0ull, whole, top, inv, 0.f, bad ? 1u : 0u};
+    p.cuts[r] = {~0ull, bad ? 0 : whole, top, inv, 0.f, bad ? 0.f : reciprocal(whole)};
   }
 }
 
@@ -290,19 +289,27 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const SampleP
         } else {
           const Kept t(cuts[i]);
           const float v = u[i];
-          if (t.c.bad || v != v) {
+          if (t.c.whole == 0 || v != v) {
             mine = kBad;
           } else {
-            const float x = to_float<T>(target[i * p.ld + d]);
-            double q = 1.0;
+            const uint32_t at = static_cast<uint32_t>(d);
+            const float x = to_float<T>(target[i * p.ld + d]), p32 = t.share(x, at);
+            float y = 0.f, q32 = 1.f;
             if (draft) {
               const Kept g(draft_cuts[i]);
-              if (g.c.bad)
-                mine = kBad;
-              else
-                q = g.probability(g.weight(to_float<T>(draft[i * p.draft_ld + d]), static_cast<uint32_t>(d)));
+              y = to_float<T>(draft[i * p.draft_ld + d]);
+              q32 = g.share(y, at);
+              if (g.c.whole == 0) mine = kBad;
             }
-            if (mine < 0 && !(__dmul_rn(static_cast<double>(v), q) < t.probability(t.weight(x, static_cast<uint32_t>(d))))) mine = kRejected;
+            if (mine < 0) {
+              // p and q in 32 bits are within 2^-22 of theirs: only where u q comes near p does it take
+              // double precision, which this chip has little of (two divisions are some microseconds)
+              const float uq = v * q32;
+              bool less = uq < p32;
+              if (fabsf(uq - p32) <= 0x1p-20f * p32)
+                less = __dmul_rn(static_cast<double>(v), draft ? Kept(draft_cuts[i]).probability(y, at) : 1.0) < t.probability(x, at);
+              if (!less) mine = kRejected;
+            }
             if (mine < 0 && rank == 0 && logprobs) logprobs[i] = t.logprob(x);
           }
         }
@@ -316,11 +323,6 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const SampleP
       }
       count += static_cast<int>(K - base < 32 ? K - base : 32);
     }
-    // (double precision in two lanes: 1024 threads would queue for it, 13 us)
-    if (lane < 2) {
-      const bool compared = stop == kRejected && draft;
-      s.over[lane] = Kept(lane == 0 || !compared ? cuts[count] : draft_cuts[count]).over();
-    }
     if (lane == 0) {
       s.count = count;
       s.stop = stop;
@@ -330,7 +332,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const SampleP
   const int n = s.count;
   int stop = s.stop;
   const float v = u[K];
-  if (stop != kBad && (cuts[n].bad || v != v)) stop = kBad;
+  if (stop != kBad && (cuts[n].whole == 0 || v != v)) stop = kBad;
   if (rank == 0) {
     for (int64_t i = threadIdx.x; i <= K; i += kVerifyThreads) {
       if (i == n && stop != kBad) continue;  // the drawn token's place
@@ -350,12 +352,12 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const SampleP
   const T* other = stop == kRejected && draft ? draft + n * p.draft_ld : nullptr;
   const Kept drafted(other ? draft_cuts[n] : cuts[n]);
   const uint32_t rejected = stop == kRejected ? static_cast<uint32_t>(drafts[n]) : 0u;
-  const float over = s.over[0], other_over = s.over[1];
   const int vocab = static_cast<int>(p.vocab), c0 = static_cast<int>(rank) * slice, size = max(0, min(slice, vocab - c0));
   const int vecs = (size + E - 1) / E;
   const bool aligned = reinterpret_cast<uintptr_t>(row) % 16 == 0 && (!other || reinterpret_cast<uintptr_t>(other) % 16 == 0);
   bool rest = stop == kRejected;  // draw from max(p - q, 0)
   const bool whole_rows = kept.all && drafted.all;  // nothing is cut
+  const uint64_t share = f2_pack(kept.c.over, kept.c.over), other_share = f2_pack(drafted.c.over, drafted.c.over);
   const Pairs kept_pairs(kept.c.top, kept.c.inv), other_pairs(drafted.c.top, drafted.c.inv);
   auto read = [&](const T* from, int vec, float (&x)[E]) {
     if (aligned && (vec + 1) * E <= size) {
@@ -384,8 +386,8 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const SampleP
       for (int e = 0; e < E; e += 2) {
         uint64_t v = kept_pairs.exponentials(x[e], x[e + 1]), a, b;
         if (rest) {
-          v = Pairs::shares(v, f2_pack(over, over));
-          const uint64_t q = other ? Pairs::shares(other_pairs.exponentials(y[e], y[e + 1]), f2_pack(other_over, other_over))
+          v = Pairs::shares(v, share);
+          const uint64_t q = other ? Pairs::shares(other_pairs.exponentials(y[e], y[e + 1]), other_share)
                                    : f2_pack(first + e == rejected ? 1.f : 0.f, first + e + 1 == rejected ? 1.f : 0.f);
           float r0, r1;
           f2_unpack(f2_fma(q, f2_pack(-1.f, -1.f), v), r0, r1);  // (one rounding: of the difference)
@@ -405,8 +407,8 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const SampleP
     if (other) read(other, vec, y);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const float q = other ? drafted.share(y[e], first + e, other_over) : first + e == rejected ? 1.f : 0.f;
-      w[e] = halves(__saturatef(__fsub_rn(kept.share(x[e], first + e, over), q)));
+      const float q = other ? drafted.share(y[e], first + e) : first + e == rejected ? 1.f : 0.f;
+      w[e] = halves(__saturatef(__fsub_rn(kept.share(x[e], first + e), q)));
     }
   };
   const int per = Row<T, kVerifyThreads>::segment_vecs(vecs), segs = (vecs + per - 1) / per;
