@@ -125,6 +125,7 @@ struct SampleParams {
   int64_t target_rows, drafts;
   int64_t batch_ld, draft_ld, draft_batch_ld;
   RowCut* cuts;
+  uint32_t* progress;  // [batch][drafts + 1]
 };
 cudaError_t launch_sample(const SampleParams& p, int sms, cudaStream_t s);
 

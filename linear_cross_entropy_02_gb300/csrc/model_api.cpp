@@ -67,7 +67,7 @@ EmbeddingSpace embedding_space(int64_t rows, int64_t hidden) {
   return {round256(sizeof(uint32_t) * static_cast<size_t>(rows)), round256(sizeof(float) * tiles * static_cast<size_t>(hidden))};
 }
 
-// Rows that a verification looks at, 0 if there are too many.
+// Rows that a verification looks at, -1 if there are too many.
 int64_t verify_rows(int64_t batch, int64_t drafts, bool with_draft) {
   if (batch < 0 || drafts < 0 || drafts > kMostDrafts || batch > kMaxRows / 8 / (2 * drafts + 1)) return -1;
   return batch * (with_draft ? 2 * drafts + 1 : drafts + 1);
@@ -319,7 +319,7 @@ int flce_embedding_backward(const void* grad_out, int dtype, int64_t ld_grad, co
 
 size_t flce_verify_workspace_size(int64_t batch, int64_t drafts) {
   const int64_t rows = verify_rows(batch, drafts, true);
-  return rows < 0 ? 0 : sizeof(RowCut) * static_cast<size_t>(rows);
+  return rows < 0 ? 0 : (sizeof(RowCut) + sizeof(uint32_t)) * static_cast<size_t>(rows);
 }
 
 int flce_verify(const void* target, int logits_dtype, int64_t batch, int64_t drafts, int64_t vocab, int64_t ld_target,
@@ -341,7 +341,8 @@ int flce_verify(const void* target, int logits_dtype, int64_t batch, int64_t dra
       !aligned(top_ks, 4) || !aligned(top_ps, 4) || !aligned(min_ps, 4) || !aligned(tokens, 8) || !aligned(accepted, 8) ||
       !aligned(logprobs, 4) || !aligned(workspace, 16))
     return FLCE_ERR_ALIGN;
-  const size_t space = sizeof(RowCut) * static_cast<size_t>(rows);
+  // (as many words as rows of the target follow the cuts)
+  const size_t space = (sizeof(RowCut) + sizeof(uint32_t)) * static_cast<size_t>(rows);
   if (workspace_bytes < space) return FLCE_ERR_WORKSPACE;
   const size_t b = static_cast<size_t>(batch), places = b * (static_cast<size_t>(drafts) + 1);
   const Span in[] = {{target, ((b - 1) * batch_ld_target + drafts * ld_target + vocab) * es},
@@ -379,6 +380,7 @@ int flce_verify(const void* target, int logits_dtype, int64_t batch, int64_t dra
   p.drafts = drafts;
   p.target_rows = batch * (drafts + 1);
   p.cuts = static_cast<RowCut*>(workspace);
+  p.progress = reinterpret_cast<uint32_t*>(p.cuts + rows);
   FLCE_LAUNCH(K_VERIFY_CUT, launch_verify_cuts(p, sms, stream));
   FLCE_LAUNCH(K_VERIFY, launch_verify(p, batch, accepted, sms, stream));
   return FLCE_OK;

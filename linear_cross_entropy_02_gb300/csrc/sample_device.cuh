@@ -1203,14 +1203,16 @@ __device__ bool segment_answer(const Row<T, kThreads>& row, Shared& s, const Sam
   return true;
 }
 
-// Verification: row r's first logit and the request whose settings it has; rows of the
+// Verification: row r's first logit, its request, whose settings it has, and its place; rows of the
 // target come first, then those of the draft. False if it lies behind the request's last draft.
 template <typename T>
-__device__ __forceinline__ bool verify_row(const SampleParams& p, int64_t r, const T** start, int64_t* request) {
-  const bool target = r < p.target_rows;
-  const int64_t at = target ? r : r - p.target_rows;
-  const int per = static_cast<int>(p.drafts) + (target ? 1 : 0), place = static_cast<int>(at % per);
+__device__ __forceinline__ bool verify_row(const SampleParams& p, uint32_t r, const T** start, int64_t* request, int* at_place) {
+  const uint32_t target_rows = static_cast<uint32_t>(p.target_rows);
+  const bool target = r < target_rows;
+  const uint32_t at = target ? r : r - target_rows, per = static_cast<uint32_t>(p.drafts) + (target ? 1 : 0);
+  const int place = static_cast<int>(at % per);
   *request = at / per;
+  *at_place = place;
   *start = target ? static_cast<const T*>(p.x) + *request * p.batch_ld + place * p.ld
                   : static_cast<const T*>(p.draft) + *request * p.draft_batch_ld + place * p.draft_ld;
   bool used = true;
@@ -1244,7 +1246,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
   int64_t setting = r;
   const T* start = static_cast<const T*>(p.x) + r * p.ld;
   if constexpr (CUTS) {
-    const bool used = verify_row(p, r, &start, &setting);
+    int place;
+    const bool used = verify_row(p, static_cast<uint32_t>(r), &start, &setting, &place);
     // rows behind a request's last draft are not looked at
     if (!used) {
       if constexpr (MULTI) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");

@@ -20,7 +20,7 @@ constexpr int kVerifyThreads = 512;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 
 // What became of a request's drafts.
-enum Stop { kRejected, kNoDraft, kBad };
+enum Stop { kAccepted = -1, kRejected, kNoDraft, kBad };
 
 struct VerifyShared {
   uint64_t seg_weight[kSegments];
@@ -96,6 +96,20 @@ struct Kept {
   }
 };
 
+// What becomes of draft d, given the target's logit x and the draft's logit y for it (`g` is
+// not used without a draft's row): kAccepted, kRejected or kBad.
+__device__ __forceinline__ int compare(const RowCut& t, const RowCut& g, bool drawn, float x, float y, uint32_t d, float u) {
+  if (t.whole == 0 || u != u || (drawn && g.whole == 0)) return kBad;
+  // p and q in 32 bits are within 2^-22 of theirs: only where u q comes near p does it take
+  // double precision, which this chip has little of (two divisions are some microseconds)
+  const Kept target(t);
+  const float p32 = target.share(x, d), uq = u * (drawn ? Kept(g).share(y, d) : 1.f);
+  bool less = uq < p32;
+  if (fabsf(uq - p32) <= 0x1p-20f * p32)
+    less = __dmul_rn(static_cast<double>(u), drawn ? Kept(g).probability(y, d) : 1.0) < target.probability(x, d);
+  return less ? kAccepted : kRejected;
+}
+
 // ---------------------------------------------------------------- rows without filters
 // Their kept set is the row, so only its maximum and the sum of its weights are wanted:
 // one pass, with the slice of the row in registers between the two. A cluster per row, of
@@ -115,6 +129,42 @@ __device__ __forceinline__ uint32_t max_nan(uint32_t a, uint32_t b, const float*
   return __float_as_uint(r);
 }
 
+// Rows behind a draft that is not accepted are not wanted. Where there are more rows than run at
+// once they go by place, all requests' first rows first, and whoever completes a draft's rows compares
+// it: rows that start later than that leave their work. (A hint: a CTA that comes too early to see it
+// works in vain, and what such rows leave in p.cuts is not looked at.)
+struct Progress {
+  uint32_t* stopped;  // [batch] drafts + 1 - place of the first draft known not to be accepted, 0 if none is
+  uint32_t* rows;     // [batch][drafts] rows that are summed
+};
+
+// What the writer of row (request, place)'s cut does then.
+template <typename T>
+__device__ void row_is_summed(const SampleParams& p, const Progress& progress, int64_t request, int place) {
+  if (place >= p.drafts) return;
+  __threadfence();
+  if (atomicAdd(&progress.rows[request * p.drafts + place], 1u) + 1 < (p.draft ? 2u : 1u)) return;
+  __threadfence();
+  const int64_t d = __ldg(p.draft_tokens + request * p.drafts + place);
+  if (d < 0 || d >= p.vocab) return;
+  auto cut = [](const RowCut* from) {  // past the L1
+    union {
+      uint4 u[2];
+      RowCut c;
+    } v;
+    static_assert(sizeof(RowCut) == 32, "two vectors");
+    v.u[0] = __ldcg(reinterpret_cast<const uint4*>(from));
+    v.u[1] = __ldcg(reinterpret_cast<const uint4*>(from) + 1);
+    return v.c;
+  };
+  const RowCut t = cut(p.cuts + request * (p.drafts + 1) + place);
+  const RowCut g = p.draft ? cut(p.cuts + p.target_rows + request * p.drafts + place) : t;
+  const float x = to_float<T>(static_cast<const T*>(p.x)[request * p.batch_ld + place * p.ld + d]);
+  const float y = p.draft ? to_float<T>(static_cast<const T*>(p.draft)[request * p.draft_batch_ld + place * p.draft_ld + d]) : 0.f;
+  if (compare(t, g, p.draft != nullptr, x, y, static_cast<uint32_t>(d), p.u[request * (p.drafts + 1) + place]) != kAccepted)
+    atomicMax(&progress.stopped[request], static_cast<uint32_t>(p.drafts + 1 - place));
+}
+
 struct PlainShared {
   uint32_t tops[kMaxCluster];
   unsigned long long totals[kMaxCluster];
@@ -123,7 +173,7 @@ struct PlainShared {
 };
 
 template <typename T, int kPlainThreads>
-__global__ void __launch_bounds__(kPlainThreads, 1024 / kPlainThreads) verify_plain_kernel(const SampleParams p, const int slice) {
+__global__ void __launch_bounds__(kPlainThreads, 1024 / kPlainThreads) verify_plain_kernel(const SampleParams p, const int slice, const Progress progress) {
   __shared__ PlainShared s;
   constexpr int E = 16 / sizeof(T);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -131,41 +181,62 @@ __global__ void __launch_bounds__(kPlainThreads, 1024 / kPlainThreads) verify_pl
   uint32_t ctas;
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
   asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");  // all are running before the first write into another
-  const int64_t r = blockIdx.x / ctas;
+  uint32_t r = blockIdx.x / ctas;  // (32 bits: divisions of 64 are a hundred instructions)
+  if (progress.stopped) {
+    // by place: a request's row of the target, then its row of the draft, then the next request's
+    const uint32_t drafts = static_cast<uint32_t>(p.drafts), target_rows = static_cast<uint32_t>(p.target_rows);
+    const uint32_t batch = target_rows / (drafts + 1), kinds = p.draft ? 2 : 1, at_place = r / (batch * kinds);
+    const uint32_t at = r - at_place * batch * kinds;
+    if (at_place >= drafts)  // of the target alone
+      r = at * (drafts + 1) + at_place;
+    else
+      r = at % kinds ? target_rows + at / kinds * drafts + at_place : at / kinds * (drafts + 1) + at_place;
+  }
   const T* start;
   int64_t request;
-  if (!verify_row(p, r, &start, &request)) {
+  int place;
+  if (!verify_row(p, r, &start, &request, &place)) {
     asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
     return;
+  }
+  // (the row's CTAs may see different answers here: all go through the barriers)
+  bool wanted = true;
+  if (progress.stopped) {
+    const uint32_t stop = __shfl_sync(0xffffffffu, *static_cast<volatile uint32_t*>(progress.stopped + request), 0);
+    wanted = stop == 0 || place <= static_cast<int>(p.drafts + 1 - stop);
   }
   const int vocab = static_cast<int>(p.vocab), c0 = static_cast<int>(rank) * slice, size = max(0, min(slice, vocab - c0));
   start += c0;
   const bool aligned = reinterpret_cast<uintptr_t>(start) % 16 == 0;
   Raw<T, E> raw[kPlainVecs];
+  uint32_t key = 0;
+  if (wanted) {
 #pragma unroll
-  for (int j = 0; j < kPlainVecs; ++j) {
-    const int v = static_cast<int>(threadIdx.x) + j * kPlainThreads;
-    if (aligned && (v + 1) * E <= size) {
-      raw[j] = load_raw<T, E>(start + v * E);
-    } else {
-      float x[E];
+    for (int j = 0; j < kPlainVecs; ++j) {
+      const int v = static_cast<int>(threadIdx.x) + j * kPlainThreads;
+      if (aligned && (v + 1) * E <= size) {
+        raw[j] = load_raw<T, E>(start + v * E);
+      } else {
+        float x[E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) x[e] = v * E + e < size ? to_float<T>(start[v * E + e]) : -INFINITY;
-      raw[j] = pack<T, E>(x);
+        for (int e = 0; e < E; ++e) x[e] = v * E + e < size ? to_float<T>(start[v * E + e]) : -INFINITY;
+        raw[j] = pack<T, E>(x);
+      }
     }
-  }
-  // the largest logit, NaN if there is one
-  uint32_t most = raw[0].u.x;
+    // the largest logit, NaN if there is one
+    uint32_t most = raw[0].u.x;
 #pragma unroll
-  for (int j = 0; j < kPlainVecs; ++j) {
-    const uint32_t w[4] = {raw[j].u.x, raw[j].u.y, raw[j].u.z, raw[j].u.w};
+    for (int j = 0; j < kPlainVecs; ++j) {
+      const uint32_t w[4] = {raw[j].u.x, raw[j].u.y, raw[j].u.z, raw[j].u.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) most = max_nan(most, w[i], static_cast<const T*>(nullptr));
+      for (int i = 0; i < 4; ++i) most = max_nan(most, w[i], static_cast<const T*>(nullptr));
+    }
+    float mine = __uint_as_float(most);
+    if constexpr (sizeof(T) == 2) mine = __uint_as_float(max_nan(most << 16, most & 0xFFFF0000u, static_cast<const float*>(nullptr)));
+    // (a NaN, made positive, ranks above infinity)
+    key = mine != mine ? 0xFFFFFFFFu : order_key(mine);
   }
-  float top = __uint_as_float(most);
-  if constexpr (sizeof(T) == 2) top = __uint_as_float(max_nan(most << 16, most & 0xFFFF0000u, static_cast<const float*>(nullptr)));
-  // (a NaN, made positive, ranks above infinity)
-  uint32_t key = __reduce_max_sync(0xffffffffu, top != top ? 0xFFFFFFFFu : order_key(top));
+  key = __reduce_max_sync(0xffffffffu, key);
   if (lane == 0) s.keys[warp] = key;
   __syncthreads();
   key = __reduce_max_sync(0xffffffffu, s.keys[lane % (kPlainThreads / 32)]);
@@ -173,28 +244,29 @@ __global__ void __launch_bounds__(kPlainThreads, 1024 / kPlainThreads) verify_pl
   if (threadIdx.x < ctas) remote_store(&s.tops[rank], threadIdx.x, key);
   row_barrier<true>();
   for (uint32_t c = 0; c < ctas; ++c) key = max(key, s.tops[c]);
-  top = key_value(key);
+  const float top = key_value(key);
   const bool bad = !(fabsf(top) < INFINITY);
   const float inv = fmaxf(1.f / p.temperature, kLeast);
-  // Weights in halves, as halves() takes them; what it subtracts from each comes off the sums at the end.
-  uint32_t hi = 0, lo = 0;
-  const Pairs pairs(top, inv);
-#pragma unroll
-  for (int j = 0; j < kPlainVecs; ++j) {
-    float x[E];
-    unpack<T, E>(raw[j], x);
-#pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      uint64_t a, b;
-      Pairs::split(pairs.exponentials(x[e], x[e + 1]), a, b);
-      hi += static_cast<uint32_t>(a) + static_cast<uint32_t>(a >> 32);
-      lo += static_cast<uint32_t>(b) + static_cast<uint32_t>(b >> 32);
-    }
-  }
-  constexpr uint32_t kLess = static_cast<uint32_t>(uint64_t{kLarge} * (kPlainVecs * E));
+  // Weights in halves, as halves() takes them; what it subtracts from each comes off the sums.
   Sum sum;
-  sum.hi = hi - kLess;
-  sum.lo = lo - kLess;
+  if (wanted) {
+    const Pairs pairs(top, inv);
+#pragma unroll
+    for (int j = 0; j < kPlainVecs; ++j) {
+      float x[E];
+      unpack<T, E>(raw[j], x);
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        uint64_t a, b;
+        Pairs::split(pairs.exponentials(x[e], x[e + 1]), a, b);
+        sum.hi += static_cast<uint32_t>(a) + static_cast<uint32_t>(a >> 32);
+        sum.lo += static_cast<uint32_t>(b) + static_cast<uint32_t>(b >> 32);
+      }
+    }
+    constexpr uint32_t kLess = static_cast<uint32_t>(uint64_t{kLarge} * (kPlainVecs * E));
+    sum.hi -= kLess;
+    sum.lo -= kLess;
+  }
   const uint64_t mine = sum.total();
   if (lane == 0) s.sums[warp] = mine;
   __syncthreads();
@@ -208,6 +280,7 @@ __global__ void __launch_bounds__(kPlainThreads, 1024 / kPlainThreads) verify_pl
     uint64_t whole = 0;
     for (uint32_t c = 0; c < ctas; ++c) whole += s.totals[c];
     p.cuts[r] = {~0ull, bad ? 0 : whole, top, inv, 0.f, bad ? 0.f : reciprocal(whole)};
+    if (progress.stopped) row_is_summed<T>(p, progress, request, place);
   }
 }
 
@@ -243,7 +316,14 @@ cudaError_t run_plain(const SampleParams& p, int sms, cudaStream_t s) {
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, verify_plain_kernel<T, kPlainThreads>, p, slice);
+  Progress progress = {};
+  if (p.rows * ctas > 1024LL / kPlainThreads * sms && p.drafts > 0) {
+    const int64_t batch = p.target_rows / (p.drafts + 1);
+    progress = {p.progress, p.progress + batch};
+    const cudaError_t e = cudaMemsetAsync(p.progress, 0, sizeof(uint32_t) * batch * (p.drafts + 1), s);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaLaunchKernelEx(&cfg, verify_plain_kernel<T, kPlainThreads>, p, slice, progress);
 }
 
 // Smaller CTAs, four on an SM, where eight of them hold a row: 704 rows of 129280 bf16 74 us, 78 with the larger ones.
@@ -279,7 +359,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const SampleP
     int count = 0, stop = kNoDraft;
     for (int64_t base = 0; base < K; base += 32) {
       const int64_t i = base + lane;
-      int mine = -1;  // accepted
+      int mine = kAccepted;
       const uint32_t none = __ballot_sync(0xffffffffu, i < K && !(drafts[i] >= 0 && drafts[i] < p.vocab));
       if (i < K) {
         const int64_t d = drafts[i];
@@ -287,31 +367,10 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const SampleP
         if (none & ((2u << lane) - 1u)) {
           mine = kNoDraft;
         } else {
-          const Kept t(cuts[i]);
-          const float v = u[i];
-          if (t.c.whole == 0 || v != v) {
-            mine = kBad;
-          } else {
-            const uint32_t at = static_cast<uint32_t>(d);
-            const float x = to_float<T>(target[i * p.ld + d]), p32 = t.share(x, at);
-            float y = 0.f, q32 = 1.f;
-            if (draft) {
-              const Kept g(draft_cuts[i]);
-              y = to_float<T>(draft[i * p.draft_ld + d]);
-              q32 = g.share(y, at);
-              if (g.c.whole == 0) mine = kBad;
-            }
-            if (mine < 0) {
-              // p and q in 32 bits are within 2^-22 of theirs: only where u q comes near p does it take
-              // double precision, which this chip has little of (two divisions are some microseconds)
-              const float uq = v * q32;
-              bool less = uq < p32;
-              if (fabsf(uq - p32) <= 0x1p-20f * p32)
-                less = __dmul_rn(static_cast<double>(v), draft ? Kept(draft_cuts[i]).probability(y, at) : 1.0) < t.probability(x, at);
-              if (!less) mine = kRejected;
-            }
-            if (mine < 0 && rank == 0 && logprobs) logprobs[i] = t.logprob(x);
-          }
+          const RowCut t = cuts[i], g = draft ? draft_cuts[i] : t;
+          const float x = to_float<T>(target[i * p.ld + d]), y = draft ? to_float<T>(draft[i * p.draft_ld + d]) : 0.f;
+          mine = compare(t, g, draft != nullptr, x, y, static_cast<uint32_t>(d), u[i]);
+          if (mine == kAccepted && rank == 0 && logprobs) logprobs[i] = Kept(t).logprob(x);
         }
       }
       const uint32_t stopped = __ballot_sync(0xffffffffu, mine >= 0);
