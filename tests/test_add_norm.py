@@ -305,3 +305,116 @@ def test_refusals():
                      ((a["gy"], None, q) + st, dict(grad_weight=torch.zeros(64, device="cuda").bfloat16(), need_grad_bias=False))):
         with pytest.raises(ValueError):
             flce.flce_add_layer_norm_backward(*args, **kw)
+
+
+@pytest.mark.gpu
+def test_x_and_residual_get_gradients_of_their_own():
+    import linear_cross_entropy_02_gb300 as flce
+    a = make(20, 64, torch.bfloat16)
+    x, res = a["x"].clone().requires_grad_(), a["res"].clone().requires_grad_()
+    y, s = flce.add_layer_norm(x, res, a["w"], rms=True)
+    torch.autograd.backward([y, s], [a["gy"], a["gs"]])
+    assert torch.equal(x.grad, res.grad) and x.grad.data_ptr() != res.grad.data_ptr()
+    before = res.grad.clone()
+    x.grad.zero_()
+    assert torch.equal(res.grad, before)
+    # one tensor as both
+    t = a["x"].clone().requires_grad_()
+    y, _ = flce.add_layer_norm(t, t, a["w"], rms=True)
+    y.backward(a["gy"])
+    out = flce.flce_add_layer_norm(a["x"], a["x"], a["w"], rms=True, return_stats=True)
+    g = flce.flce_add_layer_norm_backward(a["gy"], None, out["sum"], a["w"], None, out["rstd"], rms=True)["grad_x"]
+    assert torch.equal(t.grad, g + g)
+    # the sum changed in place before the backward pass: an error, not another gradient
+    x = a["x"].clone().requires_grad_()
+    y, s = flce.add_layer_norm(x, a["res"], a["w"], rms=True)
+    with torch.no_grad():
+        s.mul_(2)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward(a["gy"])
+
+
+@pytest.mark.gpu
+def test_wide_rows_of_every_kind():
+    """Rows of a multiple of 512: kernels of their own for bias or none, and at either end of their widths; a batch that gives CTAs several rows."""
+    import linear_cross_entropy_02_gb300 as flce
+    for H, rows in ((2048, 1300), (2560, 400), (4608, 700), (5120, 650), (6144, 33), (8192, 500), (8704, 320)):
+        for dtype in (torch.bfloat16, torch.float32):
+            for rms, bias, wdtype in ((True, False, torch.bfloat16), (True, True, torch.float32), (False, False, torch.float32), (False, True, torch.bfloat16)):
+                a = make(rows, H, dtype, wdtype, seed=H)
+                out = flce.flce_add_layer_norm(a["x"], a["res"], a["w"], rms=rms, checkpoint=True, return_stats=True)
+                for x, x64 in ((out["sum"], out["sum"]), (out["checkpoint"], flce.flce_checkpoint_load(out["checkpoint"]))):
+                    for gs in (a["gs"], None):
+                        got = flce.flce_add_layer_norm_backward(a["gy"], gs, x, a["w"], out["mean"], out["rstd"], rms=rms, need_grad_bias=bias)
+                        check_backward(got, a["gy"], gs, x64, a["w"], out["mean"], out["rstd"], rms)
+                part = flce.flce_add_layer_norm_backward(a["gy"], a["gs"], out["checkpoint"], a["w"], out["mean"], out["rstd"], rms=rms, need_grad_x=False,
+                                                         need_grad_weight=not bias, need_grad_bias=bias)
+                check_backward(part, a["gy"], None, x64, a["w"], out["mean"], out["rstd"], rms)
+
+
+@pytest.mark.gpu
+def test_blocks_of_nan_in_the_checkpoint_s_gradient():
+    import linear_cross_entropy_02_gb300 as flce
+    a = make(40, 2048, torch.bfloat16)
+    a["res"][7, 100] = float("inf")
+    out = flce.flce_add_layer_norm(a["x"], a["res"], a["w"], rms=True, checkpoint=True, return_stats=True)
+    g = flce.flce_add_layer_norm_backward(a["gy"], a["gs"], out["checkpoint"], a["w"], None, out["rstd"], rms=True)
+    good = torch.ones(40, dtype=torch.bool)
+    good[7] = False
+    assert torch.equal(g["grad_x"].isfinite().all(1).cpu(), good)
+
+
+@pytest.mark.gpu
+def test_sums_beyond_32_bits_of_elements():
+    import linear_cross_entropy_02_gb300 as flce
+    rows, H = 300000, 8192
+    x = torch.empty(rows, H, dtype=torch.bfloat16, device="cuda").normal_()
+    ends = torch.tensor([0, 1, 262143, 262144, 262145, rows - 1], device="cuda")
+    w = torch.ones(H, device="cuda")
+    out = flce.flce_add_layer_norm(x, x, w, rms=True, checkpoint=True, return_stats=True)
+    few = flce.flce_add_layer_norm(x[ends], x[ends], w, rms=True, checkpoint=True, return_stats=True)
+    assert torch.equal(out["sum"][ends], few["sum"]) and torch.equal(out["checkpoint"].codes[ends], few["checkpoint"].codes)
+    assert torch.equal(out["checkpoint"].scales[ends], few["checkpoint"].scales)
+    assert bool(((out["y"][ends].float() - few["y"].float()).abs() <= 2.0 ** -7 * few["y"].float().abs()).all())
+    q = flce.flce_checkpoint_store(x)
+    p = flce.flce_checkpoint_store(x[ends])
+    assert torch.equal(q.codes[ends], p.codes) and torch.equal(flce.flce_checkpoint_load(q, dtype=torch.bfloat16)[ends],
+                                                              flce.flce_checkpoint_load(p, dtype=torch.bfloat16))
+    g = flce.flce_add_layer_norm_backward(x, None, out["checkpoint"], w, None, out["rstd"], rms=True, need_grad_bias=False)["grad_x"]
+    f = flce.flce_add_layer_norm_backward(x[ends], None, few["checkpoint"], w, None, few["rstd"], rms=True, need_grad_bias=False)["grad_x"]
+    assert bool(((g[ends].float() - f.float()).abs() <= 2.0 ** -7 * f.float().abs() + 1e-6).all())
+
+
+@pytest.mark.gpu
+def test_a_captured_backward_pass():
+    """Forward and backward through the autograd nodes, captured where no eager graph of the leaves lives, and replayed on other values."""
+    import linear_cross_entropy_02_gb300 as flce
+    g = torch.Generator(device="cuda").manual_seed(4)
+    W = torch.randn(500, 96, generator=g, device="cuda").requires_grad_()
+    n = torch.ones(96, device="cuda").requires_grad_()
+    t = torch.randint(0, 500, (64,), generator=g, device="cuda")
+    layer, G = torch.randn(64, 96, generator=g, device="cuda"), torch.randn(64, 96, generator=g, device="cuda")
+
+    def step():
+        y, s = flce.add_layer_norm(layer, flce.embedding(t, W, scale=3.0), n, rms=True, checkpoint_8bit=True)
+        ((y + s) * G).sum().backward()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            step()
+            W.grad = n.grad = None
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step()
+    kept = W.grad, n.grad
+    t.copy_(t.flip(0))
+    layer.mul_(0.5)
+    graph.replay()
+    got = [k.clone() for k in kept]
+    W.grad = n.grad = None
+    with torch.cuda.stream(side):
+        step()
+    side.synchronize()
+    assert torch.equal(got[0], W.grad) and torch.equal(got[1], n.grad)

@@ -198,3 +198,35 @@ def test_refusals():
                      ((G, t, 10), dict(grad_W=W[:9])), ((G.half(), t, 10), {})):
         with pytest.raises(ValueError):
             flce.flce_embedding_backward(*args, **kw)
+
+
+@pytest.mark.gpu
+def test_weights_beyond_32_bits_of_elements():
+    import linear_cross_entropy_02_gb300 as flce
+    V, H = 530000, 4104
+    t = torch.tensor([0, V - 1, 529999, 261633, 1, V - 1], device="cuda")
+    G = torch.randn(6, H, device="cuda").bfloat16()
+    gW = flce.flce_embedding_backward(G, t, V)
+    assert gW.numel() > 1 << 31
+    want = torch.zeros(4, H, device="cuda")
+    want[0], want[1], want[2], want[3] = G[0], G[1].float() + G[2].float() + G[5].float(), G[3], G[4]
+    rows = torch.tensor([0, V - 1, 261633, 1], device="cuda")
+    assert torch.equal(gW[rows], want)
+    gW[rows] = 0
+    assert int(gW.view(-1, 8).any(1).sum()) == 0
+    W = gW.bfloat16()
+    del gW
+    W[rows] = G[:4]
+    assert torch.equal(flce.flce_embedding(rows, W), G[:4])
+
+
+@pytest.mark.gpu
+def test_gradients_that_are_not_numbers_stay_with_their_tokens():
+    import linear_cross_entropy_02_gb300 as flce
+    t = torch.tensor([5, 7, -1, 5, 9, 300], device="cuda")
+    G = torch.ones(6, 40, device="cuda")
+    G[1, 3] = float("nan")
+    G[2], G[5] = float("nan"), float("inf")       # rows of no token, and of one behind the vocabulary
+    gW = flce.flce_embedding_backward(G, t, 20)
+    assert int(gW.isnan().sum()) == 1 and bool(gW[7, 3].isnan()) and bool((gW[5] == 2).all()) and bool((gW[9] == 1).all())
+    assert float(gW.nan_to_num().sum()) == 39 + 80 + 40

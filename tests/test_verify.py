@@ -346,3 +346,38 @@ def test_refusals():
             flce.flce_verify(*args, **kw)
     with pytest.raises(flce.FlceError):
         flce.flce_verify(x, d, u, q, top_p=float("nan"))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("with_draft", [True, False])
+def test_batches_larger_than_the_gpu(with_draft):
+    """Unfiltered rows of which more are wanted than run at once, on clusters: rows behind a rejected draft are left out,
+    whatever the workspace held before."""
+    import linear_cross_entropy_02_gb300 as flce
+    x, q, u, g = make(70, 4, 20000, torch.bfloat16, seed=12)
+    d = draft_from(flce, q, g, {}, 4)
+    d[3, 1:], d[5, 2] = -1, 20000
+    x[7, 2, 11], q[9, 0, 5], u[11, 1] = math.nan, math.inf, math.nan
+    q = q if with_draft else None
+    for fill in (0, 255):
+        junk = torch.full((1 << 20,), fill, dtype=torch.uint8, device="cuda")
+        del junk                                # torch hands the same memory to the call
+        got = check(flce, x, d, u, q, {})
+    # (found drafts are rarely accepted: all their weight is on one token)
+    assert int(got[1].min()) == 0 and int(got[1].max()) >= (2 if with_draft else 1)
+    # a request alone, on other clusters
+    for b in (0, 7, 69):
+        one = flce.flce_verify(x[b], d[b], u[b], None if q is None else q[b])
+        assert torch.equal(one[0], got[0][b]) and torch.equal(one[1], got[1][b])
+
+
+@pytest.mark.gpu
+def test_logits_beyond_32_bits_of_elements():
+    import linear_cross_entropy_02_gb300 as flce
+    x, q, u, g = make(2, 2, 1001, torch.bfloat16, seed=13)
+    far = torch.empty((1 << 31) + (1 << 20), dtype=torch.bfloat16, device="cuda")
+    wide = far.as_strided((2, 3, 1001), ((1 << 31) - 4096, 2048, 1))
+    wide.copy_(x)
+    d = draft_from(flce, q, g, {}, 2)
+    for kw in (dict(), dict(top_k=20, top_p=0.9)):
+        assert all(torch.equal(a, b) for a, b in zip(flce.flce_verify(wide, d, u, q, **kw), flce.flce_verify(x, d, u, q, **kw)))
