@@ -5,7 +5,7 @@
 
 namespace flce {
 
-cudaError_t launch_add_norm_bwd_8bit(const NormParams& p, int sms, int* partials, cudaStream_t s) {
+cudaError_t launch_add_norm_bwd_8bit(const AddNormParams& p, int sms, int* partials, cudaStream_t s) {
   if (wide_rows(p)) return p.dtype == FLCE_DTYPE_F32 ? run_wide_bwd<float, true>(p, sms, partials, s) : run_wide_bwd<uint16_t, true>(p, sms, partials, s);
   return p.dtype == FLCE_DTYPE_F32 ? launch_bwd<float, 4, kAdd8>(p, sms, partials, s) : launch_bwd<uint16_t, 8, kAdd8>(p, sms, partials, s);
 }

@@ -51,7 +51,7 @@ struct Codes {
 
 // C vectors per thread. HOLD: the weighted gradients stay in registers between the passes.
 template <typename T, typename W, int NB, bool RMS, bool X8, bool HOLD, int C, int REGS>
-__global__ void __maxnreg__(REGS) add_norm_bwd_kernel(const NormParams p, const int stages) {
+__global__ void __maxnreg__(REGS) add_norm_bwd_kernel(const AddNormParams p, const int stages) {
   constexpr int E = 16 / sizeof(T);
   constexpr int XB = X8 ? E : 16;  // bytes of a vector of x
   extern __shared__ __align__(16) uint8_t dyn[];
@@ -201,7 +201,7 @@ __global__ void __maxnreg__(REGS) add_norm_bwd_kernel(const NormParams p, const 
 }
 
 template <typename T, typename W, int NB, bool RMS, bool X8, bool HOLD, int C, int REGS>
-cudaError_t run_add_bwd_as(const NormParams& p, int sms, int* partials, cudaStream_t s) {
+cudaError_t run_add_bwd_as(const AddNormParams& p, int sms, int* partials, cudaStream_t s) {
   constexpr int E = 16 / sizeof(T);
   const int vecs = static_cast<int>(p.hidden / E), threads = vecs / C;
   int ctas = 65536 / (REGS * threads);
@@ -215,7 +215,7 @@ cudaError_t run_add_bwd_as(const NormParams& p, int sms, int* partials, cudaStre
 }
 
 template <typename T, typename W, bool X8>
-cudaError_t run_add_bwd(const NormParams& p, int sms, int* partials, cudaStream_t s) {
+cudaError_t run_add_bwd(const AddNormParams& p, int sms, int* partials, cudaStream_t s) {
   constexpr int C = sizeof(T);  // 16 columns per thread
   // (Microseconds for 32768 rows, from 8 bits: 7168 RMS without holding 317, held 316, with 32
   // columns 295; 4096 178 and 181. With a bias' sums 7168 held 394, not 376; from the sum 353 and 374.)
@@ -230,12 +230,12 @@ cudaError_t run_add_bwd(const NormParams& p, int sms, int* partials, cudaStream_
 
 // Whether rows are for these kernels. (Shorter ones were slower: 65536 x 1024 RMS from 8 bits 153 us, 112 by
 // norm_device.cuh's; 2048 203 and 220.)
-inline bool wide_rows(const NormParams& p) {
+inline bool wide_rows(const AddNormParams& p) {
   return p.hidden >= kLeastWide && p.hidden <= kMostWide && p.hidden % kWideStep == 0 && vectors(p);
 }
 
 template <typename T, bool X8>
-cudaError_t run_wide_bwd(const NormParams& p, int sms, int* partials, cudaStream_t s) {
+cudaError_t run_wide_bwd(const AddNormParams& p, int sms, int* partials, cudaStream_t s) {
   return p.w_f32 ? run_add_bwd<T, float, X8>(p, sms, partials, s) : run_add_bwd<T, uint16_t, X8>(p, sms, partials, s);
 }
 

@@ -49,6 +49,17 @@ __device__ __forceinline__ void read_codes(const uint32_t (&words)[E == 8 ? 2 : 
   }
 }
 
+// A vector of a checkpoint as it is held.
+template <int E>
+struct CodeVector {
+  uint32_t words[E == 8 ? 2 : 1];
+  float scale;
+};
+template <typename T, int E>
+__device__ __forceinline__ void unpack(const CodeVector<E>& r, float (&v)[E]) {
+  read_codes<E>(r.words, r.scale, v);
+}
+
 // Encodes vector `vec` of a row: codes [rows, hidden], scales [rows, blocks]. Called by
 // whole warps, `vec` rising by one from lane to lane over groups of min(32 / E, lanes);
 // lanes that are not `valid` have no part of the row.

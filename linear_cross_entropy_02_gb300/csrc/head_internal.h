@@ -36,16 +36,6 @@ struct NormParams {
   float* rstd;
   float* part_w;     // backward: per-CTA partial sums [grid][hidden], or null
   float* part_b;
-  // behind the residual's addition (model_internal.h): what is added, the sum and its
-  // 8-bit checkpoint, each nullable; backward: the checkpoint in the place of x, and a
-  // gradient of the sum
-  const void* residual;
-  int64_t ld_res;
-  void* sum;
-  uint8_t* codes;
-  uint8_t* scales;
-  const void* gs;
-  int64_t ld_gs;
 };
 // Most partial rows that launch_norm_bwd writes for a call on this device.
 int norm_partial_rows(int64_t rows, int64_t hidden, int sms);
@@ -96,15 +86,6 @@ bool mx_gemm_encodes(int64_t rows, int64_t cols);
 int launch_mx_gemm(const MxGemmParams& p, int sms, cudaStream_t s);
 
 // ------------------------------------------------------------ sampling
-// What the filters keep of a row of logits: those up to `last` in rank order (list
-// entries: complemented order key, index) whose exponential is at least min_p.
-struct RowCut {
-  uint64_t last;
-  uint64_t whole;   // sum of the kept weights; 0: no distribution, the rest says nothing
-  float top, inv;   // largest logit, 1 / temperature
-  float min_p;
-  float over;       // 1 / whole, rounded to 64 bits and then to 32
-};
 struct SampleParams {
   const void* x;
   int dtype;
@@ -118,14 +99,6 @@ struct SampleParams {
   int32_t top_k;
   int64_t* tokens;
   float* logprobs;
-  // verification (model_internal.h): rows of the target [batch][drafts + 1], then of the
-  // draft [batch][drafts], and what is kept of each
-  const void* draft;
-  const int64_t* draft_tokens;
-  int64_t target_rows, drafts;
-  int64_t batch_ld, draft_ld, draft_batch_ld;
-  RowCut* cuts;
-  uint32_t* progress;  // [batch][drafts + 1]
 };
 cudaError_t launch_sample(const SampleParams& p, int sms, cudaStream_t s);
 

@@ -151,7 +151,7 @@ int flce_add_layer_norm(const void* x, int64_t ld_x, const void* residual, int64
   const int rc = device_check(&sms);
   if (rc != FLCE_OK) return rc;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_handle);
-  NormParams p = {};
+  AddNormParams p = {};
   p.x = x;
   p.dtype = dtype;
   p.rows = rows;
@@ -210,7 +210,7 @@ int flce_add_layer_norm_backward(const void* grad_y, int64_t ld_grad_y, const vo
   cudaStream_t stream = static_cast<cudaStream_t>(stream_handle);
   const size_t half = round256(sizeof(float) * static_cast<size_t>(rows > 0 ? add_norm_partial_rows(rows, hidden, sms) : 1) * hidden);
   if (sums && workspace_bytes < 2 * half) return FLCE_ERR_WORKSPACE;
-  NormParams p = {};
+  AddNormParams p = {};
   p.x = x;
   p.ld_x = x ? ld_x : hidden;
   p.codes = static_cast<uint8_t*>(const_cast<void*>(codes));
@@ -357,7 +357,7 @@ int flce_verify(const void* target, int logits_dtype, int64_t batch, int64_t dra
   const int rc = device_check(&sms);
   if (rc != FLCE_OK) return rc;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_handle);
-  SampleParams p = {};
+  VerifyParams p = {};
   p.x = target;
   p.dtype = logits_dtype;
   p.rows = rows;

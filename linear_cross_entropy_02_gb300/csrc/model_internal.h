@@ -23,12 +23,22 @@ enum ModelKernelId {
 };
 
 // ------------------------------------------------------------ residual and norm
-// (NormParams' last members; K_NORM_WGRAD joins the partial sums)
+// (K_NORM_WGRAD joins the partial sums. A struct of its own, as is VerifyParams: the norm's and sampling's
+// kernels, with more parameters than they use, were compiled to slower code.)
+struct AddNormParams : NormParams {
+  const void* residual;  // nullable
+  int64_t ld_res;
+  void* sum;             // nullable
+  uint8_t* codes;        // 8-bit checkpoint: written (nullable), or read in the place of x
+  uint8_t* scales;
+  const void* gs;        // backward: gradient of the sum, or null
+  int64_t ld_gs;
+};
 // Most partial rows that the backward passes write for a call on this device.
 int add_norm_partial_rows(int64_t rows, int64_t hidden, int sms);
-cudaError_t launch_add_norm(const NormParams& p, int sms, cudaStream_t s);
-cudaError_t launch_add_norm_bwd(const NormParams& p, int sms, int* partials, cudaStream_t s);
-cudaError_t launch_add_norm_bwd_8bit(const NormParams& p, int sms, int* partials, cudaStream_t s);
+cudaError_t launch_add_norm(const AddNormParams& p, int sms, cudaStream_t s);
+cudaError_t launch_add_norm_bwd(const AddNormParams& p, int sms, int* partials, cudaStream_t s);
+cudaError_t launch_add_norm_bwd_8bit(const AddNormParams& p, int sms, int* partials, cudaStream_t s);
 
 // ------------------------------------------------------------ 8-bit checkpoints
 struct CheckpointParams {
@@ -67,10 +77,27 @@ int launch_embedding_sort(EmbeddingParams* p, int sms, cudaStream_t stream);
 int launch_embedding_grad(const EmbeddingParams& p, cudaStream_t stream);
 
 // ------------------------------------------------------------ verification
-// SampleParams with its last members; u [batch][drafts + 1], tokens and logprobs
-// [batch][drafts + 1]; p.rows: all rows, of the target and of the draft (if it has any).
+// What the filters keep of a row of logits: those up to `last` in rank order (list
+// entries: complemented order key, index) whose exponential is at least min_p.
+struct RowCut {
+  uint64_t last;
+  uint64_t whole;   // sum of the kept weights; 0: no distribution, the rest says nothing
+  float top, inv;   // largest logit, 1 / temperature
+  float min_p;
+  float over;       // 1 / whole, rounded to 64 bits and then to 32
+};
+// Rows of the target [batch][drafts + 1] (x, with row stride ld), then of the draft [batch][drafts], if it
+// has any; p.rows: all of them. u, tokens and logprobs are [batch][drafts + 1].
+struct VerifyParams : SampleParams {
+  const void* draft;
+  const int64_t* draft_tokens;
+  int64_t target_rows, drafts;
+  int64_t batch_ld, draft_ld, draft_batch_ld;
+  RowCut* cuts;        // of every row
+  uint32_t* progress;  // [batch][drafts + 1]
+};
 // launch_verify_cuts fills p.cuts, launch_verify reads it.
-cudaError_t launch_verify_cuts(const SampleParams& p, int sms, cudaStream_t s);
-cudaError_t launch_verify(const SampleParams& p, int64_t batch, int64_t* accepted, int sms, cudaStream_t s);
+cudaError_t launch_verify_cuts(const VerifyParams& p, int sms, cudaStream_t s);
+cudaError_t launch_verify(const VerifyParams& p, int64_t batch, int64_t* accepted, int sms, cudaStream_t s);
 
 }  // namespace flce

@@ -41,6 +41,7 @@
 #include "checkpoint_device.cuh"
 #include "head_device.cuh"
 #include "head_internal.h"
+#include "model_internal.h"
 
 namespace flce {
 
@@ -50,6 +51,8 @@ namespace {
 // type, and may be written out or kept in 8 bits; backward, a gradient of that sum is
 // added to grad_x. kAdd8: the same backward, from the 8-bit checkpoint of the sum.
 constexpr int kPlain = 0, kAdd = 1, kAdd8 = 2;
+template <int MODE>
+using ParamsOf = std::conditional_t<MODE == kPlain, NormParams, AddNormParams>;
 
 constexpr int kMaxVecs = 8;           // vectors per thread of a forward row
 constexpr int kWarpRowThreads = 256;  // eight warps per CTA
@@ -114,7 +117,7 @@ struct One {
   static constexpr bool value = false;
 };
 template <typename T, int E, int C, int MODE, typename S>
-__device__ __forceinline__ void norm_row(const NormParams& p, const T* x, T* y, int64_t row, int t, int stride, int vecs,
+__device__ __forceinline__ void norm_row(const ParamsOf<MODE>& p, const T* x, T* y, int64_t row, int t, int stride, int vecs,
                                          int lanes, S sum) {
   Raw<T, E> cur[C];
 #pragma unroll
@@ -240,7 +243,7 @@ __device__ __forceinline__ void norm_row(const NormParams& p, const T* x, T* y, 
 
 // A row per CTA, of THREADS threads if that is not 0.
 template <typename T, int E, int C, int THREADS, int MODE>
-__global__ void __launch_bounds__(THREADS ? THREADS : kMaxThreads) norm_cta_kernel(const NormParams p) {
+__global__ void __launch_bounds__(THREADS ? THREADS : kMaxThreads) norm_cta_kernel(const ParamsOf<MODE> p) {
   __shared__ BlockSums sums;
   int slot = 0;
   const int64_t row = blockIdx.x;
@@ -251,7 +254,7 @@ __global__ void __launch_bounds__(THREADS ? THREADS : kMaxThreads) norm_cta_kern
 
 // A row per group of `lanes` lanes (32, or fewer if the row has fewer vectors).
 template <typename T, int E, int C, int MODE>
-__global__ void __launch_bounds__(kWarpRowThreads) norm_warp_kernel(const NormParams p, const int lanes) {
+__global__ void __launch_bounds__(kWarpRowThreads) norm_warp_kernel(const ParamsOf<MODE> p, const int lanes) {
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (kWarpRowThreads / lanes) + threadIdx.x / lanes;
   const int vecs = row < p.rows ? static_cast<int>(p.hidden) / E : 0;
   norm_row<T, E, C, MODE>(p, static_cast<const T*>(p.x) + row * p.ld_x, static_cast<T*>(p.out) + row * p.hidden, row,
@@ -263,7 +266,7 @@ __global__ void __launch_bounds__(kWarpRowThreads) norm_warp_kernel(const NormPa
 
 // Rows that no register file holds: a CTA per row, which is read three times.
 template <typename T, int MODE>
-__global__ void __launch_bounds__(kMaxThreads) norm_long_kernel(const NormParams p) {
+__global__ void __launch_bounds__(kMaxThreads) norm_long_kernel(const ParamsOf<MODE> p) {
   __shared__ BlockSums sums;
   int slot = 0;
   const int H = static_cast<int>(p.hidden);
@@ -271,7 +274,8 @@ __global__ void __launch_bounds__(kMaxThreads) norm_long_kernel(const NormParams
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
     const T* x = static_cast<const T*>(p.x) + row * p.ld_x;
     T* y = static_cast<T*>(p.out) + row * p.hidden;
-    const T* res = MODE != kPlain && p.residual ? static_cast<const T*>(p.residual) + row * p.ld_res : nullptr;
+    const T* res = nullptr;
+    if constexpr (MODE != kPlain) res = p.residual ? static_cast<const T*>(p.residual) + row * p.ld_res : nullptr;
     auto at = [&](int i) {
       if constexpr (MODE == kPlain)
         return to_float<T>(x[i]);
@@ -415,11 +419,11 @@ struct Weights {
 // One vector before its row's sums are known: with d = x - mean and
 // g = rstd grad_y w, adds grad_y xhat and grad_y to the columns' sums and g and
 // g d to the row's, and leaves g for after them.
-// (d holds x at first.)
-template <typename T, int E, int NB, bool RMS>
-__device__ __forceinline__ void bwd_visit(const Raw<T, E>& rg, bool weighted, const float (&w)[E],
+template <typename T, int E, int NB, bool RMS, typename X>
+__device__ __forceinline__ void bwd_visit(const X& rx, const Raw<T, E>& rg, bool weighted, const float (&w)[E],
                                           float mean, float rstd, float (&d)[E], float (&g)[E], float (&acc_w)[E], float (&acc_b)[E],
                                           float& sg, float& sgd) {
+  unpack<T, E>(rx, d);
   unpack<T, E>(rg, g);
 #pragma unroll
   for (int e = 0; e < E; ++e) {
@@ -471,7 +475,7 @@ struct BwdRow {
   static constexpr bool RING = kRing<T, E>, KEEP = C == 1, ADD = MODE != kPlain, X8 = MODE == kAdd8;
   static constexpr int A = ring_arrays(MODE);  // arrays in the ring: x, grad_y, grad_sum
   static constexpr bool CODES_IN_RING = RING && E >= 4;  // X8: single codes are too short for a copy
-  const NormParams& p;
+  const ParamsOf<MODE>& p;
   Place pl;
   int t, stride, threads;  // first vector, distance between vectors, distance in the ring
   Raw<T, E>* ring;
@@ -482,7 +486,7 @@ struct BwdRow {
   uint8_t next_scale[X8 ? C : 1], next_code[X8 && !CODES_IN_RING ? C : 1];
   float acc_w[C][E], acc_b[C][E];
 
-  __device__ __forceinline__ BwdRow(const NormParams& params, const Place& place, int first, int apart, int ring_apart,
+  __device__ __forceinline__ BwdRow(const ParamsOf<MODE>& params, const Place& place, int first, int apart, int ring_apart,
                                     Raw<T, E>* r, const Weights<E>& w)
       : p(params), pl(place), t(first), stride(apart), threads(ring_apart), ring(r), weights(w) {
 #pragma unroll
@@ -501,7 +505,12 @@ struct BwdRow {
     if (row < p.rows) {
       const T* xr = X8 ? nullptr : static_cast<const T*>(p.x) + row * p.ld_x + (t * E - pl.off);
       const T* gr = static_cast<const T*>(p.gy) + row * p.ld_gy + (t * E - pl.off);
-      const T* sr = ADD && p.gs ? static_cast<const T*>(p.gs) + row * p.ld_gs + (t * E - pl.off) : nullptr;
+      const T* sr = nullptr;
+      int64_t ld_gs = 0;
+      if constexpr (ADD) {
+        ld_gs = p.ld_gs;
+        if (p.gs) sr = static_cast<const T*>(p.gs) + row * ld_gs + (t * E - pl.off);
+      }
       Raw<T, E>* to = ring + stage * A * C * threads;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
@@ -517,7 +526,7 @@ struct BwdRow {
           }
           if constexpr (RING) {
             if (is_inside(c) || (in_matrix<E>(pl, row, p.ld_x, p.rows, v) && in_matrix<E>(pl, row, p.ld_gy, p.rows, v) &&
-                                 (!ADD || !sr || in_matrix<E>(pl, row, p.ld_gs, p.rows, v)))) {
+                                 (!ADD || !sr || in_matrix<E>(pl, row, ld_gs, p.rows, v)))) {
               if constexpr (!X8) copy_async<sizeof(T) * E>(to + c * threads, xr + c * stride * E);
               copy_async<sizeof(T) * E>(to + (C + c) * threads, gr + c * stride * E);
               if (ADD && sr) copy_async<sizeof(T) * E>(to + (2 * C + c) * threads, sr + c * stride * E);
@@ -548,21 +557,22 @@ struct BwdRow {
     }
   }
 
-  // x of vector c of the row in `stage`.
-  __device__ __forceinline__ void take_x(int stage, int c, const Raw<T, E>& held, uint8_t code, uint8_t scale,
-                                         float (&v)[E]) const {
+  // x of vector c of the row in `stage`, as it is held.
+  __device__ __forceinline__ std::conditional_t<X8, CodeVector<E>, Raw<T, E>> take_x(int stage, int c, const Raw<T, E>& held, uint8_t code,
+                                                                                   uint8_t scale) const {
     if constexpr (!X8) {
-      unpack<T, E>(take(stage, 0, c, held), v);
+      return take(stage, 0, c, held);
     } else {
-      uint32_t words[E == 8 ? 2 : 1];
+      CodeVector<E> r;
       if constexpr (CODES_IN_RING) {
         const uint32_t* from = reinterpret_cast<const uint32_t*>(ring + stage * A * C * threads + c * threads);
 #pragma unroll
-        for (int i = 0; i < E / 4; ++i) words[i] = from[i];
+        for (int i = 0; i < E / 4; ++i) r.words[i] = from[i];
       } else {
-        words[0] = code;
+        r.words[0] = code;
       }
-      read_codes<E>(words, scale_value(scale), v);
+      r.scale = scale_value(scale);
+      return r;
     }
   }
 
@@ -611,9 +621,8 @@ struct BwdRow {
           weights.get(c, w);
         else if (p.weight)
           load_weight<E>(p.weight, p.w_f32 != 0, (t + c * stride) * E, w);
-        take_x(stage, c, hx[RING ? 0 : c], code[X8 ? c : 0], scale[X8 ? c : 0], d[KEEP ? c : 0]);
-        bwd_visit<T, E, NB, RMS>(take(stage, 1, c, hg[RING ? 0 : c]),
-                                 SHIFT || p.weight != nullptr, w, mean, rstd,
+        bwd_visit<T, E, NB, RMS>(take_x(stage, c, hx[RING ? 0 : c], code[X8 ? c : 0], scale[X8 ? c : 0]),
+                                 take(stage, 1, c, hg[RING ? 0 : c]), SHIFT || p.weight != nullptr, w, mean, rstd,
                                  d[KEEP ? c : 0], g[c], acc_w[c], acc_b[c], sg, sgd);
       }
     }
@@ -626,7 +635,7 @@ struct BwdRow {
       for (int c = 0; c < C; ++c) {
         if (t + c * stride < vecs) {
           if (!KEEP) {
-            take_x(stage, c, hx[RING ? 0 : c], code[X8 ? c : 0], scale[X8 ? c : 0], d[0]);
+            unpack<T, E>(take_x(stage, c, hx[RING ? 0 : c], code[X8 ? c : 0], scale[X8 ? c : 0]), d[0]);
             if (!RMS) {
 #pragma unroll
               for (int e = 0; e < E; ++e) d[0][e] -= mean;
@@ -668,7 +677,7 @@ struct BwdRow {
 // its threads keep their columns. REGS: with 72 registers two CTAs of up to 448
 // threads share an SM (a row of 7168 bf16 elements).
 template <typename T, int E, int C, int NB, int REGS, bool RMS, bool SHIFT, int MODE>
-__global__ void __maxnreg__(REGS) norm_bwd_cta_kernel(const NormParams p, const int stages) {
+__global__ void __maxnreg__(REGS) norm_bwd_cta_kernel(const ParamsOf<MODE> p, const int stages) {
   constexpr bool RING = kRing<T, E>;
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ BlockSums sums;
@@ -705,7 +714,7 @@ __global__ void __maxnreg__(REGS) norm_bwd_cta_kernel(const NormParams p, const 
 // sums, in order. A group's rows are a multiple of eight apart, too.
 template <typename T, int E, int NB, bool RMS, bool SHIFT, int MODE>
 __global__ void __launch_bounds__(kWarpRowThreads)
-    norm_bwd_warp_kernel(const NormParams p, const int lanes, const int stages) {
+    norm_bwd_warp_kernel(const ParamsOf<MODE> p, const int lanes, const int stages) {
   constexpr bool RING = kRing<T, E>;
   constexpr int C = 1;  // vectors per lane
   extern __shared__ __align__(16) uint8_t dyn[];
@@ -754,7 +763,7 @@ __global__ void __launch_bounds__(kWarpRowThreads)
 
 // Element i of a row's x, from the matrix or from its checkpoint.
 template <typename T, int MODE>
-__device__ __forceinline__ float bwd_x(const NormParams& p, int64_t row, int64_t i) {
+__device__ __forceinline__ float bwd_x(const ParamsOf<MODE>& p, int64_t row, int64_t i) {
   if constexpr (MODE != kAdd8) {
     return to_float<T>(static_cast<const T*>(p.x)[row * p.ld_x + i]);
   } else {
@@ -767,7 +776,7 @@ __device__ __forceinline__ float bwd_x(const NormParams& p, int64_t row, int64_t
 
 // Long rows: grad_x by a CTA per row in two passes through the L2.
 template <typename T, int MODE>
-__global__ void __launch_bounds__(kMaxThreads) norm_bwd_long_kernel(const NormParams p) {
+__global__ void __launch_bounds__(kMaxThreads) norm_bwd_long_kernel(const ParamsOf<MODE> p) {
   __shared__ BlockSums sums;
   int slot = 0;
   const int H = static_cast<int>(p.hidden);
@@ -798,7 +807,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_long_kernel(const NormPa
 
 // Long rows: the partial sums of row group blockIdx.y, a thread per column.
 template <typename T, int MODE>
-__global__ void __launch_bounds__(256) norm_bwd_long_cols_kernel(const NormParams p, const int64_t group) {
+__global__ void __launch_bounds__(256) norm_bwd_long_cols_kernel(const ParamsOf<MODE> p, const int64_t group) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   if (i >= p.hidden) return;
   const T* gy = static_cast<const T*>(p.gy);
@@ -821,9 +830,12 @@ inline bool aligned(const void* p, int64_t ld, size_t es) {
 bool vectors(const NormParams& p) {
   const size_t es = p.dtype == FLCE_DTYPE_F32 ? 4 : 2;
   return aligned(p.x, p.ld_x, es) && aligned(p.gy, p.ld_gy, es) && aligned(p.out, p.hidden, es) &&
-         aligned(p.residual, p.ld_res, es) && aligned(p.gs, p.ld_gs, es) && aligned(p.sum, p.hidden, es) &&
-         reinterpret_cast<uintptr_t>(p.codes) % (16 / es) == 0 &&
          p.hidden % (16 / es) == 0 && aligned(p.weight, 0, 1) && aligned(p.bias, 0, 1);
+}
+inline bool vectors(const AddNormParams& p) {
+  const size_t es = p.dtype == FLCE_DTYPE_F32 ? 4 : 2;
+  return vectors(static_cast<const NormParams&>(p)) && aligned(p.residual, p.ld_res, es) && aligned(p.gs, p.ld_gs, es) &&
+         aligned(p.sum, p.hidden, es) && reinterpret_cast<uintptr_t>(p.codes) % (16 / es) == 0;
 }
 
 // Whether a row starts at the same distance from a 16-byte boundary in x, grad_y
@@ -832,8 +844,12 @@ bool in_step(const NormParams& p) {
   const int64_t es = p.dtype == FLCE_DTYPE_F32 ? 4 : 2, E = 16 / es;
   const uintptr_t x = reinterpret_cast<uintptr_t>(p.x) % 16;
   return p.hidden >= 2 * E && (p.ld_x - p.hidden) % E == 0 && (p.ld_gy - p.hidden) % E == 0 &&
-         reinterpret_cast<uintptr_t>(p.gy) % 16 == x && (!p.out || reinterpret_cast<uintptr_t>(p.out) % 16 == x) &&
-         (!p.gs || ((p.ld_gs - p.hidden) % E == 0 && reinterpret_cast<uintptr_t>(p.gs) % 16 == x));
+         reinterpret_cast<uintptr_t>(p.gy) % 16 == x && (!p.out || reinterpret_cast<uintptr_t>(p.out) % 16 == x);
+}
+inline bool in_step(const AddNormParams& p) {
+  const int64_t E = p.dtype == FLCE_DTYPE_F32 ? 4 : 8;
+  return in_step(static_cast<const NormParams&>(p)) &&
+         (!p.gs || ((p.ld_gs - p.hidden) % E == 0 && reinterpret_cast<uintptr_t>(p.gs) % 16 == reinterpret_cast<uintptr_t>(p.x) % 16));
 }
 
 inline unsigned grid_of(int64_t want, int64_t most) { return static_cast<unsigned>(want < most ? want : most); }
@@ -847,7 +863,7 @@ inline int lanes_for(int64_t vecs) {
 
 // C vectors for each of THREADS threads (0: `threads`), in steps of STEP.
 template <typename T, int E, int THREADS, int STEP, int MOST, int MODE, int C = STEP>
-cudaError_t run_fwd_cta(const NormParams& p, int64_t c, int threads, cudaStream_t s) {
+cudaError_t run_fwd_cta(const ParamsOf<MODE>& p, int64_t c, int threads, cudaStream_t s) {
   if constexpr (C < MOST)
     if (c > C) return run_fwd_cta<T, E, THREADS, STEP, MOST, MODE, C + STEP>(p, c, threads, s);
   norm_cta_kernel<T, E, C, THREADS, MODE><<<static_cast<unsigned>(p.rows), threads, 0, s>>>(p);
@@ -855,7 +871,7 @@ cudaError_t run_fwd_cta(const NormParams& p, int64_t c, int threads, cudaStream_
 }
 
 template <typename T, int E, int MODE>
-cudaError_t run_fwd(const NormParams& p, int sms, cudaStream_t s) {
+cudaError_t run_fwd(const ParamsOf<MODE>& p, int sms, cudaStream_t s) {
   const int64_t vecs = p.hidden / E;
   if (vecs <= 32 * (E == 1 ? 16 : 4)) {
     const int lanes = lanes_for(vecs);
@@ -920,7 +936,7 @@ cudaError_t launch_large(K k, std::atomic<uint64_t>& done, unsigned grid, int th
 inline int64_t most_vecs(int64_t hidden, int E, bool shift) { return shift ? (hidden + 2 * E - 2) / E : hidden / E; }
 
 template <typename T, int E, int NB, bool RMS, bool SHIFT, int MODE>
-cudaError_t run_bwd_warp(const NormParams& p, int64_t vecs, int sms, int* partials, cudaStream_t s) {
+cudaError_t run_bwd_warp(const ParamsOf<MODE>& p, int64_t vecs, int sms, int* partials, cudaStream_t s) {
   const int lanes = lanes_for(vecs);
   const int64_t groups = kWarpRowThreads / lanes;
   // one vector per lane: three rows ahead are few registers and little shared memory
@@ -936,7 +952,7 @@ cudaError_t run_bwd_warp(const NormParams& p, int64_t vecs, int sms, int* partia
 }
 
 template <typename T, int E, int C, int REGS, int NB, bool RMS, bool SHIFT, int MODE>
-cudaError_t run_bwd_cta(const NormParams& p, int64_t vecs, int sms, int* partials, cudaStream_t s) {
+cudaError_t run_bwd_cta(const ParamsOf<MODE>& p, int64_t vecs, int sms, int* partials, cudaStream_t s) {
   const int threads = static_cast<int>(((vecs + C - 1) / C + 31) / 32 * 32);
   int ctas = 65536 / (REGS * threads);
   if (ctas > bwd_ctas(p.hidden)) ctas = bwd_ctas(p.hidden);
@@ -954,7 +970,7 @@ cudaError_t run_bwd_cta(const NormParams& p, int64_t vecs, int sms, int* partial
 }
 
 template <typename T, int E, int NB, bool RMS, bool SHIFT, int MODE>
-cudaError_t run_bwd_row(const NormParams& p, int sms, int* partials, cudaStream_t s) {
+cudaError_t run_bwd_row(const ParamsOf<MODE>& p, int sms, int* partials, cudaStream_t s) {
   const int64_t vecs = most_vecs(p.hidden, E, SHIFT);
   if (vecs <= 32) return run_bwd_warp<T, E, NB, RMS, SHIFT, MODE>(p, vecs, sms, partials, s);
   // (Rows of up to four vectors per lane on a warp: 32768 x 1024 bf16 RMS 48 us so, 54
@@ -974,7 +990,7 @@ cudaError_t run_bwd_row(const NormParams& p, int sms, int* partials, cudaStream_
 }
 
 template <typename T, int E, bool SHIFT, int MODE>
-cudaError_t run_bwd(const NormParams& p, int sms, int* partials, cudaStream_t s) {
+cudaError_t run_bwd(const ParamsOf<MODE>& p, int sms, int* partials, cudaStream_t s) {
   if (most_vecs(p.hidden, E, SHIFT) <= static_cast<int64_t>(kMaxThreads) * cta_vecs(E)) {
     if (p.part_b)
       return p.rms ? run_bwd_row<T, E, 2, true, SHIFT, MODE>(p, sms, partials, s) : run_bwd_row<T, E, 2, false, SHIFT, MODE>(p, sms, partials, s);
@@ -994,7 +1010,7 @@ cudaError_t run_bwd(const NormParams& p, int sms, int* partials, cudaStream_t s)
 }
 
 template <typename T, int E, int MODE>
-cudaError_t launch_bwd(const NormParams& p, int sms, int* partials, cudaStream_t s) {
+cudaError_t launch_bwd(const ParamsOf<MODE>& p, int sms, int* partials, cudaStream_t s) {
   if (vectors(p)) return run_bwd<T, E, false, MODE>(p, sms, partials, s);
   if constexpr (MODE != kAdd8)
     if (in_step(p)) return run_bwd<T, E, true, MODE>(p, sms, partials, s);

@@ -40,10 +40,12 @@
 #include <math.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "flce_device.cuh"
 #include "head_device.cuh"
 #include "head_internal.h"
+#include "model_internal.h"
 
 namespace flce {
 
@@ -94,6 +96,10 @@ struct Counts {
 struct Answer {
   uint32_t lo[kAnswerBins], hi[kAnswerBins];
 };
+
+// CUTS: no token is drawn; what the filters keep of each row goes to p.cuts.
+template <bool CUTS>
+using ParamsOf = std::conditional_t<CUTS, VerifyParams, SampleParams>;
 
 // Shared memory of a CTA in front of its slice of the row; the same place in
 // every CTA of the cluster.
@@ -445,7 +451,7 @@ __device__ __forceinline__ float reciprocal(uint64_t whole) {
 // The row's kept set (CUTS), by one thread: all logits up to `last` in rank order, of at
 // least min_p.
 template <typename T, int kThreads>
-__device__ __forceinline__ void write_cut(const Row<T, kThreads>& row, const SampleParams& p, int64_t r, uint64_t last, uint64_t whole) {
+__device__ __forceinline__ void write_cut(const Row<T, kThreads>& row, const VerifyParams& p, int64_t r, uint64_t last, uint64_t whole) {
   p.cuts[r] = {last, whole, row.top, row.inv, row.min_p, reciprocal(whole)};
 }
 
@@ -694,7 +700,7 @@ __device__ bool select(const Row<T, kThreads>& row, Shared& s, int& buf, uint32_
 
 // The token by the general selection.
 template <typename T, int kThreads, bool MULTI, bool CUTS>
-__device__ void general_answer(const Row<T, kThreads>& row, Shared& s, const SampleParams& p, int64_t r, int64_t top_k,
+__device__ void general_answer(const Row<T, kThreads>& row, Shared& s, const ParamsOf<CUTS>& p, int64_t r, int64_t top_k,
                                float top_p, float u) {
   constexpr int E = Row<T, kThreads>::E, kWarps = kThreads / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -853,7 +859,7 @@ __device__ void general_answer(const Row<T, kThreads>& row, Shared& s, const Sam
 // rank. An entry's rank and what lies before it come from comparing it with all
 // the others, in rank order and again in index order: few barriers, no sort.
 template <typename T, int kThreads, bool CUTS>
-__device__ void short_list_answer(const Row<T, kThreads>& row, Shared& s, const SampleParams& p, int64_t r, int n, int64_t top_k,
+__device__ void short_list_answer(const Row<T, kThreads>& row, Shared& s, const ParamsOf<CUTS>& p, int64_t r, int n, int64_t top_k,
                                   float top_p, float u) {
   uint64_t* weights = reinterpret_cast<uint64_t*>(&s.hist[0]);
   static_assert(sizeof(s.hist) >= kShort * sizeof(uint64_t), "weights in the histograms' place");
@@ -942,7 +948,7 @@ __device__ uint64_t answer_bin(Shared& s, float u, uint64_t* whole) {
 
 // The same for a long list.
 template <typename T, int kThreads, bool CUTS>
-__device__ void list_answer(const Row<T, kThreads>& row, Shared& s, const SampleParams& p, int64_t r, int n, int64_t top_k,
+__device__ void list_answer(const Row<T, kThreads>& row, Shared& s, const ParamsOf<CUTS>& p, int64_t r, int n, int64_t top_k,
                             float top_p, float u, float x_hi) {
   const uint64_t lo = list_entry(row.top, 0), hi = list_entry(x_hi, ~0u);
   uint64_t last = ~0ull;  // last entry that the filters by rank keep
@@ -1093,7 +1099,7 @@ __device__ void sum_segments(const Row<T, kThreads>& row, Shared& s, float x_lo,
 // list (n entries) with the segments and walks the segment of the answer.
 // Returns false if the exact sums do not confirm that the prefix ends in the list.
 template <typename T, int kThreads, bool MULTI, bool CUTS>
-__device__ bool segment_answer(const Row<T, kThreads>& row, Shared& s, const SampleParams& p, int64_t r, int slice, float top_p,
+__device__ bool segment_answer(const Row<T, kThreads>& row, Shared& s, const ParamsOf<CUTS>& p, int64_t r, int slice, float top_p,
                                float u, bool cut, float x_lo, float x_hi) {
   constexpr int E = Row<T, kThreads>::E;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1206,7 +1212,7 @@ __device__ bool segment_answer(const Row<T, kThreads>& row, Shared& s, const Sam
 // Verification: row r's first logit, its request, whose settings it has, and its place; rows of the
 // target come first, then those of the draft. False if it lies behind the request's last draft.
 template <typename T>
-__device__ __forceinline__ bool verify_row(const SampleParams& p, uint32_t r, const T** start, int64_t* request, int* at_place) {
+__device__ __forceinline__ bool verify_row(const VerifyParams& p, uint32_t r, const T** start, int64_t* request, int* at_place) {
   const uint32_t target_rows = static_cast<uint32_t>(p.target_rows);
   const bool target = r < target_rows;
   const uint32_t at = target ? r : r - target_rows, per = static_cast<uint32_t>(p.drafts) + (target ? 1 : 0);
@@ -1224,9 +1230,8 @@ __device__ __forceinline__ bool verify_row(const SampleParams& p, uint32_t r, co
 }
 
 // ---------------------------------------------------------------- the kernel
-// CUTS: no token is drawn; what the filters keep of each row goes to p.cuts.
 template <typename T, int kThreads, bool MULTI, bool CUTS>
-__global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const SampleParams p, const int slice, const int in_smem) {
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const ParamsOf<CUTS> p, const int slice, const int in_smem) {
   extern __shared__ __align__(16) uint8_t dyn[];
   Shared& s = *reinterpret_cast<Shared*>(dyn);
   T* kept = reinterpret_cast<T*>(dyn + (sizeof(Shared) + 15) / 16 * 16);
@@ -1243,13 +1248,12 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
   }
   const int64_t r = blockIdx.x / row.ctas;
   const int vocab = static_cast<int>(p.vocab);
-  int64_t setting = r;
-  const T* start = static_cast<const T*>(p.x) + r * p.ld;
+  int64_t request = 0;
+  const T* start = nullptr;
   if constexpr (CUTS) {
     int place;
-    const bool used = verify_row(p, static_cast<uint32_t>(r), &start, &setting, &place);
     // rows behind a request's last draft are not looked at
-    if (!used) {
+    if (!verify_row(p, static_cast<uint32_t>(r), &start, &request, &place)) {
       if constexpr (MULTI) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
       return;
     }
@@ -1257,15 +1261,19 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
   row.c0 = static_cast<int>(row.rank) * slice;
   row.n = max(0, min(slice, vocab - row.c0));
   row.vecs = (row.n + E - 1) / E;
-  row.data = start + row.c0;
+  if constexpr (CUTS)
+    row.data = start + row.c0;
+  else
+    row.data = static_cast<const T*>(p.x) + r * p.ld + row.c0;
   row.padded = false;
   row.aligned = reinterpret_cast<uintptr_t>(row.data) % 16 == 0;
 
-  const float temperature = p.temperatures ? p.temperatures[setting] : p.temperature;
-  const int64_t top_k = p.top_ks ? p.top_ks[setting] : p.top_k;
-  const float top_p = p.top_ps ? p.top_ps[setting] : p.top_p;
+  const int64_t own = CUTS ? request : r;  // whose settings
+  const float temperature = p.temperatures ? p.temperatures[own] : p.temperature;
+  const int64_t top_k = p.top_ks ? p.top_ks[own] : p.top_k;
+  const float top_p = p.top_ps ? p.top_ps[own] : p.top_p;
   const float u = CUTS ? 0.f : p.u[r];
-  row.min_p = p.min_ps ? p.min_ps[setting] : p.min_p;
+  row.min_p = p.min_ps ? p.min_ps[own] : p.min_p;
   // (a reciprocal of zero would make NaN of a logit of -infinity)
   row.inv = fmaxf(1.f / temperature, kLeast);
   row.per_place = fmaxf(fminf(row.inv * (1.f / kPlaces), 3e38f), kLeast);
@@ -1544,7 +1552,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
 }
 
 template <typename T, int kThreads, bool MULTI, bool CUTS>
-cudaError_t run(const SampleParams& p, int ctas, cudaStream_t s) {
+cudaError_t run(const ParamsOf<CUTS>& p, int ctas, cudaStream_t s) {
   constexpr size_t shared = (sizeof(Shared) + 15) / 16 * 16, most = kMostShared / (1024 / kThreads) / 1024 * 1024;
   static_assert(shared <= most, "two CTAs of half the threads share an SM");
   const int slice = static_cast<int>(((p.vocab + ctas - 1) / ctas + 63) / 64 * 64);
@@ -1574,7 +1582,7 @@ cudaError_t run(const SampleParams& p, int ctas, cudaStream_t s) {
 }
 
 template <typename T, bool CUTS>
-cudaError_t run_typed(const SampleParams& p, int sms, cudaStream_t s) {
+cudaError_t run_typed(const ParamsOf<CUTS>& p, int sms, cudaStream_t s) {
   // One CTA per row where that occupies half of the SMs or more; fewer rows
   // are spread over clusters, down to 4096 logits per CTA. More rows than SMs
   // run two to an SM, so that one row's short phases, which wait on barriers, run

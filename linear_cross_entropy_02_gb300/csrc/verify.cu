@@ -140,7 +140,7 @@ struct Progress {
 
 // What the writer of row (request, place)'s cut does then.
 template <typename T>
-__device__ void row_is_summed(const SampleParams& p, const Progress& progress, int64_t request, int place) {
+__device__ void row_is_summed(const VerifyParams& p, const Progress& progress, int64_t request, int place) {
   if (place >= p.drafts) return;
   __threadfence();
   if (atomicAdd(&progress.rows[request * p.drafts + place], 1u) + 1 < (p.draft ? 2u : 1u)) return;
@@ -173,7 +173,7 @@ struct PlainShared {
 };
 
 template <typename T, int kPlainThreads>
-__global__ void __launch_bounds__(kPlainThreads, 1024 / kPlainThreads) verify_plain_kernel(const SampleParams p, const int slice, const Progress progress) {
+__global__ void __launch_bounds__(kPlainThreads, 1024 / kPlainThreads) verify_plain_kernel(const VerifyParams p, const int slice, const Progress progress) {
   __shared__ PlainShared s;
   constexpr int E = 16 / sizeof(T);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -292,14 +292,14 @@ constexpr int64_t plain_slice(int threads) {
 
 // Whether no row has a filter, as far as the host knows, and a cluster's registers hold one.
 template <typename T>
-bool plain_rows(const SampleParams& p) {
+bool plain_rows(const VerifyParams& p) {
   if (p.temperatures || p.top_ks || p.top_ps || p.min_ps) return false;
   if (!(p.temperature > 0.f) || 1.f / p.temperature > 3e38f || p.top_p < 1.f || p.min_p > 0.f) return false;
   return (p.top_k <= 0 || p.top_k >= p.vocab) && p.vocab <= kMaxCluster * plain_slice<T>(512);
 }
 
 template <typename T, int kPlainThreads>
-cudaError_t run_plain(const SampleParams& p, int sms, cudaStream_t s) {
+cudaError_t run_plain(const VerifyParams& p, int sms, cudaStream_t s) {
   // few rows are spread further, down to 4096 logits per CTA
   int ctas = 1;
   while (ctas * plain_slice<T>(kPlainThreads) < p.vocab ||
@@ -328,13 +328,13 @@ cudaError_t run_plain(const SampleParams& p, int sms, cudaStream_t s) {
 
 // Smaller CTAs, four on an SM, where eight of them hold a row: 704 rows of 129280 bf16 74 us, 78 with the larger ones.
 template <typename T>
-cudaError_t run_plain_typed(const SampleParams& p, int sms, cudaStream_t s) {
+cudaError_t run_plain_typed(const VerifyParams& p, int sms, cudaStream_t s) {
   return p.vocab <= kMaxCluster * plain_slice<T>(256) ? run_plain<T, 256>(p, sms, s) : run_plain<T, 512>(p, sms, s);
 }
 
 // ---------------------------------------------------------------- a request
 template <typename T, bool MULTI>
-__global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const SampleParams p, int64_t* accepted, const int slice) {
+__global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyParams p, int64_t* accepted, const int slice) {
   __shared__ VerifyShared s;
   constexpr int E = 16 / sizeof(T);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -560,7 +560,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const SampleP
 }
 
 template <typename T, bool MULTI>
-cudaError_t run_verify(const SampleParams& p, int64_t batch, int64_t* accepted, int ctas, cudaStream_t s) {
+cudaError_t run_verify(const VerifyParams& p, int64_t batch, int64_t* accepted, int ctas, cudaStream_t s) {
   const int slice = static_cast<int>(((p.vocab + ctas - 1) / ctas + 63) / 64 * 64);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(batch * ctas));
@@ -576,7 +576,7 @@ cudaError_t run_verify(const SampleParams& p, int64_t batch, int64_t* accepted, 
 }
 
 template <typename T>
-cudaError_t run_verify_typed(const SampleParams& p, int64_t batch, int64_t* accepted, int sms, cudaStream_t s) {
+cudaError_t run_verify_typed(const VerifyParams& p, int64_t batch, int64_t* accepted, int sms, cudaStream_t s) {
   int ctas = 1;
   while (ctas < kMaxCluster && batch * ctas * 2 <= 2LL * sms && p.vocab / ctas > 4096) ctas *= 2;
   return ctas > 1 ? run_verify<T, true>(p, batch, accepted, ctas, s) : run_verify<T, false>(p, batch, accepted, 1, s);
@@ -584,12 +584,12 @@ cudaError_t run_verify_typed(const SampleParams& p, int64_t batch, int64_t* acce
 
 }  // namespace
 
-cudaError_t launch_verify_cuts(const SampleParams& p, int sms, cudaStream_t s) {
+cudaError_t launch_verify_cuts(const VerifyParams& p, int sms, cudaStream_t s) {
   if (p.dtype == FLCE_DTYPE_F32) return plain_rows<float>(p) ? run_plain_typed<float>(p, sms, s) : run_typed<float, true>(p, sms, s);
   return plain_rows<uint16_t>(p) ? run_plain_typed<uint16_t>(p, sms, s) : run_typed<uint16_t, true>(p, sms, s);
 }
 
-cudaError_t launch_verify(const SampleParams& p, int64_t batch, int64_t* accepted, int sms, cudaStream_t s) {
+cudaError_t launch_verify(const VerifyParams& p, int64_t batch, int64_t* accepted, int sms, cudaStream_t s) {
   return p.dtype == FLCE_DTYPE_F32 ? run_verify_typed<float>(p, batch, accepted, sms, s) : run_verify_typed<uint16_t>(p, batch, accepted, sms, s);
 }
 
