@@ -217,15 +217,33 @@ cudaError_t run_add_bwd_as(const AddNormParams& p, int sms, int* partials, cudaS
 template <typename T, typename W, bool X8>
 cudaError_t run_add_bwd(const AddNormParams& p, int sms, int* partials, cudaStream_t s) {
   constexpr int C = sizeof(T);  // 16 columns per thread
-  // (Microseconds for 32768 rows, from 8 bits: 7168 RMS without holding 317, held 316, with 32
-  // columns 295; 4096 178 and 181. With a bias' sums 7168 held 394, not 376; from the sum 353 and 374.)
+  // (Microseconds for 32768 rows of bf16 from 8 bits: 7168 RMS with 16 columns held 316, not 317, with 32 held
+  // 304, and with 144 registers, where they cost no CTA, 296; 5120 at 128 registers 208, at 144, with a CTA less, 246.
+  // With a bias' sums 7168 held 394, not 376; from the sum 353 and 374. 8192 x 7168 fp32 with 32 columns 166,
+  // with 16 126.)
+  const int64_t hidden = p.hidden;
   if (p.part_b) {
-    if (p.rms) return run_add_bwd_as<T, W, 2, true, X8, !X8, C, 72>(p, sms, partials, s);
-    return run_add_bwd_as<T, W, 2, false, X8, !X8, C, 72>(p, sms, partials, s);
+    // (of 8192 columns two CTAs fit with 64 registers only: 16384 rows 249 us, 270 with one)
+    if (hidden / 16 * 72 * 2 > 65536)
+      return p.rms ? run_add_bwd_as<T, W, 2, true, X8, !X8, C, 64>(p, sms, partials, s)
+                   : run_add_bwd_as<T, W, 2, false, X8, !X8, C, 64>(p, sms, partials, s);
+    return p.rms ? run_add_bwd_as<T, W, 2, true, X8, !X8, C, 72>(p, sms, partials, s)
+                 : run_add_bwd_as<T, W, 2, false, X8, !X8, C, 72>(p, sms, partials, s);
   }
-  if (!p.rms) return run_add_bwd_as<T, W, 1, false, X8, true, C, 72>(p, sms, partials, s);
-  if (p.hidden > 4096 && p.hidden % (2 * kWideStep) == 0) return run_add_bwd_as<T, W, 1, true, X8, true, 2 * C, 144>(p, sms, partials, s);
-  return run_add_bwd_as<T, W, 1, true, X8, true, C, 72>(p, sms, partials, s);
+  if constexpr (sizeof(T) == 2) {
+    if (hidden > 4096 && hidden % (2 * kWideStep) == 0) {
+      if (65536 / (144 * (hidden / 32)) == 65536 / (128 * (hidden / 32)))
+        return p.rms ? run_add_bwd_as<T, W, 1, true, X8, true, 2 * C, 144>(p, sms, partials, s)
+                     : run_add_bwd_as<T, W, 1, false, X8, true, 2 * C, 144>(p, sms, partials, s);
+      return p.rms ? run_add_bwd_as<T, W, 1, true, X8, true, 2 * C, 128>(p, sms, partials, s)
+                   : run_add_bwd_as<T, W, 1, false, X8, true, 2 * C, 128>(p, sms, partials, s);
+    }
+  }
+  if (hidden / 16 * 72 * 2 > 65536)
+    return p.rms ? run_add_bwd_as<T, W, 1, true, X8, true, C, 64>(p, sms, partials, s)
+                 : run_add_bwd_as<T, W, 1, false, X8, true, C, 64>(p, sms, partials, s);
+  return p.rms ? run_add_bwd_as<T, W, 1, true, X8, true, C, 72>(p, sms, partials, s)
+               : run_add_bwd_as<T, W, 1, false, X8, true, C, 72>(p, sms, partials, s);
 }
 
 // Whether rows are for these kernels. (Shorter ones were slower: 65536 x 1024 RMS from 8 bits 153 us, 112 by
