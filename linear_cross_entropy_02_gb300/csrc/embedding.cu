@@ -28,10 +28,13 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kUnroll = 4;
 constexpr int kChunk = 1024;       // keys sorted by a CTA
-constexpr int kSortThreads = 512;
 constexpr int kMostShared = 48;    // chunks that shared memory holds
-constexpr int kSharedThreads = 256;
+constexpr int kSharedThreads = 512;
 constexpr int kGradThreads = 128;
+constexpr int kJoinWarps = 8;
+constexpr int kJoinCtas = 1216;    // for short runs, at least: eight per SM
+constexpr int kLongRuns = 8;       // at a time
+constexpr int kShortRun = 16;      // tiles
 constexpr int kTile = kEmbeddingTile;
 constexpr int kBatch = 8;          // rows of a tile in flight
 constexpr int kZeroFloats = 65536; // of absent rows per CTA, about
@@ -86,36 +89,40 @@ __global__ void __launch_bounds__(kThreads) embedding_kernel(const EmbeddingPara
 }
 
 // ------------------------------------------------------------------ sort
-// Sorts kChunk (token, position) keys of the CTA's piece; tokens outside of the
-// vocabulary count as `vocab` and come last.
-__global__ void __launch_bounds__(kSortThreads) embedding_chunk_kernel(const int64_t* tokens, const int64_t rows, const int64_t vocab,
-                                                                     uint32_t* sorted, uint32_t* places) {
-  __shared__ uint64_t key[kChunk];
-  const int64_t base = static_cast<int64_t>(blockIdx.x) * kChunk;
-  for (int i = threadIdx.x; i < kChunk; i += kSortThreads) {
-    uint64_t k = ~0ull;  // behind the last row
-    if (base + i < rows) {
-      const int64_t t = __ldg(tokens + base + i);
-      k = static_cast<uint64_t>(t >= 0 && t < vocab ? t : vocab) << 32 | static_cast<uint32_t>(base + i);
-    }
-    key[i] = k;
+// Sorts kChunk (token, position) keys of the CTA's piece, one in each thread; tokens outside
+// of the vocabulary count as `vocab` and come last. (A bitonic sort; most of its exchanges are within
+// a warp. With two keys per thread, all of them through shared memory, it took 10 us, so 4.)
+// Also empties the lists of runs to join.
+__global__ void __launch_bounds__(kChunk) embedding_chunk_kernel(const int64_t* tokens, const int64_t rows, const int64_t vocab,
+                                                               uint32_t* sorted, uint32_t* places, uint32_t* joins) {
+  __shared__ uint64_t other[kChunk];
+  const int t = threadIdx.x;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kChunk + t;
+  uint64_t key = ~0ull;  // behind the last row
+  if (i < rows) {
+    const int64_t token = __ldg(tokens + i);
+    key = static_cast<uint64_t>(token >= 0 && token < vocab ? token : vocab) << 32 | static_cast<uint32_t>(i);
   }
-  __syncthreads();
-  // bitonic: runs of `run` are merged into runs of twice that, up and down in turn
+  if (i < 2) joins[i] = 0;
+  // runs of `run` are merged into runs of twice that, up and down in turn
   for (int run = 2; run <= kChunk; run *= 2) {
     for (int step = run / 2; step > 0; step /= 2) {
-      const int i = 2 * threadIdx.x - (threadIdx.x & (step - 1));  // the pair's first
-      const uint64_t a = key[i], b = key[i + step];
-      if ((a > b) == ((i & run) == 0)) {
-        key[i] = b;
-        key[i + step] = a;
+      uint64_t o;
+      if (step >= 32) {
+        other[t] = key;
+        __syncthreads();
+        o = other[t ^ step];
+        __syncthreads();
+      } else {
+        o = __shfl_xor_sync(0xffffffffu, key, step);
       }
-      __syncthreads();
+      const bool low = ((t & step) == 0) == ((t & run) == 0);
+      key = low == (o < key) ? o : key;
     }
   }
-  for (int i = threadIdx.x; i < kChunk && base + i < rows; i += kSortThreads) {
-    sorted[base + i] = static_cast<uint32_t>(key[i] >> 32);
-    places[base + i] = static_cast<uint32_t>(key[i]);
+  if (i < rows) {
+    sorted[i] = static_cast<uint32_t>(key >> 32);
+    places[i] = static_cast<uint32_t>(key);
   }
 }
 
@@ -157,12 +164,13 @@ __global__ void __launch_bounds__(kThreads) embedding_merge_kernel(const uint32_
 
 // The same in one step for up to kMostShared runs of kChunk keys, all of them in shared
 // memory: the keys' loads would otherwise wait for the L2 some ten times for each run. Four
-// searches go side by side. (Sorting 32768 tokens takes 21 us so, 62 with the kernel above.)
+// searches go side by side. (Sorting 32768 tokens takes 15 us so, 60 with the kernel above.)
 __global__ void __launch_bounds__(kSharedThreads) embedding_merge_shared_kernel(const uint32_t* sorted, const uint32_t* places,
                                                                               uint32_t* to_sorted, uint32_t* to_places,
                                                                               const int rows, const int runs) {
   extern __shared__ __align__(16) uint32_t keys[];  // [runs][kChunk], behind the last key the highest number
   const int n4 = rows / 4;
+#pragma unroll 8
   for (int i = threadIdx.x; i < n4; i += kSharedThreads) reinterpret_cast<uint4*>(keys)[i] = __ldg(reinterpret_cast<const uint4*>(sorted) + i);
   for (int i = n4 * 4 + threadIdx.x; i < runs * kChunk; i += kSharedThreads) keys[i] = i < rows ? __ldg(sorted + i) : 0xFFFFFFFFu;
   __syncthreads();
@@ -294,7 +302,7 @@ __global__ void __launch_bounds__(kGradThreads) embedding_grad_kernel(const Embe
             const int64_t at = col + c * kGradThreads * E;
             if (leading)
               put<E>(p.head + tile * p.hidden + at, acc[c], 1.f, false);
-            else if (!ends)
+            else if (!ends)  // it begins here and goes on
               put<E>(p.tail + tile * p.hidden + at, acc[c], 1.f, false);
             else
               put<E>(grad_W + t * p.hidden + at, acc[c], p.scale, p.accumulate != 0);
@@ -303,43 +311,88 @@ __global__ void __launch_bounds__(kGradThreads) embedding_grad_kernel(const Embe
           }
         }
       }
+      if (last && !ends && !leading && slice == 0 && threadIdx.x == 0) {
+        const int64_t far = (tile + kShortRun) * kTile;
+        if (far < p.rows && p.sorted[far] == t)
+          p.joins[1 + tiles - atomicAdd(p.joins + 1, 1u)] = static_cast<uint32_t>(tile);
+        else
+          p.joins[2 + atomicAdd(p.joins, 1u)] = static_cast<uint32_t>(tile);
+      }
       if (ends) leading = false;
     }
   }
 }
 
-// Joins the sums of a run that begins in the CTA's tile and goes on behind it.
+// Joins the sums of runs that cross tiles, from two lists, whose order means nothing. The first `shorts`
+// CTAs take those that reach into less than kShortRun tiles more: E columns of a run for each thread. The others
+// take long ones, of which there are few (a text's most frequent tokens): 32 E columns of a run for each CTA,
+// every kJoinWarps-th tile for a warp, whose sums are added in order. What this costs is loads that wait for
+// loads. (32768 tokens of a text's frequencies, 4096 columns: 39 us with a CTA for each tile and 512 columns
+// and a binary search for the run's end, 11 us so.)
 template <int E>
-__global__ void __launch_bounds__(kGradThreads) embedding_join_kernel(const EmbeddingParams p, const int slices) {
-  const int64_t tile = blockIdx.x / slices, r0 = tile * kTile, next = r0 + kTile;
-  const int slice = static_cast<int>(blockIdx.x - tile * slices);
-  if (next >= p.rows) return;
-  const uint32_t t = p.sorted[next - 1];
-  if (t >= p.vocab || p.sorted[next] != t) return;
-  if (p.sorted[r0] == t && r0 > 0 && p.sorted[r0 - 1] == t) return;  // it began earlier
-  // the tiles that it reaches into
-  const int64_t end = next + keys_before<true>(p.sorted + next, static_cast<uint32_t>(p.rows - next), t);
-  const int64_t last = (end - 1) / kTile;
-  const int64_t col = (static_cast<int64_t>(slice) * kGradThreads + threadIdx.x) * E;
-  if (col >= p.hidden) return;
-  float acc[E];
-  auto read = [&](const float* from, float (&v)[E]) {
+__global__ void __launch_bounds__(32 * kJoinWarps) embedding_join_kernel(const EmbeddingParams p, const int shorts, const int64_t tiles) {
+  __shared__ float sums[kJoinWarps][32 * E];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto add = [&](const float* from, float (&v)[E]) {
     if constexpr (E == 1) {
-      v[0] = *from;
+      v[0] += *from;
     } else {
       const float4 f = *reinterpret_cast<const float4*>(from);
-      v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+      v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
     }
   };
-  read(p.tail + tile * p.hidden + col, acc);
+  float* out = static_cast<float*>(p.out);
+  if (static_cast<int>(blockIdx.x) < shorts) {
+    const int blocks = static_cast<int>((p.hidden + 32 * kJoinWarps * E - 1) / (32 * kJoinWarps * E));
+    const int64_t col = (static_cast<int64_t>(blockIdx.x % blocks) * (32 * kJoinWarps) + threadIdx.x) * E;
+    const uint32_t runs = p.joins[0];
+    for (uint32_t k = blockIdx.x / blocks; k < runs; k += shorts / blocks) {
+      const int64_t tile = p.joins[2 + k];
+      const uint32_t t = p.sorted[(tile + 1) * kTile - 1];
+      // tiles that begin in the run, less than kShortRun
+      const int64_t first = (tile + 1 + lane) * kTile;
+      const int n = __popc(__ballot_sync(0xffffffffu, lane < kShortRun && first < p.rows && p.sorted[first] == t));
+      if (col < p.hidden) {
+        float acc[E] = {};
+        add(p.tail + tile * p.hidden + col, acc);
 #pragma unroll 8
-  for (int64_t i = tile + 1; i <= last; ++i) {
-    float v[E];
-    read(p.head + i * p.hidden + col, v);
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] += v[e];
+        for (int i = 0; i < n; ++i) add(p.head + (tile + 1 + i) * p.hidden + col, acc);
+        put<E>(out + t * p.hidden + col, acc, p.scale, p.accumulate != 0);
+      }
+    }
+    return;
   }
-  put<E>(static_cast<float*>(p.out) + t * p.hidden + col, acc, p.scale, p.accumulate != 0);
+  const int longs = static_cast<int>(gridDim.x) - shorts, mine = static_cast<int>(blockIdx.x) - shorts;
+  const int blocks = static_cast<int>((p.hidden + 32 * E - 1) / (32 * E));
+  const int64_t col = (static_cast<int64_t>(mine % blocks) * 32 + lane) * E;
+  const uint32_t runs = p.joins[1];
+  for (uint32_t k = mine / blocks; k < runs; k += longs / blocks) {
+    const int64_t tile = p.joins[1 + tiles - k];
+    const uint32_t t = p.sorted[(tile + 1) * kTile - 1];
+    int64_t n = 0;
+    while (true) {
+      const int64_t first = (tile + 1 + n + threadIdx.x) * kTile;
+      const int more = __syncthreads_count(first < p.rows && p.sorted[first] == t);
+      n += more;
+      if (more < 32 * kJoinWarps) break;
+    }
+    float acc[E] = {};
+    if (col < p.hidden) {
+      if (warp == 0) add(p.tail + tile * p.hidden + col, acc);
+#pragma unroll 8
+      for (int64_t i = warp; i < n; i += kJoinWarps) add(p.head + (tile + 1 + i) * p.hidden + col, acc);
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) sums[warp][e * 32 + lane] = acc[e];
+    __syncthreads();
+    if (warp == 0 && col < p.hidden) {
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        for (int w = 1; w < kJoinWarps; ++w) acc[e] += sums[w][e * 32 + lane];
+      put<E>(out + t * p.hidden + col, acc, p.scale, p.accumulate != 0);
+    }
+    __syncthreads();
+  }
 }
 
 inline bool on_vectors(const void* p, int64_t ld, size_t es, int E) {
@@ -394,9 +447,13 @@ int run_grad(const EmbeddingParams& p, cudaStream_t stream) {
                                  cudaGetLastError()));
   if (tiles > 1) {
     constexpr int JE = E > 1 ? 4 : 1;
-    const int64_t join = (p.hidden + kGradThreads * JE - 1) / (kGradThreads * JE);
-    FLCE_LAUNCH(K_EMBEDDING_GRAD, (embedding_join_kernel<JE><<<static_cast<unsigned>(tiles * join), kGradThreads, 0, stream>>>(
-                                       p, static_cast<int>(join)),
+    // whole rounds of a run's blocks of columns in either part
+    const int64_t short_blocks = (p.hidden + 32 * kJoinWarps * JE - 1) / (32 * kJoinWarps * JE), long_blocks = (p.hidden + 32 * JE - 1) / (32 * JE);
+    int64_t at_once = kJoinCtas / short_blocks + 1;
+    if (at_once > tiles - 1) at_once = tiles - 1;
+    const int64_t shorts = at_once * short_blocks, longs = tiles > kShortRun ? kLongRuns * long_blocks : 0;
+    FLCE_LAUNCH(K_EMBEDDING_GRAD, (embedding_join_kernel<JE><<<static_cast<unsigned>(shorts + longs), 32 * kJoinWarps, 0, stream>>>(
+                                       p, static_cast<int>(shorts), tiles),
                                    cudaGetLastError()));
   }
   return FLCE_OK;
@@ -420,8 +477,8 @@ cudaError_t launch_embedding(const EmbeddingParams& p, cudaStream_t s) {
 
 int launch_embedding_sort(EmbeddingParams* p, int sms, cudaStream_t stream) {
   const int64_t chunks = (p->rows + kChunk - 1) / kChunk;
-  FLCE_LAUNCH(K_EMBEDDING_SORT, (embedding_chunk_kernel<<<static_cast<unsigned>(chunks), kSortThreads, 0, stream>>>(
-                                     p->tokens, p->rows, p->vocab, p->sorted, p->places),
+  FLCE_LAUNCH(K_EMBEDDING_SORT, (embedding_chunk_kernel<<<static_cast<unsigned>(chunks), kChunk, 0, stream>>>(
+                                     p->tokens, p->rows, p->vocab, p->sorted, p->places, p->joins),
                                  cudaGetLastError()));
   for (int64_t run = kChunk; run < p->rows;) {
     const int64_t runs = (p->rows + run - 1) / run;

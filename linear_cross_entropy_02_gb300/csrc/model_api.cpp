@@ -59,12 +59,13 @@ int device_check(int* sms) {
 
 // Workspace of the embedding's gradient.
 struct EmbeddingSpace {
-  size_t keys, sums;
-  size_t total() const { return 4 * keys + 2 * sums; }
+  size_t keys, sums, joins;
+  size_t total() const { return 4 * keys + 2 * sums + joins; }
 };
 EmbeddingSpace embedding_space(int64_t rows, int64_t hidden) {
   const size_t tiles = static_cast<size_t>((rows + kEmbeddingTile - 1) / kEmbeddingTile);
-  return {round256(sizeof(uint32_t) * static_cast<size_t>(rows)), round256(sizeof(float) * tiles * static_cast<size_t>(hidden))};
+  return {round256(sizeof(uint32_t) * static_cast<size_t>(rows)), round256(sizeof(float) * tiles * static_cast<size_t>(hidden)),
+          rows > 0 ? round256(sizeof(uint32_t) * (tiles + 2)) : 0};
 }
 
 // Rows that a verification looks at, -1 if there are too many.
@@ -313,6 +314,7 @@ int flce_embedding_backward(const void* grad_out, int dtype, int64_t ld_grad, co
     p.places2 = reinterpret_cast<uint32_t*>(ws + 3 * space.keys);
     p.head = reinterpret_cast<float*>(ws + 4 * space.keys);
     p.tail = reinterpret_cast<float*>(ws + 4 * space.keys + space.sums);
+    p.joins = reinterpret_cast<uint32_t*>(ws + 4 * space.keys + 2 * space.sums);
     const int sorted = launch_embedding_sort(&p, sms, stream);
     if (sorted != FLCE_OK) return sorted;
   }

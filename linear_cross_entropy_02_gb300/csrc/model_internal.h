@@ -69,6 +69,9 @@ struct EmbeddingParams {
   uint32_t* places2;
   float* head;
   float* tail;
+  // runs that cross tiles: number of short ones, of long ones, then the tiles in which they begin, the short
+  // ones' from the front, the long ones' from the end
+  uint32_t* joins;
 };
 constexpr int kEmbeddingTile = 32;
 cudaError_t launch_embedding(const EmbeddingParams& p, cudaStream_t s);
