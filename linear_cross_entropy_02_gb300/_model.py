@@ -222,7 +222,8 @@ def add_layer_norm(x, residual=None, weight=None, bias=None, *, eps: float = 1e-
     and bias where they require grad, once. With checkpoint_8bit the node keeps the sum in 8
     bits, half a bf16 tensor's memory and a quarter of an fp32 one's: y is unaffected, and the
     gradients of x, the residual and the weight are those at the sum's 8-bit values.
-    need_sum=False gives (y, None)."""
+    need_sum=False gives (y, None). As for any node, capture a backward pass into a graph
+    while no eager graph of the same leaves lives."""
     out = _AddLayerNorm.apply(x, residual, weight, bias, float(eps), bool(rms), bool(checkpoint_8bit), bool(need_sum))
     if isinstance(out, tuple):
         return out

@@ -114,8 +114,9 @@ __device__ __forceinline__ int compare(const RowCut& t, const RowCut& g, bool dr
 // Their kept set is the row, so only its maximum and the sum of its weights are wanted:
 // one pass, with the slice of the row in registers between the two. A cluster per row, of
 // as many CTAs as its registers need, several of them on an SM so that one loads while the
-// others add up. 64 requests of 5 drafts on 129280 bf16, 704 rows, take 74 us (2.5 TB/s), some 115 with
-// sampling's kernel: 19 instructions a logit, half of them the exponential, fill 62% of the issue slots.
+// others add up. 64 requests of 5 drafts on 129280 bf16, 704 rows, take 74 us (2.5 TB/s), 66 where those behind
+// a draft that is not accepted are left out (40% of them), some 115 with sampling's kernel: 19 instructions a
+// logit, half of them the exponential, fill 62% of the issue slots.
 constexpr int kPlainVecs = 8, kPlainWarps = 16;  // (of the larger CTAs)
 
 __device__ __forceinline__ uint32_t max_nan(uint32_t a, uint32_t b, const uint16_t*) {  // bf16 pairs
