@@ -418,3 +418,22 @@ def test_a_captured_backward_pass():
         step()
     side.synchronize()
     assert torch.equal(got[0], W.grad) and torch.equal(got[1], n.grad)
+
+
+@pytest.mark.gpu
+def test_what_the_node_keeps():
+    """With checkpoint_8bit the memory kept between the passes is the codes and scales instead of the sum."""
+    import linear_cross_entropy_02_gb300 as flce
+    rows, H = 4096, 4096
+    x, w = torch.randn(rows, H, device="cuda").bfloat16(), torch.ones(H, device="cuda").bfloat16().requires_grad_()
+    kept = []
+    for checkpoint_8bit in (False, True):
+        res = torch.randn(rows, H, device="cuda").bfloat16()
+        torch.cuda.synchronize()
+        before = torch.cuda.memory_allocated()
+        y, s = flce.add_layer_norm(x, res, w, rms=True, checkpoint_8bit=checkpoint_8bit, need_sum=False)
+        kept.append(torch.cuda.memory_allocated() - before - y.numel() * 2)
+        y.sum().backward()
+        del y, s, res
+    room = 4 * rows + 4096       # the rows' statistics
+    assert abs(kept[0] - rows * H * 2) <= room and abs(kept[1] - rows * H - rows * H // 32) <= room

@@ -230,3 +230,43 @@ def test_gradients_that_are_not_numbers_stay_with_their_tokens():
     gW = flce.flce_embedding_backward(G, t, 20)
     assert int(gW.isnan().sum()) == 1 and bool(gW[7, 3].isnan()) and bool((gW[5] == 2).all()) and bool((gW[9] == 1).all())
     assert float(gW.nan_to_num().sum()) == 39 + 80 + 40
+
+
+@pytest.mark.gpu
+def test_threads_on_streams_of_their_own():
+    import threading
+
+    import linear_cross_entropy_02_gb300 as flce
+    t, G = tokens_of("frequent", 20000, 3000), torch.randn(20000, 64, device="cuda").bfloat16()
+    want, bad = flce.flce_embedding_backward(G, t, 3000), []
+    torch.cuda.synchronize()
+
+    def work():
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            got = [flce.flce_embedding_backward(G, t, 3000) for _ in range(20)]
+        stream.synchronize()
+        bad.extend(i for i, o in enumerate(got) if not torch.equal(o, want))
+    threads = [threading.Thread(target=work) for _ in range(3)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not bad
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H", [8, 24, 520])
+def test_runs_around_the_tiles(H):
+    """Runs that begin, end and fill tiles of 32 rows at every offset, short ones and ones that cross more than 16 tiles."""
+    import linear_cross_entropy_02_gb300 as flce
+    for lengths in ([32] * 40, [31, 33] * 20, [1, 512, 32, 513, 64, 2000, 5], [511, 1, 480, 32, 700], [600] * 9, [16 * 32 + 1] * 3, [1500], [7] * 200):
+        t = torch.repeat_interleave(torch.arange(len(lengths)), torch.tensor(lengths))
+        t = (t * 7919 % 1009)[torch.randperm(len(t), generator=torch.Generator().manual_seed(len(t)))].cuda()
+        G = torch.randint(-8, 9, (len(t), H), generator=torch.Generator().manual_seed(H)).float().cuda()   # whole numbers: every sum is exact
+        want = torch.zeros(1009, H, dtype=torch.float64, device="cuda").index_add_(0, t, G.double())
+        for dtype in (torch.float32, torch.bfloat16):
+            assert torch.equal(flce.flce_embedding_backward(G.to(dtype), t, 1009, scale=0.5).double(), want * 0.5)
+            acc = torch.ones(1009, H, device="cuda")
+            flce.flce_embedding_backward(G.to(dtype), t, 1009, grad_W=acc)
+            assert torch.equal(acc.double(), want + 1)

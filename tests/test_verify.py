@@ -381,3 +381,53 @@ def test_logits_beyond_32_bits_of_elements():
     d = draft_from(flce, q, g, {}, 2)
     for kw in (dict(), dict(top_k=20, top_p=0.9)):
         assert all(torch.equal(a, b) for a, b in zip(flce.flce_verify(wide, d, u, q, **kw), flce.flce_verify(x, d, u, q, **kw)))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("B,V", [(2, 20000), (80, 9000), (2, 3000)])
+def test_long_lists_of_kept_tokens(B, V, dtype):
+    """top_k of hundreds and thousands, with and without cuts behind it; some as large as what the row holds."""
+    import linear_cross_entropy_02_gb300 as flce
+    x, q, u, g = make(B, 1, V, dtype, seed=14)
+    x[0, 0, 600:] = -math.inf
+    n = min(B, 6)
+    for s in (dict(top_k=257), dict(top_k=600), dict(top_k=1000, top_p=0.9), dict(top_k=2500, temperature=1.4), dict(top_k=2999, min_p=1e-4),
+              dict(top_k=400, top_p=0.7, min_p=0.01), dict(top_k=V - 1)):
+        d = draft_from(flce, q, g, s, 1)
+        for draft in (q, None):
+            got = flce.flce_verify(x, d, u, draft, **s)
+            want = reference(x[:n], d[:n], u[:n], None if draft is None else q[:n], s)
+            assert torch.equal(got[0][:n].cpu(), torch.from_numpy(want[0])) and torch.equal(got[1][:n].cpu(), torch.from_numpy(want[1])), s
+
+
+@pytest.mark.gpu
+def test_a_large_batch_in_a_graph_and_on_two_streams():
+    import linear_cross_entropy_02_gb300 as flce
+    x, q, u, g = make(100, 3, 20000, torch.bfloat16, seed=15)
+    d = draft_from(flce, q, g, {}, 3)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = flce.flce_verify(x, d, u, q)
+    for i in range(3):
+        for t in (x, d, q):
+            t.copy_(t.roll(7, 0))
+        u.uniform_(generator=g)
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(out, flce.flce_verify(x, d, u, q)))
+    import threading
+    want, bad = flce.flce_verify(x, d, u, q), []
+    torch.cuda.synchronize()
+
+    def work():
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            got = [flce.flce_verify(x, d, u, q) for _ in range(20)]
+        stream.synchronize()
+        bad.extend(i for i, o in enumerate(got) if not all(torch.equal(a, b) for a, b in zip(o, want)))
+    threads = [threading.Thread(target=work) for _ in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
