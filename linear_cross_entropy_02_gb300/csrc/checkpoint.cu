@@ -1,7 +1,7 @@
 // 8-bit checkpoints of activations: store and read back (checkpoint_device.cuh has the
 // format). Both are copies with little arithmetic, bound by memory.
 //
-// A warp takes kUnroll vectors per lane, so that that many loads are in flight. Rows
+// A warp takes several vectors per lane, so that that many loads are in flight. Rows
 // of a multiple of 32 elements without gaps are one long row, whose blocks do not know
 // where a row ends; other rows are cut into chunks of a warp each.
 #include "checkpoint_device.cuh"

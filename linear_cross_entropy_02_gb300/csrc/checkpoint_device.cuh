@@ -59,6 +59,20 @@ template <typename T, int E>
 __device__ __forceinline__ void unpack(const CodeVector<E>& r, float (&v)[E]) {
   read_codes<E>(r.words, r.scale, v);
 }
+// One that need not lie on the blocks' boundaries: elements from `second` on have the next scale,
+// and those outside of [from, to) are not the row's.
+template <int E>
+struct ShiftedCodes {
+  uint32_t words[E == 8 ? 2 : 1];
+  float scale, next;
+  int second, from, to;
+};
+template <typename T, int E>
+__device__ __forceinline__ void unpack(const ShiftedCodes<E>& r, float (&v)[E]) {
+  read_codes<E>(r.words, 1.f, v);
+#pragma unroll
+  for (int e = 0; e < E; ++e) v[e] = e >= r.from && e < r.to ? v[e] * (e < r.second ? r.scale : r.next) : 0.f;
+}
 
 // Encodes vector `vec` of a row: codes [rows, hidden], scales [rows, blocks]. Called by
 // whole warps, `vec` rising by one from lane to lane over groups of min(32 / E, lanes);
@@ -74,7 +88,11 @@ __device__ __forceinline__ void keep_vector(const Raw<T, E>& raw, int64_t vec, b
     for (int e = 0; e < E; ++e) most = max(most, __float_as_uint(v[e]) & 0x7FFFFFFFu);
   }
   const int group = min(kCheckpointBlock / E, lanes);
-  for (int o = group >> 1; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+  if (E == 1 && lanes == 32) {
+    most = __reduce_max_sync(0xffffffffu, most);
+  } else {
+    for (int o = group >> 1; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+  }
   if (!valid) return;
   const uint32_t byte = checkpoint_scale(most);
   // 2^-e; a block of NaN has codes of zero

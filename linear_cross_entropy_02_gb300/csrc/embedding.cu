@@ -1,7 +1,7 @@
 // Embeddings: rows of W looked up by token and scaled, and the gradient, which adds
 // rows up by token.
 //
-// The lookup is a copy, bound by memory: a warp takes a piece of a row with kUnroll
+// The lookup is a copy, bound by memory: a warp takes a piece of a row with several
 // vectors per lane in flight.
 //
 // The gradient sorts (token, position) pairs and then adds up runs of one token, so
@@ -26,9 +26,11 @@ namespace flce {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;
+template <int E>
+constexpr int kVectors = E == 1 ? 16 : 4;  // per lane of the lookup
 constexpr int kChunk = 1024;       // keys sorted by a CTA
 constexpr int kMostShared = 48;    // chunks that shared memory holds
+constexpr int kSharedGroup = 32;   // of more than that
 constexpr int kSharedThreads = 512;
 constexpr int kGradThreads = 128;
 constexpr int kJoinWarps = 8;
@@ -56,6 +58,7 @@ __device__ __forceinline__ void store_floats(T* to, const float (&v)[E]) {
 
 template <typename TI, typename TO, int E>
 __global__ void __launch_bounds__(kThreads) embedding_kernel(const EmbeddingParams p, const int64_t chunks) {
+  constexpr int kUnroll = kVectors<E>;
   const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32;
   if (unit >= p.rows * chunks) return;
   const int64_t row = unit / chunks, vecs = p.hidden / E;
@@ -162,12 +165,18 @@ __global__ void __launch_bounds__(kThreads) embedding_merge_kernel(const uint32_
   to_places[at] = place;
 }
 
-// The same in one step for up to kMostShared runs of kChunk keys, all of them in shared
+// The same for groups of `group` runs of kChunk keys, up to kMostShared, blockIdx.y-th group in shared
 // memory: the keys' loads would otherwise wait for the L2 some ten times for each run. Four
 // searches go side by side. (Sorting 32768 tokens takes 15 us so, 60 with the kernel above.)
 __global__ void __launch_bounds__(kSharedThreads) embedding_merge_shared_kernel(const uint32_t* sorted, const uint32_t* places,
                                                                               uint32_t* to_sorted, uint32_t* to_places,
-                                                                              const int rows, const int runs) {
+                                                                              const int64_t all_rows, const int group) {
+  const int64_t first = static_cast<int64_t>(blockIdx.y) * group * kChunk;
+  const int rows = static_cast<int>(min(static_cast<int64_t>(group) * kChunk, all_rows - first)), runs = (rows + kChunk - 1) / kChunk;
+  sorted += first;
+  places += first;
+  to_sorted += first;
+  to_places += first;
   extern __shared__ __align__(16) uint32_t keys[];  // [runs][kChunk], behind the last key the highest number
   const int n4 = rows / 4;
 #pragma unroll 8
@@ -403,7 +412,7 @@ template <typename TI, typename TO>
 cudaError_t run_forward(const EmbeddingParams& p, cudaStream_t s) {
   constexpr int E = 16 / sizeof(TI);
   const bool vectors = p.hidden % E == 0 && on_vectors(p.in, p.ld, sizeof(TI), E) && reinterpret_cast<uintptr_t>(p.out) % 16 == 0;
-  const int64_t per = 32LL * kUnroll * (vectors ? E : 1);
+  const int64_t per = 32LL * (vectors ? kVectors<E> * E : kVectors<1>);
   const int64_t chunks = (p.hidden + per - 1) / per, ctas = (p.rows * chunks + kThreads / 32 - 1) / (kThreads / 32);
   if (ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   if (vectors)
@@ -413,7 +422,7 @@ cudaError_t run_forward(const EmbeddingParams& p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_merge_shared(const EmbeddingParams& p, int runs, int sms, cudaStream_t s) {
+cudaError_t launch_merge_shared(const EmbeddingParams& p, int64_t runs, int group, int sms, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
@@ -423,9 +432,9 @@ cudaError_t launch_merge_shared(const EmbeddingParams& p, int runs, int sms, cud
     if (e != cudaSuccess) return e;
     done.fetch_or(1ull << (dev & 63));
   }
-  const int64_t want = (p.rows + kSharedThreads - 1) / kSharedThreads;
-  embedding_merge_shared_kernel<<<static_cast<unsigned>(want < sms ? want : sms), kSharedThreads, static_cast<size_t>(runs) * kChunk * 4, s>>>(
-      p.sorted, p.places, p.sorted2, p.places2, static_cast<int>(p.rows), runs);
+  const int64_t groups = (runs + group - 1) / group, want = static_cast<int64_t>(group) * kChunk / kSharedThreads;
+  const dim3 grid(static_cast<unsigned>(want < sms ? want : sms), static_cast<unsigned>(groups));
+  embedding_merge_shared_kernel<<<grid, kSharedThreads, static_cast<size_t>(group) * kChunk * 4, s>>>(p.sorted, p.places, p.sorted2, p.places2, p.rows, group);
   return cudaGetLastError();
 }
 
@@ -482,10 +491,10 @@ int launch_embedding_sort(EmbeddingParams* p, int sms, cudaStream_t stream) {
                                  cudaGetLastError()));
   for (int64_t run = kChunk; run < p->rows;) {
     const int64_t runs = (p->rows + run - 1) / run;
-    const bool shared = run == kChunk && runs <= kMostShared;
-    const int group = static_cast<int>(shared || runs < 8 ? runs : 8);
+    const bool shared = run == kChunk;
+    const int group = static_cast<int>(shared ? (runs <= kMostShared ? runs : kSharedGroup) : runs < 8 ? runs : 8);
     if (shared)
-      FLCE_LAUNCH(K_EMBEDDING_SORT, launch_merge_shared(*p, static_cast<int>(runs), sms, stream));
+      FLCE_LAUNCH(K_EMBEDDING_SORT, launch_merge_shared(*p, runs, group, sms, stream));
     else
       FLCE_LAUNCH(K_EMBEDDING_SORT,
                 (embedding_merge_kernel<<<static_cast<unsigned>((p->rows + kThreads - 1) / kThreads), kThreads, 0, stream>>>(

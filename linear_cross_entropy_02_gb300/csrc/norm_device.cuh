@@ -344,9 +344,11 @@ struct Place {
   }
 };
 // What x, grad_y and grad_x have in common: the distance of `row` from a boundary.
-template <typename T, int E, bool SHIFT>
+template <typename T, int E, bool SHIFT, int MODE>
 __device__ __forceinline__ Place place_of(const NormParams& p, int64_t row) {
-  const int64_t at = static_cast<int64_t>(reinterpret_cast<uintptr_t>(p.x) / sizeof(T)) + row * p.ld_x;
+  // (a checkpoint lies as it likes)
+  const void* x = MODE == kAdd8 ? p.gy : p.x;
+  const int64_t at = static_cast<int64_t>(reinterpret_cast<uintptr_t>(x) / sizeof(T)) + row * (MODE == kAdd8 ? p.ld_gy : p.ld_x);
   const int off = SHIFT ? static_cast<int>(at % E) : 0, hidden = static_cast<int>(p.hidden);
   return {hidden, off, (hidden + off + E - 1) / E};
 }
@@ -471,24 +473,29 @@ constexpr int ring_arrays(int mode) { return mode == kPlain ? 2 : 3; }
 template <typename T, int E, int C, int NB, bool RMS, bool SHIFT, int MODE>
 struct BwdRow {
   static_assert(E > 1 || !SHIFT, "single elements are always in place");
-  static_assert(MODE != kAdd8 || !SHIFT, "codes do not lie as the gradients do");
   static constexpr bool RING = kRing<T, E>, KEEP = C == 1, ADD = MODE != kPlain, X8 = MODE == kAdd8;
   static constexpr int A = ring_arrays(MODE);  // arrays in the ring: x, grad_y, grad_sum
-  static constexpr bool CODES_IN_RING = RING && E >= 4;  // X8: single codes are too short for a copy
+  // X8: single codes are too short for a copy, and where rows are off the vector boundary codes lie differently.
+  static constexpr bool CODES_IN_RING = RING && E >= 4 && !SHIFT;
+  // SHIFT: whole words that hold a vector's codes, in registers until they are used
+  static constexpr int WINDOW = X8 && SHIFT ? E / 4 + 1 : 1;
   const ParamsOf<MODE>& p;
   Place pl;
   int t, stride, threads;  // first vector, distance between vectors, distance in the ring
   Raw<T, E>* ring;
   Weights<E> weights;  // SHIFT
   uint32_t inside = 0;
+  uint32_t bits = 0;  // X8 and SHIFT: of a vector's first code in its word (the same for all rows and vectors of a thread)
   Raw<T, E> next_x[RING ? 1 : C], next_g[RING ? 1 : C], next_s[RING ? 1 : C];
   // X8: the next row's scales, and its codes where the ring does not take them
-  uint8_t next_scale[X8 ? C : 1], next_code[X8 && !CODES_IN_RING ? C : 1];
+  uint8_t next_scale[X8 ? C : 1], next_second[X8 && SHIFT ? C : 1], next_code[X8 && !CODES_IN_RING && !SHIFT ? C : 1];
+  uint32_t next_window[X8 && SHIFT ? C : 1][WINDOW];
   float acc_w[C][E], acc_b[C][E];
 
   __device__ __forceinline__ BwdRow(const ParamsOf<MODE>& params, const Place& place, int first, int apart, int ring_apart,
-                                    Raw<T, E>* r, const Weights<E>& w)
+                                    Raw<T, E>* r, const Weights<E>& w, int64_t row)
       : p(params), pl(place), t(first), stride(apart), threads(ring_apart), ring(r), weights(w) {
+    if constexpr (X8 && SHIFT) bits = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p.codes) + row * p.hidden - pl.off) % 4 * 8;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       if constexpr (SHIFT) {
@@ -516,7 +523,27 @@ struct BwdRow {
       for (int c = 0; c < C; ++c) {
         const int v = t + c * stride;
         if (v < pl.vecs) {
-          if constexpr (X8) {
+          if constexpr (X8 && SHIFT) {
+            // from the word boundary before the vector's first code; at the checkpoint's ends byte by byte
+            const uint8_t* code = p.codes + row * p.hidden + v * E - pl.off;
+            const uintptr_t words = reinterpret_cast<uintptr_t>(code) & ~uintptr_t{3};
+            if (words >= reinterpret_cast<uintptr_t>(p.codes) && words + 4 * WINDOW <= reinterpret_cast<uintptr_t>(p.codes) + p.rows * p.hidden) {
+#pragma unroll
+              for (int i = 0; i < WINDOW; ++i) next_window[c][i] = __ldg(reinterpret_cast<const uint32_t*>(words) + i);
+            } else {
+#pragma unroll
+              for (int i = 0; i < WINDOW; ++i) next_window[c][i] = 0;
+#pragma unroll
+              for (int i = 0; i < 4 * WINDOW; ++i) {
+                const int64_t e = static_cast<int64_t>(words) + i - static_cast<int64_t>(reinterpret_cast<uintptr_t>(code)) + v * E - pl.off;
+                if (e >= 0 && e < pl.hidden) next_window[c][i / 4] |= static_cast<uint32_t>(p.codes[row * p.hidden + e]) << (i % 4 * 8);
+              }
+            }
+            const uint8_t* scales = p.scales + row * checkpoint_blocks(p.hidden);
+            const int first = max(v * E - pl.off, 0), last = min(v * E - pl.off + E, pl.hidden) - 1;
+            next_scale[c] = __ldg(scales + first / kCheckpointBlock);
+            next_second[c] = __ldg(scales + last / kCheckpointBlock);
+          } else if constexpr (X8) {
             const uint8_t* code = p.codes + row * p.hidden + v * E;
             if constexpr (CODES_IN_RING)
               copy_async<E>(to + c * threads, code);
@@ -525,7 +552,7 @@ struct BwdRow {
             next_scale[c] = __ldg(p.scales + row * checkpoint_blocks(p.hidden) + v * E / kCheckpointBlock);
           }
           if constexpr (RING) {
-            if (is_inside(c) || (in_matrix<E>(pl, row, p.ld_x, p.rows, v) && in_matrix<E>(pl, row, p.ld_gy, p.rows, v) &&
+            if (is_inside(c) || ((X8 || in_matrix<E>(pl, row, p.ld_x, p.rows, v)) && in_matrix<E>(pl, row, p.ld_gy, p.rows, v) &&
                                  (!ADD || !sr || in_matrix<E>(pl, row, ld_gs, p.rows, v)))) {
               if constexpr (!X8) copy_async<sizeof(T) * E>(to + c * threads, xr + c * stride * E);
               copy_async<sizeof(T) * E>(to + (C + c) * threads, gr + c * stride * E);
@@ -557,11 +584,27 @@ struct BwdRow {
     }
   }
 
-  // x of vector c of the row in `stage`, as it is held.
-  __device__ __forceinline__ std::conditional_t<X8, CodeVector<E>, Raw<T, E>> take_x(int stage, int c, const Raw<T, E>& held, uint8_t code,
-                                                                                   uint8_t scale) const {
+  // x of vector c of the row in `stage`, as it is held; `code` is a vector's only code, or (SHIFT) its window.
+  struct HeldCode {
+    uint32_t word[WINDOW];
+    uint8_t scale, second;
+  };
+  using Vector = std::conditional_t<X8, std::conditional_t<SHIFT, ShiftedCodes<E>, CodeVector<E>>, Raw<T, E>>;
+  __device__ __forceinline__ Vector take_x(int stage, int c, const Raw<T, E>& held, const HeldCode& code) const {
     if constexpr (!X8) {
       return take(stage, 0, c, held);
+    } else if constexpr (SHIFT) {
+      ShiftedCodes<E> r;
+      const int start = (t + c * stride) * E - pl.off;
+#pragma unroll
+      for (int i = 0; i < E / 4; ++i) r.words[i] = __funnelshift_r(code.word[i], code.word[i + 1], bits);
+      r.scale = scale_value(code.scale);
+      r.next = scale_value(code.second);
+      r.from = -start;
+      r.to = pl.hidden - start;
+      // (a vector of at most 8 elements, not of the row but for its blocks, has two at most)
+      r.second = (min(start + E, pl.hidden) - 1) / kCheckpointBlock * kCheckpointBlock - start;
+      return r;
     } else {
       CodeVector<E> r;
       if constexpr (CODES_IN_RING) {
@@ -569,9 +612,9 @@ struct BwdRow {
 #pragma unroll
         for (int i = 0; i < E / 4; ++i) r.words[i] = from[i];
       } else {
-        r.words[0] = code;
+        r.words[0] = code.word[0];
       }
-      r.scale = scale_value(scale);
+      r.scale = scale_value(code.scale);
       return r;
     }
   }
@@ -582,7 +625,7 @@ struct BwdRow {
   __device__ __forceinline__ void visit(int64_t row, int vecs, int stage, int64_t ahead, int fill, float mean, float rstd,
                                         int stages, S sum) {
     Raw<T, E> hx[RING ? 1 : C], hg[RING ? 1 : C], hs[RING ? 1 : C];
-    uint8_t code[X8 ? C : 1], scale[X8 ? C : 1];
+    HeldCode code[X8 ? C : 1];
     auto hold = [&]() {
 #pragma unroll
       for (int c = 0; c < C; ++c) {
@@ -592,8 +635,14 @@ struct BwdRow {
           if constexpr (ADD) hs[c] = next_s[c];
         }
         if constexpr (X8) {
-          scale[c] = next_scale[c];
-          if constexpr (!CODES_IN_RING) code[c] = next_code[c];
+          code[c].scale = next_scale[c];
+          if constexpr (SHIFT) {
+            code[c].second = next_second[c];
+#pragma unroll
+            for (int i = 0; i < WINDOW; ++i) code[c].word[i] = next_window[c][i];
+          } else if constexpr (!CODES_IN_RING) {
+            code[c].word[0] = next_code[c];
+          }
         }
       }
     };
@@ -621,7 +670,7 @@ struct BwdRow {
           weights.get(c, w);
         else if (p.weight)
           load_weight<E>(p.weight, p.w_f32 != 0, (t + c * stride) * E, w);
-        bwd_visit<T, E, NB, RMS>(take_x(stage, c, hx[RING ? 0 : c], code[X8 ? c : 0], scale[X8 ? c : 0]),
+        bwd_visit<T, E, NB, RMS>(take_x(stage, c, hx[RING ? 0 : c], code[X8 ? c : 0]),
                                  take(stage, 1, c, hg[RING ? 0 : c]), SHIFT || p.weight != nullptr, w, mean, rstd,
                                  d[KEEP ? c : 0], g[c], acc_w[c], acc_b[c], sg, sgd);
       }
@@ -635,7 +684,7 @@ struct BwdRow {
       for (int c = 0; c < C; ++c) {
         if (t + c * stride < vecs) {
           if (!KEEP) {
-            unpack<T, E>(take_x(stage, c, hx[RING ? 0 : c], code[X8 ? c : 0], scale[X8 ? c : 0]), d[0]);
+            unpack<T, E>(take_x(stage, c, hx[RING ? 0 : c], code[X8 ? c : 0]), d[0]);
             if (!RMS) {
 #pragma unroll
               for (int e = 0; e < E; ++e) d[0][e] -= mean;
@@ -686,7 +735,7 @@ __global__ void __maxnreg__(REGS) norm_bwd_cta_kernel(const ParamsOf<MODE> p, co
   float4* w = reinterpret_cast<float4*>(dyn);
   Raw<T, E>* ring = reinterpret_cast<Raw<T, E>*>(w + (SHIFT ? C * Weights<E>::per * T_ : 0)) + threadIdx.x;
   int64_t row = blockIdx.x;
-  BwdRow<T, E, C, NB, RMS, SHIFT, MODE> r(p, place_of<T, E, SHIFT>(p, row), threadIdx.x, T_, T_, ring, {w + threadIdx.x, T_});
+  BwdRow<T, E, C, NB, RMS, SHIFT, MODE> r(p, place_of<T, E, SHIFT, MODE>(p, row), threadIdx.x, T_, T_, ring, {w + threadIdx.x, T_}, row);
   for (int i = 0; i < stages - 1; ++i) r.fetch(row + static_cast<int64_t>(i) * gridDim.x, i);
   float mean = !RMS && row < p.rows ? __ldg(p.mean + row) : 0.f, rstd = row < p.rows ? __ldg(p.rstd + row) : 0.f;
   int stage = 0, fill = stages - 1;
@@ -726,8 +775,8 @@ __global__ void __launch_bounds__(kWarpRowThreads)
   // whole warps go through the loop together: the groups' sums are shuffles of the warp
   const int64_t first = static_cast<int64_t>(blockIdx.x) * groups + (threadIdx.x >> 5) * (32 / lanes);
   int64_t row = first + (threadIdx.x & 31) / lanes;
-  BwdRow<T, E, C, NB, RMS, SHIFT, MODE> r(p, place_of<T, E, SHIFT>(p, row), t, 32, kWarpRowThreads, ring,
-                                    {w + threadIdx.x, kWarpRowThreads});
+  BwdRow<T, E, C, NB, RMS, SHIFT, MODE> r(p, place_of<T, E, SHIFT, MODE>(p, row), t, 32, kWarpRowThreads, ring,
+                                    {w + threadIdx.x, kWarpRowThreads}, row);
   for (int i = 0; i < stages - 1; ++i) r.fetch(row + i * step, i);
   float mean = !RMS && row < p.rows ? __ldg(p.mean + row) : 0.f, rstd = row < p.rows ? __ldg(p.rstd + row) : 0.f;
   int stage = 0, fill = stages - 1;
@@ -848,8 +897,9 @@ bool in_step(const NormParams& p) {
 }
 inline bool in_step(const AddNormParams& p) {
   const int64_t E = p.dtype == FLCE_DTYPE_F32 ? 4 : 8;
-  return in_step(static_cast<const NormParams&>(p)) &&
-         (!p.gs || ((p.ld_gs - p.hidden) % E == 0 && reinterpret_cast<uintptr_t>(p.gs) % 16 == reinterpret_cast<uintptr_t>(p.x) % 16));
+  const uintptr_t first = reinterpret_cast<uintptr_t>(p.gy) % 16;
+  auto same = [&](const void* q, int64_t ld) { return !q || ((ld - p.hidden) % E == 0 && reinterpret_cast<uintptr_t>(q) % 16 == first); };
+  return p.hidden >= 2 * E && same(p.gy, p.ld_gy) && same(p.x, p.ld_x) && same(p.gs, p.ld_gs) && same(p.out, p.hidden);
 }
 
 inline unsigned grid_of(int64_t want, int64_t most) { return static_cast<unsigned>(want < most ? want : most); }
@@ -1012,8 +1062,7 @@ cudaError_t run_bwd(const ParamsOf<MODE>& p, int sms, int* partials, cudaStream_
 template <typename T, int E, int MODE>
 cudaError_t launch_bwd(const ParamsOf<MODE>& p, int sms, int* partials, cudaStream_t s) {
   if (vectors(p)) return run_bwd<T, E, false, MODE>(p, sms, partials, s);
-  if constexpr (MODE != kAdd8)
-    if (in_step(p)) return run_bwd<T, E, true, MODE>(p, sms, partials, s);
+  if (in_step(p)) return run_bwd<T, E, true, MODE>(p, sms, partials, s);
   return run_bwd<T, 1, false, MODE>(p, sms, partials, s);
 }
 

@@ -437,3 +437,30 @@ def test_what_the_node_keeps():
         del y, s, res
     room = 4 * rows + 4096       # the rows' statistics
     assert abs(kept[0] - rows * H * 2) <= room and abs(kept[1] - rows * H - rows * H // 32) <= room
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,H", [(1500, 61), (900, 333), (1300, 1337), (700, 2050), (640, 5003), (3, 9001)])
+def test_checkpoints_off_the_boundaries(rows, H, dtype):
+    """Rows of no whole number of vectors or blocks, and codes that begin at any byte."""
+    import linear_cross_entropy_02_gb300 as flce
+    a = make(rows, H, dtype, seed=H)
+    for rms in (True, False):
+        out = flce.flce_add_layer_norm(a["x"], a["res"], a["w"], rms=rms, checkpoint=True, return_stats=True)
+        q = out["checkpoint"]
+        x64 = flce.flce_checkpoint_load(q)
+        for off in (0, 1, 2, 7):
+            wide = torch.full((rows * H + 16,), 0x7F, dtype=torch.uint8, device="cuda")     # NaN codes around it
+            codes = wide[off:off + rows * H].view(rows, H).copy_(q.codes)
+            for gs, bias in ((a["gs"], True), (None, False)):
+                got = flce.flce_add_layer_norm_backward(a["gy"], gs, flce.CheckpointTensor(codes, q.scales), a["w"], out["mean"], out["rstd"], rms=rms,
+                                                        need_grad_bias=bias)
+                check_backward(got, a["gy"], gs, x64, a["w"], out["mean"], out["rstd"], rms)
+    # a block of NaN stays in its row
+    a["res"][1, H - 1] = float("inf")
+    out = flce.flce_add_layer_norm(a["x"], a["res"], a["w"], rms=True, checkpoint=True, return_stats=True)
+    g = flce.flce_add_layer_norm_backward(a["gy"], None, out["checkpoint"], a["w"], None, out["rstd"], rms=True)["grad_x"]
+    good = torch.ones(rows, dtype=torch.bool)
+    good[1] = False
+    assert torch.equal(g.isfinite().all(1).cpu(), good)
