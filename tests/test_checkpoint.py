@@ -158,3 +158,34 @@ def test_refusals():
         flce.flce_checkpoint_store(torch.zeros(2, 0, device="cuda"))
     with pytest.raises(ValueError):
         flce.flce_checkpoint_load(flce.CheckpointTensor(u8(2, 64), u8(2, 2)), dtype=torch.float16)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,H", [(3000, 1), (999, 3), (2000, 33), (1500, 65), (700, 129), (400, 136), (130, 513), (40, 1001)])
+def test_many_rows_of_no_whole_blocks(rows, H, dtype):
+    """Vectors that are read back across rows and blocks, and rows that share a warp."""
+    import linear_cross_entropy_02_gb300 as flce
+    g = torch.Generator(device="cuda").manual_seed(H)
+    x = (torch.randn(rows, H, generator=g, device="cuda") * torch.exp(3 * torch.randn(rows, 1, generator=g, device="cuda"))).to(dtype)
+    x[rows // 2, H // 2] = float("nan")
+    q = flce.flce_checkpoint_store(x)
+    pad = -H % 32
+    b = torch.nn.functional.pad(x.float(), (0, pad)).view(rows, -1, 32)
+    top = b.abs().amax(2, keepdim=True)
+    m, k = torch.frexp(top)
+    s = torch.ldexp(torch.ones_like(top), k - 9 + (m > 0.875).int())
+    want = torch.where(top.isfinite(), (b / s).to(torch.float8_e4m3fn).float() * s, float("nan")).view(rows, -1)[:, :H]
+    for out in (torch.float32, torch.bfloat16):
+        v = flce.flce_checkpoint_load(q, dtype=out)
+        assert torch.equal(v.isnan(), want.isnan()) and torch.equal(v.nan_to_num(), want.to(out).nan_to_num())
+
+
+@pytest.mark.gpu
+def test_more_than_32_bits_of_odd_rows():
+    import linear_cross_entropy_02_gb300 as flce
+    rows, H = 540000, 4001
+    x = torch.empty(rows, H, dtype=torch.bfloat16, device="cuda").normal_()
+    ends = torch.tensor([0, 1, 268369, 268370, 536739, 536740, rows - 1], device="cuda")    # either side of 2^30 and 2^31 elements
+    v = flce.flce_checkpoint_load(flce.flce_checkpoint_store(x), dtype=torch.bfloat16)
+    assert torch.equal(v[ends], flce.flce_checkpoint_load(flce.flce_checkpoint_store(x[ends]), dtype=torch.bfloat16))
