@@ -282,8 +282,8 @@ int flce_embedding_backward(const void* grad_out, int dtype, int64_t ld_grad, co
       !grad_W)
     return FLCE_ERR_ARG;
   if (rows > 0 && (!grad_out || !tokens || !workspace)) return FLCE_ERR_ARG;
-  // (a grid's CTAs: at most one per tile and 512 columns, and one per token of the vocabulary)
-  if ((rows / kEmbeddingTile + 1) * (hidden / 512 + 1) + vocab > kMaxRows) return FLCE_ERR_ARG;
+  // (grids: at most a CTA per tile and 512 columns and one per token of the vocabulary, 65535 groups of 32768 tokens)
+  if (rows > int64_t{65535} * 32768 || (rows / kEmbeddingTile + 1) * (hidden / 512 + 1) + vocab > kMaxRows) return FLCE_ERR_ARG;
   const size_t es = element_size(dtype);
   if (!aligned(grad_out, es) || !aligned(tokens, 8) || !aligned(grad_W, 4) || !aligned(workspace, 16)) return FLCE_ERR_ALIGN;
   const EmbeddingSpace space = embedding_space(rows, hidden);

@@ -181,6 +181,7 @@ def test_refusals_without_a_gpu():
     for kw in (dict(dt=4), dict(n=-1), dict(h=0), dict(v=0), dict(ld=63), dict(s=float("nan")), dict(g=None), dict(t=None), dict(gw=None), dict(ws=None),
                dict(gw=at(1)), dict(ws=at(3)), dict(gw=at(2))):
         assert bwd(**kw) == B.FLCE_ERR_ARG, kw
+    assert bwd(n=65535 * 32768 + 1) == bwd(n=1 << 30, h=1 << 20, ld=1 << 20) == B.FLCE_ERR_ARG
     assert bwd(g=at(1, 1)) == bwd(t=at(2, 4)) == bwd(gw=at(3, 2)) == bwd(ws=at(4, 8)) == B.FLCE_ERR_ALIGN
     need = L.flce_embedding_workspace_size(100, 64)
     assert bwd(nb=need - 1) == B.FLCE_ERR_WORKSPACE and L.flce_embedding_workspace_size(-1, 64) == 0
