@@ -431,3 +431,18 @@ def test_a_large_batch_in_a_graph_and_on_two_streams():
     for t in threads:
         t.join()
     assert not bad
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("V,dtype", [(65536, torch.float32), (65537, torch.float32), (131073, torch.float32), (262144, torch.float32), (262145, torch.float32),
+                                     (131072, torch.bfloat16), (131073, torch.bfloat16), (262145, torch.bfloat16), (524289, torch.bfloat16)])
+def test_rows_at_the_limits_of_the_registers(V, dtype):
+    """Unfiltered rows that a cluster's registers just hold, with CTAs of each size, and those that they do not."""
+    import linear_cross_entropy_02_gb300 as flce
+    x, q, u, g = make(3, 1, V, dtype, seed=16)
+    x[0, 0, V - 1] = 25.0
+    d = draft_from(flce, q, g, {}, 1)
+    d[0, 0] = V - 1
+    check(flce, x, d, u, q, {})
+    x[1, 1, V - 1] = math.nan
+    check(flce, x, d, u, None, {})
