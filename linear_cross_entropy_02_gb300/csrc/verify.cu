@@ -8,7 +8,10 @@
 // distributions that flce_sample draws from. The second takes a request: it compares the
 // drafts, and goes over one row of the target and one of the draft to draw the last token.
 // That row's weights are whole multiples of 2^-40, as in sampling: sums do not depend on
-// the order or on how many CTAs share a row. Few requests are spread over clusters.
+// the order or on how many CTAs share a row. Few requests are spread over clusters. The second kernel is launched
+// while the first still ends, and waits for it: 2 of 98 us for a large batch. (It follows the first CTAs to end of
+// the kernel for rows without filters, whose are small; beside sampling's, which fill an SM each, it would
+// come to lie on few SMs: 47 us for 33 requests of mixed settings, 43 so.)
 #include "model_internal.h"
 #include "sample_device.cuh"
 
@@ -182,6 +185,7 @@ __global__ void __launch_bounds__(kPlainThreads, 1024 / kPlainThreads) verify_pl
   uint32_t ctas;
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
   asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");  // all are running before the first write into another
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // they wait for this grid's end
   uint32_t r = blockIdx.x / ctas;  // (32 bits: divisions of 64 are a hundred instructions)
   if (progress.stopped) {
     // by place: a request's row of the target, then its row of the draft, then the next request's
@@ -345,6 +349,8 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyP
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
     asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");  // all are running before the first write into another
   }
+  // this grid is launched while the one before it, which writes p.cuts, may still run
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t b = blockIdx.x / ctas, K = p.drafts;
   const T* target = static_cast<const T*>(p.x) + b * p.batch_ld;
   const T* draft = p.draft ? static_cast<const T*>(p.draft) + b * p.draft_batch_ld : nullptr;
@@ -567,12 +573,14 @@ cudaError_t run_verify(const VerifyParams& p, int64_t batch, int64_t* accepted, 
   cfg.gridDim = dim3(static_cast<unsigned>(batch * ctas));
   cfg.blockDim = dim3(kVerifyThreads);
   cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = static_cast<unsigned>(ctas);
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, verify_kernel<T, MULTI>, p, accepted, slice);
 }
 
