@@ -13,7 +13,7 @@
 // with the sum in registers and writes it where the token changes. Frequent tokens (in
 // text the first takes a tenth of all places) fill many tiles; what a tile sums of a
 // run that does not begin and end in it goes to the workspace, and a last kernel joins these sums
-// in order. 32768 x 4096 bf16 into 128256 rows of fp32 take 358 us, 6.6 TB/s. Where the gradient is not added to what grad_W holds, the rows of absent
+// in order. 32768 x 4096 bf16 into 128256 rows of fp32 take 355 us, 6.7 TB/s. Where the gradient is not added to what grad_W holds, the rows of absent
 // tokens are zeroed by CTAs of the same launch: nothing is written twice.
 #include <atomic>
 
@@ -31,7 +31,7 @@ constexpr int kVectors = E == 1 ? 16 : 4;  // per lane of the lookup
 constexpr int kChunk = 1024;       // keys sorted by a CTA
 constexpr int kMostShared = 48;    // chunks that shared memory holds
 constexpr int kSharedGroup = 32;   // of more than that
-constexpr int kSharedThreads = 512;
+constexpr int kSharedThreads = 1024;
 constexpr int kGradThreads = 128;
 constexpr int kJoinWarps = 8;
 constexpr int kJoinCtas = 1216;    // for short runs, at least: eight per SM
@@ -167,7 +167,8 @@ __global__ void __launch_bounds__(kThreads) embedding_merge_kernel(const uint32_
 
 // The same for groups of `group` runs of kChunk keys, up to kMostShared, blockIdx.y-th group in shared
 // memory: the keys' loads would otherwise wait for the L2 some ten times for each run. Four
-// searches go side by side. (Sorting 32768 tokens takes 15 us so, 60 with the kernel above.)
+// searches go side by side. All threads load, few of them search: it takes a CTA on every SM. (Sorting 32768
+// tokens takes 13 us so, 60 with the kernel above.)
 __global__ void __launch_bounds__(kSharedThreads) embedding_merge_shared_kernel(const uint32_t* sorted, const uint32_t* places,
                                                                               uint32_t* to_sorted, uint32_t* to_places,
                                                                               const int64_t all_rows, const int group) {
@@ -183,7 +184,8 @@ __global__ void __launch_bounds__(kSharedThreads) embedding_merge_shared_kernel(
   for (int i = threadIdx.x; i < n4; i += kSharedThreads) reinterpret_cast<uint4*>(keys)[i] = __ldg(reinterpret_cast<const uint4*>(sorted) + i);
   for (int i = n4 * 4 + threadIdx.x; i < runs * kChunk; i += kSharedThreads) keys[i] = i < rows ? __ldg(sorted + i) : 0xFFFFFFFFu;
   __syncthreads();
-  for (int i = blockIdx.x * kSharedThreads + threadIdx.x; i < rows; i += gridDim.x * kSharedThreads) {
+  const int each = (rows + gridDim.x - 1) / gridDim.x, from = blockIdx.x * each, to = min(from + each, rows);  // of the CTA
+  for (int i = from + threadIdx.x; i < to; i += kSharedThreads) {
     const uint32_t t = keys[i], place = __ldg(places + i);
     const int mine = i / kChunk;
     int at = i % kChunk;
@@ -432,8 +434,9 @@ cudaError_t launch_merge_shared(const EmbeddingParams& p, int64_t runs, int grou
     if (e != cudaSuccess) return e;
     done.fetch_or(1ull << (dev & 63));
   }
-  const int64_t groups = (runs + group - 1) / group, want = static_cast<int64_t>(group) * kChunk / kSharedThreads;
-  const dim3 grid(static_cast<unsigned>(want < sms ? want : sms), static_cast<unsigned>(groups));
+  // one round of CTAs, each with a warp's keys at least
+  const int64_t groups = (runs + group - 1) / group, each = sms / groups > 0 ? sms / groups : 1, most = static_cast<int64_t>(group) * kChunk / 32;
+  const dim3 grid(static_cast<unsigned>(each < most ? each : most), static_cast<unsigned>(groups));
   embedding_merge_shared_kernel<<<grid, kSharedThreads, static_cast<size_t>(group) * kChunk * 4, s>>>(p.sorted, p.places, p.sorted2, p.places2, p.rows, group);
   return cudaGetLastError();
 }
