@@ -1001,13 +1001,30 @@ cudaError_t run_bwd_warp(const ParamsOf<MODE>& p, int64_t vecs, int sms, int* pa
   return launch_large(norm_bwd_warp_kernel<T, E, NB, RMS, SHIFT, MODE>, done, grid, kWarpRowThreads, smem, s, p, lanes, stages);
 }
 
+// Shared memory of `vecs` vectors of a row in a CTA: their weights, and their place in one stage of the ring.
+template <typename T, int E, bool SHIFT, int MODE>
+constexpr size_t weights_bytes(int64_t vecs) { return SHIFT ? static_cast<size_t>(vecs) * E * sizeof(float) : 0; }
+template <typename T, int E, bool SHIFT, int MODE>
+constexpr size_t stage_bytes(int64_t vecs) { return kRing<T, E> ? static_cast<size_t>(vecs) * ring_arrays(MODE) * sizeof(Raw<T, E>) : 0; }
+inline int cta_threads(int64_t vecs, int C) { return static_cast<int>(((vecs + C - 1) / C + 31) / 32 * 32); }
+
+// Whether a CTA takes a row: its threads' registers have to hold it, and its shared memory one stage. (Behind the
+// residual's addition, with three arrays in a stage, fp32 rows off the vector boundary do up to 13821 elements.)
+template <typename T, int E, bool SHIFT, int MODE>
+bool cta_holds(int64_t vecs) {
+  constexpr int C = cta_vecs(E);
+  if (vecs > static_cast<int64_t>(kMaxThreads) * C) return false;
+  const int64_t all = static_cast<int64_t>(cta_threads(vecs, C)) * C;
+  return weights_bytes<T, E, SHIFT, MODE>(all) + stage_bytes<T, E, SHIFT, MODE>(all) <= kMostShared;
+}
+
 template <typename T, int E, int C, int REGS, int NB, bool RMS, bool SHIFT, int MODE>
 cudaError_t run_bwd_cta(const ParamsOf<MODE>& p, int64_t vecs, int sms, int* partials, cudaStream_t s) {
-  const int threads = static_cast<int>(((vecs + C - 1) / C + 31) / 32 * 32);
+  const int threads = cta_threads(vecs, C);
   int ctas = 65536 / (REGS * threads);
   if (ctas > bwd_ctas(p.hidden)) ctas = bwd_ctas(p.hidden);
-  const size_t weights = SHIFT ? static_cast<size_t>(threads) * C * E * sizeof(float) : 0;
-  const size_t row = kRing<T, E> ? static_cast<size_t>(threads) * C * ring_arrays(MODE) * sizeof(Raw<T, E>) : 0;
+  const size_t weights = weights_bytes<T, E, SHIFT, MODE>(static_cast<int64_t>(threads) * C);
+  const size_t row = stage_bytes<T, E, SHIFT, MODE>(static_cast<int64_t>(threads) * C);
   int stages = !kRing<T, E> ? 2 : kCtaStages;
   while (stages > 1 && (row * stages + weights) * ctas > kMostShared) --stages;
   // rows that a CTA visits are a multiple of eight apart
@@ -1041,7 +1058,7 @@ cudaError_t run_bwd_row(const ParamsOf<MODE>& p, int sms, int* partials, cudaStr
 
 template <typename T, int E, bool SHIFT, int MODE>
 cudaError_t run_bwd(const ParamsOf<MODE>& p, int sms, int* partials, cudaStream_t s) {
-  if (most_vecs(p.hidden, E, SHIFT) <= static_cast<int64_t>(kMaxThreads) * cta_vecs(E)) {
+  if (cta_holds<T, E, SHIFT, MODE>(most_vecs(p.hidden, E, SHIFT))) {
     if (p.part_b)
       return p.rms ? run_bwd_row<T, E, 2, true, SHIFT, MODE>(p, sms, partials, s) : run_bwd_row<T, E, 2, false, SHIFT, MODE>(p, sms, partials, s);
     return p.rms ? run_bwd_row<T, E, 1, true, SHIFT, MODE>(p, sms, partials, s) : run_bwd_row<T, E, 1, false, SHIFT, MODE>(p, sms, partials, s);

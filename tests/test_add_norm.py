@@ -464,3 +464,22 @@ def test_checkpoints_off_the_boundaries(rows, H, dtype):
     good = torch.ones(rows, dtype=torch.bool)
     good[1] = False
     assert torch.equal(g.isfinite().all(1).cpu(), good)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("H", [9002, 12288, 13820, 13821, 13822, 15001, 16381, 16382, 16384])
+def test_the_longest_rows_of_a_cta(H, dtype):
+    """Either side of the widths at which a row no longer fits in a CTA's shared memory or registers, on the vector boundary
+    and off it, a row and several rows a CTA."""
+    import linear_cross_entropy_02_gb300 as flce
+    for rows in (3, 170):
+        a = make(rows, H, dtype, seed=H)
+        off = torch.empty(H + 1, device="cuda")[1:].copy_(a["w"])       # a weight beside the 16-byte boundary
+        for rms, bias, w in ((True, False, a["w"]), (False, True, a["w"]), (False, True, off), (True, True, off)):
+            out = flce.flce_add_layer_norm(a["x"], a["res"], w, rms=rms, checkpoint=True, return_stats=True)
+            check_forward(out["y"], a["x"] + a["res"], w, None, rms)
+            for x, x64 in ((out["sum"], out["sum"]), (out["checkpoint"], flce.flce_checkpoint_load(out["checkpoint"]))):
+                for gs in (a["gs"], None):
+                    got = flce.flce_add_layer_norm_backward(a["gy"], gs, x, w, out["mean"], out["rstd"], rms=rms, need_grad_bias=bias)
+                    check_backward(got, a["gy"], gs, x64, w, out["mean"], out["rstd"], rms)
