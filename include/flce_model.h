@@ -26,7 +26,8 @@ extern "C" {
  * A matrix [rows, H] of activations in 8 bits with a scale for each 32 consecutive
  * elements of a row (the last block of a row may be shorter):
  *   e    = the least whole number >= -127 with max |x| of the block <= 448 2^e
- *   code = x 2^-e rounded to nearest (ties to even) in E4M3
+ *   code = x 2^-e rounded to nearest (ties to even) in E4M3, to 240 at most where e = 120,
+ *          as 256 2^120 is beyond fp32: what is finite reads back finite
  * codes [rows, H] bytes and scales [rows, ceil(H / 32)] bytes (e + 127, E8M0), both
  * contiguous. A block with an infinity or NaN gets the NaN scale (255) and reads
  * back as NaN. H up to 2^24. flce_checkpoint_load writes what they stand for,

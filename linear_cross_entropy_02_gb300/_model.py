@@ -68,8 +68,8 @@ class CheckpointTensor:
 def flce_checkpoint_store(x: torch.Tensor) -> CheckpointTensor:
     """x [..., H] (bf16 or fp32) in 8 bits, leading dimensions flattened: each block of
     32 elements of a row gets the least power of two 2^e with its largest magnitude
-    within 448 2^e, elements are rounded to nearest (ties to even). A block with an
-    infinity or NaN reads back as NaN."""
+    within 448 2^e, elements are rounded to nearest (ties to even; never to an infinity:
+    what is finite reads back finite). A block with an infinity or NaN reads back as NaN."""
     dtype = _floats("x", x)
     _last("x", x)
     x2, rows, ld = _rows(x)

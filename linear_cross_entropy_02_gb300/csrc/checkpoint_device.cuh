@@ -12,6 +12,9 @@
 namespace flce {
 
 constexpr int kCheckpointBlock = 32;
+// The largest scale's byte, 2^120: of blocks with a magnitude above 1.75 2^127. There the code above 240 would stand
+// for 2^128, which fp32 does not hold, so that 240 is the largest (1.9375 2^127 and more are still within 2^-4).
+constexpr uint32_t kTopScale = 247;
 
 __host__ __device__ __forceinline__ int64_t checkpoint_blocks(int64_t hidden) {
   return (hidden + kCheckpointBlock - 1) / kCheckpointBlock;
@@ -97,11 +100,17 @@ __device__ __forceinline__ void keep_vector(const Raw<T, E>& raw, int64_t vec, b
   const uint32_t byte = checkpoint_scale(most);
   // 2^-e; a block of NaN has codes of zero
   const float inv = byte == 255u ? 0.f : __uint_as_float((254u - byte) << 23);
+#pragma unroll
+  for (int e = 0; e < E; ++e) v[e] *= inv;
+  if (byte == kTopScale) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = fminf(fmaxf(v[e], -240.f), 240.f);
+  }
   uint32_t words[E == 8 ? 2 : 1] = {};
 #pragma unroll
   for (int e = 0; e < E; e += 2) {
-    const float hi = E > 1 ? v[E > 1 ? e + 1 : 0] * inv : 0.f;
-    words[e / 4] |= (byte == 255u ? 0u : encode2_e4m3(v[e] * inv, hi)) << (e % 4 * 8);
+    const float hi = E > 1 ? v[E > 1 ? e + 1 : 0] : 0.f;
+    words[e / 4] |= (byte == 255u ? 0u : encode2_e4m3(v[e], hi)) << (e % 4 * 8);
   }
   uint8_t* to = codes + row * hidden + vec * E;
   if constexpr (E == 8)

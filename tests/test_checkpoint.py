@@ -189,3 +189,36 @@ def test_more_than_32_bits_of_odd_rows():
     ends = torch.tensor([0, 1, 268369, 268370, 536739, 536740, rows - 1], device="cuda")    # either side of 2^30 and 2^31 elements
     v = flce.flce_checkpoint_load(flce.flce_checkpoint_store(x), dtype=torch.bfloat16)
     assert torch.equal(v[ends], flce.flce_checkpoint_load(flce.flce_checkpoint_store(x[ends]), dtype=torch.bfloat16))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("H", [5, 64, 1337, 2048, 16390])
+def test_the_largest_numbers_stay_finite(H, dtype):
+    """2^128 is no number of fp32: magnitudes that are nearest to it get the code below."""
+    import linear_cross_entropy_02_gb300 as flce
+    most = torch.finfo(dtype).max
+    top = 2.0 ** 127
+    x = torch.randn(8, H, generator=torch.Generator().manual_seed(H)).to(dtype)
+    for row, v in ((1, most), (2, -most), (3, 1.9375 * top), (4, 1.921875 * top), (5, -1.75 * top), (6, 1.7578125 * top)):
+        x[row, H // 2] = v
+    x[7] = -most
+    # (1.75 2^127 is 448 2^119 itself; the least value that rounds to 2^128 is 1.9375 2^127, a tie)
+    want = {1: 1.875, 2: -1.875, 3: 1.875, 4: 1.875, 5: -1.75, 6: 1.75}
+    q = flce.flce_checkpoint_store(x.cuda())
+    scales = q.scales.cpu()[:, H // 2 // 32].tolist()
+    assert scales[1:] == [247, 247, 247, 247, 246, 247, 247]
+    for out in (torch.float32, torch.bfloat16):
+        v = flce.flce_checkpoint_load(q, dtype=out).cpu()
+        assert bool(v.isfinite().all())
+        for row, m in want.items():
+            assert float(v[row, H // 2]) == m * top
+        assert bool((v[7].double() == -1.875 * top).all())
+    # the squares of such a row are beyond fp32 and its rstd is 0: its gradient is that of the sum, the weight's is the others'
+    w, gy = torch.ones(H, device="cuda"), torch.ones(8, H, device="cuda", dtype=dtype)
+    out = flce.flce_add_layer_norm(x.cuda(), None, w, rms=True, checkpoint=True, return_stats=True)
+    assert bool((out["rstd"][[1, 2, 7]] == 0).all())
+    g = flce.flce_add_layer_norm_backward(gy, gy, out["checkpoint"], w, None, out["rstd"], rms=True)
+    assert bool((g["grad_x"][[1, 2, 7]] == 1).all()) and all(bool(g[k].isfinite().all()) for k in ("grad_x", "grad_weight", "grad_bias"))
+    few = flce.flce_add_layer_norm_backward(gy[:1], None, flce.flce_checkpoint_store(x[:1].cuda()), w, None, out["rstd"][:1], rms=True)
+    assert torch.equal(g["grad_weight"], few["grad_weight"])
