@@ -1210,7 +1210,8 @@ __device__ bool segment_answer(const Row<T, kThreads>& row, Shared& s, const Par
 }
 
 // Verification: row r's first logit, its request, whose settings it has, and its place; rows of the
-// target come first, then those of the draft. False if it lies behind the request's last draft.
+// target come first, then those of the draft. False if it lies behind the request's last draft. Called by whole
+// warps, which look at 32 drafts at a time.
 template <typename T>
 __device__ __forceinline__ bool verify_row(const VerifyParams& p, uint32_t r, const T** start, int64_t* request, int* at_place) {
   const uint32_t target_rows = static_cast<uint32_t>(p.target_rows);
@@ -1221,12 +1222,13 @@ __device__ __forceinline__ bool verify_row(const VerifyParams& p, uint32_t r, co
   *at_place = place;
   *start = target ? static_cast<const T*>(p.x) + *request * p.batch_ld + place * p.ld
                   : static_cast<const T*>(p.draft) + *request * p.draft_batch_ld + place * p.draft_ld;
-  bool used = true;
-  for (int i = 0; i < place + (target ? 0 : 1); ++i) {
-    const int64_t token = __ldg(p.draft_tokens + *request * p.drafts + i);
-    used = used && token >= 0 && token < p.vocab;
+  bool none = false;
+  const int64_t* tokens = p.draft_tokens + *request * p.drafts;
+  for (int i = static_cast<int>(threadIdx.x) & 31; i < place + (target ? 0 : 1); i += 32) {
+    const int64_t token = __ldg(tokens + i);
+    none = none || token < 0 || token >= p.vocab;
   }
-  return used;
+  return !__any_sync(0xffffffffu, none);
 }
 
 // ---------------------------------------------------------------- the kernel

@@ -446,3 +446,25 @@ def test_rows_at_the_limits_of_the_registers(V, dtype):
     check(flce, x, d, u, q, {})
     x[1, 1, V - 1] = math.nan
     check(flce, x, d, u, None, {})
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("with_draft", [True, False])
+@pytest.mark.parametrize("settings", [dict(), dict(top_k=3)])
+def test_many_drafts_that_end_anywhere(settings, with_draft):
+    """The first place without a draft at and beside the multiples of 32, of up to 1024; all drafts before it are accepted."""
+    import linear_cross_entropy_02_gb300 as flce
+    ends = [0, 1, 31, 32, 33, 63, 64, 500, 992, 1023, 1024]
+    K, V = 1024, 17
+    x, q, u, g = make(len(ends), K, V, torch.float32, seed=17, noise=0.0)
+    d = draft_from(flce, q, g, settings, K)
+    u[:, :K] *= 0.5 if with_draft else 0.0      # below p of any draft that is drawn
+    for b, end in enumerate(ends):
+        if end < K:
+            d[b, end] = -1 if b % 2 else V
+    tokens, accepted, lp = flce.flce_verify(x, d, u, q if with_draft else None, **settings)
+    assert accepted.tolist() == ends
+    for b, end in enumerate(ends):
+        assert torch.equal(tokens[b, :end], d[b, :end]) and bool((tokens[b, end + 1:] == -1).all())
+        t, l = flce.flce_sample(x[b, end], u[b, K], **settings)     # the token behind them: the target's own
+        assert int(tokens[b, end]) == int(t) and float(lp[b, end]) == float(l)
