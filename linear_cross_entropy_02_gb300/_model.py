@@ -224,6 +224,10 @@ def add_layer_norm(x, residual=None, weight=None, bias=None, *, eps: float = 1e-
     gradients of x, the residual and the weight are those at the sum's 8-bit values.
     need_sum=False gives (y, None). As for any node, capture a backward pass into a graph
     while no eager graph of the same leaves lives."""
+    if not (torch.is_grad_enabled() and any(getattr(t, "requires_grad", False) for t in (x, residual, weight, bias))):
+        # no backward pass comes: nothing is written for it
+        out = flce_add_layer_norm(x, residual, weight, bias, eps=float(eps), rms=bool(rms), need_sum=bool(need_sum))
+        return out["y"], out["sum"]
     out = _AddLayerNorm.apply(x, residual, weight, bias, float(eps), bool(rms), bool(checkpoint_8bit), bool(need_sum))
     if isinstance(out, tuple):
         return out

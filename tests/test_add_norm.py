@@ -483,3 +483,31 @@ def test_the_longest_rows_of_a_cta(H, dtype):
                 for gs in (a["gs"], None):
                     got = flce.flce_add_layer_norm_backward(a["gy"], gs, x, w, out["mean"], out["rstd"], rms=rms, need_grad_bias=bias)
                     check_backward(got, a["gy"], gs, x64, w, out["mean"], out["rstd"], rms)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("checkpoint_8bit", [False, True])
+def test_nothing_is_kept_where_no_backward_pass_comes(checkpoint_8bit, monkeypatch):
+    """No checkpoint, no statistics and no sum beside the ones asked for, where nothing requires a gradient or grad mode is off."""
+    import linear_cross_entropy_02_gb300 as flce
+    from linear_cross_entropy_02_gb300 import _model
+    a, made, inner = make(20, 64, torch.bfloat16), [], _model.flce_add_layer_norm
+
+    def forward(*args, **kw):
+        made.append(inner(*args, **kw))
+        return made[-1]
+    monkeypatch.setattr(_model, "flce_add_layer_norm", forward)
+    leaf = a["x"].clone().requires_grad_()
+    y, s = flce.add_layer_norm(leaf, a["res"], a["w"], a["b"], rms=True, checkpoint_8bit=checkpoint_8bit)
+    assert y.requires_grad and made[-1]["rstd"] is not None and (made[-1]["checkpoint"] is not None) == checkpoint_8bit
+    for x, mode in ((a["x"], True), (leaf, False)):
+        with torch.set_grad_enabled(mode):
+            z, t = flce.add_layer_norm(x, a["res"], a["w"], a["b"], rms=True, checkpoint_8bit=checkpoint_8bit)
+            assert torch.equal(z, y) and torch.equal(t, s) and not z.requires_grad and not t.requires_grad
+            assert made[-1]["checkpoint"] is made[-1]["mean"] is made[-1]["rstd"] is None
+            z, t = flce.add_layer_norm(x, a["res"], a["w"], a["b"], rms=True, checkpoint_8bit=checkpoint_8bit, need_sum=False)
+            assert torch.equal(z, y) and t is None and made[-1]["sum"] is None
+            z, t = flce.add_layer_norm(x, None, a["w"], rms=True, checkpoint_8bit=checkpoint_8bit)
+            assert t is x and not z.requires_grad and made[-1]["checkpoint"] is made[-1]["rstd"] is None
+    head = flce.LanguageModelHead(torch.zeros(10, 64, device="cuda", dtype=torch.bfloat16), a["w"], a["b"], checkpoint_8bit=checkpoint_8bit)
+    assert torch.equal(head.normalise(a["x"], a["res"]), y) and made[-1]["checkpoint"] is made[-1]["sum"] is made[-1]["rstd"] is None
