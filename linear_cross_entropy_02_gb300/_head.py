@@ -356,6 +356,11 @@ def flce_sample(logits: torch.Tensor, u: torch.Tensor, *, temperature=1.0, top_k
 
 
 # ---------------------------------------------------------------- the head as a model has it
+def _given(residual) -> dict:
+    """The residual as an argument where there is one: a subclass's normalise(hidden) or logits(hidden) need not know it."""
+    return {} if residual is None else {"residual": residual}
+
+
 class LanguageModelHead(torch.nn.Module):
     """A model's last layers: the final norm and the vocabulary projection W [V, H]
     (bf16 or fp32), for training and for answering.
@@ -373,6 +378,8 @@ class LanguageModelHead(torch.nn.Module):
     keeps what it normalised in 8 bits for its backward pass. embed(tokens) looks
     tokens up in W, for a model whose embedding and head are one weight. verify(...)
     checks drafted tokens against the answers' distribution."""
+
+    checkpoint_8bit = False  # (heads that were pickled before they had it)
 
     def __init__(self, weight: torch.Tensor, norm_weight: Optional[torch.Tensor] = None,
                  norm_bias: Optional[torch.Tensor] = None, *, eps: float = 1e-5, rms: bool = True, softcap: float = 0.0,
@@ -414,7 +421,7 @@ class LanguageModelHead(torch.nn.Module):
     def loss(self, hidden: torch.Tensor, labels: torch.Tensor, residual: Optional[torch.Tensor] = None):
         """(loss, token_accuracy) of hidden [..., H] (plus residual) and int64 labels [...]."""
         from . import linear_cross_entropy
-        return linear_cross_entropy(self.normalise(hidden, residual), self.weight, labels, softcap=self.softcap,
+        return linear_cross_entropy(self.normalise(hidden, **_given(residual)), self.weight, labels, softcap=self.softcap,
                                     out_mult=self.out_mult, ignore_index=self.ignore_index, reduction=self.reduction)
 
     forward = loss
@@ -440,7 +447,7 @@ class LanguageModelHead(torch.nn.Module):
     @torch.no_grad()
     def logits(self, hidden: torch.Tensor, out_dtype: Optional[torch.dtype] = None, residual: Optional[torch.Tensor] = None) -> torch.Tensor:
         """Logits [..., V] on the microscaled W."""
-        return flce_microscale_linear(self.normalise(hidden, residual), self._current_answers(), out_mult=self.out_mult,
+        return flce_microscale_linear(self.normalise(hidden, **_given(residual)), self._current_answers(), out_mult=self.out_mult,
                                       softcap=self.softcap, out_dtype=out_dtype)
 
     @torch.no_grad()
@@ -448,7 +455,7 @@ class LanguageModelHead(torch.nn.Module):
         """(tokens, logprobs) for hidden [..., H] (plus residual) and random numbers u [...]; settings
         as in flce_sample. The logits are rounded to hidden's dtype in between; for
         32 bits of them take flce_sample(self.logits(hidden, torch.float32), u, ...)."""
-        return flce_sample(self.logits(hidden, residual=residual), u, **settings)
+        return flce_sample(self.logits(hidden, **_given(residual)), u, **settings)
 
     @torch.no_grad()
     def verify(self, hidden: torch.Tensor, draft_tokens: torch.Tensor, u: torch.Tensor, draft_logits: Optional[torch.Tensor] = None,
@@ -457,4 +464,4 @@ class LanguageModelHead(torch.nn.Module):
         drafted tokens [..., K] and the one behind them; draft_logits [..., K, V] in hidden's dtype, u
         [..., K + 1] and settings as in flce_verify."""
         from . import _model
-        return _model.flce_verify(self.logits(hidden, residual=residual), draft_tokens, u, draft_logits, **settings)
+        return _model.flce_verify(self.logits(hidden, **_given(residual)), draft_tokens, u, draft_logits, **settings)

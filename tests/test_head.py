@@ -221,3 +221,27 @@ def test_a_capture_before_the_first_answer():
     head.weight.data.copy_(W.flip(0))
     graph.replay()
     assert torch.equal(z, want.flip(2))
+
+
+def test_heads_from_before_the_residual(monkeypatch):
+    """Subclasses whose normalise and logits take hidden alone, and pickled heads without the newer attribute, work as they did."""
+    import linear_cross_entropy_02_gb300 as flce
+    from linear_cross_entropy_02_gb300 import _head
+
+    class Own(flce.LanguageModelHead):
+        def normalise(self, hidden):
+            return 2 * hidden
+
+        def logits(self, hidden, out_dtype=None):
+            return self.normalise(hidden) + 1
+    monkeypatch.setattr(flce, "linear_cross_entropy", lambda h, W, labels, **kw: (h, labels))
+    monkeypatch.setattr(_head, "flce_sample", lambda z, u, **kw: (z, u))
+    head, x = Own(torch.zeros(4, 8)), torch.ones(3, 8)
+    assert torch.equal(head.loss(x, None)[0], 2 * x) and torch.equal(head(x, None)[0], 2 * x)
+    assert torch.equal(head.next_token(x, None)[0], 2 * x + 1)
+    with pytest.raises(TypeError):
+        head.loss(x, None, residual=x)
+    monkeypatch.setattr(_head, "layer_norm", lambda h, *args, **kw: 3 * h)
+    old = flce.LanguageModelHead(torch.zeros(4, 8))
+    del old.__dict__["checkpoint_8bit"]
+    assert torch.equal(old.loss(x, None)[0], 3 * x)
