@@ -218,7 +218,10 @@ template <typename T, typename W, bool X8>
 cudaError_t run_add_bwd(const AddNormParams& p, int sms, int* partials, cudaStream_t s) {
   constexpr int C = sizeof(T);  // 16 columns per thread
   // (Microseconds for 32768 rows of bf16 from 8 bits: 7168 RMS with 16 columns held 316, not 317, with 32 held
-  // 304, and with 144 registers, where they cost no CTA, 296; 5120 at 128 registers 208, at 144, with a CTA less, 246.
+  // 304, and where 144 registers are allowed, 296: ptxas takes 127 or 128 of them all the same, and orders the loads
+  // otherwise. 5120 at 128 registers 208, where 144 are counted on, with a CTA less, 246. The one kernel that does take
+  // 144, layer norm from the sum with an fp32 weight, leaves room for one CTA of 7168 columns, as a scheduler's 16384
+  // registers hold three such warps: 427 us, 330 with 128; with a bf16 weight 326 and 328.
   // With a bias' sums 7168 held 394, not 376; from the sum 353 and 374. 8192 x 7168 fp32 with 32 columns 166,
   // with 16 126.)
   const int64_t hidden = p.hidden;
@@ -232,9 +235,10 @@ cudaError_t run_add_bwd(const AddNormParams& p, int sms, int* partials, cudaStre
   }
   if constexpr (sizeof(T) == 2) {
     if (hidden > 4096 && hidden % (2 * kWideStep) == 0) {
-      if (65536 / (144 * (hidden / 32)) == 65536 / (128 * (hidden / 32)))
-        return p.rms ? run_add_bwd_as<T, W, 1, true, X8, true, 2 * C, 144>(p, sms, partials, s)
-                     : run_add_bwd_as<T, W, 1, false, X8, true, 2 * C, 144>(p, sms, partials, s);
+      if (65536 / (144 * (hidden / 32)) == 65536 / (128 * (hidden / 32))) {
+        if (p.rms) return run_add_bwd_as<T, W, 1, true, X8, true, 2 * C, 144>(p, sms, partials, s);
+        if constexpr (X8 || sizeof(W) == 2) return run_add_bwd_as<T, W, 1, false, X8, true, 2 * C, 144>(p, sms, partials, s);
+      }
       return p.rms ? run_add_bwd_as<T, W, 1, true, X8, true, 2 * C, 128>(p, sms, partials, s)
                    : run_add_bwd_as<T, W, 1, false, X8, true, 2 * C, 128>(p, sms, partials, s);
     }

@@ -511,3 +511,17 @@ def test_nothing_is_kept_where_no_backward_pass_comes(checkpoint_8bit, monkeypat
             assert t is x and not z.requires_grad and made[-1]["checkpoint"] is made[-1]["rstd"] is None
     head = flce.LanguageModelHead(torch.zeros(10, 64, device="cuda", dtype=torch.bfloat16), a["w"], a["b"], checkpoint_8bit=checkpoint_8bit)
     assert torch.equal(head.normalise(a["x"], a["res"]), y) and made[-1]["checkpoint"] is made[-1]["sum"] is made[-1]["rstd"] is None
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("wdtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("H", [6144, 7168])
+def test_wide_rows_with_weights_of_either_type(H, wdtype):
+    """Layer norm without a bias: the kernels under a limit of 144 registers, and the one that stays under 128."""
+    import linear_cross_entropy_02_gb300 as flce
+    a = make(700, H, torch.bfloat16, wdtype, seed=H)
+    out = flce.flce_add_layer_norm(a["x"], a["res"], a["w"], checkpoint=True, return_stats=True)
+    for x, x64 in ((out["sum"], out["sum"]), (out["checkpoint"], flce.flce_checkpoint_load(out["checkpoint"]))):
+        for gs in (a["gs"], None):
+            got = flce.flce_add_layer_norm_backward(a["gy"], gs, x, a["w"], out["mean"], out["rstd"], need_grad_bias=False)
+            check_backward(got, a["gy"], gs, x64, a["w"], out["mean"], out["rstd"], False)
