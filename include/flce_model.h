@@ -70,6 +70,7 @@ int flce_embedding(const int64_t* tokens, int64_t rows, const void* W, int dtype
  * [vocab, H] contiguous, summed in an order that depends on the tokens alone: results do
  * not change from run to run. accumulate != 0 adds it to what grad_W holds (the fused
  * head's accumulator, for a weight that is both), else absent tokens' rows are zeroed.
+ * That addition takes numbers below 2^-126 as zero, in grad_W and in its result.
  * Tokens outside of the vocabulary count for nothing. vocab < 2^31 - 1, rows up to
  * 65535 x 32768. */
 size_t flce_embedding_workspace_size(int64_t rows, int64_t hidden);

@@ -269,8 +269,8 @@ def flce_embedding_backward(grad_out: torch.Tensor, tokens: torch.Tensor, vocab:
     """Gradient of flce_embedding for W, fp32 [vocab, H]: scale times the sum of grad_out
     [..., H] over each token's places, the same in every run. A grad_W that is given (fp32,
     contiguous) is ACCUMULATED in place, as the fused head does with its own: a weight that
-    is embedding and head needs one accumulator. Tokens outside of the vocabulary count
-    for nothing."""
+    is embedding and head needs one accumulator (numbers below 2^-126 count as zero
+    there). Tokens outside of the vocabulary count for nothing."""
     dtype = _floats("grad_out", grad_out)
     _last("grad_out", grad_out)
     H, index = grad_out.shape[-1], grad_out.get_device()

@@ -219,12 +219,14 @@ __global__ void __launch_bounds__(kSharedThreads) embedding_merge_shared_kernel(
 }
 
 // ------------------------------------------------------------------ gradient
-// A thread's columns: C vectors of E, kGradThreads apart.
+// Writes or adds E columns of a row. (The addition is the only one to its elements in the launch, and by the memory system, so
+// that no thread waits for what the row holds: 30000 uniform tokens of 1337 bf16 columns 91 us, 162 by loading and
+// storing; 8192 of 1024 columns 40 and 51, but 32768 of 4096 257 and 224. It takes numbers below 2^-126 as zero.)
 template <int E>
 __device__ __forceinline__ void put(float* to, const float (&v)[E], float scale, bool add) {
   if constexpr (E == 1) {
     if (add)
-      atomicAdd(to, v[0] * scale);  // (the only addition to this element in the launch)
+      atomicAdd(to, v[0] * scale);
     else
       *to = v[0] * scale;
   } else {
@@ -239,7 +241,7 @@ __device__ __forceinline__ void put(float* to, const float (&v)[E], float scale,
   }
 }
 
-// CTAs from `tiles` * `slices` on zero rows of absent tokens.
+// CTAs from `tiles` * `slices` on zero rows of absent tokens. A thread's columns: C vectors of E, kGradThreads apart.
 template <typename T, int E, int C>
 __global__ void __launch_bounds__(kGradThreads) embedding_grad_kernel(const EmbeddingParams p, const int64_t tiles, const int slices,
                                                                     const int zero_rows) {

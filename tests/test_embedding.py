@@ -271,3 +271,21 @@ def test_runs_around_the_tiles(H):
             acc = torch.ones(1009, H, device="cuda")
             flce.flce_embedding_backward(G.to(dtype), t, 1009, grad_W=acc)
             assert torch.equal(acc.double(), want + 1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H", [8, 5])
+def test_numbers_below_the_normal_range(H):
+    """Written they are kept; added to an accumulator they count as zero, in rows that have a token, and in no others."""
+    import linear_cross_entropy_02_gb300 as flce
+    t, G = torch.tensor([1, 2], device="cuda"), torch.full((2, H), 3e-39, device="cuda")
+    G[1] = 1.0
+    fresh = flce.flce_embedding_backward(G, t, 4)
+    assert torch.equal(fresh[1], G[0]) and torch.equal(fresh[2], G[1])
+    acc = torch.full((4, H), 1e-40, device="cuda")
+    acc[2] = 2.0 ** -126
+    want = acc.double()
+    want[1:3] += G.double()
+    flce.flce_embedding_backward(G, t, 4, grad_W=acc)
+    assert torch.equal(acc[0], acc[3]) and bool((acc[0] > 0).all())
+    assert bool(((acc.double() - want).abs() <= 2.0 ** -126).all())
