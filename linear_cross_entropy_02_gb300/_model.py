@@ -192,7 +192,11 @@ class _AddLayerNorm(torch.autograd.Function):
         kept = (q.codes, q.scales) if checkpoint_8bit else (out["sum"], None)
         ctx.checkpoint_8bit = checkpoint_8bit
         ctx.save_for_backward(*kept, weight, out["mean"], out["rstd"])
-        return (out["y"], out["sum"]) if residual is not None and need_sum else out["y"]
+        if residual is None or not need_sum:
+            return out["y"]
+        if not any(ctx.needs_input_grad[:2]):  # the sum is none of the weights'
+            ctx.mark_non_differentiable(out["sum"])
+        return out["y"], out["sum"]
 
     @staticmethod
     @once_differentiable

@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kThreads) embedding_kernel(const EmbeddingPara
 // ------------------------------------------------------------------ sort
 // Sorts kChunk (token, position) keys of the CTA's piece, one in each thread; tokens outside
 // of the vocabulary count as `vocab` and come last. (A bitonic sort; most of its exchanges are within
-// a warp. With two keys per thread, all of them through shared memory, it took 10 us, so 4.)
+// a warp. With two keys per thread, all of them through shared memory, it took 10 us, so 6.)
 // Also empties the lists of runs to join.
 __global__ void __launch_bounds__(kChunk) embedding_chunk_kernel(const int64_t* tokens, const int64_t rows, const int64_t vocab,
                                                                uint32_t* sorted, uint32_t* places, uint32_t* joins) {
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kThreads) embedding_merge_kernel(const uint32_
 // The same for groups of `group` runs of kChunk keys, up to kMostShared, blockIdx.y-th group in shared
 // memory: the keys' loads would otherwise wait for the L2 some ten times for each run. Four
 // searches go side by side. All threads load, few of them search: it takes a CTA on every SM. (Sorting 32768
-// tokens takes 13 us so, 60 with the kernel above.)
+// tokens takes 14 us so, 60 with the kernel above.)
 __global__ void __launch_bounds__(kSharedThreads) embedding_merge_shared_kernel(const uint32_t* sorted, const uint32_t* places,
                                                                               uint32_t* to_sorted, uint32_t* to_places,
                                                                               const int64_t all_rows, const int group) {

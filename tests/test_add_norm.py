@@ -525,3 +525,21 @@ def test_wide_rows_with_weights_of_either_type(H, wdtype):
         for gs in (a["gs"], None):
             got = flce.flce_add_layer_norm_backward(a["gy"], gs, x, a["w"], out["mean"], out["rstd"], need_grad_bias=False)
             check_backward(got, a["gy"], gs, x64, a["w"], out["mean"], out["rstd"], False)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("checkpoint_8bit", [False, True])
+def test_the_sum_depends_on_x_and_the_residual_alone(checkpoint_8bit):
+    """Where only the norm's weights learn, no gradient is asked of the residual stream behind them."""
+    import linear_cross_entropy_02_gb300 as flce
+    a = make(20, 64, torch.bfloat16)
+    w, b = a["w"].clone().requires_grad_(), a["b"].clone().requires_grad_()
+    y, s = flce.add_layer_norm(a["x"], a["res"], w, b, checkpoint_8bit=checkpoint_8bit)
+    assert y.requires_grad and not s.requires_grad and torch.equal(s, a["x"] + a["res"])
+    ((y + s) * a["gy"]).sum().backward()
+    out = flce.flce_add_layer_norm(a["x"], a["res"], a["w"], a["b"], checkpoint=True, return_stats=True)
+    want = flce.flce_add_layer_norm_backward(a["gy"], None, out["checkpoint" if checkpoint_8bit else "sum"], a["w"], out["mean"], out["rstd"], need_grad_x=False)
+    assert torch.equal(w.grad, want["grad_weight"]) and torch.equal(b.grad, want["grad_bias"])
+    for x, res in ((a["x"].clone().requires_grad_(), a["res"]), (a["x"], a["res"].clone().requires_grad_())):
+        y, s = flce.add_layer_norm(x, res, w, b, checkpoint_8bit=checkpoint_8bit)
+        assert y.requires_grad and s.requires_grad
