@@ -181,8 +181,11 @@ class _AddLayerNorm(torch.autograd.Function):
     the rows' statistics."""
 
     @staticmethod
-    def forward(ctx, x, residual, weight, bias, eps, rms, checkpoint_8bit, need_sum):
+    def forward(ctx, x, residual, weight, bias, eps, rms, checkpoint_8bit, need_sum, grad_mode):
         ctx.set_materialize_grads(False)
+        if not (grad_mode and any(ctx.needs_input_grad)):  # no backward pass comes: nothing is written for it
+            out = flce_add_layer_norm(x, residual, weight, bias, eps=eps, rms=rms, need_sum=need_sum)
+            return (out["y"], out["sum"]) if residual is not None and need_sum else out["y"]
         out = flce_add_layer_norm(x, residual, weight, bias, eps=eps, rms=rms, need_sum=need_sum or not checkpoint_8bit,
                                   checkpoint=checkpoint_8bit, return_stats=True)
         ctx.rms = rms
@@ -205,11 +208,11 @@ class _AddLayerNorm(torch.autograd.Function):
         need_x, need_r, need_w, need_b = ctx.needs_input_grad[:4]
         if grad_y is None:  # only the sum was used
             if grad_sum is None:
-                return (None,) * 8
+                return (None,) * 9
             zero = lambda need, t: torch.zeros_like(t) if need and t is not None else None  # noqa: E731
             gw = zero(need_w, weight)
             gb = torch.zeros(ctx.like[0][-1], dtype=ctx.bias_dtype, device=grad_sum.device) if need_b else None
-            return grad_sum if need_x else None, grad_sum if need_r else None, gw, gb, None, None, None, None
+            return grad_sum if need_x else None, grad_sum if need_r else None, gw, gb, None, None, None, None, None
         out = flce_add_layer_norm_backward(grad_y, grad_sum, CheckpointTensor(a, b) if ctx.checkpoint_8bit else a, weight, mean, rstd,
                                            rms=ctx.rms, need_grad_x=need_x or need_r, need_grad_weight=need_w, need_grad_bias=need_b)
         gx, gw, gb = out["grad_x"], out["grad_weight"], out["grad_bias"]
@@ -217,7 +220,7 @@ class _AddLayerNorm(torch.autograd.Function):
             gw = gw.to(weight.dtype)
         if gb is not None and ctx.bias_dtype != torch.float32:
             gb = gb.to(ctx.bias_dtype)
-        return gx if need_x else None, gx if need_r else None, gw, gb, None, None, None, None
+        return gx if need_x else None, gx if need_r else None, gw, gb, None, None, None, None, None
 
 
 def add_layer_norm(x, residual=None, weight=None, bias=None, *, eps: float = 1e-5, rms: bool = False, checkpoint_8bit: bool = False,
@@ -228,11 +231,8 @@ def add_layer_norm(x, residual=None, weight=None, bias=None, *, eps: float = 1e-
     gradients of x, the residual and the weight are those at the sum's 8-bit values.
     need_sum=False gives (y, None). As for any node, capture a backward pass into a graph
     while no eager graph of the same leaves lives."""
-    if not (torch.is_grad_enabled() and any(getattr(t, "requires_grad", False) for t in (x, residual, weight, bias))):
-        # no backward pass comes: nothing is written for it
-        out = flce_add_layer_norm(x, residual, weight, bias, eps=float(eps), rms=bool(rms), need_sum=bool(need_sum))
-        return out["y"], out["sum"]
-    out = _AddLayerNorm.apply(x, residual, weight, bias, float(eps), bool(rms), bool(checkpoint_8bit), bool(need_sum))
+    out = _AddLayerNorm.apply(x, residual, weight, bias, float(eps), bool(rms), bool(checkpoint_8bit), bool(need_sum),
+                              torch.is_grad_enabled())
     if isinstance(out, tuple):
         return out
     return out, x if need_sum and residual is None else None

@@ -543,3 +543,17 @@ def test_the_sum_depends_on_x_and_the_residual_alone(checkpoint_8bit):
     for x, res in ((a["x"].clone().requires_grad_(), a["res"]), (a["x"], a["res"].clone().requires_grad_())):
         y, s = flce.add_layer_norm(x, res, w, b, checkpoint_8bit=checkpoint_8bit)
         assert y.requires_grad and s.requires_grad
+
+
+@pytest.mark.gpu
+def test_forward_mode_derivatives_are_refused():
+    """There are none; a tangent is not dropped without a word."""
+    import torch.autograd.forward_ad as fw
+
+    import linear_cross_entropy_02_gb300 as flce
+    a = make(4, 64, torch.float32)
+    for mode in (True, False):
+        with torch.set_grad_enabled(mode), fw.dual_level():
+            x = fw.make_dual(a["x"], a["gy"])
+            with pytest.raises(NotImplementedError):
+                flce.add_layer_norm(x, a["res"], a["w"])
