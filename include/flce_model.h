@@ -83,7 +83,8 @@ int flce_embedding_backward(const void* grad_out, int dtype, int64_t ld_grad, co
  * from a draft model, and the target's logits at their places and at the one behind
  * them. With p_i the distribution that flce_sample draws from for the target's row i
  * (whole weights w of the tokens that the request's temperature, top_k, top_p and min_p
- * keep, W their sum, p = w / W), and q_i that for the draft's row i, or, where `draft` is
+ * keep, W their sum, p = w / W), and q_i that for the draft's row i under the same settings
+ * (logits of a draft sampled at another temperature are scaled first), or, where `draft` is
  * NULL, all weight on d_i:
  *   accepted  the drafts before the first with not u_i q_i(d_i) < p_i(d_i)  (in fp64)
  *   then one token more, at place n = accepted: where d_n was compared and not accepted,

@@ -332,8 +332,9 @@ def flce_verify(target_logits: torch.Tensor, draft_tokens: torch.Tensor, u: torc
     """Verifies K drafted tokens [..., K] (int64) of each request against the target's logits
     [..., K + 1, V] (bf16 or fp32) at their places and the one behind them, from given random
     numbers u [..., K + 1] (fp32, uniform in [0, 1)). The drafts were drawn by flce_sample from
-    draft_logits [..., K, V] (the target's dtype) under the same settings; None: they were not drawn
-    but found, and have no distribution. temperature, top_k, top_p and min_p are as in flce_sample, a
+    draft_logits [..., K, V] (the target's dtype) under the same settings (logits of a draft sampled at
+    another temperature T' are given times temperature / T'); None: they were not drawn but found, and
+    have no distribution. temperature, top_k, top_p and min_p are as in flce_sample, a
     tensor with one value per request. Drafts are accepted while u_i q(d_i) < p(d_i); one token more is
     drawn, from max(p - q, 0) at the first that is not, else from p, so that tokens are
     distributed as the target's own. A draft outside of [0, V) stands for none, so requests may
