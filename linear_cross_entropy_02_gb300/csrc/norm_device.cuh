@@ -106,6 +106,10 @@ __device__ __forceinline__ float group_sum(float v, int lanes) {
   return v;
 }
 
+// 1 / sqrt(variance + eps): a variance just below zero is rounding, one that is not a number stays so (fmaxf would
+// make zero of it, and numbers of the rest of its row).
+__device__ __forceinline__ float inverse_deviation(float variance, float eps) { return 1.f / sqrtf((variance < 0.f ? 0.f : variance) + eps); }
+
 // ------------------------------------------------------------------ forward
 // A row held as C vectors per thread, `stride` apart: its statistics and y.
 // sum(a, b, Both() or One()) sums a (and b) over the row's threads; vecs is 0 in
@@ -205,7 +209,7 @@ __device__ __forceinline__ void norm_row(const ParamsOf<MODE>& p, const T* x, T*
     sum(sq, rest, One());
     rest = 0.f;
   }
-  const float rstd = 1.f / sqrtf(fmaxf(sq * inv_h - rest * rest, 0.f) + p.eps);
+  const float rstd = inverse_deviation(sq * inv_h - rest * rest, p.eps);
   if (t == 0 && vecs > 0) {
     if (p.mean && !p.rms) p.mean[row] = mean + rest;
     if (p.rstd) p.rstd[row] = rstd;
@@ -310,7 +314,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_long_kernel(const ParamsOf<M
     }
     block_sum<true>(s[0], s[1], sums, slot);
     rest = p.rms ? 0.f : s[1] * inv_h;
-    const float rstd = 1.f / sqrtf(fmaxf(s[0] * inv_h - rest * rest, 0.f) + p.eps);
+    const float rstd = inverse_deviation(s[0] * inv_h - rest * rest, p.eps);
     if (threadIdx.x == 0) {
       if (p.mean && !p.rms) p.mean[row] = mean + rest;
       if (p.rstd) p.rstd[row] = rstd;

@@ -557,3 +557,27 @@ def test_forward_mode_derivatives_are_refused():
             x = fw.make_dual(a["x"], a["gy"])
             with pytest.raises(NotImplementedError):
                 flce.add_layer_norm(x, a["res"], a["w"])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rms", [True, False])
+@pytest.mark.parametrize("H", [1, 8, 100, 1337, 2048, 7168, 16385, 70000])
+def test_a_nan_is_its_whole_row_s(H, rms, dtype):
+    """NaN and infinities give what the formula gives in 64 bits: with a NaN in the row there is no variance, and no y."""
+    import linear_cross_entropy_02_gb300 as flce
+    a = make(6, H, dtype, seed=H)
+    zero = torch.zeros_like(a["res"])
+    for row, v in ((1, "nan"), (3, "inf"), (4, "-inf")):
+        a["x"][row, H // 2] = float(v)
+    x = a["x"].double()
+    d = x if rms else x - x.mean(-1, keepdim=True)      # (forward64 takes 0 times the mean, which an infinity makes NaN)
+    rstd = (d.square().mean(-1, keepdim=True) + 1e-5).rsqrt()
+    want = d * rstd * a["w"].double() + a["b"].double()
+    out = flce.flce_add_layer_norm(a["x"], zero, a["w"], a["b"], rms=rms, return_stats=True)
+    alone = flce.flce_layer_norm(a["x"], a["w"], a["b"], rms=rms, return_stats=True)
+    for y, r in ((out["y"], out["rstd"]), (alone[0], alone[2])):
+        assert torch.equal(y.isnan(), want.isnan()) and bool(y[1].isnan().all()) and bool(r[1].isnan())
+        assert torch.equal(r.isnan(), rstd.squeeze(-1).isnan()) and bool(y[[0, 2, 5]].isfinite().all())
+    got = flce.flce_add_layer_norm_backward(a["gy"], None, out["sum"], a["w"], out["mean"], out["rstd"], rms=rms)["grad_x"]
+    assert bool(got[1].isnan().all()) and bool(got[[0, 2, 5]].isfinite().all())
